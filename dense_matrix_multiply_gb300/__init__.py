@@ -43,6 +43,12 @@ SIGNATURES = {
     "gemm_quantize_rows_e4m3": ([_VP, _VP, _VP, _I, _I], _I),
     "gemm_e4m3_rowscale": ([_VP, _VP, _VP, _VP, _I, _I, _I], _I),
     "gemm_e4m3_rowscale_fused": ([_VP, _VP, _VP, _I, _I, _I], _I),
+    "gemm_fp4_code_bytes": ([_I, _I], ctypes.c_int64),
+    "gemm_fp4_scale_bytes": ([_I, _I, _I], ctypes.c_int64),
+    "gemm_fp4_quantize": ([_I, _I, _VP, ctypes.c_int64, _VP, _VP, _VP, _I, _I], _I),
+    "gemm_fp4_dequantize": ([_I, _I, _VP, _VP, _VP, _VP, ctypes.c_int64, _I, _I], _I),
+    "gemm_fp4": ([_I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64, _I, _I, _I], _I),
+    "gemm_fp4_linear": ([_I, _I, _VP, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64, _I, _I, _I], _I),
     "gemm_set_stream": ([_VP], _I),
     "gemm_get_stream": ([], _VP),
     "gemm_synchronize": ([], _I),
@@ -277,6 +283,96 @@ def gemm_ex(dtype: str, layout: str, op_a: str, op_b: str, M: int, N: int, K: in
                      float(beta), _addr(C), int(ldc), int(stride_c), int(batch))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_ex", lib.gemm_last_error().decode())
+
+
+FP4_FORMATS = {"mx": 0, "nv": 1}
+_DTYPES16 = {"f16": 1, "bf16": 2}
+
+
+def _fp4_enums(name: str, dtype: str, fmt: str):
+    if dtype not in _DTYPES16 or fmt not in FP4_FORMATS:
+        raise ValueError(f"{name}: dtype 'f16' | 'bf16' and format 'mx' | 'nv', got {dtype!r} and {fmt!r}")
+    return _DTYPES16[dtype], FP4_FORMATS[fmt]
+
+
+def gemm_fp4_code_bytes(rows: int, K: int) -> int:
+    """Bytes of the 4-bit codes of a [rows, K] matrix."""
+    return int(load().gemm_fp4_code_bytes(int(rows), int(K)))
+
+
+def gemm_fp4_scale_bytes(fmt: str, rows: int, K: int) -> int:
+    """Bytes of the block scales of a [rows, K] matrix in format 'mx' or 'nv'."""
+    return int(load().gemm_fp4_scale_bytes(FP4_FORMATS[fmt], int(rows), int(K)))
+
+
+def _check_fp4(name: str, lib, fmt: int, Q, S, g, rows: int, K: int, what: str = "") -> None:
+    """Codes, scales and tensor scale of a quantised [rows, K] operand (nothing
+    where a size is 0 or negative: the library returns or rejects the call)."""
+    some = rows > 0 and K > 0
+    _check(f"{name}: Q{what}", Q, 1, lib.gemm_fp4_code_bytes(rows, K) if some else 0)
+    _check(f"{name}: S{what}", S, 1, lib.gemm_fp4_scale_bytes(fmt, rows, K) if some else 0)
+    _check(f"{name}: tensor scale {what}", g, 4, 1 if some else 0)
+
+
+def gemm_fp4_quantize(dtype: str, fmt: str, A, lda: int, tensor_scale, Q, S, M: int, K: int) -> None:
+    """Quantises A [M,K] ('f16' | 'bf16', leading dimension lda) to 4-bit codes Q
+    and block scales S, format 'mx' or 'nv'; tensor_scale: one FP32 value on the
+    device for 'nv' (None: 1), None for 'mx'.  See include/gemm.h."""
+    lib = load()
+    d, f = _fp4_enums("gemm_fp4_quantize", dtype, fmt)
+    M, K, lda = int(M), int(K), int(lda)
+    _check("gemm_fp4_quantize: A", A, 2, _span(M, K, lda), tight=False)
+    _check_fp4("gemm_fp4_quantize", lib, f, Q, S, tensor_scale, M, K)
+    _bind_torch_stream(A, tensor_scale, Q, S)
+    st = lib.gemm_fp4_quantize(d, f, _addr(A), lda, _addr(tensor_scale), _addr(Q), _addr(S), M, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp4_quantize", lib.gemm_last_error().decode())
+
+
+def gemm_fp4_dequantize(dtype: str, fmt: str, Q, S, tensor_scale, A, lda: int, M: int, K: int) -> None:
+    """Writes the values that codes Q and scales S stand for to A [M,K]."""
+    lib = load()
+    d, f = _fp4_enums("gemm_fp4_dequantize", dtype, fmt)
+    M, K, lda = int(M), int(K), int(lda)
+    _check("gemm_fp4_dequantize: A", A, 2, _span(M, K, lda), tight=False)
+    _check_fp4("gemm_fp4_dequantize", lib, f, Q, S, tensor_scale, M, K)
+    _bind_torch_stream(A, tensor_scale, Q, S)
+    st = lib.gemm_fp4_dequantize(d, f, _addr(Q), _addr(S), _addr(tensor_scale), _addr(A), lda, M, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp4_dequantize", lib.gemm_last_error().decode())
+
+
+def gemm_fp4(dtype: str, fmt: str, Qa, Sa, ga, Qb, Sb, gb, C, ldc: int, M: int, N: int, K: int) -> None:
+    """C [M,N] ('f16' | 'bf16') = ga gb a b^T of two quantised matrices a [M,K] and
+    b [N,K] of format 'mx' or 'nv'."""
+    lib = load()
+    d, f = _fp4_enums("gemm_fp4", dtype, fmt)
+    M, N, K, ldc = int(M), int(N), int(K), int(ldc)
+    if M > 0 and N > 0:
+        _check_fp4("gemm_fp4", lib, f, Qa, Sa, ga, M, K, "a")
+        _check_fp4("gemm_fp4", lib, f, Qb, Sb, gb, N, K, "b")
+        _check("gemm_fp4: C", C, 2, _span(M, N, ldc), tight=False)
+    _bind_torch_stream(Qa, Sa, ga, Qb, Sb, gb, C)
+    st = lib.gemm_fp4(d, f, _addr(Qa), _addr(Sa), _addr(ga), _addr(Qb), _addr(Sb), _addr(gb), _addr(C), ldc, M, N, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp4", lib.gemm_last_error().decode())
+
+
+def gemm_fp4_linear(dtype: str, fmt: str, X, ldx: int, gx, Qw, Sw, gw, C, ldc: int, M: int, N: int, K: int) -> None:
+    """C [M,N] = X W^T with X [M,K] ('f16' | 'bf16', leading dimension ldx)
+    quantised within the call (tensor scale gx) and W [N,K] quantised already."""
+    lib = load()
+    d, f = _fp4_enums("gemm_fp4_linear", dtype, fmt)
+    M, N, K, ldx, ldc = int(M), int(N), int(K), int(ldx), int(ldc)
+    if M > 0 and N > 0:
+        _check("gemm_fp4_linear: X", X, 2, _span(M, K, ldx), tight=False)
+        _check("gemm_fp4_linear: tensor scale x", gx, 4, 1)
+        _check_fp4("gemm_fp4_linear", lib, f, Qw, Sw, gw, N, K, "w")
+        _check("gemm_fp4_linear: C", C, 2, _span(M, N, ldc), tight=False)
+    _bind_torch_stream(X, gx, Qw, Sw, gw, C)
+    st = lib.gemm_fp4_linear(d, f, _addr(X), ldx, _addr(gx), _addr(Qw), _addr(Sw), _addr(gw), _addr(C), ldc, M, N, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp4_linear", lib.gemm_last_error().decode())
 
 
 def gemm_set_stream(stream) -> None:

@@ -4,11 +4,13 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdio.h>
 #include <string.h>
 
 #include <atomic>
 #include <mutex>
 
+#include "fp4.h"
 #include "gemm.h"
 #include "internal.h"
 
@@ -387,6 +389,120 @@ gemm_status_t run_ex(int dtype, int layout, int op_a, int op_b, int M, int N, in
     return finish(launch_simt_ex(p, s), simt_name);
 }
 
+// ------------------------------------------------------------ 4-bit block scales
+// What the four entry points share: types, format, and the codes' and scales'
+// sizes of a [rows, K] matrix (0 where nothing is stored).
+bool fp4_types_ok(int dtype, int format) {
+    return (dtype == GEMM_F16 || dtype == GEMM_BF16) && (format == GEMM_FP4_MX || format == GEMM_FP4_NV);
+}
+Elt elt16(int dtype) { return dtype == GEMM_BF16 ? Elt::BF16 : Elt::F16; }
+size_t fp4_code_size(int rows, int K) { return K > 0 ? (size_t)rows * fp4_row_bytes(K) : 0; }
+
+// Checks of a quantised operand: codes and scales present and 16-byte aligned,
+// a tensor scale only where the format has one.
+bool fp4_operand_ok(const char *who, int format, const void *Q, const void *S, const float *g) {
+    if (!Q || !S) return false;
+    if (!aligned16(Q) || !aligned16(S)) {
+        snprintf(t_last_error, sizeof(t_last_error), "%s: codes and scales need 16-byte alignment", who);
+        return false;
+    }
+    if (format == GEMM_FP4_MX && g) {
+        snprintf(t_last_error, sizeof(t_last_error), "%s: the MX format has no tensor scale", who);
+        return false;
+    }
+    return true;
+}
+
+// Quantise (to_codes) or read back: A [M,K] with leading dimension lda.
+gemm_status_t run_fp4_convert(const char *who, bool to_codes, int dtype, int format, const void *A, int64_t lda,
+                              const float *g, const void *Q, const void *S, int M, int K) {
+    if (!fp4_types_ok(dtype, format) || M < 0 || K < 0 || lda < (K > 1 ? K : 1)) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || K == 0) { t_last_kernel = "noop"; return GEMM_OK; }
+    if (!A || !fp4_operand_ok(who, format, Q, S, g)) return GEMM_ERR_INVALID_VALUE;
+    const bool nv = format == GEMM_FP4_NV;
+    long long span = 0;
+    if (!span_elems(1, 0, M, lda, K, &span) || span > (1LL << 61)) return GEMM_ERR_INVALID_VALUE;
+    const size_t a = (size_t)span * 2, q = fp4_code_size(M, K), sc = (size_t)fp4_scale_size(nv, M, K), gs = g ? 4 : 0;
+    if (overlaps(A, a, Q, q) || overlaps(A, a, S, sc) || overlaps(Q, q, S, sc)) return GEMM_ERR_ALIAS;
+    if (to_codes ? overlaps(g, gs, Q, q) || overlaps(g, gs, S, sc) : overlaps(g, gs, A, a)) return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    if (to_codes)
+        return finish(launch_fp4_quantize(elt16(dtype), nv, A, lda, g, const_cast<void *>(Q), const_cast<void *>(S),
+                                          M, K, t_stream),
+                      nv ? "fp4_quantize_nv" : "fp4_quantize_mx");
+    return finish(launch_fp4_dequantize(elt16(dtype), nv, Q, S, g, const_cast<void *>(A), lda, M, K, t_stream),
+                  nv ? "fp4_dequantize_nv" : "fp4_dequantize_mx");
+}
+
+// The product of two quantised matrices; X non-null: the first operand is
+// X [M,K] in dtype, quantised within the call.
+gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int64_t ldx, const void *Qa,
+                      const void *Sa, const float *ga, const void *Qb, const void *Sb, const float *gb, void *C,
+                      int64_t ldc, int M, int N, int K, bool linear) {
+    if (!fp4_types_ok(dtype, format) || M < 0 || N < 0 || K < 0 || ldc < (N > 1 ? N : 1)) return GEMM_ERR_INVALID_VALUE;
+    if (linear && ldx < (K > 1 ? K : 1)) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0) { t_last_kernel = "noop"; return GEMM_OK; }
+    if (!C) return GEMM_ERR_INVALID_VALUE;
+    const bool nv = format == GEMM_FP4_NV;
+    const Elt elt = elt16(dtype);
+    long long span = 0, x_span = 0;
+    if (!span_elems(1, 0, M, ldc, N, &span) || span > (1LL << 61)) return GEMM_ERR_INVALID_VALUE;
+    const size_t c = (size_t)span * 2;
+    if (K > 0) {
+        if (!fp4_operand_ok(who, format, Qb, Sb, gb)) return GEMM_ERR_INVALID_VALUE;
+        if (linear) {
+            if (!X || (format == GEMM_FP4_MX && ga)) return GEMM_ERR_INVALID_VALUE;
+            if (!span_elems(1, 0, M, ldx, K, &x_span) || x_span > (1LL << 61)) return GEMM_ERR_INVALID_VALUE;
+            if (overlaps(C, c, X, (size_t)x_span * 2)) return GEMM_ERR_ALIAS;
+        } else {
+            if (!fp4_operand_ok(who, format, Qa, Sa, ga)) return GEMM_ERR_INVALID_VALUE;
+            if (overlaps(C, c, Qa, fp4_code_size(M, K)) || overlaps(C, c, Sa, (size_t)fp4_scale_size(nv, M, K)))
+                return GEMM_ERR_ALIAS;
+        }
+        if (overlaps(C, c, Qb, fp4_code_size(N, K)) || overlaps(C, c, Sb, (size_t)fp4_scale_size(nv, N, K)) ||
+            overlaps(C, c, ga, ga ? 4 : 0) || overlaps(C, c, gb, gb ? 4 : 0))
+            return GEMM_ERR_ALIAS;
+    }
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    cudaStream_t s = t_stream;
+    if (K == 0) {  // the empty sum
+        const unsigned grid = (unsigned)(dev->num_sms * 8);
+        note_launch();
+        scale_c_kernel<<<grid, 256, 0, s>>>((__half *)C, M, N, ldc, 0, 1, 0.0f);
+        return finish(cudaGetLastError(), "zero_fill");
+    }
+    Fp4Problem p = {};
+    p.Qa = Qa;
+    p.Sa = Sa;
+    p.Qb = Qb;
+    p.Sb = Sb;
+    p.ga = ga;
+    p.gb = gb;
+    p.C = C;
+    p.ldc = ldc;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.elt = elt;
+    p.nv = nv;
+    if (!linear) return finish(launch_fp4_gemm(p, dev->num_sms, dev->status, s), nv ? "fp4_gemm_nv" : "fp4_gemm_mx");
+    // X's codes and scales in stream-ordered scratch for the duration of the call
+    const size_t q = (fp4_code_size(M, K) + 255) & ~(size_t)255;
+    void *ws = nullptr;
+    cudaError_t e = cudaMallocAsync(&ws, q + (size_t)fp4_scale_size(nv, M, K), s);
+    if (e != cudaSuccess) return finish(e, "fp4_linear");
+    p.Qa = ws;
+    p.Sa = static_cast<uint8_t *>(ws) + q;
+    e = launch_fp4_quantize(elt, nv, X, ldx, ga, ws, static_cast<uint8_t *>(ws) + q, M, K, s);
+    if (e == cudaSuccess) e = launch_fp4_gemm(p, dev->num_sms, dev->status, s);
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    return finish(e != cudaSuccess ? e : f, nv ? "fp4_linear_nv" : "fp4_linear_mx");
+}
+
 }  // namespace
 
 extern "C" {
@@ -545,6 +661,40 @@ GEMM_API gemm_status_t gemm_e4m3_rowscale_fused(const uint16_t *A, const uint8_t
         return GEMM_ERR_INVALID_VALUE;
     }
     return finish(e, "umma_e4m3_rowscale_fused");
+}
+
+GEMM_API int64_t gemm_fp4_code_bytes(int rows, int K) {
+    if (rows < 0 || K < 0) return -1;
+    return (int64_t)fp4_code_size(rows, K);
+}
+
+GEMM_API int64_t gemm_fp4_scale_bytes(gemm_fp4_format_t format, int rows, int K) {
+    if (rows < 0 || K < 0 || ((int)format != GEMM_FP4_MX && (int)format != GEMM_FP4_NV)) return -1;
+    return fp4_scale_size((int)format == GEMM_FP4_NV, rows, K);
+}
+
+GEMM_API gemm_status_t gemm_fp4_quantize(gemm_dtype_t dtype, gemm_fp4_format_t format, const void *A, int64_t lda,
+                                         const float *tensor_scale, uint8_t *Q, uint8_t *S, int M, int K) {
+    return run_fp4_convert("gemm_fp4_quantize", true, (int)dtype, (int)format, A, lda, tensor_scale, Q, S, M, K);
+}
+
+GEMM_API gemm_status_t gemm_fp4_dequantize(gemm_dtype_t dtype, gemm_fp4_format_t format, const uint8_t *Q,
+                                           const uint8_t *S, const float *tensor_scale, void *A, int64_t lda, int M,
+                                           int K) {
+    return run_fp4_convert("gemm_fp4_dequantize", false, (int)dtype, (int)format, A, lda, tensor_scale, Q, S, M, K);
+}
+
+GEMM_API gemm_status_t gemm_fp4(gemm_dtype_t dtype, gemm_fp4_format_t format, const uint8_t *Qa, const uint8_t *Sa,
+                                const float *ga, const uint8_t *Qb, const uint8_t *Sb, const float *gb, void *C,
+                                int64_t ldc, int M, int N, int K) {
+    return run_fp4("gemm_fp4", (int)dtype, (int)format, nullptr, 0, Qa, Sa, ga, Qb, Sb, gb, C, ldc, M, N, K, false);
+}
+
+GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t format, const void *X, int64_t ldx,
+                                       const float *gx, const uint8_t *Qw, const uint8_t *Sw, const float *gw,
+                                       void *C, int64_t ldc, int M, int N, int K) {
+    return run_fp4("gemm_fp4_linear", (int)dtype, (int)format, X, ldx, nullptr, nullptr, gx, Qw, Sw, gw, C, ldc, M, N,
+                   K, true);
 }
 
 GEMM_API gemm_status_t gemm_set_stream(void *cuda_stream) {

@@ -257,6 +257,69 @@ GEMM_API gemm_status_t gemm_e4m3_rowscale(const uint8_t *Q, const float *scale, 
 GEMM_API gemm_status_t gemm_e4m3_rowscale_fused(const uint16_t *A, const uint8_t *Wt, uint16_t *C,
                                                 int M, int N, int K);
 
+/* 4-bit block-scaled floating point.  A matrix [rows, K] is kept as codes and
+ * scales; its rows are cut along K into blocks that share a scale.
+ *
+ *   GEMM_FP4_MX  blocks of 32, the scale a power of two (an E8M0 byte e + 127,
+ *                255 = NaN): the OCP microscaling format MXFP4;
+ *   GEMM_FP4_NV  blocks of 16, the scale an E4M3FN byte, and one FP32 scale g of
+ *                the whole tensor (in device memory, so that it can be computed
+ *                there; null: 1).
+ *
+ * Codes are E2M1 (a sign and 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the even
+ * k in the low half.  A row takes 16 * ceil(K / 32) bytes; the codes past K are 0.
+ * Scale bytes lie in atoms of 128 rows x 4 blocks, 512 bytes each, at
+ *     atom (row / 128) * A + block / 4,  A = 2 (MX) or 4 (NV) * ceil(K / 256)
+ *     byte (row % 32) * 16 + (row / 32 % 4) * 4 + block % 4
+ * -- the order in which the tensor cores take them.  gemm_fp4_code_bytes and
+ * gemm_fp4_scale_bytes give the sizes (-1 for a negative size or an unknown
+ * format).  Codes and scales need 16-byte alignment (GEMM_ERR_INVALID_VALUE
+ * otherwise, with a message in gemm_last_error); everything else may have any
+ * alignment and any K, M, N.
+ *
+ * For a block with the largest magnitude amax, a / step rounded to the nearest
+ * code (ties to the even code, saturating at 6), in FP32 operations:
+ *   MX  step = 2^e, e = clamp(floor(log2 amax) - 2, -127, 125);
+ *   NV  s = E4M3(amax / (6 g)), nearest, saturating at 448; step = s g; codes of
+ *       0 where the step is 0.
+ * A NaN or an infinity in a block makes the block's scale NaN and its codes 0:
+ * the block reads back as NaN, and products that use it are NaN. */
+typedef enum gemm_fp4_format_t { GEMM_FP4_MX = 0, GEMM_FP4_NV = 1 } gemm_fp4_format_t;
+
+GEMM_API int64_t gemm_fp4_code_bytes(int rows, int K);
+GEMM_API int64_t gemm_fp4_scale_bytes(gemm_fp4_format_t format, int rows, int K);
+
+/* Quantises A [M,K] (half or bf16 by dtype, row-major, leading dimension
+ * lda >= K) to codes Q and scales S.  tensor_scale: NV's g; must be null for MX.
+ * The scale bytes of rows past M and blocks past K, up to the padded sizes, are
+ * written too (those of zeros).  GEMM_ERR_ALIAS if A, Q, S overlap. */
+GEMM_API gemm_status_t gemm_fp4_quantize(gemm_dtype_t dtype, gemm_fp4_format_t format, const void *A, int64_t lda,
+                                         const float *tensor_scale, uint8_t *Q, uint8_t *S, int M, int K);
+
+/* Reads codes and scales back: A[i,k] = code * scale (* g), formed in FP32 and
+ * rounded once to dtype. */
+GEMM_API gemm_status_t gemm_fp4_dequantize(gemm_dtype_t dtype, gemm_fp4_format_t format, const uint8_t *Q,
+                                           const uint8_t *S, const float *tensor_scale, void *A, int64_t lda, int M,
+                                           int K);
+
+/* Product of two quantised matrices of one format:
+ *     C[i,j] = ga gb * sum_k a[i,k] b[j,k]
+ * with a [M,K] and b [N,K] the values code * scale, summed in FP32 and rounded
+ * once to dtype (half or bf16).  b is a linear layer's weight: every output
+ * column's K codes contiguous.  C [M,N] row-major with ldc >= N.  K = 0 gives
+ * C = 0.  GEMM_ERR_ALIAS if C overlaps an input. */
+GEMM_API gemm_status_t gemm_fp4(gemm_dtype_t dtype, gemm_fp4_format_t format, const uint8_t *Qa, const uint8_t *Sa,
+                                const float *ga, const uint8_t *Qb, const uint8_t *Sb, const float *gb, void *C,
+                                int64_t ldc, int M, int N, int K);
+
+/* A linear layer with 4-bit weights: X [M,K] (dtype, ldx >= K) quantised within
+ * the call as gemm_fp4_quantize does with tensor scale gx, then the product
+ * with the quantised weights [N,K].  The codes and scales of X are kept in the
+ * device's default stream-ordered pool for the duration of the call. */
+GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t format, const void *X, int64_t ldx,
+                                       const float *gx, const uint8_t *Qw, const uint8_t *Sw, const float *gw,
+                                       void *C, int64_t ldc, int M, int N, int K);
+
 /* Stream for the calling host thread's subsequent calls: a cudaStream_t passed
  * as void*.  NULL selects the legacy default stream.  The stream stays owned by
  * the caller and must outlive the calls issued on it. */
