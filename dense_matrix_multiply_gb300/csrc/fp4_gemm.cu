@@ -1,75 +1,444 @@
-// Product of two 4-bit block-scaled matrices on the CUDA cores: 64 x 64 tiles
-// of C, both operands decoded to FP32 in shared memory 32 k at a time.
+// Product of two 4-bit block-scaled matrices on the tensor cores:
+//     C[i,j] = ga gb sum_k (qa sa)[i,k] (qb sb)[j,k]
+// tcgen05 kind::mxf4nvf4 with block scales: the MMA multiplies E2M1 codes,
+// applies both blocks' scales to each partial sum and accumulates in FP32
+// tensor memory; the tensors' FP32 scales are applied once, in the epilogue,
+// before the one rounding to the output type.
+//
+// A 256 x bn tile of C belongs to a cluster of two CTAs (cta_group::2): CTA r
+// holds rows [128 r, 128 r + 128) of A's tile and its half of B's, and both
+// hold the scales of their own 128 rows of A and of all of B's rows.  A stage is
+// 256 k: 128 bytes a row, the 128-byte swizzle of 8- and 16-bit operands; four
+// MMAs of K = 64.  The scales' atoms of 128 rows x 4 blocks (512 bytes) go to
+// tensor memory with tcgen05.cp 32x128b.warpx4, in the order in which they are
+// stored: row % 32 is the lane, row / 32 the column, and the four bytes of a
+// column four blocks.  NV (16 k a block): an atom is one MMA's K.  MX (32 k): an
+// atom serves two MMAs, which read bytes 0-1 and 2-3 (the descriptor's scale id).
+// cp and mma of one thread execute in order, so the scales need no second copy.
+//
+// Warps: 0 loads (TMA; every load of the pair counts on the leader's full[s]), 1
+// issues the MMAs (leader), 2-5 write C.  Accumulators: bn = 256 has two that
+// share 64 columns (tensor memory holds 512: 448 of them, and 64 for the
+// scales); the epilogue reads the shared ones first, then lets the next tile's
+// MMAs start.  bn = 128: two apart.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
 #include "fp4.h"
+#include "tc_ptx.cuh"
 
 namespace gemm_gb300 {
 namespace {
 
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void put(__half *p, float x) { *p = __float2half_rn(x); }
+using namespace tc;
+
+constexpr int THREADS = 192;
+constexpr int STAGES = 5;
+constexpr int KB = 256;                  // k per stage
+constexpr int A_STAGE = 128 * KB / 2;    // 16 KiB per CTA
+constexpr int B_STAGE = 128 * KB / 2;    // 16 KiB per CTA (bn = 128: half of it)
+constexpr int STG_BOX = 32 * 64 * 2;     // one 32-row x 64-column output box
+constexpr int SMEM_STAGING = 4 * 2 * STG_BOX;
+constexpr uint32_t TMEM_COLS = 512, SF_COL = 448;
+constexpr int GROUP_M = 8;
+
+__host__ __device__ constexpr int sf_stage(bool nv) { return nv ? 2048 : 1024; }  // of 128 rows
+__host__ __device__ constexpr int stage_bytes(bool nv) { return A_STAGE + B_STAGE + 3 * sf_stage(nv); }
+__host__ __device__ constexpr int smem_bytes(bool nv) { return 1024 + STAGES * stage_bytes(nv) + SMEM_STAGING + 256; }
+static_assert(smem_bytes(true) <= 232448, "shared memory budget");
+
+struct Bars {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
+    uint64_t peer_done;
+    long long peer_issued;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+struct Args {
+    void *C;
+    long long ldc;
+    const float *ga, *gb;
+    int M, N, K;
+    int bn;         // 128 or 256
+    int tma_store;  // C's rows suit TMA stores
+    int *status;
+};
+
+// D[tmem of both CTAs] (+)= A B^T over one K step of 64, scales in tensor memory.
+template <bool NV>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         uint32_t acc) {
+    if constexpr (NV)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::
+                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::
+                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(acc)
+            : "memory");
+}
+// One atom of scales (512 bytes) from shared memory to four columns, in both CTAs.
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+// Instruction descriptor: E2M1 x E2M1, both K-major, scale type E8M0 (MX) or
+// E4M3 (NV), M = 256, N = bn, scale ids `id` in A and B.
+template <bool NV>
+__device__ __forceinline__ uint32_t make_idesc(uint32_t bn, uint32_t id) {
+    return (id << 4) | (1u << 7) | (1u << 10) | ((bn >> 3) << 17) | ((NV ? 0u : 1u) << 23) | ((256u >> 4) << 24) |
+           (id << 29);
+}
+
+__device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int &tm, int &tn) {
+    const int per_group = GROUP_M * tiles_n;
+    const int group = t / per_group;
+    const int first_m = group * GROUP_M;
+    const int gsize = min(tiles_m - first_m, GROUP_M);
+    const int r = t - group * per_group;
+    tm = first_m + r % gsize;
+    tn = r / gsize;
+}
 
 template <typename T, bool NV>
-__global__ void __launch_bounds__(256) fp4_simt_kernel(const Fp4Problem p)
+__global__ void __launch_bounds__(THREADS, 1)
+fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSa,
+                const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmSb,
+                const __grid_constant__ CUtensorMap tmC, const Args args)
 {
-    pdl_wait();
-    __shared__ float a_s[32][65], b_s[32][65];
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int r = threadIdx.x >> 2, c = threadIdx.x & 3;  // row of the tile, group of 8 k
-    const int atoms = fp4_atoms(NV, p.K);
-    constexpr int B = fp4_block(NV);
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += 32) {
-        const int k = k0 + c * 8;
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            const int row = (side ? n0 : m0) + r;
-            float v[8] = {};
-            if (row < (side ? p.N : p.M)) {
-                const uint8_t *q = static_cast<const uint8_t *>(side ? p.Qb : p.Qa);
-                const uint8_t *s = static_cast<const uint8_t *>(side ? p.Sb : p.Sa);
-                const uint32_t byte = s[fp4_scale_at(row, k / (4 * B), atoms) + (k / B & 3)];
-                fp4_unpack8(*reinterpret_cast<const uint32_t *>(q + row * fp4_row_bytes(p.K) + k / 2),
-                            fp4_scale_value<NV>(byte), v);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) (side ? b_s : a_s)[c * 8 + i][r] = v[i];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int SF = sf_stage(NV), SF_STAGE = 3 * SF;
+    uint8_t *a_tiles = smem;
+    uint8_t *b_tiles = a_tiles + STAGES * A_STAGE;
+    uint8_t *sf_tiles = b_tiles + STAGES * B_STAGE;  // per stage: A's 128 rows, then B's 128 or 256
+    uint8_t *staging = sf_tiles + STAGES * SF_STAGE;
+    Bars *bars = reinterpret_cast<Bars *>(staging + SMEM_STAGING);
+    volatile int *abort_flag = &bars->abort;
+
+    const int M = args.M, N = args.N, bn = args.bn;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
+    const int tiles_m = (M + 255) / 256, tiles_n = (N + bn - 1) / bn;
+    const int num_tiles = tiles_m * tiles_n;
+    const int num_kb = (args.K + KB - 1) / KB;
+    const bool wide = bn == 256;
+    const int halves = wide ? 2 : 1;  // of B's scales, 128 rows each
+    // both CTAs' loads of a stage, all counted on the leader's barrier
+    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (bn >> 1) * (KB / 2) + (1 + halves) * SF);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
         }
-        __syncthreads();
-#pragma unroll
-        for (int kk = 0; kk < 32; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a_s[kk][ty + 16 * i], b_s[kk][tx + 16 * j], acc[i][j]);
-        __syncthreads();
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 256);
+        }
+        mbar_init(&bars->drain, 1);
+        mbar_init(&bars->peer_done, 1);
+        bars->abort = 0;
+        mbar_init_fence();
+        prefetch_desc(&tmA);
+        prefetch_desc(&tmB);
+        prefetch_desc(&tmSa);
+        prefetch_desc(&tmSb);
+        prefetch_desc(&tmC);
     }
-    const float f = NV ? (p.ga ? *p.ga : 1.0f) * (p.gb ? *p.gb : 1.0f) : 1.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < p.M && n < p.N) put(static_cast<T *>(p.C) + m * p.ldc + n, acc[i][j] * f);
+    if (warp == 1) tmem_alloc<2>(&bars->tmem_base, TMEM_COLS);
+    fence_before();
+    cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
+    fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------------ producer (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        for (int t = cluster; t < num_tiles && ok; t += nclusters) {
+            int tm, tn;
+            tile_coords(t, tiles_m, tiles_n, tm, tn);
+            const int row0 = tm * 256 + (int)rank * 128, col0 = tn * bn + (int)rank * (bn >> 1);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
+                const uint32_t full = map_to_rank(&bars->full[stage], 0);
+                if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
+                uint8_t *sf = sf_tiles + stage * SF_STAGE;
+                tma_load_3d_pair(a_tiles + stage * A_STAGE, &tmA, full, kb * (KB / 2), row0, 0);
+                tma_load_3d_pair(b_tiles + stage * B_STAGE, &tmB, full, kb * (KB / 2), col0, 0);
+                tma_load_3d_pair(sf, &tmSa, full, 0, kb * (SF / 1024), row0 / 128);
+                tma_load_3d_pair(sf + SF, &tmSb, full, 0, kb * (SF / 1024), tn * halves);
+                ++issued;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
         }
+        if (!ok) {
+            atomicOr(args.status, ST_PRODUCER);
+            raise_abort_pair(abort_flag, rank);
+        }
+        // No load is left in flight into either CTA when the pair ends: the peer
+        // tells the leader how many stages it loaded, and the leader waits until
+        // every stage that either loaded has landed (the half that a side which
+        // gave up never loaded is counted as done, or never armed).
+        if (!leader) {
+            st_cluster_s64(map_to_rank(&bars->peer_issued, 0), issued);
+            mbar_arrive_cluster(map_to_rank(&bars->peer_done, 0));  // release: the count is visible first
+        } else {
+            long long ip = issued;
+            if (mbar_wait(&bars->peer_done, 0, abort_flag, false))
+                ip = *reinterpret_cast<volatile long long *>(&bars->peer_issued);
+            else
+                atomicOr(args.status, ST_DRAIN);
+            const long long hi = issued > ip ? issued : ip;
+            for (long long i = (hi > STAGES ? hi - STAGES : 0); i < hi; ++i) {
+                const int s = (int)(i % STAGES);
+                if (i >= issued) mbar_arrive_expect_tx(&bars->full[s], stage_tx / 2);
+                else if (i >= ip) mbar_complete_tx(&bars->full[s], stage_tx / 2);
+                if (!mbar_wait(&bars->full[s], (uint32_t)((i / STAGES) & 1), abort_flag, false)) {
+                    atomicOr(args.status, ST_DRAIN);
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------------------------------------ MMA issuer (leader)
+        const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), 16, 1024);
+        const uint64_t b_desc0 = desc_sw128(smem_u32(b_tiles), 16, 1024);
+        const uint64_t sf_desc0 = desc_plain(smem_u32(sf_tiles), 128);
+        constexpr int ATOMS = SF / 512;  // of a stage: 4 (NV) or 2 (MX)
+        const uint32_t sfa = tmem_base + SF_COL, sfb = sfa + 4 * ATOMS;
+        const uint32_t idesc0 = make_idesc<NV>((uint32_t)bn, 0), idesc1 = make_idesc<NV>((uint32_t)bn, 2);
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;
+        bool ok = true;
+        for (int t = cluster; t < num_tiles; t += nclusters, ++it) {
+            const int buf = it & 1;
+            // wide: tile it - 1's shared columns have been read (and so all of it - 2)
+            if (wide) {
+                if (it > 0 && !mbar_wait(&bars->acc_empty[buf ^ 1], (uint32_t)(((it - 1) >> 1) & 1), abort_flag, true))
+                    ok = false;
+            } else if (!mbar_wait(&bars->acc_empty[buf], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, true)) {
+                ok = false;
+            }
+            if (!ok) break;
+            fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(buf * 192);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait(&bars->full[stage], phase, abort_flag, true)) { ok = false; break; }
+                fence_after();
+                const uint64_t ad = a_desc0 + (uint64_t)((stage * A_STAGE) >> 4);
+                const uint64_t bd = b_desc0 + (uint64_t)((stage * B_STAGE) >> 4);
+                const uint64_t sd = sf_desc0 + (uint64_t)((stage * SF_STAGE) >> 4);
+#pragma unroll
+                for (int a = 0; a < ATOMS; ++a) {
+                    cp_scales_pair(sfa + 4 * a, sd + a * 32);
+                    cp_scales_pair(sfb + 4 * halves * a, sd + (ATOMS + a) * 32);
+                    if (wide) cp_scales_pair(sfb + 4 * halves * a + 4, sd + (2 * ATOMS + a) * 32);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    const int a = NV ? ks : ks >> 1;
+                    mma_pair<NV>(d, ad + ks * 2, bd + ks * 2, NV || (ks & 1) == 0 ? idesc0 : idesc1, sfa + 4 * a,
+                                 sfb + 4 * halves * a, (uint32_t)((kb | ks) != 0));
+                }
+                commit_pair_multicast(&bars->empty[stage]);
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            commit_pair_multicast(&bars->acc_full[buf]);
+        }
+        if (!ok) {
+            atomicOr(args.status, ST_MMA);
+            raise_abort_pair(abort_flag, rank);
+        }
+        commit<2>(&bars->drain);
+        if (!mbar_wait(&bars->drain, 0, abort_flag, false)) atomicOr(args.status, ST_DRAIN);
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue (both CTAs)
+        const int quarter = warp & 3;
+        uint8_t *my_stg = staging + quarter * 2 * STG_BOX;
+        const float scale = NV ? (args.ga ? *args.ga : 1.0f) * (args.gb ? *args.gb : 1.0f) : 1.0f;
+        const int groups = bn >> 6;
+        int sb = 0, it = 0;
+        bool ok = true;
+        for (int t = cluster; t < num_tiles; t += nclusters, ++it) {
+            int tm, tn;
+            tile_coords(t, tiles_m, tiles_n, tm, tn);
+            const int buf = it & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (uint32_t)((it >> 1) & 1), abort_flag, true))) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            __syncwarp();
+            const int row0 = tm * 256 + (int)rank * 128 + quarter * 32;
+            const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 192);
+            for (int i = 0; i < groups; ++i) {
+                // the columns shared with the other accumulator first: this one's last (buf 0) or first (buf 1)
+                const int g = wide && buf == 0 ? (i + 3) & 3 : i;
+                const int c0 = tn * bn + g * 64;
+                uint32_t r0[32], r1[32];
+                if (c0 < N) {  // warp-uniform
+                    tmem_ld32(t_row + (uint32_t)(g * 64), r0);
+                    tmem_ld32(t_row + (uint32_t)(g * 64 + 32), r1);
+                    tmem_ld_wait();
+                }
+                if (wide ? i == 0 : i == groups - 1) {
+                    fence_before();
+                    mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], 0));
+                }
+                if (c0 >= N) continue;
+                if (lane == 0 && args.tma_store) tma_stores_read_wait1();  // the store of two boxes ago has read its box
+                __syncwarp();
+                uint8_t *box = my_stg + sb * STG_BOX;
+                uint8_t *rowp = box + lane * 128;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint32_t *src = c < 4 ? &r0[8 * c] : &r1[8 * (c - 4)];
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = scale * __uint_as_float(src[e]);
+                    uint4 w;
+                    w.x = pack2(v[0], v[1], (T *)nullptr);
+                    w.y = pack2(v[2], v[3], (T *)nullptr);
+                    w.z = pack2(v[4], v[5], (T *)nullptr);
+                    w.w = pack2(v[6], v[7], (T *)nullptr);
+                    *reinterpret_cast<uint4 *>(rowp + ((c ^ (lane & 7)) << 4)) = w;
+                }
+                if (args.tma_store) {
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0 && row0 < M) tma_store_3d(&tmC, box, c0, row0, 0);
+                } else {
+                    // rows that TMA cannot write: 64 columns of a row by the warp, two passes
+                    __syncwarp();
+                    for (int r = 0; r < 32 && row0 + r < M; ++r) {
+                        T *crow = static_cast<T *>(args.C) + (long long)(row0 + r) * args.ldc + c0;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = h * 32 + lane;
+                            if (c0 + c < N)
+                                crow[c] = *reinterpret_cast<const T *>(box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) +
+                                                                       (c & 7) * 2);
+                        }
+                    }
+                }
+                sb ^= 1;
+            }
+        }
+        if (lane == 0) tma_stores_wait0();
+        if (!ok && lane == 0) {
+            atomicOr(args.status, ST_EPILOGUE);
+            raise_abort_pair(abort_flag, rank);
+        }
+    }
+
+    __syncwarp();
+    fence_before();
+    cluster_sync();  // no CTA leaves while its peer may still touch its memory
+    if (warp == 1) {
+        fence_after();
+        tmem_dealloc<2>(tmem_base, TMEM_COLS);
+    }
+}
+
+template <typename T, bool NV>
+int clusters_max(int dev) {
+    static std::atomic<int> cached[kMaxDevices];
+    static std::once_flag once[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        cached[dev].store(max_clusters(reinterpret_cast<const void *>(fp4_pair_kernel<T, NV>), THREADS, smem_bytes(NV), 2));
+    });
+    return cached[dev].load();
+}
+
+template <typename T, bool NV>
+cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const int cmax = clusters_max<T, NV>(dev);
+    if (cmax <= 0) return cudaErrorNotSupported;
+    // The tile's width: the one with fewer waves of work, the wide one on ties.
+    const long long tiles_m = (p.M + 255LL) / 256, n256 = tiles_m * ((p.N + 255LL) / 256),
+                    n128 = tiles_m * ((p.N + 127LL) / 128);
+    const int bn = (n128 + cmax - 1) / cmax < 2 * ((n256 + cmax - 1) / cmax) ? 128 : 256;
+    const long long tiles = bn == 256 ? n256 : n128;
+    if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const long long rb = fp4_row_bytes(p.K);
+    const long long chunks = (long long)fp4_atoms(NV, p.K) / 2;  // of 1024 bytes, a tile of 128 rows
+    constexpr int SFC = sf_stage(NV) / 1024;
+    CUtensorMap ta, tsa, tb, tsb, tc;
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const auto u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+    if (!make_map3(&ta, p.Qa, u8, rb, p.M, 1, rb, rb * p.M, 128, 128, 1, true) ||
+        !make_map3(&tb, p.Qb, u8, rb, p.N, 1, rb, rb * p.N, 128, bn / 2, 1, true) ||
+        !make_map3(&tsa, p.Sa, u32, 256, chunks, fp4_row_tiles(p.M), 1024, chunks * 1024, 256, SFC, 1, false) ||
+        !make_map3(&tsb, p.Sb, u32, 256, chunks, fp4_row_tiles(p.N), 1024, chunks * 1024, 256, SFC, bn / 128, false))
+        return cudaErrorInvalidValue;
+    Args a = {};
+    a.C = p.C;
+    a.ldc = p.ldc;
+    a.ga = p.ga;
+    a.gb = p.gb;
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.bn = bn;
+    a.status = status;
+    // TMA stores write whole 16-byte pieces of rows that start on 16 bytes.
+    a.tma_store = ((uintptr_t)p.C & 15u) == 0 && p.ldc % 8 == 0 && p.N % 8 == 0;
+    if (a.tma_store) {
+        const auto dt = p.elt == Elt::BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+        if (!make_map3(&tc, p.C, dt, p.N, p.M, 1, p.ldc * 2, p.ldc * 2 * p.M, 64, 32, 1, true)) a.tma_store = 0;
+    }
+    if (!a.tma_store) tc = tb;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * std::min<long long>(tiles, cmax)), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem_bytes(NV);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    pdl_attr(attr[1]);
+    cfg.attrs = attr;
+    cfg.numAttrs = g_pdl ? 2 : 1;
+    return launch_counted(&cfg, fp4_pair_kernel<T, NV>, ta, tsa, tb, tsb, tc, a);
 }
 
 }  // namespace
 
 cudaError_t launch_fp4_gemm(const Fp4Problem &p, int num_sms, int *status, cudaStream_t s) {
     (void)num_sms;
-    (void)status;
-    const dim3 grid((unsigned)((p.N + 63LL) / 64), (unsigned)((p.M + 63LL) / 64));
-    if (grid.y > 65535) return cudaErrorInvalidValue;
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pdl_config(grid, dim3(256), 0, s, attr);
     if (p.elt == Elt::BF16)
-        return p.nv ? launch_counted(&cfg, fp4_simt_kernel<__nv_bfloat16, true>, p)
-                    : launch_counted(&cfg, fp4_simt_kernel<__nv_bfloat16, false>, p);
-    return p.nv ? launch_counted(&cfg, fp4_simt_kernel<__half, true>, p)
-                : launch_counted(&cfg, fp4_simt_kernel<__half, false>, p);
+        return p.nv ? launch_pair<__nv_bfloat16, true>(p, status, s) : launch_pair<__nv_bfloat16, false>(p, status, s);
+    return p.nv ? launch_pair<__half, true>(p, status, s) : launch_pair<__half, false>(p, status, s);
 }
 
 }  // namespace gemm_gb300
