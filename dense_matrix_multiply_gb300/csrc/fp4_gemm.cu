@@ -15,6 +15,10 @@
 // column four blocks.  NV (16 k a block): an atom is one MMA's K.  MX (32 k): an
 // atom serves two MMAs, which read bytes 0-1 and 2-3 (the descriptor's scale id).
 // cp and mma of one thread execute in order, so the scales need no second copy.
+// The issuing warp stays converged and elects a lane for the tcgen05 instructions
+// only: with a loop run by one lane alone, the descriptors are moved to uniform
+// registers anew for every instruction, 23-25 ns a copy of an atom, and the tensor
+// cores wait for the issue (8192^3 NV 312 us, MX 236; so 162 and 164).
 //
 // Warps: 0 loads (TMA; every load of the pair counts on the leader's full[s]), 1
 // issues the MMAs (leader), 2-5 write C.  Accumulators: bn = 256 has two that
@@ -131,7 +135,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     volatile int *abort_flag = &bars->abort;
 
     const int M = args.M, N = args.N, bn = args.bn;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
@@ -221,8 +225,11 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
             }
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ------------------------------------------------------------ MMA issuer (leader)
+        // The whole warp runs the loop, so that descriptors stay in uniform
+        // registers; one elected lane issues.
+        const bool issuer = elect_one();
         const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), 16, 1024);
         const uint64_t b_desc0 = desc_sw128(smem_u32(b_tiles), 16, 1024);
         const uint64_t sf_desc0 = desc_plain(smem_u32(sf_tiles), 128);
@@ -251,30 +258,34 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const uint64_t ad = a_desc0 + (uint64_t)((stage * A_STAGE) >> 4);
                 const uint64_t bd = b_desc0 + (uint64_t)((stage * B_STAGE) >> 4);
                 const uint64_t sd = sf_desc0 + (uint64_t)((stage * SF_STAGE) >> 4);
+                if (issuer) {
 #pragma unroll
-                for (int a = 0; a < ATOMS; ++a) {
-                    cp_scales_pair(sfa + 4 * a, sd + a * 32);
-                    cp_scales_pair(sfb + 4 * halves * a, sd + (ATOMS + a) * 32);
-                    if (wide) cp_scales_pair(sfb + 4 * halves * a + 4, sd + (2 * ATOMS + a) * 32);
-                }
+                    for (int a = 0; a < ATOMS; ++a) {
+                        cp_scales_pair(sfa + 4 * a, sd + a * 32);
+                        cp_scales_pair(sfb + 4 * halves * a, sd + (ATOMS + a) * 32);
+                        if (wide) cp_scales_pair(sfb + 4 * halves * a + 4, sd + (2 * ATOMS + a) * 32);
+                    }
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const int a = NV ? ks : ks >> 1;
-                    mma_pair<NV>(d, ad + ks * 2, bd + ks * 2, NV || (ks & 1) == 0 ? idesc0 : idesc1, sfa + 4 * a,
-                                 sfb + 4 * halves * a, (uint32_t)((kb | ks) != 0));
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const int a = NV ? ks : ks >> 1;
+                        mma_pair<NV>(d, ad + ks * 2, bd + ks * 2, NV || (ks & 1) == 0 ? idesc0 : idesc1, sfa + 4 * a,
+                                     sfb + 4 * halves * a, (uint32_t)((kb | ks) != 0));
+                    }
+                    commit_pair_multicast(&bars->empty[stage]);
                 }
-                commit_pair_multicast(&bars->empty[stage]);
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
             if (!ok) break;
-            commit_pair_multicast(&bars->acc_full[buf]);
+            if (issuer) commit_pair_multicast(&bars->acc_full[buf]);
         }
-        if (!ok) {
-            atomicOr(args.status, ST_MMA);
-            raise_abort_pair(abort_flag, rank);
+        if (issuer) {
+            if (!ok) {
+                atomicOr(args.status, ST_MMA);
+                raise_abort_pair(abort_flag, rank);
+            }
+            commit<2>(&bars->drain);
+            if (!mbar_wait(&bars->drain, 0, abort_flag, false)) atomicOr(args.status, ST_DRAIN);
         }
-        commit<2>(&bars->drain);
-        if (!mbar_wait(&bars->drain, 0, abort_flag, false)) atomicOr(args.status, ST_DRAIN);
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue (both CTAs)
         const int quarter = warp & 3;
@@ -382,10 +393,12 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     const int cmax = clusters_max<T, NV>(dev);
     if (cmax <= 0) return cudaErrorNotSupported;
-    // The tile's width: the one with fewer waves of work, the wide one on ties.
+    // Narrow tiles only where they all run at once: in several waves a narrow tile
+    // costs 0.8-0.9 of a wide one's time (8192^3 in narrow tiles 418-564 us, in
+    // wide ones 236-312).
     const long long tiles_m = (p.M + 255LL) / 256, n256 = tiles_m * ((p.N + 255LL) / 256),
                     n128 = tiles_m * ((p.N + 127LL) / 128);
-    const int bn = (n128 + cmax - 1) / cmax < 2 * ((n256 + cmax - 1) / cmax) ? 128 : 256;
+    const int bn = n128 <= cmax ? 128 : 256;
     const long long tiles = bn == 256 ? n256 : n128;
     if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     const long long rb = fp4_row_bytes(p.K);
