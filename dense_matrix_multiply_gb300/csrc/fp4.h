@@ -135,6 +135,12 @@ struct Fp4Problem {
     Elt elt;   // of C
     bool nv;
 };
-cudaError_t launch_fp4_gemm(const Fp4Problem &p, int num_sms, int *status, cudaStream_t s);
+// Any M (fp4_gemm.cu).
+cudaError_t launch_fp4_gemm(const Fp4Problem &p, int *status, cudaStream_t s);
+// M <= kFp4SkinnyMaxM (fp4_skinny.cu); X non-null: the first operand is X [M,K] in
+// the element type of C, quantised as it is read (Qa, Sa unused).
+constexpr int kFp4SkinnyMaxM = 64;
+cudaError_t launch_fp4_skinny(const Fp4Problem &p, const void *X, long long ldx, int num_sms, int *status,
+                              cudaStream_t s);
 
 }  // namespace gemm_gb300

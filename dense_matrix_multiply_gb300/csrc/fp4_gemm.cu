@@ -447,8 +447,7 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_fp4_gemm(const Fp4Problem &p, int num_sms, int *status, cudaStream_t s) {
-    (void)num_sms;
+cudaError_t launch_fp4_gemm(const Fp4Problem &p, int *status, cudaStream_t s) {
     if (p.elt == Elt::BF16)
         return p.nv ? launch_pair<__nv_bfloat16, true>(p, status, s) : launch_pair<__nv_bfloat16, false>(p, status, s);
     return p.nv ? launch_pair<__half, true>(p, status, s) : launch_pair<__half, false>(p, status, s);

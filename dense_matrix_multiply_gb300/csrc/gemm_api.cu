@@ -489,7 +489,11 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     p.K = K;
     p.elt = elt;
     p.nv = nv;
-    if (!linear) return finish(launch_fp4_gemm(p, dev->num_sms, dev->status, s), nv ? "fp4_gemm_nv" : "fp4_gemm_mx");
+    // Few rows: the weight stream, with X quantised on the way.
+    if (M <= kFp4SkinnyMaxM)
+        return finish(launch_fp4_skinny(p, linear ? X : nullptr, ldx, dev->num_sms, dev->status, s),
+                      nv ? "fp4_skinny_nv" : "fp4_skinny_mx");
+    if (!linear) return finish(launch_fp4_gemm(p, dev->status, s), nv ? "fp4_gemm_nv" : "fp4_gemm_mx");
     // X's codes and scales in stream-ordered scratch for the duration of the call
     const size_t q = (fp4_code_size(M, K) + 255) & ~(size_t)255;
     void *ws = nullptr;
@@ -498,7 +502,7 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     p.Qa = ws;
     p.Sa = static_cast<uint8_t *>(ws) + q;
     e = launch_fp4_quantize(elt, nv, X, ldx, ga, ws, static_cast<uint8_t *>(ws) + q, M, K, s);
-    if (e == cudaSuccess) e = launch_fp4_gemm(p, dev->num_sms, dev->status, s);
+    if (e == cudaSuccess) e = launch_fp4_gemm(p, dev->status, s);
     const cudaError_t f = cudaFreeAsync(ws, s);
     return finish(e != cudaSuccess ? e : f, nv ? "fp4_linear_nv" : "fp4_linear_mx");
 }
