@@ -109,16 +109,18 @@ def _bind_torch_stream(*tensors) -> None:
     device's address would read memory it cannot reach."""
     dev = None
     for t in tensors:
-        if hasattr(t, "is_cuda"):
-            if not t.is_cuda:
-                raise ValueError("tensors must live on a CUDA device")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on two devices: {dev} and {t.device}")
+        if t is None or type(t) is int or not hasattr(t, "get_device"):
+            continue
+        d = t.get_device()  # an index: cheaper than a torch.device per tensor
+        if d < 0:
+            raise ValueError("tensors must live on a CUDA device")
+        if dev is None:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"tensors on two devices: cuda:{dev} and cuda:{d}")
     if dev is not None:
         import torch
-        load().gemm_set_stream(ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+        load().gemm_set_stream(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def _span(outer: int, inner: int, ld: int, stride: int = 0, batch: int = 1) -> int:
@@ -151,6 +153,15 @@ def _check(name: str, t, elt_size: int, need: int, tight: bool = True) -> None:
         room = t.untyped_storage().nbytes() // elt_size - t.storage_offset()
     if room < need:
         raise ValueError(f"{name} holds {room} elements, the call needs {need}")
+
+
+def _check_all(name: str, *args) -> None:
+    """_check of several (argument, tensor, element size, elements, tight); a
+    contiguous tensor with room passes here, without a message being built."""
+    for arg, t, size, need, tight in args:
+        if t is None or type(t) is int or (t.element_size() == size and t.is_contiguous() and t.numel() >= need):
+            continue
+        _check(f"{name}: {arg}", t, size, need, tight)
 
 
 def _dims(M: int, N: int, K: int):
@@ -305,13 +316,13 @@ def gemm_fp4_scale_bytes(fmt: str, rows: int, K: int) -> int:
     return int(load().gemm_fp4_scale_bytes(FP4_FORMATS[fmt], int(rows), int(K)))
 
 
-def _check_fp4(name: str, lib, fmt: int, Q, S, g, rows: int, K: int, what: str = "") -> None:
-    """Codes, scales and tensor scale of a quantised [rows, K] operand (nothing
-    where a size is 0 or negative: the library returns or rejects the call)."""
-    some = rows > 0 and K > 0
-    _check(f"{name}: Q{what}", Q, 1, lib.gemm_fp4_code_bytes(rows, K) if some else 0)
-    _check(f"{name}: S{what}", S, 1, lib.gemm_fp4_scale_bytes(fmt, rows, K) if some else 0)
-    _check(f"{name}: tensor scale {what}", g, 4, 1 if some else 0)
+def _fp4_sizes(fmt: int, rows: int, K: int):
+    """Bytes of the codes and scales of a quantised [rows, K] operand, and the
+    elements of its tensor scale (nothing where a size is 0 or negative: the
+    library returns or rejects the call)."""
+    if rows <= 0 or K <= 0:
+        return 0, 0, 0
+    return rows * ((K + 31) // 32 * 16), (rows + 127) // 128 * ((K + 255) // 256) * (2048 if fmt else 1024), 1
 
 
 def gemm_fp4_quantize(dtype: str, fmt: str, A, lda: int, tensor_scale, Q, S, M: int, K: int) -> None:
@@ -320,9 +331,9 @@ def gemm_fp4_quantize(dtype: str, fmt: str, A, lda: int, tensor_scale, Q, S, M: 
     device for 'nv' (None: 1), None for 'mx'.  See include/gemm.h."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4_quantize", dtype, fmt)
-    M, K, lda = int(M), int(K), int(lda)
-    _check("gemm_fp4_quantize: A", A, 2, _span(M, K, lda), tight=False)
-    _check_fp4("gemm_fp4_quantize", lib, f, Q, S, tensor_scale, M, K)
+    nq, ns, ng = _fp4_sizes(f, M, K)
+    _check_all("gemm_fp4_quantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
+               ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
     _bind_torch_stream(A, tensor_scale, Q, S)
     st = lib.gemm_fp4_quantize(d, f, _addr(A), lda, _addr(tensor_scale), _addr(Q), _addr(S), M, K)
     if st != GEMM_OK:
@@ -333,9 +344,9 @@ def gemm_fp4_dequantize(dtype: str, fmt: str, Q, S, tensor_scale, A, lda: int, M
     """Writes the values that codes Q and scales S stand for to A [M,K]."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4_dequantize", dtype, fmt)
-    M, K, lda = int(M), int(K), int(lda)
-    _check("gemm_fp4_dequantize: A", A, 2, _span(M, K, lda), tight=False)
-    _check_fp4("gemm_fp4_dequantize", lib, f, Q, S, tensor_scale, M, K)
+    nq, ns, ng = _fp4_sizes(f, M, K)
+    _check_all("gemm_fp4_dequantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
+               ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
     _bind_torch_stream(A, tensor_scale, Q, S)
     st = lib.gemm_fp4_dequantize(d, f, _addr(Q), _addr(S), _addr(tensor_scale), _addr(A), lda, M, K)
     if st != GEMM_OK:
@@ -347,11 +358,12 @@ def gemm_fp4(dtype: str, fmt: str, Qa, Sa, ga, Qb, Sb, gb, C, ldc: int, M: int, 
     b [N,K] of format 'mx' or 'nv'."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4", dtype, fmt)
-    M, N, K, ldc = int(M), int(N), int(K), int(ldc)
     if M > 0 and N > 0:
-        _check_fp4("gemm_fp4", lib, f, Qa, Sa, ga, M, K, "a")
-        _check_fp4("gemm_fp4", lib, f, Qb, Sb, gb, N, K, "b")
-        _check("gemm_fp4: C", C, 2, _span(M, N, ldc), tight=False)
+        qa, sa, na = _fp4_sizes(f, M, K)
+        qb, sb, nb = _fp4_sizes(f, N, K)
+        _check_all("gemm_fp4", ("Qa", Qa, 1, qa, True), ("Sa", Sa, 1, sa, True), ("ga", ga, 4, na, True),
+                   ("Qb", Qb, 1, qb, True), ("Sb", Sb, 1, sb, True), ("gb", gb, 4, nb, True),
+                   ("C", C, 2, _span(M, N, ldc), False))
     _bind_torch_stream(Qa, Sa, ga, Qb, Sb, gb, C)
     st = lib.gemm_fp4(d, f, _addr(Qa), _addr(Sa), _addr(ga), _addr(Qb), _addr(Sb), _addr(gb), _addr(C), ldc, M, N, K)
     if st != GEMM_OK:
@@ -363,12 +375,11 @@ def gemm_fp4_linear(dtype: str, fmt: str, X, ldx: int, gx, Qw, Sw, gw, C, ldc: i
     quantised within the call (tensor scale gx) and W [N,K] quantised already."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4_linear", dtype, fmt)
-    M, N, K, ldx, ldc = int(M), int(N), int(K), int(ldx), int(ldc)
     if M > 0 and N > 0:
-        _check("gemm_fp4_linear: X", X, 2, _span(M, K, ldx), tight=False)
-        _check("gemm_fp4_linear: tensor scale x", gx, 4, 1)
-        _check_fp4("gemm_fp4_linear", lib, f, Qw, Sw, gw, N, K, "w")
-        _check("gemm_fp4_linear: C", C, 2, _span(M, N, ldc), tight=False)
+        qw, sw, nw = _fp4_sizes(f, N, K)
+        _check_all("gemm_fp4_linear", ("X", X, 2, _span(M, K, ldx), False), ("gx", gx, 4, nw, True),
+                   ("Qw", Qw, 1, qw, True), ("Sw", Sw, 1, sw, True), ("gw", gw, 4, nw, True),
+                   ("C", C, 2, _span(M, N, ldc), False))
     _bind_torch_stream(X, gx, Qw, Sw, gw, C)
     st = lib.gemm_fp4_linear(d, f, _addr(X), ldx, _addr(gx), _addr(Qw), _addr(Sw), _addr(gw), _addr(C), ldc, M, N, K)
     if st != GEMM_OK:

@@ -47,9 +47,9 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
     for (int i = 0; i < 8; ++i) m = __vmaxu2(m, abs2(v[i]));
     m = max(m & 0xFFFFu, m >> 16);
     if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    float step;
-    uint32_t byte = fp4_block_scale<NV>(bits16_to_f32<T>(m), 6.0f * g, g, &step);
-    const uint2 codes = fp4_codes16<T, NV>(v, step);
+    const Fp4Scale sc = fp4_block_scale<NV>(bits16_to_f32<T>(m), 6.0f * g, g);
+    const uint2 codes = fp4_codes16<T, NV>(v, sc);
+    uint32_t byte = sc.byte;
     // four blocks' bytes to one word: lanes 4 i .. 4 i + 3 (NV), 8 i .. 8 i + 7 by twos (MX)
     constexpr int SPAN = NV ? 1 : 2;  // lanes to a block
     byte |= __shfl_down_sync(0xffffffffu, byte, SPAN) << 8;

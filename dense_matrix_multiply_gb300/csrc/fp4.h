@@ -35,28 +35,44 @@ __device__ __forceinline__ long long fp4_scale_at(int row, int a, int atoms) {
     return ((long long)(row >> 7) * atoms + a) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 }
 
-// Scale byte and step of a block from the bits of its largest magnitude
-// (|a| as FP32 bits: their order is the values', infinities and NaN on top).
+// A block's scale byte, and what its codes are formed with.
+struct Fp4Scale {
+    uint32_t byte;
+    float step;  // NV: the step.  0 (both): codes of 0
+    float inv;   // 1 / step: MX a power of two, exact; NV correctly rounded
+    bool near;   // NV: a / step may be formed with inv (fp4_codes16)
+};
+// From the bits of the block's largest magnitude (|a| as FP32 bits: their order
+// is the values', infinities and NaN on top).
 //   MX: e = clamp(floor(log2 amax) - 2, -127, 125), byte e + 127, so that the
 //       largest magnitude lies in [4, 8) steps; the exponent field less 2.
 //   NV: s = E4M3(amax / (6 g)), step s g.
-// A NaN or an infinity makes the scale NaN and the codes 0.  *f is what the
-// codes are formed with, 0 for codes of 0: the step (NV: a / step) or its
-// reciprocal (MX: a power of two, so that the product is exact).
+// A NaN or an infinity makes the scale NaN and the codes 0.
 template <bool NV>
-__device__ __forceinline__ uint32_t fp4_block_scale(uint32_t amax_bits, float g6, float g, float *f) {
+__device__ __forceinline__ Fp4Scale fp4_block_scale(uint32_t amax_bits, float g6, float g) {
     const bool bad = amax_bits >= 0x7F800000u;
+    Fp4Scale r;
     if constexpr (NV) {
-        const uint32_t b = __nv_cvt_float_to_fp8(__uint_as_float(amax_bits) / g6, __NV_SATFINITE, __NV_E4M3);
-        const __half s = __half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3));
-        *f = bad ? 0.0f : __half2float(s) * g;
-        return bad ? 0x7Fu : b;
+        const float amax = __uint_as_float(amax_bits);
+        r.byte = __nv_cvt_float_to_fp8(amax / g6, __NV_SATFINITE, __NV_E4M3);
+        r.step = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)r.byte, __NV_E4M3))) * g;
+        r.inv = __frcp_rn(r.step);
+        // the step and its reciprocal far from the ends of FP32's range, and the
+        // block not far into saturation
+        r.near = r.step >= 0x1p-60f && r.step <= 0x1p60f && amax <= 1024.0f * r.step;
+        if (bad) {
+            r.byte = 0x7Fu;
+            r.step = 0.0f;
+        }
     } else {
         const int be = (int)(amax_bits >> 23);
         const int byte = be > 2 ? be - 2 : 0;
-        *f = bad ? 0.0f : __uint_as_float((uint32_t)(254 - byte) << 23);
-        return bad ? 0xFFu : (uint32_t)byte;
+        r.byte = bad ? 0xFFu : (uint32_t)byte;
+        r.inv = __uint_as_float((uint32_t)(254 - byte) << 23);
+        r.step = bad ? 0.0f : 1.0f;
+        r.near = true;
     }
+    return r;
 }
 
 // Two values in steps, as codes (the first in the low half): nearest, ties to
@@ -98,22 +114,37 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
 }
 
 // Codes of the 16 values in v (eight packed pairs) of one block or half block.
+// NV's a / step, rounded to nearest as IEEE division: with y the correctly
+// rounded reciprocal of the step and q = a y, the remainder a - q step is exact
+// in one FMA, and q + remainder * y is the correctly rounded quotient (Markstein,
+// IBM J. Res. Dev. 34, 1990); a quotient so small that the remainder underflows
+// has code 0 either way.  Steps at the ends of the range divide.
 template <typename T, bool NV>
-__device__ __forceinline__ uint2 fp4_codes16(const uint32_t (&v)[8], float f) {
+__device__ __forceinline__ uint2 fp4_codes16(const uint32_t (&v)[8], const Fp4Scale &s) {
     uint32_t w[2] = {0u, 0u};
-    if (f > 0.0f) {
-#pragma unroll
+    if (!(s.step > 0.0f)) return make_uint2(0u, 0u);
+    if (NV && !s.near) {
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-            float2 x = unpack2<T>(v[i]);
-            if constexpr (NV) {
-                x.x = x.x / f;
-                x.y = x.y / f;
-            } else {
-                x.x *= f;
-                x.y *= f;
-            }
-            w[i >> 2] |= e2m1x2(x.x, x.y) << (8 * (i & 3));
+            uint32_t p = v[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j) p = i == j ? v[j] : p;
+            const float2 x = unpack2<T>(p);
+            const uint32_t c = e2m1x2(x.x / s.step, x.y / s.step) << (8 * (i & 3));
+            if (i < 4) w[0] |= c;
+            else w[1] |= c;
         }
+        return make_uint2(w[0], w[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 x = unpack2<T>(v[i]);
+        float a = x.x * s.inv, b = x.y * s.inv;
+        if constexpr (NV) {
+            a = fmaf(fmaf(-a, s.step, x.x), s.inv, a);
+            b = fmaf(fmaf(-b, s.step, x.y), s.inv, b);
+        }
+        w[i >> 2] |= e2m1x2(a, b) << (8 * (i & 3));
     }
     return make_uint2(w[0], w[1]);
 }

@@ -124,7 +124,7 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
-            mbar_init(&bars->full[s], FUSED ? 1 + 4 : 1);
+            mbar_init(&bars->full[s], FUSED ? 2 : 1);
             mbar_init(&bars->empty[s], 1);
         }
         mbar_init(&bars->acc_full, 1);
@@ -139,6 +139,14 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     __syncthreads();
     fence_after();
     const uint32_t tmem_base = bars->tmem_base;
+    if (warp == 0 && lane == 0 && g_pdl) {
+        // The strip's first weights to L2 while the previous kernel drains: a hint,
+        // which changes no value that a later load returns.
+        for (int kb = kb0; kb < min(kb1, kb0 + stages); ++kb) {
+            tma_prefetch_l2_3d(&tmW, kb * (KB / 2), strip * 128, 0);
+            tma_prefetch_l2_3d(&tmSw, 0, kb * (SF / 1024), strip);
+        }
+    }
     pdl_wait();
 
     if (warp == 0 && lane == 0) {
@@ -166,7 +174,7 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         }
         pdl_launch_dependents();
         // Every load of this thread lands before the ring is reused or the CTA
-        // ends.  (FUSED, after an abort: a phase whose converters gave up never
+        // ends.  (FUSED, after an abort: a phase whose converter gave up never
         // completes, so the wait runs out; its loads have landed long since.)
         for (long long i = (issued > stages ? issued - stages : 0); i < issued; ++i)
             if (!mbar_wait(&bars->full[i % stages], (uint32_t)((i / stages) & 1), abort_flag, false)) {
@@ -219,15 +227,13 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     } else if (warp >= 2) {
         bool ok = true;
         if constexpr (FUSED) {
-            // ------------------------------------------------------------ X quantised, stage by stage
-            // A unit is 16 consecutive k of a row (half an MX block, an NV block);
-            // lanes 0-15 of a warp hold one row's 256 k, 16-31 the next row's.
-            const int cw = warp - 2, half = lane >> 4, u = lane & 15;
-            const float g = NV && args.ga ? *args.ga : 1.0f;
-            const float g6 = 6.0f * g;
+            // ------------------------------------------------------------ X quantised, a stage to a warp
+            // Warp w takes stages w, w + 4, ...: a stage's conversion is a chain of
+            // dependent steps, so four stages are under way at once.  A unit is 16
+            // consecutive k of a row (half an MX block, an NV block); lanes 0-15
+            // hold one row's 256 k, 16-31 the next row's.
+            const int half = lane >> 4, u = lane & 15;
             const T *X = static_cast<const T *>(args.X);
-            int stage = 0;
-            uint32_t phase = 0;
             auto load = [&](int kb, int r, uint32_t (&v)[8]) {
                 const int k = kb * KB + u * 16;
 #pragma unroll
@@ -245,41 +251,54 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                         if (k + i < K) v[i >> 1] |= (uint32_t)__ldg(h + i) << (16 * (i & 1));
                 }
             };
-            const int r_first = cw * 2 + half;
-            uint32_t next[8];
-            load(kb0, r_first, next);
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true))) {
+            int slot = warp - 2;
+            uint32_t phase = 0;
+            while (slot >= stages) { slot -= stages; phase ^= 1u; }
+            // UNITS row pairs at a time, the next ones' values in flight meanwhile
+            constexpr int UNITS = 4;
+            uint32_t next[UNITS][8];
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) load(kb0 + warp - 2, half + 2 * i, next[i]);
+            const float g = NV && args.ga ? *args.ga : 1.0f;
+            const float g6 = 6.0f * g;
+            for (int kb = kb0 + warp - 2; kb < kb1; kb += 4) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[slot], phase ^ 1u, abort_flag, true))) {
                     ok = false;
                     break;
                 }
-                uint8_t *xs = x_tiles + stage * x_stage, *sx = sf_tiles + stage * 2 * SF + SF;
-                for (int r0 = cw * 2; r0 < M; r0 += 8) {
-                    const int r = r0 + half;
-                    uint32_t v[8];
+                uint8_t *xs = x_tiles + slot * x_stage, *sx = sf_tiles + slot * 2 * SF + SF;
+                for (int r0 = 0; r0 < M; r0 += 2 * UNITS) {
+                    uint32_t v[UNITS][8];
+                    const bool more = r0 + 2 * UNITS < M;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = next[i];
-                    // the values after these, while these are converted
-                    if (r0 + 8 < M) load(kb, r + 8, next);
-                    else if (kb + 1 < kb1) load(kb + 1, r_first, next);
-                    uint32_t m = 0u;
+                    for (int i = 0; i < UNITS; ++i) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, abs2(v[i]));
-                    m = max(m & 0xFFFFu, m >> 16);
-                    if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                    float f;
-                    const uint32_t byte = fp4_block_scale<NV>(bits16_to_f32<T>(m), g6, g, &f);
-                    const uint2 codes = fp4_codes16<T, NV>(v, f);
-                    if (r < M) {
-                        *reinterpret_cast<uint2 *>(xs + r * 128 + (((u >> 1) ^ (r & 7)) << 4) + ((u & 1) << 3)) = codes;
-                        const int b = NV ? u : u >> 1;  // block of the stage
-                        if (NV || (u & 1) == 0) sx[(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = (uint8_t)byte;
+                        for (int j = 0; j < 8; ++j) v[i][j] = next[i][j];
+                        load(more ? kb : kb + 4, (more ? r0 + 2 * UNITS : 0) + half + 2 * i, next[i]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < UNITS; ++i) {
+                        const int r = r0 + 2 * i + half;
+                        if (r0 + 2 * i >= M) break;  // warp-uniform
+                        uint32_t m = 0u;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) m = __vmaxu2(m, abs2(v[i][j]));
+                        m = max(m & 0xFFFFu, m >> 16);
+                        if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        const Fp4Scale sc = fp4_block_scale<NV>(bits16_to_f32<T>(m), g6, g);
+                        const uint2 codes = fp4_codes16<T, NV>(v[i], sc);
+                        if (r < M) {
+                            *reinterpret_cast<uint2 *>(xs + r * 128 + (((u >> 1) ^ (r & 7)) << 4) + ((u & 1) << 3)) = codes;
+                            const int b = NV ? u : u >> 1;  // block of the stage
+                            if (NV || (u & 1) == 0) sx[(b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3)] = (uint8_t)sc.byte;
+                        }
                     }
                 }
                 fence_async_shared();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->full[stage]);
-                if (++stage == stages) { stage = 0; phase ^= 1u; }
+                if (lane == 0) mbar_arrive(&bars->full[slot]);
+                slot += 4;
+                while (slot >= stages) { slot -= stages; phase ^= 1u; }
             }
             if (!ok && lane == 0) {
                 atomicOr(args.status, ST_PRODUCER);

@@ -19,6 +19,34 @@ using namespace gemm_gb300;
 std::atomic<unsigned long long> gemm_gb300::g_launches{0};
 
 namespace {
+struct ScratchPool {
+    std::once_flag once;
+    cudaMemPool_t pool = nullptr;
+    cudaError_t err = cudaSuccess;
+};
+ScratchPool g_scratch[kMaxDevices];
+}  // namespace
+
+cudaError_t gemm_gb300::scratch_alloc(void **p, size_t bytes, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    ScratchPool &d = g_scratch[dev];
+    std::call_once(d.once, [&] {
+        cudaMemPoolProps props = {};
+        props.allocType = cudaMemAllocationTypePinned;
+        props.location.type = cudaMemLocationTypeDevice;
+        props.location.id = dev;
+        d.err = cudaMemPoolCreate(&d.pool, &props);
+        unsigned long long keep = kScratchKept;
+        if (d.err == cudaSuccess) d.err = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    });
+    if (d.err != cudaSuccess) return d.err;
+    return cudaMallocFromPoolAsync(p, bytes, d.pool, s);
+}
+
+namespace {
 
 enum class Family { Auto, Simt, SimtScalar, Gemv, GemvScalar, Umma, UmmaSkinnyWide, UmmaStall, UmmaStallPair, UmmaStallPeer };
 
@@ -489,22 +517,29 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     p.K = K;
     p.elt = elt;
     p.nv = nv;
-    // Few rows: the weight stream, with X quantised on the way.
-    if (M <= kFp4SkinnyMaxM)
-        return finish(launch_fp4_skinny(p, linear ? X : nullptr, ldx, dev->num_sms, dev->status, s),
-                      nv ? "fp4_skinny_nv" : "fp4_skinny_mx");
-    if (!linear) return finish(launch_fp4_gemm(p, dev->status, s), nv ? "fp4_gemm_nv" : "fp4_gemm_mx");
+    // Few rows run on the weight stream.  A linear layer's X is quantised inside
+    // it for M <= 8, by a launch of its own above: every strip of 128 outputs
+    // converts X anew, which for M = 8 is hidden behind the stream (N = 12288, K =
+    // 4096, NV: 10.7 us against 11.8 in two launches; N = 4096, K = 12288, MX: 8.7
+    // against 10.9) and for M = 16 no longer is (15.6 against 12.0; 10.9 against 11.2).
+    const bool skinny = M <= kFp4SkinnyMaxM;
+    if (linear && M <= 8)
+        return finish(launch_fp4_skinny(p, X, ldx, dev->num_sms, dev->status, s),
+                      nv ? "fp4_skinny_fused_nv" : "fp4_skinny_fused_mx");
+    auto product = [&] { return skinny ? launch_fp4_skinny(p, nullptr, 0, dev->num_sms, dev->status, s) : launch_fp4_gemm(p, dev->status, s); };
+    const char *name = skinny ? (nv ? "fp4_skinny_nv" : "fp4_skinny_mx") : (nv ? "fp4_gemm_nv" : "fp4_gemm_mx");
+    if (!linear) return finish(product(), name);
     // X's codes and scales in stream-ordered scratch for the duration of the call
     const size_t q = (fp4_code_size(M, K) + 255) & ~(size_t)255;
     void *ws = nullptr;
-    cudaError_t e = cudaMallocAsync(&ws, q + (size_t)fp4_scale_size(nv, M, K), s);
+    cudaError_t e = scratch_alloc(&ws, q + (size_t)fp4_scale_size(nv, M, K), s);
     if (e != cudaSuccess) return finish(e, "fp4_linear");
     p.Qa = ws;
     p.Sa = static_cast<uint8_t *>(ws) + q;
     e = launch_fp4_quantize(elt, nv, X, ldx, ga, ws, static_cast<uint8_t *>(ws) + q, M, K, s);
-    if (e == cudaSuccess) e = launch_fp4_gemm(p, dev->status, s);
+    if (e == cudaSuccess) e = product();
     const cudaError_t f = cudaFreeAsync(ws, s);
-    return finish(e != cudaSuccess ? e : f, nv ? "fp4_linear_nv" : "fp4_linear_mx");
+    return finish(e != cudaSuccess ? e : f, name);
 }
 
 }  // namespace
