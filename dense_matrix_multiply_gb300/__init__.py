@@ -49,6 +49,8 @@ SIGNATURES = {
     "gemm_fp4_dequantize": ([_I, _I, _VP, _VP, _VP, _VP, ctypes.c_int64, _I, _I], _I),
     "gemm_fp4": ([_I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64, _I, _I, _I], _I),
     "gemm_fp4_linear": ([_I, _I, _VP, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64, _I, _I, _I], _I),
+    "gemm_gated": ([_I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
+    "gemm_gated_backward": ([_I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
     "gemm_set_stream": ([_VP], _I),
     "gemm_get_stream": ([], _VP),
     "gemm_synchronize": ([], _I),
@@ -384,6 +386,46 @@ def gemm_fp4_linear(dtype: str, fmt: str, X, ldx: int, gx, Qw, Sw, gw, C, ldc: i
     st = lib.gemm_fp4_linear(d, f, _addr(X), ldx, _addr(gx), _addr(Qw), _addr(Sw), _addr(gw), _addr(C), ldc, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4_linear", lib.gemm_last_error().decode())
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+def _gated_enums(name: str, dtype: str, act: str):
+    if dtype not in _DTYPES16 or act not in ACTIVATIONS:
+        raise ValueError(f"{name}: dtype 'f16' | 'bf16' and act 'silu' | 'gelu', got {dtype!r} and {act!r}")
+    return _DTYPES16[dtype], ACTIVATIONS[act]
+
+
+def gemm_gated(dtype: str, act: str, X, W_g, W_u, Z, G, U, M: int, N: int, K: int) -> None:
+    """Z [M,N] = act(X W_g) * (X W_u) ('f16' | 'bf16', act 'silu' | 'gelu'); G and U
+    (FP32 [M,N], or both None) keep the two products for gemm_gated_backward."""
+    lib = load()
+    d, a = _gated_enums("gemm_gated", dtype, act)
+    nx, nw, nz = _dims(M, N, K)
+    _check_all("gemm_gated", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
+               ("Z", Z, 2, nz, True), ("G", G, 4, nz, True), ("U", U, 4, nz, True))
+    _bind_torch_stream(X, W_g, W_u, Z, G, U)
+    st = lib.gemm_gated(d, a, _addr(X), _addr(W_g), _addr(W_u), _addr(Z), _addr(G), _addr(U), M, N, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_gated", lib.gemm_last_error().decode())
+
+
+def gemm_gated_backward(dtype: str, act: str, X, W_g, W_u, G, U, dZ, dX, dW_g, dW_u, M: int, N: int, K: int) -> None:
+    """Gradients of gemm_gated from dZ [M,N] and the G and U it stored: dX [M,K],
+    dW_g and dW_u [K,N]; None leaves one out."""
+    lib = load()
+    d, a = _gated_enums("gemm_gated_backward", dtype, act)
+    M, N, K = int(M), int(N), int(K)
+    nx, nw, nz = (M * K, K * N, M * N) if min(M, N, K) >= 0 else (0, 0, 0)
+    _check_all("gemm_gated_backward", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
+               ("G", G, 4, nz, True), ("U", U, 4, nz, True), ("dZ", dZ, 2, nz, True), ("dX", dX, 2, nx, True),
+               ("dW_g", dW_g, 2, nw, True), ("dW_u", dW_u, 2, nw, True))
+    _bind_torch_stream(X, W_g, W_u, G, U, dZ, dX, dW_g, dW_u)
+    st = lib.gemm_gated_backward(d, a, _addr(X), _addr(W_g), _addr(W_u), _addr(G), _addr(U), _addr(dZ), _addr(dX),
+                                 _addr(dW_g), _addr(dW_u), M, N, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_gated_backward", lib.gemm_last_error().decode())
 
 
 def gemm_set_stream(stream) -> None:

@@ -1,0 +1,638 @@
+// Gated feed-forward block on the tensor cores, forward and backward:
+//     G = X Wg, U = X Wu, Z = act(G) * U
+//     dU = dZ * act(G), dG = dZ * U * act'(G)
+//     dX = dG Wg^T + dU Wu^T, dWg = X^T dG, dWu = X^T dU
+//
+// Forward: one kernel.  A 256 x 128 tile of Z belongs to a cluster of two CTAs
+// (tcgen05 cta_group::2); per K step of 64 CTA r loads 64 columns of Wg and the
+// same 64 of Wu side by side, so that one N = 256 MMA gives G and U for the same
+// columns of Z in one accumulator, and the epilogue forms Z from the FP32 sums,
+// rounded once.  For training it also stores G and U, in FP32: a 16-bit copy would
+// put a third rounding beside those of dG and dU and of the result on every
+// gradient (1.7 times the error of the result's rounding, against 1.4).
+//
+// Backward: dG and dU (16 bits, the operands of the products to come) from G, U
+// and dZ in one pass over memory; dX as one product over the joined reduction
+// index of dG Wg^T and dU Wu^T (2N long), 256 x bn tiles on the same pair
+// pipeline, FP32 sums of both in one accumulator; dWg and dWu as one batch of two
+// on the general kernel (umma_gemm.cu).  With few tiles the joined index is split
+// over the idle clusters, whose FP32 partials a second kernel adds in order.
+//
+// Warps: 0 loads (TMA), 1 issues the MMAs (leader), 2-5 write out.  Two
+// accumulators, so that a tile is written while the next one is computed.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "gated.h"
+#include "tc_ptx.cuh"
+
+namespace gemm_gb300 {
+namespace {
+
+using namespace tc;
+
+constexpr int THREADS = 192;
+constexpr int BK = 64;                 // 16-bit k per stage: 128 bytes a row
+constexpr int A_STAGE = 128 * BK * 2;  // 16 KiB per CTA
+constexpr int B_STAGE = 128 * BK * 2;
+constexpr int BOX64 = 64 * BK * 2;     // 64 columns x 64 k of an MN-major tile
+constexpr int STG_BOX = 4096;          // 32 rows x 128 bytes of output
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int GROUP_M = 8;
+
+// Forward: four staging boxes per epilogue warp (Z, G and U), five stages; dX: two and six.
+enum Mode { FWD = 0, DX = 1 };
+__host__ __device__ constexpr int n_boxes(int mode) { return mode == FWD ? 4 : 2; }
+__host__ __device__ constexpr int n_stages(int mode) { return mode == FWD ? 5 : 6; }
+__host__ __device__ constexpr int smem_bytes(int mode) {
+    return 1024 + n_stages(mode) * (A_STAGE + B_STAGE) + 4 * n_boxes(mode) * STG_BOX + 256;
+}
+static_assert(smem_bytes(FWD) <= 232448 && smem_bytes(DX) <= 232448, "shared memory budget");
+
+struct Bars {
+    uint64_t full[6];
+    uint64_t empty[6];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
+    uint64_t peer_done;
+    long long peer_issued;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+struct Args {
+    int M, N;     // of the output: Z [M,N], dX [M,N]
+    int num_kb;   // K blocks of 64 (DX: of both halves together)
+    int kb_half;  // DX: blocks of the first half
+    int bn;       // the tile's N extent: FWD 128; DX 128, 192 or 256
+    int splits;   // DX: units per tile; > 1: FP32 partials
+    int save;     // FWD: store G and U
+    int *status;
+};
+
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// FP32 accumulator, A and B of one 16-bit type (0 f16, 1 bf16), A K-major, M = 256.
+__device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool b_mn) {
+    return (1u << 4) | (format << 7) | (format << 10) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// Unit u: tile and K-block range.
+struct Unit {
+    int tm, tn, kb0, kb1, split;
+};
+__device__ __forceinline__ Unit unit_at(int u, int tiles_m, int tiles_n, const Args &a) {
+    Unit r;
+    const int t = u / a.splits;
+    r.split = u - t * a.splits;
+    r.kb0 = (int)((long long)a.num_kb * r.split / a.splits);
+    r.kb1 = (int)((long long)a.num_kb * (r.split + 1) / a.splits);
+    const int per_group = GROUP_M * tiles_n;
+    const int group = t / per_group;
+    const int first_m = group * GROUP_M;
+    const int gsize = min(tiles_m - first_m, GROUP_M);
+    const int q = t - group * per_group;
+    r.tm = first_m + q % gsize;
+    r.tn = q / gsize;
+    return r;
+}
+
+// 32 FP32 columns of this lane's row to a box, 128-byte swizzle.
+__device__ __forceinline__ void box_put_f32(uint8_t *box, int lane, const uint32_t (&r)[32]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+}
+
+// FWD: tmA = X, tmB = Wg, tmB2 = Wu, tmC = Z, tmG, tmU (when saved).
+// DX: tmA = {dG, dU} (third coordinate), tmB = Wg, tmB2 = Wu, tmC = dX, tmG the
+// partials [splits][M][N] (splits > 1).
+template <typename T, uint32_t FORMAT, int MODE, bool GELU>
+__global__ void __launch_bounds__(THREADS, 1)
+gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                  const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmC,
+                  const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU, const Args args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int STAGES = n_stages(MODE), BOXES = n_boxes(MODE);
+    uint8_t *a_tiles = smem;
+    uint8_t *b_tiles = a_tiles + STAGES * A_STAGE;
+    uint8_t *staging = b_tiles + STAGES * B_STAGE;
+    Bars *bars = reinterpret_cast<Bars *>(staging + 4 * BOXES * STG_BOX);
+    volatile int *abort_flag = &bars->abort;
+
+    const int M = args.M, N = args.N, bn = args.bn;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
+    const int tiles_m = (M + 255) / 256, tiles_n = (N + bn - 1) / bn;
+    const int units = tiles_m * tiles_n * args.splits;
+    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (MODE == FWD ? 2 * BOX64 : (bn >> 1) * 128));
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 256);
+        }
+        mbar_init(&bars->drain, 1);
+        mbar_init(&bars->peer_done, 1);
+        bars->abort = 0;
+        mbar_init_fence();
+        prefetch_desc(&tmA);
+        prefetch_desc(&tmB);
+        prefetch_desc(&tmB2);
+        prefetch_desc(&tmC);
+    }
+    if (warp == 1) tmem_alloc<2>(&bars->tmem_base, TMEM_COLS);
+    fence_before();
+    cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
+    fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------------ producer (both CTAs)
+        int stage = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        for (int u = cluster; u < units && ok; u += nclusters) {
+            const Unit w = unit_at(u, tiles_m, tiles_n, args);
+            const int row0 = w.tm * 256 + (int)rank * 128, col0 = w.tn * bn + (int)rank * (bn >> 1);
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
+                const uint32_t full = map_to_rank(&bars->full[stage], 0);
+                if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
+                uint8_t *a = a_tiles + stage * A_STAGE, *b = b_tiles + stage * B_STAGE;
+                if (MODE == FWD) {
+                    tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
+                    tma_load_3d_pair(b, &tmB, full, col0, kb * BK, 0);
+                    tma_load_3d_pair(b + BOX64, &tmB2, full, col0, kb * BK, 0);
+                } else {
+                    const int z = kb >= args.kb_half ? 1 : 0, k0 = (kb - z * args.kb_half) * BK;
+                    tma_load_3d_pair(a, &tmA, full, k0, row0, z);
+                    tma_load_3d_pair(b, z ? &tmB2 : &tmB, full, k0, col0, 0);
+                }
+                ++issued;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+        }
+        if (!ok) {
+            atomicOr(args.status, ST_PRODUCER);
+            raise_abort_pair(abort_flag, rank);
+        }
+        // No load is left in flight into either CTA when the pair ends: the peer
+        // tells the leader how many stages it loaded, and the leader waits until
+        // every stage that either loaded has landed (the half that a side which
+        // gave up never loaded is counted as done, or never armed).
+        if (!leader) {
+            st_cluster_s64(map_to_rank(&bars->peer_issued, 0), issued);
+            mbar_arrive_cluster(map_to_rank(&bars->peer_done, 0));  // release: the count is visible first
+        } else {
+            long long ip = issued;
+            if (mbar_wait(&bars->peer_done, 0, abort_flag, false))
+                ip = *reinterpret_cast<volatile long long *>(&bars->peer_issued);
+            else
+                atomicOr(args.status, ST_DRAIN);
+            const long long hi = issued > ip ? issued : ip;
+            for (long long i = (hi > STAGES ? hi - STAGES : 0); i < hi; ++i) {
+                const int s = (int)(i % STAGES);
+                if (i >= issued) mbar_arrive_expect_tx(&bars->full[s], stage_tx / 2);
+                else if (i >= ip) mbar_complete_tx(&bars->full[s], stage_tx / 2);
+                if (!mbar_wait(&bars->full[s], (uint32_t)((i / STAGES) & 1), abort_flag, false)) {
+                    atomicOr(args.status, ST_DRAIN);
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1 && leader) {
+        // ------------------------------------------------------------ MMA issuer (leader)
+        // The whole warp runs the loop (descriptors in uniform registers), one lane issues.
+        const bool issuer = elect_one();
+        constexpr bool b_mn = MODE == FWD;
+        const uint32_t idesc = make_idesc(FORMAT, MODE == FWD ? 256u : (uint32_t)bn, b_mn);
+        const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), 16, 1024);
+        const uint64_t b_desc0 = desc_sw128(smem_u32(b_tiles), b_mn ? BOX64 : 16, 1024);
+        constexpr uint32_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;
+        bool ok = true;
+        for (int u = cluster; u < units && ok; u += nclusters, ++it) {
+            const Unit w = unit_at(u, tiles_m, tiles_n, args);
+            const int buf = it & 1;
+            if (!mbar_wait(&bars->acc_empty[buf], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, true)) { ok = false; break; }
+            fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+            for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                if (!mbar_wait(&bars->full[stage], phase, abort_flag, true)) { ok = false; break; }
+                fence_after();
+                const uint64_t ad = a_desc0 + (uint64_t)((stage * A_STAGE) >> 4);
+                const uint64_t bd = b_desc0 + (uint64_t)((stage * B_STAGE) >> 4);
+                if (issuer) {
+#pragma unroll
+                    for (int ks = 0; ks < BK / 16; ++ks)
+                        mma_f16_pair(d, ad + ks * a_step, bd + ks * b_step, idesc, (uint32_t)(kb != w.kb0 || ks != 0));
+                    commit_pair_multicast(&bars->empty[stage]);
+                }
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            if (issuer) commit_pair_multicast(&bars->acc_full[buf]);
+        }
+        if (issuer) {
+            if (!ok) {
+                atomicOr(args.status, ST_MMA);
+                raise_abort_pair(abort_flag, rank);
+            }
+            commit<2>(&bars->drain);
+            if (!mbar_wait(&bars->drain, 0, abort_flag, false)) atomicOr(args.status, ST_DRAIN);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue (both CTAs)
+        const int quarter = warp & 3;
+        uint8_t *my_stg = staging + quarter * BOXES * STG_BOX;
+        int sb = 0, it = 0;
+        bool ok = true;
+        // The next staging box, once the store that last read it has done so.
+        auto box_begin = [&]() {
+            if (lane == 0) {
+                if constexpr (BOXES == 4) asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
+                else tma_stores_read_wait1();
+            }
+            __syncwarp();
+            uint8_t *b = my_stg + sb * STG_BOX;
+            sb = (sb + 1) % BOXES;
+            return b;
+        };
+        auto box_end = [&](const CUtensorMap *map, uint8_t *b, int x, int y, int z) {
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0 && y < M) tma_store_3d(map, b, x, y, z);
+        };
+        for (int u = cluster; u < units; u += nclusters, ++it) {
+            const Unit w = unit_at(u, tiles_m, tiles_n, args);
+            const int buf = it & 1;
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (uint32_t)((it >> 1) & 1), abort_flag, true))) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            __syncwarp();
+            const int row0 = w.tm * 256 + (int)rank * 128 + quarter * 32;
+            const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
+            if constexpr (MODE == FWD) {
+                // accumulator columns 128 g + j: G, 128 g + 64 + j: U of Z's column 64 g + j
+#pragma unroll 1
+                for (int g = 0; g < 2; ++g) {
+                    const int c0 = w.tn * 128 + g * 64;
+                    if (c0 >= N) break;  // warp-uniform
+                    uint32_t z[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t rg[32], ru[32];
+                        tmem_ld32(t_row + (uint32_t)(g * 128 + h * 32), rg);
+                        tmem_ld32(t_row + (uint32_t)(g * 128 + 64 + h * 32), ru);
+                        tmem_ld_wait();
+                        if (args.save && c0 + h * 32 < N) {
+                            uint8_t *b = box_begin();
+                            box_put_f32(b, lane, rg);
+                            box_end(&tmG, b, c0 + h * 32, row0, 0);
+                            b = box_begin();
+                            box_put_f32(b, lane, ru);
+                            box_end(&tmU, b, c0 + h * 32, row0, 0);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            z[h * 16 + j] = pack2(gate_act<GELU>(__uint_as_float(rg[2 * j])) * __uint_as_float(ru[2 * j]),
+                                                  gate_act<GELU>(__uint_as_float(rg[2 * j + 1])) * __uint_as_float(ru[2 * j + 1]),
+                                                  (T *)nullptr);
+                    }
+                    uint8_t *b = box_begin();
+                    box_put_f32(b, lane, z);
+                    box_end(&tmC, b, c0, row0, 0);
+                }
+            } else {
+#pragma unroll 1
+                for (int g = 0; g < (bn >> 6); ++g) {
+                    const int c0 = w.tn * bn + g * 64;
+                    if (c0 >= N) break;  // warp-uniform
+                    uint32_t r0[32], r1[32];
+                    tmem_ld32(t_row + (uint32_t)(g * 64), r0);
+                    tmem_ld32(t_row + (uint32_t)(g * 64 + 32), r1);
+                    tmem_ld_wait();
+                    if (args.splits > 1) {
+                        uint8_t *b = box_begin();
+                        box_put_f32(b, lane, r0);
+                        box_end(&tmG, b, c0, row0, w.split);
+                        if (c0 + 32 < N) {
+                            b = box_begin();
+                            box_put_f32(b, lane, r1);
+                            box_end(&tmG, b, c0 + 32, row0, w.split);
+                        }
+                    } else {
+                        uint32_t z[32];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            z[j] = pack2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), (T *)nullptr);
+                            z[16 + j] = pack2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), (T *)nullptr);
+                        }
+                        uint8_t *b = box_begin();
+                        box_put_f32(b, lane, z);
+                        box_end(&tmC, b, c0, row0, 0);
+                    }
+                }
+            }
+            fence_before();
+            mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], 0));
+        }
+        if (lane == 0) tma_stores_wait0();
+        if (!ok && lane == 0) {
+            atomicOr(args.status, ST_EPILOGUE);
+            raise_abort_pair(abort_flag, rank);
+        }
+    }
+
+    __syncwarp();
+    fence_before();
+    cluster_sync();  // no CTA leaves while its peer may still touch its memory
+    if (warp == 1) {
+        fence_after();
+        tmem_dealloc<2>(tmem_base, TMEM_COLS);
+    }
+}
+
+__device__ __forceinline__ float2 unpack(uint32_t v, const __nv_bfloat16 *) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 unpack(uint32_t v, const __half *) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); }
+
+// dG and dU from G, U and dZ, eight elements (N % 8 == 0) to a thread: 10 bytes
+// read and 4 written an element.
+template <typename T, bool GELU>
+__global__ void __launch_bounds__(256)
+gated_grad_kernel(const float4 *__restrict__ G, const float4 *__restrict__ U, const uint4 *__restrict__ dZ,
+                  uint4 *__restrict__ dG, uint4 *__restrict__ dU, long long n8)
+{
+    pdl_wait();
+    const long long stride = (long long)gridDim.x * blockDim.x;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += stride) {
+        const float4 g0 = __ldcs(G + 2 * i), g1 = __ldcs(G + 2 * i + 1);
+        const float4 u0 = __ldcs(U + 2 * i), u1 = __ldcs(U + 2 * i + 1);
+        const uint4 z = __ldcs(dZ + i);
+        const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+        const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+        const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
+        uint32_t og[4], ou[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 d = unpack(zz[j], (const T *)nullptr);
+            float a0, da0, a1, da1;
+            gate_act_grad<GELU>(g[2 * j], a0, da0);
+            gate_act_grad<GELU>(g[2 * j + 1], a1, da1);
+            ou[j] = pack2(d.x * a0, d.y * a1, (T *)nullptr);
+            og[j] = pack2(d.x * u[2 * j] * da0, d.y * u[2 * j + 1] * da1, (T *)nullptr);
+        }
+        dG[i] = make_uint4(og[0], og[1], og[2], og[3]);
+        dU[i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    }
+}
+
+// Adds the FP32 partials of dX in order, four elements to a thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+gated_sum_kernel(const float4 *__restrict__ part, uint2 *__restrict__ out, int splits, long long n4)
+{
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n4) return;
+    float4 a = part[i];
+    for (int s = 1; s < splits; ++s) {
+        const float4 b = part[(long long)s * n4 + i];
+        a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+    }
+    out[i] = make_uint2(pack2(a.x, a.y, (T *)nullptr), pack2(a.z, a.w, (T *)nullptr));
+}
+
+template <typename T, uint32_t FORMAT, int MODE, bool GELU>
+int clusters_max(int dev) {
+    static std::atomic<int> cached[kMaxDevices];
+    static std::once_flag once[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        cached[dev].store(max_clusters(reinterpret_cast<const void *>(gated_pair_kernel<T, FORMAT, MODE, GELU>), THREADS,
+                                       smem_bytes(MODE), 2));
+    });
+    return cached[dev].load();
+}
+
+constexpr CUtensorMapDataType map_type(uint32_t format) {
+    return format == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+// A row-major 16-bit matrix [rows, cols] (two of them, `stride` bytes apart, for z = 2).
+bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long long cols, int box_cols, int box_rows,
+           int z = 1, long long stride = 0) {
+    return make_map3(m, p, map_type(format), cols, rows, z, cols * 2, z > 1 ? stride : rows * cols * 2, box_cols, box_rows,
+                     1, true);
+}
+
+template <typename T, uint32_t FORMAT, int MODE, bool GELU>
+cudaError_t launch_pair(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb2, const CUtensorMap &tc,
+                        const CUtensorMap &tg, const CUtensorMap &tu, const Args &args, int clusters, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem_bytes(MODE);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    pdl_attr(attr[1]);
+    cfg.attrs = attr;
+    cfg.numAttrs = g_pdl ? 2 : 1;
+    return launch_counted(&cfg, gated_pair_kernel<T, FORMAT, MODE, GELU>, ta, tb, tb2, tc, tg, tu, args);
+}
+
+template <typename T, uint32_t FORMAT, bool GELU>
+cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s) {
+    const int cmax = clusters_max<T, FORMAT, FWD, GELU>(dev);
+    if (cmax <= 0) return cudaErrorNotSupported;
+    const long long tiles = (p.M + 255LL) / 256 * ((p.N + 127LL) / 128);
+    if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    CUtensorMap tx, tg, tu, tz, tsg, tsu;
+    if (!map16(&tx, p.X, FORMAT, p.M, p.K, BK, 128) || !map16(&tg, p.Wg, FORMAT, p.K, p.N, 64, BK) ||
+        !map16(&tu, p.Wu, FORMAT, p.K, p.N, 64, BK) || !map16(&tz, p.Z, FORMAT, p.M, p.N, 64, 32))
+        return cudaErrorInvalidValue;
+    tsg = tsu = tz;
+    const long long row = 4LL * p.N;
+    if (p.G && (!make_map3(&tsg, p.G, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.N, p.M, 1, row, row * p.M, 32, 32, 1, true) ||
+                !make_map3(&tsu, p.U, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.N, p.M, 1, row, row * p.M, 32, 32, 1, true)))
+        return cudaErrorInvalidValue;
+    Args a = {};
+    a.M = p.M;
+    a.N = p.N;
+    a.num_kb = (p.K + BK - 1) / BK;
+    a.bn = 128;
+    a.splits = 1;
+    a.save = p.G != nullptr;
+    a.status = status;
+    return launch_pair<T, FORMAT, FWD, GELU>(tx, tg, tu, tz, tsg, tsu, a, (int)std::min<long long>(tiles, cmax), s);
+}
+
+template <typename T, uint32_t FORMAT, bool GELU>
+cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, cudaStream_t s) {
+    const int cmax = clusters_max<T, FORMAT, DX, false>(dev);
+    if (cmax <= 0) return cudaErrorNotSupported;
+    const long long mn = (long long)p.M * p.N;
+    // dX: tile width and split.  Waves of tiles over the clusters, widest on ties
+    // (a tile's time is set mostly by the operand feed); with under half the
+    // clusters busy, the joined index is split over the idle ones.
+    const long long tiles_m = (p.M + 255LL) / 256;
+    const int half = (p.N + BK - 1) / BK;
+    int bn = 256, splits = 1;
+    long long best = -1;
+    for (int c = 256; c >= 128; c -= 64) {
+        const long long t = tiles_m * ((p.K + c - 1) / c);
+        const long long cost = (t + cmax - 1) / cmax * (c > 224 ? c : 224);
+        if (best < 0 || cost < best) { best = cost; bn = c; }
+    }
+    const long long wide = tiles_m * ((p.K + 255) / 256);
+    if (wide * 2 <= cmax) {
+        bn = 256;
+        splits = (int)std::max<long long>(1, std::min<long long>({cmax / wide, 2LL * half / 8, 16LL}));
+    }
+    const long long tiles = tiles_m * ((p.K + bn - 1) / bn);
+    if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    // scratch: dG and dU, and dX's partials
+    const size_t grads = (size_t)mn * 4, parts = p.dX && splits > 1 ? (size_t)splits * p.M * p.K * 4 : 0;
+    const size_t off = (grads + 255) & ~(size_t)255;
+    void *ws = nullptr;
+    cudaError_t e = scratch_alloc(&ws, off + parts, s);
+    if (e != cudaSuccess) return e;
+    // The gradient whose dW lies lower comes first, so that the two dW are a batch
+    // with a positive stride.
+    const bool g_first = !p.dWg || !p.dWu || (uintptr_t)p.dWg < (uintptr_t)p.dWu;
+    T *d0 = static_cast<T *>(ws), *d1 = d0 + mn;
+    T *dG = g_first ? d0 : d1, *dU = g_first ? d1 : d0;
+    {
+        const long long n8 = mn / 8;
+        const unsigned grid = (unsigned)std::min<long long>((n8 + 255) / 256, (long long)num_sms * 8);
+        cudaLaunchAttribute attr[1];
+        const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(256), 0, s, attr);
+        e = launch_counted(&cfg, gated_grad_kernel<T, GELU>, reinterpret_cast<const float4 *>(p.G),
+                           reinterpret_cast<const float4 *>(p.U), static_cast<const uint4 *>(p.dZ),
+                           reinterpret_cast<uint4 *>(dG), reinterpret_cast<uint4 *>(dU), n8);
+    }
+    if (e == cudaSuccess && p.dX) {
+        CUtensorMap ta, tb, tb2, tc, tp;
+        bool ok = map16(&ta, d0, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) &&
+                  map16(&tb, g_first ? p.Wg : p.Wu, FORMAT, p.K, p.N, BK, bn / 2) &&
+                  map16(&tb2, g_first ? p.Wu : p.Wg, FORMAT, p.K, p.N, BK, bn / 2) &&
+                  map16(&tc, p.dX, FORMAT, p.M, p.K, 64, 32);
+        tp = tc;
+        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + off);
+        const long long row = 4LL * p.K;
+        if (splits > 1)
+            ok = ok && make_map3(&tp, part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, row, row * p.M, 32, 32, 1, true);
+        Args a = {};
+        a.M = p.M;
+        a.N = p.K;
+        a.num_kb = 2 * half;
+        a.kb_half = half;
+        a.bn = bn;
+        a.splits = splits;
+        a.status = status;
+        e = ok ? launch_pair<T, FORMAT, DX, false>(ta, tb, tb2, tc, tp, tp, a,
+                                                   (int)std::min<long long>(tiles * splits, cmax), s)
+               : cudaErrorInvalidValue;
+        if (e == cudaSuccess && splits > 1) {
+            const long long n4 = (long long)p.M * p.K / 4;
+            cudaLaunchAttribute attr[1];
+            const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, attr);
+            e = launch_counted(&cfg, gated_sum_kernel<T>, reinterpret_cast<const float4 *>(part),
+                               static_cast<uint2 *>(p.dX), splits, n4);
+        }
+    }
+    if (e == cudaSuccess && (p.dWg || p.dWu)) {
+        // dW = X^T {dG, dU}: X stored [M, K] is the transposed operand
+        ProblemEx q = {};
+        q.A = p.X;
+        q.M = p.K;
+        q.N = p.N;
+        q.K = p.M;
+        q.a_t = true;
+        q.lda = p.K;
+        q.ldb = q.ldc = p.N;
+        q.alpha = 1.0f;
+        q.elt = p.elt;
+        const bool both = p.dWg && p.dWu;
+        bool done = false;
+        if (both) {
+            q.B = d0;
+            q.C = g_first ? p.dWg : p.dWu;
+            q.batch = 2;
+            q.sb = mn;
+            q.sc = (long long)(((uintptr_t)(g_first ? p.dWu : p.dWg) - (uintptr_t)q.C) / 2);
+            e = launch_umma_ex(q, status, s);
+            done = e != cudaErrorNotSupported;  // (outputs too far apart for a tensor map: one at a time)
+        }
+        if (!done) {
+            q.batch = 1;
+            q.sb = q.sc = 0;
+            e = cudaSuccess;
+            for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+                q.B = i ? dU : dG;
+                q.C = i ? p.dWu : p.dWg;
+                if (q.C) e = launch_umma_ex(q, status, s);
+            }
+        }
+    }
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    return e != cudaSuccess ? e : f;
+}
+
+}  // namespace
+
+cudaError_t launch_gated(const GatedProblem &p, int *status, cudaStream_t s) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (p.elt == Elt::BF16)
+        return p.gelu ? forward<__nv_bfloat16, 1, true>(p, dev, status, s) : forward<__nv_bfloat16, 1, false>(p, dev, status, s);
+    return p.gelu ? forward<__half, 0, true>(p, dev, status, s) : forward<__half, 0, false>(p, dev, status, s);
+}
+
+cudaError_t launch_gated_backward(const GatedBackward &p, int num_sms, int *status, cudaStream_t s) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (p.elt == Elt::BF16)
+        return p.gelu ? backward<__nv_bfloat16, 1, true>(p, dev, num_sms, status, s)
+                      : backward<__nv_bfloat16, 1, false>(p, dev, num_sms, status, s);
+    return p.gelu ? backward<__half, 0, true>(p, dev, num_sms, status, s)
+                  : backward<__half, 0, false>(p, dev, num_sms, status, s);
+}
+
+}  // namespace gemm_gb300

@@ -1,0 +1,328 @@
+// Gated projections for few rows (M <= 64: single tokens, decode batches), bound
+// by reading Wg and Wu [K, N] once.
+//
+// The operands swap roles: a CTA's strip is 64 columns of Z, and the MMA's 128
+// rows are those columns of Wg and the same of Wu (MN-major in shared memory: one
+// 64-column x 128-k box of each per stage); the M rows of X are its N = nb (M
+// rounded up to 16; K-major, two boxes of 64 k).  So tensor-memory lanes 0-63 hold
+// G and 64-127 U of the strip, and both meet in shared memory, where Z is formed.
+// The CS CTAs of a cluster share a strip's K and add their FP32 partials through
+// distributed shared memory in rank order; CS is the largest for which every CTA
+// is resident at once, two to an SM.  Deterministic, one launch, no workspace.
+//
+// Every wait is bounded; on expiry a code goes to the status word, the CTA's own
+// loads and MMAs are waited for, and its tensor memory is released.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "gated.h"
+#include "tc_ptx.cuh"
+
+namespace gemm_gb300 {
+namespace {
+
+using namespace tc;
+
+constexpr int THREADS = 192;
+constexpr int KB = 128;                // k per stage
+constexpr int MAX_STAGES = 3;
+constexpr int W_BOX = 64 * KB * 2;     // 64 columns x 128 k: 16 KiB
+constexpr int W_STAGE = 2 * W_BOX;     // of Wg and of Wu
+constexpr int RING = 108 * 1024;       // two CTAs to an SM: 3 stages (M <= 16), 2 above
+constexpr int SMEM = 1024 + RING + 256;
+constexpr uint32_t TMEM_COLS = 64;
+constexpr int LD = 128 + 4;            // floats per row of a partial [M][64 G, 64 U]
+static_assert(64 * LD * 4 <= RING, "a partial fits the drained ring");
+
+__host__ __device__ constexpr int nb_of(int M) { return (M + 15) / 16 * 16; }
+__host__ __device__ constexpr int stages_of(int nb) {
+    return RING / (W_STAGE + 2 * nb * 128) < MAX_STAGES ? RING / (W_STAGE + 2 * nb * 128) : MAX_STAGES;
+}
+
+struct Bars {
+    uint64_t full[MAX_STAGES];
+    uint64_t empty[MAX_STAGES];
+    uint64_t acc_full;
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+struct Args {
+    void *Z;
+    float *G, *U;
+    int M, N, K, cs;
+    int *status;
+};
+
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+template <typename T, uint32_t FORMAT, bool GELU>
+__global__ void __launch_bounds__(THREADS, 2)
+gated_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmG,
+                    const __grid_constant__ CUtensorMap tmU, const Args args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int M = args.M, N = args.N, cs = args.cs;
+    const int nb = nb_of(M), stages = stages_of(nb), x_box = nb * 128, x_stage = 2 * x_box;
+    uint8_t *w_tiles = smem;
+    uint8_t *x_tiles = w_tiles + stages * W_STAGE;
+    float *part = reinterpret_cast<float *>(smem);  // [M][LD] once the ring is drained
+    Bars *bars = reinterpret_cast<Bars *>(smem + RING);
+    volatile int *abort_flag = &bars->abort;
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = cs > 1 ? (int)cluster_ctarank() : 0;
+    const int n0 = (int)(cs > 1 ? cluster_id_x() : blockIdx.x) * 64;
+    const int num_kb = (args.K + KB - 1) / KB;
+    const int kb0 = (int)((long long)num_kb * rank / cs), kb1 = (int)((long long)num_kb * (rank + 1) / cs);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        mbar_init(&bars->acc_full, 1);
+        mbar_init(&bars->drain, 1);
+        bars->abort = 0;
+        mbar_init_fence();
+        prefetch_desc(&tmX);
+        prefetch_desc(&tmG);
+        prefetch_desc(&tmU);
+    }
+    if (warp == 1) tmem_alloc<1>(&bars->tmem_base, TMEM_COLS);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+    if (warp == 0 && lane == 0 && g_pdl) {
+        // The strip's first weights to L2 while the previous kernel drains: a hint,
+        // which changes no value that a later load returns.
+        for (int kb = kb0; kb < min(kb1, kb0 + stages); ++kb) {
+            tma_prefetch_l2_3d(&tmG, n0, kb * KB, 0);
+            tma_prefetch_l2_3d(&tmU, n0, kb * KB, 0);
+        }
+    }
+    pdl_wait();
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------------ producer
+        const uint32_t tx = (uint32_t)(W_STAGE + x_stage);
+        int stage = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) {
+                atomicOr(args.status, ST_PRODUCER);
+                *abort_flag = 1;
+                break;
+            }
+            mbar_arrive_expect_tx(&bars->full[stage], tx);
+            uint8_t *w = w_tiles + stage * W_STAGE, *x = x_tiles + stage * x_stage;
+            tma_load_3d(w, &tmG, &bars->full[stage], n0, kb * KB, 0);
+            tma_load_3d(w + W_BOX, &tmU, &bars->full[stage], n0, kb * KB, 0);
+            tma_load_3d(x, &tmX, &bars->full[stage], kb * KB, 0, 0);
+            tma_load_3d(x + x_box, &tmX, &bars->full[stage], kb * KB + 64, 0, 0);
+            ++issued;
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        pdl_launch_dependents();
+        for (long long i = (issued > stages ? issued - stages : 0); i < issued; ++i)
+            if (!mbar_wait(&bars->full[i % stages], (uint32_t)((i / stages) & 1), abort_flag, false)) {
+                atomicOr(args.status, ST_DRAIN);
+                break;
+            }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        // A = the weights, MN-major: 64-column boxes W_BOX bytes apart, a K step of
+        // 16 rows is 2048 bytes.  B = X, K-major: a K step is 32 bytes of a row.
+        const bool issuer = elect_one();
+        const uint32_t idesc = (1u << 4) | (FORMAT << 7) | (FORMAT << 10) | (1u << 15) | (((uint32_t)nb >> 3) << 17) |
+                               ((128u >> 4) << 24);
+        const uint64_t w_desc0 = desc_sw128(smem_u32(w_tiles), W_BOX, 1024);
+        const uint64_t x_desc0 = desc_sw128(smem_u32(x_tiles), 16, 1024);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait(&bars->full[stage], phase, abort_flag, true)) { ok = false; break; }
+            fence_after();
+            const uint64_t wd = w_desc0 + (uint64_t)((stage * W_STAGE) >> 4);
+            const uint64_t xd = x_desc0 + (uint64_t)((stage * x_stage) >> 4);
+            const uint64_t xd1 = xd + (uint64_t)(x_box >> 4);
+            if (issuer) {
+#pragma unroll
+                for (int ks = 0; ks < KB / 16; ++ks)
+                    mma_f16(tmem_base, wd + ks * (2048u >> 4), (ks < 4 ? xd : xd1) + (ks & 3) * 2, idesc,
+                            (uint32_t)(kb != kb0 || ks != 0));
+                commit<1>(&bars->empty[stage]);
+            }
+            if (++stage == stages) { stage = 0; phase ^= 1u; }
+        }
+        if (issuer) {
+            if (ok) {
+                commit<1>(&bars->acc_full);
+            } else {
+                atomicOr(args.status, ST_MMA);
+                *abort_flag = 1;
+            }
+            commit<1>(&bars->drain);
+            if (!mbar_wait(&bars->drain, 0, abort_flag, false)) atomicOr(args.status, ST_DRAIN);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ partial to shared memory
+        const int quarter = warp & 3, nl = quarter * 32 + lane;
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full, 0, abort_flag, true));
+        if (!ok && lane == 0) {
+            atomicOr(args.status, ST_EPILOGUE);
+            *abort_flag = 1;
+        }
+        fence_after();
+        __syncwarp();
+#pragma unroll 1
+        for (int c = 0; c < M; c += 32) {
+            uint32_t r[32];
+            if (ok) {
+                tmem_ld32(tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c, r);
+                tmem_ld_wait();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = 0u;
+            }
+            // (the ring is drained: every MMA that read it has completed)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j < M) part[(c + j) * LD + nl] = __uint_as_float(r[j]);
+        }
+    }
+
+    fence_before();
+    __syncwarp();
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+    {
+        // (row, four columns) pairs dealt out to the CTAs in equal ranges; partials added in rank order
+        const int groups = min(64, N - n0) / 4;  // N % 8 == 0
+        const int total = M * groups;
+        const int e1 = (int)((long long)total * (rank + 1) / cs);
+        for (int e = (int)((long long)total * rank / cs) + (int)threadIdx.x; e < e1; e += THREADS) {
+            const int m = e / groups, c4 = (e - m * groups) * 4;
+            const float *at = part + m * LD + c4;
+            float4 g, u;
+            if (cs == 1) {
+                g = *reinterpret_cast<const float4 *>(at);
+                u = *reinterpret_cast<const float4 *>(at + 64);
+            } else {
+                float4 pg[8], pu[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < cs) {
+                        const uint32_t a = map_to_rank(at, (uint32_t)j);
+                        pg[j] = ld_cluster_f4(a);
+                        pu[j] = ld_cluster_f4(a + 256);
+                    }
+                g = pg[0];
+                u = pu[0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j)
+                    if (j < cs) {
+                        g.x += pg[j].x; g.y += pg[j].y; g.z += pg[j].z; g.w += pg[j].w;
+                        u.x += pu[j].x; u.y += pu[j].y; u.z += pu[j].z; u.w += pu[j].w;
+                    }
+            }
+            const size_t o = (size_t)m * N + n0 + c4;
+            if (args.G) {
+                *reinterpret_cast<float4 *>(args.G + o) = g;
+                *reinterpret_cast<float4 *>(args.U + o) = u;
+            }
+            uint2 w;
+            w.x = pack2(gate_act<GELU>(g.x) * u.x, gate_act<GELU>(g.y) * u.y, (T *)nullptr);
+            w.y = pack2(gate_act<GELU>(g.z) * u.z, gate_act<GELU>(g.w) * u.w, (T *)nullptr);
+            *reinterpret_cast<uint2 *>(static_cast<T *>(args.Z) + o) = w;
+        }
+    }
+    __syncwarp();
+    if (cs > 1) cluster_sync();  // every CTA keeps its shared memory until the others have read it
+    if (warp == 1) {
+        fence_after();
+        tmem_dealloc<1>(tmem_base, TMEM_COLS);
+    }
+}
+
+template <typename T, uint32_t FORMAT, bool GELU>
+int clusters_max(int dev, int cs) {
+    static std::atomic<int> cached[kMaxDevices][9];
+    static std::once_flag once[kMaxDevices][9];
+    std::call_once(once[dev][cs], [&] {
+        cached[dev][cs].store(
+            max_clusters(reinterpret_cast<const void *>(gated_skinny_kernel<T, FORMAT, GELU>), THREADS, SMEM, cs));
+    });
+    return cached[dev][cs].load();
+}
+
+template <typename T, uint32_t FORMAT, bool GELU>
+cudaError_t launch(const GatedProblem &p, int num_sms, int *status, cudaStream_t s) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    const long long strips = (p.N + 63LL) / 64, num_kb = (p.K + KB - 1LL) / KB;
+    if (clusters_max<T, FORMAT, GELU>(dev, 1) <= 0) return cudaErrorNotSupported;
+    int cs = 1;
+    for (int c = 2; c <= 8 && c <= num_kb && strips * c <= 2LL * num_sms; ++c)
+        if (clusters_max<T, FORMAT, GELU>(dev, c) >= strips) cs = c;
+    const auto dt = FORMAT == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap tx, tg, tu;
+    const long long xr = 2LL * p.K, wr = 2LL * p.N;
+    if (!make_map3(&tx, p.X, dt, p.K, p.M, 1, xr, xr * p.M, 64, nb_of(p.M), 1, true) ||
+        !make_map3(&tg, p.Wg, dt, p.N, p.K, 1, wr, wr * p.K, 64, KB, 1, true) ||
+        !make_map3(&tu, p.Wu, dt, p.N, p.K, 1, wr, wr * p.K, 64, KB, 1, true))
+        return cudaErrorInvalidValue;
+    Args a = {};
+    a.Z = p.Z;
+    a.G = p.G;
+    a.U = p.U;
+    a.M = p.M;
+    a.N = p.N;
+    a.K = p.K;
+    a.cs = cs;
+    a.status = status;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(strips * cs), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    pdl_attr(attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cs;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = g_pdl ? attr : attr + 1;
+    cfg.numAttrs = (g_pdl ? 1 : 0) + (cs > 1 ? 1 : 0);
+    return launch_counted(&cfg, gated_skinny_kernel<T, FORMAT, GELU>, tx, tg, tu, a);
+}
+
+}  // namespace
+
+cudaError_t launch_gated_skinny(const GatedProblem &p, int num_sms, int *status, cudaStream_t s) {
+    if (p.M < 1 || p.M > kGatedSkinnyMaxM) return cudaErrorInvalidValue;
+    if (p.elt == Elt::BF16)
+        return p.gelu ? launch<__nv_bfloat16, 1, true>(p, num_sms, status, s)
+                      : launch<__nv_bfloat16, 1, false>(p, num_sms, status, s);
+    return p.gelu ? launch<__half, 0, true>(p, num_sms, status, s) : launch<__half, 0, false>(p, num_sms, status, s);
+}
+
+}  // namespace gemm_gb300

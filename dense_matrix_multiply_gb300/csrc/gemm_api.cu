@@ -8,9 +8,11 @@
 #include <string.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "fp4.h"
+#include "gated.h"
 #include "gemm.h"
 #include "internal.h"
 
@@ -542,6 +544,72 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     return finish(e != cudaSuccess ? e : f, name);
 }
 
+// ------------------------------------------------------------ gated block
+bool gated_args_ok(const char *who, int dtype, int act, int M, int N, int K, std::initializer_list<const void *> ptrs) {
+    if ((dtype != GEMM_F16 && dtype != GEMM_BF16) || (act != GEMM_ACT_SILU && act != GEMM_ACT_GELU_TANH)) return false;
+    if (M < 0 || N < 0 || K < 0) return false;
+    bool ok = N % 8 == 0 && K % 8 == 0;
+    for (const void *p : ptrs) ok = ok && aligned16(p);
+    if (!ok) snprintf(t_last_error, sizeof(t_last_error), "%s: needs every pointer 16-byte aligned and N, K multiples of 8", who);
+    return ok;
+}
+struct Span {
+    const void *p;
+    size_t bytes;
+};
+bool any_overlap(std::initializer_list<Span> out, std::initializer_list<Span> in) {
+    for (const Span *o = out.begin(); o != out.end(); ++o) {
+        for (const Span &i : in)
+            if (o->p && i.p && overlaps(o->p, o->bytes, i.p, i.bytes)) return true;
+        for (const Span *q = o + 1; q != out.end(); ++q)
+            if (o->p && q->p && overlaps(o->p, o->bytes, q->p, q->bytes)) return true;
+    }
+    return false;
+}
+cudaError_t zero(const Span &s, cudaStream_t st, cudaError_t e) {
+    return e == cudaSuccess && s.p && s.bytes ? cudaMemsetAsync(const_cast<void *>(s.p), 0, s.bytes, st) : e;
+}
+
+gemm_status_t run_gated(int dtype, int act, const void *X, const void *Wg, const void *Wu, void *Z, float *G, float *U,
+                        int M, int N, int K) {
+    if (!gated_args_ok("gemm_gated", dtype, act, M, N, K, {X, Wg, Wu, Z, G, U})) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0 || N == 0) { t_last_kernel = "noop"; return GEMM_OK; }
+    if (!Z || (K > 0 && (!X || !Wg || !Wu)) || !G != !U) return GEMM_ERR_INVALID_VALUE;
+    const size_t mn = (size_t)M * N, x = (size_t)M * K * 2, w = (size_t)K * N * 2;
+    const Span z{Z, mn * 2}, gs{G, mn * 4}, us{U, mn * 4};
+    if (any_overlap({z, gs, us}, {{X, x}, {Wg, w}, {Wu, w}})) return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    cudaStream_t s = t_stream;
+    if (K == 0)  // G = U = 0, and act(0) * 0 = 0
+        return finish(zero(us, s, zero(gs, s, zero(z, s, cudaSuccess))), "zero_fill");
+    const GatedProblem p{X, Wg, Wu, Z, G, U, M, N, K, elt16(dtype), act == GEMM_ACT_GELU_TANH};
+    if (M <= kGatedSkinnyMaxM) return finish(launch_gated_skinny(p, dev->num_sms, dev->status, s), "gated_skinny");
+    return finish(launch_gated(p, dev->status, s), "gated_pair");
+}
+
+gemm_status_t run_gated_backward(int dtype, int act, const void *X, const void *Wg, const void *Wu, const float *G,
+                                 const float *U, const void *dZ, void *dX, void *dWg, void *dWu, int M, int N, int K) {
+    if (!gated_args_ok("gemm_gated_backward", dtype, act, M, N, K, {X, Wg, Wu, G, U, dZ, dX, dWg, dWu}))
+        return GEMM_ERR_INVALID_VALUE;
+    if (K == 0 || (!dX && !dWg && !dWu)) { t_last_kernel = "noop"; return GEMM_OK; }
+    const size_t mn = (size_t)M * N, x = (size_t)M * K * 2, w = (size_t)K * N * 2;
+    const Span ox{dX, x}, og{dWg, w}, ou{dWu, w};
+    const bool work = M > 0 && N > 0;
+    if (work && (!G || !U || !dZ || (dX && (!Wg || !Wu)) || ((dWg || dWu) && !X))) return GEMM_ERR_INVALID_VALUE;
+    if (any_overlap({ox, og, ou}, {{X, x}, {Wg, w}, {Wu, w}, {G, mn * 4}, {U, mn * 4}, {dZ, mn * 2}}))
+        return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    cudaStream_t s = t_stream;
+    if (!work)  // empty sums: no rows (dW), no hidden units (dX)
+        return finish(zero(ou, s, zero(og, s, zero(ox, s, cudaSuccess))), "zero_fill");
+    const GatedBackward p{X, Wg, Wu, dZ, G, U, dX, dWg, dWu, M, N, K, elt16(dtype), act == GEMM_ACT_GELU_TANH};
+    return finish(launch_gated_backward(p, dev->num_sms, dev->status, s), "gated_backward");
+}
+
 }  // namespace
 
 extern "C" {
@@ -734,6 +802,17 @@ GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t for
                                        void *C, int64_t ldc, int M, int N, int K) {
     return run_fp4("gemm_fp4_linear", (int)dtype, (int)format, X, ldx, nullptr, nullptr, gx, Qw, Sw, gw, C, ldc, M, N,
                    K, true);
+}
+
+GEMM_API gemm_status_t gemm_gated(gemm_dtype_t dtype, gemm_act_t act, const void *X, const void *W_g, const void *W_u,
+                                  void *Z, float *G, float *U, int M, int N, int K) {
+    return run_gated((int)dtype, (int)act, X, W_g, W_u, Z, G, U, M, N, K);
+}
+
+GEMM_API gemm_status_t gemm_gated_backward(gemm_dtype_t dtype, gemm_act_t act, const void *X, const void *W_g,
+                                           const void *W_u, const float *G, const float *U, const void *dZ, void *dX,
+                                           void *dW_g, void *dW_u, int M, int N, int K) {
+    return run_gated_backward((int)dtype, (int)act, X, W_g, W_u, G, U, dZ, dX, dW_g, dW_u, M, N, K);
 }
 
 GEMM_API gemm_status_t gemm_set_stream(void *cuda_stream) {

@@ -322,6 +322,37 @@ GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t for
                                        const float *gx, const uint8_t *Qw, const uint8_t *Sw, const float *gw,
                                        void *C, int64_t ldc, int M, int N, int K);
 
+/* Gated feed-forward projections, for training and serving:
+ *     G = X W_g,  U = X W_u,  Z = act(G) * U  (element by element)
+ * X [M,K], W_g and W_u [K,N], Z [M,N] row-major half or bf16 (dtype) with tight
+ * strides, both products and the activation in one kernel; G, U and act in FP32,
+ * Z rounded once.  act: SiLU, g / (1 + e^-g), or the tanh form of GELU,
+ * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2.  G and U (both or neither):
+ * FP32 [M,N], stored for gemm_gated_backward.  (gemm_bf16_rm_silu_mul keeps the
+ * rounding points of the unfused chain instead: G, U and act(G) rounded to bf16.)
+ * M may be any size: one token to a long prompt.  Needs every pointer 16-byte
+ * aligned and N, K multiples of 8 (GEMM_ERR_INVALID_VALUE otherwise, with a
+ * message in gemm_last_error).  K = 0 gives zeros.  GEMM_ERR_ALIAS if an output
+ * overlaps an input or another output. */
+typedef enum gemm_act_t { GEMM_ACT_SILU = 0, GEMM_ACT_GELU_TANH = 1 } gemm_act_t;
+
+GEMM_API gemm_status_t gemm_gated(gemm_dtype_t dtype, gemm_act_t act, const void *X, const void *W_g, const void *W_u,
+                                  void *Z, float *G, float *U, int M, int N, int K);
+
+/* Its gradients, from G and U as gemm_gated stored them and dZ [M,N] (dtype):
+ *     dG = dZ * U * act'(G),  dU = dZ * act(G)
+ *     dX = dG W_g^T + dU W_u^T,  dW_g = X^T dG,  dW_u = X^T dU
+ * dX [M,K], dW_g and dW_u [K,N] (dtype), each overwritten; a null one is left out
+ * (and X, W_g, W_u may be null where nothing that is asked for reads them).  dG
+ * and dU are formed in FP32 and rounded to dtype, the operands of the products,
+ * whose sums are FP32, rounded once.  dG, dU and, with few rows, FP32 partials of
+ * dX lie in stream-ordered scratch (from a pool of the library's own that keeps up
+ * to 1 GiB on the device between calls).  M = 0 or N = 0 gives zeros.  Needs and
+ * errors as gemm_gated. */
+GEMM_API gemm_status_t gemm_gated_backward(gemm_dtype_t dtype, gemm_act_t act, const void *X, const void *W_g,
+                                           const void *W_u, const float *G, const float *U, const void *dZ, void *dX,
+                                           void *dW_g, void *dW_u, int M, int N, int K);
+
 /* Stream for the calling host thread's subsequent calls: a cudaStream_t passed
  * as void*.  NULL selects the legacy default stream.  The stream stays owned by
  * the caller and must outlive the calls issued on it. */
