@@ -1,140 +1,176 @@
 // 4-bit block-scaled quantisation of 16-bit rows, and reading it back.
 //
 // Quantiser.  A lane holds 16 consecutive elements of a row (half an MX block
-// or a whole NV block), a warp 512; the block's largest magnitude is an integer
+// or a whole NV block), a warp 512 elements of each of ROWS rows, all of whose
+// loads are in flight together; the block's largest magnitude is an integer
 // maximum over packed magnitude bits (a NaN is above an infinity is above every
 // number), shared between two lanes for MX.  Rows past M and elements past K,
 // up to the padded sizes, count as zeros: their scale bytes are written, so
 // that no scale that a product reads is left undefined.
-// Bound: HBM, 2 bytes read and 0.53 (MX) or 0.56 (NV) written an element.
+// Read-back: a lane writes 16 bytes (eight values), a warp 512 elements of each
+// of ROWS rows.
+// Loads of A (stores of the values read back) are as wide as its rows' alignment
+// allows: 16, 8, 4 or 2 bytes.
+// Bound: HBM, 2 bytes read and 0.53 (MX) or 0.56 (NV) written an element, or the
+// other way round.
 #include <cuda_runtime.h>
 
 #include "fp4.h"
+#include "tc_ptx.cuh"
 
 namespace gemm_gb300 {
 namespace {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 4, ROWS = 2;
 
-template <typename T, bool NV, bool VEC>
+// Block (x, y): rows [8 x, 8 x + 8), elements [512 y, 512 y + 512) and, past
+// 65535 x 512 elements, every gridDim.y-th such piece.
+template <typename T, bool NV, int VEC>
 __global__ void __launch_bounds__(WARPS * 32)
 fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restrict__ tensor_scale,
-                    uint8_t *__restrict__ Q, uint8_t *__restrict__ S, int M, int K, int segs, long long units)
+                    uint8_t *__restrict__ Q, uint8_t *__restrict__ S, int M, int K)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);  // one row's 512 elements
-    if (unit >= units) return;
-    const int row = (int)(unit / segs);
-    const int k = (int)(unit - (long long)row * segs) * 512 + lane * 16;
-    const float g = NV && tensor_scale ? *tensor_scale : 1.0f;
-    uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    if (row < M && k < K) {
-        const T *a = A + row * lda + k;
-        if (VEC && k + 16 <= K) {
-            const uint4 u0 = __ldg(reinterpret_cast<const uint4 *>(a)), u1 = __ldg(reinterpret_cast<const uint4 *>(a) + 1);
-            v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
-            v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
-        } else {
-            const unsigned short *h = reinterpret_cast<const unsigned short *>(a);
+    const int row0 = (int)blockIdx.x * (WARPS * ROWS) + (int)(threadIdx.x >> 5) * ROWS;
+    const Fp4Tensor t = fp4_tensor<NV>(tensor_scale);
+    const int atoms = fp4_atoms(NV, K);
+    const long long rb = fp4_row_bytes(K);
+    constexpr int SPAN = NV ? 1 : 2;  // lanes to a block
+    for (long long k = (long long)blockIdx.y * 512 + lane * 16; k - lane * 16 < K; k += (long long)gridDim.y * 512) {
+        uint32_t v[ROWS][8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (k + i < K) v[i >> 1] |= (uint32_t)__ldg(h + i) << (16 * (i & 1));
+        for (int i = 0; i < ROWS; ++i) {
+            const int row = row0 + i;
+            const long long left = row < M ? K - k : 0;
+            fp4_load16<VEC>(A + row * lda + k, (int)(left > 16 ? 16 : left), v[i]);
+        }
+        const int a = (int)(k / (64 * SPAN));
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int row = row0 + i;
+            uint32_t m = 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = __vmaxu2(m, abs2(v[i][j]));
+            m = max(m & 0xFFFFu, m >> 16);
+            if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            const Fp4Scale sc = fp4_block_scale<NV>(bits16_to_f32<T>(m), t);
+            const uint2 codes = fp4_codes16<T, NV>(v[i], sc);
+            // four blocks' bytes to one word: lanes 4 j .. 4 j + 3 (NV), 8 j .. 8 j + 7 by twos (MX)
+            uint32_t byte = sc.byte;
+            byte |= __shfl_down_sync(0xffffffffu, byte, SPAN) << 8;
+            byte |= __shfl_down_sync(0xffffffffu, byte, 2 * SPAN) << 16;
+            if (lane % (4 * SPAN) == 0 && a < atoms)
+                *reinterpret_cast<uint32_t *>(S + fp4_scale_at(row, a, atoms)) = byte;
+            if (row < M && k / 2 < rb) *reinterpret_cast<uint2 *>(Q + row * rb + k / 2) = codes;
         }
     }
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, abs2(v[i]));
-    m = max(m & 0xFFFFu, m >> 16);
-    if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const Fp4Scale sc = fp4_block_scale<NV>(bits16_to_f32<T>(m), 6.0f * g, g);
-    const uint2 codes = fp4_codes16<T, NV>(v, sc);
-    uint32_t byte = sc.byte;
-    // four blocks' bytes to one word: lanes 4 i .. 4 i + 3 (NV), 8 i .. 8 i + 7 by twos (MX)
-    constexpr int SPAN = NV ? 1 : 2;  // lanes to a block
-    byte |= __shfl_down_sync(0xffffffffu, byte, SPAN) << 8;
-    byte |= __shfl_down_sync(0xffffffffu, byte, 2 * SPAN) << 16;
-    const int atoms = fp4_atoms(NV, K);
-    const int a = k / (64 * SPAN);
-    if (lane % (4 * SPAN) == 0 && a < atoms)
-        *reinterpret_cast<uint32_t *>(S + fp4_scale_at(row, a, atoms)) = byte;
-    const long long rb = fp4_row_bytes(K);
-    if (row < M && k / 2 < rb) *reinterpret_cast<uint2 *>(Q + row * rb + k / 2) = codes;
 }
 
-template <typename T>
-__device__ __forceinline__ T from_f32(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
-
-// A lane reads eight codes (4 bytes) and their block's scale and writes eight
-// values (16 bytes).  v s is exact in FP32 (6 significant bits at most); times
-// g one rounding, and one to T.
-template <typename T, bool NV, bool VEC>
+// v s is exact in FP32 (6 significant bits at most); times g one rounding, and one
+// to T.
+template <typename T, bool NV, int VEC>
 __global__ void __launch_bounds__(WARPS * 32)
 fp4_dequantize_kernel(const uint8_t *__restrict__ Q, const uint8_t *__restrict__ S,
-                      const float *__restrict__ tensor_scale, T *__restrict__ A, long long lda, int M, int K, int segs,
-                      long long units)
+                      const float *__restrict__ tensor_scale, T *__restrict__ A, long long lda, int M, int K)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    const long long unit = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);  // one row's 256 elements
-    if (unit >= units) return;
-    const int row = (int)(unit / segs);
-    const int k = (int)(unit - (long long)row * segs) * 256 + lane * 8;
-    if (k >= K) return;
+    const int row0 = (int)blockIdx.x * (WARPS * ROWS) + (int)(threadIdx.x >> 5) * ROWS;
     const float g = NV && tensor_scale ? *tensor_scale : 1.0f;
-    const uint32_t codes = *reinterpret_cast<const uint32_t *>(Q + row * fp4_row_bytes(K) + k / 2);
+    const int atoms = fp4_atoms(NV, K);
+    const long long rb = fp4_row_bytes(K);
     constexpr int B = fp4_block(NV);
-    const uint32_t byte = S[fp4_scale_at(row, k / (4 * B), fp4_atoms(NV, K)) + (k / B & 3)];
-    float v[8];
-    fp4_unpack8(codes, fp4_scale_value<NV>(byte), v);
-    T *a = A + row * lda + k;
-    T o[8];
+    for (long long k0 = (long long)blockIdx.y * 512 + lane * 8; k0 - lane * 8 < K; k0 += (long long)gridDim.y * 512) {
+        uint32_t codes[ROWS][2], byte[ROWS][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = from_f32<T>(NV ? v[i] * g : v[i]);
-    if (VEC && k + 8 <= K) {
-        uint4 w;
-        memcpy(&w, o, 16);
-        *reinterpret_cast<uint4 *>(a) = w;
-    } else {
+        for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (k + i < K) a[i] = o[i];
+            for (int h = 0; h < 2; ++h) {
+                const long long k = k0 + h * 256;
+                const int row = row0 + i;
+                codes[i][h] = byte[i][h] = 0u;
+                if (row < M && k < K) {
+                    codes[i][h] = __ldg(reinterpret_cast<const uint32_t *>(Q + row * rb + k / 2));
+                    byte[i][h] = __ldg(S + fp4_scale_at(row, (int)(k / (4 * B)), atoms) + (k / B & 3));
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const long long k = k0 + h * 256;
+                const int row = row0 + i;
+                if (row >= M || k >= K) continue;
+                float v[8];
+                fp4_unpack8(codes[i][h], fp4_scale_value<NV>(byte[i][h]), v);
+                if (NV) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] *= g;
+                }
+                T *a = A + row * lda + k;
+                const uint32_t o[4] = {tc::pack2(v[0], v[1], (T *)nullptr), tc::pack2(v[2], v[3], (T *)nullptr),
+                                       tc::pack2(v[4], v[5], (T *)nullptr), tc::pack2(v[6], v[7], (T *)nullptr)};
+                if (VEC >= 4 && k + 8 <= K) {
+                    if constexpr (VEC == 16) {
+                        *reinterpret_cast<uint4 *>(a) = make_uint4(o[0], o[1], o[2], o[3]);
+                    } else if constexpr (VEC == 8) {
+                        reinterpret_cast<uint2 *>(a)[0] = make_uint2(o[0], o[1]);
+                        reinterpret_cast<uint2 *>(a)[1] = make_uint2(o[2], o[3]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t *>(a)[j] = o[j];
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (k + j < K) tc::store1(a + j, v[j]);
+                }
+            }
     }
+}
+
+// The widest access that every row of A allows.
+int row_vec(const void *A, long long lda) {
+    const uintptr_t x = (uintptr_t)A | (uintptr_t)(lda * 2);
+    return (x & 15) == 0 ? 16 : (x & 7) == 0 ? 8 : (x & 3) == 0 ? 4 : 2;
+}
+dim3 grid_of(long long rows, int K) {
+    const long long pieces = ((long long)K + 511) / 512;
+    return dim3((unsigned)((rows + WARPS * ROWS - 1) / (WARPS * ROWS)), (unsigned)(pieces < 65535 ? pieces : 65535));
 }
 
 template <typename T, bool NV>
 cudaError_t quantize(const void *A, long long lda, const float *g, void *Q, void *S, int M, int K, cudaStream_t s) {
-    const int segs = (int)(((long long)K + 511) / 512);
-    const long long units = fp4_row_tiles(M) * 128 * segs;
-    const long long blocks = (units + WARPS - 1) / WARPS;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(WARPS * 32), 0, s, attr);
-    const T *a = static_cast<const T *>(A);
-    uint8_t *q = static_cast<uint8_t *>(Q), *sc = static_cast<uint8_t *>(S);
-    if (((uintptr_t)A & 15u) == 0 && lda % 8 == 0)
-        return launch_counted(&cfg, fp4_quantize_kernel<T, NV, true>, a, lda, g, q, sc, M, K, segs, units);
-    return launch_counted(&cfg, fp4_quantize_kernel<T, NV, false>, a, lda, g, q, sc, M, K, segs, units);
+    const cudaLaunchConfig_t cfg = pdl_config(grid_of(fp4_row_tiles(M) * 128, K), dim3(WARPS * 32), 0, s, attr);
+    auto go = [&](auto kern) {
+        return launch_counted(&cfg, kern, static_cast<const T *>(A), lda, g, static_cast<uint8_t *>(Q),
+                              static_cast<uint8_t *>(S), M, K);
+    };
+    switch (row_vec(A, lda)) {
+    case 16: return go(fp4_quantize_kernel<T, NV, 16>);
+    case 8: return go(fp4_quantize_kernel<T, NV, 8>);
+    case 4: return go(fp4_quantize_kernel<T, NV, 4>);
+    }
+    return go(fp4_quantize_kernel<T, NV, 2>);
 }
 
 template <typename T, bool NV>
 cudaError_t dequantize(const void *Q, const void *S, const float *g, void *A, long long lda, int M, int K,
                        cudaStream_t s) {
-    const int segs = (int)(((long long)K + 255) / 256);
-    const long long units = (long long)M * segs;
-    const long long blocks = (units + WARPS - 1) / WARPS;
-    if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(WARPS * 32), 0, s, attr);
-    const uint8_t *q = static_cast<const uint8_t *>(Q), *sc = static_cast<const uint8_t *>(S);
-    T *a = static_cast<T *>(A);
-    if (((uintptr_t)A & 15u) == 0 && lda % 8 == 0)
-        return launch_counted(&cfg, fp4_dequantize_kernel<T, NV, true>, q, sc, g, a, lda, M, K, segs, units);
-    return launch_counted(&cfg, fp4_dequantize_kernel<T, NV, false>, q, sc, g, a, lda, M, K, segs, units);
+    const cudaLaunchConfig_t cfg = pdl_config(grid_of(M, K), dim3(WARPS * 32), 0, s, attr);
+    auto go = [&](auto kern) {
+        return launch_counted(&cfg, kern, static_cast<const uint8_t *>(Q), static_cast<const uint8_t *>(S), g,
+                              static_cast<T *>(A), lda, M, K);
+    };
+    switch (row_vec(A, lda)) {
+    case 16: return go(fp4_dequantize_kernel<T, NV, 16>);
+    case 8: return go(fp4_dequantize_kernel<T, NV, 8>);
+    case 4: return go(fp4_dequantize_kernel<T, NV, 4>);
+    }
+    return go(fp4_dequantize_kernel<T, NV, 2>);
 }
 
 }  // namespace

@@ -35,12 +35,37 @@ __device__ __forceinline__ long long fp4_scale_at(int row, int a, int atoms) {
     return ((long long)(row >> 7) * atoms + a) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 }
 
+// A quotient rounded to nearest as IEEE division rounds it, from the correctly
+// rounded reciprocal y of the divisor: with q = a y the remainder a - q b is exact
+// in one FMA, and q + remainder * y is the correctly rounded quotient (Markstein,
+// IBM J. Res. Dev. 34, 1990).  Three operations where a division takes about ten;
+// valid away from the ends of FP32's range.
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+    const float q = a * y;
+    return fmaf(fmaf(-q, b, a), y, q);
+}
+
+// The tensor's scale and what blocks need of it.
+struct Fp4Tensor {
+    float g, g6, y6;  // g, 6 g, 1 / (6 g)
+    bool mid;         // 6 g far from the ends of FP32's range: quotients by quotient()
+};
+template <bool NV>
+__device__ __forceinline__ Fp4Tensor fp4_tensor(const float *tensor_scale) {
+    Fp4Tensor t;
+    t.g = NV && tensor_scale ? *tensor_scale : 1.0f;
+    t.g6 = 6.0f * t.g;
+    t.y6 = __frcp_rn(t.g6);
+    t.mid = t.g6 >= 0x1p-60f && t.g6 <= 0x1p60f;
+    return t;
+}
+
 // A block's scale byte, and what its codes are formed with.
 struct Fp4Scale {
     uint32_t byte;
     float step;  // NV: the step.  0 (both): codes of 0
     float inv;   // 1 / step: MX a power of two, exact; NV correctly rounded
-    bool near;   // NV: a / step may be formed with inv (fp4_codes16)
+    bool near;   // NV: a / step by quotient()
 };
 // From the bits of the block's largest magnitude (|a| as FP32 bits: their order
 // is the values', infinities and NaN on top).
@@ -48,18 +73,20 @@ struct Fp4Scale {
 //       largest magnitude lies in [4, 8) steps; the exponent field less 2.
 //   NV: s = E4M3(amax / (6 g)), step s g.
 // A NaN or an infinity makes the scale NaN and the codes 0.
+// (quotient() here: an amax below 2^-80, where the remainder could underflow, is
+// under 2^-20 steps of s and rounds to 0 either way; of the codes, a value below
+// 2^-4 steps likewise; a block far into saturation divides.)
 template <bool NV>
-__device__ __forceinline__ Fp4Scale fp4_block_scale(uint32_t amax_bits, float g6, float g) {
+__device__ __forceinline__ Fp4Scale fp4_block_scale(uint32_t amax_bits, const Fp4Tensor &t) {
     const bool bad = amax_bits >= 0x7F800000u;
     Fp4Scale r;
     if constexpr (NV) {
-        const float amax = __uint_as_float(amax_bits);
-        r.byte = __nv_cvt_float_to_fp8(amax / g6, __NV_SATFINITE, __NV_E4M3);
-        r.step = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)r.byte, __NV_E4M3))) * g;
+        const float amax = bad ? 0.0f : __uint_as_float(amax_bits);
+        const float v = t.mid && amax <= 0x1p60f ? quotient(amax, t.g6, t.y6) : amax / t.g6;
+        r.byte = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+        r.step = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)r.byte, __NV_E4M3))) * t.g;
         r.inv = __frcp_rn(r.step);
-        // the step and its reciprocal far from the ends of FP32's range, and the
-        // block not far into saturation
-        r.near = r.step >= 0x1p-60f && r.step <= 0x1p60f && amax <= 1024.0f * r.step;
+        r.near = t.mid && amax <= 1024.0f * r.step;
         if (bad) {
             r.byte = 0x7Fu;
             r.step = 0.0f;
@@ -75,10 +102,37 @@ __device__ __forceinline__ Fp4Scale fp4_block_scale(uint32_t amax_bits, float g6
     return r;
 }
 
-// Two values in steps, as codes (the first in the low half): nearest, ties to
-// the even code, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
-    return (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(lo, hi), __NV_E2M1, cudaRoundNearest);
+// Eight values in steps as codes, the first in the lowest four bits: nearest,
+// ties to the even code, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1x8(const float2 &a, const float2 &b, const float2 &c, const float2 &d) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+    return r;
+}
+
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(const float2 &a, const float2 &b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(const float2 &a, const float2 &b, const float2 &c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
 // Values of eight packed codes times a factor.
@@ -113,40 +167,55 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 
-// Codes of the 16 values in v (eight packed pairs) of one block or half block.
-// NV's a / step, rounded to nearest as IEEE division: with y the correctly
-// rounded reciprocal of the step and q = a y, the remainder a - q step is exact
-// in one FMA, and q + remainder * y is the correctly rounded quotient (Markstein,
-// IBM J. Res. Dev. 34, 1990); a quotient so small that the remainder underflows
-// has code 0 either way.  Steps at the ends of the range divide.
-template <typename T, bool NV>
-__device__ __forceinline__ uint2 fp4_codes16(const uint32_t (&v)[8], const Fp4Scale &s) {
-    uint32_t w[2] = {0u, 0u};
-    if (!(s.step > 0.0f)) return make_uint2(0u, 0u);
-    if (NV && !s.near) {
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            uint32_t p = v[0];
+// 16 consecutive values at a (eight packed pairs), of which `left` are in the
+// row; loads of VEC bytes, the alignment of the rows.
+template <int VEC>
+__device__ __forceinline__ void fp4_load16(const void *a, int left, uint32_t (&v)[8]) {
+    if (left >= 16 && VEC >= 4) {
+        if constexpr (VEC == 16) {
+            const uint4 u0 = __ldg(static_cast<const uint4 *>(a)), u1 = __ldg(static_cast<const uint4 *>(a) + 1);
+            v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
+            v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
+        } else if constexpr (VEC == 8) {
 #pragma unroll
-            for (int j = 1; j < 8; ++j) p = i == j ? v[j] : p;
-            const float2 x = unpack2<T>(p);
-            const uint32_t c = e2m1x2(x.x / s.step, x.y / s.step) << (8 * (i & 3));
-            if (i < 4) w[0] |= c;
-            else w[1] |= c;
+            for (int i = 0; i < 4; ++i) {
+                const uint2 u = __ldg(static_cast<const uint2 *>(a) + i);
+                v[2 * i] = u.x;
+                v[2 * i + 1] = u.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __ldg(static_cast<const uint32_t *>(a) + i);
         }
-        return make_uint2(w[0], w[1]);
+        return;
     }
+    const unsigned short *h = static_cast<const unsigned short *>(a);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 x = unpack2<T>(v[i]);
-        float a = x.x * s.inv, b = x.y * s.inv;
-        if constexpr (NV) {
-            a = fmaf(fmaf(-a, s.step, x.x), s.inv, a);
-            b = fmaf(fmaf(-b, s.step, x.y), s.inv, b);
-        }
-        w[i >> 2] |= e2m1x2(a, b) << (8 * (i & 3));
+        v[i] = 2 * i < left ? (uint32_t)__ldg(h + 2 * i) : 0u;
+        if (2 * i + 1 < left) v[i] |= (uint32_t)__ldg(h + 2 * i + 1) << 16;
     }
-    return make_uint2(w[0], w[1]);
+}
+
+// Codes of the 16 values in v (eight packed pairs) of one block or half block.
+template <typename T, bool NV>
+__device__ __forceinline__ uint2 fp4_codes16(const uint32_t (&v)[8], const Fp4Scale &s) {
+    if (!(s.step > 0.0f)) return make_uint2(0u, 0u);
+    float2 x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = unpack2<T>(v[i]);
+    if (NV && !s.near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = make_float2(x[i].x / s.step, x[i].y / s.step);
+    } else {
+        const float2 y = make_float2(s.inv, s.inv), b = make_float2(-s.step, -s.step);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 q = mul2(x[i], y);
+            x[i] = NV ? fma2(fma2(q, b, x[i]), y, q) : q;  // quotient(), two at a time
+        }
+    }
+    return make_uint2(e2m1x8(x[0], x[1], x[2], x[3]), e2m1x8(x[4], x[5], x[6], x[7]));
 }
 #endif
 

@@ -236,20 +236,10 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             const T *X = static_cast<const T *>(args.X);
             auto load = [&](int kb, int r, uint32_t (&v)[8]) {
                 const int k = kb * KB + u * 16;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0u;
-                if (r >= M || k >= K) return;
+                const int left = r < M && k < K ? K - k : 0;
                 const T *x = X + (long long)r * args.ldx + k;
-                if (args.x_vec && k + 16 <= K) {
-                    const uint4 a = __ldg(reinterpret_cast<const uint4 *>(x)), b = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
-                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-                } else {
-                    const unsigned short *h = reinterpret_cast<const unsigned short *>(x);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (k + i < K) v[i >> 1] |= (uint32_t)__ldg(h + i) << (16 * (i & 1));
-                }
+                if (args.x_vec) fp4_load16<16>(x, left, v);
+                else fp4_load16<2>(x, left, v);
             };
             int slot = warp - 2;
             uint32_t phase = 0;
@@ -259,8 +249,7 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             uint32_t next[UNITS][8];
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) load(kb0 + warp - 2, half + 2 * i, next[i]);
-            const float g = NV && args.ga ? *args.ga : 1.0f;
-            const float g6 = 6.0f * g;
+            const Fp4Tensor ts = fp4_tensor<NV>(args.ga);
             for (int kb = kb0 + warp - 2; kb < kb1; kb += 4) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[slot], phase ^ 1u, abort_flag, true))) {
                     ok = false;
@@ -285,7 +274,7 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                         for (int j = 0; j < 8; ++j) m = __vmaxu2(m, abs2(v[i][j]));
                         m = max(m & 0xFFFFu, m >> 16);
                         if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                        const Fp4Scale sc = fp4_block_scale<NV>(bits16_to_f32<T>(m), g6, g);
+                        const Fp4Scale sc = fp4_block_scale<NV>(bits16_to_f32<T>(m), ts);
                         const uint2 codes = fp4_codes16<T, NV>(v[i], sc);
                         if (r < M) {
                             *reinterpret_cast<uint2 *>(xs + r * 128 + (((u >> 1) ^ (r & 7)) << 4) + ((u & 1) << 3)) = codes;
