@@ -21,10 +21,10 @@
 // cores wait for the issue (8192^3 NV 312 us, MX 236; so 162 and 164).
 //
 // Warps: 0 loads (TMA; every load of the pair counts on the leader's full[s]), 1
-// issues the MMAs (leader), 2-5 write C.  Accumulators: bn = 256 has two that
-// share 64 columns (tensor memory holds 512: 448 of them, and 64 for the
-// scales); the epilogue reads the shared ones first, then lets the next tile's
-// MMAs start.  bn = 128: two apart.
+// issues the MMAs (leader), 2-9 write C, half of the tile's columns to each four.
+// Accumulators: bn = 256 has two that share 64 columns (tensor memory holds 512:
+// 448 of them, and 64 for the scales); the epilogue reads the shared ones first,
+// then lets the next tile's MMAs start.  bn = 128: two apart.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -39,13 +39,14 @@ namespace {
 
 using namespace tc;
 
-constexpr int THREADS = 192;
+constexpr int THREADS = 320;
 constexpr int STAGES = 5;
 constexpr int KB = 256;                  // k per stage
 constexpr int A_STAGE = 128 * KB / 2;    // 16 KiB per CTA
 constexpr int B_STAGE = 128 * KB / 2;    // 16 KiB per CTA (bn = 128: half of it)
 constexpr int STG_BOX = 32 * 64 * 2;     // one 32-row x 64-column output box
-constexpr int SMEM_STAGING = 4 * 2 * STG_BOX;
+constexpr int EPI_WARPS = 8;
+constexpr int SMEM_STAGING = EPI_WARPS * STG_BOX;
 constexpr uint32_t TMEM_COLS = 512, SF_COL = 448;
 constexpr int GROUP_M = 8;
 
@@ -154,7 +155,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 256);
+            mbar_init(&bars->acc_empty[b], 2 * EPI_WARPS);
         }
         mbar_init(&bars->drain, 1);
         mbar_init(&bars->peer_done, 1);
@@ -288,11 +289,12 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue (both CTAs)
-        const int quarter = warp & 3;
-        uint8_t *my_stg = staging + quarter * 2 * STG_BOX;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint8_t *box = staging + (warp - 2) * STG_BOX;
+        uint8_t *rowp = box + lane * 128;
         const float scale = NV ? (args.ga ? *args.ga : 1.0f) * (args.gb ? *args.gb : 1.0f) : 1.0f;
-        const int groups = bn >> 6;
-        int sb = 0, it = 0;
+        const int groups = bn >> 7;  // of 64 columns, this half's
+        int it = 0;
         bool ok = true;
         for (int t = cluster; t < num_tiles; t += nclusters, ++it) {
             int tm, tn;
@@ -306,9 +308,15 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             __syncwarp();
             const int row0 = tm * 256 + (int)rank * 128 + quarter * 32;
             const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 192);
+            const uint32_t empty = map_to_rank(&bars->acc_empty[buf], 0);
+            // The columns shared with the other accumulator are group 3 of buf 0 and
+            // group 0 of buf 1.  The half that holds them reads them first; the other
+            // has nothing to read before the next tile's MMAs, but has finished the
+            // tile before this one.
+            const bool shares = wide && half == (buf ^ 1);
+            if (wide && !shares && lane == 0) mbar_arrive_cluster(empty);
             for (int i = 0; i < groups; ++i) {
-                // the columns shared with the other accumulator first: this one's last (buf 0) or first (buf 1)
-                const int g = wide && buf == 0 ? (i + 3) & 3 : i;
+                const int g = half * groups + (shares && buf == 0 ? i ^ 1 : i);
                 const int c0 = tn * bn + g * 64;
                 uint32_t r0[32], r1[32];
                 if (c0 < N) {  // warp-uniform
@@ -316,15 +324,14 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     tmem_ld32(t_row + (uint32_t)(g * 64 + 32), r1);
                     tmem_ld_wait();
                 }
-                if (wide ? i == 0 : i == groups - 1) {
+                if (wide ? shares && i == 0 : i == groups - 1) {
                     fence_before();
-                    mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], 0));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(empty);
                 }
                 if (c0 >= N) continue;
-                if (lane == 0 && args.tma_store) tma_stores_read_wait1();  // the store of two boxes ago has read its box
+                if (lane == 0 && args.tma_store) tma_stores_read_wait0();  // the last store has read the box
                 __syncwarp();
-                uint8_t *box = my_stg + sb * STG_BOX;
-                uint8_t *rowp = box + lane * 128;
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const uint32_t *src = c < 4 ? &r0[8 * c] : &r1[8 * (c - 4)];
@@ -355,8 +362,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                                                                        (c & 7) * 2);
                         }
                     }
+                    __syncwarp();
                 }
-                sb ^= 1;
             }
         }
         if (lane == 0) tma_stores_wait0();
