@@ -14,17 +14,25 @@
 // stored: row % 32 is the lane, row / 32 the column, and the four bytes of a
 // column four blocks.  NV (16 k a block): an atom is one MMA's K.  MX (32 k): an
 // atom serves two MMAs, which read bytes 0-1 and 2-3 (the descriptor's scale id).
-// cp and mma of one thread execute in order, so the scales need no second copy.
-// The issuing warp stays converged and elects a lane for the tcgen05 instructions
-// only: with a loop run by one lane alone, the descriptors are moved to uniform
-// registers anew for every instruction, 23-25 ns a copy of an atom, and the tensor
-// cores wait for the issue (8192^3 NV 312 us, MX 236; so 162 and 164).
+// A tile of B that starts 64 rows into a 128-row tile of scales reads them from
+// the third column on (tile widths are multiples of 64, because an MMA's scales
+// must start on an even column).  cp and mma of one thread execute in order, so
+// the scales need no second copy.
+//
+// Tile widths, by tensor memory (512 columns, 64 of them scales): 192 leaves two
+// whole accumulators, so that a tile is written while the next is computed; 256
+// two that share 64 columns, which the epilogue reads first before it lets the
+// next tile's MMAs start (1.2 us a tile in which the tensor cores wait); 128 for
+// few tiles.  launch_pair says which runs when.
+//
+// The loading and issuing warps stay converged and elect a lane for the TMA and
+// tcgen05 instructions only: with loops run by one lane alone, operands are moved
+// to uniform registers anew for every instruction, 23-25 ns a copy of an atom, and
+// the tensor cores wait for the issue (8192^3 in 256-wide tiles, NV 312 us, MX
+// 236; so 162 and 164).
 //
 // Warps: 0 loads (TMA; every load of the pair counts on the leader's full[s]), 1
 // issues the MMAs (leader), 2-9 write C, half of the tile's columns to each four.
-// Accumulators: bn = 256 has two that share 64 columns (tensor memory holds 512:
-// 448 of them, and 64 for the scales); the epilogue reads the shared ones first,
-// then lets the next tile's MMAs start.  bn = 128: two apart.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,24 +48,33 @@ namespace {
 using namespace tc;
 
 constexpr int THREADS = 320;
-constexpr int STAGES = 5;
 constexpr int KB = 256;                  // k per stage
 constexpr int A_STAGE = 128 * KB / 2;    // 16 KiB per CTA
-constexpr int B_STAGE = 128 * KB / 2;    // 16 KiB per CTA (bn = 128: half of it)
-constexpr int STG_BOX = 32 * 64 * 2;     // one 32-row x 64-column output box
+constexpr int STG_BOX = 32 * 32 * 2;     // one 32-row x 32-column output box
 constexpr int EPI_WARPS = 8;
 constexpr int SMEM_STAGING = EPI_WARPS * STG_BOX;
 constexpr uint32_t TMEM_COLS = 512, SF_COL = 448;
 constexpr int GROUP_M = 8;
 
 __host__ __device__ constexpr int sf_stage(bool nv) { return nv ? 2048 : 1024; }  // of 128 rows
-__host__ __device__ constexpr int stage_bytes(bool nv) { return A_STAGE + B_STAGE + 3 * sf_stage(nv); }
-__host__ __device__ constexpr int smem_bytes(bool nv) { return 1024 + STAGES * stage_bytes(nv) + SMEM_STAGING + 256; }
+// A's codes, B's codes, the scales of A's 128 rows and of the one or two 128-row
+// tiles that B's tile meets.
+__host__ __device__ constexpr int stage_bytes(bool nv, int bn) {
+    return A_STAGE + bn / 2 * (KB / 2) + (bn == 128 ? 2 : 3) * sf_stage(nv);
+}
+constexpr int MAX_STAGES = 6;
+__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 5 : 6; }
+__host__ __device__ constexpr int ring_bytes(bool nv) {
+    return stages_of(192) * stage_bytes(nv, 192) > stages_of(256) * stage_bytes(nv, 256)
+               ? stages_of(192) * stage_bytes(nv, 192) : stages_of(256) * stage_bytes(nv, 256);
+}
+__host__ __device__ constexpr int smem_bytes(bool nv) { return 1024 + ring_bytes(nv) + SMEM_STAGING + 256; }
 static_assert(smem_bytes(true) <= 232448, "shared memory budget");
+static_assert(ring_bytes(true) % 1024 == 0 && ring_bytes(false) % 1024 == 0, "staging boxes on 1024 bytes");
 
 struct Bars {
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
+    uint64_t full[MAX_STAGES];
+    uint64_t empty[MAX_STAGES];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint64_t drain;
@@ -73,7 +90,7 @@ struct Args {
     long long ldc;
     const float *ga, *gb;
     int M, N, K;
-    int bn;         // 128 or 256
+    int bn;         // 128, 192 or 256
     int tma_store;  // C's rows suit TMA stores
     int *status;
 };
@@ -127,15 +144,18 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    constexpr int SF = sf_stage(NV), SF_STAGE = 3 * SF;
+    constexpr int SF = sf_stage(NV);
+    const int M = args.M, N = args.N, bn = args.bn;
+    const int STAGES = stages_of(bn), B_STAGE = (bn >> 1) * (KB / 2);
+    const int sf_tiles_b = bn == 128 ? 1 : 2;  // 128-row tiles of scales that a tile of B meets
+    const int SF_STAGE = (1 + sf_tiles_b) * SF;
     uint8_t *a_tiles = smem;
     uint8_t *b_tiles = a_tiles + STAGES * A_STAGE;
-    uint8_t *sf_tiles = b_tiles + STAGES * B_STAGE;  // per stage: A's 128 rows, then B's 128 or 256
-    uint8_t *staging = sf_tiles + STAGES * SF_STAGE;
+    uint8_t *sf_tiles = b_tiles + STAGES * B_STAGE;  // per stage: A's 128 rows, then B's row tiles
+    uint8_t *staging = smem + ring_bytes(NV);
     Bars *bars = reinterpret_cast<Bars *>(staging + SMEM_STAGING);
     volatile int *abort_flag = &bars->abort;
 
-    const int M = args.M, N = args.N, bn = args.bn;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: uniform
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -144,9 +164,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int num_tiles = tiles_m * tiles_n;
     const int num_kb = (args.K + KB - 1) / KB;
     const bool wide = bn == 256;
-    const int halves = wide ? 2 : 1;  // of B's scales, 128 rows each
+    constexpr uint32_t acc_off = 192;  // of the second accumulator
     // both CTAs' loads of a stage, all counted on the leader's barrier
-    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (bn >> 1) * (KB / 2) + (1 + halves) * SF);
+    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + B_STAGE + SF_STAGE);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -175,8 +195,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     pdl_launch_dependents();
     pdl_wait();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------------ producer (both CTAs)
+        const bool issuer = elect_one();
         int stage = 0;
         uint32_t phase = 0;
         long long issued = 0;
@@ -185,20 +206,23 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             int tm, tn;
             tile_coords(t, tiles_m, tiles_n, tm, tn);
             const int row0 = tm * 256 + (int)rank * 128, col0 = tn * bn + (int)rank * (bn >> 1);
+            const int sf_b = tn * bn / 128;
             for (int kb = 0; kb < num_kb; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
                 const uint32_t full = map_to_rank(&bars->full[stage], 0);
-                if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
                 uint8_t *sf = sf_tiles + stage * SF_STAGE;
-                tma_load_3d_pair(a_tiles + stage * A_STAGE, &tmA, full, kb * (KB / 2), row0, 0);
-                tma_load_3d_pair(b_tiles + stage * B_STAGE, &tmB, full, kb * (KB / 2), col0, 0);
-                tma_load_3d_pair(sf, &tmSa, full, 0, kb * (SF / 1024), row0 / 128);
-                tma_load_3d_pair(sf + SF, &tmSb, full, 0, kb * (SF / 1024), tn * halves);
+                if (issuer) {
+                    if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
+                    tma_load_3d_pair(a_tiles + stage * A_STAGE, &tmA, full, kb * (KB / 2), row0, 0);
+                    tma_load_3d_pair(b_tiles + stage * B_STAGE, &tmB, full, kb * (KB / 2), col0, 0);
+                    tma_load_3d_pair(sf, &tmSa, full, 0, kb * (SF / 1024), row0 / 128);
+                    tma_load_3d_pair(sf + SF, &tmSb, full, 0, kb * (SF / 1024), sf_b);
+                }
                 ++issued;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        if (!ok) {
+        if (!ok && issuer) {
             atomicOr(args.status, ST_PRODUCER);
             raise_abort_pair(abort_flag, rank);
         }
@@ -206,7 +230,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // tells the leader how many stages it loaded, and the leader waits until
         // every stage that either loaded has landed (the half that a side which
         // gave up never loaded is counted as done, or never armed).
-        if (!leader) {
+        if (!issuer) {
+        } else if (!leader) {
             st_cluster_s64(map_to_rank(&bars->peer_issued, 0), issued);
             mbar_arrive_cluster(map_to_rank(&bars->peer_done, 0));  // release: the count is visible first
         } else {
@@ -236,14 +261,17 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const uint64_t sf_desc0 = desc_plain(smem_u32(sf_tiles), 128);
         constexpr int ATOMS = SF / 512;  // of a stage: 4 (NV) or 2 (MX)
         const uint32_t sfa = tmem_base + SF_COL, sfb = sfa + 4 * ATOMS;
+        const uint32_t sfb_atom = 4u * (uint32_t)sf_tiles_b;
         const uint32_t idesc0 = make_idesc<NV>((uint32_t)bn, 0), idesc1 = make_idesc<NV>((uint32_t)bn, 2);
         int stage = 0;
         uint32_t phase = 0;
         int it = 0;
         bool ok = true;
         for (int t = cluster; t < num_tiles; t += nclusters, ++it) {
+            int tm, tn;
+            tile_coords(t, tiles_m, tiles_n, tm, tn);
             const int buf = it & 1;
-            // wide: tile it - 1's shared columns have been read (and so all of it - 2)
+            // 256: tile it - 1's shared columns have been read (and so all of it - 2)
             if (wide) {
                 if (it > 0 && !mbar_wait(&bars->acc_empty[buf ^ 1], (uint32_t)(((it - 1) >> 1) & 1), abort_flag, true))
                     ok = false;
@@ -252,7 +280,8 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
             if (!ok) break;
             fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(buf * 192);
+            const uint32_t d = tmem_base + (uint32_t)buf * acc_off;
+            const uint32_t sfb_first = ((uint32_t)(tn * bn) & 64u) >> 5;  // column of the tile's first row
             for (int kb = 0; kb < num_kb; ++kb) {
                 if (!mbar_wait(&bars->full[stage], phase, abort_flag, true)) { ok = false; break; }
                 fence_after();
@@ -263,14 +292,14 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                     for (int a = 0; a < ATOMS; ++a) {
                         cp_scales_pair(sfa + 4 * a, sd + a * 32);
-                        cp_scales_pair(sfb + 4 * halves * a, sd + (ATOMS + a) * 32);
-                        if (wide) cp_scales_pair(sfb + 4 * halves * a + 4, sd + (2 * ATOMS + a) * 32);
+                        cp_scales_pair(sfb + sfb_atom * a, sd + (ATOMS + a) * 32);
+                        if (bn > 128) cp_scales_pair(sfb + sfb_atom * a + 4, sd + (2 * ATOMS + a) * 32);
                     }
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
                         const int a = NV ? ks : ks >> 1;
                         mma_pair<NV>(d, ad + ks * 2, bd + ks * 2, NV || (ks & 1) == 0 ? idesc0 : idesc1, sfa + 4 * a,
-                                     sfb + 4 * halves * a, (uint32_t)((kb | ks) != 0));
+                                     sfb + sfb_first + sfb_atom * a, (uint32_t)((kb | ks) != 0));
                     }
                     commit_pair_multicast(&bars->empty[stage]);
                 }
@@ -291,9 +320,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // ------------------------------------------------------------ epilogue (both CTAs)
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         uint8_t *box = staging + (warp - 2) * STG_BOX;
-        uint8_t *rowp = box + lane * 128;
+        uint8_t *rowp = box + lane * 64;
         const float scale = NV ? (args.ga ? *args.ga : 1.0f) * (args.gb ? *args.gb : 1.0f) : 1.0f;
-        const int groups = bn >> 7;  // of 64 columns, this half's
+        const int groups = bn >> 6, first = half * groups;  // this half's groups of 32 columns
         int it = 0;
         bool ok = true;
         for (int t = cluster; t < num_tiles; t += nclusters, ++it) {
@@ -307,24 +336,23 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             fence_after();
             __syncwarp();
             const int row0 = tm * 256 + (int)rank * 128 + quarter * 32;
-            const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 192);
+            const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)buf * acc_off;
             const uint32_t empty = map_to_rank(&bars->acc_empty[buf], 0);
-            // The columns shared with the other accumulator are group 3 of buf 0 and
-            // group 0 of buf 1.  The half that holds them reads them first; the other
-            // has nothing to read before the next tile's MMAs, but has finished the
-            // tile before this one.
+            // 256: the columns shared with the other accumulator are groups 6 and 7 of
+            // buf 0, 0 and 1 of buf 1.  The half that holds them reads them first; the
+            // other has nothing to read before the next tile's MMAs, but has finished
+            // the tile before this one.
             const bool shares = wide && half == (buf ^ 1);
             if (wide && !shares && lane == 0) mbar_arrive_cluster(empty);
             for (int i = 0; i < groups; ++i) {
-                const int g = half * groups + (shares && buf == 0 ? i ^ 1 : i);
-                const int c0 = tn * bn + g * 64;
-                uint32_t r0[32], r1[32];
+                const int g = first + (shares && buf == 0 ? i ^ 2 : i);
+                const int c0 = tn * bn + g * 32;
+                uint32_t r[32];
                 if (c0 < N) {  // warp-uniform
-                    tmem_ld32(t_row + (uint32_t)(g * 64), r0);
-                    tmem_ld32(t_row + (uint32_t)(g * 64 + 32), r1);
+                    tmem_ld32(t_row + (uint32_t)(g * 32), r);
                     tmem_ld_wait();
                 }
-                if (wide ? shares && i == 0 : i == groups - 1) {
+                if (wide ? shares && i == 1 : i == groups - 1) {
                     fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(empty);
@@ -333,35 +361,29 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (lane == 0 && args.tma_store) tma_stores_read_wait0();  // the last store has read the box
                 __syncwarp();
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const uint32_t *src = c < 4 ? &r0[8 * c] : &r1[8 * (c - 4)];
+                for (int c = 0; c < 4; ++c) {
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = scale * __uint_as_float(src[e]);
+                    for (int e = 0; e < 8; ++e) v[e] = scale * __uint_as_float(r[8 * c + e]);
                     uint4 w;
                     w.x = pack2(v[0], v[1], (T *)nullptr);
                     w.y = pack2(v[2], v[3], (T *)nullptr);
                     w.z = pack2(v[4], v[5], (T *)nullptr);
                     w.w = pack2(v[6], v[7], (T *)nullptr);
-                    *reinterpret_cast<uint4 *>(rowp + ((c ^ (lane & 7)) << 4)) = w;
+                    *reinterpret_cast<uint4 *>(rowp + ((c ^ ((lane >> 1) & 3)) << 4)) = w;  // the 64-byte swizzle
                 }
                 if (args.tma_store) {
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0 && row0 < M) tma_store_3d(&tmC, box, c0, row0, 0);
                 } else {
-                    // rows that TMA cannot write: 64 columns of a row by the warp, two passes
+                    // rows that TMA cannot write: 32 columns of a row by the warp
                     __syncwarp();
-                    for (int r = 0; r < 32 && row0 + r < M; ++r) {
-                        T *crow = static_cast<T *>(args.C) + (long long)(row0 + r) * args.ldc + c0;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int c = h * 32 + lane;
-                            if (c0 + c < N)
-                                crow[c] = *reinterpret_cast<const T *>(box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) +
-                                                                       (c & 7) * 2);
-                        }
-                    }
+                    for (int q = 0; q < 32 && row0 + q < M; ++q)
+                        if (c0 + lane < N)
+                            static_cast<T *>(args.C)[(long long)(row0 + q) * args.ldc + c0 + lane] =
+                                *reinterpret_cast<const T *>(box + q * 64 + (((lane >> 3) ^ ((q >> 1) & 3)) << 4) +
+                                                             (lane & 7) * 2);
                     __syncwarp();
                 }
             }
@@ -400,13 +422,22 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     const int cmax = clusters_max<T, NV>(dev);
     if (cmax <= 0) return cudaErrorNotSupported;
-    // Narrow tiles only where they all run at once: in several waves a narrow tile
-    // costs 0.8-0.9 of a wide one's time (8192^3 in narrow tiles 418-564 us, in
-    // wide ones 236-312).
-    const long long tiles_m = (p.M + 255LL) / 256, n256 = tiles_m * ((p.N + 255LL) / 256),
-                    n128 = tiles_m * ((p.N + 127LL) / 128);
-    const int bn = n128 <= cmax ? 128 : 256;
-    const long long tiles = bn == 256 ? n256 : n128;
+    // The tile's width: the least waves x time of a tile.  A tile takes the longer
+    // of its stages (measured 0.25 us each at 192, 0.31 at 256 and 0.22 at 128, with
+    // the 1 us in which 256's accumulators change hands) and its writing (2.2, 2.5
+    // and 1.7 us).  Measured, NV, at 192 and 256: 8192^3 157 and 159 us, 2048 x 12288
+    // x 4096 38.2 and 42.1, 2048 x 4096 x 4096 18.1 and 16.7, 8192 x 12288 x 512 59.7
+    // and 53.5; 1000 x 1001 x 4100 17.1, 18.7 and 13.2 at 128.
+    const long long tiles_m = (p.M + 255LL) / 256, kbs = (p.K + KB - 1LL) / KB;
+    int bn = 0;
+    long long tiles = 0, best = 0;
+    for (int c : {192, 256, 128}) {
+        const long long t = tiles_m * ((p.N + c - 1LL) / c);
+        const long long ns = c == 192 ? std::max(250 * kbs, 2200LL)
+                                      : c == 256 ? std::max(310 * kbs + 1000, 2500LL) : std::max(220 * kbs, 1700LL);
+        const long long cost = (t + cmax - 1) / cmax * ns;
+        if (bn == 0 || cost < best) { bn = c; tiles = t; best = cost; }
+    }
     if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     const long long rb = fp4_row_bytes(p.K);
     const long long chunks = (long long)fp4_atoms(NV, p.K) / 2;  // of 1024 bytes, a tile of 128 rows
@@ -414,10 +445,10 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
     CUtensorMap ta, tsa, tb, tsb, tc;
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const auto u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
-    if (!make_map3(&ta, p.Qa, u8, rb, p.M, 1, rb, rb * p.M, 128, 128, 1, true) ||
-        !make_map3(&tb, p.Qb, u8, rb, p.N, 1, rb, rb * p.N, 128, bn / 2, 1, true) ||
-        !make_map3(&tsa, p.Sa, u32, 256, chunks, fp4_row_tiles(p.M), 1024, chunks * 1024, 256, SFC, 1, false) ||
-        !make_map3(&tsb, p.Sb, u32, 256, chunks, fp4_row_tiles(p.N), 1024, chunks * 1024, 256, SFC, bn / 128, false))
+    if (!make_map3(&ta, p.Qa, u8, rb, p.M, 1, rb, rb * p.M, 128, 128, 1, 128) ||
+        !make_map3(&tb, p.Qb, u8, rb, p.N, 1, rb, rb * p.N, 128, bn / 2, 1, 128) ||
+        !make_map3(&tsa, p.Sa, u32, 256, chunks, fp4_row_tiles(p.M), 1024, chunks * 1024, 256, SFC, 1, 0) ||
+        !make_map3(&tsb, p.Sb, u32, 256, chunks, fp4_row_tiles(p.N), 1024, chunks * 1024, 256, SFC, bn == 128 ? 1 : 2, 0))
         return cudaErrorInvalidValue;
     Args a = {};
     a.C = p.C;
@@ -433,7 +464,7 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
     a.tma_store = ((uintptr_t)p.C & 15u) == 0 && p.ldc % 8 == 0 && p.N % 8 == 0;
     if (a.tma_store) {
         const auto dt = p.elt == Elt::BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-        if (!make_map3(&tc, p.C, dt, p.N, p.M, 1, p.ldc * 2, p.ldc * 2 * p.M, 64, 32, 1, true)) a.tma_store = 0;
+        if (!make_map3(&tc, p.C, dt, p.N, p.M, 1, p.ldc * 2, p.ldc * 2 * p.M, 32, 32, 1, 64)) a.tma_store = 0;
     }
     if (!a.tma_store) tc = tb;
     cudaLaunchConfig_t cfg = {};

@@ -451,7 +451,7 @@ constexpr CUtensorMapDataType map_type(uint32_t format) {
 bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long long cols, int box_cols, int box_rows,
            int z = 1, long long stride = 0) {
     return make_map3(m, p, map_type(format), cols, rows, z, cols * 2, z > 1 ? stride : rows * cols * 2, box_cols, box_rows,
-                     1, true);
+                     1, 128);
 }
 
 template <typename T, uint32_t FORMAT, int MODE, bool GELU>
@@ -485,8 +485,8 @@ cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s)
         return cudaErrorInvalidValue;
     tsg = tsu = tz;
     const long long row = 4LL * p.N;
-    if (p.G && (!make_map3(&tsg, p.G, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.N, p.M, 1, row, row * p.M, 32, 32, 1, true) ||
-                !make_map3(&tsu, p.U, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.N, p.M, 1, row, row * p.M, 32, 32, 1, true)))
+    if (p.G && (!make_map3(&tsg, p.G, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.N, p.M, 1, row, row * p.M, 32, 32, 1, 128) ||
+                !make_map3(&tsu, p.U, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.N, p.M, 1, row, row * p.M, 32, 32, 1, 128)))
         return cudaErrorInvalidValue;
     Args a = {};
     a.M = p.M;
@@ -553,7 +553,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
         float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + off);
         const long long row = 4LL * p.K;
         if (splits > 1)
-            ok = ok && make_map3(&tp, part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, row, row * p.M, 32, 32, 1, true);
+            ok = ok && make_map3(&tp, part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, row, row * p.M, 32, 32, 1, 128);
         Args a = {};
         a.M = p.M;
         a.N = p.K;

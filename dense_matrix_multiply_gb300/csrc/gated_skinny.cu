@@ -286,9 +286,9 @@ cudaError_t launch(const GatedProblem &p, int num_sms, int *status, cudaStream_t
     const auto dt = FORMAT == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     CUtensorMap tx, tg, tu;
     const long long xr = 2LL * p.K, wr = 2LL * p.N;
-    if (!make_map3(&tx, p.X, dt, p.K, p.M, 1, xr, xr * p.M, 64, nb_of(p.M), 1, true) ||
-        !make_map3(&tg, p.Wg, dt, p.N, p.K, 1, wr, wr * p.K, 64, KB, 1, true) ||
-        !make_map3(&tu, p.Wu, dt, p.N, p.K, 1, wr, wr * p.K, 64, KB, 1, true))
+    if (!make_map3(&tx, p.X, dt, p.K, p.M, 1, xr, xr * p.M, 64, nb_of(p.M), 1, 128) ||
+        !make_map3(&tg, p.Wg, dt, p.N, p.K, 1, wr, wr * p.K, 64, KB, 1, 128) ||
+        !make_map3(&tu, p.Wu, dt, p.N, p.K, 1, wr, wr * p.K, 64, KB, 1, 128))
         return cudaErrorInvalidValue;
     Args a = {};
     a.Z = p.Z;

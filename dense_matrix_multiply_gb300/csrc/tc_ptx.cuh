@@ -274,9 +274,9 @@ inline EncodeTiledFn encode_fn() {
     return fn;
 }
 // 3-D map: extents and box in elements, strides of the two outer dimensions in
-// bytes (multiples of 16), zero fill out of bounds.
+// bytes (multiples of 16), swizzle in bytes (0, 64, 128), zero fill out of bounds.
 inline bool make_map3(CUtensorMap *map, const void *base, CUtensorMapDataType dt, long long d0, long long d1,
-                      long long d2, long long s1, long long s2, int b0, int b1, int b2, bool swizzle128) {
+                      long long d2, long long s1, long long s2, int b0, int b1, int b2, int swizzle) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
@@ -284,7 +284,8 @@ inline bool make_map3(CUtensorMap *map, const void *base, CUtensorMapDataType dt
     const cuuint32_t box[3] = {(cuuint32_t)b0, (cuuint32_t)b1, (cuuint32_t)b2};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                             : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // Largest number of co-resident clusters of `cs` CTAs (0: none), after raising

@@ -179,6 +179,15 @@ def test_linear(M, N, K, fmt):
         check(C, va, vb, dtype, K)
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("M,N,K", [(512, 12288, 2048), (1600, 5000, 1000)])
+def test_product_over_several_waves_of_tiles(M, N, K, fmt):
+    """192-wide tiles (every second one starts inside a 128-row tile of scales) and
+    256-wide ones, several to a cluster, so that both accumulators are used."""
+    C, va, vb = product(fmt, "bf16", M, N, K, 13)
+    check(C, va, vb, "bf16", K)
+
+
 @pytest.mark.parametrize("M,N,K,ldc_pad,c_off", [(300, 264, 512, 8, 0), (300, 264, 512, 1, 0), (300, 264, 512, 0, 1),
                                                  (7, 264, 512, 8, 0), (7, 263, 512, 2, 1), (130, 70, 320, 6, 2)])
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
