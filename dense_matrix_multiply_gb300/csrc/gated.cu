@@ -169,8 +169,10 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     pdl_launch_dependents();
     pdl_wait();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------------------ producer (both CTAs)
+        // The whole warp runs the loop (operands in uniform registers), one lane issues.
+        const bool issuer = elect_one();
         int stage = 0;
         uint32_t phase = 0;
         long long issued = 0;
@@ -181,22 +183,24 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
                 const uint32_t full = map_to_rank(&bars->full[stage], 0);
-                if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
                 uint8_t *a = a_tiles + stage * A_STAGE, *b = b_tiles + stage * B_STAGE;
-                if (MODE == FWD) {
-                    tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
-                    tma_load_3d_pair(b, &tmB, full, col0, kb * BK, 0);
-                    tma_load_3d_pair(b + BOX64, &tmB2, full, col0, kb * BK, 0);
-                } else {
-                    const int z = kb >= args.kb_half ? 1 : 0, k0 = (kb - z * args.kb_half) * BK;
-                    tma_load_3d_pair(a, &tmA, full, k0, row0, z);
-                    tma_load_3d_pair(b, z ? &tmB2 : &tmB, full, k0, col0, 0);
+                if (issuer) {
+                    if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
+                    if (MODE == FWD) {
+                        tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
+                        tma_load_3d_pair(b, &tmB, full, col0, kb * BK, 0);
+                        tma_load_3d_pair(b + BOX64, &tmB2, full, col0, kb * BK, 0);
+                    } else {
+                        const int z = kb >= args.kb_half ? 1 : 0, k0 = (kb - z * args.kb_half) * BK;
+                        tma_load_3d_pair(a, &tmA, full, k0, row0, z);
+                        tma_load_3d_pair(b, z ? &tmB2 : &tmB, full, k0, col0, 0);
+                    }
                 }
                 ++issued;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
         }
-        if (!ok) {
+        if (!ok && issuer) {
             atomicOr(args.status, ST_PRODUCER);
             raise_abort_pair(abort_flag, rank);
         }
@@ -204,7 +208,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         // tells the leader how many stages it loaded, and the leader waits until
         // every stage that either loaded has landed (the half that a side which
         // gave up never loaded is counted as done, or never armed).
-        if (!leader) {
+        if (!issuer) {
+        } else if (!leader) {
             st_cluster_s64(map_to_rank(&bars->peer_issued, 0), issued);
             mbar_arrive_cluster(map_to_rank(&bars->peer_done, 0));  // release: the count is visible first
         } else {
@@ -386,34 +391,40 @@ __device__ __forceinline__ float2 unpack(uint32_t v, const __nv_bfloat16 *) {
 }
 __device__ __forceinline__ float2 unpack(uint32_t v, const __half *) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); }
 
-// dG and dU from G, U and dZ, eight elements (N % 8 == 0) to a thread: 10 bytes
-// read and 4 written an element.
+// dG and dU from G, U and dZ, four times four elements to a thread (every load and
+// store a full line across the warp): 10 bytes read and 4 written an element.
+constexpr int GRAD_UNITS = 4;
 template <typename T, bool GELU>
 __global__ void __launch_bounds__(256)
-gated_grad_kernel(const float4 *__restrict__ G, const float4 *__restrict__ U, const uint4 *__restrict__ dZ,
-                  uint4 *__restrict__ dG, uint4 *__restrict__ dU, long long n8)
+gated_grad_kernel(const float4 *__restrict__ G, const float4 *__restrict__ U, const uint2 *__restrict__ dZ,
+                  uint2 *__restrict__ dG, uint2 *__restrict__ dU, long long n4)
 {
     pdl_wait();
-    const long long stride = (long long)gridDim.x * blockDim.x;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += stride) {
-        const float4 g0 = __ldcs(G + 2 * i), g1 = __ldcs(G + 2 * i + 1);
-        const float4 u0 = __ldcs(U + 2 * i), u1 = __ldcs(U + 2 * i + 1);
-        const uint4 z = __ldcs(dZ + i);
-        const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
-        const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-        const uint32_t zz[4] = {z.x, z.y, z.z, z.w};
-        uint32_t og[4], ou[4];
+    const long long i0 = (long long)blockIdx.x * (256 * GRAD_UNITS) + threadIdx.x;
+    float4 g[GRAD_UNITS], u[GRAD_UNITS];
+    uint2 z[GRAD_UNITS];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 d = unpack(zz[j], (const T *)nullptr);
-            float a0, da0, a1, da1;
-            gate_act_grad<GELU>(g[2 * j], a0, da0);
-            gate_act_grad<GELU>(g[2 * j + 1], a1, da1);
-            ou[j] = pack2(d.x * a0, d.y * a1, (T *)nullptr);
-            og[j] = pack2(d.x * u[2 * j] * da0, d.y * u[2 * j + 1] * da1, (T *)nullptr);
+    for (int j = 0; j < GRAD_UNITS; ++j) {
+        const long long i = i0 + j * 256;
+        if (i < n4) {
+            g[j] = __ldcs(G + i);
+            u[j] = __ldcs(U + i);
+            z[j] = __ldcs(dZ + i);
         }
-        dG[i] = make_uint4(og[0], og[1], og[2], og[3]);
-        dU[i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+    }
+#pragma unroll
+    for (int j = 0; j < GRAD_UNITS; ++j) {
+        const long long i = i0 + j * 256;
+        if (i >= n4) break;
+        const float2 d0 = unpack(z[j].x, (const T *)nullptr), d1 = unpack(z[j].y, (const T *)nullptr);
+        float a[4], da[4];
+        gate_act_grad<GELU>(g[j].x, a[0], da[0]);
+        gate_act_grad<GELU>(g[j].y, a[1], da[1]);
+        gate_act_grad<GELU>(g[j].z, a[2], da[2]);
+        gate_act_grad<GELU>(g[j].w, a[3], da[3]);
+        dU[i] = make_uint2(pack2(d0.x * a[0], d0.y * a[1], (T *)nullptr), pack2(d1.x * a[2], d1.y * a[3], (T *)nullptr));
+        dG[i] = make_uint2(pack2(d0.x * u[j].x * da[0], d0.y * u[j].y * da[1], (T *)nullptr),
+                           pack2(d1.x * u[j].z * da[2], d1.y * u[j].w * da[3], (T *)nullptr));
     }
 }
 
@@ -535,13 +546,14 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     T *d0 = static_cast<T *>(ws), *d1 = d0 + mn;
     T *dG = g_first ? d0 : d1, *dU = g_first ? d1 : d0;
     {
-        const long long n8 = mn / 8;
-        const unsigned grid = (unsigned)std::min<long long>((n8 + 255) / 256, (long long)num_sms * 8);
+        const long long n4 = mn / 4, blocks = (n4 + 256 * GRAD_UNITS - 1) / (256 * GRAD_UNITS);
         cudaLaunchAttribute attr[1];
-        const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(256), 0, s, attr);
-        e = launch_counted(&cfg, gated_grad_kernel<T, GELU>, reinterpret_cast<const float4 *>(p.G),
-                           reinterpret_cast<const float4 *>(p.U), static_cast<const uint4 *>(p.dZ),
-                           reinterpret_cast<uint4 *>(dG), reinterpret_cast<uint4 *>(dU), n8);
+        const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(256), 0, s, attr);
+        e = blocks > 0x7FFFFFFFLL
+                ? cudaErrorInvalidValue
+                : launch_counted(&cfg, gated_grad_kernel<T, GELU>, reinterpret_cast<const float4 *>(p.G),
+                                 reinterpret_cast<const float4 *>(p.U), static_cast<const uint2 *>(p.dZ),
+                                 reinterpret_cast<uint2 *>(dG), reinterpret_cast<uint2 *>(dU), n4);
     }
     if (e == cudaSuccess && p.dX) {
         CUtensorMap ta, tb, tb2, tc, tp;
