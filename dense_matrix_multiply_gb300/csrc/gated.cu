@@ -14,12 +14,15 @@
 // Backward: dG and dU (16 bits, the operands of the products to come) from G, U
 // and dZ in one pass over memory; dX as one product over the joined reduction
 // index of dG Wg^T and dU Wu^T (2N long), 256 x bn tiles on the same pair
-// pipeline, FP32 sums of both in one accumulator; dWg and dWu as one batch of two
-// on the general kernel (umma_gemm.cu).  With few tiles the joined index is split
-// over the idle clusters, whose FP32 partials a second kernel adds in order.
+// pipeline, FP32 sums of both in one accumulator; dWg and dWu in one launch over
+// the tiles of both, 256 x 256, X and the gradients as they are stored (both
+// operands MN-major).  With few tiles dX's joined index is split over the idle
+// clusters, whose FP32 partials a second kernel adds in order.
 //
-// Warps: 0 loads (TMA), 1 issues the MMAs (leader), 2-5 write out.  Two
-// accumulators, so that a tile is written while the next one is computed.
+// Warps: 0 loads (TMA), 1 issues the MMAs (leader) -- both converged, with one
+// elected lane for the instructions, so that operands stay in uniform registers --
+// and 2-9 write out, half of the tile's columns to each four.  Two accumulators,
+// so that a tile is written while the next one is computed.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,7 +37,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int THREADS = 192;
+constexpr int THREADS = 320, EPI_WARPS = 8;
 constexpr int BK = 64;                 // 16-bit k per stage: 128 bytes a row
 constexpr int A_STAGE = 128 * BK * 2;  // 16 KiB per CTA
 constexpr int B_STAGE = 128 * BK * 2;
@@ -43,12 +46,14 @@ constexpr int STG_BOX = 4096;          // 32 rows x 128 bytes of output
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_M = 8;
 
-// Forward: four staging boxes per epilogue warp (Z, G and U), five stages; dX: two and six.
-enum Mode { FWD = 0, DX = 1 };
-__host__ __device__ constexpr int n_boxes(int mode) { return mode == FWD ? 4 : 2; }
+// Forward: two staging boxes per epilogue warp (Z, G and U), five stages; the
+// others one and six.
+enum Mode { FWD = 0, DX = 1, DW = 2 };
+__host__ __device__ constexpr int n_boxes(int mode) { return mode == FWD ? 2 : 1; }
 __host__ __device__ constexpr int n_stages(int mode) { return mode == FWD ? 5 : 6; }
+__host__ __device__ constexpr int staging_bytes(int mode) { return EPI_WARPS * n_boxes(mode) * STG_BOX; }
 __host__ __device__ constexpr int smem_bytes(int mode) {
-    return 1024 + n_stages(mode) * (A_STAGE + B_STAGE) + 4 * n_boxes(mode) * STG_BOX + 256;
+    return 1024 + n_stages(mode) * (A_STAGE + B_STAGE) + staging_bytes(mode) + 256;
 }
 static_assert(smem_bytes(FWD) <= 232448 && smem_bytes(DX) <= 232448, "shared memory budget");
 
@@ -66,11 +71,12 @@ struct Bars {
 static_assert(sizeof(Bars) <= 256, "barrier block");
 
 struct Args {
-    int M, N;     // of the output: Z [M,N], dX [M,N]
+    int M, N;     // of the output: Z, dX or a dW
     int num_kb;   // K blocks of 64 (DX: of both halves together)
     int kb_half;  // DX: blocks of the first half
-    int bn;       // the tile's N extent: FWD 128; DX 128, 192 or 256
+    int bn;       // the tile's N extent: FWD 128; DX 128, 192 or 256; DW 256
     int splits;   // DX: units per tile; > 1: FP32 partials
+    int batch;    // DW: outputs, 1 or 2; else 1
     int save;     // FWD: store G and U
     int *status;
 };
@@ -83,19 +89,21 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t a, uint64_t b,
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// FP32 accumulator, A and B of one 16-bit type (0 f16, 1 bf16), A K-major, M = 256.
-__device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool b_mn) {
-    return (1u << 4) | (format << 7) | (format << 10) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((256u >> 4) << 24);
+// FP32 accumulator, A and B of one 16-bit type (0 f16, 1 bf16), M = 256.
+__device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (format << 7) | (format << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((256u >> 4) << 24);
 }
 
-// Unit u: tile and K-block range.
+// Unit u: output (DW), tile and K-block range.
 struct Unit {
-    int tm, tn, kb0, kb1, split;
+    int tm, tn, kb0, kb1, split, z;
 };
 __device__ __forceinline__ Unit unit_at(int u, int tiles_m, int tiles_n, const Args &a) {
     Unit r;
-    const int t = u / a.splits;
+    int t = u / a.splits;
     r.split = u - t * a.splits;
+    r.z = t / (tiles_m * tiles_n);
+    t -= r.z * tiles_m * tiles_n;
     r.kb0 = (int)((long long)a.num_kb * r.split / a.splits);
     r.kb1 = (int)((long long)a.num_kb * (r.split + 1) / a.splits);
     const int per_group = GROUP_M * tiles_n;
@@ -119,6 +127,7 @@ __device__ __forceinline__ void box_put_f32(uint8_t *box, int lane, const uint32
 // FWD: tmA = X, tmB = Wg, tmB2 = Wu, tmC = Z, tmG, tmU (when saved).
 // DX: tmA = {dG, dU} (third coordinate), tmB = Wg, tmB2 = Wu, tmC = dX, tmG the
 // partials [splits][M][N] (splits > 1).
+// DW: tmA = X, tmB = {dG, dU}, tmC and tmG the outputs of its two matrices.
 template <typename T, uint32_t FORMAT, int MODE, bool GELU>
 __global__ void __launch_bounds__(THREADS, 1)
 gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -131,7 +140,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     uint8_t *a_tiles = smem;
     uint8_t *b_tiles = a_tiles + STAGES * A_STAGE;
     uint8_t *staging = b_tiles + STAGES * B_STAGE;
-    Bars *bars = reinterpret_cast<Bars *>(staging + 4 * BOXES * STG_BOX);
+    Bars *bars = reinterpret_cast<Bars *>(staging + staging_bytes(MODE));
     volatile int *abort_flag = &bars->abort;
 
     const int M = args.M, N = args.N, bn = args.bn;
@@ -140,8 +149,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const bool leader = rank == 0;
     const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
     const int tiles_m = (M + 255) / 256, tiles_n = (N + bn - 1) / bn;
-    const int units = tiles_m * tiles_n * args.splits;
-    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (MODE == FWD ? 2 * BOX64 : (bn >> 1) * 128));
+    const int units = tiles_m * tiles_n * args.splits * args.batch;
+    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (MODE == DX ? (bn >> 1) * 128 : 2 * BOX64));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -150,7 +159,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 256);
+            mbar_init(&bars->acc_empty[b], 2 * EPI_WARPS);
         }
         mbar_init(&bars->drain, 1);
         mbar_init(&bars->peer_done, 1);
@@ -190,6 +199,11 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
                         tma_load_3d_pair(b, &tmB, full, col0, kb * BK, 0);
                         tma_load_3d_pair(b + BOX64, &tmB2, full, col0, kb * BK, 0);
+                    } else if (MODE == DW) {
+                        tma_load_3d_pair(a, &tmA, full, row0, kb * BK, 0);
+                        tma_load_3d_pair(a + BOX64, &tmA, full, row0 + 64, kb * BK, 0);
+                        tma_load_3d_pair(b, &tmB, full, col0, kb * BK, w.z);
+                        tma_load_3d_pair(b + BOX64, &tmB, full, col0 + 64, kb * BK, w.z);
                     } else {
                         const int z = kb >= args.kb_half ? 1 : 0, k0 = (kb - z * args.kb_half) * BK;
                         tma_load_3d_pair(a, &tmA, full, k0, row0, z);
@@ -233,11 +247,13 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         // ------------------------------------------------------------ MMA issuer (leader)
         // The whole warp runs the loop (descriptors in uniform registers), one lane issues.
         const bool issuer = elect_one();
-        constexpr bool b_mn = MODE == FWD;
-        const uint32_t idesc = make_idesc(FORMAT, MODE == FWD ? 256u : (uint32_t)bn, b_mn);
-        const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), 16, 1024);
+        // K-major: a K step of 16 is 32 bytes of a 128-byte row.  MN-major: 16 rows of
+        // 128 bytes, 64-element boxes BOX64 bytes apart.
+        constexpr bool a_mn = MODE == DW, b_mn = MODE != DX;
+        const uint32_t idesc = make_idesc(FORMAT, MODE == DX ? (uint32_t)bn : 256u, a_mn, b_mn);
+        const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), a_mn ? BOX64 : 16, 1024);
         const uint64_t b_desc0 = desc_sw128(smem_u32(b_tiles), b_mn ? BOX64 : 16, 1024);
-        constexpr uint32_t a_step = 32 >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
         int stage = 0;
         uint32_t phase = 0;
         int it = 0;
@@ -274,19 +290,19 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         }
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue (both CTAs)
-        const int quarter = warp & 3;
-        uint8_t *my_stg = staging + quarter * BOXES * STG_BOX;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint8_t *my_stg = staging + (warp - 2) * BOXES * STG_BOX;
         int sb = 0, it = 0;
         bool ok = true;
         // The next staging box, once the store that last read it has done so.
         auto box_begin = [&]() {
             if (lane == 0) {
-                if constexpr (BOXES == 4) asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
-                else tma_stores_read_wait1();
+                if constexpr (BOXES == 2) tma_stores_read_wait1();
+                else tma_stores_read_wait0();
             }
             __syncwarp();
             uint8_t *b = my_stg + sb * STG_BOX;
-            sb = (sb + 1) % BOXES;
+            if (BOXES == 2) sb ^= 1;
             return b;
         };
         auto box_end = [&](const CUtensorMap *map, uint8_t *b, int x, int y, int z) {
@@ -307,10 +323,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
             if constexpr (MODE == FWD) {
                 // accumulator columns 128 g + j: G, 128 g + 64 + j: U of Z's column 64 g + j
-#pragma unroll 1
-                for (int g = 0; g < 2; ++g) {
-                    const int c0 = w.tn * 128 + g * 64;
-                    if (c0 >= N) break;  // warp-uniform
+                const int g = half, c0 = w.tn * 128 + g * 64;
+                if (c0 < N) {  // warp-uniform
                     uint32_t z[32];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -337,15 +351,16 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     box_end(&tmC, b, c0, row0, 0);
                 }
             } else {
+                const int groups = bn >> 6, mid = (groups + 1) >> 1;  // of 64 columns; this half's first or last
 #pragma unroll 1
-                for (int g = 0; g < (bn >> 6); ++g) {
+                for (int g = half ? mid : 0; g < (half ? groups : mid); ++g) {
                     const int c0 = w.tn * bn + g * 64;
                     if (c0 >= N) break;  // warp-uniform
                     uint32_t r0[32], r1[32];
                     tmem_ld32(t_row + (uint32_t)(g * 64), r0);
                     tmem_ld32(t_row + (uint32_t)(g * 64 + 32), r1);
                     tmem_ld_wait();
-                    if (args.splits > 1) {
+                    if (MODE == DX && args.splits > 1) {
                         uint8_t *b = box_begin();
                         box_put_f32(b, lane, r0);
                         box_end(&tmG, b, c0, row0, w.split);
@@ -363,12 +378,13 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         }
                         uint8_t *b = box_begin();
                         box_put_f32(b, lane, z);
-                        box_end(&tmC, b, c0, row0, 0);
+                        box_end(MODE == DW && w.z ? &tmG : &tmC, b, c0, row0, 0);
                     }
                 }
             }
             fence_before();
-            mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], 0));
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], 0));
         }
         if (lane == 0) tma_stores_wait0();
         if (!ok && lane == 0) {
@@ -504,7 +520,7 @@ cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s)
     a.N = p.N;
     a.num_kb = (p.K + BK - 1) / BK;
     a.bn = 128;
-    a.splits = 1;
+    a.splits = a.batch = 1;
     a.save = p.G != nullptr;
     a.status = status;
     return launch_pair<T, FORMAT, FWD, GELU>(tx, tg, tu, tz, tsg, tsu, a, (int)std::min<long long>(tiles, cmax), s);
@@ -540,11 +556,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(&ws, off + parts, s);
     if (e != cudaSuccess) return e;
-    // The gradient whose dW lies lower comes first, so that the two dW are a batch
-    // with a positive stride.
-    const bool g_first = !p.dWg || !p.dWu || (uintptr_t)p.dWg < (uintptr_t)p.dWu;
-    T *d0 = static_cast<T *>(ws), *d1 = d0 + mn;
-    T *dG = g_first ? d0 : d1, *dU = g_first ? d1 : d0;
+    T *dG = static_cast<T *>(ws), *dU = dG + mn;
     {
         const long long n4 = mn / 4, blocks = (n4 + 256 * GRAD_UNITS - 1) / (256 * GRAD_UNITS);
         cudaLaunchAttribute attr[1];
@@ -557,9 +569,9 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     }
     if (e == cudaSuccess && p.dX) {
         CUtensorMap ta, tb, tb2, tc, tp;
-        bool ok = map16(&ta, d0, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) &&
-                  map16(&tb, g_first ? p.Wg : p.Wu, FORMAT, p.K, p.N, BK, bn / 2) &&
-                  map16(&tb2, g_first ? p.Wu : p.Wg, FORMAT, p.K, p.N, BK, bn / 2) &&
+        bool ok = map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) &&
+                  map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) &&
+                  map16(&tb2, p.Wu, FORMAT, p.K, p.N, BK, bn / 2) &&
                   map16(&tc, p.dX, FORMAT, p.M, p.K, 64, 32);
         tp = tc;
         float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + off);
@@ -573,6 +585,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
         a.kb_half = half;
         a.bn = bn;
         a.splits = splits;
+        a.batch = 1;
         a.status = status;
         e = ok ? launch_pair<T, FORMAT, DX, false>(ta, tb, tb2, tc, tp, tp, a,
                                                    (int)std::min<long long>(tiles * splits, cmax), s)
@@ -586,37 +599,25 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
         }
     }
     if (e == cudaSuccess && (p.dWg || p.dWu)) {
-        // dW = X^T {dG, dU}: X stored [M, K] is the transposed operand
-        ProblemEx q = {};
-        q.A = p.X;
-        q.M = p.K;
-        q.N = p.N;
-        q.K = p.M;
-        q.a_t = true;
-        q.lda = p.K;
-        q.ldb = q.ldc = p.N;
-        q.alpha = 1.0f;
-        q.elt = p.elt;
+        const int wmax = clusters_max<T, FORMAT, DW, false>(dev);
         const bool both = p.dWg && p.dWu;
-        bool done = false;
-        if (both) {
-            q.B = d0;
-            q.C = g_first ? p.dWg : p.dWu;
-            q.batch = 2;
-            q.sb = mn;
-            q.sc = (long long)(((uintptr_t)(g_first ? p.dWu : p.dWg) - (uintptr_t)q.C) / 2);
-            e = launch_umma_ex(q, status, s);
-            done = e != cudaErrorNotSupported;  // (outputs too far apart for a tensor map: one at a time)
-        }
-        if (!done) {
-            q.batch = 1;
-            q.sb = q.sc = 0;
-            e = cudaSuccess;
-            for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-                q.B = i ? dU : dG;
-                q.C = i ? p.dWu : p.dWg;
-                if (q.C) e = launch_umma_ex(q, status, s);
-            }
+        const long long wt = (p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1);
+        CUtensorMap ta, tb, tc, tc2;
+        if (wmax <= 0 || wt > 0x7FFFFFFFLL || !map16(&ta, p.X, FORMAT, p.M, p.K, 64, BK) ||
+            !map16(&tb, both || p.dWg ? dG : dU, FORMAT, p.M, p.N, 64, BK, both ? 2 : 1, mn * 2) ||
+            !map16(&tc, p.dWg ? p.dWg : p.dWu, FORMAT, p.K, p.N, 64, 32) ||
+            !map16(&tc2, p.dWu ? p.dWu : p.dWg, FORMAT, p.K, p.N, 64, 32)) {
+            e = cudaErrorInvalidValue;
+        } else {
+            Args a = {};
+            a.M = p.K;
+            a.N = p.N;
+            a.num_kb = (p.M + BK - 1) / BK;
+            a.bn = 256;
+            a.splits = 1;
+            a.batch = both ? 2 : 1;
+            a.status = status;
+            e = launch_pair<T, FORMAT, DW, false>(ta, tb, tb, tc, tc2, tc2, a, (int)std::min<long long>(wt, wmax), s);
         }
     }
     const cudaError_t f = cudaFreeAsync(ws, s);

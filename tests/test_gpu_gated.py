@@ -85,6 +85,19 @@ def test_forward_and_backward(M, N, K, dtype, act):
         close(got[name], want, tol, name)
 
 
+@pytest.mark.parametrize("M,N,K", [(600, 5000, 264), (5000, 64, 2056)])
+def test_several_waves_of_tiles(M, N, K):
+    """More tiles than clusters, forward and dW, then dX: every buffer of the
+    kernels is used again and again."""
+    t, (X, Wg, Wu, dZ) = make(M, N, K, "bf16", 11)
+    got = run("bf16", "silu", t, M, N, K)
+    for name, want, tol in zip("ZGU", ref.forward("silu", X, Wg, Wu), ref.forward_tolerance("silu", X, Wg, Wu, "bf16")):
+        close(got[name], want, tol, name)
+    grads = ref.backward("silu", X, Wg, Wu, dZ)
+    for name, want, tol in zip(("dX", "dWg", "dWu"), grads, ref.backward_tolerance("silu", X, Wg, Wu, dZ, "bf16")):
+        close(got[name], want, tol, name)
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 72, 40), (200, 264, 128)])
 def test_without_saving_gives_the_same_z(M, N, K):
     t, _ = make(M, N, K, "bf16", 5)
