@@ -46,11 +46,11 @@ constexpr int STG_BOX = 4096;          // 32 rows x 128 bytes of output
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_M = 8;
 
-// Forward: two staging boxes per epilogue warp (Z, G and U), five stages; the
-// others one and six.
+// Two staging boxes per epilogue warp and five stages where a tile's output is
+// much against its stages (Z, G and U; dW over few rows), one and six for dX.
 enum Mode { FWD = 0, DX = 1, DW = 2 };
-__host__ __device__ constexpr int n_boxes(int mode) { return mode == FWD ? 2 : 1; }
-__host__ __device__ constexpr int n_stages(int mode) { return mode == FWD ? 5 : 6; }
+__host__ __device__ constexpr int n_boxes(int mode) { return mode == DX ? 1 : 2; }
+__host__ __device__ constexpr int n_stages(int mode) { return mode == DX ? 6 : 5; }
 __host__ __device__ constexpr int staging_bytes(int mode) { return EPI_WARPS * n_boxes(mode) * STG_BOX; }
 __host__ __device__ constexpr int smem_bytes(int mode) {
     return 1024 + n_stages(mode) * (A_STAGE + B_STAGE) + staging_bytes(mode) + 256;
@@ -551,7 +551,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     const long long tiles = tiles_m * ((p.K + bn - 1) / bn);
     if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     // scratch: dG and dU, and dX's partials
-    const size_t grads = (size_t)mn * 4, parts = p.dX && splits > 1 ? (size_t)splits * p.M * p.K * 4 : 0;
+    const size_t grads = (size_t)mn * 4, parts = p.dX && p.M > kGatedSkinnyMaxM && splits > 1 ? (size_t)splits * p.M * p.K * 4 : 0;
     const size_t off = (grads + 255) & ~(size_t)255;
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(&ws, off + parts, s);
@@ -567,7 +567,9 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
                                  reinterpret_cast<const float4 *>(p.U), static_cast<const uint2 *>(p.dZ),
                                  reinterpret_cast<uint2 *>(dG), reinterpret_cast<uint2 *>(dU), n4);
     }
-    if (e == cudaSuccess && p.dX) {
+    if (e == cudaSuccess && p.dX && p.M <= kGatedSkinnyMaxM) {
+        e = launch_gated_skinny_dx(p, dG, num_sms, status, s);
+    } else if (e == cudaSuccess && p.dX) {
         CUtensorMap ta, tb, tb2, tc, tp;
         bool ok = map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) &&
                   map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) &&

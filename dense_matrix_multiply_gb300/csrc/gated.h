@@ -32,6 +32,8 @@ struct GatedBackward {
 cudaError_t launch_gated(const GatedProblem &p, int *status, cudaStream_t s);            // any M
 constexpr int kGatedSkinnyMaxM = 64;
 cudaError_t launch_gated_skinny(const GatedProblem &p, int num_sms, int *status, cudaStream_t s);
+// dX from dG and dU [2][M][N].
+cudaError_t launch_gated_skinny_dx(const GatedBackward &p, const void *dGU, int num_sms, int *status, cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedBackward &p, int num_sms, int *status, cudaStream_t s);
 
 #ifdef __CUDACC__
