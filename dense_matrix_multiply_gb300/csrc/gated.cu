@@ -16,8 +16,13 @@
 // index of dG Wg^T and dU Wu^T (2N long), 256 x bn tiles on the same pair
 // pipeline, FP32 sums of both in one accumulator; dWg and dWu in one launch over
 // the tiles of both, 256 x 256, X and the gradients as they are stored (both
-// operands MN-major).  With few tiles dX's joined index is split over the idle
-// clusters, whose FP32 partials a second kernel adds in order.
+// operands MN-major).
+//
+// A last wave of tiles that would leave at least half of the clusters idle is split
+// along K (plan()): FP32 partials go to scratch and are added, in order, by
+// gated_fix_kernel.  The clusters of one split walk the same K range together, so
+// that operands are still read from memory once (shares cut tile after tile, each
+// cluster at a K of its own, took dX of 1024 x 12288 x 4096 from 145 us to 214).
 //
 // Warps: 0 loads (TMA), 1 issues the MMAs (leader) -- both converged, with one
 // elected lane for the instructions, so that operands stay in uniform registers --
@@ -75,9 +80,10 @@ struct Args {
     int num_kb;   // K blocks of 64 (DX: of both halves together)
     int kb_half;  // DX: blocks of the first half
     int bn;       // the tile's N extent: FWD 128; DX 128, 192 or 256; DW 256
-    int splits;   // DX: units per tile; > 1: FP32 partials
     int batch;    // DW: outputs, 1 or 2; else 1
     int save;     // FWD: store G and U
+    int whole;    // tiles computed whole; the rest are split
+    int splits;   // in so many K ranges, one to a cluster
     int *status;
 };
 
@@ -94,26 +100,42 @@ __device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool
     return (1u << 4) | (format << 7) | (format << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((256u >> 4) << 24);
 }
 
-// Unit u: output (DW), tile and K-block range.
-struct Unit {
-    int tm, tn, kb0, kb1, split, z;
+// A tile of the output: which output (DW), row and column of tiles.
+struct Tile {
+    int z, m, n;
 };
-__device__ __forceinline__ Unit unit_at(int u, int tiles_m, int tiles_n, const Args &a) {
-    Unit r;
-    int t = u / a.splits;
-    r.split = u - t * a.splits;
+__device__ __forceinline__ Tile tile_at(int t, int tiles_m, int tiles_n) {
+    Tile r;
     r.z = t / (tiles_m * tiles_n);
     t -= r.z * tiles_m * tiles_n;
-    r.kb0 = (int)((long long)a.num_kb * r.split / a.splits);
-    r.kb1 = (int)((long long)a.num_kb * (r.split + 1) / a.splits);
     const int per_group = GROUP_M * tiles_n;
     const int group = t / per_group;
     const int first_m = group * GROUP_M;
     const int gsize = min(tiles_m - first_m, GROUP_M);
     const int q = t - group * per_group;
-    r.tm = first_m + q % gsize;
-    r.tn = q / gsize;
+    r.m = first_m + q % gsize;
+    r.n = q / gsize;
     return r;
+}
+// Unit u of cluster c of G: the whole tiles c, c + G, ... first (slab -1), then,
+// for c < (tiles - whole) * splits, K range c / (tiles - whole) of split tile
+// c % (tiles - whole), whose partial is slab c.  Every warp walks the same sequence.
+struct Unit {
+    int t, kb0, kb1, slab;
+};
+__device__ __forceinline__ bool unit_at(int u, int c, int G, int tiles, const Args &a, Unit &r) {
+    const int n = c < a.whole ? (a.whole - 1 - c) / G + 1 : 0, rest = tiles - a.whole;
+    if (u < n) {
+        r = {c + u * G, 0, a.num_kb, -1};
+        return true;
+    }
+    if (u > n || c >= rest * a.splits) return false;
+    const int j = c / rest;
+    r.t = a.whole + c - j * rest;
+    r.kb0 = (int)((long long)a.num_kb * j / a.splits);
+    r.kb1 = (int)((long long)a.num_kb * (j + 1) / a.splits);
+    r.slab = c;
+    return true;
 }
 
 // 32 FP32 columns of this lane's row to a box, 128-byte swizzle.
@@ -125,14 +147,15 @@ __device__ __forceinline__ void box_put_f32(uint8_t *box, int lane, const uint32
 }
 
 // FWD: tmA = X, tmB = Wg, tmB2 = Wu, tmC = Z, tmG, tmU (when saved).
-// DX: tmA = {dG, dU} (third coordinate), tmB = Wg, tmB2 = Wu, tmC = dX, tmG the
-// partials [splits][M][N] (splits > 1).
+// DX: tmA = {dG, dU} (third coordinate), tmB = Wg, tmB2 = Wu, tmC = dX.
 // DW: tmA = X, tmB = {dG, dU}, tmC and tmG the outputs of its two matrices.
+// tmP: the partials, slabs of 256 x 256 accumulators.
 template <typename T, uint32_t FORMAT, int MODE, bool GELU>
 __global__ void __launch_bounds__(THREADS, 1)
 gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmC,
-                  const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU, const Args args)
+                  const __grid_constant__ CUtensorMap tmG, const __grid_constant__ CUtensorMap tmU,
+                  const __grid_constant__ CUtensorMap tmP, const Args args)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -149,7 +172,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const bool leader = rank == 0;
     const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
     const int tiles_m = (M + 255) / 256, tiles_n = (N + bn - 1) / bn;
-    const int units = tiles_m * tiles_n * args.splits * args.batch;
+    const int tiles = tiles_m * tiles_n * args.batch;
     const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (MODE == DX ? (bn >> 1) * 128 : 2 * BOX64));
 
     if (threadIdx.x == 0) {
@@ -186,9 +209,10 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         uint32_t phase = 0;
         long long issued = 0;
         bool ok = true;
-        for (int u = cluster; u < units && ok; u += nclusters) {
-            const Unit w = unit_at(u, tiles_m, tiles_n, args);
-            const int row0 = w.tm * 256 + (int)rank * 128, col0 = w.tn * bn + (int)rank * (bn >> 1);
+        Unit w;
+        for (int u = 0; ok && unit_at(u, cluster, nclusters, tiles, args, w); ++u) {
+            const Tile t = tile_at(w.t, tiles_m, tiles_n);
+            const int row0 = t.m * 256 + (int)rank * 128, col0 = t.n * bn + (int)rank * (bn >> 1);
             for (int kb = w.kb0; kb < w.kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
                 const uint32_t full = map_to_rank(&bars->full[stage], 0);
@@ -202,8 +226,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     } else if (MODE == DW) {
                         tma_load_3d_pair(a, &tmA, full, row0, kb * BK, 0);
                         tma_load_3d_pair(a + BOX64, &tmA, full, row0 + 64, kb * BK, 0);
-                        tma_load_3d_pair(b, &tmB, full, col0, kb * BK, w.z);
-                        tma_load_3d_pair(b + BOX64, &tmB, full, col0 + 64, kb * BK, w.z);
+                        tma_load_3d_pair(b, &tmB, full, col0, kb * BK, t.z);
+                        tma_load_3d_pair(b + BOX64, &tmB, full, col0 + 64, kb * BK, t.z);
                     } else {
                         const int z = kb >= args.kb_half ? 1 : 0, k0 = (kb - z * args.kb_half) * BK;
                         tma_load_3d_pair(a, &tmA, full, k0, row0, z);
@@ -258,8 +282,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         uint32_t phase = 0;
         int it = 0;
         bool ok = true;
-        for (int u = cluster; u < units && ok; u += nclusters, ++it) {
-            const Unit w = unit_at(u, tiles_m, tiles_n, args);
+        Unit w;
+        for (int u = 0; ok && unit_at(u, cluster, nclusters, tiles, args, w); ++u, ++it) {
             const int buf = it & 1;
             if (!mbar_wait(&bars->acc_empty[buf], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, true)) { ok = false; break; }
             fence_after();
@@ -310,8 +334,9 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             __syncwarp();
             if (lane == 0 && y < M) tma_store_3d(map, b, x, y, z);
         };
-        for (int u = cluster; u < units; u += nclusters, ++it) {
-            const Unit w = unit_at(u, tiles_m, tiles_n, args);
+        Unit w;
+        for (int u = 0; unit_at(u, cluster, nclusters, tiles, args, w); ++u, ++it) {
+            const Tile t = tile_at(w.t, tiles_m, tiles_n);
             const int buf = it & 1;
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (uint32_t)((it >> 1) & 1), abort_flag, true))) {
                 ok = false;
@@ -319,11 +344,25 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             }
             fence_after();
             __syncwarp();
-            const int row0 = w.tm * 256 + (int)rank * 128 + quarter * 32;
+            const int row0 = t.m * 256 + (int)rank * 128 + quarter * 32;
             const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
-            if constexpr (MODE == FWD) {
+            if (w.slab >= 0) {
+                // a partial: the accumulators as they are
+                const int chunks = (MODE == FWD ? 256 : bn) / 32, mid = (chunks + 1) >> 1;
+#pragma unroll 1
+                for (int c = half ? mid : 0; c < (half ? chunks : mid); ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(t_row + (uint32_t)(c * 32), r);
+                    tmem_ld_wait();
+                    uint8_t *b = box_begin();
+                    box_put_f32(b, lane, r);
+                    fence_async_shared();
+                    __syncwarp();
+                    if (lane == 0 && row0 < M) tma_store_3d(&tmP, b, c * 32, (int)rank * 128 + quarter * 32, w.slab);
+                }
+            } else if constexpr (MODE == FWD) {
                 // accumulator columns 128 g + j: G, 128 g + 64 + j: U of Z's column 64 g + j
-                const int g = half, c0 = w.tn * 128 + g * 64;
+                const int g = half, c0 = t.n * 128 + g * 64;
                 if (c0 < N) {  // warp-uniform
                     uint32_t z[32];
 #pragma unroll
@@ -354,32 +393,21 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 const int groups = bn >> 6, mid = (groups + 1) >> 1;  // of 64 columns; this half's first or last
 #pragma unroll 1
                 for (int g = half ? mid : 0; g < (half ? groups : mid); ++g) {
-                    const int c0 = w.tn * bn + g * 64;
+                    const int c0 = t.n * bn + g * 64;
                     if (c0 >= N) break;  // warp-uniform
                     uint32_t r0[32], r1[32];
                     tmem_ld32(t_row + (uint32_t)(g * 64), r0);
                     tmem_ld32(t_row + (uint32_t)(g * 64 + 32), r1);
                     tmem_ld_wait();
-                    if (MODE == DX && args.splits > 1) {
-                        uint8_t *b = box_begin();
-                        box_put_f32(b, lane, r0);
-                        box_end(&tmG, b, c0, row0, w.split);
-                        if (c0 + 32 < N) {
-                            b = box_begin();
-                            box_put_f32(b, lane, r1);
-                            box_end(&tmG, b, c0 + 32, row0, w.split);
-                        }
-                    } else {
-                        uint32_t z[32];
+                    uint32_t z[32];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            z[j] = pack2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), (T *)nullptr);
-                            z[16 + j] = pack2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), (T *)nullptr);
-                        }
-                        uint8_t *b = box_begin();
-                        box_put_f32(b, lane, z);
-                        box_end(MODE == DW && w.z ? &tmG : &tmC, b, c0, row0, 0);
+                    for (int j = 0; j < 16; ++j) {
+                        z[j] = pack2(__uint_as_float(r0[2 * j]), __uint_as_float(r0[2 * j + 1]), (T *)nullptr);
+                        z[16 + j] = pack2(__uint_as_float(r1[2 * j]), __uint_as_float(r1[2 * j + 1]), (T *)nullptr);
                     }
+                    uint8_t *b = box_begin();
+                    box_put_f32(b, lane, z);
+                    box_end(MODE == DW && t.z ? &tmG : &tmC, b, c0, row0, 0);
                 }
             }
             fence_before();
@@ -444,20 +472,49 @@ gated_grad_kernel(const float4 *__restrict__ G, const float4 *__restrict__ U, co
     }
 }
 
-// Adds the FP32 partials of dX in order, four elements to a thread.
-template <typename T>
+// The split tiles: each is the sum of its partials, in K order, through the
+// epilogue of its mode.  Block (x, y, z): rows 8 x .. 8 x + 7 and columns 128 z ..
+// 128 z + 127 of split tile y, four columns to a lane (FWD: G and U lie 64
+// accumulators apart).
+template <typename T, int MODE, bool GELU>
 __global__ void __launch_bounds__(256)
-gated_sum_kernel(const float4 *__restrict__ part, uint2 *__restrict__ out, int splits, long long n4)
+gated_fix_kernel(const float *__restrict__ part, T *out0, T *out1, float *G, float *U, const Args a)
 {
     pdl_wait();
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n4) return;
-    float4 a = part[i];
-    for (int s = 1; s < splits; ++s) {
-        const float4 b = part[(long long)s * n4 + i];
-        a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+    const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + a.bn - 1) / a.bn;
+    const int k = (int)blockIdx.y;
+    const Tile t = tile_at(a.whole + k, tiles_m, tiles_n);
+    const int r = (int)blockIdx.x * 8 + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int row = t.m * 256 + r;
+    if (row >= a.M) return;
+    const size_t next = (size_t)gridDim.y * 256 * 256;  // the next split's partial of this tile
+    const int j = (int)blockIdx.z * 128 + lane * 4, col = t.n * a.bn + j;
+    if (j >= a.bn || col >= a.N) return;
+    const int acc = MODE == FWD ? (j >> 6) * 128 + (j & 63) : j;
+    const float *p = part + ((size_t)k * 256 + r) * 256 + acc;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f), u = s;
+#pragma unroll 8
+    for (int c = 0; c < a.splits; ++c) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + c * next));
+        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        if (MODE == FWD) {
+            const float4 w = __ldcg(reinterpret_cast<const float4 *>(p + c * next + 64));
+            u.x += w.x; u.y += w.y; u.z += w.z; u.w += w.w;
+        }
     }
-    out[i] = make_uint2(pack2(a.x, a.y, (T *)nullptr), pack2(a.z, a.w, (T *)nullptr));
+    const size_t o = (size_t)row * a.N + col;
+    if (MODE == FWD) {
+        if (a.save) {
+            *reinterpret_cast<float4 *>(G + o) = s;
+            *reinterpret_cast<float4 *>(U + o) = u;
+        }
+        s.x = gate_act<GELU>(s.x) * u.x;
+        s.y = gate_act<GELU>(s.y) * u.y;
+        s.z = gate_act<GELU>(s.z) * u.z;
+        s.w = gate_act<GELU>(s.w) * u.w;
+    }
+    *reinterpret_cast<uint2 *>((t.z ? out1 : out0) + o) =
+        make_uint2(pack2(s.x, s.y, (T *)nullptr), pack2(s.z, s.w, (T *)nullptr));
 }
 
 template <typename T, uint32_t FORMAT, int MODE, bool GELU>
@@ -481,11 +538,45 @@ bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long 
                      1, 128);
 }
 
+// How the tiles go to the clusters.  Whole waves of tiles first; the rest is split
+// when that saves more than the partials and the second kernel cost: a K block
+// takes 0.3 us, they about 5 us (17 blocks); a split is eight blocks at least.
+// Measured, forward: 1024 x 12288 x 4096 (384 tiles on 76 clusters) 112 us against
+// 120 with whole tiles, 128 x 12288 x 4096 (96 tiles) 46.8 against 51.8.
+struct Plan {
+    long long tiles, blocks;  // blocks: the longest cluster's, and 17 where tiles are split
+    int clusters, whole, splits;
+};
+Plan plan(long long tiles, int cmax, long long num_kb) {
+    const long long waves = tiles / cmax, rem = tiles - waves * cmax;
+    Plan p = {tiles, (waves + (rem > 0)) * num_kb, (int)std::min<long long>(tiles, cmax), (int)tiles, 1};
+    if (rem == 0) return p;
+    const long long splits = std::min<long long>({cmax / rem, num_kb / 8, 16});
+    if (splits < 2 || num_kb - num_kb / splits < 17) return p;
+    p.blocks = waves * num_kb + num_kb / splits + 17;
+    p.whole = (int)(waves * cmax);
+    p.splits = (int)splits;
+    p.clusters = waves > 0 ? cmax : (int)(rem * splits);
+    return p;
+}
+// A plan's partials: 256 x 256 FP32 slabs.
+long long plan_slabs(const Plan &p) { return p.splits > 1 ? (p.tiles - p.whole) * p.splits : 0; }
+size_t plan_scratch(const Plan &p) { return (size_t)plan_slabs(p) * 256 * 256 * 4; }
+
+// Launches the pair kernel and, where tiles were split, the one that adds
+// their partials (in `part`).
 template <typename T, uint32_t FORMAT, int MODE, bool GELU>
 cudaError_t launch_pair(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb2, const CUtensorMap &tc,
-                        const CUtensorMap &tg, const CUtensorMap &tu, const Args &args, int clusters, cudaStream_t s) {
+                        const CUtensorMap &tg, const CUtensorMap &tu, Args args, const Plan &p, void *part, T *out0,
+                        T *out1, float *G, float *U, cudaStream_t s) {
+    args.whole = p.whole;
+    args.splits = p.splits;
+    CUtensorMap tp = tc;
+    if (p.splits > 1 && !make_map3(&tp, part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 256, 256, plan_slabs(p), 1024, 256 * 1024,
+                                   32, 32, 1, 128))
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * clusters), 1, 1);
+    cfg.gridDim = dim3((unsigned)(2 * p.clusters), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem_bytes(MODE);
     cfg.stream = s;
@@ -497,7 +588,12 @@ cudaError_t launch_pair(const CUtensorMap &ta, const CUtensorMap &tb, const CUte
     pdl_attr(attr[1]);
     cfg.attrs = attr;
     cfg.numAttrs = g_pdl ? 2 : 1;
-    return launch_counted(&cfg, gated_pair_kernel<T, FORMAT, MODE, GELU>, ta, tb, tb2, tc, tg, tu, args);
+    const cudaError_t e = launch_counted(&cfg, gated_pair_kernel<T, FORMAT, MODE, GELU>, ta, tb, tb2, tc, tg, tu, tp, args);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    cudaLaunchAttribute fa[1];
+    const cudaLaunchConfig_t fc = pdl_config(dim3(32, (unsigned)(p.tiles - p.whole), (unsigned)((args.bn + 127) / 128)),
+                                             dim3(256), 0, s, fa);
+    return launch_counted(&fc, gated_fix_kernel<T, MODE, GELU>, static_cast<const float *>(part), out0, out1, G, U, args);
 }
 
 template <typename T, uint32_t FORMAT, bool GELU>
@@ -520,42 +616,46 @@ cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s)
     a.N = p.N;
     a.num_kb = (p.K + BK - 1) / BK;
     a.bn = 128;
-    a.splits = a.batch = 1;
+    a.batch = 1;
     a.save = p.G != nullptr;
     a.status = status;
-    return launch_pair<T, FORMAT, FWD, GELU>(tx, tg, tu, tz, tsg, tsu, a, (int)std::min<long long>(tiles, cmax), s);
+    const Plan pl = plan(tiles, cmax, a.num_kb);
+    void *ws = nullptr;
+    cudaError_t e = pl.splits > 1 ? scratch_alloc(&ws, plan_scratch(pl), s) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    e = launch_pair<T, FORMAT, FWD, GELU>(tx, tg, tu, tz, tsg, tsu, a, pl, ws, static_cast<T *>(p.Z),
+                                          static_cast<T *>(p.Z), p.G, p.U, s);
+    const cudaError_t f = ws ? cudaFreeAsync(ws, s) : cudaSuccess;
+    return e != cudaSuccess ? e : f;
 }
 
 template <typename T, uint32_t FORMAT, bool GELU>
 cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, cudaStream_t s) {
-    const int cmax = clusters_max<T, FORMAT, DX, false>(dev);
-    if (cmax <= 0) return cudaErrorNotSupported;
+    const int cmax = clusters_max<T, FORMAT, DX, false>(dev), wmax = clusters_max<T, FORMAT, DW, false>(dev);
+    if (cmax <= 0 || wmax <= 0) return cudaErrorNotSupported;
     const long long mn = (long long)p.M * p.N;
-    // dX: tile width and split.  Waves of tiles over the clusters, widest on ties
-    // (a tile's time is set mostly by the operand feed); with under half the
-    // clusters busy, the joined index is split over the idle ones.
+    const bool pair_dx = p.dX && p.M > kGatedSkinnyMaxM, both = p.dWg && p.dWu;
+    // dX: the tile width with the shortest plan, widest on ties; a K block of a
+    // narrower tile takes little less time (the operand feed).
     const long long tiles_m = (p.M + 255LL) / 256;
     const int half = (p.N + BK - 1) / BK;
-    int bn = 256, splits = 1;
-    long long best = -1;
+    int bn = 0;
+    Plan px = {};
+    long long best = 0;
     for (int c = 256; c >= 128; c -= 64) {
-        const long long t = tiles_m * ((p.K + c - 1) / c);
-        const long long cost = (t + cmax - 1) / cmax * (c > 224 ? c : 224);
-        if (best < 0 || cost < best) { best = cost; bn = c; }
+        const Plan q = plan(tiles_m * ((p.K + c - 1LL) / c), cmax, 2LL * half);
+        const long long cost = q.blocks * (c > 224 ? c : 224);
+        if (bn == 0 || cost < best) { bn = c; px = q; best = cost; }
     }
-    const long long wide = tiles_m * ((p.K + 255) / 256);
-    if (wide * 2 <= cmax) {
-        bn = 256;
-        splits = (int)std::max<long long>(1, std::min<long long>({cmax / wide, 2LL * half / 8, 16LL}));
-    }
-    const long long tiles = tiles_m * ((p.K + bn - 1) / bn);
-    if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-    // scratch: dG and dU, and dX's partials
-    const size_t grads = (size_t)mn * 4, parts = p.dX && p.M > kGatedSkinnyMaxM && splits > 1 ? (size_t)splits * p.M * p.K * 4 : 0;
-    const size_t off = (grads + 255) & ~(size_t)255;
+    const Plan pw = plan((p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1), wmax, (p.M + BK - 1LL) / BK);
+    if (px.tiles > 0x7FFFFFFFLL || pw.tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    // scratch: dG and dU, and the partials of the two products, one after the other
+    const size_t off = ((size_t)mn * 4 + 1023) & ~(size_t)1023;
+    const size_t parts = std::max(pair_dx ? plan_scratch(px) : 0, p.dWg || p.dWu ? plan_scratch(pw) : 0);
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(&ws, off + parts, s);
     if (e != cudaSuccess) return e;
+    void *part = static_cast<uint8_t *>(ws) + off;
     T *dG = static_cast<T *>(ws), *dU = dG + mn;
     {
         const long long n4 = mn / 4, blocks = (n4 + 256 * GRAD_UNITS - 1) / (256 * GRAD_UNITS);
@@ -567,48 +667,32 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
                                  reinterpret_cast<const float4 *>(p.U), static_cast<const uint2 *>(p.dZ),
                                  reinterpret_cast<uint2 *>(dG), reinterpret_cast<uint2 *>(dU), n4);
     }
-    if (e == cudaSuccess && p.dX && p.M <= kGatedSkinnyMaxM) {
+    if (e == cudaSuccess && p.dX && !pair_dx) {
         e = launch_gated_skinny_dx(p, dG, num_sms, status, s);
     } else if (e == cudaSuccess && p.dX) {
-        CUtensorMap ta, tb, tb2, tc, tp;
-        bool ok = map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) &&
-                  map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) &&
-                  map16(&tb2, p.Wu, FORMAT, p.K, p.N, BK, bn / 2) &&
-                  map16(&tc, p.dX, FORMAT, p.M, p.K, 64, 32);
-        tp = tc;
-        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + off);
-        const long long row = 4LL * p.K;
-        if (splits > 1)
-            ok = ok && make_map3(&tp, part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, row, row * p.M, 32, 32, 1, 128);
-        Args a = {};
-        a.M = p.M;
-        a.N = p.K;
-        a.num_kb = 2 * half;
-        a.kb_half = half;
-        a.bn = bn;
-        a.splits = splits;
-        a.batch = 1;
-        a.status = status;
-        e = ok ? launch_pair<T, FORMAT, DX, false>(ta, tb, tb2, tc, tp, tp, a,
-                                                   (int)std::min<long long>(tiles * splits, cmax), s)
-               : cudaErrorInvalidValue;
-        if (e == cudaSuccess && splits > 1) {
-            const long long n4 = (long long)p.M * p.K / 4;
-            cudaLaunchAttribute attr[1];
-            const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s, attr);
-            e = launch_counted(&cfg, gated_sum_kernel<T>, reinterpret_cast<const float4 *>(part),
-                               static_cast<uint2 *>(p.dX), splits, n4);
+        CUtensorMap ta, tb, tb2, tc;
+        if (!map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) || !map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) ||
+            !map16(&tb2, p.Wu, FORMAT, p.K, p.N, BK, bn / 2) || !map16(&tc, p.dX, FORMAT, p.M, p.K, 64, 32)) {
+            e = cudaErrorInvalidValue;
+        } else {
+            Args a = {};
+            a.M = p.M;
+            a.N = p.K;
+            a.num_kb = 2 * half;
+            a.kb_half = half;
+            a.bn = bn;
+            a.batch = 1;
+            a.status = status;
+            T *out = static_cast<T *>(p.dX);
+            e = launch_pair<T, FORMAT, DX, false>(ta, tb, tb2, tc, tc, tc, a, px, part, out, out, nullptr, nullptr, s);
         }
     }
     if (e == cudaSuccess && (p.dWg || p.dWu)) {
-        const int wmax = clusters_max<T, FORMAT, DW, false>(dev);
-        const bool both = p.dWg && p.dWu;
-        const long long wt = (p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1);
+        T *w0 = static_cast<T *>(p.dWg ? p.dWg : p.dWu), *w1 = static_cast<T *>(p.dWu ? p.dWu : p.dWg);
         CUtensorMap ta, tb, tc, tc2;
-        if (wmax <= 0 || wt > 0x7FFFFFFFLL || !map16(&ta, p.X, FORMAT, p.M, p.K, 64, BK) ||
-            !map16(&tb, both || p.dWg ? dG : dU, FORMAT, p.M, p.N, 64, BK, both ? 2 : 1, mn * 2) ||
-            !map16(&tc, p.dWg ? p.dWg : p.dWu, FORMAT, p.K, p.N, 64, 32) ||
-            !map16(&tc2, p.dWu ? p.dWu : p.dWg, FORMAT, p.K, p.N, 64, 32)) {
+        if (!map16(&ta, p.X, FORMAT, p.M, p.K, 64, BK) ||
+            !map16(&tb, p.dWg ? dG : dU, FORMAT, p.M, p.N, 64, BK, both ? 2 : 1, mn * 2) ||
+            !map16(&tc, w0, FORMAT, p.K, p.N, 64, 32) || !map16(&tc2, w1, FORMAT, p.K, p.N, 64, 32)) {
             e = cudaErrorInvalidValue;
         } else {
             Args a = {};
@@ -616,10 +700,9 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
             a.N = p.N;
             a.num_kb = (p.M + BK - 1) / BK;
             a.bn = 256;
-            a.splits = 1;
             a.batch = both ? 2 : 1;
             a.status = status;
-            e = launch_pair<T, FORMAT, DW, false>(ta, tb, tb, tc, tc2, tc2, a, (int)std::min<long long>(wt, wmax), s);
+            e = launch_pair<T, FORMAT, DW, false>(ta, tb, tb, tc, tc2, tc2, a, pw, part, w0, w1, nullptr, nullptr, s);
         }
     }
     const cudaError_t f = cudaFreeAsync(ws, s);
