@@ -236,16 +236,20 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             const T *X = static_cast<const T *>(args.X);
             auto load = [&](int kb, int r, uint32_t (&v)[8]) {
                 const int k = kb * KB + u * 16;
-                const int left = r < M && k < K ? K - k : 0;
+                if (r >= M || k >= K) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = 0u;
+                    return;
+                }
                 const T *x = X + (long long)r * args.ldx + k;
-                if (args.x_vec) fp4_load16<16>(x, left, v);
-                else fp4_load16<2>(x, left, v);
+                if (args.x_vec) fp4_load16<16>(x, K - k, v);
+                else fp4_load16<2>(x, K - k, v);
             };
             int slot = warp - 2;
             uint32_t phase = 0;
             while (slot >= stages) { slot -= stages; phase ^= 1u; }
             // UNITS row pairs at a time, the next ones' values in flight meanwhile
-            constexpr int UNITS = 4;
+            constexpr int UNITS = 2;
             uint32_t next[UNITS][8];
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) load(kb0 + warp - 2, half + 2 * i, next[i]);
