@@ -84,6 +84,7 @@ struct Args {
     int save;     // FWD: store G and U
     int whole;    // tiles computed whole; the rest are split
     int splits;   // in so many K ranges, one to a cluster
+    int beside;   // DX: runs beside the dW kernel before it (below)
     int *status;
 };
 
@@ -198,8 +199,19 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
     fence_after();
     const uint32_t tmem_base = bars->tmem_base;
-    pdl_launch_dependents();
-    pdl_wait();
+    // The backward pass launches dW, then dX, which reads nothing that dW writes: dW
+    // lets its dependent start only after its own wait, so that dG and dU are
+    // complete by then, and dX (args.beside) begins at once, on the SMs that dW
+    // leaves, and waits for dW before it ends, so that whatever follows finds both.
+    // Backward of 1024 x 12288 x 4096 270 us against 282 one after the other, 128 x
+    // 12288 x 4096 108 against 114, 333 x 1000 x 1000 20.6 against 22.3.
+    if (MODE == DW) {
+        pdl_wait();
+        pdl_launch_dependents();
+    } else {
+        pdl_launch_dependents();
+        if (!(MODE == DX && args.beside)) pdl_wait();
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer (both CTAs)
@@ -428,6 +440,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         fence_after();
         tmem_dealloc<2>(tmem_base, TMEM_COLS);
     }
+    if (MODE == DX && args.beside) pdl_wait();
 }
 
 __device__ __forceinline__ float2 unpack(uint32_t v, const __nv_bfloat16 *) {
@@ -443,6 +456,7 @@ __global__ void __launch_bounds__(256)
 gated_grad_kernel(const float4 *__restrict__ G, const float4 *__restrict__ U, const uint2 *__restrict__ dZ,
                   uint2 *__restrict__ dG, uint2 *__restrict__ dU, long long n4)
 {
+    pdl_launch_dependents();
     pdl_wait();
     const long long i0 = (long long)blockIdx.x * (256 * GRAD_UNITS) + threadIdx.x;
     float4 g[GRAD_UNITS], u[GRAD_UNITS];
@@ -667,26 +681,6 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
                                  reinterpret_cast<const float4 *>(p.U), static_cast<const uint2 *>(p.dZ),
                                  reinterpret_cast<uint2 *>(dG), reinterpret_cast<uint2 *>(dU), n4);
     }
-    if (e == cudaSuccess && p.dX && !pair_dx) {
-        e = launch_gated_skinny_dx(p, dG, num_sms, status, s);
-    } else if (e == cudaSuccess && p.dX) {
-        CUtensorMap ta, tb, tb2, tc;
-        if (!map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) || !map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) ||
-            !map16(&tb2, p.Wu, FORMAT, p.K, p.N, BK, bn / 2) || !map16(&tc, p.dX, FORMAT, p.M, p.K, 64, 32)) {
-            e = cudaErrorInvalidValue;
-        } else {
-            Args a = {};
-            a.M = p.M;
-            a.N = p.K;
-            a.num_kb = 2 * half;
-            a.kb_half = half;
-            a.bn = bn;
-            a.batch = 1;
-            a.status = status;
-            T *out = static_cast<T *>(p.dX);
-            e = launch_pair<T, FORMAT, DX, false>(ta, tb, tb2, tc, tc, tc, a, px, part, out, out, nullptr, nullptr, s);
-        }
-    }
     if (e == cudaSuccess && (p.dWg || p.dWu)) {
         T *w0 = static_cast<T *>(p.dWg ? p.dWg : p.dWu), *w1 = static_cast<T *>(p.dWu ? p.dWu : p.dWg);
         CUtensorMap ta, tb, tc, tc2;
@@ -703,6 +697,29 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
             a.batch = both ? 2 : 1;
             a.status = status;
             e = launch_pair<T, FORMAT, DW, false>(ta, tb, tb, tc, tc2, tc2, a, pw, part, w0, w1, nullptr, nullptr, s);
+        }
+    }
+    if (e == cudaSuccess && p.dX && !pair_dx) {
+        e = launch_gated_skinny_dx(p, dG, num_sms, status, s);
+    } else if (e == cudaSuccess && p.dX) {
+        CUtensorMap ta, tb, tb2, tc;
+        if (!map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) || !map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) ||
+            !map16(&tb2, p.Wu, FORMAT, p.K, p.N, BK, bn / 2) || !map16(&tc, p.dX, FORMAT, p.M, p.K, 64, 32)) {
+            e = cudaErrorInvalidValue;
+        } else {
+            Args a = {};
+            a.M = p.M;
+            a.N = p.K;
+            a.num_kb = 2 * half;
+            a.kb_half = half;
+            a.bn = bn;
+            a.batch = 1;
+            // (where dW's tiles are split, a kernel that adds them lies between, and
+            // the partials' scratch is shared)
+            a.beside = g_pdl && (p.dWg || p.dWu) && pw.splits == 1;
+            a.status = status;
+            T *out = static_cast<T *>(p.dX);
+            e = launch_pair<T, FORMAT, DX, false>(ta, tb, tb2, tc, tc, tc, a, px, part, out, out, nullptr, nullptr, s);
         }
     }
     const cudaError_t f = cudaFreeAsync(ws, s);
