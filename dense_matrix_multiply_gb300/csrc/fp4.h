@@ -135,15 +135,19 @@ __device__ __forceinline__ float2 fma2(const float2 &a, const float2 &b, const f
     return r;
 }
 
-// Values of eight packed codes times a factor.
-__device__ __forceinline__ void fp4_unpack8(uint32_t codes, float f, float (&v)[8]) {
+// Values of eight packed codes, in pairs.
+__device__ __forceinline__ void fp4_unpack8(uint32_t codes, float2 (&v)[4]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((codes >> (8 * i)) & 255u), __NV_E2M1));
-        const float2 p = __half22float2(h);
-        v[2 * i] = p.x * f;
-        v[2 * i + 1] = p.y * f;
-    }
+    for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
 }
 template <bool NV>
 __device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
