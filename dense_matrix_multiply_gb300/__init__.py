@@ -333,6 +333,7 @@ def gemm_fp4_quantize(dtype: str, fmt: str, A, lda: int, tensor_scale, Q, S, M: 
     device for 'nv' (None: 1), None for 'mx'.  See include/gemm.h."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4_quantize", dtype, fmt)
+    M, K, lda = int(M), int(K), int(lda)
     nq, ns, ng = _fp4_sizes(f, M, K)
     _check_all("gemm_fp4_quantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
                ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
@@ -346,6 +347,7 @@ def gemm_fp4_dequantize(dtype: str, fmt: str, Q, S, tensor_scale, A, lda: int, M
     """Writes the values that codes Q and scales S stand for to A [M,K]."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4_dequantize", dtype, fmt)
+    M, K, lda = int(M), int(K), int(lda)
     nq, ns, ng = _fp4_sizes(f, M, K)
     _check_all("gemm_fp4_dequantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
                ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
@@ -360,6 +362,7 @@ def gemm_fp4(dtype: str, fmt: str, Qa, Sa, ga, Qb, Sb, gb, C, ldc: int, M: int, 
     b [N,K] of format 'mx' or 'nv'."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4", dtype, fmt)
+    M, N, K, ldc = int(M), int(N), int(K), int(ldc)
     if M > 0 and N > 0:
         qa, sa, na = _fp4_sizes(f, M, K)
         qb, sb, nb = _fp4_sizes(f, N, K)
@@ -377,6 +380,7 @@ def gemm_fp4_linear(dtype: str, fmt: str, X, ldx: int, gx, Qw, Sw, gw, C, ldc: i
     quantised within the call (tensor scale gx) and W [N,K] quantised already."""
     lib = load()
     d, f = _fp4_enums("gemm_fp4_linear", dtype, fmt)
+    M, N, K, ldx, ldc = int(M), int(N), int(K), int(ldx), int(ldc)
     if M > 0 and N > 0:
         qw, sw, nw = _fp4_sizes(f, N, K)
         _check_all("gemm_fp4_linear", ("X", X, 2, _span(M, K, ldx), False), ("gx", gx, 4, nw, True),
@@ -402,6 +406,7 @@ def gemm_gated(dtype: str, act: str, X, W_g, W_u, Z, G, U, M: int, N: int, K: in
     (FP32 [M,N], or both None) keep the two products for gemm_gated_backward."""
     lib = load()
     d, a = _gated_enums("gemm_gated", dtype, act)
+    M, N, K = int(M), int(N), int(K)
     nx, nw, nz = _dims(M, N, K)
     _check_all("gemm_gated", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
                ("Z", Z, 2, nz, True), ("G", G, 4, nz, True), ("U", U, 4, nz, True))

@@ -56,7 +56,7 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
         uint32_t v[ROWS][8];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const int left = row0 + i < M ? K - (int)k : 0;
+            const int left = row0 + i < M ? (int)((uint32_t)K - k) : 0;
             fp4_load16<VEC>(a_row + i * lda + k, left, v[i]);
         }
         const uint32_t a = k / (64 * SPAN);

@@ -48,8 +48,9 @@
  * that kernel has completed, so stream order holds for any producer of A or B
  * and any consumer of C, the library's or not.  (An FP32 call whose last round
  * of tiles is at most half full launches two grids; the second reads A and B
- * while the first still runs, and completes only after it.)  A call launches
- * one to three kernels, or more for a general-form batch beyond 65535 matrices;
+ * while the first still runs, and completes only after it; so do the two
+ * products of gemm_gated_backward.)  A call launches one to five kernels, or
+ * more for a general-form batch beyond 65535 matrices;
  * gemm_kernel_launches() counts them.  Calls may be captured into CUDA
  * graphs.  Results are deterministic: the same inputs give bit-identical C on
  * every run (no atomics, fixed summation order per element).
@@ -400,7 +401,7 @@ GEMM_API const char *gemm_last_error(void);
  * after loading one stage while the first has loaded further, so that the pair
  * ends with loads of only one CTA outstanding.  gemm_bf16_rm_noalloc
  * honours "umma_stall" (recording in its static status word) and ignores the
- * other families. */
+ * other families; the FP8, 4-bit and gated entry points ignore them all. */
 GEMM_API gemm_status_t gemm_force_kernel(const char *family);
 
 #ifdef __cplusplus
