@@ -9,15 +9,17 @@
 // that no scale that a product reads is left undefined.
 // Read-back: a lane writes 16 bytes (eight values), a warp 512 elements of each
 // of ROWS rows.
-// Loads of A (stores of the values read back) are as wide as its rows' alignment
-// allows: 16, 8, 4 or 2 bytes.
+// Rows that do not start on 16 bytes (an odd K, a slice of a wider matrix) are
+// loaded in whole 16-byte pieces too, shifted between lanes (fp4.h), and stored so,
+// each lane reading the codes of a piece.
 //
 // Bound: HBM, 2 bytes read and 0.53 (MX) or 0.56 (NV) written an element, or the
 // other way round; NV's quantiser by its arithmetic nearly as much (a quotient of
 // three operations an element, two elements to an instruction).  Measured back to
 // back from DRAM: bf16 16384 x 8192 NV quantised in 59.4 us (5.79 TB/s, 0.87 of the
-// copy bandwidth) and read back in 53.3 (6.45, 0.97); 4096 x 4096 MX 7.8 and 8.2 us,
-// NV 9.4 and 8.3; f16 777 x 12300 NV (rows on 8 bytes) 7.4 and 6.7.  Two rows to a
+// copy bandwidth) and read back in 53.3 (6.45, 0.97); 4096 x 4096 MX 7.7 and 8.0 us,
+// NV 9.4 and 8.2; f16 777 x 12300 NV (rows on 8 bytes) 8.7 and 6.7; 4096 x 4095 NV
+// (rows on 2) 13.2 and 11.3.  Two rows to a
 // warp and four warps to a block: one row 75.9 and 66.1 us for the first, four rows
 // 70.5 and 61.3, eight warps 68.4 and 63.7, against 63.3 and 59.4 (before row
 // addresses were formed once a row, 12.9 instructions an element of the read-back).
@@ -33,7 +35,7 @@ constexpr int WARPS = 4, ROWS = 2;
 
 // Block (x, y): rows [8 x, 8 x + 8), elements [512 y, 512 y + 512) and, past
 // 65535 x 512 elements, every gridDim.y-th such piece.
-template <typename T, bool NV, int VEC>
+template <typename T, bool NV, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32)
 fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restrict__ tensor_scale,
                     uint8_t *__restrict__ Q, uint8_t *__restrict__ S, int M, int K)
@@ -49,6 +51,8 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
     const uint32_t atoms = (uint32_t)fp4_atoms(NV, K), rb = (uint32_t)fp4_row_bytes(K);
     constexpr uint32_t SPAN = NV ? 1 : 2;  // lanes to a block
     const T *a_row = A + row0 * lda;
+    const uint8_t *lo = reinterpret_cast<const uint8_t *>(A),
+                  *hi = reinterpret_cast<const uint8_t *>(A + (M - 1) * lda + K);
     uint8_t *q_row = Q + (long long)row0 * rb;
     uint8_t *s_row = S + fp4_scale_at(row0, 0, (int)atoms);  // ROWS divides 32: rows 16 bytes apart
     static_assert(32 % ROWS == 0, "rows of one group of 32");
@@ -56,8 +60,9 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
         uint32_t v[ROWS][8];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const int left = row0 + i < M ? (int)((uint32_t)K - k) : 0;
-            fp4_load16<VEC>(a_row + i * lda + k, left, v[i]);
+            const int left = row0 + i < M ? (int)((uint32_t)K - k) : -512;
+            if (VEC) fp4_load16<true>(a_row + i * lda + k, left, v[i]);
+            else fp4_load16_any(a_row + i * lda + k, left, lo, hi, v[i]);
         }
         const uint32_t a = k / (64 * SPAN);
 #pragma unroll
@@ -82,7 +87,7 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
 
 // v s is exact in FP32 (6 significant bits at most); times g one rounding, and one
 // to T.
-template <typename T, bool NV, int VEC>
+template <typename T, bool NV, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32)
 fp4_dequantize_kernel(const uint8_t *__restrict__ Q, const uint8_t *__restrict__ S,
                       const float *__restrict__ tensor_scale, T *__restrict__ A, long long lda, int M, int K)
@@ -96,8 +101,13 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ Q, const uint8_t *__restrict__
     T *a_row = A + row0 * lda;
     const uint8_t *q_row = Q + (long long)row0 * rb;
     const uint8_t *s_row = S + fp4_scale_at(row0, 0, fp4_atoms(NV, K));  // rows 16 bytes apart, as above
-    for (uint32_t k0 = blockIdx.y * 512 + lane * 8; k0 - lane * 8 < (uint32_t)K; k0 += gridDim.y * 512) {
-        uint32_t codes[ROWS][2], byte[ROWS][2];
+    // VEC: a lane's eight values are k .. k + 7.  Else they are the ones that make up
+    // an aligned 16-byte piece of the row: `off` before that, the row's distance from
+    // 16 bytes, with the end of one code word and the start of the next, and the
+    // scales of two blocks where they fall into two.  (A last piece past the
+    // grid's 512 y + 511 is the first blocks' second.)
+    for (uint32_t k0 = blockIdx.y * 512 + lane * 8; k0 - lane * 8 < (uint32_t)K + (VEC ? 0 : 7); k0 += gridDim.y * 512) {
+        uint32_t codes[ROWS][2], byte[ROWS][2], before[VEC ? 1 : ROWS][2], byte1[VEC ? 1 : ROWS][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t k = k0 + h * 256;
@@ -105,9 +115,16 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ Q, const uint8_t *__restrict__
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
                 codes[i][h] = byte[i][h] = 0u;
-                if (row0 + i < M && k < (uint32_t)K) {
-                    codes[i][h] = __ldg(reinterpret_cast<const uint32_t *>(q_row + (size_t)i * rb + k / 2));
-                    byte[i][h] = __ldg(s_row + at + i * 16);
+                const bool here = row0 + i < M && k / 2 < rb;
+                if (here) codes[i][h] = __ldg(reinterpret_cast<const uint32_t *>(q_row + (size_t)i * rb + k / 2));
+                if (here) byte[i][h] = __ldg(s_row + at + i * 16);
+                if constexpr (!VEC) {
+                    before[i][h] = byte1[i][h] = 0u;
+                    if (row0 + i < M && k >= 8 && (k - 8) / 2 < rb) {
+                        const uint32_t p = k - 8;
+                        before[i][h] = __ldg(reinterpret_cast<const uint32_t *>(q_row + (size_t)i * rb + p / 2));
+                        byte1[i][h] = __ldg(s_row + (size_t)(p / (4 * B)) * 512 + (p / B & 3) + i * 16);
+                    }
                 }
             }
         }
@@ -115,45 +132,50 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ Q, const uint8_t *__restrict__
         for (int i = 0; i < ROWS; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (row0 + i >= M) break;  // warp-uniform
                 const uint32_t k = k0 + h * 256;
-                if (row0 + i >= M || k >= (uint32_t)K) continue;
                 const float f = fp4_scale_value<NV>(byte[i][h]);
+                T *a = a_row + i * lda + k;
                 float2 v[4];
                 uint32_t o[4];
-                fp4_unpack8(codes[i][h], v);
+                int first = 0, left = (int)((uint32_t)K - k);  // of the eight values, those in the row
+                if constexpr (VEC) {
+                    fp4_unpack8(codes[i][h], v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], make_float2(f, f));
+                } else {
+                    const int off = (int)(((uintptr_t)a & 15) >> 1);
+                    // values 0 .. off - 1 are the last `off` of the word before (k - 8 .. k - 1)
+                    const float f1 = fp4_scale_value<NV>(byte1[i][h]);
+                    const uint32_t c = off ? __funnelshift_l(before[i][h], codes[i][h], 4 * off) : codes[i][h];
+                    fp4_unpack8(c, v);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = mul2(v[j], make_float2(2 * j < off ? f1 : f, 2 * j + 1 < off ? f1 : f));
+                    a -= off;
+                    left += off;
+                    first = k == 0 ? off : 0;  // (nothing lies before the row)
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    v[j] = mul2(v[j], make_float2(f, f));
                     if (NV) v[j] = mul2(v[j], make_float2(g, g));
                     o[j] = tc::pack2(v[j].x, v[j].y, (T *)nullptr);
                 }
-                T *a = a_row + i * lda + k;
-                if (VEC >= 4 && k + 8 <= (uint32_t)K) {
-                    if constexpr (VEC == 16) {
-                        *reinterpret_cast<uint4 *>(a) = make_uint4(o[0], o[1], o[2], o[3]);
-                    } else if constexpr (VEC == 8) {
-                        reinterpret_cast<uint2 *>(a)[0] = make_uint2(o[0], o[1]);
-                        reinterpret_cast<uint2 *>(a)[1] = make_uint2(o[2], o[3]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) reinterpret_cast<uint32_t *>(a)[j] = o[j];
-                    }
+                if (left >= 8 && first == 0) {
+                    *reinterpret_cast<uint4 *>(a) = make_uint4(o[0], o[1], o[2], o[3]);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        if (k + 2 * j < (uint32_t)K) tc::store1(a + 2 * j, v[j].x);
-                        if (k + 2 * j + 1 < (uint32_t)K) tc::store1(a + 2 * j + 1, v[j].y);
+                        if (2 * j < left && 2 * j >= first) tc::store1(a + 2 * j, v[j].x);
+                        if (2 * j + 1 < left && 2 * j + 1 >= first) tc::store1(a + 2 * j + 1, v[j].y);
                     }
                 }
             }
     }
 }
 
-// The widest access that every row of A allows.
-int row_vec(const void *A, long long lda) {
-    const uintptr_t x = (uintptr_t)A | (uintptr_t)(lda * 2);
-    return (x & 15) == 0 ? 16 : (x & 7) == 0 ? 8 : (x & 3) == 0 ? 4 : 2;
-}
+// Whether every row of A starts on 16 bytes.
+bool rows_vec(const void *A, long long lda) { return (((uintptr_t)A | (uintptr_t)(lda * 2)) & 15) == 0; }
 dim3 grid_of(long long rows, int K) {
     const long long pieces = ((long long)K + 511) / 512;
     return dim3((unsigned)((rows + WARPS * ROWS - 1) / (WARPS * ROWS)), (unsigned)(pieces < 65535 ? pieces : 65535));
@@ -167,29 +189,20 @@ cudaError_t quantize(const void *A, long long lda, const float *g, void *Q, void
         return launch_counted(&cfg, kern, static_cast<const T *>(A), lda, g, static_cast<uint8_t *>(Q),
                               static_cast<uint8_t *>(S), M, K);
     };
-    switch (row_vec(A, lda)) {
-    case 16: return go(fp4_quantize_kernel<T, NV, 16>);
-    case 8: return go(fp4_quantize_kernel<T, NV, 8>);
-    case 4: return go(fp4_quantize_kernel<T, NV, 4>);
-    }
-    return go(fp4_quantize_kernel<T, NV, 2>);
+    return rows_vec(A, lda) ? go(fp4_quantize_kernel<T, NV, true>) : go(fp4_quantize_kernel<T, NV, false>);
 }
 
 template <typename T, bool NV>
 cudaError_t dequantize(const void *Q, const void *S, const float *g, void *A, long long lda, int M, int K,
                        cudaStream_t s) {
     cudaLaunchAttribute attr[1];
+    const bool vec = rows_vec(A, lda);
     const cudaLaunchConfig_t cfg = pdl_config(grid_of(M, K), dim3(WARPS * 32), 0, s, attr);
     auto go = [&](auto kern) {
         return launch_counted(&cfg, kern, static_cast<const uint8_t *>(Q), static_cast<const uint8_t *>(S), g,
                               static_cast<T *>(A), lda, M, K);
     };
-    switch (row_vec(A, lda)) {
-    case 16: return go(fp4_dequantize_kernel<T, NV, 16>);
-    case 8: return go(fp4_dequantize_kernel<T, NV, 8>);
-    case 4: return go(fp4_dequantize_kernel<T, NV, 4>);
-    }
-    return go(fp4_dequantize_kernel<T, NV, 2>);
+    return vec ? go(fp4_dequantize_kernel<T, NV, true>) : go(fp4_dequantize_kernel<T, NV, false>);
 }
 
 }  // namespace

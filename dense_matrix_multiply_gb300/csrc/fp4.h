@@ -171,26 +171,20 @@ __device__ __forceinline__ float2 unpack2(uint32_t v) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&v));
 }
 
-// 16 consecutive values at a (eight packed pairs), of which `left` are in the
-// row; loads of VEC bytes, the alignment of the rows.
-template <int VEC>
+// The first `left` of 16 values (eight packed pairs), the others 0.
+__device__ __forceinline__ void fp4_keep(int left, uint32_t (&v)[8]) {
+    if (left >= 16) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 2 * i + 1 < left ? v[i] : 2 * i < left ? v[i] & 0xFFFFu : 0u;
+}
+// 16 consecutive values at a, of which `left` are in the row: a on 16 bytes, or
+// (VEC = false) value by value.
+template <bool VEC>
 __device__ __forceinline__ void fp4_load16(const void *a, int left, uint32_t (&v)[8]) {
-    if (left >= 16 && VEC >= 4) {
-        if constexpr (VEC == 16) {
-            const uint4 u0 = __ldg(static_cast<const uint4 *>(a)), u1 = __ldg(static_cast<const uint4 *>(a) + 1);
-            v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
-            v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
-        } else if constexpr (VEC == 8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint2 u = __ldg(static_cast<const uint2 *>(a) + i);
-                v[2 * i] = u.x;
-                v[2 * i + 1] = u.y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __ldg(static_cast<const uint32_t *>(a) + i);
-        }
+    if (VEC && left >= 16) {
+        const uint4 u0 = __ldg(static_cast<const uint4 *>(a)), u1 = __ldg(static_cast<const uint4 *>(a) + 1);
+        v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
+        v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
         return;
     }
     const unsigned short *h = static_cast<const unsigned short *>(a);
@@ -199,6 +193,56 @@ __device__ __forceinline__ void fp4_load16(const void *a, int left, uint32_t (&v
         v[i] = 2 * i < left ? (uint32_t)__ldg(h + 2 * i) : 0u;
         if (2 * i + 1 < left) v[i] |= (uint32_t)__ldg(h + 2 * i + 1) << 16;
     }
+}
+
+// Rows that do not start on 16 bytes: a warp takes 16 values to a lane with loads
+// of whole 16-byte pieces all the same, the pieces shifted by d bytes, the distance
+// of a lane's first value from its piece (even, the same in all lanes), and each
+// lane's last part from the lane after it.  The pieces' other bytes are of the same
+// matrix (or are not read: load_piece).
+// An aligned 16-byte piece of [lo, hi): whole, or its values one by one at the ends.
+__device__ __forceinline__ uint4 load_piece(const uint8_t *p, const uint8_t *lo, const uint8_t *hi) {
+    if (p >= lo && p + 16 <= hi) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint8_t *q = p + 2 * i;
+        if (q >= lo && q < hi) w[i >> 1] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(q)) << (16 * (i & 1));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int WORDS>
+__device__ __forceinline__ void fp4_shift_words(const uint32_t (&w)[12], int d, uint32_t (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __funnelshift_r(w[i + WORDS], w[i + WORDS + 1], 8 * (d & 2));
+}
+// The whole warp: the 16 values at a (lane l: base + 16 l values), of which `left`
+// are in the row (K - k, so below 0 past its end; -32 or less in every lane for no
+// row); [lo, hi): the matrix.
+__device__ __forceinline__ void fp4_load16_any(const void *a, int left, const uint8_t *lo, const uint8_t *hi,
+                                               uint32_t (&v)[8]) {
+    const uint8_t *p = static_cast<const uint8_t *>(a);
+    const int d = (int)((uintptr_t)p & 15);
+    const uint8_t *q = p - d, *end = p + 2 * (long long)left;  // of the row, the same in all lanes
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 a0 = q < end ? load_piece(q, lo, hi) : zero;  // (may hold the last values of the lane before)
+    const uint4 a1 = q + 16 < end ? load_piece(q + 16, lo, hi) : zero;
+    uint32_t w[12] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    w[8] = __shfl_down_sync(0xffffffffu, a0.x, 1);
+    w[9] = __shfl_down_sync(0xffffffffu, a0.y, 1);
+    w[10] = __shfl_down_sync(0xffffffffu, a0.z, 1);
+    w[11] = __shfl_down_sync(0xffffffffu, a0.w, 1);
+    if ((threadIdx.x & 31) == 31 && d != 0 && q + 32 < end) {
+        const uint4 a2 = load_piece(q + 32, lo, hi);
+        w[8] = a2.x; w[9] = a2.y; w[10] = a2.z; w[11] = a2.w;
+    }
+    switch (d >> 2) {  // the same in all lanes
+    case 0: fp4_shift_words<0>(w, d, v); break;
+    case 1: fp4_shift_words<1>(w, d, v); break;
+    case 2: fp4_shift_words<2>(w, d, v); break;
+    default: fp4_shift_words<3>(w, d, v); break;
+    }
+    fp4_keep(left, v);
 }
 
 // Codes of the 16 values in v (eight packed pairs) of one block or half block.

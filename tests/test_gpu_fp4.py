@@ -62,7 +62,8 @@ def quantize(a, fmt, gs, pad=0, off=0):
 
 
 SHAPES = [(1, 1, 0, 0), (1, 4096, 0, 0), (3, 31, 0, 0), (2, 33, 0, 1), (129, 256, 8, 0), (130, 515, 1, 0),
-          (64, 1000, 0, 0), (257, 4100, 4, 3), (5, 12288, 0, 0), (300, 96, 0, 0)]
+          (64, 1000, 0, 0), (257, 4100, 4, 3), (5, 12288, 0, 0), (300, 96, 0, 0), (40, 1001, 0, 0), (9, 1030, 0, 5),
+          (16, 2047, 0, 7), (11, 513, 4, 2), (8, 511, 0, 6)]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
