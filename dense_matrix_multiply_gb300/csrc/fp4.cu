@@ -10,15 +10,15 @@
 // Read-back: a lane writes 16 bytes (eight values), a warp 512 elements of each
 // of ROWS rows.
 // Rows that do not start on 16 bytes (an odd K, a slice of a wider matrix) are
-// loaded in whole 16-byte pieces too, shifted between lanes (fp4.h), and stored so,
-// each lane reading the codes of a piece.
+// loaded 8 bytes at a time, or in whole 16-byte pieces shifted between lanes
+// (fp4.h), and stored in such pieces, each lane reading the codes of one.
 //
 // Bound: HBM, 2 bytes read and 0.53 (MX) or 0.56 (NV) written an element, or the
 // other way round; NV's quantiser by its arithmetic nearly as much (a quotient of
 // three operations an element, two elements to an instruction).  Measured back to
 // back from DRAM: bf16 16384 x 8192 NV quantised in 59.4 us (5.79 TB/s, 0.87 of the
 // copy bandwidth) and read back in 53.3 (6.45, 0.97); 4096 x 4096 MX 7.7 and 8.0 us,
-// NV 9.4 and 8.2; f16 777 x 12300 NV (rows on 8 bytes) 8.7 and 6.7; 4096 x 4095 NV
+// NV 9.4 and 8.2; f16 777 x 12300 NV (rows on 8 bytes) 7.4 and 6.7; 4096 x 4095 NV
 // (rows on 2) 13.2 and 11.3.  Two rows to a
 // warp and four warps to a block: one row 75.9 and 66.1 us for the first, four rows
 // 70.5 and 61.3, eight warps 68.4 and 63.7, against 63.3 and 59.4 (before row
@@ -35,7 +35,7 @@ constexpr int WARPS = 4, ROWS = 2;
 
 // Block (x, y): rows [8 x, 8 x + 8), elements [512 y, 512 y + 512) and, past
 // 65535 x 512 elements, every gridDim.y-th such piece.
-template <typename T, bool NV, bool VEC>
+template <typename T, bool NV, int VEC>
 __global__ void __launch_bounds__(WARPS * 32)
 fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restrict__ tensor_scale,
                     uint8_t *__restrict__ Q, uint8_t *__restrict__ S, int M, int K)
@@ -61,7 +61,7 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             const int left = row0 + i < M ? (int)((uint32_t)K - k) : -512;
-            if (VEC) fp4_load16<true>(a_row + i * lda + k, left, v[i]);
+            if (VEC) fp4_load16<VEC>(a_row + i * lda + k, left, v[i]);
             else fp4_load16_any(a_row + i * lda + k, left, lo, hi, v[i]);
         }
         const uint32_t a = k / (64 * SPAN);
@@ -174,8 +174,10 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ Q, const uint8_t *__restrict__
     }
 }
 
-// Whether every row of A starts on 16 bytes.
-bool rows_vec(const void *A, long long lda) { return (((uintptr_t)A | (uintptr_t)(lda * 2)) & 15) == 0; }
+// Whether every row of A starts on so many bytes.
+bool rows_on(const void *A, long long lda, uintptr_t bytes) {
+    return (((uintptr_t)A | (uintptr_t)(lda * 2)) & (bytes - 1)) == 0;
+}
 dim3 grid_of(long long rows, int K) {
     const long long pieces = ((long long)K + 511) / 512;
     return dim3((unsigned)((rows + WARPS * ROWS - 1) / (WARPS * ROWS)), (unsigned)(pieces < 65535 ? pieces : 65535));
@@ -189,20 +191,23 @@ cudaError_t quantize(const void *A, long long lda, const float *g, void *Q, void
         return launch_counted(&cfg, kern, static_cast<const T *>(A), lda, g, static_cast<uint8_t *>(Q),
                               static_cast<uint8_t *>(S), M, K);
     };
-    return rows_vec(A, lda) ? go(fp4_quantize_kernel<T, NV, true>) : go(fp4_quantize_kernel<T, NV, false>);
+    // Rows on 8 bytes: loads of 8 (f16 777 x 12300 NV 7.4 us, in shifted pieces 8.7).
+    // On 4 or 2: in pieces (4096 x 4095 NV 13.2 us, value by value 18.9).
+    return rows_on(A, lda, 16) ? go(fp4_quantize_kernel<T, NV, 16>)
+           : rows_on(A, lda, 8) ? go(fp4_quantize_kernel<T, NV, 8>)
+                                : go(fp4_quantize_kernel<T, NV, 0>);
 }
 
 template <typename T, bool NV>
 cudaError_t dequantize(const void *Q, const void *S, const float *g, void *A, long long lda, int M, int K,
                        cudaStream_t s) {
     cudaLaunchAttribute attr[1];
-    const bool vec = rows_vec(A, lda);
     const cudaLaunchConfig_t cfg = pdl_config(grid_of(M, K), dim3(WARPS * 32), 0, s, attr);
     auto go = [&](auto kern) {
         return launch_counted(&cfg, kern, static_cast<const uint8_t *>(Q), static_cast<const uint8_t *>(S), g,
                               static_cast<T *>(A), lda, M, K);
     };
-    return vec ? go(fp4_dequantize_kernel<T, NV, true>) : go(fp4_dequantize_kernel<T, NV, false>);
+    return rows_on(A, lda, 16) ? go(fp4_dequantize_kernel<T, NV, true>) : go(fp4_dequantize_kernel<T, NV, false>);
 }
 
 }  // namespace

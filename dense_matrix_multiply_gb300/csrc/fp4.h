@@ -177,14 +177,23 @@ __device__ __forceinline__ void fp4_keep(int left, uint32_t (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = 2 * i + 1 < left ? v[i] : 2 * i < left ? v[i] & 0xFFFFu : 0u;
 }
-// 16 consecutive values at a, of which `left` are in the row: a on 16 bytes, or
-// (VEC = false) value by value.
-template <bool VEC>
+// 16 consecutive values at a, of which `left` are in the row: a on VEC = 16 or 8
+// bytes, or (2) value by value.
+template <int VEC>
 __device__ __forceinline__ void fp4_load16(const void *a, int left, uint32_t (&v)[8]) {
-    if (VEC && left >= 16) {
+    if (VEC == 16 && left >= 16) {
         const uint4 u0 = __ldg(static_cast<const uint4 *>(a)), u1 = __ldg(static_cast<const uint4 *>(a) + 1);
         v[0] = u0.x; v[1] = u0.y; v[2] = u0.z; v[3] = u0.w;
         v[4] = u1.x; v[5] = u1.y; v[6] = u1.z; v[7] = u1.w;
+        return;
+    }
+    if (VEC == 8 && left >= 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint2 u = __ldg(static_cast<const uint2 *>(a) + i);
+            v[2 * i] = u.x;
+            v[2 * i + 1] = u.y;
+        }
         return;
     }
     const unsigned short *h = static_cast<const unsigned short *>(a);

@@ -242,8 +242,8 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     return;
                 }
                 const T *x = X + (long long)r * args.ldx + k;
-                if (args.x_vec) fp4_load16<true>(x, K - k, v);
-                else fp4_load16<false>(x, K - k, v);
+                if (args.x_vec) fp4_load16<16>(x, K - k, v);
+                else fp4_load16<2>(x, K - k, v);
             };
             int slot = warp - 2;
             uint32_t phase = 0;
