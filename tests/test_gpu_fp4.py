@@ -181,7 +181,7 @@ def test_linear(M, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
-@pytest.mark.parametrize("M,N,K", [(512, 12288, 2048), (1600, 5000, 1000)])
+@pytest.mark.parametrize("M,N,K", [(512, 12288, 2048), (1600, 5000, 1000), (1601, 5003, 999)])
 def test_product_over_several_waves_of_tiles(M, N, K, fmt):
     """192-wide tiles (every second one starts inside a 128-row tile of scales) and
     256-wide ones, several to a cluster, so that both accumulators are used."""
