@@ -519,13 +519,16 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     p.K = K;
     p.elt = elt;
     p.nv = nv;
-    // Few rows run on the weight stream.  A linear layer's X is quantised inside
-    // it for M <= 8, by a launch of its own above: every strip of 128 outputs
-    // converts X anew, which for M = 8 is hidden behind the stream (N = 12288, K =
-    // 4096, NV: 10.7 us against 11.8 in two launches; N = 4096, K = 12288, MX: 8.7
-    // against 10.9) and for M = 16 no longer is (15.6 against 12.0; 10.9 against 11.2).
+    // Few rows run on the weight stream.  A linear layer's X is quantised inside it
+    // for M <= 8, by a launch of its own above: every strip of 128 outputs converts X
+    // anew, which for M = 8 is hidden behind the stream (N = 12288, K = 4096, NV: 10.9
+    // us against 11.1 in two launches; N = 4096, K = 12288, MX: 8.9 against 11.3) and
+    // for M = 16 no longer is (15.6 against 11.2).  Rows of X that do not start on 16
+    // bytes are read value by value there, and only for one row (N = 12288, K = 4095, NV:
+    // M = 1 10.2 against 10.8 us, M = 8 20.8 against 11.8).
     const bool skinny = M <= kFp4SkinnyMaxM;
-    if (linear && M <= 8)
+    const bool x16 = aligned16(X) && ldx % 8 == 0;
+    if (linear && M <= (x16 ? 8 : 1))
         return finish(launch_fp4_skinny(p, X, ldx, dev->num_sms, dev->status, s),
                       nv ? "fp4_skinny_fused_nv" : "fp4_skinny_fused_mx");
     auto product = [&] { return skinny ? launch_fp4_skinny(p, nullptr, 0, dev->num_sms, dev->status, s) : launch_fp4_gemm(p, dev->status, s); };

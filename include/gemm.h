@@ -315,10 +315,10 @@ GEMM_API gemm_status_t gemm_fp4(gemm_dtype_t dtype, gemm_fp4_format_t format, co
 
 /* A linear layer with 4-bit weights: X [M,K] (dtype, ldx >= K) quantised within
  * the call as gemm_fp4_quantize does with tensor scale gx, then the product
- * with the quantised weights [N,K].  For M > 8 the codes and scales of X lie in
- * stream-ordered scratch for the duration of the call, from a pool of the
- * library's own that keeps up to 1 GiB on the device between calls; M <= 8
- * converts X inside the product and needs none. */
+ * with the quantised weights [N,K].  For M > 8 (M > 1 where X's rows do not start
+ * on 16 bytes) the codes and scales of X lie in stream-ordered scratch for the
+ * duration of the call, from a pool of the library's own that keeps up to 1 GiB
+ * on the device between calls; fewer rows are converted inside the product. */
 GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t format, const void *X, int64_t ldx,
                                        const float *gx, const uint8_t *Qw, const uint8_t *Sw, const float *gw,
                                        void *C, int64_t ldc, int M, int N, int K);
