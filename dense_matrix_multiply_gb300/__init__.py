@@ -105,6 +105,18 @@ def _addr(x) -> int:
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream(device: int) -> int:
+    """Handle of torch's current stream on a device."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(device)
+
+
 def _bind_torch_stream(*tensors) -> None:
     """Points the library at torch's current stream of the tensors' device.
     Every tensor argument must live on one CUDA device: a kernel given another
@@ -121,8 +133,7 @@ def _bind_torch_stream(*tensors) -> None:
         elif d != dev:
             raise ValueError(f"tensors on two devices: cuda:{dev} and cuda:{d}")
     if dev is not None:
-        import torch
-        load().gemm_set_stream(torch._C._cuda_getCurrentRawStream(dev))
+        load().gemm_set_stream(_current_stream(dev))
 
 
 def _span(outer: int, inner: int, ld: int, stride: int = 0, batch: int = 1) -> int:
@@ -157,13 +168,33 @@ def _check(name: str, t, elt_size: int, need: int, tight: bool = True) -> None:
         raise ValueError(f"{name} holds {room} elements, the call needs {need}")
 
 
-def _check_all(name: str, *args) -> None:
-    """_check of several (argument, tensor, element size, elements, tight); a
-    contiguous tensor with room passes here, without a message being built."""
+def _take(lib, name: str, *args):
+    """Addresses of several tensor arguments (argument, tensor, element size,
+    elements, tight), each checked as by _check -- a contiguous tensor with room
+    passes without a message being built -- and all on one CUDA device, to whose
+    current torch stream the library is pointed."""
+    out, dev, mixed = [], None, False
     for arg, t, size, need, tight in args:
-        if t is None or type(t) is int or (t.element_size() == size and t.is_contiguous() and t.numel() >= need):
+        if t is None:
+            out.append(0)
             continue
-        _check(f"{name}: {arg}", t, size, need, tight)
+        if type(t) is int:
+            out.append(t)
+            continue
+        if t.element_size() != size or not t.is_contiguous() or t.numel() < need:
+            _check(f"{name}: {arg}", t, size, need, tight)
+        d = t.get_device()
+        if d != dev:
+            mixed = dev is not None
+            dev = d if dev is None or d < 0 else dev
+        out.append(t.data_ptr())
+    if dev is not None:
+        if dev < 0:
+            raise ValueError("tensors must live on a CUDA device")
+        if mixed:
+            raise ValueError("tensors on two devices")
+        lib.gemm_set_stream(_current_stream(dev))
+    return out
 
 
 def _dims(M: int, N: int, K: int):
@@ -331,28 +362,26 @@ def gemm_fp4_quantize(dtype: str, fmt: str, A, lda: int, tensor_scale, Q, S, M: 
     """Quantises A [M,K] ('f16' | 'bf16', leading dimension lda) to 4-bit codes Q
     and block scales S, format 'mx' or 'nv'; tensor_scale: one FP32 value on the
     device for 'nv' (None: 1), None for 'mx'.  See include/gemm.h."""
-    lib = load()
+    lib = _lib or load()
     d, f = _fp4_enums("gemm_fp4_quantize", dtype, fmt)
     M, K, lda = int(M), int(K), int(lda)
     nq, ns, ng = _fp4_sizes(f, M, K)
-    _check_all("gemm_fp4_quantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
-               ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
-    _bind_torch_stream(A, tensor_scale, Q, S)
-    st = lib.gemm_fp4_quantize(d, f, _addr(A), lda, _addr(tensor_scale), _addr(Q), _addr(S), M, K)
+    a, q, s, g = _take(lib, "gemm_fp4_quantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
+                       ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
+    st = lib.gemm_fp4_quantize(d, f, a, lda, g, q, s, M, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4_quantize", lib.gemm_last_error().decode())
 
 
 def gemm_fp4_dequantize(dtype: str, fmt: str, Q, S, tensor_scale, A, lda: int, M: int, K: int) -> None:
     """Writes the values that codes Q and scales S stand for to A [M,K]."""
-    lib = load()
+    lib = _lib or load()
     d, f = _fp4_enums("gemm_fp4_dequantize", dtype, fmt)
     M, K, lda = int(M), int(K), int(lda)
     nq, ns, ng = _fp4_sizes(f, M, K)
-    _check_all("gemm_fp4_dequantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
-               ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
-    _bind_torch_stream(A, tensor_scale, Q, S)
-    st = lib.gemm_fp4_dequantize(d, f, _addr(Q), _addr(S), _addr(tensor_scale), _addr(A), lda, M, K)
+    a, q, s, g = _take(lib, "gemm_fp4_dequantize", ("A", A, 2, _span(M, K, lda), False), ("Q", Q, 1, nq, True),
+                       ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
+    st = lib.gemm_fp4_dequantize(d, f, q, s, g, a, lda, M, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4_dequantize", lib.gemm_last_error().decode())
 
@@ -360,17 +389,16 @@ def gemm_fp4_dequantize(dtype: str, fmt: str, Q, S, tensor_scale, A, lda: int, M
 def gemm_fp4(dtype: str, fmt: str, Qa, Sa, ga, Qb, Sb, gb, C, ldc: int, M: int, N: int, K: int) -> None:
     """C [M,N] ('f16' | 'bf16') = ga gb a b^T of two quantised matrices a [M,K] and
     b [N,K] of format 'mx' or 'nv'."""
-    lib = load()
+    lib = _lib or load()
     d, f = _fp4_enums("gemm_fp4", dtype, fmt)
     M, N, K, ldc = int(M), int(N), int(K), int(ldc)
-    if M > 0 and N > 0:
-        qa, sa, na = _fp4_sizes(f, M, K)
-        qb, sb, nb = _fp4_sizes(f, N, K)
-        _check_all("gemm_fp4", ("Qa", Qa, 1, qa, True), ("Sa", Sa, 1, sa, True), ("ga", ga, 4, na, True),
-                   ("Qb", Qb, 1, qb, True), ("Sb", Sb, 1, sb, True), ("gb", gb, 4, nb, True),
-                   ("C", C, 2, _span(M, N, ldc), False))
-    _bind_torch_stream(Qa, Sa, ga, Qb, Sb, gb, C)
-    st = lib.gemm_fp4(d, f, _addr(Qa), _addr(Sa), _addr(ga), _addr(Qb), _addr(Sb), _addr(gb), _addr(C), ldc, M, N, K)
+    some = M > 0 and N > 0  # else a no-op or a call that the library rejects
+    qa, sa, na = _fp4_sizes(f, M, K if some else 0)
+    qb, sb, nb = _fp4_sizes(f, N, K if some else 0)
+    pqa, psa, pga, pqb, psb, pgb, c = _take(
+        lib, "gemm_fp4", ("Qa", Qa, 1, qa, True), ("Sa", Sa, 1, sa, True), ("ga", ga, 4, na, True),
+        ("Qb", Qb, 1, qb, True), ("Sb", Sb, 1, sb, True), ("gb", gb, 4, nb, True), ("C", C, 2, _span(M, N, ldc), False))
+    st = lib.gemm_fp4(d, f, pqa, psa, pga, pqb, psb, pgb, c, ldc, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4", lib.gemm_last_error().decode())
 
@@ -378,16 +406,15 @@ def gemm_fp4(dtype: str, fmt: str, Qa, Sa, ga, Qb, Sb, gb, C, ldc: int, M: int, 
 def gemm_fp4_linear(dtype: str, fmt: str, X, ldx: int, gx, Qw, Sw, gw, C, ldc: int, M: int, N: int, K: int) -> None:
     """C [M,N] = X W^T with X [M,K] ('f16' | 'bf16', leading dimension ldx)
     quantised within the call (tensor scale gx) and W [N,K] quantised already."""
-    lib = load()
+    lib = _lib or load()
     d, f = _fp4_enums("gemm_fp4_linear", dtype, fmt)
     M, N, K, ldx, ldc = int(M), int(N), int(K), int(ldx), int(ldc)
-    if M > 0 and N > 0:
-        qw, sw, nw = _fp4_sizes(f, N, K)
-        _check_all("gemm_fp4_linear", ("X", X, 2, _span(M, K, ldx), False), ("gx", gx, 4, nw, True),
-                   ("Qw", Qw, 1, qw, True), ("Sw", Sw, 1, sw, True), ("gw", gw, 4, nw, True),
-                   ("C", C, 2, _span(M, N, ldc), False))
-    _bind_torch_stream(X, gx, Qw, Sw, gw, C)
-    st = lib.gemm_fp4_linear(d, f, _addr(X), ldx, _addr(gx), _addr(Qw), _addr(Sw), _addr(gw), _addr(C), ldc, M, N, K)
+    some = M > 0 and N > 0  # else a no-op or a call that the library rejects
+    qw, sw, nw = _fp4_sizes(f, N, K if some else 0)
+    x, pgx, q, s, pgw, c = _take(
+        lib, "gemm_fp4_linear", ("X", X, 2, _span(M, K, ldx) if some else 0, False), ("gx", gx, 4, nw, True),
+        ("Qw", Qw, 1, qw, True), ("Sw", Sw, 1, sw, True), ("gw", gw, 4, nw, True), ("C", C, 2, _span(M, N, ldc), False))
+    st = lib.gemm_fp4_linear(d, f, x, ldx, pgx, q, s, pgw, c, ldc, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4_linear", lib.gemm_last_error().decode())
 
@@ -404,14 +431,13 @@ def _gated_enums(name: str, dtype: str, act: str):
 def gemm_gated(dtype: str, act: str, X, W_g, W_u, Z, G, U, M: int, N: int, K: int) -> None:
     """Z [M,N] = act(X W_g) * (X W_u) ('f16' | 'bf16', act 'silu' | 'gelu'); G and U
     (FP32 [M,N], or both None) keep the two products for gemm_gated_backward."""
-    lib = load()
+    lib = _lib or load()
     d, a = _gated_enums("gemm_gated", dtype, act)
     M, N, K = int(M), int(N), int(K)
     nx, nw, nz = _dims(M, N, K)
-    _check_all("gemm_gated", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
-               ("Z", Z, 2, nz, True), ("G", G, 4, nz, True), ("U", U, 4, nz, True))
-    _bind_torch_stream(X, W_g, W_u, Z, G, U)
-    st = lib.gemm_gated(d, a, _addr(X), _addr(W_g), _addr(W_u), _addr(Z), _addr(G), _addr(U), M, N, K)
+    p = _take(lib, "gemm_gated", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
+              ("Z", Z, 2, nz, True), ("G", G, 4, nz, True), ("U", U, 4, nz, True))
+    st = lib.gemm_gated(d, a, *p, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated", lib.gemm_last_error().decode())
 
@@ -419,16 +445,14 @@ def gemm_gated(dtype: str, act: str, X, W_g, W_u, Z, G, U, M: int, N: int, K: in
 def gemm_gated_backward(dtype: str, act: str, X, W_g, W_u, G, U, dZ, dX, dW_g, dW_u, M: int, N: int, K: int) -> None:
     """Gradients of gemm_gated from dZ [M,N] and the G and U it stored: dX [M,K],
     dW_g and dW_u [K,N]; None leaves one out."""
-    lib = load()
+    lib = _lib or load()
     d, a = _gated_enums("gemm_gated_backward", dtype, act)
     M, N, K = int(M), int(N), int(K)
     nx, nw, nz = (M * K, K * N, M * N) if min(M, N, K) >= 0 else (0, 0, 0)
-    _check_all("gemm_gated_backward", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
-               ("G", G, 4, nz, True), ("U", U, 4, nz, True), ("dZ", dZ, 2, nz, True), ("dX", dX, 2, nx, True),
-               ("dW_g", dW_g, 2, nw, True), ("dW_u", dW_u, 2, nw, True))
-    _bind_torch_stream(X, W_g, W_u, G, U, dZ, dX, dW_g, dW_u)
-    st = lib.gemm_gated_backward(d, a, _addr(X), _addr(W_g), _addr(W_u), _addr(G), _addr(U), _addr(dZ), _addr(dX),
-                                 _addr(dW_g), _addr(dW_u), M, N, K)
+    p = _take(lib, "gemm_gated_backward", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
+              ("G", G, 4, nz, True), ("U", U, 4, nz, True), ("dZ", dZ, 2, nz, True), ("dX", dX, 2, nx, True),
+              ("dW_g", dW_g, 2, nw, True), ("dW_u", dW_u, 2, nw, True))
+    st = lib.gemm_gated_backward(d, a, *p, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated_backward", lib.gemm_last_error().decode())
 
