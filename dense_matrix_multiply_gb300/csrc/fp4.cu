@@ -138,7 +138,7 @@ fp4_dequantize_kernel(const uint8_t *__restrict__ Q, const uint8_t *__restrict__
                 T *a = a_row + i * lda + k;
                 float2 v[4];
                 uint32_t o[4];
-                int first = 0, left = (int)((uint32_t)K - k);  // of the eight values, those in the row
+                int first = 0, left = min((int)((uint32_t)K - k), 16);  // of the eight values, those in the row
                 if constexpr (VEC) {
                     fp4_unpack8(codes[i][h], v);
 #pragma unroll

@@ -419,7 +419,11 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             // other has nothing to read before the next tile's MMAs, but has finished
             // the tile before this one.
             const bool shares = wide && half == (buf ^ 1);
-            if (wide && !shares && lane == 0) mbar_arrive_cluster(empty);
+            if (wide && !shares) {
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(empty);
+            }
             RowStore out = {box, args.ldc * 2, M - row0, nullptr, 0u};
             for (int i = 0; i < groups; ++i) {
                 const int g = first + (shares && buf == 0 ? i ^ 2 : i);
