@@ -1,5 +1,5 @@
-// Gated feed-forward block: launchers (gated.cu, gated_skinny.cu) and the
-// activations they share.
+// Gated feed-forward block: launchers (gated.cu, gated_skinny.cu, gated_pad.cu) and
+// the activations they share.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,6 +29,11 @@ struct GatedBackward {
     Elt elt;
     bool gelu;
 };
+// Any N, K >= 1 and alignment of elements (gated_pad.cu); the launchers below need
+// N and K to be multiples of 8 and every base on 16 bytes.
+cudaError_t launch_gated_forward(const GatedProblem &p, int num_sms, int *status, cudaStream_t s);
+cudaError_t launch_gated_gradients(const GatedBackward &p, int num_sms, int *status, cudaStream_t s);
+
 cudaError_t launch_gated(const GatedProblem &p, int *status, cudaStream_t s);            // any M
 constexpr int kGatedSkinnyMaxM = 64;
 cudaError_t launch_gated_skinny(const GatedProblem &p, int num_sms, int *status, cudaStream_t s);

@@ -419,6 +419,17 @@ gemm_status_t run_ex(int dtype, int layout, int op_a, int op_b, int M, int N, in
     return finish(launch_simt_ex(p, s), simt_name);
 }
 
+// 16-bit operands on 2 bytes, FP32 ones on 4: the kernels load whole elements.
+bool elements_aligned(const char *who, std::initializer_list<const void *> halves,
+                      std::initializer_list<const void *> floats) {
+    uintptr_t h = 0, f = 0;
+    for (const void *p : halves) h |= (uintptr_t)p;
+    for (const void *p : floats) f |= (uintptr_t)p;
+    if ((h & 1) == 0 && (f & 3) == 0) return true;
+    snprintf(t_last_error, sizeof(t_last_error), "%s: needs 16-bit operands on 2 bytes and FP32 ones on 4", who);
+    return false;
+}
+
 // ------------------------------------------------------------ 4-bit block scales
 // What the four entry points share: types, format, and the codes' and scales'
 // sizes of a [rows, K] matrix (0 where nothing is stored).
@@ -431,7 +442,7 @@ size_t fp4_code_size(int rows, int K) { return K > 0 ? (size_t)rows * fp4_row_by
 // Checks of a quantised operand: codes and scales present and 16-byte aligned,
 // a tensor scale only where the format has one.
 bool fp4_operand_ok(const char *who, int format, const void *Q, const void *S, const float *g) {
-    if (!Q || !S) return false;
+    if (!Q || !S || !elements_aligned(who, {}, {g})) return false;
     if (!aligned16(Q) || !aligned16(S)) {
         snprintf(t_last_error, sizeof(t_last_error), "%s: codes and scales need 16-byte alignment", who);
         return false;
@@ -448,7 +459,7 @@ gemm_status_t run_fp4_convert(const char *who, bool to_codes, int dtype, int for
                               const float *g, const void *Q, const void *S, int M, int K) {
     if (!fp4_types_ok(dtype, format) || M < 0 || K < 0 || lda < (K > 1 ? K : 1)) return GEMM_ERR_INVALID_VALUE;
     if (M == 0 || K == 0) { t_last_kernel = "noop"; return GEMM_OK; }
-    if (!A || !fp4_operand_ok(who, format, Q, S, g)) return GEMM_ERR_INVALID_VALUE;
+    if (!A || !fp4_operand_ok(who, format, Q, S, g) || !elements_aligned(who, {A}, {})) return GEMM_ERR_INVALID_VALUE;
     const bool nv = format == GEMM_FP4_NV;
     long long span = 0;
     if (!span_elems(1, 0, M, lda, K, &span) || span > (1LL << 61)) return GEMM_ERR_INVALID_VALUE;
@@ -474,7 +485,7 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     if (!fp4_types_ok(dtype, format) || M < 0 || N < 0 || K < 0 || ldc < (N > 1 ? N : 1)) return GEMM_ERR_INVALID_VALUE;
     if (linear && ldx < (K > 1 ? K : 1)) return GEMM_ERR_INVALID_VALUE;
     if (M == 0 || N == 0) { t_last_kernel = "noop"; return GEMM_OK; }
-    if (!C) return GEMM_ERR_INVALID_VALUE;
+    if (!C || !elements_aligned(who, {C, X}, {ga})) return GEMM_ERR_INVALID_VALUE;
     const bool nv = format == GEMM_FP4_NV;
     const Elt elt = elt16(dtype);
     long long span = 0, x_span = 0;
@@ -548,13 +559,10 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
 }
 
 // ------------------------------------------------------------ gated block
-bool gated_args_ok(const char *who, int dtype, int act, int M, int N, int K, std::initializer_list<const void *> ptrs) {
+bool gated_args_ok(const char *who, int dtype, int act, int M, int N, int K, std::initializer_list<const void *> halves,
+                   std::initializer_list<const void *> floats) {
     if ((dtype != GEMM_F16 && dtype != GEMM_BF16) || (act != GEMM_ACT_SILU && act != GEMM_ACT_GELU_TANH)) return false;
-    if (M < 0 || N < 0 || K < 0) return false;
-    bool ok = N % 8 == 0 && K % 8 == 0;
-    for (const void *p : ptrs) ok = ok && aligned16(p);
-    if (!ok) snprintf(t_last_error, sizeof(t_last_error), "%s: needs every pointer 16-byte aligned and N, K multiples of 8", who);
-    return ok;
+    return M >= 0 && N >= 0 && K >= 0 && elements_aligned(who, halves, floats);
 }
 struct Span {
     const void *p;
@@ -575,7 +583,7 @@ cudaError_t zero(const Span &s, cudaStream_t st, cudaError_t e) {
 
 gemm_status_t run_gated(int dtype, int act, const void *X, const void *Wg, const void *Wu, void *Z, float *G, float *U,
                         int M, int N, int K) {
-    if (!gated_args_ok("gemm_gated", dtype, act, M, N, K, {X, Wg, Wu, Z, G, U})) return GEMM_ERR_INVALID_VALUE;
+    if (!gated_args_ok("gemm_gated", dtype, act, M, N, K, {X, Wg, Wu, Z}, {G, U})) return GEMM_ERR_INVALID_VALUE;
     if (M == 0 || N == 0) { t_last_kernel = "noop"; return GEMM_OK; }
     if (!Z || (K > 0 && (!X || !Wg || !Wu)) || !G != !U) return GEMM_ERR_INVALID_VALUE;
     const size_t mn = (size_t)M * N, x = (size_t)M * K * 2, w = (size_t)K * N * 2;
@@ -588,13 +596,12 @@ gemm_status_t run_gated(int dtype, int act, const void *X, const void *Wg, const
     if (K == 0)  // G = U = 0, and act(0) * 0 = 0
         return finish(zero(us, s, zero(gs, s, zero(z, s, cudaSuccess))), "zero_fill");
     const GatedProblem p{X, Wg, Wu, Z, G, U, M, N, K, elt16(dtype), act == GEMM_ACT_GELU_TANH};
-    if (M <= kGatedSkinnyMaxM) return finish(launch_gated_skinny(p, dev->num_sms, dev->status, s), "gated_skinny");
-    return finish(launch_gated(p, dev->status, s), "gated_pair");
+    return finish(launch_gated_forward(p, dev->num_sms, dev->status, s), M <= kGatedSkinnyMaxM ? "gated_skinny" : "gated_pair");
 }
 
 gemm_status_t run_gated_backward(int dtype, int act, const void *X, const void *Wg, const void *Wu, const float *G,
                                  const float *U, const void *dZ, void *dX, void *dWg, void *dWu, int M, int N, int K) {
-    if (!gated_args_ok("gemm_gated_backward", dtype, act, M, N, K, {X, Wg, Wu, G, U, dZ, dX, dWg, dWu}))
+    if (!gated_args_ok("gemm_gated_backward", dtype, act, M, N, K, {X, Wg, Wu, dZ, dX, dWg, dWu}, {G, U}))
         return GEMM_ERR_INVALID_VALUE;
     if (K == 0 || (!dX && !dWg && !dWu)) { t_last_kernel = "noop"; return GEMM_OK; }
     const size_t mn = (size_t)M * N, x = (size_t)M * K * 2, w = (size_t)K * N * 2;
@@ -610,7 +617,7 @@ gemm_status_t run_gated_backward(int dtype, int act, const void *X, const void *
     if (!work)  // empty sums: no rows (dW), no hidden units (dX)
         return finish(zero(ou, s, zero(og, s, zero(ox, s, cudaSuccess))), "zero_fill");
     const GatedBackward p{X, Wg, Wu, dZ, G, U, dX, dWg, dWu, M, N, K, elt16(dtype), act == GEMM_ACT_GELU_TANH};
-    return finish(launch_gated_backward(p, dev->num_sms, dev->status, s), "gated_backward");
+    return finish(launch_gated_gradients(p, dev->num_sms, dev->status, s), "gated_backward");
 }
 
 }  // namespace

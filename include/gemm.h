@@ -50,7 +50,8 @@
  * of tiles is at most half full launches two grids; the second reads A and B
  * while the first still runs, and completes only after it; so do the two
  * products of gemm_gated_backward.)  A call launches one to five kernels, or
- * more for a general-form batch beyond 65535 matrices;
+ * more for a general-form batch beyond 65535 matrices and for a gated block's
+ * operands that are padded;
  * gemm_kernel_launches() counts them.  Calls may be captured into CUDA
  * graphs.  Results are deterministic: the same inputs give bit-identical C on
  * every run (no atomics, fixed summation order per element).
@@ -275,8 +276,8 @@ GEMM_API gemm_status_t gemm_e4m3_rowscale_fused(const uint16_t *A, const uint8_t
  * -- the order in which the tensor cores take them.  gemm_fp4_code_bytes and
  * gemm_fp4_scale_bytes give the sizes (-1 for a negative size or an unknown
  * format).  Codes and scales need 16-byte alignment (GEMM_ERR_INVALID_VALUE
- * otherwise, with a message in gemm_last_error); everything else may have any
- * alignment and any K, M, N.
+ * otherwise, with a message in gemm_last_error); everything else its elements'
+ * alignment, and any K, M, N.
  *
  * For a block with the largest magnitude amax, a / step rounded to the nearest
  * code (ties to the even code, saturating at 6), in FP32 operations:
@@ -331,10 +332,10 @@ GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t for
  * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2.  G and U (both or neither):
  * FP32 [M,N], stored for gemm_gated_backward.  (gemm_bf16_rm_silu_mul keeps the
  * rounding points of the unfused chain instead: G, U and act(G) rounded to bf16.)
- * M may be any size: one token to a long prompt.  Needs every pointer 16-byte
- * aligned and N, K multiples of 8 (GEMM_ERR_INVALID_VALUE otherwise, with a
- * message in gemm_last_error).  K = 0 gives zeros.  GEMM_ERR_ALIAS if an output
- * overlaps an input or another output. */
+ * Any M, N, K: one token to a long prompt.  Operands that are not 16-byte aligned,
+ * or whose N or K is no multiple of 8, are copied to or from padded rows in
+ * stream-ordered scratch, which costs a pass over each of them.  K = 0 gives
+ * zeros.  GEMM_ERR_ALIAS if an output overlaps an input or another output. */
 typedef enum gemm_act_t { GEMM_ACT_SILU = 0, GEMM_ACT_GELU_TANH = 1 } gemm_act_t;
 
 GEMM_API gemm_status_t gemm_gated(gemm_dtype_t dtype, gemm_act_t act, const void *X, const void *W_g, const void *W_u,

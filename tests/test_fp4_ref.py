@@ -75,16 +75,20 @@ def test_host_side_errors(built):
     assert q(2, 1, A, 64, G, Q + 8, S, 4, 64) == 1               # alignment
     assert q(2, 1, A, 64, G, A + 16, S, 4, 64) == 2 and q(2, 1, A, 64, S + 16, Q, S, 4, 64) == 2
     assert q(2, 1, A, 64, G, Q, S, 0, 64) == 0 and q(2, 1, A, 64, G, Q, S, 4, 0) == 0
+    assert q(2, 1, A + 1, 64, G, Q, S, 4, 64) == 1 and q(2, 1, A, 64, G + 2, Q, S, 4, 64) == 1
+    assert b"on 4" in built.gemm_last_error()
     d = built.gemm_fp4_dequantize
     assert d(2, 1, Q, S, G, None, 64, 4, 64) == 1 and d(2, 1, Q, S, G, Q, 64, 4, 64) == 2
     assert d(2, 1, Q, S, A + 4, A, 64, 4, 64) == 2               # the scale inside the output
     f = built.gemm_fp4
+    assert f(2, 1, Q, S, G, Q, S, G, C + 1, 4, 4, 4, 64) == 1 and f(2, 1, Q, S, G, Q, S, G + 1, C, 4, 4, 4, 64) == 1
     assert f(2, 1, Q, S, G, Q, S, G, C, 3, 4, 4, 64) == 1        # ldc
     assert f(2, 1, Q, S, G, Q, S, G, None, 4, 4, 4, 64) == 1 and f(2, 1, Q, None, G, Q, S, G, C, 4, 4, 4, 64) == 1
     assert f(2, 1, Q, S, G, Q, S, G, S, 4, 4, 4, 64) == 2 and f(2, 1, Q, S, C, Q, S, G, C, 4, 4, 4, 64) == 2
     assert f(2, 0, Q, S, G, Q, S, None, C, 4, 4, 4, 64) == 1
     assert f(2, 1, Q, S, G, Q, S, G, C, 4, 0, 4, 64) == 0
     li = built.gemm_fp4_linear
+    assert li(2, 1, A + 1, 64, G, Q, S, G, C, 4, 4, 4, 64) == 1 and li(2, 1, A, 64, G + 2, Q, S, G, C, 4, 4, 4, 64) == 1
     assert li(2, 1, A, 63, G, Q, S, G, C, 4, 4, 4, 64) == 1 and li(2, 1, None, 64, G, Q, S, G, C, 4, 4, 4, 64) == 1
     assert li(2, 1, A, 64, G, Q, S, G, A + 8, 4, 4, 4, 64) == 2
     with pytest.raises(ValueError):

@@ -52,16 +52,16 @@ def test_host_side_errors(built):
     f = built.gemm_gated
     ok = dict(d=2, a=0, X=X, Wg=Wg, Wu=Wu, Z=Z, G=None, U=None, M=4, N=16, K=8)
     call = lambda **k: f(*{**ok, **k}.values())
-    assert call(d=0) == 1 and call(a=2) == 1 and call(M=-1) == 1 and call(N=12) == 1 and call(K=4) == 1
-    assert b"multiples of 8" in built.gemm_last_error()
-    assert call(X=X + 8) == 1 and call(Z=None) == 1 and call(Wu=None) == 1
+    assert call(d=0) == 1 and call(a=2) == 1 and call(M=-1) == 1 and call(N=-8) == 1 and call(K=-4) == 1
+    assert call(G=G + 2, U=U) == 1 and b"on 4" in built.gemm_last_error()
+    assert call(X=X + 1) == 1 and call(Z=None) == 1 and call(Wu=None) == 1
     assert call(G=G) == 1                        # G without U
     assert call(Z=X + 16) == 2 and call(G=G, U=G + 64) == 2 and call(G=Z + 16, U=U) == 2
     assert call(M=0) == 0 and built.gemm_last_kernel() == b"noop"
     b = built.gemm_gated_backward
     okb = dict(d=2, a=1, X=X, Wg=Wg, Wu=Wu, G=G, U=U, dZ=dZ, dX=dX, dWg=dWg, dWu=dWu, M=4, N=16, K=8)
     callb = lambda **k: b(*{**okb, **k}.values())
-    assert callb(d=0) == 1 and callb(a=-1) == 1 and callb(K=-8) == 1 and callb(N=4) == 1
+    assert callb(d=0) == 1 and callb(a=-1) == 1 and callb(K=-8) == 1 and callb(dX=dX + 1) == 1 and callb(U=U + 2) == 1
     assert callb(G=None) == 1 and callb(dZ=None) == 1 and callb(Wg=None) == 1 and callb(X=None) == 1
     assert callb(dX=X) == 2 and callb(dWu=dWg + 16) == 2 and callb(dWg=G) == 2
     assert callb(dX=None, dWg=None, dWu=None) == 0 and callb(K=0) == 0

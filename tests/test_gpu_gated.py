@@ -99,6 +99,42 @@ def test_several_waves_of_tiles(M, N, K):
         close(got[name], want, tol, name)
 
 
+ODD = [(1, 1, 1), (1, 7, 5), (3, 9, 1000), (5, 1001, 8), (65, 129, 333), (64, 255, 33), (200, 1001, 137), (70, 8, 9),
+       (333, 1000, 1001)]
+
+
+@pytest.mark.parametrize("act,dtype", [("silu", "bf16"), ("gelu", "f16")])
+@pytest.mark.parametrize("M,N,K", ODD)
+def test_sizes_that_are_no_multiples_of_8(M, N, K, dtype, act):
+    """Operands through padded copies: the same tolerances, nothing written past the outputs."""
+    test_forward_and_backward(M, N, K, dtype, act)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 72, 40), (100, 264, 128), (100, 263, 127)])
+def test_operands_off_16_bytes(M, N, K):
+    """Every operand one element past an aligned base: the results of the aligned call, bit for bit."""
+    t, _ = make(M, N, K, "bf16", 12)
+    want = run("bf16", "gelu", t, M, N, K)
+
+    def off(rows, cols, dt=torch.bfloat16, x=None):
+        b = torch.full((rows * cols + 64,), FILL, dtype=dt, device="cuda")
+        v = b[1:1 + rows * cols]
+        if x is not None:
+            v.copy_(x.reshape(-1))
+        return b, v
+
+    X, Wg, Wu, dZ = (off(*x.shape, x=x)[1] for x in t)
+    outs = {n: off(r, c, d) for n, r, c, d in (("Z", M, N, X.dtype), ("G", M, N, torch.float32), ("U", M, N, torch.float32),
+                                              ("dX", M, K, X.dtype), ("dWg", K, N, X.dtype), ("dWu", K, N, X.dtype))}
+    o = {n: v for n, (_, v) in outs.items()}
+    g.gemm_gated("bf16", "gelu", X, Wg, Wu, o["Z"], o["G"], o["U"], M, N, K)
+    g.gemm_gated_backward("bf16", "gelu", X, Wg, Wu, o["G"], o["U"], dZ, o["dX"], o["dWg"], o["dWu"], M, N, K)
+    g.gemm_synchronize()
+    for n, (b, v) in outs.items():
+        assert b[0] == FILL and (b[1 + v.numel():] == FILL).all(), n
+        assert np.array_equal(v.double().cpu().numpy(), want[n].reshape(-1)), n
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 72, 40), (200, 264, 128)])
 def test_without_saving_gives_the_same_z(M, N, K):
     t, _ = make(M, N, K, "bf16", 5)
