@@ -50,6 +50,10 @@ __host__ __device__ constexpr int stages_of(bool nv, int nb) {
     return RING / stage_bytes(nv, nb) < MAX_STAGES ? RING / stage_bytes(nv, nb) : MAX_STAGES;
 }
 
+// FUSED: converting warp j mod 4 at use j of the ring has seen every use up to j - 4 -
+// stages done, and its wait on one bit of phase needs j - 2 stages.
+static_assert(RING / stage_bytes(true, 16) >= 4 && RING / stage_bytes(false, 16) >= 4, "stages of the fused form");
+
 struct Bars {
     uint64_t full[MAX_STAGES];
     uint64_t empty[MAX_STAGES];
@@ -235,15 +239,15 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             const int half = lane >> 4, u = lane & 15;
             const T *X = static_cast<const T *>(args.X);
             auto load = [&](int kb, int r, uint32_t (&v)[8]) {
-                const int k = kb * KB + u * 16;
+                const long long k = (long long)kb * KB + u * 16;
                 if (r >= M || k >= K) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] = 0u;
                     return;
                 }
                 const T *x = X + (long long)r * args.ldx + k;
-                if (args.x_vec) fp4_load16<16>(x, K - k, v);
-                else fp4_load16<2>(x, K - k, v);
+                if (args.x_vec) fp4_load16<16>(x, (int)(K - k), v);
+                else fp4_load16<2>(x, (int)(K - k), v);
             };
             int slot = warp - 2;
             uint32_t phase = 0;
