@@ -204,7 +204,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     // complete by then, and dX (args.beside) begins at once, on the SMs that dW
     // leaves, and waits for dW before it ends, so that whatever follows finds both.
     // Backward of 1024 x 12288 x 4096 270 us against 282 one after the other, 128 x
-    // 12288 x 4096 108 against 114, 333 x 1000 x 1000 20.6 against 22.3.
+    // 12288 x 4096 108 against 114, 333 x 1000 x 1000 15.6 against 22.3.
     if (MODE == DW) {
         pdl_wait();
         pdl_launch_dependents();
@@ -649,19 +649,29 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     if (cmax <= 0 || wmax <= 0) return cudaErrorNotSupported;
     const long long mn = (long long)p.M * p.N;
     const bool pair_dx = p.dX && p.M > kGatedSkinnyMaxM, both = p.dWg && p.dWu;
-    // dX: the tile width with the shortest plan, widest on ties; a K block of a
-    // narrower tile takes little less time (the operand feed).
+    const Plan pw = plan((p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1), wmax, (p.M + BK - 1LL) / BK);
+    // (where dW's tiles are split, a kernel that adds them lies between, and the
+    // partials' scratch is shared)
+    const bool beside = pair_dx && g_pdl && (p.dWg || p.dWu) && pw.splits == 1;
+    // dX: the tile width and plan that are done first, widest on ties; a K block of a
+    // narrower tile takes little less time (the operand feed).  Beside dW, a plan may
+    // keep to the clusters that dW leaves; one that needs more waits for dW, its
+    // blocks and about 12 blocks' time of set-up and writing (backward of 333 x 1000
+    // x 1000 15.6 us, with dX's plan for all clusters 20.5; 500 x 1504 x 704 15.7 and 20.3).
     const long long tiles_m = (p.M + 255LL) / 256;
-    const int half = (p.N + BK - 1) / BK;
+    const int half = (p.N + BK - 1) / BK, left = beside ? std::max(cmax - pw.clusters, 0) : cmax;
     int bn = 0;
     Plan px = {};
     long long best = 0;
     for (int c = 256; c >= 128; c -= 64) {
-        const Plan q = plan(tiles_m * ((p.K + c - 1LL) / c), cmax, 2LL * half);
-        const long long cost = q.blocks * (c > 224 ? c : 224);
-        if (bn == 0 || cost < best) { bn = c; px = q; best = cost; }
+        const long long tiles = tiles_m * ((p.K + c - 1LL) / c);
+        for (int clusters : {cmax, left}) {
+            if (clusters == 0) continue;
+            const Plan q = plan(tiles, clusters, 2LL * half);
+            const long long cost = q.blocks * (c > 224 ? c : 224) + (q.clusters > left ? (pw.blocks + 12) * 256 : 0);
+            if (bn == 0 || cost < best) { bn = c; px = q; best = cost; }
+        }
     }
-    const Plan pw = plan((p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1), wmax, (p.M + BK - 1LL) / BK);
     if (px.tiles > 0x7FFFFFFFLL || pw.tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     // scratch: dG and dU, and the partials of the two products, one after the other
     const size_t off = ((size_t)mn * 4 + 1023) & ~(size_t)1023;
@@ -714,9 +724,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
             a.kb_half = half;
             a.bn = bn;
             a.batch = 1;
-            // (where dW's tiles are split, a kernel that adds them lies between, and
-            // the partials' scratch is shared)
-            a.beside = g_pdl && (p.dWg || p.dWu) && pw.splits == 1;
+            a.beside = beside;
             a.status = status;
             T *out = static_cast<T *>(p.dX);
             e = launch_pair<T, FORMAT, DX, false>(ta, tb, tb2, tc, tc, tc, a, px, part, out, out, nullptr, nullptr, s);
