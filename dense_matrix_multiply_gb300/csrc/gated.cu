@@ -7,7 +7,8 @@
 // (tcgen05 cta_group::2); per K step of 64 CTA r loads 64 columns of Wg and the
 // same 64 of Wu side by side, so that one N = 256 MMA gives G and U for the same
 // columns of Z in one accumulator, and the epilogue forms Z from the FP32 sums,
-// rounded once.  For training it also stores G and U, in FP32: a 16-bit copy would
+// rounded once.  (Few tiles: 256 x 64 ones, for which CTA 0 loads Wg's columns and
+// CTA 1 Wu's, N = 128.)  For training it also stores G and U, in FP32: a 16-bit copy would
 // put a third rounding beside those of dG and dU and of the result on every
 // gradient (1.7 times the error of the result's rounding, against 1.4).
 //
@@ -79,7 +80,7 @@ struct Args {
     int M, N;     // of the output: Z, dX or a dW
     int num_kb;   // K blocks of 64 (DX: of both halves together)
     int kb_half;  // DX: blocks of the first half
-    int bn;       // the tile's N extent: FWD 128; DX 128, 192 or 256; DW 256
+    int bn;       // the tile's N extent: FWD 128 or 64; DX 128, 192 or 256; DW 256
     int batch;    // DW: outputs, 1 or 2; else 1
     int save;     // FWD: store G and U
     int whole;    // tiles computed whole; the rest are split
@@ -174,7 +175,8 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
     const int tiles_m = (M + 255) / 256, tiles_n = (N + bn - 1) / bn;
     const int tiles = tiles_m * tiles_n * args.batch;
-    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (MODE == DX ? (bn >> 1) * 128 : 2 * BOX64));
+    const bool thin = MODE == FWD && bn == 64;
+    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (MODE == DX ? (bn >> 1) * 128 : thin ? BOX64 : 2 * BOX64));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -233,8 +235,12 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
                     if (MODE == FWD) {
                         tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
-                        tma_load_3d_pair(b, &tmB, full, col0, kb * BK, 0);
-                        tma_load_3d_pair(b + BOX64, &tmB2, full, col0, kb * BK, 0);
+                        if (thin) {
+                            tma_load_3d_pair(b, leader ? &tmB : &tmB2, full, t.n * 64, kb * BK, 0);
+                        } else {
+                            tma_load_3d_pair(b, &tmB, full, col0, kb * BK, 0);
+                            tma_load_3d_pair(b + BOX64, &tmB2, full, col0, kb * BK, 0);
+                        }
                     } else if (MODE == DW) {
                         tma_load_3d_pair(a, &tmA, full, row0, kb * BK, 0);
                         tma_load_3d_pair(a + BOX64, &tmA, full, row0 + 64, kb * BK, 0);
@@ -286,7 +292,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         // K-major: a K step of 16 is 32 bytes of a 128-byte row.  MN-major: 16 rows of
         // 128 bytes, 64-element boxes BOX64 bytes apart.
         constexpr bool a_mn = MODE == DW, b_mn = MODE != DX;
-        const uint32_t idesc = make_idesc(FORMAT, MODE == DX ? (uint32_t)bn : 256u, a_mn, b_mn);
+        const uint32_t idesc = make_idesc(FORMAT, MODE == DX ? (uint32_t)bn : thin ? 128u : 256u, a_mn, b_mn);
         const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), a_mn ? BOX64 : 16, 1024);
         const uint64_t b_desc0 = desc_sw128(smem_u32(b_tiles), b_mn ? BOX64 : 16, 1024);
         constexpr uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
@@ -360,7 +366,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             const uint32_t t_row = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
             if (w.slab >= 0) {
                 // a partial: the accumulators as they are
-                const int chunks = (MODE == FWD ? 256 : bn) / 32, mid = (chunks + 1) >> 1;
+                const int chunks = (MODE == FWD ? 2 * bn : bn) / 32, mid = (chunks + 1) >> 1;
 #pragma unroll 1
                 for (int c = half ? mid : 0; c < (half ? chunks : mid); ++c) {
                     uint32_t r[32];
@@ -371,6 +377,35 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     fence_async_shared();
                     __syncwarp();
                     if (lane == 0 && row0 < M) tma_store_3d(&tmP, b, c * 32, (int)rank * 128 + quarter * 32, w.slab);
+                }
+            } else if (thin) {
+                // columns 0-63: G, 64-127: U; 32 of them to each half
+                const int c0 = t.n * 64 + half * 32;
+                if (c0 < N) {  // warp-uniform
+                    uint32_t rg[32], ru[32];
+                    tmem_ld32(t_row + (uint32_t)(half * 32), rg);
+                    tmem_ld32(t_row + (uint32_t)(64 + half * 32), ru);
+                    tmem_ld_wait();
+                    if (args.save) {
+                        uint8_t *b = box_begin();
+                        box_put_f32(b, lane, rg);
+                        box_end(&tmG, b, c0, row0, 0);
+                        b = box_begin();
+                        box_put_f32(b, lane, ru);
+                        box_end(&tmU, b, c0, row0, 0);
+                    }
+                    uint32_t z[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        z[j] = pack2(gate_act<GELU>(__uint_as_float(rg[2 * j])) * __uint_as_float(ru[2 * j]),
+                                     gate_act<GELU>(__uint_as_float(rg[2 * j + 1])) * __uint_as_float(ru[2 * j + 1]),
+                                     (T *)nullptr);
+                    uint8_t *b = box_begin();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)  // 64 bytes a row, the 64-byte swizzle
+                        *reinterpret_cast<uint4 *>(b + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(z[4 * c], z[4 * c + 1], z[4 * c + 2], z[4 * c + 3]);
+                    box_end(&tmC, b, c0, row0, 0);
                 }
             } else if constexpr (MODE == FWD) {
                 // accumulator columns 128 g + j: G, 128 g + 64 + j: U of Z's column 64 g + j
@@ -553,21 +588,31 @@ bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long 
 }
 
 // How the tiles go to the clusters.  Whole waves of tiles first; the rest is split
-// when that saves more than the partials and the second kernel cost: a K block
-// takes 0.3 us, they about 5 us (17 blocks); a split is eight blocks at least.
-// Measured, forward: 1024 x 12288 x 4096 (384 tiles on 76 clusters) 112 us against
-// 120 with whole tiles, 128 x 12288 x 4096 (96 tiles) 46.8 against 51.8.
+// when that saves more than the partials and the second kernel cost; a split is
+// eight blocks at least.  Times are in 256ths of a K block of a 256 x 256
+// accumulator, 0.3 us; `block` is one of this tile's.  Measured, forward: 1024 x 12288 x
+// 4096 (384 tiles on 76 clusters) 112 us against 120 with whole tiles, 128 x 12288 x
+// 4096 (96 tiles) 46.8 against 51.8; dX of 777 x 11008 x 4096 in 64 whole tiles
+// 113 us, in 76 of 192 columns and 12 split in six 120.
+constexpr long long fix_time(long long slabs) { return 10 * 256 + slabs * 51; }  // 3 us and 0.06 a partial
+// Blocks of narrower accumulators: dX of 128 x 12288 x 4096 in one wave takes 0.27 us
+// a block at 256 columns, 0.22 at 192 and 0.205 at 128, forward 1024 x 12160 x 4096
+// 0.33 at 256 and 0.23 at 128.  Rows that do not start on 128 bytes: forward of 333 x
+// 1000 x 1000 12.4 us where 333 x 1024 x 1024 takes 9.5.
+constexpr int block_time(int columns, bool rows_on_128) {
+    return (columns == 256 ? 256 : columns == 192 ? 208 : 180) * (rows_on_128 ? 5 : 8) / 5;
+}
 struct Plan {
-    long long tiles, blocks;  // blocks: the longest cluster's, and 17 where tiles are split
+    long long tiles, time;
     int clusters, whole, splits;
 };
-Plan plan(long long tiles, int cmax, long long num_kb) {
+Plan plan(long long tiles, int cmax, long long num_kb, int block) {
     const long long waves = tiles / cmax, rem = tiles - waves * cmax;
-    Plan p = {tiles, (waves + (rem > 0)) * num_kb, (int)std::min<long long>(tiles, cmax), (int)tiles, 1};
+    Plan p = {tiles, (waves + (rem > 0)) * num_kb * block, (int)std::min<long long>(tiles, cmax), (int)tiles, 1};
     if (rem == 0) return p;
     const long long splits = std::min<long long>({cmax / rem, num_kb / 8, 16});
-    if (splits < 2 || num_kb - num_kb / splits < 17) return p;
-    p.blocks = waves * num_kb + num_kb / splits + 17;
+    if (splits < 2 || (num_kb - num_kb / splits) * block < fix_time(rem * splits)) return p;
+    p.time = (waves * num_kb + num_kb / splits) * block + fix_time(rem * splits);
     p.whole = (int)(waves * cmax);
     p.splits = (int)splits;
     p.clusters = waves > 0 ? cmax : (int)(rem * splits);
@@ -614,11 +659,23 @@ template <typename T, uint32_t FORMAT, bool GELU>
 cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s) {
     const int cmax = clusters_max<T, FORMAT, FWD, GELU>(dev);
     if (cmax <= 0) return cudaErrorNotSupported;
-    const long long tiles = (p.M + 255LL) / 256 * ((p.N + 127LL) / 128);
-    if (tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
+    const long long tiles_m = (p.M + 255LL) / 256;
+    const int num_kb = (p.K + BK - 1) / BK;
+    // 64-wide tiles where they are done first, as they are where 128-wide ones leave
+    // clusters idle (forward of 333 x 1000 x 1000 9.1 us against 12.4, 300 x 512 x 2048
+    // 8.4 against 11.8; 128 x 12288 x 4096 55 against 45, 1024 x 12160 x 4096 149
+    // against 107).
+    const bool on128 = p.N % 64 == 0 && p.K % 64 == 0;
+    Plan pl = plan(tiles_m * ((p.N + 127LL) / 128), cmax, num_kb, block_time(256, on128));
+    const Plan thin = plan(tiles_m * ((p.N + 63LL) / 64), cmax, num_kb, block_time(128, on128));
+    const int bn = thin.time < pl.time ? 64 : 128;
+    if (bn == 64) pl = thin;
+    if (pl.tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     CUtensorMap tx, tg, tu, tz, tsg, tsu;
+    const long long zr = 2LL * p.N;
     if (!map16(&tx, p.X, FORMAT, p.M, p.K, BK, 128) || !map16(&tg, p.Wg, FORMAT, p.K, p.N, 64, BK) ||
-        !map16(&tu, p.Wu, FORMAT, p.K, p.N, 64, BK) || !map16(&tz, p.Z, FORMAT, p.M, p.N, 64, 32))
+        !map16(&tu, p.Wu, FORMAT, p.K, p.N, 64, BK) ||
+        !make_map3(&tz, p.Z, map_type(FORMAT), p.N, p.M, 1, zr, zr * p.M, bn / 2, 32, 1, /*swizzle: a row's bytes*/ bn))
         return cudaErrorInvalidValue;
     tsg = tsu = tz;
     const long long row = 4LL * p.N;
@@ -628,12 +685,11 @@ cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s)
     Args a = {};
     a.M = p.M;
     a.N = p.N;
-    a.num_kb = (p.K + BK - 1) / BK;
-    a.bn = 128;
+    a.num_kb = num_kb;
+    a.bn = bn;
     a.batch = 1;
     a.save = p.G != nullptr;
     a.status = status;
-    const Plan pl = plan(tiles, cmax, a.num_kb);
     void *ws = nullptr;
     cudaError_t e = pl.splits > 1 ? scratch_alloc(&ws, plan_scratch(pl), s) : cudaSuccess;
     if (e != cudaSuccess) return e;
@@ -649,14 +705,14 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     if (cmax <= 0 || wmax <= 0) return cudaErrorNotSupported;
     const long long mn = (long long)p.M * p.N;
     const bool pair_dx = p.dX && p.M > kGatedSkinnyMaxM, both = p.dWg && p.dWu;
-    const Plan pw = plan((p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1), wmax, (p.M + BK - 1LL) / BK);
+    const Plan pw = plan((p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1), wmax, (p.M + BK - 1LL) / BK,
+                         block_time(256, p.N % 64 == 0 && p.K % 64 == 0));
     // (where dW's tiles are split, a kernel that adds them lies between, and the
     // partials' scratch is shared)
     const bool beside = pair_dx && g_pdl && (p.dWg || p.dWu) && pw.splits == 1;
-    // dX: the tile width and plan that are done first, widest on ties; a K block of a
-    // narrower tile takes little less time (the operand feed).  Beside dW, a plan may
-    // keep to the clusters that dW leaves; one that needs more waits for dW, its
-    // blocks and about 12 blocks' time of set-up and writing (backward of 333 x 1000
+    // dX: the tile width and plan that are done first, widest on ties.  Beside dW, a
+    // plan may keep to the clusters that dW leaves; one that needs more waits for dW,
+    // its blocks and about 12 blocks' time of set-up and writing (backward of 333 x 1000
     // x 1000 15.6 us, with dX's plan for all clusters 20.5; 500 x 1504 x 704 15.7 and 20.3).
     const long long tiles_m = (p.M + 255LL) / 256;
     const int half = (p.N + BK - 1) / BK, left = beside ? std::max(cmax - pw.clusters, 0) : cmax;
@@ -667,9 +723,9 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
         const long long tiles = tiles_m * ((p.K + c - 1LL) / c);
         for (int clusters : {cmax, left}) {
             if (clusters == 0) continue;
-            const Plan q = plan(tiles, clusters, 2LL * half);
-            const long long cost = q.blocks * (c > 224 ? c : 224) + (q.clusters > left ? (pw.blocks + 12) * 256 : 0);
-            if (bn == 0 || cost < best) { bn = c; px = q; best = cost; }
+            const Plan q = plan(tiles, clusters, 2LL * half, block_time(c, p.N % 64 == 0));
+            const long long time = q.time + (q.clusters > left ? pw.time + 12 * 256 : 0);
+            if (bn == 0 || time < best) { bn = c; px = q; best = time; }
         }
     }
     if (px.tiles > 0x7FFFFFFFLL || pw.tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;

@@ -85,11 +85,13 @@ def test_forward_and_backward(M, N, K, dtype, act):
         close(got[name], want, tol, name)
 
 
-@pytest.mark.parametrize("M,N,K", [(600, 5000, 264), (5000, 64, 2056), (512, 5120, 1600), (900, 1000, 1792)])
+@pytest.mark.parametrize("M,N,K", [(600, 5000, 264), (5000, 64, 2056), (512, 5120, 1600), (900, 1000, 1792), (100, 72, 8200),
+                                   (800, 700, 136)])
 def test_several_waves_of_tiles(M, N, K):
     """More tiles than clusters, forward and dW, then dX: every buffer of the
     kernels is used again and again.  The third: four tiles past a whole wave,
-    split along K.  The last: dX beside dW, on the few clusters that it leaves."""
+    split along K.  The fourth: dX beside dW, on the few clusters that it
+    leaves.  The last two: forward in 64-wide tiles, split along K and whole."""
     t, (X, Wg, Wu, dZ) = make(M, N, K, "bf16", 11)
     got = run("bf16", "silu", t, M, N, K)
     for name, want, tol in zip("ZGU", ref.forward("silu", X, Wg, Wu), ref.forward_tolerance("silu", X, Wg, Wu, "bf16")):
