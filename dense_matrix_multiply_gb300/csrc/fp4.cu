@@ -38,7 +38,7 @@ constexpr int WARPS = 4, ROWS = 2;
 template <typename T, bool NV, int VEC>
 __global__ void __launch_bounds__(WARPS * 32)
 fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restrict__ tensor_scale,
-                    uint8_t *__restrict__ Q, uint8_t *__restrict__ S, int M, int K)
+                    uint8_t *__restrict__ Q, long long pitch, uint8_t *__restrict__ S, int M, int K)
 {
     // The product that reads these codes may set up, and bring its first weights to
     // L2, meanwhile: linear layer of 32 x 4096 x 12288 (MX) 11.6 us from 12.9, 1024 x
@@ -53,7 +53,7 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
     const T *a_row = A + row0 * lda;
     const uint8_t *lo = reinterpret_cast<const uint8_t *>(A),
                   *hi = reinterpret_cast<const uint8_t *>(A + (M - 1) * lda + K);
-    uint8_t *q_row = Q + (long long)row0 * rb;
+    uint8_t *q_row = Q + row0 * pitch;
     uint8_t *s_row = S + fp4_scale_at(row0, 0, (int)atoms);  // ROWS divides 32: rows 16 bytes apart
     static_assert(32 % ROWS == 0, "rows of one group of 32");
     for (uint32_t k = blockIdx.y * 512 + lane * 16; k - lane * 16 < (uint32_t)K; k += gridDim.y * 512) {
@@ -80,7 +80,7 @@ fp4_quantize_kernel(const T *__restrict__ A, long long lda, const float *__restr
             byte |= __shfl_down_sync(0xffffffffu, byte, 2 * SPAN) << 16;
             if (lane % (4 * SPAN) == 0 && a < atoms)
                 *reinterpret_cast<uint32_t *>(s_row + (size_t)a * 512 + i * 16) = byte;
-            if (row0 + i < M && k / 2 < rb) *reinterpret_cast<uint2 *>(q_row + (size_t)i * rb + k / 2) = codes;
+            if (row0 + i < M && k / 2 < rb) *reinterpret_cast<uint2 *>(q_row + i * pitch + k / 2) = codes;
         }
     }
 }
@@ -184,12 +184,13 @@ dim3 grid_of(long long rows, int K) {
 }
 
 template <typename T, bool NV>
-cudaError_t quantize(const void *A, long long lda, const float *g, void *Q, void *S, int M, int K, cudaStream_t s) {
+cudaError_t quantize(const void *A, long long lda, const float *g, void *Q, long long pitch, void *S, int M, int K,
+                     cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pdl_config(grid_of(fp4_row_tiles(M) * 128, K), dim3(WARPS * 32), 0, s, attr);
     auto go = [&](auto kern) {
         return launch_counted(&cfg, kern, static_cast<const T *>(A), lda, g, static_cast<uint8_t *>(Q),
-                              static_cast<uint8_t *>(S), M, K);
+                              pitch, static_cast<uint8_t *>(S), M, K);
     };
     // Rows on 8 bytes: loads of 8 (f16 777 x 12300 NV 7.4 us, in shifted pieces 8.7).
     // On 4 or 2: in pieces (4096 x 4095 NV 13.2 us, value by value 18.9).
@@ -212,12 +213,13 @@ cudaError_t dequantize(const void *Q, const void *S, const float *g, void *A, lo
 
 }  // namespace
 
-cudaError_t launch_fp4_quantize(Elt elt, bool nv, const void *A, long long lda, const float *g, void *Q, void *S,
-                                int M, int K, cudaStream_t s) {
+cudaError_t launch_fp4_quantize(Elt elt, bool nv, const void *A, long long lda, const float *g, void *Q,
+                                long long pitch, void *S, int M, int K, cudaStream_t s) {
     if (elt == Elt::BF16)
-        return nv ? quantize<__nv_bfloat16, true>(A, lda, g, Q, S, M, K, s)
-                  : quantize<__nv_bfloat16, false>(A, lda, g, Q, S, M, K, s);
-    return nv ? quantize<__half, true>(A, lda, g, Q, S, M, K, s) : quantize<__half, false>(A, lda, g, Q, S, M, K, s);
+        return nv ? quantize<__nv_bfloat16, true>(A, lda, g, Q, pitch, S, M, K, s)
+                  : quantize<__nv_bfloat16, false>(A, lda, g, Q, pitch, S, M, K, s);
+    return nv ? quantize<__half, true>(A, lda, g, Q, pitch, S, M, K, s)
+              : quantize<__half, false>(A, lda, g, Q, pitch, S, M, K, s);
 }
 
 cudaError_t launch_fp4_dequantize(Elt elt, bool nv, const void *Q, const void *S, const float *g, void *A,

@@ -20,6 +20,9 @@ __host__ __device__ constexpr int fp4_block(bool nv) { return nv ? 16 : 32; }
 // Bytes of one row's codes: two to a byte, rows padded to whole groups of 32
 // elements, so that every row starts on 16 bytes.
 __host__ __device__ constexpr long long fp4_row_bytes(int K) { return ((long long)K + 31) / 32 * 16; }
+// Rows of codes in scratch start on 128 bytes: a TMA load of 128 bytes a row then
+// asks L2 for one line a row, not two (fp4_gemm.cu).
+__host__ __device__ constexpr long long fp4_scratch_pitch(int K) { return (fp4_row_bytes(K) + 127) / 128 * 128; }
 // Scale bytes are kept in atoms of 128 rows x 4 blocks, the order in which
 // tcgen05.cp's 32x128b form takes them to tensor memory: byte (row % 32) * 16 +
 // (row / 32) * 4 + block of 512.  Atoms per tile of 128 rows: K padded to 256.
@@ -276,15 +279,16 @@ __device__ __forceinline__ uint2 fp4_codes16(const uint32_t (&v)[8], const Fp4Sc
 }
 #endif
 
-// fp4.cu
-cudaError_t launch_fp4_quantize(Elt elt, bool nv, const void *A, long long lda, const float *g, void *Q, void *S,
-                                int M, int K, cudaStream_t s);
+// fp4.cu; pitch: bytes from one row's codes to the next's.
+cudaError_t launch_fp4_quantize(Elt elt, bool nv, const void *A, long long lda, const float *g, void *Q,
+                                long long pitch, void *S, int M, int K, cudaStream_t s);
 cudaError_t launch_fp4_dequantize(Elt elt, bool nv, const void *Q, const void *S, const float *g, void *A,
                                   long long lda, int M, int K, cudaStream_t s);
 
 // C [M,N] (leading dimension ldc) = ga gb (Qa Sa)(Qb Sb)^T, FP32 sums.
 struct Fp4Problem {
     const void *Qa, *Sa, *Qb, *Sb;
+    long long pitch_a, pitch_b;  // bytes from one row's codes to the next's
     const float *ga, *gb;  // NV: the tensors' scales (null: 1)
     void *C;
     long long ldc;

@@ -524,8 +524,8 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
     CUtensorMap ta, tsa, tb, tsb, tc;
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const auto u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
-    if (!make_map3(&ta, p.Qa, u8, rb, p.M, 1, rb, rb * p.M, 128, 128, 1, 128) ||
-        !make_map3(&tb, p.Qb, u8, rb, p.N, 1, rb, rb * p.N, 128, bn / 2, 1, 128) ||
+    if (!make_map3(&ta, p.Qa, u8, rb, p.M, 1, p.pitch_a, p.pitch_a * p.M, 128, 128, 1, 128) ||
+        !make_map3(&tb, p.Qb, u8, rb, p.N, 1, p.pitch_b, p.pitch_b * p.N, 128, bn / 2, 1, 128) ||
         !make_map3(&tsa, p.Sa, u32, 256, chunks, fp4_row_tiles(p.M), 1024, chunks * 1024, 256, SFC, 1, 0) ||
         !make_map3(&tsb, p.Sb, u32, 256, chunks, fp4_row_tiles(p.N), 1024, chunks * 1024, 256, SFC, bn == 128 ? 1 : 2, 0))
         return cudaErrorInvalidValue;

@@ -413,13 +413,13 @@ cudaError_t launch(const Fp4Problem &p, const void *X, long long ldx, int num_sm
     CUtensorMap tw, tsw, tx, tsx;
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const auto u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
-    if (!make_map3(&tw, p.Qb, u8, rb, p.N, 1, rb, rb * p.N, 128, 128, 1, 128) ||
+    if (!make_map3(&tw, p.Qb, u8, rb, p.N, 1, p.pitch_b, p.pitch_b * p.N, 128, 128, 1, 128) ||
         !make_map3(&tsw, p.Sb, u32, 256, chunks, strips, 1024, chunks * 1024, 256, SFC, 1, 0))
         return cudaErrorInvalidValue;
     if (FUSED) {
         tx = tw;
         tsx = tsw;
-    } else if (!make_map3(&tx, p.Qa, u8, rb, p.M, 1, rb, rb * p.M, 128, nb, 1, 128) ||
+    } else if (!make_map3(&tx, p.Qa, u8, rb, p.M, 1, p.pitch_a, p.pitch_a * p.M, 128, nb, 1, 128) ||
                !make_map3(&tsx, p.Sa, u32, 256, chunks, 1, 1024, chunks * 1024, 256, SFC, 1, 0)) {
         return cudaErrorInvalidValue;
     }

@@ -470,8 +470,8 @@ gemm_status_t run_fp4_convert(const char *who, bool to_codes, int dtype, int for
     gemm_status_t st = device_info(&dev);
     if (st != GEMM_OK) return st;
     if (to_codes)
-        return finish(launch_fp4_quantize(elt16(dtype), nv, A, lda, g, const_cast<void *>(Q), const_cast<void *>(S),
-                                          M, K, t_stream),
+        return finish(launch_fp4_quantize(elt16(dtype), nv, A, lda, g, const_cast<void *>(Q),
+                                          fp4_row_bytes(K), const_cast<void *>(S), M, K, t_stream),
                       nv ? "fp4_quantize_nv" : "fp4_quantize_mx");
     return finish(launch_fp4_dequantize(elt16(dtype), nv, Q, S, g, const_cast<void *>(A), lda, M, K, t_stream),
                   nv ? "fp4_dequantize_nv" : "fp4_dequantize_mx");
@@ -521,6 +521,7 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     p.Sa = Sa;
     p.Qb = Qb;
     p.Sb = Sb;
+    p.pitch_a = p.pitch_b = fp4_row_bytes(K);
     p.ga = ga;
     p.gb = gb;
     p.C = C;
@@ -546,13 +547,14 @@ gemm_status_t run_fp4(const char *who, int dtype, int format, const void *X, int
     const char *name = skinny ? (nv ? "fp4_skinny_nv" : "fp4_skinny_mx") : (nv ? "fp4_gemm_nv" : "fp4_gemm_mx");
     if (!linear) return finish(product(), name);
     // X's codes and scales in stream-ordered scratch for the duration of the call
-    const size_t q = (fp4_code_size(M, K) + 255) & ~(size_t)255;
+    p.pitch_a = fp4_scratch_pitch(K);
+    const size_t q = ((size_t)M * p.pitch_a + 255) & ~(size_t)255;
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(&ws, q + (size_t)fp4_scale_size(nv, M, K), s);
     if (e != cudaSuccess) return finish(e, "fp4_linear");
     p.Qa = ws;
     p.Sa = static_cast<uint8_t *>(ws) + q;
-    e = launch_fp4_quantize(elt, nv, X, ldx, ga, ws, static_cast<uint8_t *>(ws) + q, M, K, s);
+    e = launch_fp4_quantize(elt, nv, X, ldx, ga, ws, p.pitch_a, static_cast<uint8_t *>(ws) + q, M, K, s);
     if (e == cudaSuccess) e = product();
     const cudaError_t f = cudaFreeAsync(ws, s);
     return finish(e != cudaSuccess ? e : f, name);
