@@ -206,7 +206,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     // complete by then, and dX (args.beside) begins at once, on the SMs that dW
     // leaves, and waits for dW before it ends, so that whatever follows finds both.
     // Backward of 1024 x 12288 x 4096 270 us against 282 one after the other, 128 x
-    // 12288 x 4096 108 against 114, 333 x 1000 x 1000 15.6 against 22.3.
+    // 12288 x 4096 108 against 114.
     if (MODE == DW) {
         pdl_wait();
         pdl_launch_dependents();
@@ -484,12 +484,13 @@ __device__ __forceinline__ float2 unpack(uint32_t v, const __nv_bfloat16 *) {
 __device__ __forceinline__ float2 unpack(uint32_t v, const __half *) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); }
 
 // dG and dU from G, U and dZ, four times four elements to a thread (every load and
-// store a full line across the warp): 10 bytes read and 4 written an element.
+// store a full line across the warp): 10 bytes read and 4 written an element.  G, U
+// and dZ lie without gaps, dG's and dU's rows are `pad` units further apart.
 constexpr int GRAD_UNITS = 4;
 template <typename T, bool GELU>
 __global__ void __launch_bounds__(256)
 gated_grad_kernel(const float4 *__restrict__ G, const float4 *__restrict__ U, const uint2 *__restrict__ dZ,
-                  uint2 *__restrict__ dG, uint2 *__restrict__ dU, long long n4)
+                  uint2 *__restrict__ dG, uint2 *__restrict__ dU, long long n4, uint32_t n4_row, uint32_t pad)
 {
     pdl_launch_dependents();
     pdl_wait();
@@ -515,8 +516,10 @@ gated_grad_kernel(const float4 *__restrict__ G, const float4 *__restrict__ U, co
         gate_act_grad<GELU>(g[j].y, a[1], da[1]);
         gate_act_grad<GELU>(g[j].z, a[2], da[2]);
         gate_act_grad<GELU>(g[j].w, a[3], da[3]);
-        dU[i] = make_uint2(pack2(d0.x * a[0], d0.y * a[1], (T *)nullptr), pack2(d1.x * a[2], d1.y * a[3], (T *)nullptr));
-        dG[i] = make_uint2(pack2(d0.x * u[j].x * da[0], d0.y * u[j].y * da[1], (T *)nullptr),
+        const long long row = pad == 0 ? 0 : n4 <= 0xFFFFFFFFLL ? (uint32_t)i / n4_row : i / n4_row;
+        const long long o = i + row * pad;
+        dU[o] = make_uint2(pack2(d0.x * a[0], d0.y * a[1], (T *)nullptr), pack2(d1.x * a[2], d1.y * a[3], (T *)nullptr));
+        dG[o] = make_uint2(pack2(d0.x * u[j].x * da[0], d0.y * u[j].y * da[1], (T *)nullptr),
                            pack2(d1.x * u[j].z * da[2], d1.y * u[j].w * da[3], (T *)nullptr));
     }
 }
@@ -580,25 +583,30 @@ int clusters_max(int dev) {
 constexpr CUtensorMapDataType map_type(uint32_t format) {
     return format == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
-// A row-major 16-bit matrix [rows, cols] (two of them, `stride` bytes apart, for z = 2).
+// A row-major 16-bit matrix [rows, cols], rows ld elements apart; z of them, one after the other.
 bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long long cols, int box_cols, int box_rows,
-           int z = 1, long long stride = 0) {
-    return make_map3(m, p, map_type(format), cols, rows, z, cols * 2, z > 1 ? stride : rows * cols * 2, box_cols, box_rows,
-                     1, 128);
+           long long ld, int z) {
+    return make_map3(m, p, map_type(format), cols, rows, z, ld * 2, rows * ld * 2, box_cols, box_rows, 1, 128);
+}
+bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long long cols, int box_cols, int box_rows) {
+    return map16(m, p, format, rows, cols, box_cols, box_rows, cols, 1);
 }
 
 // How the tiles go to the clusters.  Whole waves of tiles first; the rest is split
 // when that saves more than the partials and the second kernel cost; a split is
 // eight blocks at least.  Times are in 256ths of a K block of a 256 x 256
-// accumulator, 0.3 us; `block` is one of this tile's.  Measured, forward: 1024 x 12288 x
+// accumulator, 0.3 us.  Measured, forward: 1024 x 12288 x
 // 4096 (384 tiles on 76 clusters) 112 us against 120 with whole tiles, 128 x 12288 x
 // 4096 (96 tiles) 46.8 against 51.8; dX of 777 x 11008 x 4096 in 64 whole tiles
 // 113 us, in 76 of 192 columns and 12 split in six 120.
-constexpr long long fix_time(long long slabs) { return 10 * 256 + slabs * 51; }  // 3 us and 0.06 a partial
+// Partials and the second kernel: 4.2 us, and 0.06 a partial of 256 columns.
+constexpr long long fix_time(long long slabs, int columns) { return 14 * 256 + slabs * columns / 5; }
 // Blocks of narrower accumulators: dX of 128 x 12288 x 4096 in one wave takes 0.27 us
 // a block at 256 columns, 0.22 at 192 and 0.205 at 128, forward 1024 x 12160 x 4096
-// 0.33 at 256 and 0.23 at 128.  Rows that do not start on 128 bytes: forward of 333 x
-// 1000 x 1000 12.4 us where 333 x 1024 x 1024 takes 9.5.
+// 0.33 at 256 and 0.23 at 128.  Where rows of neither operand start on 128 bytes, TMA
+// asks L2 for two lines for most of a box's rows, and that bounds the blocks: forward
+// of 1024 x 12280 x 4088 165 us, where 1024 x 12288 x 4088 and 1024 x 12280 x 4096, with
+// one such operand, take 122 and 1024 x 12288 x 4096 114.
 constexpr int block_time(int columns, bool rows_on_128) {
     return (columns == 256 ? 256 : columns == 192 ? 208 : 180) * (rows_on_128 ? 5 : 8) / 5;
 }
@@ -606,13 +614,16 @@ struct Plan {
     long long tiles, time;
     int clusters, whole, splits;
 };
-Plan plan(long long tiles, int cmax, long long num_kb, int block) {
+// `columns`: of a tile's accumulator; rows_on_128: of one operand at least.
+Plan plan(long long tiles, int cmax, long long num_kb, int columns, bool rows_on_128) {
+    const int block = block_time(columns, rows_on_128);
     const long long waves = tiles / cmax, rem = tiles - waves * cmax;
     Plan p = {tiles, (waves + (rem > 0)) * num_kb * block, (int)std::min<long long>(tiles, cmax), (int)tiles, 1};
     if (rem == 0) return p;
     const long long splits = std::min<long long>({cmax / rem, num_kb / 8, 16});
-    if (splits < 2 || (num_kb - num_kb / splits) * block < fix_time(rem * splits)) return p;
-    p.time = (waves * num_kb + num_kb / splits) * block + fix_time(rem * splits);
+    const long long fix = fix_time(rem * splits, columns);
+    if (splits < 2 || (num_kb - num_kb / splits) * block < fix) return p;
+    p.time = (waves * num_kb + num_kb / splits) * block + fix;
     p.whole = (int)(waves * cmax);
     p.splits = (int)splits;
     p.clusters = waves > 0 ? cmax : (int)(rem * splits);
@@ -665,9 +676,9 @@ cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s)
     // clusters idle (forward of 333 x 1000 x 1000 9.1 us against 12.4, 300 x 512 x 2048
     // 8.4 against 11.8; 128 x 12288 x 4096 55 against 45, 1024 x 12160 x 4096 149
     // against 107).
-    const bool on128 = p.N % 64 == 0 && p.K % 64 == 0;
-    Plan pl = plan(tiles_m * ((p.N + 127LL) / 128), cmax, num_kb, block_time(256, on128));
-    const Plan thin = plan(tiles_m * ((p.N + 63LL) / 64), cmax, num_kb, block_time(128, on128));
+    const bool on128 = p.N % 64 == 0 || p.K % 64 == 0;
+    Plan pl = plan(tiles_m * ((p.N + 127LL) / 128), cmax, num_kb, 256, on128);
+    const Plan thin = plan(tiles_m * ((p.N + 63LL) / 64), cmax, num_kb, 128, on128);
     const int bn = thin.time < pl.time ? 64 : 128;
     if (bn == 64) pl = thin;
     if (pl.tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
@@ -704,16 +715,19 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     const int cmax = clusters_max<T, FORMAT, DX, false>(dev), wmax = clusters_max<T, FORMAT, DW, false>(dev);
     if (cmax <= 0 || wmax <= 0) return cudaErrorNotSupported;
     const long long mn = (long long)p.M * p.N;
+    // dG and dU on rows of 128 bytes, whatever N: of a product's two operands one may
+    // lie otherwise at little cost (block_time)
+    const long long ldg = gated_ldg(p.N);
     const bool pair_dx = p.dX && p.M > kGatedSkinnyMaxM, both = p.dWg && p.dWu;
     const Plan pw = plan((p.K + 255LL) / 256 * ((p.N + 255LL) / 256) * (both ? 2 : 1), wmax, (p.M + BK - 1LL) / BK,
-                         block_time(256, p.N % 64 == 0 && p.K % 64 == 0));
+                         256, true);
     // (where dW's tiles are split, a kernel that adds them lies between, and the
     // partials' scratch is shared)
     const bool beside = pair_dx && g_pdl && (p.dWg || p.dWu) && pw.splits == 1;
     // dX: the tile width and plan that are done first, widest on ties.  Beside dW, a
     // plan may keep to the clusters that dW leaves; one that needs more waits for dW,
-    // its blocks and about 12 blocks' time of set-up and writing (backward of 333 x 1000
-    // x 1000 15.6 us, with dX's plan for all clusters 20.5; 500 x 1504 x 704 15.7 and 20.3).
+    // its blocks and about 12 blocks' time of set-up and writing (backward of 500 x 1504
+    // x 704 16.1 us, with dX's plan for all clusters 20.3; 333 x 1000 x 1000 13.7).
     const long long tiles_m = (p.M + 255LL) / 256;
     const int half = (p.N + BK - 1) / BK, left = beside ? std::max(cmax - pw.clusters, 0) : cmax;
     int bn = 0;
@@ -723,20 +737,20 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
         const long long tiles = tiles_m * ((p.K + c - 1LL) / c);
         for (int clusters : {cmax, left}) {
             if (clusters == 0) continue;
-            const Plan q = plan(tiles, clusters, 2LL * half, block_time(c, p.N % 64 == 0));
+            const Plan q = plan(tiles, clusters, 2LL * half, c, true);
             const long long time = q.time + (q.clusters > left ? pw.time + 12 * 256 : 0);
             if (bn == 0 || time < best) { bn = c; px = q; best = time; }
         }
     }
     if (px.tiles > 0x7FFFFFFFLL || pw.tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     // scratch: dG and dU, and the partials of the two products, one after the other
-    const size_t off = ((size_t)mn * 4 + 1023) & ~(size_t)1023;
+    const size_t off = ((size_t)(p.M * ldg) * 4 + 1023) & ~(size_t)1023;
     const size_t parts = std::max(pair_dx ? plan_scratch(px) : 0, p.dWg || p.dWu ? plan_scratch(pw) : 0);
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(&ws, off + parts, s);
     if (e != cudaSuccess) return e;
     void *part = static_cast<uint8_t *>(ws) + off;
-    T *dG = static_cast<T *>(ws), *dU = dG + mn;
+    T *dG = static_cast<T *>(ws), *dU = dG + p.M * ldg;
     {
         const long long n4 = mn / 4, blocks = (n4 + 256 * GRAD_UNITS - 1) / (256 * GRAD_UNITS);
         cudaLaunchAttribute attr[1];
@@ -745,13 +759,14 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
                 ? cudaErrorInvalidValue
                 : launch_counted(&cfg, gated_grad_kernel<T, GELU>, reinterpret_cast<const float4 *>(p.G),
                                  reinterpret_cast<const float4 *>(p.U), static_cast<const uint2 *>(p.dZ),
-                                 reinterpret_cast<uint2 *>(dG), reinterpret_cast<uint2 *>(dU), n4);
+                                 reinterpret_cast<uint2 *>(dG), reinterpret_cast<uint2 *>(dU), n4, (uint32_t)(p.N / 4),
+                                 (uint32_t)((ldg - p.N) / 4));
     }
     if (e == cudaSuccess && (p.dWg || p.dWu)) {
         T *w0 = static_cast<T *>(p.dWg ? p.dWg : p.dWu), *w1 = static_cast<T *>(p.dWu ? p.dWu : p.dWg);
         CUtensorMap ta, tb, tc, tc2;
         if (!map16(&ta, p.X, FORMAT, p.M, p.K, 64, BK) ||
-            !map16(&tb, p.dWg ? dG : dU, FORMAT, p.M, p.N, 64, BK, both ? 2 : 1, mn * 2) ||
+            !map16(&tb, p.dWg ? dG : dU, FORMAT, p.M, p.N, 64, BK, ldg, both ? 2 : 1) ||
             !map16(&tc, w0, FORMAT, p.K, p.N, 64, 32) || !map16(&tc2, w1, FORMAT, p.K, p.N, 64, 32)) {
             e = cudaErrorInvalidValue;
         } else {
@@ -769,7 +784,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
         e = launch_gated_skinny_dx(p, dG, num_sms, status, s);
     } else if (e == cudaSuccess && p.dX) {
         CUtensorMap ta, tb, tb2, tc;
-        if (!map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, 2, mn * 2) || !map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) ||
+        if (!map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, ldg, 2) || !map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) ||
             !map16(&tb2, p.Wu, FORMAT, p.K, p.N, BK, bn / 2) || !map16(&tc, p.dX, FORMAT, p.M, p.K, 64, 32)) {
             e = cudaErrorInvalidValue;
         } else {

@@ -37,7 +37,8 @@ cudaError_t launch_gated_gradients(const GatedBackward &p, int num_sms, int *sta
 cudaError_t launch_gated(const GatedProblem &p, int *status, cudaStream_t s);            // any M
 constexpr int kGatedSkinnyMaxM = 64;
 cudaError_t launch_gated_skinny(const GatedProblem &p, int num_sms, int *status, cudaStream_t s);
-// dX from dG and dU [2][M][N].
+// dX from dG and dU [2][M][N], rows gated_ldg(N) elements apart.
+constexpr long long gated_ldg(int N) { return ((long long)N + 63) / 64 * 64; }
 cudaError_t launch_gated_skinny_dx(const GatedBackward &p, const void *dGU, int num_sms, int *status, cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedBackward &p, int num_sms, int *status, cudaStream_t s);
 

@@ -365,9 +365,9 @@ cudaError_t forward(const GatedProblem &p, int num_sms, int *status, cudaStream_
 template <typename T, uint32_t FORMAT>
 cudaError_t grad_x(const GatedBackward &p, const void *dGU, int num_sms, int *status, cudaStream_t s) {
     constexpr auto dt = map_type(FORMAT);
-    const long long wr = 2LL * p.N;
+    const long long wr = 2LL * p.N, gr = 2 * gated_ldg(p.N);
     CUtensorMap tx, tg, tu;
-    if (!make_map3(&tx, dGU, dt, p.N, p.M, 2, wr, wr * p.M, 64, nb_of(p.M), 1, 128) ||
+    if (!make_map3(&tx, dGU, dt, p.N, p.M, 2, gr, gr * p.M, 64, nb_of(p.M), 1, 128) ||
         !make_map3(&tg, p.Wg, dt, p.N, p.K, 1, wr, wr * p.K, 64, 128, 1, 128) ||
         !make_map3(&tu, p.Wu, dt, p.N, p.K, 1, wr, wr * p.K, 64, 128, 1, 128))
         return cudaErrorInvalidValue;
