@@ -676,7 +676,7 @@ cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s)
     // clusters idle (forward of 333 x 1000 x 1000 9.1 us against 12.4, 300 x 512 x 2048
     // 8.4 against 11.8; 128 x 12288 x 4096 55 against 45, 1024 x 12160 x 4096 149
     // against 107).
-    const bool on128 = p.N % 64 == 0 || p.K % 64 == 0;
+    const bool on128 = p.N % 64 == 0 || p.ldx % 64 == 0;
     Plan pl = plan(tiles_m * ((p.N + 127LL) / 128), cmax, num_kb, 256, on128);
     const Plan thin = plan(tiles_m * ((p.N + 63LL) / 64), cmax, num_kb, 128, on128);
     const int bn = thin.time < pl.time ? 64 : 128;
@@ -684,7 +684,7 @@ cudaError_t forward(const GatedProblem &p, int dev, int *status, cudaStream_t s)
     if (pl.tiles > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     CUtensorMap tx, tg, tu, tz, tsg, tsu;
     const long long zr = 2LL * p.N;
-    if (!map16(&tx, p.X, FORMAT, p.M, p.K, BK, 128) || !map16(&tg, p.Wg, FORMAT, p.K, p.N, 64, BK) ||
+    if (!map16(&tx, p.X, FORMAT, p.M, p.K, BK, 128, p.ldx, 1) || !map16(&tg, p.Wg, FORMAT, p.K, p.N, 64, BK) ||
         !map16(&tu, p.Wu, FORMAT, p.K, p.N, 64, BK) ||
         !make_map3(&tz, p.Z, map_type(FORMAT), p.N, p.M, 1, zr, zr * p.M, bn / 2, 32, 1, /*swizzle: a row's bytes*/ bn))
         return cudaErrorInvalidValue;

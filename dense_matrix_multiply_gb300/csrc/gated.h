@@ -17,7 +17,8 @@ struct GatedProblem {
     float *G, *U;
     int M, N, K;
     Elt elt;
-    bool gelu;  // GELU (tanh form), else SiLU
+    bool gelu;      // GELU (tanh form), else SiLU
+    long long ldx;  // elements from one row of X to the next
 };
 // The gradients of X, Wg and Wu from dZ and the saved G and U; a null one is
 // left out.

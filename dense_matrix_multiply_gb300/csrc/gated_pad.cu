@@ -3,12 +3,11 @@
 // multiple of 8, a base off 16 bytes) are copied to scratch with rows of whole 16
 // bytes, zeros behind the row and below the matrix, the products run over the
 // padded sizes, and results are copied back: the zeros add nothing to a sum, and a
-// column past N or K is dropped.
+// column past N or K is dropped.  (X alone goes to rows of 128 bytes for speed, below.)
 //
 // A copy is bound by memory, each byte read and written once, a call of few rows
 // by it: bf16 SiLU forward 1 x 12289 x 4096 110 us (both weights copied at 5.1 TB/s),
-// where 1 x 12288 x 4096 takes 30.7; 1024 x 12285 x 4095 201 us against 113; forward
-// and backward of f16 333 x 1001 x 1001 61 against 35.
+// where 1 x 12288 x 4096 takes 30.7; 1024 x 12285 x 4095 201 us against 113.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -73,13 +72,14 @@ bool on16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 class Padded {
   public:
     // A matrix [rows, cols] of `words` 16-bit words an element (null: left out), which
-    // the products see as [prows, up8(cols)]; *at: the address for them, once begin()
-    // has returned.
-    void add(const void **at, const void *user, long long rows, long long prows, long long cols, int words, bool out) {
+    // the products see as [prows, pcols]; *at: the address for them, once begin() has
+    // returned.
+    void add(const void **at, const void *user, long long rows, long long prows, long long cols, long long pcols,
+             int words, bool out) {
         *at = user;
-        if (!user || (on16(user) && rows == prows && cols == up8(cols))) return;
+        if (!user || (on16(user) && rows == prows && cols == pcols)) return;
         Operand &o = ops_[n_++];
-        o = {at, const_cast<void *>(user), rows, prows, cols * words, up8(cols) * words, out, bytes_};
+        o = {at, const_cast<void *>(user), rows, prows, cols * words, pcols * words, out, bytes_};
         bytes_ += ((size_t)(o.prows * o.pcols) * 2 + 255) & ~(size_t)255;
     }
     cudaError_t begin(cudaStream_t s) {
@@ -125,13 +125,20 @@ cudaError_t launch_gated_forward(const GatedProblem &p, int num_sms, int *status
     if (n8 > 0x7FFFFFFFLL || k8 > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
     GatedProblem q = p;
     const void *z, *g, *u;
+    // X also goes to rows of 128 bytes where rows of neither it nor the weights start
+    // on 128 and the products, some 1.3 times slower then (gated.cu), take long
+    // enough: the copy's own time and about 10 us of allocation, launch and lost
+    // overlap.  Forward of 1024 x 12280 x 4088 122 us, 153 as it lies.
+    const bool odd = p.N % 64 != 0 && p.K % 64 != 0, large = p.M > kGatedSkinnyMaxM;
+    const double ns = 4.0 * p.M * p.N * p.K / 1.7e6, copy_ns = 1e4 + 4.0 * p.M * p.K / 5e3;
+    q.ldx = p.K % 8 != 0 || !on16(p.X) || (odd && large && 0.3 * ns > copy_ns) ? (p.K + 63LL) / 64 * 64 : p.K;
     Padded pad;
-    pad.add(&q.X, p.X, p.M, p.M, p.K, 1, false);
-    pad.add(&q.Wg, p.Wg, p.K, k8, p.N, 1, false);
-    pad.add(&q.Wu, p.Wu, p.K, k8, p.N, 1, false);
-    pad.add(&z, p.Z, p.M, p.M, p.N, 1, true);
-    pad.add(&g, p.G, p.M, p.M, p.N, 2, true);
-    pad.add(&u, p.U, p.M, p.M, p.N, 2, true);
+    pad.add(&q.X, p.X, p.M, p.M, p.K, q.ldx, 1, false);
+    pad.add(&q.Wg, p.Wg, p.K, k8, p.N, n8, 1, false);
+    pad.add(&q.Wu, p.Wu, p.K, k8, p.N, n8, 1, false);
+    pad.add(&z, p.Z, p.M, p.M, p.N, n8, 1, true);
+    pad.add(&g, p.G, p.M, p.M, p.N, n8, 2, true);
+    pad.add(&u, p.U, p.M, p.M, p.N, n8, 2, true);
     cudaError_t e = pad.begin(s);
     q.Z = const_cast<void *>(z);
     q.G = static_cast<float *>(const_cast<void *>(g));
@@ -150,17 +157,17 @@ cudaError_t launch_gated_gradients(const GatedBackward &p, int num_sms, int *sta
     const void *g, *u, *dx, *dwg, *dwu;
     Padded pad;
     const bool weights = p.dWg || p.dWu;
-    if (weights) pad.add(&q.X, p.X, p.M, p.M, p.K, 1, false);
+    if (weights) pad.add(&q.X, p.X, p.M, p.M, p.K, k8, 1, false);
     if (p.dX) {
-        pad.add(&q.Wg, p.Wg, p.K, k8, p.N, 1, false);
-        pad.add(&q.Wu, p.Wu, p.K, k8, p.N, 1, false);
+        pad.add(&q.Wg, p.Wg, p.K, k8, p.N, n8, 1, false);
+        pad.add(&q.Wu, p.Wu, p.K, k8, p.N, n8, 1, false);
     }
-    pad.add(&q.dZ, p.dZ, p.M, p.M, p.N, 1, false);
-    pad.add(&g, p.G, p.M, p.M, p.N, 2, false);
-    pad.add(&u, p.U, p.M, p.M, p.N, 2, false);
-    pad.add(&dx, p.dX, p.M, p.M, p.K, 1, true);
-    pad.add(&dwg, p.dWg, p.K, k8, p.N, 1, true);
-    pad.add(&dwu, p.dWu, p.K, k8, p.N, 1, true);
+    pad.add(&q.dZ, p.dZ, p.M, p.M, p.N, n8, 1, false);
+    pad.add(&g, p.G, p.M, p.M, p.N, n8, 2, false);
+    pad.add(&u, p.U, p.M, p.M, p.N, n8, 2, false);
+    pad.add(&dx, p.dX, p.M, p.M, p.K, k8, 1, true);
+    pad.add(&dwg, p.dWg, p.K, k8, p.N, n8, 1, true);
+    pad.add(&dwu, p.dWu, p.K, k8, p.N, n8, 1, true);
     cudaError_t e = pad.begin(s);
     q.G = static_cast<const float *>(g);
     q.U = static_cast<const float *>(u);

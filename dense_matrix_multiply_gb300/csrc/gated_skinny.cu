@@ -344,7 +344,7 @@ cudaError_t launch(const CUtensorMap &tx, const CUtensorMap &tg, const CUtensorM
 template <typename T, uint32_t FORMAT>
 cudaError_t forward(const GatedProblem &p, int num_sms, int *status, cudaStream_t s) {
     constexpr auto dt = map_type(FORMAT);
-    const long long xr = 2LL * p.K, wr = 2LL * p.N;
+    const long long xr = 2 * p.ldx, wr = 2LL * p.N;
     CUtensorMap tx, tg, tu;
     if (!make_map3(&tx, p.X, dt, p.K, p.M, 1, xr, xr * p.M, 64, nb_of(p.M), 1, 128) ||
         !make_map3(&tg, p.Wg, dt, p.N, p.K, 1, wr, wr * p.K, 64, KB, 1, 128) ||

@@ -597,7 +597,7 @@ gemm_status_t run_gated(int dtype, int act, const void *X, const void *Wg, const
     cudaStream_t s = t_stream;
     if (K == 0)  // G = U = 0, and act(0) * 0 = 0
         return finish(zero(us, s, zero(gs, s, zero(z, s, cudaSuccess))), "zero_fill");
-    const GatedProblem p{X, Wg, Wu, Z, G, U, M, N, K, elt16(dtype), act == GEMM_ACT_GELU_TANH};
+    const GatedProblem p{X, Wg, Wu, Z, G, U, M, N, K, elt16(dtype), act == GEMM_ACT_GELU_TANH, K};
     return finish(launch_gated_forward(p, dev->num_sms, dev->status, s), M <= kGatedSkinnyMaxM ? "gated_skinny" : "gated_pair");
 }
 

@@ -334,7 +334,8 @@ GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t for
  * rounding points of the unfused chain instead: G, U and act(G) rounded to bf16.)
  * Any M, N, K: one token to a long prompt.  Operands that are not 16-byte aligned,
  * or whose N or K is no multiple of 8, are copied to or from padded rows in
- * stream-ordered scratch, which costs a pass over each of them.  K = 0 gives
+ * stream-ordered scratch, which costs a pass over each of them; so is X for a long
+ * product with neither N nor K a multiple of 64.  N or K a multiple of 64 is fastest.  K = 0 gives
  * zeros.  GEMM_ERR_ALIAS if an output overlaps an input or another output. */
 typedef enum gemm_act_t { GEMM_ACT_SILU = 0, GEMM_ACT_GELU_TANH = 1 } gemm_act_t;
 

@@ -112,6 +112,20 @@ def test_sizes_that_are_no_multiples_of_8(M, N, K, dtype, act):
     test_forward_and_backward(M, N, K, dtype, act)
 
 
+def test_long_products_of_rows_off_128_bytes():
+    """X goes to aligned rows first: the same bits as with K filled up with zeros,
+    where it does not."""
+    M, N, K, K0 = 1400, 4104, 4104, 4160
+    (X, Wg, Wu, _), _ = make(M, N, K, "bf16", 13)
+    wide = torch.zeros(M, K0, dtype=X.dtype)
+    wide[:, :K] = X
+    tall = [torch.cat([w, torch.zeros(K0 - K, N, dtype=w.dtype)]) for w in (Wg, Wu)]
+    a = run("bf16", "silu", (X, Wg, Wu, X[:1]), M, N, K, grads=False)
+    b = run("bf16", "silu", (wide, *tall, X[:1]), M, N, K0, grads=False)
+    for n in "ZGU":
+        assert np.array_equal(a[n], b[n]), n
+
+
 @pytest.mark.parametrize("M,N,K", [(3, 72, 40), (100, 264, 128), (100, 263, 127)])
 def test_operands_off_16_bytes(M, N, K):
     """Every operand one element past an aligned base: the results of the aligned call, bit for bit."""
