@@ -22,8 +22,8 @@
 // Tile widths, by tensor memory (512 columns, 64 of them scales): 192 leaves two
 // whole accumulators, so that a tile is written while the next is computed; 256
 // two that share 64 columns, which the epilogue reads first before it lets the
-// next tile's MMAs start (1.2 us a tile in which the tensor cores wait); 128 for
-// few tiles.  launch_pair says which runs when.
+// next tile's MMAs start (1.2 us a tile in which the tensor cores wait); 128 and 64
+// for few tiles.  launch_pair says which runs when.
 //
 // The loading and issuing warps stay converged and elect a lane for the TMA and
 // tcgen05 instructions only: with loops run by one lane alone, operands are moved
@@ -61,7 +61,7 @@ __host__ __device__ constexpr int sf_stage(bool nv) { return nv ? 2048 : 1024; }
 // A's codes, B's codes, the scales of A's 128 rows and of the one or two 128-row
 // tiles that B's tile meets.
 __host__ __device__ constexpr int stage_bytes(bool nv, int bn) {
-    return A_STAGE + bn / 2 * (KB / 2) + (bn == 128 ? 2 : 3) * sf_stage(nv);
+    return A_STAGE + bn / 2 * (KB / 2) + (bn <= 128 ? 2 : 3) * sf_stage(nv);
 }
 constexpr int MAX_STAGES = 6;
 __host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 5 : 6; }
@@ -91,7 +91,7 @@ struct Args {
     long long ldc;
     const float *ga, *gb;
     int M, N, K;
-    int bn;         // 128, 192 or 256
+    int bn;         // 64, 128, 192 or 256
     int tma_store;  // C's rows suit TMA stores
     int *status;
 };
@@ -223,7 +223,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     constexpr int SF = sf_stage(NV);
     const int M = args.M, N = args.N, bn = args.bn;
     const int STAGES = stages_of(bn), B_STAGE = (bn >> 1) * (KB / 2);
-    const int sf_tiles_b = bn == 128 ? 1 : 2;  // 128-row tiles of scales that a tile of B meets
+    const int sf_tiles_b = bn <= 128 ? 1 : 2;  // 128-row tiles of scales that a tile of B meets
     const int SF_STAGE = (1 + sf_tiles_b) * SF;
     uint8_t *a_tiles = smem;
     uint8_t *b_tiles = a_tiles + STAGES * A_STAGE;
@@ -502,18 +502,21 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
     const int cmax = clusters_max<T, NV>(dev);
     if (cmax <= 0) return cudaErrorNotSupported;
     // The tile's width: the least waves x time of a tile.  A tile takes the longer
-    // of its stages (measured 0.25 us each at 192, 0.31 at 256 and 0.22 at 128, with
-    // the 1 us in which 256's accumulators change hands) and its writing (2.2, 2.5
-    // and 1.7 us).  Measured, NV, at 192 and 256: 8192^3 157 and 159 us, 2048 x 12288
-    // x 4096 38.2 and 42.1, 2048 x 4096 x 4096 18.1 and 16.7, 8192 x 12288 x 512 59.7
-    // and 53.5; 1000 x 1001 x 4100 17.1, 18.7 and 13.2 at 128.
+    // of its stages (measured 0.25 us each at 192, 0.31 at 256, 0.22 at 128 and 0.205
+    // at 64, with the 1 us in which 256's accumulators change hands) and its writing
+    // (2.2, 2.5, 1.7 and 1.5 us).  Measured, NV, at 192 and 256: 8192^3 157 and 159 us,
+    // 2048 x 12288 x 4096 38.2 and 42.1, 2048 x 4096 x 4096 18.1 and 16.7, 8192 x 12288
+    // x 512 59.7 and 53.5; 1000 x 1001 x 4100 17.1, 18.7, 13.2 at 128; that in MX 10.8 at
+    // 128 and 9.4 at 64, 200 x 2000 x 1000 4.7 and 4.3, 300 x 4096 x 4096 7.7 and 10.4.
     const long long tiles_m = (p.M + 255LL) / 256, kbs = (p.K + KB - 1LL) / KB;
     int bn = 0;
     long long tiles = 0, best = 0;
-    for (int c : {192, 256, 128}) {
+    for (int c : {192, 256, 128, 64}) {
         const long long t = tiles_m * ((p.N + c - 1LL) / c);
-        const long long ns = c == 192 ? std::max(250 * kbs, 2200LL)
-                                      : c == 256 ? std::max(310 * kbs + 1000, 2500LL) : std::max(220 * kbs, 1700LL);
+        const long long ns = c == 192   ? std::max(250 * kbs, 2200LL)
+                             : c == 256 ? std::max(310 * kbs + 1000, 2500LL)
+                             : c == 128 ? std::max(220 * kbs, 1700LL)
+                                        : std::max(205 * kbs, 1500LL);
         const long long cost = (t + cmax - 1) / cmax * ns;
         if (bn == 0 || cost < best) { bn = c; tiles = t; best = cost; }
     }
@@ -527,7 +530,7 @@ cudaError_t launch_pair(const Fp4Problem &p, int *status, cudaStream_t s) {
     if (!make_map3(&ta, p.Qa, u8, rb, p.M, 1, p.pitch_a, p.pitch_a * p.M, 128, 128, 1, 128) ||
         !make_map3(&tb, p.Qb, u8, rb, p.N, 1, p.pitch_b, p.pitch_b * p.N, 128, bn / 2, 1, 128) ||
         !make_map3(&tsa, p.Sa, u32, 256, chunks, fp4_row_tiles(p.M), 1024, chunks * 1024, 256, SFC, 1, 0) ||
-        !make_map3(&tsb, p.Sb, u32, 256, chunks, fp4_row_tiles(p.N), 1024, chunks * 1024, 256, SFC, bn == 128 ? 1 : 2, 0))
+        !make_map3(&tsb, p.Sb, u32, 256, chunks, fp4_row_tiles(p.N), 1024, chunks * 1024, 256, SFC, bn <= 128 ? 1 : 2, 0))
         return cudaErrorInvalidValue;
     Args a = {};
     a.C = p.C;
