@@ -203,7 +203,7 @@ gated_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const uint32_t tmem_base = bars->tmem_base;
     // The backward pass launches dW, then dX, which reads nothing that dW writes: dW
     // lets its dependent start only after its own wait, so that dG and dU are
-    // complete by then, and dX (args.beside) begins at once, on the SMs that dW
+    // complete by then, and dX (args.beside; gated_skinny.cu's too) begins at once, on the SMs that dW
     // leaves, and waits for dW before it ends, so that whatever follows finds both.
     // Backward of 1024 x 12288 x 4096 270 us against 282 one after the other, 128 x
     // 12288 x 4096 108 against 114.
@@ -723,7 +723,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
                          256, true);
     // (where dW's tiles are split, a kernel that adds them lies between, and the
     // partials' scratch is shared)
-    const bool beside = pair_dx && g_pdl && (p.dWg || p.dWu) && pw.splits == 1;
+    const bool beside = p.dX && g_pdl && (p.dWg || p.dWu) && pw.splits == 1;
     // dX: the tile width and plan that are done first, widest on ties.  Beside dW, a
     // plan may keep to the clusters that dW leaves; one that needs more waits for dW,
     // its blocks and about 12 blocks' time of set-up and writing (backward of 500 x 1504
@@ -781,7 +781,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
         }
     }
     if (e == cudaSuccess && p.dX && !pair_dx) {
-        e = launch_gated_skinny_dx(p, dG, num_sms, status, s);
+        e = launch_gated_skinny_dx(p, dG, beside, num_sms, status, s);
     } else if (e == cudaSuccess && p.dX) {
         CUtensorMap ta, tb, tb2, tc;
         if (!map16(&ta, dG, FORMAT, p.M, p.N, BK, 128, ldg, 2) || !map16(&tb, p.Wg, FORMAT, p.K, p.N, BK, bn / 2) ||

@@ -40,7 +40,9 @@ constexpr int kGatedSkinnyMaxM = 64;
 cudaError_t launch_gated_skinny(const GatedProblem &p, int num_sms, int *status, cudaStream_t s);
 // dX from dG and dU [2][M][N], rows gated_ldg(N) elements apart.
 constexpr long long gated_ldg(int N) { return ((long long)N + 63) / 64 * 64; }
-cudaError_t launch_gated_skinny_dx(const GatedBackward &p, const void *dGU, int num_sms, int *status, cudaStream_t s);
+// beside: the launch before is dW's, which writes nothing that dX reads.
+cudaError_t launch_gated_skinny_dx(const GatedBackward &p, const void *dGU, bool beside, int num_sms, int *status,
+                                   cudaStream_t s);
 cudaError_t launch_gated_backward(const GatedBackward &p, int num_sms, int *status, cudaStream_t s);
 
 #ifdef __CUDACC__

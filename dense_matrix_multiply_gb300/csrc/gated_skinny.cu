@@ -65,6 +65,9 @@ struct Args {
     int num_kb;    // stages of the reduction (dX: of both halves)
     int kb_half;   // dX: stages of the first half
     int cs;
+    // dX: runs beside the dW kernel before it, as in gated.cu (backward of 64 x 1000 x
+    // 504 9.8 us from 12.5, 1 x 12288 x 4096 90 from 93)
+    int beside;
     int *status;
 };
 
@@ -133,7 +136,7 @@ gated_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
             }
         }
     }
-    pdl_wait();
+    if (!(DX && args.beside)) pdl_wait();
 
     if (warp == 0 && lane == 0) {
         // ------------------------------------------------------------ producer
@@ -294,6 +297,7 @@ gated_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
         fence_after();
         tmem_dealloc<1>(tmem_base, TMEM_COLS);
     }
+    if (DX && args.beside) pdl_wait();
 }
 
 template <typename T, uint32_t FORMAT, bool DX, bool GELU>
@@ -363,7 +367,7 @@ cudaError_t forward(const GatedProblem &p, int num_sms, int *status, cudaStream_
 }
 
 template <typename T, uint32_t FORMAT>
-cudaError_t grad_x(const GatedBackward &p, const void *dGU, int num_sms, int *status, cudaStream_t s) {
+cudaError_t grad_x(const GatedBackward &p, const void *dGU, bool beside, int num_sms, int *status, cudaStream_t s) {
     constexpr auto dt = map_type(FORMAT);
     const long long wr = 2LL * p.N, gr = 2 * gated_ldg(p.N);
     CUtensorMap tx, tg, tu;
@@ -377,6 +381,7 @@ cudaError_t grad_x(const GatedBackward &p, const void *dGU, int num_sms, int *st
     a.N = p.K;
     a.kb_half = (p.N + KB - 1) / KB;
     a.num_kb = 2 * a.kb_half;
+    a.beside = beside;
     a.status = status;
     return launch<T, FORMAT, true, false>(tx, tg, tu, a, num_sms, s);
 }
@@ -389,10 +394,11 @@ cudaError_t launch_gated_skinny(const GatedProblem &p, int num_sms, int *status,
                               : forward<__half, 0>(p, num_sms, status, s);
 }
 
-cudaError_t launch_gated_skinny_dx(const GatedBackward &p, const void *dGU, int num_sms, int *status, cudaStream_t s) {
+cudaError_t launch_gated_skinny_dx(const GatedBackward &p, const void *dGU, bool beside, int num_sms, int *status,
+                                   cudaStream_t s) {
     if (p.M < 1 || p.M > kGatedSkinnyMaxM) return cudaErrorInvalidValue;
-    return p.elt == Elt::BF16 ? grad_x<__nv_bfloat16, 1>(p, dGU, num_sms, status, s)
-                              : grad_x<__half, 0>(p, dGU, num_sms, status, s);
+    return p.elt == Elt::BF16 ? grad_x<__nv_bfloat16, 1>(p, dGU, beside, num_sms, status, s)
+                              : grad_x<__half, 0>(p, dGU, beside, num_sms, status, s);
 }
 
 }  // namespace gemm_gb300
