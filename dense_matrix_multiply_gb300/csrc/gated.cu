@@ -80,7 +80,7 @@ struct Args {
     int M, N;     // of the output: Z, dX or a dW
     int num_kb;   // K blocks of 64 (DX: of both halves together)
     int kb_half;  // DX: blocks of the first half
-    int bn;       // the tile's N extent: FWD 128 or 64; DX 128, 192 or 256; DW 256
+    int bn;       // the tile's N extent: FWD 128 or 64; DX 64, 128, 192 or 256; DW 256
     int batch;    // DW: outputs, 1 or 2; else 1
     int save;     // FWD: store G and U
     int whole;    // tiles computed whole; the rest are split
@@ -604,12 +604,13 @@ bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long 
 constexpr long long fix_time(long long slabs, int columns) { return 14 * 256 + slabs * columns / 5; }
 // Blocks of narrower accumulators: dX of 128 x 12288 x 4096 in one wave takes 0.27 us
 // a block at 256 columns, 0.22 at 192 and 0.205 at 128, forward 1024 x 12160 x 4096
-// 0.33 at 256 and 0.23 at 128.  Where rows of neither operand start on 128 bytes, TMA
+// 0.33 at 256 and 0.23 at 128; at 64 (dX of 333 x 1000 x 1000 10.8 us, at 128 11.9;
+// 700 x 2816 x 1024 takes wider ones) by what is loaded.  Where rows of neither operand start on 128 bytes, TMA
 // asks L2 for two lines for most of a box's rows, and that bounds the blocks: forward
 // of 1024 x 12280 x 4088 165 us, where 1024 x 12288 x 4088 and 1024 x 12280 x 4096, with
 // one such operand, take 122 and 1024 x 12288 x 4096 114.
 constexpr int block_time(int columns, bool rows_on_128) {
-    return (columns == 256 ? 256 : columns == 192 ? 208 : 180) * (rows_on_128 ? 5 : 8) / 5;
+    return (columns == 256 ? 256 : columns == 192 ? 208 : columns == 128 ? 180 : 150) * (rows_on_128 ? 5 : 8) / 5;
 }
 struct Plan {
     long long tiles, time;
@@ -734,7 +735,7 @@ cudaError_t backward(const GatedBackward &p, int dev, int num_sms, int *status, 
     int bn = 0;
     Plan px = {};
     long long best = 0;
-    for (int c = 256; c >= 128; c -= 64) {
+    for (int c = 256; c >= 64; c -= 64) {
         const long long tiles = tiles_m * ((p.K + c - 1LL) / c);
         for (int clusters : {cmax, left}) {
             if (clusters == 0) continue;
