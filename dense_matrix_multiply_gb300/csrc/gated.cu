@@ -605,10 +605,11 @@ constexpr long long fix_time(long long slabs, int columns) { return 14 * 256 + s
 // Blocks of narrower accumulators: dX of 128 x 12288 x 4096 in one wave takes 0.27 us
 // a block at 256 columns, 0.22 at 192 and 0.205 at 128, forward 1024 x 12160 x 4096
 // 0.33 at 256 and 0.23 at 128; at 64 (dX of 333 x 1000 x 1000 10.8 us, at 128 11.9;
-// 700 x 2816 x 1024 takes wider ones) by what is loaded.  Where rows of neither operand start on 128 bytes, TMA
-// asks L2 for two lines for most of a box's rows, and that bounds the blocks: forward
-// of 1024 x 12280 x 4088 165 us, where 1024 x 12288 x 4088 and 1024 x 12280 x 4096, with
-// one such operand, take 122 and 1024 x 12288 x 4096 114.
+// 700 x 2816 x 1024 takes wider ones) by what is loaded.  Where rows of neither
+// operand start on 128 bytes, TMA asks L2 for two lines for most of a box's rows, and
+// that bounds the blocks: forward of 1024 x 12280 x 4088 165 us, where 1024 x 12288 x
+// 4088 and 1024 x 12280 x 4096, with one such operand, take 122 and 1024 x 12288 x 4096
+// 114.
 constexpr int block_time(int columns, bool rows_on_128) {
     return (columns == 256 ? 256 : columns == 192 ? 208 : columns == 128 ? 180 : 150) * (rows_on_128 ? 5 : 8) / 5;
 }
