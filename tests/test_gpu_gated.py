@@ -274,3 +274,42 @@ def test_runs_on_the_callers_stream_and_repeats_bit_for_bit(M):
     assert all(x.float().abs().max() > 0 for x in outs[0])
     for other in outs[1:]:
         assert all(torch.equal(x, y) for x, y in zip(outs[0], other))
+
+
+def test_queued_calls_of_mixed_sizes_repeat_bit_for_bit():
+    """Forward, backward and 4-bit calls queued without a wait: kernels of one call
+    start while the last one's drain, and find its scratch and outputs whole."""
+    cases = []
+    for i, (M, N, K) in enumerate([(1, 500, 300), (64, 1000, 504), (333, 1000, 1000), (500, 1504, 704), (900, 1000, 1792)]):
+        (X, Wg, Wu, dZ), _ = make(M, N, K, "bf16", 20 + i)
+        X, Wg, Wu, dZ = (x.cuda() for x in (X, Wg, Wu, dZ))
+        Q = torch.empty(g.gemm_fp4_code_bytes(N, K), dtype=torch.uint8, device="cuda")
+        S = torch.empty(g.gemm_fp4_scale_bytes("nv", N, K), dtype=torch.uint8, device="cuda")
+        g.gemm_fp4_quantize("bf16", "nv", Wg.t().contiguous(), K, None, Q, S, N, K)
+        cases.append((M, N, K, X, Wg, Wu, dZ, Q, S))
+
+    def outputs(M, N, K):
+        half = lambda r, c: torch.full((r, c), FILL, dtype=torch.bfloat16, device="cuda")
+        full = lambda r, c: torch.full((r, c), FILL, device="cuda")
+        return [half(M, N), full(M, N), full(M, N), half(M, K), half(K, N), half(K, N), half(M, N)]
+
+    def call(case, o):
+        M, N, K, X, Wg, Wu, dZ, Q, S = case
+        g.gemm_gated("bf16", "silu", X, Wg, Wu, *o[:3], M, N, K)
+        g.gemm_gated_backward("bf16", "silu", X, Wg, Wu, o[1], o[2], dZ, *o[3:6], M, N, K)
+        g.gemm_fp4_linear("bf16", "nv", X, K, None, Q, S, None, o[6], N, M, N, K)
+
+    want = []
+    for c in cases:
+        want.append(outputs(*c[:3]))
+        call(c, want[-1])
+        g.gemm_synchronize()
+    order = [int(i) for i in np.random.default_rng(4).integers(0, len(cases), 60)]
+    got = [outputs(*cases[i][:3]) for i in order]
+    torch.cuda.synchronize()
+    for i, o in zip(order, got):
+        call(cases[i], o)
+    g.gemm_synchronize()
+    for i, o in zip(order, got):
+        for k, (x, y) in enumerate(zip(o, want[i])):
+            assert torch.equal(x, y), (cases[i][:3], k)
