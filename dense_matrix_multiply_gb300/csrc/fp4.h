@@ -74,7 +74,8 @@ struct Fp4Scale {
 // is the values', infinities and NaN on top).
 //   MX: e = clamp(floor(log2 amax) - 2, -127, 125), byte e + 127, so that the
 //       largest magnitude lies in [4, 8) steps; the exponent field less 2.
-//   NV: s = E4M3(amax / (6 g)), step s g.
+//   NV: s = E4M3(amax / (6 g)), step s g; a block of zeros has s = 0 whatever g is (a
+//       tensor of zeros has g = 0, and 0 / 0 would make its scale NaN).
 // A NaN or an infinity makes the scale NaN and the codes 0.
 // (quotient() here: an amax below 2^-80, where the remainder could underflow, is
 // under 2^-20 steps of s and rounds to 0 either way; of the codes, a value below
@@ -85,7 +86,9 @@ __device__ __forceinline__ Fp4Scale fp4_block_scale(uint32_t amax_bits, const Fp
     Fp4Scale r;
     if constexpr (NV) {
         const float amax = bad ? 0.0f : __uint_as_float(amax_bits);
-        const float v = t.mid && amax <= 0x1p60f ? quotient(amax, t.g6, t.y6) : amax / t.g6;
+        const float v = amax == 0.0f                  ? 0.0f
+                        : t.mid && amax <= 0x1p60f ? quotient(amax, t.g6, t.y6)
+                                                   : amax / t.g6;
         r.byte = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
         r.step = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)r.byte, __NV_E4M3))) * t.g;
         r.inv = __frcp_rn(r.step);

@@ -266,7 +266,7 @@ GEMM_API gemm_status_t gemm_e4m3_rowscale_fused(const uint16_t *A, const uint8_t
  *                255 = NaN): the OCP microscaling format MXFP4;
  *   GEMM_FP4_NV  blocks of 16, the scale an E4M3FN byte, and one FP32 scale g of
  *                the whole tensor (in device memory, so that it can be computed
- *                there; null: 1).
+ *                there; null: 1), which is not negative.
  *
  * Codes are E2M1 (a sign and 0, 0.5, 1, 1.5, 2, 3, 4, 6), two to a byte, the even
  * k in the low half.  A row takes 16 * ceil(K / 32) bytes; the codes past K are 0.
@@ -283,7 +283,9 @@ GEMM_API gemm_status_t gemm_e4m3_rowscale_fused(const uint16_t *A, const uint8_t
  * code (ties to the even code, saturating at 6), in FP32 operations:
  *   MX  step = 2^e, e = clamp(floor(log2 amax) - 2, -127, 125);
  *   NV  s = E4M3(amax / (6 g)), nearest, saturating at 448; step = s g; codes of
- *       0 where the step is 0.
+ *       0 where the step is 0.  A block of zeros has s = 0 whatever g is, so that a
+ *       tensor of zeros with the scale amax / 2688 = 0 stays one of zeros; with g = 0
+ *       any other block has s = 448 and codes of 0: it reads back, and multiplies, as 0.
  * A NaN or an infinity in a block makes the block's scale NaN and its codes 0:
  * the block reads back as NaN, and products that use it are NaN. */
 typedef enum gemm_fp4_format_t { GEMM_FP4_MX = 0, GEMM_FP4_NV = 1 } gemm_fp4_format_t;
