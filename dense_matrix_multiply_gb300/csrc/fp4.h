@@ -108,6 +108,21 @@ __device__ __forceinline__ Fp4Scale fp4_block_scale(uint32_t amax_bits, const Fp
     return r;
 }
 
+// What a product's FP32 sums are multiplied with, one factor after the other: ga gb and
+// 1 where ga gb is a normal number, or one of them is 0; else (two small scales, or
+// two large ones) the larger and then the smaller, since ga gb would lose bits, vanish
+// or be infinite where the result need not.
+struct Fp4Factors {
+    float first, second;
+};
+template <bool NV>
+__device__ __forceinline__ Fp4Factors fp4_factors(const float *ga, const float *gb) {
+    if (!NV) return {1.0f, 1.0f};
+    const float a = ga ? *ga : 1.0f, b = gb ? *gb : 1.0f, p = a * b;
+    if ((p >= 0x1p-126f && p < __int_as_float(0x7F800000)) || a == 0.0f || b == 0.0f) return {p, 1.0f};
+    return a >= b ? Fp4Factors{a, b} : Fp4Factors{b, a};
+}
+
 // Eight values in steps as codes, the first in the lowest four bits: nearest,
 // ties to the even code, saturating at 6.
 __device__ __forceinline__ uint32_t e2m1x8(const float2 &a, const float2 &b, const float2 &c, const float2 &d) {

@@ -2,8 +2,8 @@
 //     C[i,j] = ga gb sum_k (qa sa)[i,k] (qb sb)[j,k]
 // tcgen05 kind::mxf4nvf4 with block scales: the MMA multiplies E2M1 codes,
 // applies both blocks' scales to each partial sum and accumulates in FP32
-// tensor memory; the tensors' FP32 scales are applied once, in the epilogue,
-// before the one rounding to the output type.
+// tensor memory; the tensors' FP32 scales are applied in the epilogue, before the
+// rounding to the output type.
 //
 // A 256 x bn tile of C belongs to a cluster of two CTAs (cta_group::2): CTA r
 // holds rows [128 r, 128 r + 128) of A's tile and its half of B's, and both
@@ -397,8 +397,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const int quarter = warp & 3, half = (warp - 2) >> 2;
         uint8_t *box = staging + (warp - 2) * STG_BOX;
         uint8_t *rowp = box + lane * 64;
-        const float scale = NV ? (args.ga ? *args.ga : 1.0f) * (args.gb ? *args.gb : 1.0f) : 1.0f;
-        const int groups = bn >> 6, first = half * groups;  // this half's groups of 32 columns
+        const Fp4Factors f = fp4_factors<NV>(args.ga, args.gb);
+        const float2 first = make_float2(f.first, f.first), second = make_float2(f.second, f.second);
+        const int groups = bn >> 6, group0 = half * groups;  // this half's groups of 32 columns
         int it = 0;
         bool ok = true;
         for (int t = cluster; t < num_tiles; t += nclusters, ++it) {
@@ -426,7 +427,7 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
             RowStore out = {box, args.ldc * 2, M - row0, nullptr, 0u};
             for (int i = 0; i < groups; ++i) {
-                const int g = first + (shares && buf == 0 ? i ^ 2 : i);
+                const int g = group0 + (shares && buf == 0 ? i ^ 2 : i);
                 const int c0 = tn * bn + g * 32;
                 uint32_t r[32];
                 if (c0 < N) {  // warp-uniform
@@ -443,8 +444,11 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 __syncwarp();
                 uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    w[j] = pack2(scale * __uint_as_float(r[2 * j]), scale * __uint_as_float(r[2 * j + 1]), (T *)nullptr);
+                for (int j = 0; j < 16; ++j) {
+                    float2 v = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    if (NV) v = mul2(mul2(v, first), second);
+                    w[j] = pack2(v.x, v.y, (T *)nullptr);
+                }
                 if (args.tma_store) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)  // the 64-byte swizzle

@@ -314,7 +314,7 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         }
         fence_after();
         __syncwarp();
-        const float scale = NV ? (args.ga ? *args.ga : 1.0f) * (args.gb ? *args.gb : 1.0f) : 1.0f;
+        const Fp4Factors f = fp4_factors<NV>(args.ga, args.gb);
 #pragma unroll 1
         for (int c = 0; c < M; c += 32) {
             uint32_t r[32];
@@ -330,13 +330,13 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 if (n < N) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (c + j < M) store1(col + (long long)(c + j) * args.ldc, scale * __uint_as_float(r[j]));
+                        if (c + j < M) store1(col + (long long)(c + j) * args.ldc, __uint_as_float(r[j]) * f.first * f.second);
                 }
             } else {
                 // (the ring is drained: every MMA that read it has completed)
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    if (c + j < M) part[(c + j) * LD + nl] = scale * __uint_as_float(r[j]);
+                    if (c + j < M) part[(c + j) * LD + nl] = __uint_as_float(r[j]) * f.first * f.second;
             }
         }
     }
