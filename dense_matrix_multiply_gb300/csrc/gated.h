@@ -49,13 +49,18 @@ cudaError_t launch_gated_backward(const GatedBackward &p, int num_sms, int *stat
 // Both activations are g s(z), s the logistic function: SiLU with z = g, the tanh
 // form of GELU with z = 2 sqrt(2/pi) (g + 0.044715 g^3), since (1 + tanh y) / 2 =
 // s(2 y) -- which also keeps the relative accuracy of the negative tail, where 1 +
-// tanh cancels.  The fast exponential and division are off by a few 2^-22, far
-// below the 2^-9 or 2^-12 of the rounding that follows.
+// tanh cancels.  s from t = e^-|z|, at most 1: 1 / (1 + t), or t / (1 + t) for negative
+// z, whose divisor stays within the fast division's range (1 / (1 + e^-z) would be 0
+// from z = -87.3 down, where g s is still a normal number of bf16).  The fast
+// exponential's relative error grows with its argument, 2 + 1.2 |z| units of 2^-23: under
+// 2^-20 for |z| < 5 and 2^-16 at the end of the range, far below the 2^-9 or 2^-12 of
+// the rounding that follows; the division adds 2 units.
 template <bool GELU>
 __device__ __forceinline__ float gate_sigmoid(float g) {
     constexpr float c2 = 1.5957691216057308f, c3 = 0.044715f;  // 2 sqrt(2 / pi)
     const float z = GELU ? c2 * g * fmaf(c3 * g, g, 1.0f) : g;
-    return __fdividef(1.0f, 1.0f + __expf(-z));
+    const float t = __expf(-fabsf(z));
+    return __fdividef(z < 0.0f ? t : 1.0f, 1.0f + t);
 }
 template <bool GELU>
 __device__ __forceinline__ float gate_act(float g) { return g * gate_sigmoid<GELU>(g); }
