@@ -367,6 +367,8 @@ def gemm_fp4_code_bytes(rows: int, K: int) -> int:
 
 def gemm_fp4_scale_bytes(fmt: str, rows: int, K: int) -> int:
     """Bytes of the block scales of a [rows, K] matrix in format 'mx' or 'nv'."""
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"gemm_fp4_scale_bytes: format 'mx' | 'nv', got {fmt!r}")
     return int(load().gemm_fp4_scale_bytes(FP4_FORMATS[fmt], int(rows), int(K)))
 
 
