@@ -15,38 +15,17 @@
 #include "gated.h"
 #include "gemm.h"
 #include "internal.h"
+#include "scratch.h"
 
 using namespace gemm_gb300;
 
 std::atomic<unsigned long long> gemm_gb300::g_launches{0};
 
 namespace {
-struct ScratchPool {
-    std::once_flag once;
-    cudaMemPool_t pool = nullptr;
-    cudaError_t err = cudaSuccess;
-};
-ScratchPool g_scratch[kMaxDevices];
+ScratchPools g_scratch;
 }  // namespace
 
-cudaError_t gemm_gb300::scratch_alloc(void **p, size_t bytes, cudaStream_t s) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    ScratchPool &d = g_scratch[dev];
-    std::call_once(d.once, [&] {
-        cudaMemPoolProps props = {};
-        props.allocType = cudaMemAllocationTypePinned;
-        props.location.type = cudaMemLocationTypeDevice;
-        props.location.id = dev;
-        d.err = cudaMemPoolCreate(&d.pool, &props);
-        unsigned long long keep = kScratchKept;
-        if (d.err == cudaSuccess) d.err = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep);
-    });
-    if (d.err != cudaSuccess) return d.err;
-    return cudaMallocFromPoolAsync(p, bytes, d.pool, s);
-}
+cudaError_t gemm_gb300::scratch_alloc(void **p, size_t bytes, cudaStream_t s) { return g_scratch.alloc(p, bytes, s); }
 
 namespace {
 

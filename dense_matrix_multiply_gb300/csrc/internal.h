@@ -102,11 +102,8 @@ struct ProblemEx {
 };
 
 // Stream-ordered scratch of the 4-bit and gated operators, from a pool of the
-// library's own on the current device that keeps up to kScratchKept bytes across
-// synchronisations.  (The device's default pool gives everything back whenever
-// the stream is waited for; mapping it anew cost a call that is waited for
-// 200 us.)  Free with cudaFreeAsync on the same stream.
-constexpr unsigned long long kScratchKept = 1ull << 30;
+// library's own on the current device (scratch.h).  Free with cudaFreeAsync on the
+// same stream.
 cudaError_t scratch_alloc(void **p, size_t bytes, cudaStream_t s);
 
 // FP32 (or 16-bit fallback) SIMT kernel on the CUDA cores.  vec4: float4
