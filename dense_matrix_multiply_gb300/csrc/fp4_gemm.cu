@@ -37,7 +37,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "fp4.h"
 #include "tc_ptx.cuh"
@@ -489,12 +488,9 @@ fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
 template <typename T, bool NV>
 int clusters_max(int dev) {
-    static std::atomic<int> cached[kMaxDevices];
-    static std::once_flag once[kMaxDevices];
-    std::call_once(once[dev], [&] {
-        cached[dev].store(max_clusters(reinterpret_cast<const void *>(fp4_pair_kernel<T, NV>), THREADS, smem_bytes(NV), 2));
-    });
-    return cached[dev].load();
+    static std::atomic<int> known[kMaxDevices];
+    return cluster_limit(known[dev], reinterpret_cast<const void *>(fp4_pair_kernel<T, NV>), THREADS,
+                         smem_bytes(NV), 2);
 }
 
 template <typename T, bool NV>

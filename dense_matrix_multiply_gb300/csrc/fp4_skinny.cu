@@ -23,7 +23,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "fp4.h"
 #include "tc_ptx.cuh"
@@ -387,13 +386,9 @@ fp4_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
 
 template <typename T, bool NV, bool FUSED>
 int clusters_max(int dev, int cs) {
-    static std::atomic<int> cached[kMaxDevices][9];
-    static std::once_flag once[kMaxDevices][9];
-    std::call_once(once[dev][cs], [&] {
-        cached[dev][cs].store(
-            max_clusters(reinterpret_cast<const void *>(fp4_skinny_kernel<T, NV, FUSED>), THREADS, SMEM, cs));
-    });
-    return cached[dev][cs].load();
+    static std::atomic<int> known[kMaxDevices][9];
+    return cluster_limit(known[dev][cs], reinterpret_cast<const void *>(fp4_skinny_kernel<T, NV, FUSED>),
+                         THREADS, SMEM, cs);
 }
 
 template <typename T, bool NV, bool FUSED>
@@ -405,8 +400,11 @@ cudaError_t launch(const Fp4Problem &p, const void *X, long long ldx, int num_sm
     const long long strips = fp4_row_tiles(p.N), num_kb = (p.K + KB - 1LL) / KB;
     int cs = 1;
     if (clusters_max<T, NV, FUSED>(dev, 1) <= 0) return cudaErrorNotSupported;
-    for (int c = 2; c <= 8 && c <= num_kb && strips * c <= 2LL * num_sms; ++c)
-        if (clusters_max<T, NV, FUSED>(dev, c) >= strips) cs = c;
+    for (int c = 2; c <= 8 && c <= num_kb && strips * c <= 2LL * num_sms; ++c) {
+        const int n = clusters_max<T, NV, FUSED>(dev, c);
+        if (n < 0) return cudaErrorNotSupported;  // not another split, whose sums would differ
+        if (n >= strips) cs = c;
+    }
     const long long rb = fp4_row_bytes(p.K), chunks = (long long)fp4_atoms(NV, p.K) / 2;
     constexpr int SFC = sf_stage(NV) / 1024;
     const int nb = nb_of(p.M);

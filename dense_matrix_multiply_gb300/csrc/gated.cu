@@ -33,7 +33,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "gated.h"
 #include "tc_ptx.cuh"
@@ -572,13 +571,9 @@ gated_fix_kernel(const float *__restrict__ part, T *out0, T *out1, float *G, flo
 
 template <typename T, uint32_t FORMAT, int MODE, bool GELU>
 int clusters_max(int dev) {
-    static std::atomic<int> cached[kMaxDevices];
-    static std::once_flag once[kMaxDevices];
-    std::call_once(once[dev], [&] {
-        cached[dev].store(max_clusters(reinterpret_cast<const void *>(gated_pair_kernel<T, FORMAT, MODE, GELU>), THREADS,
-                                       smem_bytes(MODE), 2));
-    });
-    return cached[dev].load();
+    static std::atomic<int> known[kMaxDevices];
+    return cluster_limit(known[dev], reinterpret_cast<const void *>(gated_pair_kernel<T, FORMAT, MODE, GELU>), THREADS,
+                         smem_bytes(MODE), 2);
 }
 
 constexpr CUtensorMapDataType map_type(uint32_t format) {

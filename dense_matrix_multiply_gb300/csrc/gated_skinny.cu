@@ -22,7 +22,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "gated.h"
 #include "tc_ptx.cuh"
@@ -302,13 +301,9 @@ gated_skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_consta
 
 template <typename T, uint32_t FORMAT, bool DX, bool GELU>
 int clusters_max(int dev, int cs) {
-    static std::atomic<int> cached[kMaxDevices][9];
-    static std::once_flag once[kMaxDevices][9];
-    std::call_once(once[dev][cs], [&] {
-        cached[dev][cs].store(
-            max_clusters(reinterpret_cast<const void *>(gated_skinny_kernel<T, FORMAT, DX, GELU>), THREADS, SMEM, cs));
-    });
-    return cached[dev][cs].load();
+    static std::atomic<int> known[kMaxDevices][9];
+    return cluster_limit(known[dev][cs], reinterpret_cast<const void *>(gated_skinny_kernel<T, FORMAT, DX, GELU>),
+                         THREADS, SMEM, cs);
 }
 
 constexpr CUtensorMapDataType map_type(uint32_t format) {
@@ -326,8 +321,11 @@ cudaError_t launch(const CUtensorMap &tx, const CUtensorMap &tg, const CUtensorM
     const long long strips = (a.N + STRIP - 1LL) / STRIP;
     if (clusters_max<T, FORMAT, DX, GELU>(dev, 1) <= 0) return cudaErrorNotSupported;
     int cs = 1;
-    for (int c = 2; c <= 8 && c <= a.num_kb && strips * c <= 2LL * num_sms; ++c)
-        if (clusters_max<T, FORMAT, DX, GELU>(dev, c) >= strips) cs = c;
+    for (int c = 2; c <= 8 && c <= a.num_kb && strips * c <= 2LL * num_sms; ++c) {
+        const int n = clusters_max<T, FORMAT, DX, GELU>(dev, c);
+        if (n < 0) return cudaErrorNotSupported;  // not another split, whose sums would differ
+        if (n >= strips) cs = c;
+    }
     a.cs = cs;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(strips * cs), 1, 1);

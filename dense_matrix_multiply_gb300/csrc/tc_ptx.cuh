@@ -8,9 +8,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
-#include <mutex>
-
 #include "internal.h"
+#include "launch_setup.h"
 
 namespace gemm_gb300 {
 namespace tc {
@@ -256,23 +255,6 @@ __device__ __forceinline__ void store1(__nv_bfloat16 *p, float x) { *p = __float
 __device__ __forceinline__ void store1(__half *p, float x) { *p = __float2half_rn(x); }
 
 // ---- host: tensor maps
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-inline EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
 // 3-D map: extents and box in elements, strides of the two outer dimensions in
 // bytes (multiples of 16), swizzle in bytes (0, 64, 128), zero fill out of bounds.
 inline bool make_map3(CUtensorMap *map, const void *base, CUtensorMapDataType dt, long long d0, long long d1,
@@ -287,27 +269,6 @@ inline bool make_map3(CUtensorMap *map, const void *base, CUtensorMapDataType dt
               swizzle == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                              : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-// Largest number of co-resident clusters of `cs` CTAs (0: none), after raising
-// the kernel's shared-memory limit.
-inline int max_clusters(const void *kern, int threads, int smem, int cs) {
-    int n = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)cs, 1, 1);
-        cfg.blockDim = dim3((unsigned)threads, 1, 1);
-        cfg.dynamicSmemBytes = (size_t)smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)cs;
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
-    }
-    cudaGetLastError();
-    return n;
 }
 
 }  // namespace tc
