@@ -37,12 +37,12 @@ thread_local char t_last_error[256] = "";
 thread_local Family t_force = Family::Auto;
 
 struct DeviceInfo {
-    std::once_flag once;
+    std::mutex setup;
+    std::atomic<bool> known{false};  // set once the device has been looked at
     std::atomic<bool> ready{false};  // set once the status word exists
     bool supported = false;
     int num_sms = 0;
     int *status = nullptr;  // device word the tensor-core kernel reports timeouts in
-    cudaError_t init_error = cudaSuccess;
 };
 DeviceInfo g_devices[kMaxDevices];
 
@@ -98,27 +98,56 @@ void record_cuda_error(cudaError_t e) {
     t_last_error[sizeof(t_last_error) - 1] = '\0';
 }
 
-// Per-device set-up on first use: capability check, SM count, status word.
+// A zeroed device word.  The calling thread may be capturing a stream, which has no part
+// in this: allocations are allowed meanwhile, and the word is zeroed on a stream that
+// waits for no other.
+cudaError_t make_status_word(int **out) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    int *word = nullptr;
+    cudaStream_t s = nullptr;
+    e = cudaMalloc(&word, sizeof(int));
+    if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e == cudaSuccess) e = cudaMemsetAsync(word, 0, sizeof(int), s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (s) cudaStreamDestroy(s);
+    if (e != cudaSuccess && word) cudaFree(word);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e == cudaSuccess) *out = word;
+    return e != cudaSuccess ? e : back;
+}
+
+cudaError_t set_up(DeviceInfo &d, int dev) {
+    int major = 0, minor = 0;
+    cudaError_t e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && major == 10 && minor == 3) {
+        d.supported = true;
+        if (!d.status) e = make_status_word(&d.status);
+        if (e == cudaSuccess) d.ready.store(true, std::memory_order_release);
+    }
+    if (e != cudaSuccess) cudaGetLastError();  // reported by this call, found by no later one
+    return e;
+}
+
+// Per-device set-up on first use: capability check, SM count, status word.  One that
+// failed is tried again by the next call.
 gemm_status_t device_info(DeviceInfo **out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) { record_cuda_error(e); return GEMM_ERR_CUDA; }
     if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED_DEVICE;
     DeviceInfo &d = g_devices[dev];
-    std::call_once(d.once, [&] {
-        int major = 0, minor = 0;
-        cudaError_t err = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-        if (err == cudaSuccess) err = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-        if (err == cudaSuccess) err = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
-        if (err != cudaSuccess) { d.init_error = err; return; }
-        d.supported = (major == 10 && minor == 3);
-        if (!d.supported) return;
-        err = cudaMalloc(&d.status, sizeof(int));
-        if (err == cudaSuccess) err = cudaMemset(d.status, 0, sizeof(int));
-        if (err != cudaSuccess) d.init_error = err;
-        else d.ready.store(true, std::memory_order_release);
-    });
-    if (d.init_error != cudaSuccess) { record_cuda_error(d.init_error); return GEMM_ERR_CUDA; }
+    if (!d.known.load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(d.setup);
+        if (!d.known.load(std::memory_order_relaxed)) {
+            e = set_up(d, dev);
+            if (e != cudaSuccess) { record_cuda_error(e); return GEMM_ERR_CUDA; }
+            d.known.store(true, std::memory_order_release);
+        }
+    }
     if (!d.supported) return GEMM_ERR_UNSUPPORTED_DEVICE;
     *out = &d;
     return GEMM_OK;
