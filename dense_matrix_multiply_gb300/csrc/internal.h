@@ -16,19 +16,36 @@ namespace gemm_gb300 {
 // Programmatic dependent launch.  Every kernel is launched with programmatic
 // stream serialisation allowed: it may start while the previous kernel on the
 // stream drains.  After a prologue that touches only its shared memory, tensor
-// memory and parameters -- the skinny kernels add L2 prefetch hints for their
-// first weight tiles, which read nothing and change no value a later load
+// memory and parameters -- the weight streams (skinny kernels) add L2 prefetch hints
+// for their first weight tiles, which read nothing and change no value a later load
 // returns -- it waits for the previous grid to complete and its writes to
 // become visible (pdl_wait) before its first global-memory access.
-// The tensor-core kernels (one CTA per SM) also let their own dependents launch
-// at once (pdl_launch_dependents) -- the skinny ones once every CTA has issued
-// its last load, so that the dependent's CTAs prefetch their first weights
-// into L2 while this grid drains; kernels with several CTAs per SM leave that
-// to their CTAs' exit, so that a small grid's successor is not placed, and
-// packed onto the same SMs, while the grid still runs (FP32 1000^3: 86 against
-// 49 us).  The one exception is the first grid of an FP32 problem split in two,
-// whose dependent is its own last round (that packing is the point).  Back to back on GB300 this hides the 2-3 us between kernels: a
-// 100 MB weight stream went from 18.5 to 15.9 us.
+//
+// Two grids read and write global memory before they wait, and wait before they end,
+// so that whatever follows finds the grid before them complete as well.  Both rest on
+// what the launch order of their own call says of the grid before them:
+//  - the last round of an FP32 problem split in two (simt_gemm.cu, MODE 2) reads A and B,
+//    which its first grid only reads, and writes other tiles of C;
+//  - dX beside dW (gated.cu, gated_skinny.cu; args.beside) reads dG, dU and the weights,
+//    which dW does not write.  It has no wait of its own behind it when it reads: dW
+//    lets it start only after dW's own wait, so that every grid before dW -- the one
+//    that wrote dG and dU, those that padded operands, and whatever used dX's buffer -- is
+//    complete, its writes in memory, before dX's first instruction.  It is launched so
+//    only directly behind dW, never behind the kernel that adds dW's split tiles.
+//
+// When dependents may start (pdl_launch_dependents):
+//  - at once, from the tensor-core kernels with one CTA per SM (dW: after its wait, as
+//    above), and from the quantiser (fp4.cu) and the gate's gradients (gated.cu), whose
+//    dependents are such kernels or weight streams, set up meanwhile;
+//  - from the weight streams, once every CTA has issued its last load, so that the
+//    dependent's CTAs prefetch their first weights into L2 while this grid drains;
+//  - from the first grid of an FP32 problem split in two, after its wait, for its last
+//    round (packed onto the same SMs: that is the point);
+//  - from all other kernels with several CTAs per SM as their CTAs exit, so that a small
+//    grid's successor is not placed, and packed onto the same SMs, while the grid still
+//    runs (FP32 1000^3: 86 against 49 us).
+// Back to back on GB300 this hides the 2-3 us between kernels: a 100 MB weight stream
+// went from 18.5 to 15.9 us.
 #ifndef GEMM_PDL
 #define GEMM_PDL 1
 #endif
