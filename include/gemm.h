@@ -29,8 +29,9 @@
  * leave a nearly empty last wave (at most a quarter of the clusters busy, K of
  * at least 48 blocks of 64) takes FP32 partial tiles for its stream-K tail from
  * the same pool (512 KiB per participating CTA pair, at most ~39 MB), freed on
- * the stream after the call; without it the call runs whole tiles.  The
- * allocation-free entry point never allocates.
+ * the stream after the call; without it the call runs whole tiles.  The FP8, 4-bit
+ * and gated entry points name their scratch below.  The allocation-free entry point
+ * never allocates.
  *
  * Leading dimensions are tight:
  *   _rm (row-major):    A is [M,K] with lda = K, B is [K,N] with ldb = N,
@@ -329,16 +330,21 @@ GEMM_API gemm_status_t gemm_fp4_linear(gemm_dtype_t dtype, gemm_fp4_format_t for
 /* Gated feed-forward projections, for training and serving:
  *     G = X W_g,  U = X W_u,  Z = act(G) * U  (element by element)
  * X [M,K], W_g and W_u [K,N], Z [M,N] row-major half or bf16 (dtype) with tight
- * strides, both products and the activation in one kernel; G, U and act in FP32,
- * Z rounded once.  act: SiLU, g / (1 + e^-g), or the tanh form of GELU,
+ * strides, both products and the activation in one kernel (a second one adds FP32
+ * partials where the last wave of tiles is split along K, for M > 64); G, U and act in
+ * FP32, Z rounded once.  act: SiLU, g / (1 + e^-g), or the tanh form of GELU,
  * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2.  G and U (both or neither):
  * FP32 [M,N], stored for gemm_gated_backward.  (gemm_bf16_rm_silu_mul keeps the
  * rounding points of the unfused chain instead: G, U and act(G) rounded to bf16.)
  * Any M, N, K: one token to a long prompt.  Operands that are not 16-byte aligned,
- * or whose N or K is no multiple of 8, are copied to or from padded rows in
- * stream-ordered scratch, which costs a pass over each of them; so is X for a long
- * product with neither N nor K a multiple of 64.  N or K a multiple of 64 is fastest.  K = 0 gives
- * zeros.  GEMM_ERR_ALIAS if an output overlaps an input or another output. */
+ * or whose N or K is no multiple of 8, are copied to or from padded rows in scratch,
+ * which costs a pass over each of them; so is X for a long product with neither N
+ * nor K a multiple of 64.  N or K a multiple of 64 is fastest.  Scratch, for these
+ * copies and the partials (256 KiB each, one at most for every two SMs), is
+ * stream-ordered and lives for the duration of the call, from a pool of the
+ * library's own that keeps up to 1 GiB on the device between calls; M <= 64 with
+ * aligned operands takes none.  K = 0 gives zeros.  GEMM_ERR_ALIAS if an output
+ * overlaps an input or another output. */
 typedef enum gemm_act_t { GEMM_ACT_SILU = 0, GEMM_ACT_GELU_TANH = 1 } gemm_act_t;
 
 GEMM_API gemm_status_t gemm_gated(gemm_dtype_t dtype, gemm_act_t act, const void *X, const void *W_g, const void *W_u,
@@ -350,10 +356,10 @@ GEMM_API gemm_status_t gemm_gated(gemm_dtype_t dtype, gemm_act_t act, const void
  * dX [M,K], dW_g and dW_u [K,N] (dtype), each overwritten; a null one is left out
  * (and X, W_g, W_u may be null where nothing that is asked for reads them).  dG
  * and dU are formed in FP32 and rounded to dtype, the operands of the products,
- * whose sums are FP32, rounded once.  dG, dU and, with few rows, FP32 partials of
- * dX lie in stream-ordered scratch (from a pool of the library's own that keeps up
- * to 1 GiB on the device between calls).  M = 0 or N = 0 gives zeros.  Needs and
- * errors as gemm_gated. */
+ * whose sums are FP32, rounded once.  dG, dU (rows of whole 128 bytes) and, where
+ * the last wave of tiles of dX (M > 64) or of the weight gradients is split along its
+ * sum, FP32 partials as in gemm_gated lie in the same scratch.  M = 0 or
+ * N = 0 gives zeros.  Needs and errors as gemm_gated. */
 GEMM_API gemm_status_t gemm_gated_backward(gemm_dtype_t dtype, gemm_act_t act, const void *X, const void *W_g,
                                            const void *W_u, const float *G, const float *U, const void *dZ, void *dX,
                                            void *dW_g, void *dW_u, int M, int N, int K);
