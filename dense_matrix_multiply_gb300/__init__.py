@@ -168,31 +168,30 @@ def _check(name: str, t, elt_size: int, need: int, tight: bool = True) -> None:
         raise ValueError(f"{name} holds {room} elements, the call needs {need}")
 
 
-def _rows_apart(t, ld: int, need: int) -> bool:
-    """Whether the elements of t lie as a matrix with leading dimension ld that
-    spans `need` elements has them: unit stride along a row and, if there are
-    several, ld from one row to the next (through any further dimensions).  A flat
-    buffer has no rows of its own."""
+def _check_rows(name: str, t, ld: int, need: int) -> None:
+    """A tensor in the place of a matrix with leading dimension ld that spans `need`
+    elements: unit stride along a row and, if there are several, ld from one row to
+    the next (through any further dimensions).  A flat buffer has no rows of its own."""
+    if not need or t is None or type(t) is int or t.stride() == (ld, 1):
+        return
     size, stride = t.shape, t.stride()
-    if len(size) and size[-1] > 1 and stride[-1] != 1:
-        return False
+    good = not len(size) or size[-1] <= 1 or stride[-1] == 1
     if need > ld:
         step = ld
         for n, apart in zip(size[-2::-1], stride[-2::-1]):
-            if n > 1 and apart != step:
-                return False
+            good = good and (n <= 1 or apart == step)
             step *= n
-    return True
+    if not good:
+        raise ValueError(f"{name} must have rows of adjacent elements, {ld} elements apart; its strides are {stride}")
 
 
 def _take(lib, name: str, *args):
     """Addresses of several tensor arguments (argument, tensor, element size,
-    elements, strides), each checked as by _check -- a contiguous tensor with
-    room passes without a message being built -- and all on one CUDA device, to whose
-    current torch stream the library is pointed.  strides: None for a tight operand,
-    (ld, 1) for one with a leading dimension, which the tensor has to agree with."""
+    elements, tight), each checked as by _check -- a contiguous tensor with room
+    passes without a message being built -- and all on one CUDA device, to whose
+    current torch stream the library is pointed."""
     out, dev, mixed = [], None, False
-    for arg, t, size, need, apart in args:
+    for arg, t, size, need, tight in args:
         if t is None:
             out.append(0)
             continue
@@ -200,10 +199,7 @@ def _take(lib, name: str, *args):
             out.append(t)
             continue
         if t.element_size() != size or not t.is_contiguous() or t.numel() < need:
-            _check(f"{name}: {arg}", t, size, need, not apart)
-        if apart and t.stride() != apart and need and not _rows_apart(t, apart[0], need):
-            raise ValueError(f"{name}: {arg} must have rows of adjacent elements, {apart[0]} elements apart; "
-                             f"its strides are {t.stride()}")
+            _check(f"{name}: {arg}", t, size, need, tight)
         d = t.get_device()
         if d != dev:
             mixed = dev is not None
@@ -381,6 +377,11 @@ def _fp4_sizes(fmt: int, rows: int, K: int):
     return rows * ((K + 31) // 32 * 16), (rows + 127) // 128 * ((K + 255) // 256) * (2048 if fmt else 1024), 1
 
 
+def _fp4_span(rows: int, cols: int, ld: int) -> int:
+    """_span of one matrix."""
+    return (rows - 1) * ld + cols if rows > 0 and cols > 0 and ld >= 0 else 0
+
+
 def gemm_fp4_quantize(dtype: str, fmt: str, A, lda: int, tensor_scale, Q, S, M: int, K: int) -> None:
     """Quantises A [M,K] ('f16' | 'bf16', leading dimension lda) to 4-bit codes Q
     and block scales S, format 'mx' or 'nv'; tensor_scale: one FP32 value on the
@@ -391,8 +392,10 @@ def gemm_fp4_quantize(dtype: str, fmt: str, A, lda: int, tensor_scale, Q, S, M: 
     d, f = _fp4_enums("gemm_fp4_quantize", dtype, fmt)
     M, K, lda = int(M), int(K), int(lda)
     nq, ns, ng = _fp4_sizes(f, M, K)
-    a, q, s, g = _take(lib, "gemm_fp4_quantize", ("A", A, 2, _span(M, K, lda), (lda, 1)),
-                       ("Q", Q, 1, nq, None), ("S", S, 1, ns, None), ("tensor_scale", tensor_scale, 4, ng, None))
+    na = _fp4_span(M, K, lda)
+    _check_rows("gemm_fp4_quantize: A", A, lda, na)
+    a, q, s, g = _take(lib, "gemm_fp4_quantize", ("A", A, 2, na, False),
+                       ("Q", Q, 1, nq, True), ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
     st = lib.gemm_fp4_quantize(d, f, a, lda, g, q, s, M, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4_quantize", lib.gemm_last_error().decode())
@@ -404,8 +407,10 @@ def gemm_fp4_dequantize(dtype: str, fmt: str, Q, S, tensor_scale, A, lda: int, M
     d, f = _fp4_enums("gemm_fp4_dequantize", dtype, fmt)
     M, K, lda = int(M), int(K), int(lda)
     nq, ns, ng = _fp4_sizes(f, M, K)
-    a, q, s, g = _take(lib, "gemm_fp4_dequantize", ("A", A, 2, _span(M, K, lda), (lda, 1)),
-                       ("Q", Q, 1, nq, None), ("S", S, 1, ns, None), ("tensor_scale", tensor_scale, 4, ng, None))
+    na = _fp4_span(M, K, lda)
+    _check_rows("gemm_fp4_dequantize: A", A, lda, na)
+    a, q, s, g = _take(lib, "gemm_fp4_dequantize", ("A", A, 2, na, False),
+                       ("Q", Q, 1, nq, True), ("S", S, 1, ns, True), ("tensor_scale", tensor_scale, 4, ng, True))
     st = lib.gemm_fp4_dequantize(d, f, q, s, g, a, lda, M, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4_dequantize", lib.gemm_last_error().decode())
@@ -420,10 +425,12 @@ def gemm_fp4(dtype: str, fmt: str, Qa, Sa, ga, Qb, Sb, gb, C, ldc: int, M: int, 
     some = M > 0 and N > 0  # else a no-op or a call that the library rejects
     qa, sa, na = _fp4_sizes(f, M, K if some else 0)
     qb, sb, nb = _fp4_sizes(f, N, K if some else 0)
+    nc = _fp4_span(M, N, ldc)
+    _check_rows("gemm_fp4: C", C, ldc, nc)
     pqa, psa, pga, pqb, psb, pgb, c = _take(
-        lib, "gemm_fp4", ("Qa", Qa, 1, qa, None), ("Sa", Sa, 1, sa, None), ("ga", ga, 4, na, None),
-        ("Qb", Qb, 1, qb, None), ("Sb", Sb, 1, sb, None), ("gb", gb, 4, nb, None),
-        ("C", C, 2, _span(M, N, ldc), (ldc, 1)))
+        lib, "gemm_fp4", ("Qa", Qa, 1, qa, True), ("Sa", Sa, 1, sa, True), ("ga", ga, 4, na, True),
+        ("Qb", Qb, 1, qb, True), ("Sb", Sb, 1, sb, True), ("gb", gb, 4, nb, True),
+        ("C", C, 2, nc, False))
     st = lib.gemm_fp4(d, f, pqa, psa, pga, pqb, psb, pgb, c, ldc, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4", lib.gemm_last_error().decode())
@@ -437,10 +444,13 @@ def gemm_fp4_linear(dtype: str, fmt: str, X, ldx: int, gx, Qw, Sw, gw, C, ldc: i
     M, N, K, ldx, ldc = int(M), int(N), int(K), int(ldx), int(ldc)
     some = M > 0 and N > 0  # else a no-op or a call that the library rejects
     qw, sw, nw = _fp4_sizes(f, N, K if some else 0)
+    nx, nc = _fp4_span(M, K, ldx) if some else 0, _fp4_span(M, N, ldc)
+    _check_rows("gemm_fp4_linear: X", X, ldx, nx)
+    _check_rows("gemm_fp4_linear: C", C, ldc, nc)
     x, pgx, q, s, pgw, c = _take(
-        lib, "gemm_fp4_linear", ("X", X, 2, _span(M, K, ldx) if some else 0, (ldx, 1)), ("gx", gx, 4, nw, None),
-        ("Qw", Qw, 1, qw, None), ("Sw", Sw, 1, sw, None), ("gw", gw, 4, nw, None),
-        ("C", C, 2, _span(M, N, ldc), (ldc, 1)))
+        lib, "gemm_fp4_linear", ("X", X, 2, nx, False), ("gx", gx, 4, nw, True),
+        ("Qw", Qw, 1, qw, True), ("Sw", Sw, 1, sw, True), ("gw", gw, 4, nw, True),
+        ("C", C, 2, nc, False))
     st = lib.gemm_fp4_linear(d, f, x, ldx, pgx, q, s, pgw, c, ldc, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp4_linear", lib.gemm_last_error().decode())
@@ -462,8 +472,8 @@ def gemm_gated(dtype: str, act: str, X, W_g, W_u, Z, G, U, M: int, N: int, K: in
     d, a = _gated_enums("gemm_gated", dtype, act)
     M, N, K = int(M), int(N), int(K)
     nx, nw, nz = _dims(M, N, K)
-    p = _take(lib, "gemm_gated", ("X", X, 2, nx, None), ("W_g", W_g, 2, nw, None), ("W_u", W_u, 2, nw, None),
-              ("Z", Z, 2, nz, None), ("G", G, 4, nz, None), ("U", U, 4, nz, None))
+    p = _take(lib, "gemm_gated", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
+              ("Z", Z, 2, nz, True), ("G", G, 4, nz, True), ("U", U, 4, nz, True))
     st = lib.gemm_gated(d, a, *p, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated", lib.gemm_last_error().decode())
@@ -476,9 +486,9 @@ def gemm_gated_backward(dtype: str, act: str, X, W_g, W_u, G, U, dZ, dX, dW_g, d
     d, a = _gated_enums("gemm_gated_backward", dtype, act)
     M, N, K = int(M), int(N), int(K)
     nx, nw, nz = (M * K, K * N, M * N) if min(M, N, K) >= 0 else (0, 0, 0)
-    p = _take(lib, "gemm_gated_backward", ("X", X, 2, nx, None), ("W_g", W_g, 2, nw, None), ("W_u", W_u, 2, nw, None),
-              ("G", G, 4, nz, None), ("U", U, 4, nz, None), ("dZ", dZ, 2, nz, None), ("dX", dX, 2, nx, None),
-              ("dW_g", dW_g, 2, nw, None), ("dW_u", dW_u, 2, nw, None))
+    p = _take(lib, "gemm_gated_backward", ("X", X, 2, nx, True), ("W_g", W_g, 2, nw, True), ("W_u", W_u, 2, nw, True),
+              ("G", G, 4, nz, True), ("U", U, 4, nz, True), ("dZ", dZ, 2, nz, True), ("dX", dX, 2, nx, True),
+              ("dW_g", dW_g, 2, nw, True), ("dW_u", dW_u, 2, nw, True))
     st = lib.gemm_gated_backward(d, a, *p, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated_backward", lib.gemm_last_error().decode())
