@@ -16,10 +16,10 @@
 // Bound: HBM, 2 bytes read and 0.53 (MX) or 0.56 (NV) written an element, or the
 // other way round; NV's quantiser by its arithmetic nearly as much (a quotient of
 // three operations an element, two elements to an instruction).  Measured back to
-// back from DRAM: bf16 16384 x 8192 NV quantised in 59.4 us (5.79 TB/s, 0.87 of the
-// copy bandwidth) and read back in 53.3 (6.45, 0.97); 4096 x 4096 MX 7.7 and 8.0 us,
-// NV 9.4 and 8.2; f16 777 x 12300 NV (rows on 8 bytes) 7.4 and 6.7; 4096 x 4095 NV
-// (rows on 2) 13.2 and 11.3.  Two rows to a
+// back from DRAM: bf16 16384 x 8192 NV quantised in 60.6 us (5.67 TB/s, 0.85 of the
+// copy bandwidth) and read back in 53.1 (6.47, 0.97); 4096 x 4096 MX 7.8 and 8.0 us,
+// NV 9.7 and 8.2; f16 777 x 12300 NV (rows on 8 bytes) 7.6 and 6.6; 4096 x 4095 NV
+// (rows on 2) 13.5 and 11.0, by the instructions of the shifts.  Two rows to a
 // warp and four warps to a block: one row 75.9 and 66.1 us for the first, four rows
 // 70.5 and 61.3, eight warps 68.4 and 63.7, against 63.3 and 59.4 (before row
 // addresses were formed once a row, 12.9 instructions an element of the read-back).
