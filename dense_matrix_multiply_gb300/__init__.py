@@ -51,6 +51,9 @@ SIGNATURES = {
     "gemm_fp4_linear": ([_I, _I, _VP, ctypes.c_int64, _VP, _VP, _VP, _VP, _VP, ctypes.c_int64, _I, _I, _I], _I),
     "gemm_gated": ([_I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
     "gemm_gated_backward": ([_I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
+    "gemm_rms_norm": ([_I, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _I, _I], _I),
+    "gemm_rms_norm_e4m3": ([_I, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _I, _I], _I),
+    "gemm_rms_norm_backward": ([_I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I], _I),
     "gemm_set_stream": ([_VP], _I),
     "gemm_get_stream": ([], _VP),
     "gemm_synchronize": ([], _I),
@@ -492,6 +495,63 @@ def gemm_gated_backward(dtype: str, act: str, X, W_g, W_u, G, U, dZ, dX, dW_g, d
     st = lib.gemm_gated_backward(d, a, *p, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_gated_backward", lib.gemm_last_error().decode())
+
+
+def _dtype16(name: str, dtype: str) -> int:
+    if dtype not in _DTYPES16:
+        raise ValueError(f"{name}: dtype 'f16' | 'bf16', got {dtype!r}")
+    return _DTYPES16[dtype]
+
+
+def gemm_rms_norm(dtype: str, X, R, w, eps: float, H, Y, rstd, M: int, K: int) -> None:
+    """H = X + R, Y = w H / sqrt(mean(H^2) + eps) over rows of K ('f16' | 'bf16').  R None:
+    no residual (H None too); H None: the sum is not kept; H may be X or R itself; w
+    None: ones; rstd (FP32 [M], or None) is kept for gemm_rms_norm_backward."""
+    lib = _lib or load()
+    d = _dtype16("gemm_rms_norm", dtype)
+    M, K = int(M), int(K)
+    n, m, k = _rows_dims(M, K)
+    x, r, pw, h, y, rs = _take(lib, "gemm_rms_norm", ("X", X, 2, n, True), ("R", R, 2, n, True), ("w", w, 2, k, True),
+                               ("H", H, 2, n, True), ("Y", Y, 2, n, True), ("rstd", rstd, 4, m, True))
+    st = lib.gemm_rms_norm(d, x, r, pw, eps, h, y, rs, M, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_rms_norm", lib.gemm_last_error().decode())
+
+
+def gemm_rms_norm_e4m3(dtype: str, X, R, w, eps: float, H, Q, scale, M: int, K: int) -> None:
+    """gemm_rms_norm with Y as E4M3 codes Q [M,K] and row scales (FP32 [M]), the operand
+    of gemm_e4m3_rowscale: Y ~ Q scale, scale = amax |Y| / 448."""
+    lib = _lib or load()
+    d = _dtype16("gemm_rms_norm_e4m3", dtype)
+    M, K = int(M), int(K)
+    n, m, k = _rows_dims(M, K)
+    x, r, pw, h, q, sc = _take(lib, "gemm_rms_norm_e4m3", ("X", X, 2, n, True), ("R", R, 2, n, True),
+                               ("w", w, 2, k, True), ("H", H, 2, n, True), ("Q", Q, 1, n, True),
+                               ("scale", scale, 4, m, True))
+    st = lib.gemm_rms_norm_e4m3(d, x, r, pw, eps, h, q, sc, M, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_rms_norm_e4m3", lib.gemm_last_error().decode())
+
+
+def gemm_rms_norm_backward(dtype: str, H, w, rstd, dY, dH, dX, dw, M: int, K: int) -> None:
+    """Gradients of gemm_rms_norm from dY and dH (None: 0): dX [M,K] of X and R alike (may
+    be dH itself), dw FP32 [K]; None leaves one out."""
+    lib = _lib or load()
+    d = _dtype16("gemm_rms_norm_backward", dtype)
+    M, K = int(M), int(K)
+    n, m, k = _rows_dims(M, K)
+    kw = max(K, 0) if M >= 0 else 0  # dw is written for M = 0 too
+    p = _take(lib, "gemm_rms_norm_backward", ("H", H, 2, n, True), ("w", w, 2, k, True), ("rstd", rstd, 4, m, True),
+              ("dY", dY, 2, n, True), ("dH", dH, 2, n, True), ("dX", dX, 2, n, True), ("dw", dw, 4, kw, True))
+    st = lib.gemm_rms_norm_backward(d, *p, M, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_rms_norm_backward", lib.gemm_last_error().decode())
+
+
+def _rows_dims(M: int, K: int):
+    """Elements of an [M,K] operand, of a value a row and of one a column: none where M or
+    K is 0 or negative (a no-op, or a call that the library rejects)."""
+    return (M * K, M, K) if M > 0 and K > 0 else (0, 0, 0)
 
 
 def gemm_set_stream(stream) -> None:

@@ -15,6 +15,7 @@
 #include "gated.h"
 #include "gemm.h"
 #include "internal.h"
+#include "norm.h"
 #include "scratch.h"
 
 using namespace gemm_gb300;
@@ -630,6 +631,53 @@ gemm_status_t run_gated_backward(int dtype, int act, const void *X, const void *
     return finish(launch_gated_gradients(p, dev->num_sms, dev->status, s), "gated_backward");
 }
 
+// ------------------------------------------------------------ root-mean-square norm
+bool norm_args_ok(const char *who, int dtype, int M, int K, std::initializer_list<const void *> halves,
+                  std::initializer_list<const void *> floats) {
+    return (dtype == GEMM_F16 || dtype == GEMM_BF16) && M >= 0 && K >= 0 && elements_aligned(who, halves, floats);
+}
+
+// Y, or with e4m3 Q and scale.
+gemm_status_t run_rms_norm(const char *who, bool e4m3, int dtype, const void *X, const void *R, const void *w, float eps,
+                           void *H, void *Y, uint8_t *Q, float *scale, float *rstd, int M, int K) {
+    if (!norm_args_ok(who, dtype, M, K, {X, R, w, H, Y}, {scale, rstd})) return GEMM_ERR_INVALID_VALUE;
+    if (!(eps >= 1.17549435e-38f && eps < 1.0737418e9f)) {
+        snprintf(t_last_error, sizeof(t_last_error), "%s: eps has to be a normal number below 2^30", who);
+        return GEMM_ERR_INVALID_VALUE;
+    }
+    if (M == 0 || K == 0) { t_last_kernel = "noop"; return GEMM_OK; }
+    if (!X || (e4m3 ? !Q || !scale : !Y) || (H && !R)) return GEMM_ERR_INVALID_VALUE;
+    const size_t x = (size_t)M * K * 2;
+    const Span h{H, x}, y{Y, x}, q{Q, x / 2}, sc{scale, (size_t)M * 4}, rs{rstd, (size_t)M * 4};
+    // H may be X or R itself: the residual stream updated in place
+    if (any_overlap({h}, {{H == X ? nullptr : X, x}, {H == R ? nullptr : R, x}, {w, (size_t)K * 2}}) ||
+        any_overlap({y, q, sc, rs}, {{X, x}, {R, x}, h, {w, (size_t)K * 2}}))
+        return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    const NormProblem p{X, R, w, H, Y, Q, scale, rstd, eps, M, K, elt16(dtype)};
+    return finish(launch_rms_norm(p, t_stream), e4m3 ? "rms_norm_e4m3" : "rms_norm");
+}
+
+gemm_status_t run_rms_norm_backward(int dtype, const void *H, const void *w, const float *rstd, const void *dY,
+                                    const void *dH, void *dX, float *dw, int M, int K) {
+    if (!norm_args_ok("gemm_rms_norm_backward", dtype, M, K, {H, w, dY, dH, dX}, {rstd, dw})) return GEMM_ERR_INVALID_VALUE;
+    if (K == 0 || (!dX && !dw) || (M == 0 && !dw)) { t_last_kernel = "noop"; return GEMM_OK; }
+    if (M > 0 && (!H || !rstd || !dY)) return GEMM_ERR_INVALID_VALUE;
+    const size_t x = (size_t)M * K * 2;
+    const Span ox{dX, x}, ow{dw, (size_t)K * 4}, wi{w, (size_t)K * 2}, ri{rstd, (size_t)M * 4};
+    if (any_overlap({ox, ow}, {{H, x}, {dY, x}, wi, ri}) || any_overlap({ow}, {{dH, x}}) ||
+        (dX != dH && any_overlap({ox}, {{dH, x}})))
+        return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    if (M == 0) return finish(zero(ow, t_stream, cudaSuccess), "zero_fill");
+    const NormBackward p{H, w, rstd, dY, dH, dX, dw, M, K, elt16(dtype)};
+    return finish(launch_rms_norm_backward(p, dev->num_sms, t_stream), "rms_norm_backward");
+}
+
 }  // namespace
 
 extern "C" {
@@ -833,6 +881,21 @@ GEMM_API gemm_status_t gemm_gated_backward(gemm_dtype_t dtype, gemm_act_t act, c
                                            const void *W_u, const float *G, const float *U, const void *dZ, void *dX,
                                            void *dW_g, void *dW_u, int M, int N, int K) {
     return run_gated_backward((int)dtype, (int)act, X, W_g, W_u, G, U, dZ, dX, dW_g, dW_u, M, N, K);
+}
+
+GEMM_API gemm_status_t gemm_rms_norm(gemm_dtype_t dtype, const void *X, const void *R, const void *w, float eps, void *H,
+                                     void *Y, float *rstd, int M, int K) {
+    return run_rms_norm("gemm_rms_norm", false, (int)dtype, X, R, w, eps, H, Y, nullptr, nullptr, rstd, M, K);
+}
+
+GEMM_API gemm_status_t gemm_rms_norm_e4m3(gemm_dtype_t dtype, const void *X, const void *R, const void *w, float eps,
+                                          void *H, uint8_t *Q, float *scale, int M, int K) {
+    return run_rms_norm("gemm_rms_norm_e4m3", true, (int)dtype, X, R, w, eps, H, nullptr, Q, scale, nullptr, M, K);
+}
+
+GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H, const void *w, const float *rstd,
+                                              const void *dY, const void *dH, void *dX, float *dw, int M, int K) {
+    return run_rms_norm_backward((int)dtype, H, w, rstd, dY, dH, dX, dw, M, K);
 }
 
 GEMM_API gemm_status_t gemm_set_stream(void *cuda_stream) {

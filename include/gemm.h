@@ -364,6 +364,43 @@ GEMM_API gemm_status_t gemm_gated_backward(gemm_dtype_t dtype, gemm_act_t act, c
                                            const void *W_u, const float *G, const float *U, const void *dZ, void *dX,
                                            void *dW_g, void *dW_u, int M, int N, int K);
 
+/* Root-mean-square norm of rows with the residual's addition before it:
+ *     H = X + R  (rounded to dtype),  rstd_i = 1 / sqrt(mean_k H[i,k]^2 + eps)
+ *     Y[i,k] = w[k] H[i,k] rstd_i  (formed in FP32, rounded once)
+ * X, R, H, Y [M,K] row-major half or bf16 (dtype) with tight strides, w [K] of dtype
+ * (null: ones).  R null: no addition, H is X, and the argument H must be null.  H null
+ * with R given: the sum is not stored.  H may be X or R itself (the residual stream
+ * updated in place).  rstd (null: not stored): FP32 [M], for gemm_rms_norm_backward.
+ * eps: a normal number below 2^30 (GEMM_ERR_INVALID_VALUE otherwise).  Any M and K: one
+ * token to a long prompt; rows up to 16384 elements are read once.  Operands whose bases
+ * lie alike to 16 bytes are fastest (any K).  Rows of bf16 whose squares overflow FP32
+ * are summed again, scaled down; a NaN or an infinity in a row reaches that row alone.
+ * M = 0 or K = 0: nothing is written.  GEMM_ERR_ALIAS if any other output overlaps an
+ * input or another output. */
+GEMM_API gemm_status_t gemm_rms_norm(gemm_dtype_t dtype, const void *X, const void *R, const void *w, float eps, void *H,
+                                     void *Y, float *rstd, int M, int K);
+
+/* The same Y as row-scaled E4M3, the operand that gemm_e4m3_rowscale takes: of the
+ * FP32 values, not rounded to dtype in between,
+ *     scale_i = amax_k |Y[i,k]| / 448,  Q[i,k] = E4M3(Y[i,k] * (448 / amax_i))
+ * nearest, ties to even, clamped to +-448 (as gemm_quantize_rows_e4m3).  Q [M,K] codes,
+ * scale FP32 [M].  A row of zeros gives codes 0 and scale 0; a NaN or an infinity in a
+ * row makes its scale NaN. */
+GEMM_API gemm_status_t gemm_rms_norm_e4m3(gemm_dtype_t dtype, const void *X, const void *R, const void *w, float eps,
+                                          void *H, uint8_t *Q, float *scale, int M, int K);
+
+/* Gradients of gemm_rms_norm from dY (of Y) and dH (of H from its other uses, the
+ * residual's path; null: 0), with H (X where there was no residual) and rstd as the
+ * forward call left them:
+ *     dX = rstd (w dY - H rstd^2 mean_k(w dY H)) + dH   (of X and of R alike)
+ *     dw = sum_i dY H rstd
+ * dX [M,K] (dtype; may be dH itself), dw FP32 [K], each overwritten; a null one is left
+ * out.  Sums in FP32, in a fixed order.  FP32 partials of dw (4 K bytes for each of up to
+ * four CTAs an SM) lie in stream-ordered scratch for the duration of the call, from the
+ * library's pool (see gemm_gated).  M = 0 gives dw = 0.  GEMM_ERR_ALIAS as above. */
+GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H, const void *w, const float *rstd,
+                                              const void *dY, const void *dH, void *dX, float *dw, int M, int K);
+
 /* Stream for the calling host thread's subsequent calls: a cudaStream_t passed
  * as void*.  NULL selects the legacy default stream.  The stream stays owned by
  * the caller and must outlive the calls issued on it. */
