@@ -54,6 +54,8 @@ SIGNATURES = {
     "gemm_rms_norm": ([_I, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _I, _I], _I),
     "gemm_rms_norm_e4m3": ([_I, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _I, _I], _I),
     "gemm_rms_norm_backward": ([_I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I], _I),
+    "gemm_cross_entropy": ([_I, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
+    "gemm_cross_entropy_backward": ([_I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
     "gemm_set_stream": ([_VP], _I),
     "gemm_get_stream": ([], _VP),
     "gemm_synchronize": ([], _I),
@@ -546,6 +548,37 @@ def gemm_rms_norm_backward(dtype: str, H, w, rstd, dY, dH, dX, dw, M: int, K: in
     st = lib.gemm_rms_norm_backward(d, *p, M, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_rms_norm_backward", lib.gemm_last_error().decode())
+
+
+def gemm_cross_entropy(dtype: str, X, W, targets, loss, lse, M: int, N: int, K: int) -> None:
+    """loss (FP32 [M]) = lse - Z[i, targets_i] of the logits Z = X W^T, never kept: X [M,K],
+    W [N,K] ('f16' | 'bf16'), targets int64 [M] (outside 0 .. N-1: the row is left out, loss
+    0); lse (FP32 [M], or None) is kept for gemm_cross_entropy_backward."""
+    lib = _lib or load()
+    d = _dtype16("gemm_cross_entropy", dtype)
+    M, N, K = int(M), int(N), int(K)
+    nx, nw, _ = _dims(M, N, K)
+    m = M if min(M, N, K) >= 0 else 0
+    p = _take(lib, "gemm_cross_entropy", ("X", X, 2, nx, True), ("W", W, 2, nw, True), ("targets", targets, 8, m, True),
+              ("loss", loss, 4, m, True), ("lse", lse, 4, m, True))
+    st = lib.gemm_cross_entropy(d, *p, M, N, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_cross_entropy", lib.gemm_last_error().decode())
+
+
+def gemm_cross_entropy_backward(dtype: str, X, W, targets, lse, dloss, dX, dW, M: int, N: int, K: int) -> None:
+    """Gradients of gemm_cross_entropy from dloss (FP32 [M]) and the lse it stored: dX [M,K]
+    and dW [N,K]; None leaves one out."""
+    lib = _lib or load()
+    d = _dtype16("gemm_cross_entropy_backward", dtype)
+    M, N, K = int(M), int(N), int(K)
+    nx, nw, m = (M * K, N * K, M) if min(M, N, K) >= 0 else (0, 0, 0)
+    p = _take(lib, "gemm_cross_entropy_backward", ("X", X, 2, nx, True), ("W", W, 2, nw, True),
+              ("targets", targets, 8, m, True), ("lse", lse, 4, m, True), ("dloss", dloss, 4, m, True),
+              ("dX", dX, 2, nx, True), ("dW", dW, 2, nw, True))
+    st = lib.gemm_cross_entropy_backward(d, *p, M, N, K)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_cross_entropy_backward", lib.gemm_last_error().decode())
 
 
 def _rows_dims(M: int, K: int):

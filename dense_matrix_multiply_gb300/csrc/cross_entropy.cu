@@ -1,0 +1,564 @@
+// Softmax cross entropy of a linear head, Z = X W^T over a large vocabulary, and its
+// gradients, without the logits in memory.
+//
+// Forward: tiles of Z stay in tensor memory; the epilogue takes the largest logit m and
+// s = sum exp(z - m) of each row's 128 columns (online, 32 at a time: s <- s e^(m - m')
+// + sum e^(z - m')), and the row's own target's logit.  A second kernel joins the pairs
+// of a row, in order: lse = m + log s.  All in FP32.
+//
+// Backward, in pieces of the vocabulary: the piece's logits anew, dZ = (e^(z - lse) -
+// [j = t]) dloss rounded to 16 bits (the operand of the products to come) in scratch,
+// dW of the piece = dZ^T X, and dX += dZ W in FP32.  Where a piece of dX has few tiles
+// its sum is cut into K ranges, a slab of FP32 each; the ranges' sums grow piece after
+// piece (one addition to an element a launch, in stream order) and are added in order by
+// the last kernel: deterministic.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "cross_entropy.h"
+#include "fp4.h"
+#include "pair_pipe.cuh"
+
+namespace gemm_gb300 {
+namespace {
+
+using namespace pair;
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {  // 2^x, 2 units of 2^-23 off; 0 for -inf
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Of the columns [c0, c0 + 32) within a row's [0, N), c0 < N: the rest count as -inf.
+struct LseEpi {
+    static constexpr bool LOWER = false;
+    float2 *part;             // (m, s) of slot column / (bn / 2), [slot][M]
+    float *zt;                // Z_i,t_i
+    const long long *target;
+    int M, N, v0, total;      // rows; columns of this piece, and its first; of Z
+
+    __device__ __forceinline__ void run(const Part &p) const {
+        const int row = p.row0 + p.lane, width = p.bn >> 1, first = p.col0 + p.half * width;
+        if (first >= N) return;  // warp-uniform
+        long long t = row < M ? target[row] : -1;
+        t = t >= 0 && t < total ? t - v0 : -1;
+        float m = -INFINITY, s = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < width && first + c < N; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(p.tmem + (uint32_t)(p.half * width + c), r);
+            tmem_ld_wait();
+            const int left = N - first - c;
+            if (left < 32) {  // warp-uniform
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j >= left) r[j] = 0xFF800000u;
+            }
+            const long long at = t - (first + c);
+            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j == at) zt[row] = __uint_as_float(r[j]);
+            }
+            float top = __uint_as_float(r[0]);
+#pragma unroll
+            for (int j = 1; j < 32; ++j) top = fmaxf(top, __uint_as_float(r[j]));
+            top = fmaxf(top, m);
+            // differences to a finite maximum: e^(-inf) = 0 and e^inf = inf come out of themselves
+            const float base = (isfinite(top) ? top : 0.0f) * kLog2e;
+            float s0 = s * ex2(m * kLog2e - base), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                s0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -base));
+                s1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -base));
+                s2 += ex2(fmaf(__uint_as_float(r[j + 2]), kLog2e, -base));
+                s3 += ex2(fmaf(__uint_as_float(r[j + 3]), kLog2e, -base));
+            }
+            s = (s0 + s1) + (s2 + s3);
+            m = top;
+        }
+        if (row < M) part[(long long)((v0 + first) / width) * M + row] = make_float2(m, s);
+    }
+};
+
+// Scale factors of dZ: (up, down), powers of two whose product is 1.
+struct DzEpi {
+    static constexpr bool LOWER = false;
+    CUtensorMap tm;  // dZ of the piece
+    const float *lse, *dloss;
+    const long long *target;
+    const float2 *scale;  // null: 1
+    int M, N, v0, total;  // total: columns of Z
+    bool bf16;
+
+    __device__ __forceinline__ void run(const Part &p) const {
+        const int row = p.row0 + p.lane, width = p.bn >> 1;
+        long long t = row < M ? target[row] : -1;
+        const bool counts = t >= 0 && t < total;
+        const float d = counts ? dloss[row] * (scale ? scale->x : 1.0f) : 0.0f;
+        const float base = counts ? lse[row] * kLog2e : 0.0f;
+        t = counts ? t - v0 : -1;
+#pragma unroll 1
+        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+            const int c0 = p.col0 + g;
+            if (c0 >= N) return;  // warp-uniform
+            uint32_t z[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
+                tmem_ld_wait();
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -base));
+                const long long at = t - (c0 + h * 32);
+                if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j == at) v[j] -= 1.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = counts ? v[2 * j] * d : 0.0f, y = counts ? v[2 * j + 1] * d : 0.0f;
+                    z[h * 16 + j] = bf16 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
+                }
+            }
+            box_begin(p.lane);
+            box_put(p.box, p.lane, z);
+            box_store(&tm, p.box, p.lane, c0, p.row0, 0);
+        }
+    }
+};
+
+// FP32 sums to slab `split`, or added to it.
+struct AccEpi {
+    static constexpr bool LOWER = false;
+    CUtensorMap tm;
+    int N;
+    bool add;
+
+    __device__ __forceinline__ void run(const Part &p) const {
+        const int width = p.bn >> 1;
+#pragma unroll 1
+        for (int g = p.half * width; g < (p.half + 1) * width; g += 32) {
+            if (p.col0 + g >= N) return;  // warp-uniform
+            uint32_t r[32];
+            tmem_ld32(p.tmem + (uint32_t)g, r);
+            tmem_ld_wait();
+            box_begin(p.lane);
+            box_put(p.box, p.lane, r);
+            if (add) {
+                fence_async_shared();
+                __syncwarp();
+                if (p.lane == 0) tma_add_3d(&tm, p.box, p.col0 + g, p.row0, p.split);
+            } else {
+                box_store(&tm, p.box, p.lane, p.col0 + g, p.row0, p.split);
+            }
+        }
+    }
+};
+
+// 16-bit results times scale->y.
+struct OutEpi {
+    static constexpr bool LOWER = false;
+    CUtensorMap tm;
+    const float2 *scale;  // null: 1
+    uint16_t *out;        // not null: by the element, rows ld apart
+    long long ld;
+    int M, N;
+    bool bf16;
+
+    __device__ __forceinline__ void run(const Part &p) const {
+        const int width = p.bn >> 1;
+        const float f = scale ? scale->y : 1.0f;
+#pragma unroll 1
+        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+            const int c0 = p.col0 + g;
+            if (c0 >= N) return;  // warp-uniform
+            uint32_t z[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = __uint_as_float(r[2 * j]) * f, y = __uint_as_float(r[2 * j + 1]) * f;
+                    z[h * 16 + j] = bf16 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
+                }
+            }
+            box_begin(p.lane);
+            box_put(p.box, p.lane, z);
+            if (out) box_scatter(p.box, p.lane, out, ld, p.row0, c0, M, N);
+            else box_store(&tm, p.box, p.lane, c0, p.row0, 0);
+        }
+    }
+};
+
+// Joins the (m, s) of a row's slots: 32 rows to a CTA, slots dealt to its 32 warps.
+__global__ void __launch_bounds__(1024)
+head_join_kernel(const float2 *__restrict__ part, const float *__restrict__ zt, const long long *__restrict__ target,
+                 float *__restrict__ loss, float *__restrict__ lse, int slots, int M, int N)
+{
+    __shared__ float2 mine[32][32];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = blockIdx.x * 32LL + lane;
+    float m = -INFINITY, s = 0.0f;
+    auto join = [&](float2 v) {
+        const float top = fmaxf(m, v.x), base = (isfinite(top) ? top : 0.0f) * kLog2e;
+        s = s * ex2(m * kLog2e - base) + v.y * ex2(v.x * kLog2e - base);
+        m = top;
+    };
+    if (row < M) {
+#pragma unroll 8
+        for (int i = warp; i < slots; i += 32) join(__ldcg(part + (long long)i * M + row));
+    }
+    mine[warp][lane] = make_float2(m, s);
+    __syncthreads();
+    if (warp != 0 || row >= M) return;
+    for (int w = 1; w < 32; ++w) join(mine[w][lane]);
+    const float l = (isfinite(m) ? m : 0.0f) + logf(s);
+    const long long t = target[row];
+    loss[row] = t >= 0 && t < N ? l - zt[row] : 0.0f;
+    if (lse) lse[row] = l;
+}
+
+__global__ void __launch_bounds__(256)
+head_flat_kernel(const long long *__restrict__ target, float *__restrict__ loss, float *__restrict__ lse, int M, int N)
+{
+    pdl_wait();
+    const long long row = blockIdx.x * 256LL + threadIdx.x;
+    if (row >= M) return;
+    const float l = logf((float)N);
+    const long long t = target[row];
+    loss[row] = t >= 0 && t < N ? l : 0.0f;
+    if (lse) lse[row] = l;
+}
+
+// dst [rows, dst_cols] (rows of whole 16 bytes) = src [rows, cols] (any 2 bytes), zeros
+// behind the row and, where targets are given, in rows whose target is no column of N: a
+// lane two 16-byte pieces (fp4.h).
+constexpr int COPY_WARPS = 4;
+__global__ void __launch_bounds__(COPY_WARPS * 32)
+head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long cols, uint16_t *__restrict__ dst,
+                 long long dst_cols, const long long *__restrict__ target, int N)
+{
+    pdl_wait();
+    const long long row = (long long)blockIdx.x * COPY_WARPS + (threadIdx.x >> 5);
+    if (row >= rows) return;  // warp-uniform
+    const int lane = threadIdx.x & 31;
+    const long long t = target ? target[row] : 0;
+    const long long width = t >= 0 && t < N ? cols : -1024;
+    const uint8_t *lo = reinterpret_cast<const uint8_t *>(src), *hi = reinterpret_cast<const uint8_t *>(src + rows * cols);
+    uint16_t *d = dst + row * dst_cols;
+    for (long long k0 = blockIdx.y * 512LL; k0 < dst_cols; k0 += gridDim.y * 512LL) {
+        const long long k = k0 + lane * 16;
+        uint32_t v[8];
+        fp4_load16_any(src + row * cols + k, (int)max(min(width - k, 512LL), -512LL), lo, hi, v);
+        if (k < dst_cols) *reinterpret_cast<uint4 *>(d + k) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (k + 8 < dst_cols) *reinterpret_cast<uint4 *>(d + k + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+cudaError_t copy(const void *src, long long rows, long long cols, void *dst, long long dst_cols, const long long *target,
+                 int N, cudaStream_t s) {
+    const long long gx = (rows + COPY_WARPS - 1) / COPY_WARPS, gy = std::min<long long>((dst_cols + 511) / 512, 65535);
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)gx, (unsigned)gy), dim3(COPY_WARPS * 32), 0, s, attr);
+    return launch_counted(&cfg, head_copy_kernel, static_cast<const uint16_t *>(src), rows, cols, static_cast<uint16_t *>(dst),
+                          dst_cols, target, N);
+}
+
+// Half precision: the power of two that takes the largest |dloss| of a row with a target
+// to [2^14, 2^15), so that dZ, at most as large, keeps half's full precision down to
+// probabilities of 2^-28; and its inverse.
+__global__ void __launch_bounds__(1024)
+head_scale_kernel(const float *__restrict__ dloss, const long long *__restrict__ target, float2 *scale, int M, int N)
+{
+    __shared__ float tops[32];
+    pdl_wait();
+    float top = 0.0f;
+    for (long long i = threadIdx.x; i < M; i += 1024) {
+        const long long t = target[i];
+        if (t >= 0 && t < N) top = fmaxf(top, fabsf(dloss[i]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w]);
+    int e = 0;
+    if (top > 0.0f && isfinite(top)) {
+        frexpf(top, &e);
+        e = max(min(15 - e, 126), -126);
+    }
+    *scale = make_float2(ldexpf(1.0f, e), ldexpf(1.0f, -e));
+}
+
+// dX = (sum of the slabs, in order) scale->y, four elements to a thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+head_finish_kernel(const float *__restrict__ slab, int slabs, long long rows, int cols, long long ld, const float2 *scale,
+                   T *__restrict__ out)
+{
+    pdl_wait();
+    const long long per = (cols + 3) / 4, i = blockIdx.x * 256LL + threadIdx.x;
+    if (i >= rows * per) return;
+    const long long row = i / per;
+    const int c = (int)(i - row * per) * 4;
+    const float *p = slab + row * ld + c;
+    float4 v = __ldcg(reinterpret_cast<const float4 *>(p));
+#pragma unroll 4
+    for (int j = 1; j < slabs; ++j) {
+        const float4 w = __ldcg(reinterpret_cast<const float4 *>(p + j * rows * ld));
+        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+    }
+    const float f = scale ? scale->y : 1.0f;
+    T *o = out + row * cols + c;
+    if (((uintptr_t)o & 7) == 0 && c + 4 <= cols) {
+        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(v.x * f, v.y * f, (T *)nullptr), pack2(v.z * f, v.w * f, (T *)nullptr));
+    } else {
+        const float e[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < 4 && c + j < cols; ++j) store1(o + j, e[j] * f);
+    }
+}
+
+long long up(long long n, long long to) { return (n + to - 1) / to * to; }
+bool on16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// A piece's part of scratch, 256 bytes aligned.
+struct Layout {
+    size_t bytes = 0;
+    size_t add(size_t n) {
+        const size_t at = bytes;
+        bytes += (n + 255) & ~(size_t)255;
+        return at;
+    }
+};
+
+constexpr long long kPiece = 256LL << 20;  // bytes of a piece of dZ, or of a padded piece of W
+
+template <uint32_t FORMAT>
+cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) {
+    const int cmax = clusters_max<FORMAT, LseEpi>(dev);
+    if (cmax <= 0) return cudaErrorNotSupported;
+    const bool aligned = p.K % 8 == 0;
+    const bool pad_x = !aligned || !on16(p.X), pad_w = !aligned || !on16(p.W);
+    const long long kp = aligned ? p.K : up(p.K, 64);
+    const int bn = 256, rows_max = 16384;
+    const int rows = std::min(p.M, rows_max);
+    const long long vp = pad_w ? std::min<long long>(up(p.N, bn), std::max<long long>(kPiece / (2 * kp) / bn * bn, bn)) : p.N;
+    const int slots = (int)ceil_div(p.N, bn / 2);
+    Layout l;
+    const size_t at_x = l.add(pad_x ? (size_t)rows * kp * 2 : 0), at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0),
+                 at_part = l.add((size_t)slots * rows * 8), at_zt = l.add((size_t)rows * 4);
+    void *ws = nullptr;
+    cudaError_t e = scratch_alloc(&ws, l.bytes, s);
+    if (e != cudaSuccess) return e;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    for (long long r0 = 0; r0 < p.M && e == cudaSuccess; r0 += rows) {
+        const int m = (int)std::min<long long>(rows, p.M - r0);
+        const uint16_t *x = static_cast<const uint16_t *>(p.X) + r0 * p.K;
+        if (pad_x) {
+            e = copy(x, m, p.K, base + at_x, kp, nullptr, 1, s);
+            x = reinterpret_cast<const uint16_t *>(base + at_x);
+        }
+        LseEpi epi = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N};
+        for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
+            const int n = (int)std::min<long long>(vp, p.N - v0);
+            const uint16_t *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
+            if (pad_w) {
+                e = copy(w, n, p.K, base + at_w, kp, nullptr, 1, s);
+                if (e != cudaSuccess) break;
+                w = reinterpret_cast<const uint16_t *>(base + at_w);
+            }
+            const long long tiles = ceil_div(m, 256) * ceil_div(n, bn);
+            CUtensorMap ta, tb;
+            if (tiles > 0x7FFFFFFFLL || !map_operand(&ta, x, FORMAT, false, m, kp, kp, 128) ||
+                !map_operand(&tb, w, FORMAT, false, n, kp, kp, bn / 2)) {
+                e = cudaErrorInvalidValue;
+                break;
+            }
+            epi.N = n;
+            epi.v0 = (int)v0;
+            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, status};
+            e = launch<FORMAT>(ta, tb, epi, a, cmax, s);
+        }
+        if (e != cudaSuccess) break;
+        cudaLaunchAttribute attr[1];
+        const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ceil_div(m, 32)), dim3(1024), 0, s, attr);
+        e = launch_counted(&cfg, head_join_kernel, static_cast<const float2 *>(epi.part), static_cast<const float *>(epi.zt),
+                           epi.target, p.loss + r0, p.lse ? p.lse + r0 : nullptr, slots, m, p.N);
+    }
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    return e != cudaSuccess ? e : f;
+}
+
+// K ranges of dX's tiles over a piece: as many as end first, a block of 64 in 0.3 us,
+// writing a tile about 2 us, a slab's share of the last kernel.
+int dx_splits(long long tiles, long long num_kb, int cmax, double slab_us) {
+    int best = 1;
+    double least = 0.0;
+    for (int n = 1; n <= 16 && num_kb / n >= 8; ++n) {
+        const double t = (double)ceil_div(tiles * n, cmax) * ((double)ceil_div(num_kb, n) * 0.3 + 2.0) + n * slab_us;
+        if (n == 1 || t < least) { best = n; least = t; }
+    }
+    return best;
+}
+
+template <typename T, uint32_t FORMAT>
+cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s) {
+    const int cz = clusters_max<FORMAT, DzEpi>(dev), cx = clusters_max<FORMAT, AccEpi>(dev), cw = clusters_max<FORMAT, OutEpi>(dev);
+    if (cz <= 0 || cx <= 0 || cw <= 0) return cudaErrorNotSupported;
+    const bool aligned = p.K % 8 == 0;
+    const long long kp = aligned ? p.K : up(p.K, 64);
+    // X: rows without a target are zeros in dW's product, whatever they hold (0 times an
+    // infinity is a NaN)
+    const bool copy_x = p.dW || !aligned || !on16(p.X), pad_w = !aligned || !on16(p.W);
+    long long vp = std::max<long long>(kPiece / (2LL * p.M) / 256 * 256, 256);
+    if (pad_w) vp = std::min(vp, std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256));
+    const long long pieces = ceil_div(p.N, vp);
+    vp = up(ceil_div(p.N, pieces), 256);
+    // dX
+    const long long x_tiles = ceil_div(p.M, 256) * ceil_div(p.K, 256), ldx = up(p.K, 64);
+    const double slab_us = (double)p.M * ldx * 4 * 2 / 5e6;
+    int splits = dx_splits(x_tiles, vp / BK, cx, slab_us);
+    splits = (int)std::max<long long>(1, std::min<long long>(splits, kPiece / ((long long)p.M * ldx * 4)));
+    Layout l;
+    const size_t at_z = l.add((size_t)p.M * vp * 2), at_x = l.add(copy_x ? (size_t)p.M * kp * 2 : 0),
+                 at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0),
+                 at_slab = l.add(p.dX ? (size_t)splits * p.M * ldx * 4 : 0), at_scale = l.add(8);
+    void *ws = nullptr;
+    cudaError_t e = scratch_alloc(&ws, l.bytes, s);
+    if (e != cudaSuccess) return e;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    cudaLaunchAttribute attr[1];
+    const float2 *scale = nullptr;
+    const bool bf16 = FORMAT == 1;
+    if (!bf16) {
+        scale = reinterpret_cast<const float2 *>(base + at_scale);
+        const cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(1024), 0, s, attr);
+        e = launch_counted(&cfg, head_scale_kernel, p.dloss, p.target, reinterpret_cast<float2 *>(base + at_scale), p.M, p.N);
+    }
+    const void *x = p.X;
+    if (e == cudaSuccess && copy_x) {
+        e = copy(p.X, p.M, p.K, base + at_x, kp, p.dW ? p.target : nullptr, p.dW ? p.N : 1, s);
+        x = base + at_x;
+    }
+    for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
+        const int n = (int)std::min<long long>(vp, p.N - v0);
+        const void *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
+        if (pad_w) {
+            e = copy(w, n, p.K, base + at_w, kp, nullptr, 1, s);
+            if (e != cudaSuccess) break;
+            w = base + at_w;
+        }
+        const void *z = base + at_z;
+        const long long z_tiles = ceil_div(p.M, 256) * ceil_div(n, 256), w_tiles = ceil_div(n, 256) * ceil_div(p.K, 256);
+        if (z_tiles > 0x7FFFFFFFLL || w_tiles > 0x7FFFFFFFLL || x_tiles * splits > 0x7FFFFFFFLL) {
+            e = cudaErrorInvalidValue;
+            break;
+        }
+        CUtensorMap ta, tb;
+        {
+            DzEpi epi;
+            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, 128) || !map_operand(&tb, w, FORMAT, false, n, kp, kp, 128) ||
+                !map16(&epi.tm, z, FORMAT, p.M, n, vp, 32, 64)) {
+                e = cudaErrorInvalidValue;
+                break;
+            }
+            epi.lse = p.lse;
+            epi.dloss = p.dloss;
+            epi.target = p.target;
+            epi.scale = scale;
+            epi.M = p.M;
+            epi.N = n;
+            epi.v0 = (int)v0;
+            epi.total = p.N;
+            epi.bf16 = bf16;
+            const Args a = {p.M, n, (int)ceil_div(kp, BK), 256, 0, 0, (int)z_tiles, 1, status};
+            e = launch<FORMAT>(ta, tb, epi, a, cz, s);
+        }
+        if (e == cudaSuccess && p.dW) {
+            OutEpi epi;
+            uint16_t *out = static_cast<uint16_t *>(p.dW) + v0 * p.K;
+            const bool tma = aligned && on16(p.dW);
+            if (!map_operand(&ta, z, FORMAT, true, n, p.M, vp, 0) || !map_operand(&tb, x, FORMAT, true, kp, p.M, kp, 0) ||
+                !map16(&epi.tm, tma ? (const void *)out : z, FORMAT, n, tma ? p.K : 64, tma ? p.K : 64, 32, 64)) {
+                e = cudaErrorInvalidValue;
+                break;
+            }
+            epi.scale = scale;
+            epi.out = tma ? nullptr : out;
+            epi.ld = p.K;
+            epi.M = n;
+            epi.N = p.K;
+            epi.bf16 = bf16;
+            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, status};
+            e = launch<FORMAT>(ta, tb, epi, a, cw, s);
+        }
+        if (e == cudaSuccess && p.dX) {
+            AccEpi epi;
+            if (!map_operand(&ta, z, FORMAT, false, p.M, n, vp, 128) || !map_operand(&tb, w, FORMAT, true, kp, n, kp, 0) ||
+                !make_map3(&epi.tm, base + at_slab, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, ldx * 4,
+                           p.M * ldx * 4, 32, 32, 1, 128)) {
+                e = cudaErrorInvalidValue;
+                break;
+            }
+            epi.N = p.K;
+            epi.add = v0 > 0;
+            // (a short last piece: fewer ranges, each of one block at least)
+            const int kb = (int)ceil_div(n, BK);
+            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), status};
+            e = launch<FORMAT>(ta, tb, epi, a, cx, s);
+        }
+    }
+    if (e == cudaSuccess && p.dX) {
+        const long long blocks = ceil_div((long long)p.M * ((p.K + 3) / 4), 256);
+        const int used = (int)std::min<long long>(splits, ceil_div(std::min<long long>(vp, p.N), BK));
+        const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(256), 0, s, attr);
+        e = blocks > 0x7FFFFFFFLL ? cudaErrorInvalidValue
+                                  : launch_counted(&cfg, head_finish_kernel<T>, reinterpret_cast<const float *>(base + at_slab),
+                                                   used, (long long)p.M, p.K, ldx, scale, static_cast<T *>(p.dX));
+    }
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    return e != cudaSuccess ? e : f;
+}
+
+cudaError_t device(int *dev) {
+    const cudaError_t e = cudaGetDevice(dev);
+    return e != cudaSuccess ? e : *dev < 0 || *dev >= kMaxDevices ? cudaErrorInvalidDevice : cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_cross_entropy(const HeadProblem &p, int *status, cudaStream_t s) {
+    int dev = 0;
+    const cudaError_t e = device(&dev);
+    if (e != cudaSuccess) return e;
+    return p.elt == Elt::BF16 ? forward<1>(p, dev, status, s) : forward<0>(p, dev, status, s);
+}
+
+cudaError_t launch_cross_entropy_backward(const HeadBackward &p, int *status, cudaStream_t s) {
+    int dev = 0;
+    const cudaError_t e = device(&dev);
+    if (e != cudaSuccess) return e;
+    return p.elt == Elt::BF16 ? backward<__nv_bfloat16, 1>(p, dev, status, s) : backward<__half, 0>(p, dev, status, s);
+}
+
+cudaError_t launch_cross_entropy_flat(const HeadProblem &p, cudaStream_t s) {
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ceil_div(p.M, 256)), dim3(256), 0, s, attr);
+    return launch_counted(&cfg, head_flat_kernel, p.target, p.loss, p.lse, p.M, p.N);
+}
+
+}  // namespace gemm_gb300

@@ -11,6 +11,7 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "cross_entropy.h"
 #include "fp4.h"
 #include "gated.h"
 #include "gemm.h"
@@ -678,6 +679,52 @@ gemm_status_t run_rms_norm_backward(int dtype, const void *H, const void *w, con
     return finish(launch_rms_norm_backward(p, dev->num_sms, t_stream), "rms_norm_backward");
 }
 
+// ------------------------------------------------------------ cross entropy of a linear head
+bool targets_aligned(const char *who, const int64_t *t) {
+    if (((uintptr_t)t & 7) == 0) return true;
+    snprintf(t_last_error, sizeof(t_last_error), "%s: targets need 8-byte alignment", who);
+    return false;
+}
+
+gemm_status_t run_cross_entropy(int dtype, const void *X, const void *W, const int64_t *targets, float *loss, float *lse,
+                                int M, int N, int K) {
+    const char *who = "gemm_cross_entropy";
+    if ((dtype != GEMM_F16 && dtype != GEMM_BF16) || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (!elements_aligned(who, {X, W}, {loss, lse}) || !targets_aligned(who, targets)) return GEMM_ERR_INVALID_VALUE;
+    if (M == 0) { t_last_kernel = "noop"; return GEMM_OK; }
+    const bool work = N > 0 && K > 0;
+    if (!loss || !targets || (work && (!X || !W))) return GEMM_ERR_INVALID_VALUE;
+    const size_t m4 = (size_t)M * 4;
+    const Span lo{loss, m4}, ls{lse, m4};
+    if (any_overlap({lo, ls}, {{X, (size_t)M * K * 2}, {W, (size_t)N * K * 2}, {targets, (size_t)M * 8}})) return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    const HeadProblem p{X, W, reinterpret_cast<const long long *>(targets), loss, lse, M, N, K, elt16(dtype)};
+    if (!work) return finish(launch_cross_entropy_flat(p, t_stream), "cross_entropy_flat");
+    return finish(launch_cross_entropy(p, dev->status, t_stream), "cross_entropy");
+}
+
+gemm_status_t run_cross_entropy_backward(int dtype, const void *X, const void *W, const int64_t *targets, const float *lse,
+                                         const float *dloss, void *dX, void *dW, int M, int N, int K) {
+    const char *who = "gemm_cross_entropy_backward";
+    if ((dtype != GEMM_F16 && dtype != GEMM_BF16) || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_VALUE;
+    if (!elements_aligned(who, {X, W, dX, dW}, {lse, dloss}) || !targets_aligned(who, targets)) return GEMM_ERR_INVALID_VALUE;
+    if (K == 0 || (!dX && !dW)) { t_last_kernel = "noop"; return GEMM_OK; }
+    const bool work = M > 0 && N > 0;
+    if (work && (!X || !W || !targets || !lse || !dloss)) return GEMM_ERR_INVALID_VALUE;
+    const size_t x = (size_t)M * K * 2, w = (size_t)N * K * 2, m4 = (size_t)M * 4;
+    const Span ox{dX, x}, ow{dW, w};
+    if (any_overlap({ox, ow}, {{X, x}, {W, w}, {targets, (size_t)M * 8}, {lse, m4}, {dloss, m4}})) return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    if (!work)  // empty sums: no rows (dW), no vocabulary (dX)
+        return finish(zero(ow, t_stream, zero(ox, t_stream, cudaSuccess)), "zero_fill");
+    const HeadBackward p{X, W, reinterpret_cast<const long long *>(targets), lse, dloss, dX, dW, M, N, K, elt16(dtype)};
+    return finish(launch_cross_entropy_backward(p, dev->status, t_stream), "cross_entropy_backward");
+}
+
 }  // namespace
 
 extern "C" {
@@ -896,6 +943,17 @@ GEMM_API gemm_status_t gemm_rms_norm_e4m3(gemm_dtype_t dtype, const void *X, con
 GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H, const void *w, const float *rstd,
                                               const void *dY, const void *dH, void *dX, float *dw, int M, int K) {
     return run_rms_norm_backward((int)dtype, H, w, rstd, dY, dH, dX, dw, M, K);
+}
+
+GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
+                                          float *loss, float *lse, int M, int N, int K) {
+    return run_cross_entropy((int)dtype, X, W, targets, loss, lse, M, N, K);
+}
+
+GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
+                                                   const float *lse, const float *dloss, void *dX, void *dW, int M, int N,
+                                                   int K) {
+    return run_cross_entropy_backward((int)dtype, X, W, targets, lse, dloss, dX, dW, M, N, K);
 }
 
 GEMM_API gemm_status_t gemm_set_stream(void *cuda_stream) {

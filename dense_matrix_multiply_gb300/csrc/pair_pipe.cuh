@@ -1,0 +1,393 @@
+// The tensor-core pipeline of the head's cross entropy (cross_entropy.cu) and of the
+// orthogonalised update (orthogonalize.cu): D = A B of 16-bit operands, FP32 sums, whose
+// tiles are handed to an epilogue of the caller's.
+//
+// A 256 x bn tile (bn 64, 128 or 256; 64 only where B lies K-major) belongs to a cluster of two CTAs (tcgen05
+// cta_group::2), 128 rows of A and half of B's columns loaded by each, K in stages of
+// 64.  Either operand may lie K-major (rows of adjacent k) or MN-major (k by k, adjacent
+// rows or columns), as its tensor map and the flags say.  Warp 0 loads, warp 1 of the
+// leader issues the MMAs -- both converged, one elected lane for the instructions -- and
+// warps 2-9 write out, 32 rows and half of the columns to each.  Two accumulators, so
+// that a tile is written while the next is computed.  Clusters walk over the units (a
+// tile, or one of its K ranges) in the same order.
+//
+// Every wait is bounded; on expiry a code goes to the status word, both CTAs give up,
+// their loads and MMAs are waited for, and the tensor memory is released.
+#pragma once
+
+#include "tc_ptx.cuh"
+
+namespace gemm_gb300 {
+namespace pair {
+
+using namespace tc;
+
+constexpr int THREADS = 320, EPI_WARPS = 8;
+constexpr int BK = 64;                 // 16-bit k per stage: 128 bytes a row
+constexpr int STAGES = 6;
+constexpr int A_STAGE = 128 * BK * 2;  // 16 KiB per CTA
+constexpr int B_STAGE = 128 * BK * 2;  // up to 128 of the tile's columns
+constexpr int BOX64 = 64 * BK * 2;     // 64 columns x 64 k of an MN-major tile
+constexpr int STG_BOX = 4096;          // 32 rows x 128 bytes, one box to an epilogue warp
+constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * STG_BOX + 256;
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int GROUP_M = 8;
+static_assert(SMEM <= 232448, "shared memory budget");
+
+struct Bars {
+    uint64_t full[STAGES];
+    uint64_t empty[STAGES];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
+    uint64_t peer_done;
+    long long peer_issued;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(Bars) <= 256, "barrier block");
+
+struct Args {
+    int M, N;        // of D
+    int num_kb;      // K blocks of 64
+    int bn;
+    int a_mn, b_mn;  // operands that lie MN-major
+    int tiles;
+    int splits;      // K ranges of a tile
+    int *status;
+};
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// FP32 accumulator, A and B of one 16-bit type (0 f16, 1 bf16), M = 256.
+__device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (format << 7) | (format << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((n >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+struct Tile {
+    int m, n;
+};
+// Tiles in groups of GROUP_M rows of them, column by column within a group.  LOWER: only
+// those of a square D that hold an element on or below its diagonal block of 256, row
+// after row: (m + 1) 256 / bn of them in row m (fewer in the last).
+template <bool LOWER>
+__device__ __forceinline__ Tile tile_at(int t, const Args &a) {
+    if constexpr (LOWER) {
+        const int q = 256 / a.bn;
+        int m = (int)((sqrtf(8.0f * (float)(t / q) + 1.0f) - 1.0f) * 0.5f);
+        while (q * (m + 1) * (m + 2) / 2 <= t) ++m;
+        while (q * m * (m + 1) / 2 > t) --m;
+        return {m, t - q * m * (m + 1) / 2};
+    }
+    const int tiles_m = (a.M + 255) / 256, tiles_n = (a.N + a.bn - 1) / a.bn;
+    const int group = t / (GROUP_M * tiles_n), first = group * GROUP_M, size = min(tiles_m - first, GROUP_M);
+    const int q = t - group * GROUP_M * tiles_n;
+    return {first + q % size, q / size};
+}
+inline long long lower_tiles(int n, int bn) {
+    const long long rows = (n + 255LL) / 256, q = 256 / bn;
+    return q * (rows - 1) * rows / 2 + (n + bn - 1LL) / bn;
+}
+
+// What an epilogue warp sees of a unit.
+struct Part {
+    uint32_t tmem;    // this warp's rows, the tile's first column
+    int row0, col0;   // of D: the warp's first row, the tile's first column
+    int bn, half;     // which half of the columns: first (0) or last
+    int split;        // which K range
+    int lane;
+    uint8_t *box;     // STG_BOX bytes of this warp's
+};
+
+// 32 registers of this lane's row to a box of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ void box_put(uint8_t *box, int lane, const uint32_t (&r)[32]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+            make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+}
+// The box once the store that last read it has done so.
+__device__ __forceinline__ void box_begin(int lane) {
+    if (lane == 0) tma_stores_read_wait0();
+    __syncwarp();
+}
+__device__ __forceinline__ void box_store(const CUtensorMap *map, const uint8_t *box, int lane, int x, int y, int z) {
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) tma_store_3d(map, box, x, y, z);
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// A box of 64 16-bit columns to a matrix that TMA cannot describe: by the element.
+__device__ __forceinline__ void box_scatter(const uint8_t *box, int lane, uint16_t *out, long long ld, int row0, int col0,
+                                            int M, int N) {
+    __syncwarp();
+    for (int r = 0; r < 32 && row0 + r < M; ++r) {
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(box + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+        uint16_t *p = out + (row0 + r) * ld + col0 + 2 * lane;
+        if (col0 + 2 * lane < N) p[0] = (uint16_t)v;
+        if (col0 + 2 * lane + 1 < N) p[1] = (uint16_t)(v >> 16);
+    }
+    __syncwarp();
+}
+
+// Epi: static constexpr bool LOWER; run(Part), called by whole warps with row0 < M.
+template <uint32_t FORMAT, typename Epi>
+__global__ void __launch_bounds__(THREADS, 1)
+pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ Epi epi, const Args args)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *a_tiles = smem;
+    uint8_t *b_tiles = a_tiles + STAGES * A_STAGE;
+    uint8_t *staging = b_tiles + STAGES * B_STAGE;
+    Bars *bars = reinterpret_cast<Bars *>(staging + EPI_WARPS * STG_BOX);
+    volatile int *abort_flag = &bars->abort;
+
+    const int bn = args.bn;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
+    const int units = args.tiles * args.splits;
+    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (bn >> 1) * 128);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 2 * EPI_WARPS);
+        }
+        mbar_init(&bars->drain, 1);
+        mbar_init(&bars->peer_done, 1);
+        bars->abort = 0;
+        mbar_init_fence();
+        prefetch_desc(&tmA);
+        prefetch_desc(&tmB);
+    }
+    if (warp == 1) tmem_alloc<2>(&bars->tmem_base, TMEM_COLS);
+    fence_before();
+    cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
+    fence_after();
+    const uint32_t tmem_base = bars->tmem_base;
+    pdl_launch_dependents();
+    pdl_wait();
+
+    // unit u: K range u / tiles of tile u % tiles (clusters share a range's operands)
+    auto range = [&](int u, int &kb0, int &kb1) {
+        const int j = u / args.tiles;
+        kb0 = (int)((long long)args.num_kb * j / args.splits);
+        kb1 = (int)((long long)args.num_kb * (j + 1) / args.splits);
+        return tile_at<Epi::LOWER>(u - j * args.tiles, args);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer (both CTAs)
+        const bool issuer = elect_one();
+        int stage = 0;
+        uint32_t phase = 0;
+        long long issued = 0;
+        bool ok = true;
+        for (int u = cluster; ok && u < units; u += nclusters) {
+            int kb0, kb1;
+            const Tile t = range(u, kb0, kb1);
+            const int row0 = t.m * 256 + (int)rank * 128, col0 = t.n * bn + (int)rank * (bn >> 1);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
+                const uint32_t full = map_to_rank(&bars->full[stage], 0);
+                uint8_t *a = a_tiles + stage * A_STAGE, *b = b_tiles + stage * B_STAGE;
+                if (issuer) {
+                    if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
+                    if (args.a_mn) {
+                        tma_load_3d_pair(a, &tmA, full, row0, kb * BK, 0);
+                        tma_load_3d_pair(a + BOX64, &tmA, full, row0 + 64, kb * BK, 0);
+                    } else {
+                        tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
+                    }
+                    if (args.b_mn) {
+                        for (int c = 0; c < (bn >> 1); c += 64)
+                            tma_load_3d_pair(b + (c >> 6) * BOX64, &tmB, full, col0 + c, kb * BK, 0);
+                    } else {
+                        tma_load_3d_pair(b, &tmB, full, kb * BK, col0, 0);
+                    }
+                }
+                ++issued;
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+        }
+        if (!ok && issuer) {
+            atomicOr(args.status, ST_PRODUCER);
+            raise_abort_pair(abort_flag, rank);
+        }
+        // No load is left in flight into either CTA when the pair ends: the peer tells the
+        // leader how many stages it loaded, and the leader waits until every stage that
+        // either loaded has landed (the half that a side which gave up never loaded is
+        // counted as done, or never armed).
+        if (!issuer) {
+        } else if (!leader) {
+            st_cluster_s64(map_to_rank(&bars->peer_issued, 0), issued);
+            mbar_arrive_cluster(map_to_rank(&bars->peer_done, 0));  // release: the count is visible first
+        } else {
+            long long ip = issued;
+            if (mbar_wait(&bars->peer_done, 0, abort_flag, false))
+                ip = *reinterpret_cast<volatile long long *>(&bars->peer_issued);
+            else
+                atomicOr(args.status, ST_DRAIN);
+            const long long hi = issued > ip ? issued : ip;
+            for (long long i = (hi > STAGES ? hi - STAGES : 0); i < hi; ++i) {
+                const int s = (int)(i % STAGES);
+                if (i >= issued) mbar_arrive_expect_tx(&bars->full[s], stage_tx / 2);
+                else if (i >= ip) mbar_complete_tx(&bars->full[s], stage_tx / 2);
+                if (!mbar_wait(&bars->full[s], (uint32_t)((i / STAGES) & 1), abort_flag, false)) {
+                    atomicOr(args.status, ST_DRAIN);
+                    break;
+                }
+            }
+        }
+    } else if (warp == 1 && leader) {
+        // ------------------------------------------------------------ MMA issuer (leader)
+        const bool issuer = elect_one();
+        // K-major: a K step of 16 is 32 bytes of a 128-byte row.  MN-major: 16 rows of
+        // 128 bytes, 64-element boxes BOX64 bytes apart.
+        const bool a_mn = args.a_mn != 0, b_mn = args.b_mn != 0;
+        const uint32_t idesc = make_idesc(FORMAT, (uint32_t)bn, a_mn, b_mn);
+        const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), a_mn ? BOX64 : 16, 1024);
+        const uint64_t b_desc0 = desc_sw128(smem_u32(b_tiles), b_mn ? BOX64 : 16, 1024);
+        const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;
+        bool ok = true;
+        for (int u = cluster; ok && u < units; u += nclusters, ++it) {
+            int kb0, kb1;
+            range(u, kb0, kb1);
+            const int buf = it & 1;
+            if (!mbar_wait(&bars->acc_empty[buf], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, true)) { ok = false; break; }
+            fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(buf * 256);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&bars->full[stage], phase, abort_flag, true)) { ok = false; break; }
+                fence_after();
+                const uint64_t ad = a_desc0 + (uint64_t)((stage * A_STAGE) >> 4);
+                const uint64_t bd = b_desc0 + (uint64_t)((stage * B_STAGE) >> 4);
+                if (issuer) {
+#pragma unroll
+                    for (int ks = 0; ks < BK / 16; ++ks)
+                        mma(d, ad + ks * a_step, bd + ks * b_step, idesc, (uint32_t)(kb != kb0 || ks != 0));
+                    commit_pair_multicast(&bars->empty[stage]);
+                }
+                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+            }
+            if (!ok) break;
+            if (issuer) commit_pair_multicast(&bars->acc_full[buf]);
+        }
+        if (issuer) {
+            if (!ok) {
+                atomicOr(args.status, ST_MMA);
+                raise_abort_pair(abort_flag, rank);
+            }
+            commit<2>(&bars->drain);
+            if (!mbar_wait(&bars->drain, 0, abort_flag, false)) atomicOr(args.status, ST_DRAIN);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------------ epilogue (both CTAs)
+        const int quarter = warp & 3;
+        Part p;
+        p.bn = bn;
+        p.half = (warp - 2) >> 2;
+        p.lane = lane;
+        p.box = staging + (warp - 2) * STG_BOX;
+        int it = 0;
+        bool ok = true;
+        for (int u = cluster; u < units; u += nclusters, ++it) {
+            const int buf = it & 1;
+            p.split = u / args.tiles;
+            const Tile t = tile_at<Epi::LOWER>(u - p.split * args.tiles, args);
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (uint32_t)((it >> 1) & 1), abort_flag, true))) {
+                ok = false;
+                break;
+            }
+            fence_after();
+            __syncwarp();
+            p.row0 = t.m * 256 + (int)rank * 128 + quarter * 32;
+            p.col0 = t.n * bn;
+            p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
+            if (p.row0 < args.M) epi.run(p);
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], 0));
+        }
+        if (lane == 0) tma_stores_wait0();
+        if (!ok && lane == 0) {
+            atomicOr(args.status, ST_EPILOGUE);
+            raise_abort_pair(abort_flag, rank);
+        }
+    }
+
+    __syncwarp();
+    fence_before();
+    cluster_sync();  // no CTA leaves while its peer may still touch its memory
+    if (warp == 1) {
+        fence_after();
+        tmem_dealloc<2>(tmem_base, TMEM_COLS);
+    }
+}
+
+template <uint32_t FORMAT, typename Epi>
+int clusters_max(int dev) {
+    static std::atomic<int> known[kMaxDevices];
+    return cluster_limit(known[dev], reinterpret_cast<const void *>(pair_kernel<FORMAT, Epi>), THREADS, SMEM, 2);
+}
+
+template <uint32_t FORMAT, typename Epi>
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Epi &epi, const Args &args, int cmax, cudaStream_t s) {
+    const long long units = (long long)args.tiles * args.splits;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * (units < cmax ? units : cmax)), 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    pdl_attr(attr[1]);
+    cfg.attrs = attr;
+    cfg.numAttrs = g_pdl ? 2 : 1;
+    return launch_counted(&cfg, pair_kernel<FORMAT, Epi>, ta, tb, epi, args);
+}
+
+constexpr CUtensorMapDataType map_type(uint32_t format) {
+    return format == 1 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+// A row-major 16-bit matrix [rows, cols], rows ld elements apart, in boxes of box_rows x box_cols.
+inline bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows, long long cols, long long ld, int box_rows,
+                  int box_cols) {
+    return make_map3(m, p, map_type(format), cols, rows, 1, ld * 2, rows * ld * 2, box_cols, box_rows, 1, 128);
+}
+// An operand of the product from its stored matrix: mn: [K, MN] in 64 x 64 boxes, else
+// [MN, K] in boxes of `rows` x 64.
+inline bool map_operand(CUtensorMap *m, const void *p, uint32_t format, bool mn, long long mn_size, long long k, long long ld,
+                        int rows) {
+    return mn ? map16(m, p, format, k, mn_size, ld, BK, 64) : map16(m, p, format, mn_size, k, ld, rows, BK);
+}
+
+}  // namespace pair
+}  // namespace gemm_gb300

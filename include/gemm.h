@@ -401,6 +401,39 @@ GEMM_API gemm_status_t gemm_rms_norm_e4m3(gemm_dtype_t dtype, const void *X, con
 GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H, const void *w, const float *rstd,
                                               const void *dY, const void *dH, void *dX, float *dw, int M, int K);
 
+/* Softmax cross entropy of a linear head over a vocabulary of N, for training and for
+ * scoring: of the logits Z = X W^T, which are never kept,
+ *     lse_i = log sum_j exp(Z[i,j]),  loss_i = lse_i - Z[i,targets_i]
+ * X [M,K] hidden states and W [N,K] (a row to each entry of the vocabulary: the layout of
+ * an embedding, or of a linear layer's weight), row-major half or bf16 (dtype) with tight
+ * strides; targets int64 [M]; loss and lse FP32 [M] (lse null: not stored).  A target
+ * outside 0 .. N - 1 leaves its row out: loss 0 (lse is stored all the same), and no part
+ * in the gradients, whatever the row of X holds.  Logits, largest value, sum and
+ * logarithm in FP32.  Any M, N, K; K and the bases multiples of 8 elements are fastest:
+ * other operands are copied to padded rows in scratch, W a piece (up to 256 MiB) at a time.  Scratch:
+ * 8 bytes for each row and 128 entries, for up to 16384 rows at once, and the copies, in
+ * stream-ordered memory for the duration of the call from the library's pool (see
+ * gemm_gated).  K = 0: logits of 0; N = 0: lse is -inf.  GEMM_ERR_ALIAS if an output
+ * overlaps an input or the other output. */
+GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
+                                          float *loss, float *lse, int M, int N, int K);
+
+/* Its gradients from dloss FP32 [M], the weight of each row's loss, and lse as
+ * gemm_cross_entropy stored it:
+ *     dZ[i,j] = (exp(Z[i,j] - lse_i) - [j = targets_i]) dloss_i  (0 in rows left out)
+ *     dX = dZ W,  dW = dZ^T X
+ * dX [M,K], dW [N,K] (dtype), each overwritten; a null one is left out.  The logits are
+ * computed anew, a piece of the vocabulary at a time; dZ is formed in FP32 and rounded to
+ * dtype (half: scaled by a power of two from the largest |dloss|, so that small
+ * probabilities are not lost; loss scales up to FP32's range do no harm), the operand of
+ * the products, whose sums are FP32, in a fixed order, rounded once.  Scratch as above:
+ * a piece of dZ (256 MiB, or 256 entries of every row where that is more), FP32 sums of
+ * dX (up to 256 MiB, or once 4 M K bytes where that is more) and a copy of X (for dW, with
+ * zeros in the rows left out).  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as above. */
+GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
+                                                   const float *lse, const float *dloss, void *dX, void *dW, int M, int N,
+                                                   int K);
+
 /* Stream for the calling host thread's subsequent calls: a cudaStream_t passed
  * as void*.  NULL selects the legacy default stream.  The stream stays owned by
  * the caller and must outlive the calls issued on it. */
