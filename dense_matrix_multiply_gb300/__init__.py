@@ -56,6 +56,8 @@ SIGNATURES = {
     "gemm_rms_norm_backward": ([_I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I], _I),
     "gemm_cross_entropy": ([_I, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
     "gemm_cross_entropy_backward": ([_I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I], _I),
+    "gemm_orthogonalize": ([_I, _VP, ctypes.c_int64, _VP, ctypes.c_int64, _I, ctypes.c_float, ctypes.c_float,
+                            ctypes.c_float, _I, _I], _I),
     "gemm_set_stream": ([_VP], _I),
     "gemm_get_stream": ([], _VP),
     "gemm_synchronize": ([], _I),
@@ -579,6 +581,27 @@ def gemm_cross_entropy_backward(dtype: str, X, W, targets, lse, dloss, dX, dW, M
     st = lib.gemm_cross_entropy_backward(d, *p, M, N, K)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_cross_entropy_backward", lib.gemm_last_error().decode())
+
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+
+
+def gemm_orthogonalize(dtype: str, G, ldg: int, O, ldo: int, steps: int, M: int, N: int, coefficients=QUINTIC) -> None:
+    """O [M,N] = G / |G|_F after `steps` times X <- a X + (b A + c A^2) X, A = X X^T (X^T X
+    from the right for M > N), coefficients (a, b, c); 'f16' | 'bf16', leading dimensions
+    ldg and ldo; O may be G itself.  A tensor of two or more dimensions with other strides
+    than its leading dimension's is refused."""
+    lib = _lib or load()
+    d = _dtype16("gemm_orthogonalize", dtype)
+    M, N, ldg, ldo = int(M), int(N), int(ldg), int(ldo)
+    a, b, c = coefficients
+    ng, no = _fp4_span(M, N, ldg), _fp4_span(M, N, ldo)
+    _check_rows("gemm_orthogonalize: G", G, ldg, ng)
+    _check_rows("gemm_orthogonalize: O", O, ldo, no)
+    pg, po = _take(lib, "gemm_orthogonalize", ("G", G, 2, ng, False), ("O", O, 2, no, False))
+    st = lib.gemm_orthogonalize(d, pg, ldg, po, ldo, int(steps), a, b, c, M, N)
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_orthogonalize", lib.gemm_last_error().decode())
 
 
 def _rows_dims(M: int, K: int):

@@ -17,6 +17,7 @@
 #include "gemm.h"
 #include "internal.h"
 #include "norm.h"
+#include "orthogonalize.h"
 #include "scratch.h"
 
 using namespace gemm_gb300;
@@ -725,6 +726,30 @@ gemm_status_t run_cross_entropy_backward(int dtype, const void *X, const void *W
     return finish(launch_cross_entropy_backward(p, dev->status, t_stream), "cross_entropy_backward");
 }
 
+// ------------------------------------------------------------ orthogonalised update
+gemm_status_t run_orthogonalize(int dtype, const void *G, int64_t ldg, void *O, int64_t ldo, int steps, float a, float b,
+                                float c, int M, int N) {
+    const char *who = "gemm_orthogonalize";
+    if ((dtype != GEMM_F16 && dtype != GEMM_BF16) || M < 0 || N < 0 || steps < 1 || ldg < (N > 1 ? N : 1) ||
+        ldo < (N > 1 ? N : 1) || !elements_aligned(who, {G, O}, {}))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!(a - a == 0.0f && b - b == 0.0f && c - c == 0.0f)) {
+        snprintf(t_last_error, sizeof(t_last_error), "%s: the coefficients have to be finite", who);
+        return GEMM_ERR_INVALID_VALUE;
+    }
+    if (M == 0 || N == 0) { t_last_kernel = "noop"; return GEMM_OK; }
+    if (!G || !O) return GEMM_ERR_INVALID_VALUE;
+    long long g = 0, o = 0;
+    if (!span_elems(1, 0, M, ldg, N, &g) || !span_elems(1, 0, M, ldo, N, &o) || g > (1LL << 61) || o > (1LL << 61))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!(O == G && ldo == ldg) && overlaps(O, (size_t)o * 2, G, (size_t)g * 2)) return GEMM_ERR_ALIAS;
+    DeviceInfo *dev = nullptr;
+    gemm_status_t st = device_info(&dev);
+    if (st != GEMM_OK) return st;
+    const OrthProblem p{G, ldg, O, ldo, M, N, steps, a, b, c, elt16(dtype)};
+    return finish(launch_orthogonalize(p, dev->num_sms, dev->status, t_stream), "orthogonalize");
+}
+
 }  // namespace
 
 extern "C" {
@@ -954,6 +979,11 @@ GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const voi
                                                    const float *lse, const float *dloss, void *dX, void *dW, int M, int N,
                                                    int K) {
     return run_cross_entropy_backward((int)dtype, X, W, targets, lse, dloss, dX, dW, M, N, K);
+}
+
+GEMM_API gemm_status_t gemm_orthogonalize(gemm_dtype_t dtype, const void *G, int64_t ldg, void *O, int64_t ldo, int steps,
+                                          float a, float b, float c, int M, int N) {
+    return run_orthogonalize((int)dtype, G, ldg, O, ldo, steps, a, b, c, M, N);
 }
 
 GEMM_API gemm_status_t gemm_set_stream(void *cuda_stream) {

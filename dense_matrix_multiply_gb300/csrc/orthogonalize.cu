@@ -1,0 +1,385 @@
+// Orthogonalised update: the singular values of G / |G|_F driven towards 1 by steps of an
+// odd quintic polynomial, products only (Newton-Schulz):
+//     A = X X^T,  B = b A + c A^2,  X <- a X + B X
+// for M <= N; for M > N from the right, A = X^T X and X <- a X + X B, so that A is the
+// smaller square, m = min(M, N), without a transposed copy.
+//
+// Bound: the tensor cores, m^2 n + m^3 + 2 m^2 n operations a step: A and B are
+// symmetric, and only the tiles on and below the diagonal blocks of 256 are computed and
+// written twice, the second time transposed.
+//
+// Precision.  Operands are half: iterates and A are bounded by about 1.2 in norm, so
+// that half's 11 bits serve where bf16 has 8.  What the rounding of X loses in
+// directions of small singular values the coming steps magnify, up to 3.4 times each; so
+// X is kept as hi + lo, two halves (22 bits): the products take hi, the epilogue adds
+// a (hi + lo) in FP32 -- lo left out of B X costs lo times B, which is small in just those
+// directions.  Relative error (2-norm) of the five usual steps, in simulation against 64
+// bits, 512 x 1024: singular values from 1 down to 1e-4 7.5e-4 (hi alone 5.4e-3, bf16
+// 3e-2), Gaussian 1.6e-3, 16 strong directions in noise 1.5e-4 (4.0e-3).  G goes in
+// unrounded, times a power of two that takes |G|_F to [2^14, 2^15), and its norm is
+// applied to the sums.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "fp4.h"
+#include "orthogonalize.h"
+#include "pair_pipe.cuh"
+
+namespace gemm_gb300 {
+namespace {
+
+using namespace pair;
+
+constexpr float kLo = 2048.0f;  // lo is stored times 2^11, within half's normal range
+
+__device__ __forceinline__ float2 half2_at(uint32_t v) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); }
+
+// A [m, m] = f X X^T, or B = b A + c A A^T: both triangles.
+struct SymEpi {
+    static constexpr bool LOWER = true;
+    CUtensorMap tm, tmT;    // the output, and in boxes of 64 rows x 32 columns
+    const uint16_t *old;    // A, or null
+    long long ld;
+    const float *scale;     // null: 1; its square is a factor of the sums
+    float f, b;             // f the sums' other factor, b A's
+    int m;
+
+    __device__ __forceinline__ void run(const Part &p) const {
+        const int width = p.bn >> 1, row = p.row0 + p.lane;
+        const float s = scale ? *scale : 1.0f, by = f * s * s;
+        const bool mirror = p.col0 + p.bn <= p.row0 / 256 * 256;
+#pragma unroll 1
+        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+            const int c0 = p.col0 + g;
+            if (c0 >= m) return;  // warp-uniform
+            uint32_t z[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * by);
+                if (old && row < m) {
+                    const uint4 *o = reinterpret_cast<const uint4 *>(old + row * ld + c0 + h * 32);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 v = o[q];
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 e = half2_at(w[j]);
+                            const int k = q * 8 + j * 2;
+                            r[k] = __float_as_uint(fmaf(b, e.x, __uint_as_float(r[k])));
+                            r[k + 1] = __float_as_uint(fmaf(b, e.y, __uint_as_float(r[k + 1])));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    z[h * 16 + j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), (__half *)nullptr);
+            }
+            box_begin(p.lane);
+            box_put(p.box, p.lane, z);
+            box_store(&tm, p.box, p.lane, c0, p.row0, 0);
+            if (mirror) {
+                box_begin(p.lane);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {  // columns 2 j and 2 j + 1 are rows of 64 bytes, 64-byte swizzle
+                    const int r0 = 2 * j, at = (((p.lane >> 3) ^ (j & 3)) << 4) + (p.lane & 7) * 2;
+                    *reinterpret_cast<uint16_t *>(p.box + r0 * 64 + at) = (uint16_t)z[j];
+                    *reinterpret_cast<uint16_t *>(p.box + (r0 + 1) * 64 + at) = (uint16_t)(z[j] >> 16);
+                }
+                box_store(&tmT, p.box, p.lane, p.row0, c0, 0);
+            }
+        }
+    }
+};
+
+// X' = s (a (hi + lo) + sums): hi and lo, or the result in its own type.
+struct MulEpi {
+    static constexpr bool LOWER = false;
+    CUtensorMap tm, tmLo;         // hi or the result; lo
+    const uint16_t *hi, *lo;      // X (lo null: 0)
+    long long ld;
+    const float *scale;           // s; null: 1
+    float a;
+    int M, N;
+    int kind;                     // 0: hi and lo, 1: half, 2: bf16
+    uint16_t *out;                // not null: the result by the element
+    long long ldo;
+
+    __device__ __forceinline__ void run(const Part &p) const {
+        const int width = p.bn >> 1, row = p.row0 + p.lane;
+        const float s = scale ? *scale : 1.0f;
+#pragma unroll 1
+        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+            const int c0 = p.col0 + g;
+            if (c0 >= N) return;  // warp-uniform
+            uint32_t z[32], e[32];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
+                tmem_ld_wait();
+                if (row < M) {
+                    const long long at = row * ld + c0 + h * 32;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 v = reinterpret_cast<const uint4 *>(hi + at)[q];
+                        const uint4 u = lo ? reinterpret_cast<const uint4 *>(lo + at)[q] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w}, y[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 x = half2_at(w[j]), l = half2_at(y[j]);
+                            const int k = q * 8 + j * 2;
+                            r[k] = __float_as_uint(s * fmaf(a, fmaf(l.x, 1.0f / kLo, x.x), __uint_as_float(r[k])));
+                            r[k + 1] = __float_as_uint(s * fmaf(a, fmaf(l.y, 1.0f / kLo, x.y), __uint_as_float(r[k + 1])));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float x = __uint_as_float(r[2 * j]), y = __uint_as_float(r[2 * j + 1]);
+                    z[h * 16 + j] = kind == 2 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
+                    if (kind == 0) {
+                        const float2 v = half2_at(z[h * 16 + j]);
+                        e[h * 16 + j] = pack2((x - v.x) * kLo, (y - v.y) * kLo, (__half *)nullptr);
+                    }
+                }
+            }
+            box_begin(p.lane);
+            box_put(p.box, p.lane, z);
+            if (out) {
+                box_scatter(p.box, p.lane, out, ldo, p.row0, c0, M, N);
+                continue;
+            }
+            box_store(&tm, p.box, p.lane, c0, p.row0, 0);
+            if (kind == 0) {
+                box_begin(p.lane);
+                box_put(p.box, p.lane, e);
+                box_store(&tmLo, p.box, p.lane, c0, p.row0, 0);
+            }
+        }
+    }
+};
+
+// Sixteen packed 16-bit values in FP32.
+template <bool BF16>
+__device__ __forceinline__ void widen16(const uint32_t (&v)[8], float (&f)[16]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float2 t = BF16 ? make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xFFFF0000u)) : half2_at(v[j]);
+        f[2 * j] = t.x;
+        f[2 * j + 1] = t.y;
+    }
+}
+// The row pieces of 512 elements of G, dealt to the grid's warps: f(row, first element of
+// the lane's sixteen, its values; zeros past N).
+constexpr int SCAN_WARPS = 8;
+template <bool BF16, typename F>
+__device__ __forceinline__ void scan(const uint16_t *G, long long ldg, int M, int N, F f) {
+    const long long per = (N + 511LL) / 512, total = M * per;
+    const uint8_t *lo = reinterpret_cast<const uint8_t *>(G),
+                  *hi = reinterpret_cast<const uint8_t *>(G + (M - 1) * ldg + N);
+    for (long long i = (long long)blockIdx.x * SCAN_WARPS + (threadIdx.x >> 5); i < total;
+         i += (long long)gridDim.x * SCAN_WARPS) {
+        const long long row = i / per;
+        const long long k = (i - row * per) * 512 + (threadIdx.x & 31) * 16;
+        uint32_t v[8];
+        fp4_load16_any(G + row * ldg + k, (int)max(min(N - k, 512LL), -512LL), lo, hi, v);
+        float x[16];
+        widen16<BF16>(v, x);
+        f(row, k, x);
+    }
+}
+
+// Sums of squares, one to a CTA, in 64 bits: sixteen values at a time in FP32, taken by a
+// power of two so that the largest is in [1, 2) -- no square overflows or is lost.
+template <bool BF16>
+__global__ void __launch_bounds__(SCAN_WARPS * 32)
+orth_norm_kernel(const uint16_t *G, long long ldg, int M, int N, double *part)
+{
+    __shared__ double sums[SCAN_WARPS];
+    pdl_wait();
+    double sum = 0.0;
+    scan<BF16>(G, ldg, M, N, [&](long long, long long, const float(&x)[16]) {
+        float top = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x[j]));
+        const int e = max(min((int)(__float_as_uint(top) >> 23), 253), 1) - 127;
+        const float by = __uint_as_float((uint32_t)(127 - e) << 23);
+        float s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) s = fmaf(x[j] * by, x[j] * by, s);
+        sum += (double)s * __longlong_as_double((long long)(1023 + 2 * e) << 52);
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < SCAN_WARPS; ++w) sum += sums[w];
+    part[blockIdx.x] = sum;
+}
+
+// X = G 2^k in half, and s = 2^-k / |G|; every CTA adds the partial sums alike.  A matrix
+// of zeros has s = 0 (and stays zero), one with a NaN or an infinity s = NaN.
+template <bool BF16>
+__global__ void __launch_bounds__(SCAN_WARPS * 32)
+orth_start_kernel(const uint16_t *G, long long ldg, int M, int N, const double *part, int parts, float *scale, uint16_t *X,
+                  long long ldx)
+{
+    __shared__ float by_s;
+    pdl_wait();
+    if (threadIdx.x < 32) {
+        double sum = 0.0;
+        for (int i = threadIdx.x; i < parts; i += 32) sum += part[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(sum);
+            double by = 0.0, s = 0.0;
+            if (!isfinite(norm)) {
+                s = NAN;
+            } else if (norm > 0.0) {
+                int e;
+                frexp(norm, &e);
+                by = ldexp(1.0, max(min(15 - e, 126), -126));
+                s = 1.0 / (norm * by);
+            }
+            by_s = (float)by;
+            if (blockIdx.x == 0) *scale = (float)s;
+        }
+    }
+    __syncthreads();
+    const float by = by_s;
+    scan<BF16>(G, ldg, M, N, [&](long long row, long long k, const float(&x)[16]) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = pack2(x[2 * j] * by, x[2 * j + 1] * by, (__half *)nullptr);
+        uint4 *o = reinterpret_cast<uint4 *>(X + row * ldx + k);
+        if (k < ldx) o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (k + 8 < ldx) o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    });
+}
+
+long long up64(long long n) { return (n + 63) / 64 * 64; }
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStream_t s) {
+    const int cs = clusters_max<0, SymEpi>(dev), cm = clusters_max<0, MulEpi>(dev);
+    if (cs <= 0 || cm <= 0) return cudaErrorNotSupported;
+    const bool tall = p.M > p.N, bf16 = p.elt == Elt::BF16;
+    const int m = std::min(p.M, p.N), n = std::max(p.M, p.N);
+    const long long ldx = up64(p.N), lda = up64(m);
+    const size_t x_bytes = (size_t)p.M * ldx * 2, a_bytes = (size_t)m * lda * 2;
+    const int parts = (int)std::min<long long>(2LL * num_sms, ceil_div(p.M * ceil_div(p.N, 512), SCAN_WARPS));
+    auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
+    const size_t need = 4 * al(x_bytes) + 2 * al(a_bytes) + al((size_t)parts * 8) + 256;
+    void *ws = nullptr;
+    cudaError_t e = scratch_alloc(&ws, need, s);
+    if (e != cudaSuccess) return e;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    auto take = [&](size_t b) {
+        uint8_t *q = at;
+        at += al(b);
+        return q;
+    };
+    uint16_t *hi[2], *lo[2];
+    for (int i = 0; i < 2; ++i) {
+        hi[i] = reinterpret_cast<uint16_t *>(take(x_bytes));
+        lo[i] = reinterpret_cast<uint16_t *>(take(x_bytes));
+    }
+    uint16_t *A = reinterpret_cast<uint16_t *>(take(a_bytes)), *B = reinterpret_cast<uint16_t *>(take(a_bytes));
+    double *part = reinterpret_cast<double *>(take((size_t)parts * 8));
+    float *scale = reinterpret_cast<float *>(take(4));
+
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)parts), dim3(SCAN_WARPS * 32), 0, s, attr);
+    const uint16_t *G = static_cast<const uint16_t *>(p.G);
+    e = bf16 ? launch_counted(&cfg, orth_norm_kernel<true>, G, p.ldg, p.M, p.N, part)
+             : launch_counted(&cfg, orth_norm_kernel<false>, G, p.ldg, p.M, p.N, part);
+    if (e == cudaSuccess)
+        e = bf16 ? launch_counted(&cfg, orth_start_kernel<true>, G, p.ldg, p.M, p.N, static_cast<const double *>(part), parts,
+                                  scale, hi[0], ldx)
+                 : launch_counted(&cfg, orth_start_kernel<false>, G, p.ldg, p.M, p.N, static_cast<const double *>(part), parts,
+                                  scale, hi[0], ldx);
+    const long long sym_tiles = lower_tiles(m, 256), mul_tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
+    if (sym_tiles > 0x7FFFFFFFLL || mul_tiles > 0x7FFFFFFFLL) e = cudaErrorInvalidValue;
+    SymEpi sy;
+    MulEpi mu;
+    CUtensorMap ta, tb, xa, xb, outA, outAT, outB, outBT, hiM[2], loM[2];
+    bool ok = map16(&outA, A, 0, m, m, lda, 32, 64) && map16(&outB, B, 0, m, m, lda, 32, 64) &&
+              make_map3(&outAT, A, map_type(0), m, m, 1, lda * 2, m * lda * 2, 32, 64, 1, 64) &&
+              make_map3(&outBT, B, map_type(0), m, m, 1, lda * 2, m * lda * 2, 32, 64, 1, 64) &&
+              map_operand(&ta, A, 0, false, m, m, lda, 128) && map_operand(&tb, B, 0, false, m, m, lda, 128);
+    for (int i = 0; i < 2; ++i)
+        ok = ok && map16(&hiM[i], hi[i], 0, p.M, p.N, ldx, 32, 64) && map16(&loM[i], lo[i], 0, p.M, p.N, ldx, 32, 64);
+    const bool tma_out = ((uintptr_t)p.O & 15) == 0 && p.ldo % 8 == 0;
+    CUtensorMap res = hiM[0];
+    if (tma_out) ok = ok && map16(&res, p.O, bf16 ? 1 : 0, p.M, p.N, p.ldo, 32, 64);
+    if (!ok) e = cudaErrorInvalidValue;
+    for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
+        const int in = i & 1, out = in ^ 1;
+        const bool last = i == p.steps - 1;
+        // A = X X^T, or X^T X
+        if (!map_operand(&xa, hi[in], 0, tall, m, n, ldx, 128) || !map_operand(&xb, hi[in], 0, !tall, tall ? p.M : p.N, m, ldx, 128)) {
+            e = cudaErrorInvalidValue;
+            break;
+        }
+        sy.tm = outA;
+        sy.tmT = outAT;
+        sy.old = nullptr;
+        sy.ld = lda;
+        sy.scale = i == 0 ? scale : nullptr;
+        sy.f = 1.0f;
+        sy.b = 0.0f;
+        sy.m = m;
+        Args g = {m, m, (int)ceil_div(n, BK), 256, tall, tall, (int)sym_tiles, 1, status};
+        e = launch<0>(xa, xa, sy, g, cs, s);
+        if (e != cudaSuccess) break;
+        sy.tm = outB;
+        sy.tmT = outBT;
+        sy.old = A;
+        sy.scale = nullptr;
+        sy.f = p.c;
+        sy.b = p.b;
+        g = {m, m, (int)ceil_div(m, BK), 256, 0, 0, (int)sym_tiles, 1, status};
+        e = launch<0>(ta, ta, sy, g, cs, s);
+        if (e != cudaSuccess) break;
+        mu.tm = last ? res : hiM[out];
+        mu.tmLo = loM[out];
+        mu.hi = hi[in];
+        mu.lo = i == 0 ? nullptr : lo[in];
+        mu.ld = ldx;
+        mu.scale = i == 0 ? scale : nullptr;
+        mu.a = p.a;
+        mu.M = p.M;
+        mu.N = p.N;
+        mu.kind = last ? (bf16 ? 2 : 1) : 0;
+        mu.out = last && !tma_out ? static_cast<uint16_t *>(p.O) : nullptr;
+        mu.ldo = p.ldo;
+        // B X: B's rows and X, [m, N], N-major; X B: X's rows and B's
+        g = {p.M, p.N, (int)ceil_div(m, BK), 256, 0, !tall, (int)mul_tiles, 1, status};
+        e = tall ? launch<0>(xb, tb, mu, g, cm, s) : launch<0>(tb, xb, mu, g, cm, s);
+    }
+    const cudaError_t f = cudaFreeAsync(ws, s);
+    return e != cudaSuccess ? e : f;
+}
+
+}  // namespace
+
+cudaError_t launch_orthogonalize(const OrthProblem &p, int num_sms, int *status, cudaStream_t s) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    return run(p, dev, num_sms, status, s);
+}
+
+}  // namespace gemm_gb300

@@ -434,6 +434,23 @@ GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const voi
                                                    const float *lse, const float *dloss, void *dX, void *dW, int M, int N,
                                                    int K);
 
+/* Orthogonalised update of a weight matrix (the matrix that an optimiser such as Muon
+ * applies in place of its momentum G): singular values driven towards 1 by products,
+ *     X = G / |G|_F,  then `steps` times  X <- a X + (b A + c A^2) X,  A = X X^T
+ * (from the right, with A = X^T X, where M > N: the same in exact arithmetic).  G and O
+ * [M,N] row-major half or bf16 (dtype) with leading dimensions ldg, ldo >= N; O may be G
+ * itself (with ldo = ldg).  The usual five steps with a = 3.4445, b = -4.7750, c = 2.0315
+ * bring singular values from about 0.01 of |G|_F up to between 0.7 and 1.2.  steps >= 1;
+ * a, b, c finite, and such that X and A stay within half's range: intermediate matrices
+ * are half (X in two halves, 22 bits), sums and |G|_F^2 FP32 or more.  The relative error
+ * of the usual five steps is 1e-3 to 2e-3 (2-norm) before O's own rounding.  A matrix of
+ * zeros gives zeros; a NaN or an infinity in G makes O NaN.  Any M, N and alignment of
+ * elements.  Scratch: 8 bytes for each element of G and 4 for each of A, in stream-ordered
+ * memory for the duration of the call from the library's pool (see gemm_gated).
+ * GEMM_ERR_ALIAS if O overlaps G otherwise. */
+GEMM_API gemm_status_t gemm_orthogonalize(gemm_dtype_t dtype, const void *G, int64_t ldg, void *O, int64_t ldo, int steps,
+                                          float a, float b, float c, int M, int N);
+
 /* Stream for the calling host thread's subsequent calls: a cudaStream_t passed
  * as void*.  NULL selects the legacy default stream.  The stream stays owned by
  * the caller and must outlive the calls issued on it. */
