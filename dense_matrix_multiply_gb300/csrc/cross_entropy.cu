@@ -38,14 +38,17 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 units of 2^-23 off; 0
 
 // Of the columns [c0, c0 + 32) within a row's [0, N), c0 < N: the rest count as -inf.
 struct LseEpi {
-    static constexpr bool LOWER = false;
+    static constexpr bool LOWER = false, JOIN = false;
+    static constexpr int BOXES = 1;
     float2 *part;             // (m, s) of slot column / (bn / 2), [slot][M]
     float *zt;                // Z_i,t_i
     const long long *target;
     int M, N, v0, total;      // rows; columns of this piece, and its first; of Z
 
-    __device__ __forceinline__ void run(const Part &p) const {
-        const int row = p.row0 + p.lane, width = p.bn >> 1, first = p.col0 + p.half * width;
+    struct Pre {};
+    __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
+    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
+        const int row = p.row0 + p.lane, width = p.width, first = p.col0 + p.first;
         if (first >= N) return;  // warp-uniform
         long long t = row < M ? target[row] : -1;
         t = t >= 0 && t < total ? t - v0 : -1;
@@ -53,8 +56,7 @@ struct LseEpi {
 #pragma unroll 1
         for (int c = 0; c < width && first + c < N; c += 32) {
             uint32_t r[32];
-            tmem_ld32(p.tmem + (uint32_t)(p.half * width + c), r);
-            tmem_ld_wait();
+            p.load<false>(p.first + c, r);
             const int left = N - first - c;
             if (left < 32) {  // warp-uniform
 #pragma unroll
@@ -90,7 +92,8 @@ struct LseEpi {
 
 // Scale factors of dZ: (up, down), powers of two whose product is 1.
 struct DzEpi {
-    static constexpr bool LOWER = false;
+    static constexpr bool LOWER = false, JOIN = false;
+    static constexpr int BOXES = 1;
     CUtensorMap tm;  // dZ of the piece
     const float *lse, *dloss;
     const long long *target;
@@ -98,23 +101,24 @@ struct DzEpi {
     int M, N, v0, total;  // total: columns of Z
     bool bf16;
 
-    __device__ __forceinline__ void run(const Part &p) const {
-        const int row = p.row0 + p.lane, width = p.bn >> 1;
+    struct Pre {};
+    __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
+    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
+        const int row = p.row0 + p.lane;
         long long t = row < M ? target[row] : -1;
         const bool counts = t >= 0 && t < total;
         const float d = counts ? dloss[row] * (scale ? scale->x : 1.0f) : 0.0f;
         const float base = counts ? lse[row] * kLog2e : 0.0f;
         t = counts ? t - v0 : -1;
 #pragma unroll 1
-        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+        for (int g = p.first; g < p.first + p.width; g += 64) {
             const int c0 = p.col0 + g;
             if (c0 >= N) return;  // warp-uniform
             uint32_t z[32];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
-                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
-                tmem_ld_wait();
+                p.load<false>(g + h * 32, r);
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -base));
@@ -139,19 +143,20 @@ struct DzEpi {
 
 // FP32 sums to slab `split`, or added to it.
 struct AccEpi {
-    static constexpr bool LOWER = false;
+    static constexpr bool LOWER = false, JOIN = false;
+    static constexpr int BOXES = 1;
     CUtensorMap tm;
     int N;
     bool add;
 
-    __device__ __forceinline__ void run(const Part &p) const {
-        const int width = p.bn >> 1;
+    struct Pre {};
+    __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
+    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
 #pragma unroll 1
-        for (int g = p.half * width; g < (p.half + 1) * width; g += 32) {
+        for (int g = p.first; g < p.first + p.width; g += 32) {
             if (p.col0 + g >= N) return;  // warp-uniform
             uint32_t r[32];
-            tmem_ld32(p.tmem + (uint32_t)g, r);
-            tmem_ld_wait();
+            p.load<false>(g, r);
             box_begin(p.lane);
             box_put(p.box, p.lane, r);
             if (add) {
@@ -167,7 +172,8 @@ struct AccEpi {
 
 // 16-bit results times scale->y.
 struct OutEpi {
-    static constexpr bool LOWER = false;
+    static constexpr bool LOWER = false, JOIN = false;
+    static constexpr int BOXES = 1;
     CUtensorMap tm;
     const float2 *scale;  // null: 1
     uint16_t *out;        // not null: by the element, rows ld apart
@@ -175,19 +181,19 @@ struct OutEpi {
     int M, N;
     bool bf16;
 
-    __device__ __forceinline__ void run(const Part &p) const {
-        const int width = p.bn >> 1;
+    struct Pre {};
+    __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
+    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
         const float f = scale ? scale->y : 1.0f;
 #pragma unroll 1
-        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+        for (int g = p.first; g < p.first + p.width; g += 64) {
             const int c0 = p.col0 + g;
             if (c0 >= N) return;  // warp-uniform
             uint32_t z[32];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
-                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
-                tmem_ld_wait();
+                p.load<false>(g + h * 32, r);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float x = __uint_as_float(r[2 * j]) * f, y = __uint_as_float(r[2 * j + 1]) * f;
@@ -390,7 +396,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             }
             epi.N = n;
             epi.v0 = (int)v0;
-            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, status};
+            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, 1, status};
             e = launch<FORMAT>(ta, tb, epi, a, cmax, s);
         }
         if (e != cudaSuccess) break;
@@ -485,7 +491,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.v0 = (int)v0;
             epi.total = p.N;
             epi.bf16 = bf16;
-            const Args a = {p.M, n, (int)ceil_div(kp, BK), 256, 0, 0, (int)z_tiles, 1, status};
+            const Args a = {p.M, n, (int)ceil_div(kp, BK), 256, 0, 0, (int)z_tiles, 1, 1, status};
             e = launch<FORMAT>(ta, tb, epi, a, cz, s);
         }
         if (e == cudaSuccess && p.dW) {
@@ -503,7 +509,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.M = n;
             epi.N = p.K;
             epi.bf16 = bf16;
-            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, status};
+            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, status};
             e = launch<FORMAT>(ta, tb, epi, a, cw, s);
         }
         if (e == cudaSuccess && p.dX) {
@@ -518,7 +524,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.add = v0 > 0;
             // (a short last piece: fewer ranges, each of one block at least)
             const int kb = (int)ceil_div(n, BK);
-            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), status};
+            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, status};
             e = launch<FORMAT>(ta, tb, epi, a, cx, s);
         }
     }

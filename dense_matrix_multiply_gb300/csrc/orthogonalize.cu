@@ -38,9 +38,46 @@ constexpr float kLo = 2048.0f;  // lo is stored times 2^11, within half's normal
 
 __device__ __forceinline__ float2 half2_at(uint32_t v) { return __half22float2(*reinterpret_cast<__half2 *>(&v)); }
 
+// A 32 x 64 block of half from memory, a row to eight lanes and four rows to a load (a row
+// to a lane costs a load 32 cycles), and each lane's row of it, through the warp's box.
+struct Block {
+    uint4 v[8];
+    // rows left, 1 or more: those from row0 on that exist
+    __device__ __forceinline__ void fetch(const uint16_t *at, long long ld, int lane, int rows) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            if (r < rows) v[i] = *reinterpret_cast<const uint4 *>(at + r * ld + (lane & 7) * 8);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void to_box(uint8_t *box, int lane) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            *reinterpret_cast<uint4 *>(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = v[i];
+        }
+    }
+};
+// Half h of a lane's row: 32 values.
+__device__ __forceinline__ void row_half(const uint8_t *box, int lane, int h, uint32_t (&w)[16]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(box + lane * 128 + (((h * 4 + c) ^ (lane & 7)) << 4));
+        w[4 * c] = v.x;
+        w[4 * c + 1] = v.y;
+        w[4 * c + 2] = v.z;
+        w[4 * c + 3] = v.w;
+    }
+}
+
 // A [m, m] = f X X^T, or B = b A + c A A^T: both triangles.
 struct SymEpi {
-    static constexpr bool LOWER = true;
+    static constexpr bool LOWER = true, JOIN = true;
+    static constexpr int BOXES = 2;
     CUtensorMap tm, tmT;    // the output, and in boxes of 64 rows x 32 columns
     const uint16_t *old;    // A, or null
     long long ld;
@@ -48,53 +85,55 @@ struct SymEpi {
     float f, b;             // f the sums' other factor, b A's
     int m;
 
-    __device__ __forceinline__ void run(const Part &p) const {
-        const int width = p.bn >> 1, row = p.row0 + p.lane;
+    struct Pre {
+        Block old;
+    };
+    // The tile's columns c .. c + 63 of A.
+    __device__ __forceinline__ void fetch(const Part &p, int c, Pre &pre) const {
+        if (old && p.col0 + c < m) pre.old.fetch(old + p.row0 * ld + p.col0 + c, ld, p.lane, m - p.row0);
+    }
+    __device__ __forceinline__ void prefetch(const Part &p, Pre &pre) const {
+        pre.old.clear();
+        fetch(p, p.first, pre);
+    }
+    __device__ __forceinline__ void run(const Part &p, Pre &pre) const {
         const float s = scale ? *scale : 1.0f, by = f * s * s;
         const bool mirror = p.col0 + p.bn <= p.row0 / 256 * 256;
 #pragma unroll 1
-        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+        for (int g = p.first; g < p.first + p.width; g += 64) {
             const int c0 = p.col0 + g;
             if (c0 >= m) return;  // warp-uniform
+            box_begin(p.lane);
+            if (old) {
+                pre.old.to_box(p.box, p.lane);
+                __syncwarp();
+                if (g + 64 < p.first + p.width) fetch(p, g + 64, pre);
+            }
             uint32_t z[32];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
-                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
-                tmem_ld_wait();
+                p.load<true>(g + h * 32, r);
+                uint32_t w[16] = {};
+                if (old) row_half(p.box, p.lane, h, w);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * by);
-                if (old && row < m) {
-                    const uint4 *o = reinterpret_cast<const uint4 *>(old + row * ld + c0 + h * 32);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 v = o[q];
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 e = half2_at(w[j]);
-                            const int k = q * 8 + j * 2;
-                            r[k] = __float_as_uint(fmaf(b, e.x, __uint_as_float(r[k])));
-                            r[k + 1] = __float_as_uint(fmaf(b, e.y, __uint_as_float(r[k + 1])));
-                        }
-                    }
+                for (int j = 0; j < 16; ++j) {
+                    const float2 e = half2_at(w[j]);
+                    z[h * 16 + j] = pack2(fmaf(b, e.x, __uint_as_float(r[2 * j]) * by),
+                                          fmaf(b, e.y, __uint_as_float(r[2 * j + 1]) * by), (__half *)nullptr);
                 }
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    z[h * 16 + j] = pack2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]), (__half *)nullptr);
             }
-            box_begin(p.lane);
-            box_put(p.box, p.lane, z);
+            box_put(p.box, p.lane, z);  // (each lane its own row, which it alone has read)
             box_store(&tm, p.box, p.lane, c0, p.row0, 0);
             if (mirror) {
-                box_begin(p.lane);
+                uint8_t *box = p.box + STG_BOX;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {  // columns 2 j and 2 j + 1 are rows of 64 bytes, 64-byte swizzle
                     const int r0 = 2 * j, at = (((p.lane >> 3) ^ (j & 3)) << 4) + (p.lane & 7) * 2;
-                    *reinterpret_cast<uint16_t *>(p.box + r0 * 64 + at) = (uint16_t)z[j];
-                    *reinterpret_cast<uint16_t *>(p.box + (r0 + 1) * 64 + at) = (uint16_t)(z[j] >> 16);
+                    *reinterpret_cast<uint16_t *>(box + r0 * 64 + at) = (uint16_t)z[j];
+                    *reinterpret_cast<uint16_t *>(box + (r0 + 1) * 64 + at) = (uint16_t)(z[j] >> 16);
                 }
-                box_store(&tmT, p.box, p.lane, p.row0, c0, 0);
+                box_store(&tmT, box, p.lane, p.row0, c0, 0);
             }
         }
     }
@@ -102,7 +141,8 @@ struct SymEpi {
 
 // X' = s (a (hi + lo) + sums): hi and lo, or the result in its own type.
 struct MulEpi {
-    static constexpr bool LOWER = false;
+    static constexpr bool LOWER = false, JOIN = true;
+    static constexpr int BOXES = 2;
     CUtensorMap tm, tmLo;         // hi or the result; lo
     const uint16_t *hi, *lo;      // X (lo null: 0)
     long long ld;
@@ -113,57 +153,57 @@ struct MulEpi {
     uint16_t *out;                // not null: the result by the element
     long long ldo;
 
-    __device__ __forceinline__ void run(const Part &p) const {
-        const int width = p.bn >> 1, row = p.row0 + p.lane;
+    struct Pre {
+        Block hi, lo;
+    };
+    __device__ __forceinline__ void fetch(const Part &p, int c, Pre &pre) const {
+        if (p.col0 + c >= N) return;
+        const long long at = p.row0 * ld + p.col0 + c;
+        pre.hi.fetch(hi + at, ld, p.lane, M - p.row0);
+        if (lo) pre.lo.fetch(lo + at, ld, p.lane, M - p.row0);
+    }
+    __device__ __forceinline__ void prefetch(const Part &p, Pre &pre) const {
+        pre.hi.clear();
+        pre.lo.clear();
+        fetch(p, p.first, pre);
+    }
+    __device__ __forceinline__ void run(const Part &p, Pre &pre) const {
         const float s = scale ? *scale : 1.0f;
 #pragma unroll 1
-        for (int g = p.half * width; g < (p.half + 1) * width; g += 64) {
+        for (int g = p.first; g < p.first + p.width; g += 64) {
             const int c0 = p.col0 + g;
             if (c0 >= N) return;  // warp-uniform
-            uint32_t z[32], e[32];
+            uint8_t *box_lo = p.box + STG_BOX;
+            box_begin(p.lane);
+            pre.hi.to_box(p.box, p.lane);
+            if (lo) pre.lo.to_box(box_lo, p.lane);
+            __syncwarp();
+            if (g + 64 < p.first + p.width) fetch(p, g + 64, pre);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t r[32];
-                tmem_ld32(p.tmem + (uint32_t)(g + h * 32), r);
-                tmem_ld_wait();
-                if (row < M) {
-                    const long long at = row * ld + c0 + h * 32;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint4 v = reinterpret_cast<const uint4 *>(hi + at)[q];
-                        const uint4 u = lo ? reinterpret_cast<const uint4 *>(lo + at)[q] : make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w}, y[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 x = half2_at(w[j]), l = half2_at(y[j]);
-                            const int k = q * 8 + j * 2;
-                            r[k] = __float_as_uint(s * fmaf(a, fmaf(l.x, 1.0f / kLo, x.x), __uint_as_float(r[k])));
-                            r[k + 1] = __float_as_uint(s * fmaf(a, fmaf(l.y, 1.0f / kLo, x.y), __uint_as_float(r[k + 1])));
-                        }
-                    }
-                }
+                uint32_t r[32], z[16], w[16], e[16] = {};
+                p.load<true>(g + h * 32, r);
+                row_half(p.box, p.lane, h, w);
+                if (lo) row_half(box_lo, p.lane, h, e);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float x = __uint_as_float(r[2 * j]), y = __uint_as_float(r[2 * j + 1]);
-                    z[h * 16 + j] = kind == 2 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
-                    if (kind == 0) {
-                        const float2 v = half2_at(z[h * 16 + j]);
-                        e[h * 16 + j] = pack2((x - v.x) * kLo, (y - v.y) * kLo, (__half *)nullptr);
-                    }
+                    const float2 u = half2_at(w[j]), l = half2_at(e[j]);
+                    const float x = s * fmaf(a, fmaf(l.x, 1.0f / kLo, u.x), __uint_as_float(r[2 * j]));
+                    const float y = s * fmaf(a, fmaf(l.y, 1.0f / kLo, u.y), __uint_as_float(r[2 * j + 1]));
+                    z[j] = kind == 2 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
+                    const float2 v = half2_at(z[j]);
+                    e[j] = pack2((x - v.x) * kLo, (y - v.y) * kLo, (__half *)nullptr);
                 }
+                // (each lane its own row, which it alone has read)
+                box_put_half(p.box, p.lane, h, z);
+                if (kind == 0) box_put_half(box_lo, p.lane, h, e);
             }
-            box_begin(p.lane);
-            box_put(p.box, p.lane, z);
             if (out) {
                 box_scatter(p.box, p.lane, out, ldo, p.row0, c0, M, N);
                 continue;
             }
             box_store(&tm, p.box, p.lane, c0, p.row0, 0);
-            if (kind == 0) {
-                box_begin(p.lane);
-                box_put(p.box, p.lane, e);
-                box_store(&tmLo, p.box, p.lane, c0, p.row0, 0);
-            }
+            if (kind == 0) box_store(&tmLo, box_lo, p.lane, c0, p.row0, 0);
         }
     }
 };
@@ -234,14 +274,18 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32)
 orth_start_kernel(const uint16_t *G, long long ldg, int M, int N, const double *part, int parts, float *scale, uint16_t *X,
                   long long ldx)
 {
+    __shared__ double sums[SCAN_WARPS];
     __shared__ float by_s;
     pdl_wait();
-    if (threadIdx.x < 32) {
-        double sum = 0.0;
-        for (int i = threadIdx.x; i < parts; i += 32) sum += part[i];
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < parts; i += SCAN_WARPS * 32) sum += part[i];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    {
         if (threadIdx.x == 0) {
+            for (int w = 1; w < SCAN_WARPS; ++w) sum += sums[w];
             const double norm = sqrt(sum);
             double by = 0.0, s = 0.0;
             if (!isfinite(norm)) {
@@ -271,14 +315,41 @@ orth_start_kernel(const uint16_t *G, long long ldg, int M, int N, const double *
 long long up64(long long n) { return (n + 63) / 64 * 64; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
+// A product's tiles: their width, and pairs joined on a tile, as are done first.  Times in
+// 1/100 us: a block of 64 k of 256 x bn, a tile's writing, a join.
+struct Plan {
+    int bn, joined, clusters;
+    long long tiles;
+};
+Plan plan(bool lower, int rows, int cols, int k, int dev) {
+    const long long kb = ceil_div(k, BK);
+    Plan best = {};
+    long long least = 0;
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        const long long tiles = lower ? lower_tiles(rows, bn) : ceil_div(rows, 256) * ceil_div(cols, bn);
+        if (tiles > 0x7FFFFFFFLL) continue;
+        for (int joined = 1; joined <= (bn == 128 ? 2 : 1); ++joined) {
+            const int c = joined == 1 ? (lower ? clusters_max<0, SymEpi>(dev) : clusters_max<0, MulEpi>(dev))
+                                      : (lower ? joined_max<0, SymEpi>(dev) : joined_max<0, MulEpi>(dev));
+            if (c <= 0 || joined > kb) continue;
+            const long long block = bn == 256 ? 30 : 20, write = bn == 256 ? 250 : joined == 1 ? 150 : 250;
+            const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * block + write;
+            if (!best.bn || time < least) {
+                best = {bn, joined, c, tiles};
+                least = time;
+            }
+        }
+    }
+    return best;
+}
+
 cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStream_t s) {
-    const int cs = clusters_max<0, SymEpi>(dev), cm = clusters_max<0, MulEpi>(dev);
-    if (cs <= 0 || cm <= 0) return cudaErrorNotSupported;
+    if (clusters_max<0, SymEpi>(dev) <= 0 || clusters_max<0, MulEpi>(dev) <= 0) return cudaErrorNotSupported;
     const bool tall = p.M > p.N, bf16 = p.elt == Elt::BF16;
     const int m = std::min(p.M, p.N), n = std::max(p.M, p.N);
     const long long ldx = up64(p.N), lda = up64(m);
     const size_t x_bytes = (size_t)p.M * ldx * 2, a_bytes = (size_t)m * lda * 2;
-    const int parts = (int)std::min<long long>(2LL * num_sms, ceil_div(p.M * ceil_div(p.N, 512), SCAN_WARPS));
+    const int parts = (int)std::min<long long>(8LL * num_sms, ceil_div(p.M * ceil_div(p.N, 512), SCAN_WARPS));
     auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
     const size_t need = 4 * al(x_bytes) + 2 * al(a_bytes) + al((size_t)parts * 8) + 256;
     void *ws = nullptr;
@@ -309,29 +380,34 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
                                   scale, hi[0], ldx)
                  : launch_counted(&cfg, orth_start_kernel<false>, G, p.ldg, p.M, p.N, static_cast<const double *>(part), parts,
                                   scale, hi[0], ldx);
-    const long long sym_tiles = lower_tiles(m, 256), mul_tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
-    if (sym_tiles > 0x7FFFFFFFLL || mul_tiles > 0x7FFFFFFFLL) e = cudaErrorInvalidValue;
+    // A over n, B over m, X over m
+    const Plan pa = plan(true, m, m, n, dev), pb = plan(true, m, m, m, dev), px = plan(false, p.M, p.N, m, dev);
+    if (e == cudaSuccess && (!pa.bn || !pb.bn || !px.bn)) e = cudaErrorInvalidValue;
     SymEpi sy;
     MulEpi mu;
-    CUtensorMap ta, tb, xa, xb, outA, outAT, outB, outBT, hiM[2], loM[2];
+    CUtensorMap aL, aR, aM, outA, outAT, outB, outBT, hiM[2], loM[2], sym[2][2], mul[2];
+    // operands: A's rows as the left one, and as the right one of B's product and of X's
     bool ok = map16(&outA, A, 0, m, m, lda, 32, 64) && map16(&outB, B, 0, m, m, lda, 32, 64) &&
               make_map3(&outAT, A, map_type(0), m, m, 1, lda * 2, m * lda * 2, 32, 64, 1, 64) &&
               make_map3(&outBT, B, map_type(0), m, m, 1, lda * 2, m * lda * 2, 32, 64, 1, 64) &&
-              map_operand(&ta, A, 0, false, m, m, lda, 128) && map_operand(&tb, B, 0, false, m, m, lda, 128);
+              map_operand(&aL, A, 0, false, m, m, lda, 128) && map_operand(&aR, A, 0, false, m, m, lda, pb.bn / 2) &&
+              map_operand(&aM, B, 0, false, m, m, lda, tall ? px.bn / 2 : 128);
     for (int i = 0; i < 2; ++i)
-        ok = ok && map16(&hiM[i], hi[i], 0, p.M, p.N, ldx, 32, 64) && map16(&loM[i], lo[i], 0, p.M, p.N, ldx, 32, 64);
+        ok = ok && map16(&hiM[i], hi[i], 0, p.M, p.N, ldx, 32, 64) && map16(&loM[i], lo[i], 0, p.M, p.N, ldx, 32, 64) &&
+             map_operand(&sym[i][0], hi[i], 0, tall, m, n, ldx, 128) &&
+             map_operand(&sym[i][1], hi[i], 0, tall, m, n, ldx, pa.bn / 2) &&
+             map_operand(&mul[i], hi[i], 0, !tall, n, m, ldx, 128);
     const bool tma_out = ((uintptr_t)p.O & 15) == 0 && p.ldo % 8 == 0;
     CUtensorMap res = hiM[0];
     if (tma_out) ok = ok && map16(&res, p.O, bf16 ? 1 : 0, p.M, p.N, p.ldo, 32, 64);
-    if (!ok) e = cudaErrorInvalidValue;
+    if (!ok && e == cudaSuccess) e = cudaErrorInvalidValue;
+    auto args = [&](int rows, int cols, int k, const Plan &q, bool a_mn, bool b_mn) {
+        return Args{rows, cols, (int)ceil_div(k, BK), q.bn, a_mn, b_mn, (int)q.tiles, 1, q.joined, status};
+    };
     for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
         const int in = i & 1, out = in ^ 1;
         const bool last = i == p.steps - 1;
         // A = X X^T, or X^T X
-        if (!map_operand(&xa, hi[in], 0, tall, m, n, ldx, 128) || !map_operand(&xb, hi[in], 0, !tall, tall ? p.M : p.N, m, ldx, 128)) {
-            e = cudaErrorInvalidValue;
-            break;
-        }
         sy.tm = outA;
         sy.tmT = outAT;
         sy.old = nullptr;
@@ -340,8 +416,7 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
         sy.f = 1.0f;
         sy.b = 0.0f;
         sy.m = m;
-        Args g = {m, m, (int)ceil_div(n, BK), 256, tall, tall, (int)sym_tiles, 1, status};
-        e = launch<0>(xa, xa, sy, g, cs, s);
+        e = launch<0>(sym[in][0], sym[in][1], sy, args(m, m, n, pa, tall, tall), pa.clusters, s);
         if (e != cudaSuccess) break;
         sy.tm = outB;
         sy.tmT = outBT;
@@ -349,8 +424,7 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
         sy.scale = nullptr;
         sy.f = p.c;
         sy.b = p.b;
-        g = {m, m, (int)ceil_div(m, BK), 256, 0, 0, (int)sym_tiles, 1, status};
-        e = launch<0>(ta, ta, sy, g, cs, s);
+        e = launch<0>(aL, aR, sy, args(m, m, m, pb, false, false), pb.clusters, s);
         if (e != cudaSuccess) break;
         mu.tm = last ? res : hiM[out];
         mu.tmLo = loM[out];
@@ -365,8 +439,8 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
         mu.out = last && !tma_out ? static_cast<uint16_t *>(p.O) : nullptr;
         mu.ldo = p.ldo;
         // B X: B's rows and X, [m, N], N-major; X B: X's rows and B's
-        g = {p.M, p.N, (int)ceil_div(m, BK), 256, 0, !tall, (int)mul_tiles, 1, status};
-        e = tall ? launch<0>(xb, tb, mu, g, cm, s) : launch<0>(tb, xb, mu, g, cm, s);
+        e = tall ? launch<0>(mul[in], aM, mu, args(p.M, p.N, m, px, false, false), px.clusters, s)
+                 : launch<0>(aM, mul[in], mu, args(p.M, p.N, m, px, false, true), px.clusters, s);
     }
     const cudaError_t f = cudaFreeAsync(ws, s);
     return e != cudaSuccess ? e : f;

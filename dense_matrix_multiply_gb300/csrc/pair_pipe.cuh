@@ -11,6 +11,11 @@
 // that a tile is written while the next is computed.  Clusters walk over the units (a
 // tile, or one of its K ranges) in the same order.
 //
+// Where there are few tiles of a long K, two pairs of one cluster are joined on a tile of
+// 256 x 128, half of K each: every CTA stores the FP32 sums of the other pair's 64 columns
+// to the shared memory of its counterpart there and writes out its own 64.  (All of a
+// tile's sums through the cluster, among four pairs: 7 us a tile; this way about 1.)
+//
 // Every wait is bounded; on expiry a code goes to the status word, both CTAs give up,
 // their loads and MMAs are waited for, and the tensor memory is released.
 #pragma once
@@ -24,21 +29,23 @@ using namespace tc;
 
 constexpr int THREADS = 320, EPI_WARPS = 8;
 constexpr int BK = 64;                 // 16-bit k per stage: 128 bytes a row
-constexpr int STAGES = 6;
 constexpr int A_STAGE = 128 * BK * 2;  // 16 KiB per CTA
 constexpr int B_STAGE = 128 * BK * 2;  // up to 128 of the tile's columns
 constexpr int BOX64 = 64 * BK * 2;     // 64 columns x 64 k of an MN-major tile
-constexpr int STG_BOX = 4096;          // 32 rows x 128 bytes, one box to an epilogue warp
-constexpr int SMEM = 1024 + STAGES * (A_STAGE + B_STAGE) + EPI_WARPS * STG_BOX + 256;
+constexpr int STG_BOX = 4096;          // 32 rows x 128 bytes: an epilogue warp's output
+// Boxes of a warp, 1 or 2, and stages.
+constexpr int stages_of(int boxes) { return 7 - boxes; }
+constexpr int smem_of(int boxes) { return 1024 + stages_of(boxes) * (A_STAGE + B_STAGE) + boxes * EPI_WARPS * STG_BOX + 256; }
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_M = 8;
-static_assert(SMEM <= 232448, "shared memory budget");
+static_assert(smem_of(1) <= 232448 && smem_of(2) <= 232448, "shared memory budget");
 
 struct Bars {
-    uint64_t full[STAGES];
-    uint64_t empty[STAGES];
+    uint64_t full[6];
+    uint64_t empty[6];
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
+    uint64_t joined;  // the other pair's sums are here
     uint64_t drain;
     uint64_t peer_done;
     long long peer_issued;
@@ -53,7 +60,8 @@ struct Args {
     int bn;
     int a_mn, b_mn;  // operands that lie MN-major
     int tiles;
-    int splits;      // K ranges of a tile
+    int splits;      // K ranges of a tile, each a unit of its own
+    int joined;      // pairs on a tile: 1, or 2 (bn 128, splits 1, a cluster to each tile)
     int *status;
 };
 
@@ -69,6 +77,15 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 __device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool a_mn, bool b_mn) {
     return (1u << 4) | (format << 7) | (format << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((n >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// On the barrier at this offset in both CTAs of the pair whose leader is CTA `lead`.
+__device__ __forceinline__ void commit_to_pair(uint64_t *bar, uint32_t lead) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)(3u << lead))
+        : "memory");
 }
 
 struct Tile {
@@ -96,14 +113,45 @@ inline long long lower_tiles(int n, int bn) {
     return q * (rows - 1) * rows / 2 + (n + bn - 1LL) / bn;
 }
 
-// What an epilogue warp sees of a unit.
+// Joined pairs: the sums that come in, 32 columns after 32, of those four columns of all
+// 128 rows after four -- a warp's stores, a row to a lane, are of 512 adjacent bytes
+// (stores of 16 bytes to rows apart cross the cluster one by one).  They lie in the boxes
+// of the warps that have no columns to write.
+constexpr int JOIN_QUAD = 128 * 16, JOIN_CHUNK = 8 * JOIN_QUAD, JOIN_AT = EPI_WARPS * STG_BOX;
+static_assert(JOIN_AT + 2 * JOIN_CHUNK <= 2 * EPI_WARPS * STG_BOX, "two boxes a warp");
+__device__ __forceinline__ void st_cluster_f4(uint32_t cluster_addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+// What an epilogue warp sees of a unit: 32 rows of D and columns [first, first + width) of
+// a tile, width a multiple of 32 (of 64 unless bn is 64).
 struct Part {
-    uint32_t tmem;    // this warp's rows, the tile's first column
-    int row0, col0;   // of D: the warp's first row, the tile's first column
-    int bn, half;     // which half of the columns: first (0) or last
-    int split;        // which K range
-    int lane;
-    uint8_t *box;     // STG_BOX bytes of this warp's
+    uint32_t tmem;          // this warp's rows, the tile's first column
+    int row0, col0;         // of D: the warp's first row, the tile's first column
+    int first, width;
+    int split;              // which K range
+    int bn, lane;
+    uint8_t *box;           // STG_BOX bytes of this warp's, once or twice
+    const uint8_t *joined;  // null, or this lane's row of the other pair's sums from column `first` on
+
+    // Columns c .. c + 31 of the tile, this lane's row.
+    template <bool JOIN>
+    __device__ __forceinline__ void load(int c, uint32_t (&r)[32]) const {
+        tmem_ld32(tmem + (uint32_t)c, r);
+        tmem_ld_wait();
+        if (JOIN && joined) {
+            const uint8_t *at = joined + ((c - first) >> 5) * JOIN_CHUNK;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float4 v = *reinterpret_cast<const float4 *>(at + j * JOIN_QUAD);
+                r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v.x);
+                r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v.y);
+                r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v.z);
+                r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v.w);
+            }
+        }
+    }
 };
 
 // 32 registers of this lane's row to a box of 128-byte rows, 128-byte swizzle.
@@ -113,7 +161,14 @@ __device__ __forceinline__ void box_put(uint8_t *box, int lane, const uint32_t (
         *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
             make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
 }
-// The box once the store that last read it has done so.
+// Half h of them: sixteen registers.
+__device__ __forceinline__ void box_put_half(uint8_t *box, int lane, int h, const uint32_t (&r)[16]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4 *>(box + lane * 128 + (((h * 4 + c) ^ (lane & 7)) << 4)) =
+            make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+}
+// The boxes once the stores that last read them have done so.
 __device__ __forceinline__ void box_begin(int lane) {
     if (lane == 0) tma_stores_read_wait0();
     __syncwarp();
@@ -143,7 +198,9 @@ __device__ __forceinline__ void box_scatter(const uint8_t *box, int lane, uint16
     __syncwarp();
 }
 
-// Epi: static constexpr bool LOWER; run(Part), called by whole warps with row0 < M.
+// Epi: static constexpr bool LOWER, and JOIN (whether pairs may be joined); int BOXES, 2
+// with JOIN; a type Pre and prefetch(Part, Pre), for what a unit's writing reads from memory,
+// before its sums are waited for; run(Part, Pre); both called by whole warps with row0 < M.
 template <uint32_t FORMAT, typename Epi>
 __global__ void __launch_bounds__(THREADS, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -151,18 +208,21 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int STAGES = stages_of(Epi::BOXES);
+    static_assert(!Epi::JOIN || Epi::BOXES == 2, "room for the other pair's sums");
     uint8_t *a_tiles = smem;
     uint8_t *b_tiles = a_tiles + STAGES * A_STAGE;
     uint8_t *staging = b_tiles + STAGES * B_STAGE;
-    Bars *bars = reinterpret_cast<Bars *>(staging + EPI_WARPS * STG_BOX);
+    Bars *bars = reinterpret_cast<Bars *>(staging + Epi::BOXES * EPI_WARPS * STG_BOX);
     volatile int *abort_flag = &bars->abort;
 
     const int bn = args.bn;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
+    const uint32_t cta = cluster_ctarank(), rank = cta & 1, lead = cta & ~1u;
     const bool leader = rank == 0;
     const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
     const int units = args.tiles * args.splits;
+    const bool joined = Epi::JOIN && args.joined > 1;
     const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (bn >> 1) * 128);
 
     if (threadIdx.x == 0) {
@@ -174,6 +234,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             mbar_init(&bars->acc_full[b], 1);
             mbar_init(&bars->acc_empty[b], 2 * EPI_WARPS);
         }
+        mbar_init(&bars->joined, 4);
         mbar_init(&bars->drain, 1);
         mbar_init(&bars->peer_done, 1);
         bars->abort = 0;
@@ -189,11 +250,12 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     pdl_launch_dependents();
     pdl_wait();
 
-    // unit u: K range u / tiles of tile u % tiles (clusters share a range's operands)
+    // unit u: K range u / tiles of tile u % tiles (clusters share a range's operands); joined
+    // pairs: a half of K each
     auto range = [&](int u, int &kb0, int &kb1) {
-        const int j = u / args.tiles;
-        kb0 = (int)((long long)args.num_kb * j / args.splits);
-        kb1 = (int)((long long)args.num_kb * (j + 1) / args.splits);
+        const int j = u / args.tiles, at = joined ? (int)(cta >> 1) : j, n = joined ? 2 : args.splits;
+        kb0 = (int)((long long)args.num_kb * at / n);
+        kb1 = (int)((long long)args.num_kb * (at + 1) / n);
         return tile_at<Epi::LOWER>(u - j * args.tiles, args);
     };
 
@@ -210,7 +272,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const int row0 = t.m * 256 + (int)rank * 128, col0 = t.n * bn + (int)rank * (bn >> 1);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
-                const uint32_t full = map_to_rank(&bars->full[stage], 0);
+                const uint32_t full = map_to_rank(&bars->full[stage], lead);
                 uint8_t *a = a_tiles + stage * A_STAGE, *b = b_tiles + stage * B_STAGE;
                 if (issuer) {
                     if (leader) mbar_arrive_expect_tx(&bars->full[stage], stage_tx);
@@ -233,7 +295,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         if (!ok && issuer) {
             atomicOr(args.status, ST_PRODUCER);
-            raise_abort_pair(abort_flag, rank);
+            raise_abort_pair(abort_flag, cta);
         }
         // No load is left in flight into either CTA when the pair ends: the peer tells the
         // leader how many stages it loaded, and the leader waits until every stage that
@@ -241,8 +303,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         // counted as done, or never armed).
         if (!issuer) {
         } else if (!leader) {
-            st_cluster_s64(map_to_rank(&bars->peer_issued, 0), issued);
-            mbar_arrive_cluster(map_to_rank(&bars->peer_done, 0));  // release: the count is visible first
+            st_cluster_s64(map_to_rank(&bars->peer_issued, lead), issued);
+            mbar_arrive_cluster(map_to_rank(&bars->peer_done, lead));  // release: the count is visible first
         } else {
             long long ip = issued;
             if (mbar_wait(&bars->peer_done, 0, abort_flag, false))
@@ -290,59 +352,90 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ++ks)
                         mma(d, ad + ks * a_step, bd + ks * b_step, idesc, (uint32_t)(kb != kb0 || ks != 0));
-                    commit_pair_multicast(&bars->empty[stage]);
+                    commit_to_pair(&bars->empty[stage], lead);
                 }
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
             if (!ok) break;
-            if (issuer) commit_pair_multicast(&bars->acc_full[buf]);
+            if (issuer) commit_to_pair(&bars->acc_full[buf], lead);
         }
         if (issuer) {
             if (!ok) {
                 atomicOr(args.status, ST_MMA);
-                raise_abort_pair(abort_flag, rank);
+                raise_abort_pair(abort_flag, cta);
             }
             commit<2>(&bars->drain);
             if (!mbar_wait(&bars->drain, 0, abort_flag, false)) atomicOr(args.status, ST_DRAIN);
         }
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue (both CTAs)
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const bool gives = joined && half != (int)(cta >> 1);  // its columns are the other pair's
         Part p;
         p.bn = bn;
-        p.half = (warp - 2) >> 2;
         p.lane = lane;
-        p.box = staging + (warp - 2) * STG_BOX;
+        p.box = staging + (joined ? quarter : warp - 2) * Epi::BOXES * STG_BOX;
+        p.first = half * (bn >> 1);
+        p.width = bn >> 1;
+        p.joined = nullptr;
         int it = 0;
         bool ok = true;
         for (int u = cluster; u < units; u += nclusters, ++it) {
             const int buf = it & 1;
             p.split = u / args.tiles;
             const Tile t = tile_at<Epi::LOWER>(u - p.split * args.tiles, args);
+            p.row0 = t.m * 256 + (int)rank * 128 + quarter * 32;
+            p.col0 = t.n * bn;
+            p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
+            const bool some = p.row0 < args.M;
+            typename Epi::Pre pre;
+            if (some && !gives) epi.prefetch(p, pre);
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->acc_full[buf], (uint32_t)((it >> 1) & 1), abort_flag, true))) {
                 ok = false;
                 break;
             }
             fence_after();
             __syncwarp();
-            p.row0 = t.m * 256 + (int)rank * 128 + quarter * 32;
-            p.col0 = t.n * bn;
-            p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
-            if (p.row0 < args.M) epi.run(p);
+            if (joined) {
+                uint8_t *in = staging + JOIN_AT + (quarter * 32 + lane) * 16;
+                if (gives) {
+                    const uint32_t at = map_to_rank(in, cta ^ 2u);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(p.tmem + (uint32_t)(p.first + c * 32), r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            st_cluster_f4(at + c * JOIN_CHUNK + j * JOIN_QUAD,
+                                          make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                      __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->joined, cta ^ 2u));  // release: the sums are visible first
+                } else {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&bars->joined, 0, abort_flag, true))) {
+                        ok = false;
+                        break;
+                    }
+                    p.joined = in;
+                }
+            }
+            if (some && !gives) epi.run(p, pre);
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], 0));
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], lead));
         }
         if (lane == 0) tma_stores_wait0();
         if (!ok && lane == 0) {
             atomicOr(args.status, ST_EPILOGUE);
-            raise_abort_pair(abort_flag, rank);
+            raise_abort_pair(abort_flag, cta);
         }
     }
 
     __syncwarp();
     fence_before();
-    cluster_sync();  // no CTA leaves while its peer may still touch its memory
+    cluster_sync();  // no CTA leaves while another may still touch its memory
     if (warp == 1) {
         fence_after();
         tmem_dealloc<2>(tmem_base, TMEM_COLS);
@@ -352,20 +445,26 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 template <uint32_t FORMAT, typename Epi>
 int clusters_max(int dev) {
     static std::atomic<int> known[kMaxDevices];
-    return cluster_limit(known[dev], reinterpret_cast<const void *>(pair_kernel<FORMAT, Epi>), THREADS, SMEM, 2);
+    return cluster_limit(known[dev], reinterpret_cast<const void *>(pair_kernel<FORMAT, Epi>), THREADS, smem_of(Epi::BOXES), 2);
+}
+// The same of clusters of two joined pairs.
+template <uint32_t FORMAT, typename Epi>
+int joined_max(int dev) {
+    static std::atomic<int> known[kMaxDevices];
+    return cluster_limit(known[dev], reinterpret_cast<const void *>(pair_kernel<FORMAT, Epi>), THREADS, smem_of(Epi::BOXES), 4);
 }
 
 template <uint32_t FORMAT, typename Epi>
 cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Epi &epi, const Args &args, int cmax, cudaStream_t s) {
     const long long units = (long long)args.tiles * args.splits;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (units < cmax ? units : cmax)), 1, 1);
+    cfg.gridDim = dim3((unsigned)(args.joined > 1 ? 4 * units : 2 * (units < cmax ? units : cmax)), 1, 1);
     cfg.blockDim = dim3(THREADS, 1, 1);
-    cfg.dynamicSmemBytes = SMEM;
+    cfg.dynamicSmemBytes = smem_of(Epi::BOXES);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = (unsigned)(2 * args.joined);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     pdl_attr(attr[1]);
