@@ -139,19 +139,23 @@ struct SymEpi {
     }
 };
 
-// X' = s (a (hi + lo) + sums): hi and lo, or the result in its own type.
-struct MulEpi {
-    static constexpr bool LOWER = false, JOIN = true;
-    static constexpr int BOXES = 2;
+// X' = s (a (hi + lo) + sums): hi and lo, or (LAST) the result in its own type.  LO: X has a
+// lo, and s is 1 (the first step's X has none).
+struct MulArgs {
     CUtensorMap tm, tmLo;         // hi or the result; lo
-    const uint16_t *hi, *lo;      // X (lo null: 0)
+    const uint16_t *hi, *lo;      // X
     long long ld;
-    const float *scale;           // s; null: 1
+    const float *scale;           // s
     float a;
     int M, N;
-    int kind;                     // 0: hi and lo, 1: half, 2: bf16
+    bool bf16;                    // the result's type, or half
     uint16_t *out;                // not null: the result by the element
     long long ldo;
+};
+template <bool LO, bool LAST>
+struct MulEpi : MulArgs {
+    static constexpr bool LOWER = false, JOIN = true;
+    static constexpr int BOXES = 2;
 
     struct Pre {
         Block hi, lo;
@@ -160,15 +164,19 @@ struct MulEpi {
         if (p.col0 + c >= N) return;
         const long long at = p.row0 * ld + p.col0 + c;
         pre.hi.fetch(hi + at, ld, p.lane, M - p.row0);
-        if (lo) pre.lo.fetch(lo + at, ld, p.lane, M - p.row0);
+        if (LO) pre.lo.fetch(lo + at, ld, p.lane, M - p.row0);
     }
     __device__ __forceinline__ void prefetch(const Part &p, Pre &pre) const {
         pre.hi.clear();
-        pre.lo.clear();
+        if (LO) pre.lo.clear();
         fetch(p, p.first, pre);
     }
+    // Two lanes of FP32 at a time: the conversions and these, ten instructions for two
+    // elements, bound a tile's writing.
     __device__ __forceinline__ void run(const Part &p, Pre &pre) const {
-        const float s = scale ? *scale : 1.0f;
+        const float s = LO ? 1.0f : *scale, sa = s * a;
+        const float2 s2 = make_float2(s, s), a2 = make_float2(sa, sa), lo2 = make_float2(sa / kLo, sa / kLo),
+                     up2 = make_float2(kLo, kLo), down2 = make_float2(-kLo, -kLo), zero2 = make_float2(0.0f, 0.0f);
 #pragma unroll 1
         for (int g = p.first; g < p.first + p.width; g += 64) {
             const int c0 = p.col0 + g;
@@ -176,34 +184,39 @@ struct MulEpi {
             uint8_t *box_lo = p.box + STG_BOX;
             box_begin(p.lane);
             pre.hi.to_box(p.box, p.lane);
-            if (lo) pre.lo.to_box(box_lo, p.lane);
+            if (LO) pre.lo.to_box(box_lo, p.lane);
             __syncwarp();
             if (g + 64 < p.first + p.width) fetch(p, g + 64, pre);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t r[32], z[16], w[16], e[16] = {};
+                uint32_t r[32], z[16], w[16], e[16];
                 p.load<true>(g + h * 32, r);
                 row_half(p.box, p.lane, h, w);
-                if (lo) row_half(box_lo, p.lane, h, e);
+                if (LO) row_half(box_lo, p.lane, h, e);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float2 u = half2_at(w[j]), l = half2_at(e[j]);
-                    const float x = s * fmaf(a, fmaf(l.x, 1.0f / kLo, u.x), __uint_as_float(r[2 * j]));
-                    const float y = s * fmaf(a, fmaf(l.y, 1.0f / kLo, u.y), __uint_as_float(r[2 * j + 1]));
-                    z[j] = kind == 2 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
-                    const float2 v = half2_at(z[j]);
-                    e[j] = pack2((x - v.x) * kLo, (y - v.y) * kLo, (__half *)nullptr);
+                    float2 x = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    if (LO) x = __ffma2_rn(half2_at(e[j]), lo2, x);
+                    else x = __ffma2_rn(x, s2, zero2);
+                    x = __ffma2_rn(half2_at(w[j]), a2, x);
+                    if (LAST) {
+                        z[j] = bf16 ? pack2(x.x, x.y, (__nv_bfloat16 *)nullptr) : pack2(x.x, x.y, (__half *)nullptr);
+                    } else {
+                        z[j] = pack2(x.x, x.y, (__half *)nullptr);
+                        x = __ffma2_rn(half2_at(z[j]), down2, __ffma2_rn(x, up2, zero2));
+                        e[j] = pack2(x.x, x.y, (__half *)nullptr);
+                    }
                 }
                 // (each lane its own row, which it alone has read)
                 box_put_half(p.box, p.lane, h, z);
-                if (kind == 0) box_put_half(box_lo, p.lane, h, e);
+                if (!LAST) box_put_half(box_lo, p.lane, h, e);
             }
-            if (out) {
+            if (LAST && out) {
                 box_scatter(p.box, p.lane, out, ldo, p.row0, c0, M, N);
                 continue;
             }
             box_store(&tm, p.box, p.lane, c0, p.row0, 0);
-            if (kind == 0) box_store(&tmLo, box_lo, p.lane, c0, p.row0, 0);
+            if (!LAST) box_store(&tmLo, box_lo, p.lane, c0, p.row0, 0);
         }
     }
 };
@@ -321,6 +334,22 @@ struct Plan {
     int bn, joined, clusters;
     long long tiles;
 };
+// Clusters of every kernel of X's product (all of one size and shared memory).
+template <bool LO, bool LAST>
+int mul_clusters_of(int dev, int joined) {
+    return joined == 1 ? clusters_max<0, MulEpi<LO, LAST>>(dev) : joined_max<0, MulEpi<LO, LAST>>(dev);
+}
+int mul_clusters(int dev, int joined) {
+    return std::min({mul_clusters_of<false, false>(dev, joined), mul_clusters_of<true, false>(dev, joined),
+                     mul_clusters_of<false, true>(dev, joined), mul_clusters_of<true, true>(dev, joined)});
+}
+template <bool LO, bool LAST>
+cudaError_t launch_mul(const CUtensorMap &ta, const CUtensorMap &tb, const MulArgs &m, const Args &args, int clusters,
+                       cudaStream_t s) {
+    MulEpi<LO, LAST> e;
+    static_cast<MulArgs &>(e) = m;
+    return launch<0>(ta, tb, e, args, clusters, s);
+}
 Plan plan(bool lower, int rows, int cols, int k, int dev) {
     const long long kb = ceil_div(k, BK);
     Plan best = {};
@@ -329,8 +358,9 @@ Plan plan(bool lower, int rows, int cols, int k, int dev) {
         const long long tiles = lower ? lower_tiles(rows, bn) : ceil_div(rows, 256) * ceil_div(cols, bn);
         if (tiles > 0x7FFFFFFFLL) continue;
         for (int joined = 1; joined <= (bn == 128 ? 2 : 1); ++joined) {
-            const int c = joined == 1 ? (lower ? clusters_max<0, SymEpi>(dev) : clusters_max<0, MulEpi>(dev))
-                                      : (lower ? joined_max<0, SymEpi>(dev) : joined_max<0, MulEpi>(dev));
+            const int c = !lower        ? mul_clusters(dev, joined)
+                          : joined == 1 ? clusters_max<0, SymEpi>(dev)
+                                        : joined_max<0, SymEpi>(dev);
             if (c <= 0 || joined > kb) continue;
             const long long block = bn == 256 ? 30 : 20, write = bn == 256 ? 250 : joined == 1 ? 150 : 250;
             const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * block + write;
@@ -344,7 +374,7 @@ Plan plan(bool lower, int rows, int cols, int k, int dev) {
 }
 
 cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStream_t s) {
-    if (clusters_max<0, SymEpi>(dev) <= 0 || clusters_max<0, MulEpi>(dev) <= 0) return cudaErrorNotSupported;
+    if (clusters_max<0, SymEpi>(dev) <= 0 || mul_clusters(dev, 1) <= 0) return cudaErrorNotSupported;
     const bool tall = p.M > p.N, bf16 = p.elt == Elt::BF16;
     const int m = std::min(p.M, p.N), n = std::max(p.M, p.N);
     const long long ldx = up64(p.N), lda = up64(m);
@@ -384,7 +414,7 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
     const Plan pa = plan(true, m, m, n, dev), pb = plan(true, m, m, m, dev), px = plan(false, p.M, p.N, m, dev);
     if (e == cudaSuccess && (!pa.bn || !pb.bn || !px.bn)) e = cudaErrorInvalidValue;
     SymEpi sy;
-    MulEpi mu;
+    MulArgs mu;
     CUtensorMap aL, aR, aM, outA, outAT, outB, outBT, hiM[2], loM[2], sym[2][2], mul[2];
     // operands: A's rows as the left one, and as the right one of B's product and of X's
     bool ok = map16(&outA, A, 0, m, m, lda, 32, 64) && map16(&outB, B, 0, m, m, lda, 32, 64) &&
@@ -429,18 +459,20 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
         mu.tm = last ? res : hiM[out];
         mu.tmLo = loM[out];
         mu.hi = hi[in];
-        mu.lo = i == 0 ? nullptr : lo[in];
+        mu.lo = lo[in];
         mu.ld = ldx;
-        mu.scale = i == 0 ? scale : nullptr;
+        mu.scale = scale;
         mu.a = p.a;
         mu.M = p.M;
         mu.N = p.N;
-        mu.kind = last ? (bf16 ? 2 : 1) : 0;
+        mu.bf16 = bf16;
         mu.out = last && !tma_out ? static_cast<uint16_t *>(p.O) : nullptr;
         mu.ldo = p.ldo;
         // B X: B's rows and X, [m, N], N-major; X B: X's rows and B's
-        e = tall ? launch<0>(mul[in], aM, mu, args(p.M, p.N, m, px, false, false), px.clusters, s)
-                 : launch<0>(aM, mul[in], mu, args(p.M, p.N, m, px, false, true), px.clusters, s);
+        const auto f = i == 0 ? (last ? launch_mul<false, true> : launch_mul<false, false>)
+                              : (last ? launch_mul<true, true> : launch_mul<true, false>);
+        e = tall ? f(mul[in], aM, mu, args(p.M, p.N, m, px, false, false), px.clusters, s)
+                 : f(aM, mul[in], mu, args(p.M, p.N, m, px, false, true), px.clusters, s);
     }
     const cudaError_t f = cudaFreeAsync(ws, s);
     return e != cudaSuccess ? e : f;

@@ -247,15 +247,17 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     cluster_sync();  // barriers of both CTAs initialised before any cross-CTA use
     fence_after();
     const uint32_t tmem_base = bars->tmem_base;
+    // The previous grid is waited for by the warps that touch global memory, once they know
+    // their first unit: a few hundred cycles of index arithmetic, and the code itself, are
+    // fetched while that grid drains.
     pdl_launch_dependents();
-    pdl_wait();
 
     // unit u: K range u / tiles of tile u % tiles (clusters share a range's operands); joined
     // pairs: a half of K each
     auto range = [&](int u, int &kb0, int &kb1) {
         const int j = u / args.tiles, at = joined ? (int)(cta >> 1) : j, n = joined ? 2 : args.splits;
-        kb0 = (int)((long long)args.num_kb * at / n);
-        kb1 = (int)((long long)args.num_kb * (at + 1) / n);
+        kb0 = args.num_kb * at / n;  // (num_kb < 2^26, n <= 16)
+        kb1 = args.num_kb * (at + 1) / n;
         return tile_at<Epi::LOWER>(u - j * args.tiles, args);
     };
 
@@ -266,9 +268,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         uint32_t phase = 0;
         long long issued = 0;
         bool ok = true;
-        for (int u = cluster; ok && u < units; u += nclusters) {
-            int kb0, kb1;
-            const Tile t = range(u, kb0, kb1);
+        int kb0, kb1;
+        Tile t = range(cluster, kb0, kb1);
+        pdl_wait();
+        for (int u = cluster; ok && u < units;) {
             const int row0 = t.m * 256 + (int)rank * 128, col0 = t.n * bn + (int)rank * (bn >> 1);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
@@ -292,6 +295,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 ++issued;
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
             }
+            u += nclusters;
+            if (u < units) t = range(u, kb0, kb1);
         }
         if (!ok && issuer) {
             atomicOr(args.status, ST_PRODUCER);
@@ -380,10 +385,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         p.joined = nullptr;
         int it = 0;
         bool ok = true;
-        for (int u = cluster; u < units; u += nclusters, ++it) {
+        p.split = cluster / args.tiles;
+        Tile t = tile_at<Epi::LOWER>(cluster - p.split * args.tiles, args);
+        pdl_wait();
+        for (int u = cluster; u < units; ++it) {
             const int buf = it & 1;
-            p.split = u / args.tiles;
-            const Tile t = tile_at<Epi::LOWER>(u - p.split * args.tiles, args);
             p.row0 = t.m * 256 + (int)rank * 128 + quarter * 32;
             p.col0 = t.n * bn;
             p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
@@ -425,6 +431,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], lead));
+            u += nclusters;
+            if (u < units) {
+                p.split = u / args.tiles;
+                t = tile_at<Epi::LOWER>(u - p.split * args.tiles, args);
+            }
         }
         if (lane == 0) tma_stores_wait0();
         if (!ok && lane == 0) {
