@@ -677,7 +677,7 @@ gemm_status_t run_rms_norm_backward(int dtype, const void *H, const void *w, con
     if (st != GEMM_OK) return st;
     if (M == 0) return finish(zero(ow, t_stream, cudaSuccess), "zero_fill");
     const NormBackward p{H, w, rstd, dY, dH, dX, dw, M, K, elt16(dtype)};
-    return finish(launch_rms_norm_backward(p, dev->num_sms, t_stream), "rms_norm_backward");
+    return finish(launch_rms_norm_backward(p, dev->num_sms, dev->status, t_stream), "rms_norm_backward");
 }
 
 // ------------------------------------------------------------ cross entropy of a linear head

@@ -31,6 +31,6 @@ struct NormBackward {
     Elt elt;
 };
 cudaError_t launch_rms_norm(const NormProblem &p, cudaStream_t s);
-cudaError_t launch_rms_norm_backward(const NormBackward &p, int num_sms, cudaStream_t s);
+cudaError_t launch_rms_norm_backward(const NormBackward &p, int num_sms, int *status, cudaStream_t s);
 
 }  // namespace gemm_gb300

@@ -8,10 +8,12 @@
 // a lane.  The E4M3 form needs one reduction too: |Y| = |w H| rstd rises with |w H|,
 // so the largest |w H| is found with the sum of squares.
 //
-// Pieces lie on 16 bytes of memory.  Where K is no multiple of 8 a row starts inside a
-// piece, `off` elements behind its start; whole pieces are still loaded and stored as
-// such (every operand's row lies alike, if the bases do), the row's two ends by the
-// element.  An operand whose base lies otherwise is read and written by the element.
+// Pieces lie on 16 bytes of memory.  Where K is no multiple of 8, a row is whole pieces
+// between a head and a tail of up to seven elements, which one thread each takes; every
+// operand's row lies alike, if the bases do.  (Pieces that reach over the row's ends,
+// masked there, took 8192 x 4095 from 42 to 123 us: masks and elements cost more
+// instructions than the row.)  Rows longer than 16384, and operands whose bases lie
+// otherwise to 16 bytes, are read twice, piece by piece, by the element where need be.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -22,6 +24,7 @@
 #include <type_traits>
 
 #include "norm.h"
+#include "tc_ptx.cuh"
 
 namespace gemm_gb300 {
 namespace {
@@ -61,32 +64,60 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Elements k .. k + 7 of a row of K, 0 outside it.  ODD: some may lie outside, or the
-// row is not `wide` (its pieces off 16 bytes); else all lie inside or none.
-template <bool ODD>
-__device__ __forceinline__ uint4 load8(const uint16_t *row, long long k, int K, bool wide) {
-    if (!ODD) return k < K ? *reinterpret_cast<const uint4 *>(row + k) : make_uint4(0u, 0u, 0u, 0u);
-    if (wide && k >= 0 && k + 8 <= K) return *reinterpret_cast<const uint4 *>(row + k);
+// Bytes of an address behind 16.
+__device__ __forceinline__ int behind16(const void *p) { return (int)((uintptr_t)p & 15); }
+
+// Elements k .. k + 7 of a row of K by the element, 0 outside it; the same stored, in 16 or
+// 8 bits.  For rows' ends and what lies off 16 bytes; not inlined, so that the code of the
+// whole pieces around them stays small (8192 x 4095 with these inlined: 2500 instructions a
+// warp, 123 us).
+__device__ __noinline__ uint4 elements8(const uint16_t *row, long long k, int K) {
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (k + j >= 0 && k + j < K) w[j >> 1] |= (uint32_t)row[k + j] << (16 * (j & 1));
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <bool ODD>
-__device__ __forceinline__ void store8(uint16_t *row, long long k, int K, bool wide, const uint4 &v) {
-    if (!ODD) {
-        if (k < K) *reinterpret_cast<uint4 *>(row + k) = v;
-        return;
-    }
-    if (wide && k >= 0 && k + 8 <= K) {
-        *reinterpret_cast<uint4 *>(row + k) = v;
-        return;
-    }
+__device__ __noinline__ void put8(uint16_t *row, long long k, int K, uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         if (k + j >= 0 && k + j < K) row[k + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+}
+__device__ __noinline__ void put8_codes(uint8_t *row, long long k, int K, uint2 v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (k + j >= 0 && k + j < K) row[k + j] = (uint8_t)((j < 4 ? v.x : v.y) >> (8 * (j & 3)));
+}
+// Bytes d .. d + 15 of two pieces, d even and below 16.
+__device__ __forceinline__ uint4 shift16(const uint4 &a, const uint4 &b, int d) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t t[5];
+#pragma unroll
+    for (int j = 0; j < 5; ++j)  // d / 4 whole words: 0, 1, 2 or 3
+        t[j] = d < 8 ? (d < 4 ? w[j] : w[j + 1]) : (d < 12 ? w[j + 2] : w[j + 3]);
+    const uint32_t sh = (d & 2) * 8;
+    return make_uint4(__funnelshift_r(t[0], t[1], sh), __funnelshift_r(t[1], t[2], sh), __funnelshift_r(t[2], t[3], sh),
+                      __funnelshift_r(t[3], t[4], sh));
+}
+__device__ __forceinline__ uint4 ld16(const uint16_t *p) { return *reinterpret_cast<const uint4 *>(p); }
+constexpr uint4 kZero = {0u, 0u, 0u, 0u};
+
+// One piece of a row, anywhere.
+__device__ __forceinline__ uint4 load8(const uint16_t *row, long long k, int K) {
+    const int d = behind16(row + k), e = d >> 1;
+    if (d == 0 && k >= 0 && k + 8 <= K) return ld16(row + k);
+    if (d != 0 && k >= e && k - e + 16 <= K) return shift16(ld16(row + k - e), ld16(row + k - e + 8), d);
+    return elements8(row, k, K);
+}
+// The same stored; wide: the row's pieces lie on 16 bytes (codes: 8).
+__device__ __forceinline__ void store8(uint16_t *row, long long k, int K, bool wide, const uint4 &v) {
+    if (wide && k >= 0 && k + 8 <= K) *reinterpret_cast<uint4 *>(row + k) = v;
+    else put8(row, k, K, v);
+}
+__device__ __forceinline__ void store8_codes(uint8_t *row, long long k, int K, bool wide, const uint2 &v) {
+    if (wide && k >= 0 && k + 8 <= K) *reinterpret_cast<uint2 *>(row + k) = v;
+    else put8_codes(row, k, K, v);
 }
 // Eight E4M3 codes of v scale, clamped at +-448; a NaN gives the NaN code.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
@@ -95,20 +126,6 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
     for (int j = 0; j < 4; ++j)
         c[j] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2 * j] * inv, v[2 * j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
     return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-template <bool ODD>
-__device__ __forceinline__ void store8_codes(uint8_t *row, long long k, int K, bool wide, const uint2 &v) {
-    if (!ODD) {
-        if (k < K) *reinterpret_cast<uint2 *>(row + k) = v;
-        return;
-    }
-    if (wide && k >= 0 && k + 8 <= K) {
-        *reinterpret_cast<uint2 *>(row + k) = v;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (k + j >= 0 && k + j < K) row[k + j] = (uint8_t)((j < 4 ? v.x : v.y) >> (8 * (j & 3)));
 }
 __host__ __device__ __forceinline__ bool on(const void *p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
 
@@ -147,11 +164,11 @@ __device__ __forceinline__ uint4 add8(const uint4 &a, const uint4 &b) {
     for (int j = 0; j < 8; ++j) x[j] += y[j];
     return pack8<T>(x);
 }
-// The gains of elements k .. k + 7 (w null: ones).
-template <typename T, bool ODD>
-__device__ __forceinline__ void weight8(const uint16_t *w, long long k, int K, bool wide, float (&f)[8]) {
-    if (w) {
-        unpack8<T>(load8<ODD>(w, k, K, wide), f);
+// Eight gains (none: ones).
+template <typename T>
+__device__ __forceinline__ void gains8(bool some, const uint4 &w, float (&f)[8]) {
+    if (some) {
+        unpack8<T>(w, f);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = 1.0f;
@@ -178,48 +195,107 @@ __device__ __forceinline__ float rstd_of(float sum, int K, float eps, float by) 
     return 1.0f / sqrtf(sum / (float)K + eps * by * by);
 }
 
-// Rows held in registers, WPR warps to a row, four warps at least to a CTA.
+// How a thread of a row's warps takes the row: pieces k0 + i STEP below `body` from element
+// `head` on, and, where they are not whole pieces, one element `one` of the head or the tail.
+struct Share {
+    int head, body, k0, one;  // one: -1 for none
+};
+template <int WPR, bool ODD>
+__device__ __forceinline__ Share share_of(const uint16_t *row, int K) {
+    Share s;
+    const int t = (int)(threadIdx.x & (WPR * 32 - 1));
+    s.k0 = t * 8;
+    if (!ODD) {
+        s.head = 0;
+        s.body = K;
+        s.one = -1;
+        return s;
+    }
+    s.head = min((8 - (behind16(row) >> 1)) & 7, K);
+    s.body = (K - s.head) & ~7;
+    s.one = t < s.head ? t : t < K - s.body ? s.body + t : -1;
+    return s;
+}
+// The gains in shared memory (ODD: pieces start at any element of theirs), w null: ones.
+__device__ __forceinline__ int gains_bytes(int K) { return ((K + 15) & ~7) * 2; }
+template <typename T>
+__device__ __forceinline__ void stage_gains(const uint16_t *w, int K, uint16_t *to) {
+    const bool wide = w && behind16(w) == 0;
+    const int whole = wide ? K >> 3 : 0;
+    for (int i = threadIdx.x; i < whole; i += blockDim.x) reinterpret_cast<uint4 *>(to)[i] = ld16(w + 8 * i);
+    const T unit = T(1.0f);
+    for (int k = whole * 8 + threadIdx.x; k < ((K + 15) & ~7); k += blockDim.x)
+        to[k] = k >= K ? (uint16_t)0 : w ? w[k] : *reinterpret_cast<const uint16_t *>(&unit);
+}
+// Gains of the piece k of a row with this head.
+__device__ __forceinline__ uint4 staged8(const uint16_t *w, int head, int k) {
+    return shift16(ld16(w + k), ld16(w + k + 8), head * 2);
+}
+template <typename T>
+__device__ __forceinline__ float value(const uint16_t *p) { return (float)*reinterpret_cast<const T *>(p); }
+template <typename T>
+__device__ __forceinline__ uint16_t bits(float f) {
+    const T t = T(f);
+    return *reinterpret_cast<const uint16_t *>(&t);
+}
+
+// Rows held in registers, WPR warps to a row, four warps at least to a CTA.  ODD: K is no
+// multiple of 8, or the bases lie off 16 bytes, all alike.
+__host__ __device__ constexpr int fwd_ctas(int wpr) { return wpr == 16 ? 2 : wpr == 8 ? 4 : 7; }
 template <typename T, int WPR, bool ODD, bool E4M3>
-__global__ void __launch_bounds__(row_warps(WPR) * 32)
+__global__ void __launch_bounds__(row_warps(WPR) * 32, fwd_ctas(WPR))
 rms_norm_kernel(const FwdArgs a)
 {
+    extern __shared__ __align__(16) uint16_t gains_s[];  // ODD
     __shared__ float2 red[2][row_warps(WPR)];
     pdl_wait();  // dependents launch as this grid's CTAs exit (several CTAs per SM: no early trigger)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, K = a.K;
-    constexpr int ROWS = row_warps(WPR) / WPR;
+    constexpr int ROWS = row_warps(WPR) / WPR, STEP = WPR * 256;
     const long long row = (long long)blockIdx.x * ROWS + warp / WPR;
     const bool valid = row < a.M, first = valid && lane == 0 && warp % WPR == 0;
-    if (WPR == 1 && !valid) return;
+    if (WPR == 1 && !ODD && !valid) return;
     const long long at = valid ? row * K : 0;
-    const int n = valid ? K : 0;
-    const int off = ODD ? (int)(((uintptr_t)(a.X + at) & 15) >> 1) : 0;
-    const long long k0 = (long long)(warp % WPR * 32 + lane) * 8 - off;
-    constexpr long long STEP = WPR * 256;
+    const Share me = share_of<WPR, ODD>(a.X + at, valid ? K : 0);
 
     uint4 h[NV];
-    const bool wx = on(a.X + at - off, 16), wr = on(a.R + at - off, 16), ww = on(a.w - off, 16);
+    const long long body = at + me.head;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) h[i] = load8<ODD>(a.X + at, k0 + i * STEP, n, wx);
+    for (int i = 0; i < NV; ++i) h[i] = me.k0 + i * STEP < me.body ? ld16(a.X + body + me.k0 + i * STEP) : kZero;
+    float one = ODD && me.one >= 0 ? value<T>(a.X + at + me.one) : 0.0f;
     if (a.R) {
         uint4 r[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) r[i] = load8<ODD>(a.R + at, k0 + i * STEP, n, wr);
+        for (int i = 0; i < NV; ++i) r[i] = me.k0 + i * STEP < me.body ? ld16(a.R + body + me.k0 + i * STEP) : kZero;
+        if (ODD && me.one >= 0) one = (float)T(one + value<T>(a.R + at + me.one));
+        if (ODD) stage_gains<T>(a.w, K, gains_s);
 #pragma unroll
         for (int i = 0; i < NV; ++i) h[i] = add8<T>(h[i], r[i]);
         if (a.H) {
-            const bool wh = on(a.H + at - off, 16);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) store8<ODD>(a.H + at, k0 + i * STEP, n, wh, h[i]);
+            for (int i = 0; i < NV; ++i)
+                if (me.k0 + i * STEP < me.body) *reinterpret_cast<uint4 *>(a.H + body + me.k0 + i * STEP) = h[i];
+            if (ODD && me.one >= 0) a.H[at + me.one] = bits<T>(one);
         }
+    } else if (ODD) {
+        stage_gains<T>(a.w, K, gains_s);
     }
+    if (ODD) __syncthreads();
+    // the gains of piece i: from shared memory, or from L1
+    auto gains = [&](int i, float(&g)[8]) {
+        const int k = me.k0 + i * STEP;
+        if (ODD) unpack8<T>(k < me.body ? staged8(gains_s, me.head, k) : kZero, g);
+        else gains8<T>(a.w != nullptr, a.w && k < me.body ? ld16(a.w + k) : kZero, g);
+    };
+    const float one_gain = ODD && me.one >= 0 ? value<T>(gains_s + me.one) : 0.0f;
     float by = 1.0f, sum, top;
     auto sums = [&] {
-        sum = top = 0.0f;
+        sum = ODD ? (one * by) * (one * by) : 0.0f;
+        top = ODD && E4M3 ? fabsf(one * by * one_gain) : 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float f[8], g[8];
             unpack8<T>(h[i], f);
-            if (E4M3) weight8<T, ODD>(a.w, k0 + i * STEP, n, ww, g);
+            if (E4M3) gains(i, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float v = f[j] * by;
@@ -246,20 +322,25 @@ rms_norm_kernel(const FwdArgs a)
         inv = amax == 0.0f ? 0.0f : 448.0f / amax;
         if (first) a.scale[row] = amax / 448.0f;
     }
-    const bool wy = E4M3 ? on(a.Q + at - off, 8) : on(a.Y + at - off, 16);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+        if (me.k0 + i * STEP >= me.body) break;
         float f[8], g[8];
         unpack8<T>(h[i], f);
-        weight8<T, ODD>(a.w, k0 + i * STEP, n, ww, g);
+        gains(i, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = f[j] * by * r * g[j];
-        if (E4M3) store8_codes<ODD>(a.Q + at, k0 + i * STEP, n, wy, codes8(f, inv));
-        else store8<ODD>(a.Y + at, k0 + i * STEP, n, wy, pack8<T>(f));
+        if (E4M3) *reinterpret_cast<uint2 *>(a.Q + body + me.k0 + i * STEP) = codes8(f, inv);
+        else *reinterpret_cast<uint4 *>(a.Y + body + me.k0 + i * STEP) = pack8<T>(f);
+    }
+    if (ODD && me.one >= 0) {
+        const float y = one * by * r * one_gain;
+        if (E4M3) a.Q[at + me.one] = (uint8_t)__nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3);
+        else a.Y[at + me.one] = bits<T>(y);
     }
 }
 
-// Longer rows: a CTA to a row, which is read twice (three times where its squares
+// Any rows: a CTA to a row, which is read twice (three times where its squares
 // overflow), the second time mostly from L2.
 template <typename T, bool E4M3>
 __global__ void __launch_bounds__(MAX_WPR * 32)
@@ -270,21 +351,22 @@ rms_norm_long_kernel(const FwdArgs a)
     const long long row = blockIdx.x;
     const int K = a.K;
     const long long at = row * K;
-    const int off = (int)(((uintptr_t)(a.X + at) & 15) >> 1);
+    const int off = behind16(a.X + at) >> 1;
     const long long k0 = (long long)threadIdx.x * 8 - off;
     constexpr long long STEP = MAX_WPR * 256;
-    const bool wx = on(a.X + at - off, 16), wr = on(a.R + at - off, 16), ww = on(a.w - off, 16), wh = on(a.H + at - off, 16);
+    const bool wh = on(a.H + at - off, 16);
     auto value = [&](long long k) {
-        const uint4 x = load8<true>(a.X + at, k, K, wx);
-        return a.R ? add8<T>(x, load8<true>(a.R + at, k, K, wr)) : x;
+        const uint4 x = load8(a.X + at, k, K);
+        return a.R ? add8<T>(x, load8(a.R + at, k, K)) : x;
     };
+    auto gain = [&](long long k, float(&g)[8]) { gains8<T>(a.w != nullptr, a.w ? load8(a.w, k, K) : kZero, g); };
     float by = 1.0f, sum, top;
     auto sums = [&] {
         sum = top = 0.0f;
         for (long long k = k0; k < K; k += STEP) {
             float f[8], g[8];
             unpack8<T>(value(k), f);
-            if (E4M3) weight8<T, true>(a.w, k, K, ww, g);
+            if (E4M3) gain(k, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float v = f[j] * by;
@@ -311,14 +393,14 @@ rms_norm_long_kernel(const FwdArgs a)
     const bool wy = E4M3 ? on(a.Q + at - off, 8) : on(a.Y + at - off, 16);
     for (long long k = k0; k < K; k += STEP) {
         const uint4 h = value(k);
-        if (a.H) store8<true>(a.H + at, k, K, wh, h);
+        if (a.H) store8(a.H + at, k, K, wh, h);
         float f[8], g[8];
         unpack8<T>(h, f);
-        weight8<T, true>(a.w, k, K, ww, g);
+        gain(k, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = f[j] * by * r * g[j];
-        if (E4M3) store8_codes<true>(a.Q + at, k, K, wy, codes8(f, inv));
-        else store8<true>(a.Y + at, k, K, wy, pack8<T>(f));
+        if (E4M3) store8_codes(a.Q + at, k, K, wy, codes8(f, inv));
+        else store8(a.Y + at, k, K, wy, pack8<T>(f));
     }
 }
 
@@ -331,112 +413,226 @@ struct BwdArgs {
     int M, K;
 };
 
-// CTAs walk over the rows; dw's sums stay with them, in registers (every row of a
-// thread has the same columns) or, ODD, in shared memory, element k of a group of
-// warps at (k % 8) WPR 128 + k / 8 (a warp's threads on different banks).
-template <typename T, int WPR, bool ODD>
-__global__ void __launch_bounds__(row_warps(WPR) * 32)
-rms_norm_backward_kernel(const BwdArgs a)
+// Rows on 16 bytes: CTAs walk over the rows, ROWS at a time, which come to shared memory
+// by bulk copies a few turns ahead (adjacent rows are adjacent in memory), so that enough
+// bytes are under way at all times; loads to registers, waited for row by row, reached
+// half of the rate (8192 x 4096: 72 us against 39).  dw's sums stay in registers: a thread
+// has the same columns of every row.
+constexpr int ctas_per_sm(int wpr) { return wpr <= 4 ? 3 : wpr == 8 ? 2 : 1; }
+template <typename T, int WPR>
+__global__ void __launch_bounds__(row_warps(WPR) * 32, ctas_per_sm(WPR))
+rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
 {
-    extern __shared__ float acc_s[];
-    constexpr int WARPS = row_warps(WPR), ROWS = WARPS / WPR, PLANE = WPR * 128;
+    constexpr int WARPS = row_warps(WPR), ROWS = WARPS / WPR, MAX_STAGES = 8;
+    extern __shared__ __align__(16) uint8_t ring[];  // stage: H, dY and dH, ROWS rows each
+    __shared__ uint64_t full[MAX_STAGES];
     __shared__ float2 red[2][WARPS];
+    __shared__ int abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, K = a.K, group = warp / WPR;
-    constexpr long long STEP = WPR * 256;
-    float *mine = acc_s + group * 8 * PLANE;
-    if (ODD && a.part) {
-        for (int i = threadIdx.x; i < ROWS * 8 * PLANE; i += WARPS * 32) acc_s[i] = 0.0f;
-        __syncthreads();
+    const uint32_t plane = (uint32_t)(ROWS * K * 2), stage_bytes = 3 * plane;
+    const bool has_dh = a.dH && a.dX;
+    const long long step = (long long)gridDim.x * ROWS, row00 = (long long)blockIdx.x * ROWS;
+    if (threadIdx.x == 0) {
+        abort = 0;
+        for (int i = 0; i < stages; ++i) tc::mbar_init(&full[i], 1);
+        tc::mbar_init_fence();
     }
+    __syncthreads();
     pdl_wait();
-    float acc[ODD ? 1 : NV][8] = {};
-    int flip = 0;
-    for (long long row0 = (long long)blockIdx.x * ROWS; row0 < a.M; row0 += (long long)gridDim.x * ROWS, flip ^= 1) {
+    auto fetch = [&](long long row0, int stage) {  // one thread
+        if (row0 >= a.M) return;
+        const uint32_t bytes = (uint32_t)min((long long)ROWS, a.M - row0) * (uint32_t)(K * 2);
+        uint8_t *to = ring + stage * stage_bytes;
+        tc::mbar_arrive_expect_tx(&full[stage], bytes * (has_dh ? 3u : 2u));
+        tc::bulk_load(to, a.H + row0 * K, bytes, &full[stage]);
+        tc::bulk_load(to + plane, a.dY + row0 * K, bytes, &full[stage]);
+        if (has_dh) tc::bulk_load(to + 2 * plane, a.dH + row0 * K, bytes, &full[stage]);
+    };
+    if (threadIdx.x == 0)
+        for (int i = 0; i < stages; ++i) fetch(row00 + i * step, i);
+    constexpr int STEP = WPR * 256;
+    const int k0 = (warp % WPR * 32 + lane) * 8;
+    constexpr bool KEEP = WPR <= 4;  // the gains, in registers; else from L1
+    uint4 w[NV];
+    auto gain = [&](int i) { return a.w && k0 + i * STEP < K ? ld16(a.w + k0 + i * STEP) : kZero; };
+    if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) w[i] = gain(i);
+    }
+    float acc[NV][8] = {};
+    int stage = 0, flip = 0;
+    uint32_t phase = 0;
+    for (long long row0 = row00; row0 < a.M; row0 += step, flip ^= 1) {
         const long long row = row0 + group;
         const bool valid = row < a.M;
-        const long long at = valid ? row * K : 0;
-        const int n = valid ? K : 0;
-        const int off = ODD ? (int)(((uintptr_t)(a.H + at) & 15) >> 1) : 0;
-        const long long k0 = (long long)(warp % WPR * 32 + lane) * 8 - off;
-        const bool wh = on(a.H + at - off, 16), wy = on(a.dY + at - off, 16), wd = on(a.dH + at - off, 16),
-                   wx = on(a.dX + at - off, 16), ww = on(a.w - off, 16);
+        const float r = valid ? a.rstd[row] : 0.0f;
+        if (!tc::mbar_wait(&full[stage], phase, &abort, true)) {  // (the results are then undefined)
+            abort = 1;
+            if (lane == 0) atomicOr(status, tc::ST_PRODUCER);
+        }
+        const uint8_t *at = ring + stage * stage_bytes + group * K * 2;
         uint4 h[NV], dy[NV], dh[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) h[i] = load8<ODD>(a.H + at, k0 + i * STEP, n, wh);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) dy[i] = load8<ODD>(a.dY + at, k0 + i * STEP, n, wy);
-        if (a.dH && a.dX) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) dh[i] = load8<ODD>(a.dH + at, k0 + i * STEP, n, wd);
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) dh[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < NV; ++i) {
+            const int k = k0 + i * STEP;
+            const bool in = valid && k < K;
+            h[i] = in ? *reinterpret_cast<const uint4 *>(at + k * 2) : kZero;
+            dy[i] = in ? *reinterpret_cast<const uint4 *>(at + plane + k * 2) : kZero;
+            dh[i] = in && has_dh ? *reinterpret_cast<const uint4 *>(at + 2 * plane + k * 2) : kZero;
         }
-        const float r = valid ? a.rstd[row] : 0.0f;
         float sum = 0.0f, top = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float f[8], d[8], g[8];
             unpack8<T>(h[i], f);
             unpack8<T>(dy[i], d);
-            weight8<T, ODD>(a.w, k0 + i * STEP, n, ww, g);
+            gains8<T>(a.w != nullptr, KEEP ? w[i] : gain(i), g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float xhat = f[j] * r, k = d[j] * xhat;
+                const float k = d[j] * (f[j] * r);
                 sum = fmaf(k, g[j], sum);
-                if constexpr (ODD) {
-                    const long long at_k = k0 + i * STEP + j;
-                    if (a.part && at_k >= 0 && at_k < n) mine[(int)(at_k & 7) * PLANE + (int)(at_k >> 3)] += k;
-                } else {
-                    acc[i][j] += k;
-                }
+                acc[i][j] += k;
             }
         }
+        if (WPR == 1) __syncthreads();
         reduce_row<WPR>(sum, top, red[flip]);
-        const float mean = sum / (float)K;
+        // every thread has its part of the stage
+        if (threadIdx.x == 0) fetch(row0 + stages * step, stage);
+        if (++stage == stages) { stage = 0; phase ^= 1u; }
         if (a.dX) {
+            const float mean = sum / (float)K;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float f[8], d[8], g[8], e[8];
                 unpack8<T>(h[i], f);
                 unpack8<T>(dy[i], d);
                 unpack8<T>(dh[i], e);
-                weight8<T, ODD>(a.w, k0 + i * STEP, n, ww, g);
+                gains8<T>(a.w != nullptr, KEEP ? w[i] : gain(i), g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d[j] = fmaf(r, fmaf(-f[j] * r, mean, d[j] * g[j]), e[j]);
-                store8<ODD>(a.dX + at, k0 + i * STEP, n, wx, pack8<T>(d));
+                if (valid && k0 + i * STEP < K) *reinterpret_cast<uint4 *>(a.dX + row * K + k0 + i * STEP) = pack8<T>(d);
             }
         }
     }
     if (!a.part) return;
     float *part = a.part + (long long)blockIdx.x * K;
-    if constexpr (!ODD && ROWS == 1) {
+    if constexpr (ROWS == 1) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const long long k = (long long)(warp * 32 + lane) * 8 + i * STEP;
+            const int k = k0 + i * STEP;
             if (k < K) {
                 *reinterpret_cast<float4 *>(part + k) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
                 *reinterpret_cast<float4 *>(part + k + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
             }
         }
     } else {
-        if constexpr (!ODD) {
+        // the groups' sums meet in the ring, [group][K], every copy into which has been read
+        __syncthreads();
+        float *sums = reinterpret_cast<float *>(ring);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) mine[j * PLANE + (warp % WPR * 32 + lane) + i * WPR * 32] = acc[i][j];
+        for (int i = 0; i < NV; ++i) {
+            const int k = k0 + i * STEP;
+            if (k < K) {
+                *reinterpret_cast<float4 *>(sums + group * K + k) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                *reinterpret_cast<float4 *>(sums + group * K + k + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+            }
         }
         __syncthreads();
         for (int k = threadIdx.x; k < K; k += WARPS * 32) {
             float s = 0.0f;
 #pragma unroll
-            for (int g = 0; g < ROWS; ++g) s += acc_s[g * 8 * PLANE + (k & 7) * PLANE + (k >> 3)];
+            for (int g = 0; g < ROWS; ++g) s += sums[g * K + k];
             part[k] = s;
         }
     }
 }
 
-// dX of longer rows, a CTA to a row.
+// Rows that are no whole pieces (as in rms_norm_kernel), through registers.  dw's sums lie
+// in shared memory behind the gains, element k of a group of warps at (k % 8) PLANE + k / 8
+// (a warp's threads on different banks): a thread's columns are others in every row.
+template <typename T, int WPR>
+__global__ void __launch_bounds__(row_warps(WPR) * 32)
+rms_norm_backward_odd_kernel(const BwdArgs a)
+{
+    extern __shared__ __align__(16) uint16_t gains_s[];
+    constexpr int WARPS = row_warps(WPR), ROWS = WARPS / WPR, PLANE = WPR * 128 + 1, STEP = WPR * 256;
+    __shared__ float2 red[2][WARPS];
+    const int warp = threadIdx.x >> 5, K = a.K, group = warp / WPR;
+    float *sums = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(gains_s) + gains_bytes(K));
+    float *mine = sums + group * 8 * PLANE;
+    if (a.part)
+        for (int i = threadIdx.x; i < ROWS * 8 * PLANE; i += WARPS * 32) sums[i] = 0.0f;
+    pdl_wait();
+    stage_gains<T>(a.w, K, gains_s);
+    __syncthreads();
+    int flip = 0;
+    for (long long row0 = (long long)blockIdx.x * ROWS; row0 < a.M; row0 += (long long)gridDim.x * ROWS, flip ^= 1) {
+        const long long row = row0 + group;
+        const bool valid = row < a.M;
+        const long long at = valid ? row * K : 0;
+        const Share me = share_of<WPR, true>(a.H + at, valid ? K : 0);
+        const long long body = at + me.head;
+        const bool has_dh = a.dH && a.dX, some = me.one >= 0;
+        uint4 h[NV], dy[NV], dh[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = me.k0 + i * STEP;
+            h[i] = k < me.body ? ld16(a.H + body + k) : kZero;
+            dy[i] = k < me.body ? ld16(a.dY + body + k) : kZero;
+            dh[i] = k < me.body && has_dh ? ld16(a.dH + body + k) : kZero;
+        }
+        const float h1 = some ? value<T>(a.H + at + me.one) : 0.0f, y1 = some ? value<T>(a.dY + at + me.one) : 0.0f,
+                    d1 = some && has_dh ? value<T>(a.dH + at + me.one) : 0.0f, g1 = some ? value<T>(gains_s + me.one) : 0.0f;
+        const float r = valid ? a.rstd[row] : 0.0f;
+        float sum = y1 * (h1 * r) * g1, top = 0.0f;
+        if (a.part && some) mine[(me.one & 7) * PLANE + (me.one >> 3)] += y1 * (h1 * r);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int k = me.k0 + i * STEP;
+            if (k >= me.body) break;
+            float f[8], d[8], g[8];
+            unpack8<T>(h[i], f);
+            unpack8<T>(dy[i], d);
+            unpack8<T>(staged8(gains_s, me.head, k), g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float t = d[j] * (f[j] * r);
+                sum = fmaf(t, g[j], sum);
+                if (a.part) mine[((me.head + j) & 7) * PLANE + ((me.head + k + j) >> 3)] += t;
+            }
+        }
+        reduce_row<WPR>(sum, top, red[flip]);
+        if (WPR == 1) __syncwarp();  // the group's sums: the next row's columns are other threads'
+        const float mean = sum / (float)K;
+        if (a.dX) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int k = me.k0 + i * STEP;
+                if (k >= me.body) break;
+                float f[8], d[8], g[8], e[8];
+                unpack8<T>(h[i], f);
+                unpack8<T>(dy[i], d);
+                unpack8<T>(dh[i], e);
+                unpack8<T>(staged8(gains_s, me.head, k), g);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] = fmaf(r, fmaf(-f[j] * r, mean, d[j] * g[j]), e[j]);
+                *reinterpret_cast<uint4 *>(a.dX + body + k) = pack8<T>(d);
+            }
+            if (some) a.dX[at + me.one] = bits<T>(fmaf(r, fmaf(-h1 * r, mean, y1 * g1), d1));
+        }
+    }
+    if (!a.part) return;
+    float *part = a.part + (long long)blockIdx.x * K;
+    __syncthreads();
+    for (int k = threadIdx.x; k < K; k += WARPS * 32) {
+        float s = 0.0f;
+#pragma unroll
+        for (int g = 0; g < ROWS; ++g) s += sums[g * 8 * PLANE + (k & 7) * PLANE + (k >> 3)];
+        part[k] = s;
+    }
+}
+
+// dX of any rows, a CTA to a row.
 template <typename T>
 __global__ void __launch_bounds__(MAX_WPR * 32)
 rms_norm_long_dx_kernel(const BwdArgs a)
@@ -446,18 +642,18 @@ rms_norm_long_dx_kernel(const BwdArgs a)
     const long long row = blockIdx.x;
     const int K = a.K;
     const long long at = row * K;
-    const int off = (int)(((uintptr_t)(a.H + at) & 15) >> 1);
+    const int off = behind16(a.H + at) >> 1;
     constexpr long long STEP = MAX_WPR * 256;
     const long long k0 = (long long)threadIdx.x * 8 - off;
-    const bool wh = on(a.H + at - off, 16), wy = on(a.dY + at - off, 16), wd = on(a.dH + at - off, 16),
-               wx = on(a.dX + at - off, 16), ww = on(a.w - off, 16);
+    const bool wx = on(a.dX + at - off, 16);
+    auto gain = [&](long long k, float(&g)[8]) { gains8<T>(a.w != nullptr, a.w ? load8(a.w, k, K) : kZero, g); };
     const float r = a.rstd[row];
     float sum = 0.0f, top = 0.0f;
     for (long long k = k0; k < K; k += STEP) {
         float f[8], d[8], g[8];
-        unpack8<T>(load8<true>(a.H + at, k, K, wh), f);
-        unpack8<T>(load8<true>(a.dY + at, k, K, wy), d);
-        weight8<T, true>(a.w, k, K, ww, g);
+        unpack8<T>(load8(a.H + at, k, K), f);
+        unpack8<T>(load8(a.dY + at, k, K), d);
+        gain(k, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(d[j] * (f[j] * r), g[j], sum);
     }
@@ -465,13 +661,13 @@ rms_norm_long_dx_kernel(const BwdArgs a)
     const float mean = sum / (float)K;
     for (long long k = k0; k < K; k += STEP) {
         float f[8], d[8], g[8], e[8];
-        unpack8<T>(load8<true>(a.H + at, k, K, wh), f);
-        unpack8<T>(load8<true>(a.dY + at, k, K, wy), d);
-        unpack8<T>(a.dH ? load8<true>(a.dH + at, k, K, wd) : make_uint4(0u, 0u, 0u, 0u), e);
-        weight8<T, true>(a.w, k, K, ww, g);
+        unpack8<T>(load8(a.H + at, k, K), f);
+        unpack8<T>(load8(a.dY + at, k, K), d);
+        unpack8<T>(a.dH ? load8(a.dH + at, k, K) : kZero, e);
+        gain(k, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) d[j] = fmaf(r, fmaf(-f[j] * r, mean, d[j] * g[j]), e[j]);
-        store8<true>(a.dX + at, k, K, wx, pack8<T>(d));
+        store8(a.dX + at, k, K, wx, pack8<T>(d));
     }
 }
 // Their dw: a thread to a column, block y a range of the rows.
@@ -491,39 +687,46 @@ rms_norm_long_dw_kernel(const BwdArgs a)
     a.part[blockIdx.y * (long long)a.K + k] = s;
 }
 
-// dw[k] = sum over n partials, each warp its share of them in order, then the warps' sums in order.
-__global__ void __launch_bounds__(256)
+// dw[k] = sum over n partials, each of 32 warps its share of them in order, then the
+// warps' sums in order.
+__global__ void __launch_bounds__(1024)
 rms_norm_dw_kernel(const float *__restrict__ part, float *__restrict__ dw, int n, int K)
 {
-    __shared__ float sums[8][32];
+    __shared__ float sums[32][32];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long k = blockIdx.x * 32LL + lane;
     float s = 0.0f;
     if (k < K) {
 #pragma unroll 8
-        for (int g = warp; g < n; g += 8) s += __ldcg(part + (long long)g * K + k);
+        for (int g = warp; g < n; g += 32) s += __ldcg(part + (long long)g * K + k);
     }
     sums[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && k < K) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) s += sums[w][lane];
+        for (int w = 1; w < 32; ++w) s += sums[w][lane];
         dw[k] = s;
     }
 }
 
-// Warps to a row of K elements (of so many pieces, if its rows start inside one); 0: a long row.
-int row_split(int K, bool odd) {
-    const long long n = (long long)K + (odd ? 14 : 0);
+// Warps to a row of K elements that lies as kind_of says; 0: for the kernels of any rows.
+int row_split(int K, int kind) {
+    if (kind == 2) return 0;
     for (int w = 1; w <= MAX_WPR; w *= 2)
-        if (n <= (long long)w * WARP_ELEMS) return w;
+        if (K <= w * WARP_ELEMS) return w;
     return 0;
 }
-bool all_on16(std::initializer_list<const void *> ps, int K) {
-    uintptr_t a = 0;
-    for (const void *p : ps) a |= (uintptr_t)p;
-    return (a & 15) == 0 && K % 8 == 0;
+// How the rows of operands lie: 0 all on 16 bytes, 1 alike, 2 otherwise (null ones lie anywhere).
+int kind_of(const void *first, std::initializer_list<const void *> others, const void *w, int K) {
+    uintptr_t a = (uintptr_t)first & 15, any = a | ((uintptr_t)w & 15);
+    bool alike = true;
+    for (const void *p : others)
+        if (p) {
+            alike = alike && ((uintptr_t)p & 15) == a;
+            any |= (uintptr_t)p & 15;
+        }
+    return any == 0 && K % 8 == 0 ? 0 : alike ? 1 : 2;
 }
 
 template <typename F>
@@ -535,6 +738,20 @@ cudaError_t with_split(int wpr, F f) {
     case 8: return f(std::integral_constant<int, 8>());
     default: return f(std::integral_constant<int, 16>());
     }
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_smem(void (*kern)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args... args) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e;
+        }
+    }
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3((unsigned)threads), smem, s, attr);
+    return launch_counted(&cfg, kern, args...);
 }
 
 template <typename T, bool E4M3>
@@ -551,8 +768,9 @@ cudaError_t forward(const NormProblem &p, cudaStream_t s) {
     a.eps = p.eps;
     a.M = p.M;
     a.K = p.K;
-    const bool odd = !all_on16({p.X, p.R, p.w, p.H, p.Y}, p.K) || !on(p.Q, 8);
-    const int wpr = row_split(p.K, odd);
+    int kind = kind_of(p.X, {p.R, p.H, p.Y}, p.w, p.K);
+    if (p.Q && ((uintptr_t)p.Q & 7) != ((uintptr_t)p.X & 15) >> 1) kind = 2;  // codes on 8 bytes where X is on 16
+    const int wpr = row_split(p.K, kind);
     cudaLaunchAttribute attr[1];
     if (wpr == 0) {
         const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)p.M), dim3(MAX_WPR * 32), 0, s, attr);
@@ -560,30 +778,15 @@ cudaError_t forward(const NormProblem &p, cudaStream_t s) {
     }
     return with_split(wpr, [&](auto w) {
         constexpr int W = decltype(w)::value, ROWS = row_warps(W) / W;
-        const cudaLaunchConfig_t cfg =
-            pdl_config(dim3((unsigned)(((long long)p.M + ROWS - 1) / ROWS)), dim3(row_warps(W) * 32), 0, s, attr);
-        return odd ? launch_counted(&cfg, rms_norm_kernel<T, W, true, E4M3>, a)
-                   : launch_counted(&cfg, rms_norm_kernel<T, W, false, E4M3>, a);
+        const unsigned grid = (unsigned)(((long long)p.M + ROWS - 1) / ROWS);
+        const size_t gains = kind ? (size_t)((p.K + 15) & ~7) * 2 : 0;
+        return launch_smem(kind ? rms_norm_kernel<T, W, true, E4M3> : rms_norm_kernel<T, W, false, E4M3>, grid,
+                           row_warps(W) * 32, gains, s, a);
     });
 }
 
-template <typename T, int W, bool ODD>
-cudaError_t launch_backward(const BwdArgs &a, unsigned grid, size_t smem, cudaStream_t s) {
-    auto kern = rms_norm_backward_kernel<T, W, ODD>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            return e;
-        }
-    }
-    cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pdl_config(dim3(grid), dim3(row_warps(W) * 32), smem, s, attr);
-    return launch_counted(&cfg, kern, a);
-}
-
 template <typename T>
-cudaError_t backward(const NormBackward &p, int num_sms, cudaStream_t s) {
+cudaError_t backward(const NormBackward &p, int num_sms, int *status, cudaStream_t s) {
     BwdArgs a = {};
     a.H = static_cast<const uint16_t *>(p.H);
     a.w = static_cast<const uint16_t *>(p.w);
@@ -593,11 +796,11 @@ cudaError_t backward(const NormBackward &p, int num_sms, cudaStream_t s) {
     a.dX = static_cast<uint16_t *>(p.dX);
     a.M = p.M;
     a.K = p.K;
-    const bool odd = !all_on16({p.H, p.w, p.dY, p.dH, p.dX}, p.K);
-    const int wpr = row_split(p.K, odd);
+    const int kind = kind_of(p.H, {p.dY, p.dH, p.dX}, p.w, p.K);
+    const int wpr = row_split(p.K, kind);
     const int rows = wpr ? row_warps(wpr) / wpr : 1;
     // as many CTAs as stay resident, and partial sums of dw
-    const int per_sm = wpr <= 4 ? 4 : wpr == 8 ? 2 : 1;
+    const int per_sm = ctas_per_sm(wpr ? wpr : MAX_WPR);
     const long long ctas = std::min<long long>(((long long)p.M + rows - 1) / rows, (long long)num_sms * per_sm);
     const int n = wpr ? (int)ctas : std::min(p.M, 256);
     void *ws = nullptr;
@@ -623,13 +826,19 @@ cudaError_t backward(const NormBackward &p, int num_sms, cudaStream_t s) {
     } else {
         e = with_split(wpr, [&](auto w) {
             constexpr int W = decltype(w)::value;
-            const size_t smem = p.dw && (odd || rows > 1) ? (size_t)row_warps(W) * WARP_ELEMS * 4 : 0;
-            return odd ? launch_backward<T, W, true>(a, (unsigned)ctas, smem, s)
-                       : launch_backward<T, W, false>(a, (unsigned)ctas, smem, s);
+            constexpr int THREADS = row_warps(W) * 32;
+            if (kind != 0) {
+                const size_t gains = (size_t)((p.K + 15) & ~7) * 2, sums = (size_t)rows * 8 * (W * 128 + 1) * 4;
+                return launch_smem(rms_norm_backward_odd_kernel<T, W>, (unsigned)ctas, THREADS, gains + (p.dw ? sums : 0), s, a);
+            }
+            // stages: those that per_sm CTAs find room for, at most eight
+            const size_t stage = (size_t)3 * rows * p.K * 2;
+            const int stages = (int)std::max<size_t>(2, std::min<size_t>(8, 220 * 1024 / per_sm / stage));
+            return launch_smem(rms_norm_backward_bulk_kernel<T, W>, (unsigned)ctas, THREADS, stages * stage, s, a, stages, status);
         });
     }
     if (e == cudaSuccess && ws) {
-        const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((p.K + 31LL) / 32)), dim3(256), 0, s, attr);
+        const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)((p.K + 31LL) / 32)), dim3(1024), 0, s, attr);
         e = launch_counted(&cfg, rms_norm_dw_kernel, static_cast<const float *>(ws), p.dw, n, p.K);
     }
     const cudaError_t f = ws ? cudaFreeAsync(ws, s) : cudaSuccess;
@@ -643,8 +852,8 @@ cudaError_t launch_rms_norm(const NormProblem &p, cudaStream_t s) {
     return p.Y ? forward<__half, false>(p, s) : forward<__half, true>(p, s);
 }
 
-cudaError_t launch_rms_norm_backward(const NormBackward &p, int num_sms, cudaStream_t s) {
-    return p.elt == Elt::BF16 ? backward<__nv_bfloat16>(p, num_sms, s) : backward<__half>(p, num_sms, s);
+cudaError_t launch_rms_norm_backward(const NormBackward &p, int num_sms, int *status, cudaStream_t s) {
+    return p.elt == Elt::BF16 ? backward<__nv_bfloat16>(p, num_sms, status, s) : backward<__half>(p, num_sms, status, s);
 }
 
 }  // namespace gemm_gb300
