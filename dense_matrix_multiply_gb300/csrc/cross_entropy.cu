@@ -47,7 +47,7 @@ struct LseEpi {
 
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
-    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
+    __device__ __forceinline__ void run(Part &p, const Pre &) const {
         const int row = p.row0 + p.lane, width = p.width, first = p.col0 + p.first;
         if (first >= N) return;  // warp-uniform
         long long t = row < M ? target[row] : -1;
@@ -103,7 +103,7 @@ struct DzEpi {
 
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
-    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
+    __device__ __forceinline__ void run(Part &p, const Pre &) const {
         const int row = p.row0 + p.lane;
         long long t = row < M ? target[row] : -1;
         const bool counts = t >= 0 && t < total;
@@ -134,9 +134,9 @@ struct DzEpi {
                     z[h * 16 + j] = bf16 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
                 }
             }
-            box_begin(p.lane);
-            box_put(p.box, p.lane, z);
-            box_store(&tm, p.box, p.lane, c0, p.row0, 0);
+            uint8_t *box = box_next<BOXES>(p);
+            box_put(box, p.lane, z);
+            box_store(&tm, box, p.lane, c0, p.row0, 0);
         }
     }
 };
@@ -151,20 +151,20 @@ struct AccEpi {
 
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
-    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
+    __device__ __forceinline__ void run(Part &p, const Pre &) const {
 #pragma unroll 1
         for (int g = p.first; g < p.first + p.width; g += 32) {
             if (p.col0 + g >= N) return;  // warp-uniform
             uint32_t r[32];
             p.load<false>(g, r);
-            box_begin(p.lane);
-            box_put(p.box, p.lane, r);
+            uint8_t *box = box_next<BOXES>(p);
+            box_put(box, p.lane, r);
             if (add) {
                 fence_async_shared();
                 __syncwarp();
-                if (p.lane == 0) tma_add_3d(&tm, p.box, p.col0 + g, p.row0, p.split);
+                if (p.lane == 0) tma_add_3d(&tm, box, p.col0 + g, p.row0, p.split);
             } else {
-                box_store(&tm, p.box, p.lane, p.col0 + g, p.row0, p.split);
+                box_store(&tm, box, p.lane, p.col0 + g, p.row0, p.split);
             }
         }
     }
@@ -173,7 +173,7 @@ struct AccEpi {
 // 16-bit results times scale->y.
 struct OutEpi {
     static constexpr bool LOWER = false, JOIN = false;
-    static constexpr int BOXES = 1;
+    static constexpr int BOXES = 2;
     CUtensorMap tm;
     const float2 *scale;  // null: 1
     uint16_t *out;        // not null: by the element, rows ld apart
@@ -183,7 +183,7 @@ struct OutEpi {
 
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
-    __device__ __forceinline__ void run(const Part &p, const Pre &) const {
+    __device__ __forceinline__ void run(Part &p, const Pre &) const {
         const float f = scale ? scale->y : 1.0f;
 #pragma unroll 1
         for (int g = p.first; g < p.first + p.width; g += 64) {
@@ -200,10 +200,10 @@ struct OutEpi {
                     z[h * 16 + j] = bf16 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
                 }
             }
-            box_begin(p.lane);
-            box_put(p.box, p.lane, z);
-            if (out) box_scatter(p.box, p.lane, out, ld, p.row0, c0, M, N);
-            else box_store(&tm, p.box, p.lane, c0, p.row0, 0);
+            uint8_t *box = box_next<BOXES>(p);
+            box_put(box, p.lane, z);
+            if (out) box_scatter(box, p.lane, out, ld, p.row0, c0, M, N);
+            else box_store(&tm, box, p.lane, c0, p.row0, 0);
         }
     }
 };
@@ -389,14 +389,14 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             }
             const long long tiles = ceil_div(m, 256) * ceil_div(n, bn);
             CUtensorMap ta, tb;
-            if (tiles > 0x7FFFFFFFLL || !map_operand(&ta, x, FORMAT, false, m, kp, kp, 128) ||
+            if (tiles > 0x7FFFFFFFLL || !map_operand(&ta, x, FORMAT, false, m, kp, kp, left_rows(m)) ||
                 !map_operand(&tb, w, FORMAT, false, n, kp, kp, bn / 2)) {
                 e = cudaErrorInvalidValue;
                 break;
             }
             epi.N = n;
             epi.v0 = (int)v0;
-            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, 1, status};
+            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, 1, left_rows(m), BK, status};
             e = launch<FORMAT>(ta, tb, epi, a, cmax, s);
         }
         if (e != cudaSuccess) break;
@@ -477,7 +477,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
         CUtensorMap ta, tb;
         {
             DzEpi epi;
-            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, 128) || !map_operand(&tb, w, FORMAT, false, n, kp, kp, 128) ||
+            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, left_rows(p.M)) || !map_operand(&tb, w, FORMAT, false, n, kp, kp, 128) ||
                 !map16(&epi.tm, z, FORMAT, p.M, n, vp, 32, 64)) {
                 e = cudaErrorInvalidValue;
                 break;
@@ -491,14 +491,16 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.v0 = (int)v0;
             epi.total = p.N;
             epi.bf16 = bf16;
-            const Args a = {p.M, n, (int)ceil_div(kp, BK), 256, 0, 0, (int)z_tiles, 1, 1, status};
+            const Args a = {p.M, n, (int)ceil_div(kp, BK), 256, 0, 0, (int)z_tiles, 1, 1, left_rows(p.M), BK, status};
             e = launch<FORMAT>(ta, tb, epi, a, cz, s);
         }
         if (e == cudaSuccess && p.dW) {
             OutEpi epi;
             uint16_t *out = static_cast<uint16_t *>(p.dW) + v0 * p.K;
             const bool tma = aligned && on16(p.dW);
-            if (!map_operand(&ta, z, FORMAT, true, n, p.M, vp, 0) || !map_operand(&tb, x, FORMAT, true, kp, p.M, kp, 0) ||
+            const int k_rows = p.M <= 48 ? (p.M + 15) / 16 * 16 : BK;
+            if (!map_operand(&ta, z, FORMAT, true, n, p.M, vp, 0, k_rows) ||
+                !map_operand(&tb, x, FORMAT, true, kp, p.M, kp, 0, k_rows) ||
                 !map16(&epi.tm, tma ? (const void *)out : z, FORMAT, n, tma ? p.K : 64, tma ? p.K : 64, 32, 64)) {
                 e = cudaErrorInvalidValue;
                 break;
@@ -509,12 +511,12 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.M = n;
             epi.N = p.K;
             epi.bf16 = bf16;
-            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, status};
+            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, status};
             e = launch<FORMAT>(ta, tb, epi, a, cw, s);
         }
         if (e == cudaSuccess && p.dX) {
             AccEpi epi;
-            if (!map_operand(&ta, z, FORMAT, false, p.M, n, vp, 128) || !map_operand(&tb, w, FORMAT, true, kp, n, kp, 0) ||
+            if (!map_operand(&ta, z, FORMAT, false, p.M, n, vp, left_rows(p.M)) || !map_operand(&tb, w, FORMAT, true, kp, n, kp, 0) ||
                 !make_map3(&epi.tm, base + at_slab, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, ldx * 4,
                            p.M * ldx * 4, 32, 32, 1, 128)) {
                 e = cudaErrorInvalidValue;
@@ -524,7 +526,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.add = v0 > 0;
             // (a short last piece: fewer ranges, each of one block at least)
             const int kb = (int)ceil_div(n, BK);
-            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, status};
+            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, left_rows(p.M), BK, status};
             e = launch<FORMAT>(ta, tb, epi, a, cx, s);
         }
     }

@@ -96,7 +96,7 @@ struct SymEpi {
         pre.old.clear();
         fetch(p, p.first, pre);
     }
-    __device__ __forceinline__ void run(const Part &p, Pre &pre) const {
+    __device__ __forceinline__ void run(Part &p, Pre &pre) const {
         const float s = scale ? *scale : 1.0f, by = f * s * s;
         const bool mirror = p.col0 + p.bn <= p.row0 / 256 * 256;
 #pragma unroll 1
@@ -173,7 +173,7 @@ struct MulEpi : MulArgs {
     }
     // Two lanes of FP32 at a time: the conversions and these, ten instructions for two
     // elements, bound a tile's writing.
-    __device__ __forceinline__ void run(const Part &p, Pre &pre) const {
+    __device__ __forceinline__ void run(Part &p, Pre &pre) const {
         const float s = LO ? 1.0f : *scale, sa = s * a;
         const float2 s2 = make_float2(s, s), a2 = make_float2(sa, sa), lo2 = make_float2(sa / kLo, sa / kLo),
                      up2 = make_float2(kLo, kLo), down2 = make_float2(-kLo, -kLo), zero2 = make_float2(0.0f, 0.0f);
@@ -432,7 +432,7 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
     if (tma_out) ok = ok && map16(&res, p.O, bf16 ? 1 : 0, p.M, p.N, p.ldo, 32, 64);
     if (!ok && e == cudaSuccess) e = cudaErrorInvalidValue;
     auto args = [&](int rows, int cols, int k, const Plan &q, bool a_mn, bool b_mn) {
-        return Args{rows, cols, (int)ceil_div(k, BK), q.bn, a_mn, b_mn, (int)q.tiles, 1, q.joined, status};
+        return Args{rows, cols, (int)ceil_div(k, BK), q.bn, a_mn, b_mn, (int)q.tiles, 1, q.joined, 128, BK, status};
     };
     for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
         const int in = i & 1, out = in ^ 1;

@@ -62,6 +62,14 @@ struct Args {
     int tiles;
     int splits;      // K ranges of a tile, each a unit of its own
     int joined;      // pairs on a tile: 1, or 2 (bn 128, splits 1, a cluster to each tile)
+    // Rows of A's boxes.  For M <= 128 those that there are, up to eights: the leader's, the
+    // peer loads none (zeros behind the matrix cost a load as much time as its elements: M =
+    // 1, N = 32000, K = 4096 84 us with boxes of 128 rows); what the rows behind them hold
+    // reaches no row of D but theirs.
+    int a_rows;
+    // k that a stage's boxes hold, 64, where both operands lie MN-major and K is less 16, 32
+    // or 48 at least as many: the rest of the only block is neither loaded nor multiplied.
+    int k_rows;
     int *status;
 };
 
@@ -133,6 +141,7 @@ struct Part {
     int split;              // which K range
     int bn, lane;
     uint8_t *box;           // STG_BOX bytes of this warp's, once or twice
+    int turn;               // which of two is next (box_next)
     const uint8_t *joined;  // null, or this lane's row of the other pair's sums from column `first` on
 
     // Columns c .. c + 31 of the tile, this lane's row.
@@ -172,6 +181,19 @@ __device__ __forceinline__ void box_put_half(uint8_t *box, int lane, int h, cons
 __device__ __forceinline__ void box_begin(int lane) {
     if (lane == 0) tma_stores_read_wait0();
     __syncwarp();
+}
+// One box, or two in turn: the next one, once the store that last read it has done so.
+template <int BOXES>
+__device__ __forceinline__ uint8_t *box_next(Part &p) {
+    if (BOXES == 1) {
+        box_begin(p.lane);
+        return p.box;
+    }
+    if (p.lane == 0) tma_stores_read_wait1();
+    __syncwarp();
+    uint8_t *box = p.box + p.turn * STG_BOX;
+    p.turn ^= 1;
+    return box;
 }
 __device__ __forceinline__ void box_store(const CUtensorMap *map, const uint8_t *box, int lane, int x, int y, int z) {
     fence_async_shared();
@@ -223,7 +245,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int cluster = (int)cluster_id_x(), nclusters = (int)cluster_count_x();
     const int units = args.tiles * args.splits;
     const bool joined = Epi::JOIN && args.joined > 1;
-    const uint32_t stage_tx = 2u * (uint32_t)(A_STAGE + (bn >> 1) * 128);
+    // bytes of a stage that this CTA loads, and its peer
+    const uint32_t a_bytes = args.a_mn ? 2u * (uint32_t)args.k_rows * 128u : (uint32_t)args.a_rows * 128u;
+    const uint32_t b_bytes = args.b_mn ? (uint32_t)(bn >> 7) * (uint32_t)args.k_rows * 128u : (uint32_t)(bn >> 1) * 128u;
+    const bool few = args.a_rows < 128;
+    const uint32_t peer_tx = b_bytes + (few ? 0u : a_bytes), stage_tx = a_bytes + b_bytes + peer_tx;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -282,7 +308,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if (args.a_mn) {
                         tma_load_3d_pair(a, &tmA, full, row0, kb * BK, 0);
                         tma_load_3d_pair(a + BOX64, &tmA, full, row0 + 64, kb * BK, 0);
-                    } else {
+                    } else if (leader || !few) {
                         tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
                     }
                     if (args.b_mn) {
@@ -319,8 +345,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             const long long hi = issued > ip ? issued : ip;
             for (long long i = (hi > STAGES ? hi - STAGES : 0); i < hi; ++i) {
                 const int s = (int)(i % STAGES);
-                if (i >= issued) mbar_arrive_expect_tx(&bars->full[s], stage_tx / 2);
-                else if (i >= ip) mbar_complete_tx(&bars->full[s], stage_tx / 2);
+                if (i >= issued) mbar_arrive_expect_tx(&bars->full[s], peer_tx);
+                else if (i >= ip) mbar_complete_tx(&bars->full[s], peer_tx);
                 if (!mbar_wait(&bars->full[s], (uint32_t)((i / STAGES) & 1), abort_flag, false)) {
                     atomicOr(args.status, ST_DRAIN);
                     break;
@@ -356,7 +382,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 if (issuer) {
 #pragma unroll
                     for (int ks = 0; ks < BK / 16; ++ks)
-                        mma(d, ad + ks * a_step, bd + ks * b_step, idesc, (uint32_t)(kb != kb0 || ks != 0));
+                        if (ks * 16 < args.k_rows) mma(d, ad + ks * a_step, bd + ks * b_step, idesc, (uint32_t)(kb != kb0 || ks != 0));
                     commit_to_pair(&bars->empty[stage], lead);
                 }
                 if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -383,6 +409,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         p.first = half * (bn >> 1);
         p.width = bn >> 1;
         p.joined = nullptr;
+        p.turn = 0;
         int it = 0;
         bool ok = true;
         p.split = cluster / args.tiles;
@@ -492,11 +519,13 @@ inline bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows
                   int box_cols) {
     return make_map3(m, p, map_type(format), cols, rows, 1, ld * 2, rows * ld * 2, box_cols, box_rows, 1, 128);
 }
-// An operand of the product from its stored matrix: mn: [K, MN] in 64 x 64 boxes, else
+// left_rows: of the left operand's boxes, K-major.
+// An operand of the product from its stored matrix: mn: [K, MN] in k_rows x 64 boxes, else
 // [MN, K] in boxes of `rows` x 64.
+inline int left_rows(long long m) { return m <= 120 ? (int)(m + 7) / 8 * 8 : 128; }
 inline bool map_operand(CUtensorMap *m, const void *p, uint32_t format, bool mn, long long mn_size, long long k, long long ld,
-                        int rows) {
-    return mn ? map16(m, p, format, k, mn_size, ld, BK, 64) : map16(m, p, format, mn_size, k, ld, rows, BK);
+                        int rows, int k_rows = BK) {
+    return mn ? map16(m, p, format, k, mn_size, ld, k_rows, 64) : map16(m, p, format, mn_size, k, ld, rows, BK);
 }
 
 }  // namespace pair
