@@ -37,13 +37,16 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 units of 2^-23 off; 0
 }
 
 // Of the columns [c0, c0 + 32) within a row's [0, N), c0 < N: the rest count as -inf.
-struct LseEpi {
-    static constexpr bool LOWER = false, JOIN = false;
-    static constexpr int BOXES = 1;
+struct LseArgs {
     float2 *part;             // (m, s) of slot column / (bn / 2), [slot][M]
     float *zt;                // Z_i,t_i
     const long long *target;
     int M, N, v0, total;      // rows; columns of this piece, and its first; of Z
+};
+template <bool JOINED>
+struct LseEpi : LseArgs {
+    static constexpr bool LOWER = false, JOIN = JOINED;
+    static constexpr int BOXES = JOINED ? 2 : 1;
 
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
@@ -56,7 +59,7 @@ struct LseEpi {
 #pragma unroll 1
         for (int c = 0; c < width && first + c < N; c += 32) {
             uint32_t r[32];
-            p.load<false>(p.first + c, r);
+            p.load<JOIN>(p.first + c, r);
             const int left = N - first - c;
             if (left < 32) {  // warp-uniform
 #pragma unroll
@@ -91,15 +94,18 @@ struct LseEpi {
 };
 
 // Scale factors of dZ: (up, down), powers of two whose product is 1.
-struct DzEpi {
-    static constexpr bool LOWER = false, JOIN = false;
-    static constexpr int BOXES = 1;
+struct DzArgs {
     CUtensorMap tm;  // dZ of the piece
     const float *lse, *dloss;
     const long long *target;
     const float2 *scale;  // null: 1
     int M, N, v0, total;  // total: columns of Z
     bool bf16;
+};
+template <bool JOINED>
+struct DzEpi : DzArgs {
+    static constexpr bool LOWER = false, JOIN = JOINED;
+    static constexpr int BOXES = JOINED ? 2 : 1;
 
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
@@ -118,7 +124,7 @@ struct DzEpi {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t r[32];
-                p.load<false>(g + h * 32, r);
+                p.load<JOIN>(g + h * 32, r);
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -base));
@@ -353,17 +359,44 @@ struct Layout {
 
 constexpr long long kPiece = 256LL << 20;  // bytes of a piece of dZ, or of a padded piece of W
 
+// How the logits' tiles are cut: few go in 128 columns, and where one wave of them takes
+// joined pairs, a half of K each, if they are done first (forward of 1 x 1000 x 4096 18.5 us
+// against 26.8, 4 x 5000 x 4096 22.9 against 27.0, 1500 x 1500 x 4000 24.7 against 28.7; 1 x
+// 12000 x 4096, three waves of joined pairs, 45.6 against 29.0).  Times in 1/100 us: a block
+// of 64 k of 256 x bn, a join.
+struct LogitPlan {
+    int bn, joined, clusters;
+    long long tiles;
+};
+template <uint32_t FORMAT, template <bool> class Epi>
+LogitPlan logit_plan(int M, int N, long long kb, int dev) {
+    LogitPlan best = {};
+    long long least = 0;
+    for (int way = 0; way < 3; ++way) {
+        const int bn = way == 0 ? 256 : 128, joined = way == 2 ? 2 : 1;
+        const int c = joined == 1 ? clusters_max<FORMAT, Epi<false>>(dev) : joined_max<FORMAT, Epi<true>>(dev);
+        const long long tiles = ceil_div(M, 256) * ceil_div(N, bn);
+        if (c <= 0 || tiles > 0x7FFFFFFFLL || (joined > 1 && (tiles > c || kb < 2))) continue;
+        const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * (bn == 256 ? 28 : 20) + (joined > 1 ? 150 : 0);
+        if (!best.bn || time < least) {
+            best = {bn, joined, c, tiles};
+            least = time;
+        }
+    }
+    return best;
+}
+
 template <uint32_t FORMAT>
 cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) {
-    const int cmax = clusters_max<FORMAT, LseEpi>(dev);
-    if (cmax <= 0) return cudaErrorNotSupported;
     const bool aligned = p.K % 8 == 0;
     const bool pad_x = !aligned || !on16(p.X), pad_w = !aligned || !on16(p.W);
     const long long kp = aligned ? p.K : up(p.K, 64);
-    const int bn = 256, rows_max = 16384;
+    const int rows_max = 16384;
     const int rows = std::min(p.M, rows_max);
-    const long long vp = pad_w ? std::min<long long>(up(p.N, bn), std::max<long long>(kPiece / (2 * kp) / bn * bn, bn)) : p.N;
-    const int slots = (int)ceil_div(p.N, bn / 2);
+    const long long vp = pad_w ? std::min<long long>(up(p.N, 256), std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256)) : p.N;
+    const LogitPlan pl = logit_plan<FORMAT, LseEpi>(rows, (int)std::min<long long>(vp, p.N), ceil_div(kp, BK), dev);
+    if (!pl.bn) return cudaErrorNotSupported;
+    const int bn = pl.bn, slots = (int)ceil_div(p.N, bn / 2);
     Layout l;
     const size_t at_x = l.add(pad_x ? (size_t)rows * kp * 2 : 0), at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0),
                  at_part = l.add((size_t)slots * rows * 8), at_zt = l.add((size_t)rows * 4);
@@ -378,7 +411,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             e = copy(x, m, p.K, base + at_x, kp, nullptr, 1, s);
             x = reinterpret_cast<const uint16_t *>(base + at_x);
         }
-        LseEpi epi = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N};
+        LseArgs lse = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N};
         for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
             const int n = (int)std::min<long long>(vp, p.N - v0);
             const uint16_t *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
@@ -394,16 +427,17 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
                 e = cudaErrorInvalidValue;
                 break;
             }
-            epi.N = n;
-            epi.v0 = (int)v0;
-            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, 1, left_rows(m), BK, status};
-            e = launch<FORMAT>(ta, tb, epi, a, cmax, s);
+            lse.N = n;
+            lse.v0 = (int)v0;
+            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, pl.joined, left_rows(m), BK, status};
+            e = pl.joined > 1 ? launch<FORMAT>(ta, tb, LseEpi<true>{lse}, a, pl.clusters, s)
+                              : launch<FORMAT>(ta, tb, LseEpi<false>{lse}, a, pl.clusters, s);
         }
         if (e != cudaSuccess) break;
         cudaLaunchAttribute attr[1];
         const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)ceil_div(m, 32)), dim3(1024), 0, s, attr);
-        e = launch_counted(&cfg, head_join_kernel, static_cast<const float2 *>(epi.part), static_cast<const float *>(epi.zt),
-                           epi.target, p.loss + r0, p.lse ? p.lse + r0 : nullptr, slots, m, p.N);
+        e = launch_counted(&cfg, head_join_kernel, static_cast<const float2 *>(lse.part), static_cast<const float *>(lse.zt),
+                           lse.target, p.loss + r0, p.lse ? p.lse + r0 : nullptr, slots, m, p.N);
     }
     const cudaError_t f = cudaFreeAsync(ws, s);
     return e != cudaSuccess ? e : f;
@@ -423,8 +457,8 @@ int dx_splits(long long tiles, long long num_kb, int cmax, double slab_us) {
 
 template <typename T, uint32_t FORMAT>
 cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s) {
-    const int cz = clusters_max<FORMAT, DzEpi>(dev), cx = clusters_max<FORMAT, AccEpi>(dev), cw = clusters_max<FORMAT, OutEpi>(dev);
-    if (cz <= 0 || cx <= 0 || cw <= 0) return cudaErrorNotSupported;
+    const int cx = clusters_max<FORMAT, AccEpi>(dev), cw = clusters_max<FORMAT, OutEpi>(dev);
+    if (cx <= 0 || cw <= 0) return cudaErrorNotSupported;
     const bool aligned = p.K % 8 == 0;
     const long long kp = aligned ? p.K : up(p.K, 64);
     // X: rows without a target are zeros in dW's product, whatever they hold (0 times an
@@ -469,15 +503,17 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             w = base + at_w;
         }
         const void *z = base + at_z;
-        const long long z_tiles = ceil_div(p.M, 256) * ceil_div(n, 256), w_tiles = ceil_div(n, 256) * ceil_div(p.K, 256);
-        if (z_tiles > 0x7FFFFFFFLL || w_tiles > 0x7FFFFFFFLL || x_tiles * splits > 0x7FFFFFFFLL) {
+        const LogitPlan pl = logit_plan<FORMAT, DzEpi>(p.M, n, ceil_div(kp, BK), dev);
+        const long long w_tiles = ceil_div(n, 256) * ceil_div(p.K, 256);
+        if (!pl.bn || w_tiles > 0x7FFFFFFFLL || x_tiles * splits > 0x7FFFFFFFLL) {
             e = cudaErrorInvalidValue;
             break;
         }
         CUtensorMap ta, tb;
         {
-            DzEpi epi;
-            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, left_rows(p.M)) || !map_operand(&tb, w, FORMAT, false, n, kp, kp, 128) ||
+            DzArgs epi;
+            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, left_rows(p.M)) ||
+                !map_operand(&tb, w, FORMAT, false, n, kp, kp, pl.bn / 2) ||
                 !map16(&epi.tm, z, FORMAT, p.M, n, vp, 32, 64)) {
                 e = cudaErrorInvalidValue;
                 break;
@@ -491,8 +527,9 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.v0 = (int)v0;
             epi.total = p.N;
             epi.bf16 = bf16;
-            const Args a = {p.M, n, (int)ceil_div(kp, BK), 256, 0, 0, (int)z_tiles, 1, 1, left_rows(p.M), BK, status};
-            e = launch<FORMAT>(ta, tb, epi, a, cz, s);
+            const Args a = {p.M, n, (int)ceil_div(kp, BK), pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, left_rows(p.M), BK, status};
+            e = pl.joined > 1 ? launch<FORMAT>(ta, tb, DzEpi<true>{epi}, a, pl.clusters, s)
+                              : launch<FORMAT>(ta, tb, DzEpi<false>{epi}, a, pl.clusters, s);
         }
         if (e == cudaSuccess && p.dW) {
             OutEpi epi;
