@@ -112,14 +112,15 @@ def _addr(x) -> int:
     return x.data_ptr()
 
 
-_raw_stream = None
+_raw_stream = _raw_device = None
 
 
 def _current_stream(device: int) -> int:
     """Handle of torch's current stream on a device."""
-    global _raw_stream
+    global _raw_stream, _raw_device
     if _raw_stream is None:
         import torch
+        _raw_device = torch._C._cuda_getDevice
         _raw_stream = torch._C._cuda_getCurrentRawStream
     return _raw_stream(device)
 
@@ -218,6 +219,8 @@ def _take(lib, name: str, *args):
         if mixed:
             raise ValueError("tensors on two devices")
         lib.gemm_set_stream(_current_stream(dev))
+        if dev != _raw_device():  # (known since _current_stream) the library launches on the current device
+            raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{_raw_device()}")
     return out
 
 

@@ -746,7 +746,9 @@ gemm_status_t run_orthogonalize(int dtype, const void *G, int64_t ldg, void *O, 
     DeviceInfo *dev = nullptr;
     gemm_status_t st = device_info(&dev);
     if (st != GEMM_OK) return st;
-    const OrthProblem p{G, ldg, O, ldo, M, N, steps, a, b, c, elt16(dtype)};
+    // (a single row's leading dimension is never stepped by, and may be too large for TMA)
+    const long long one = ((long long)N + 7) / 8 * 8;
+    const OrthProblem p{G, M > 1 ? (long long)ldg : one, O, M > 1 ? (long long)ldo : one, M, N, steps, a, b, c, elt16(dtype)};
     return finish(launch_orthogonalize(p, dev->num_sms, dev->status, t_stream), "orthogonalize");
 }
 

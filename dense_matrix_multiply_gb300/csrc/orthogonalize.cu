@@ -427,7 +427,8 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
              map_operand(&sym[i][0], hi[i], 0, tall, m, n, ldx, 128) &&
              map_operand(&sym[i][1], hi[i], 0, tall, m, n, ldx, pa.bn / 2) &&
              map_operand(&mul[i], hi[i], 0, !tall, n, m, ldx, 128);
-    const bool tma_out = ((uintptr_t)p.O & 15) == 0 && p.ldo % 8 == 0;
+    // (TMA writes whole 16-byte pieces, past a row's last element too)
+    const bool tma_out = ((uintptr_t)p.O & 15) == 0 && p.ldo % 8 == 0 && p.N % 8 == 0;
     CUtensorMap res = hiM[0];
     if (tma_out) ok = ok && map16(&res, p.O, bf16 ? 1 : 0, p.M, p.N, p.ldo, 32, 64);
     if (!ok && e == cudaSuccess) e = cudaErrorInvalidValue;

@@ -439,8 +439,10 @@ rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
     }
     __syncthreads();
     pdl_wait();
+    long long fetched = 0;
     auto fetch = [&](long long row0, int stage) {  // one thread
         if (row0 >= a.M) return;
+        ++fetched;
         const uint32_t bytes = (uint32_t)min((long long)ROWS, a.M - row0) * (uint32_t)(K * 2);
         uint8_t *to = ring + stage * stage_bytes;
         tc::mbar_arrive_expect_tx(&full[stage], bytes * (has_dh ? 3u : 2u));
@@ -514,6 +516,9 @@ rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
             }
         }
     }
+    if (abort && threadIdx.x == 0)  // given up: no copy is left in flight when the CTA ends
+        for (long long i = max(fetched - stages, 0LL); i < fetched; ++i)
+            tc::mbar_wait(&full[i % stages], (uint32_t)((i / stages) & 1), &abort, false);
     if (!a.part) return;
     float *part = a.part + (long long)blockIdx.x * K;
     if constexpr (ROWS == 1) {

@@ -98,14 +98,21 @@ def test_large():
     assert float((got - X).norm()) <= tol
 
 
-@pytest.mark.parametrize("M,N", [(70, 136), (200, 72)])
+@pytest.mark.parametrize("M,N", [(70, 136), (200, 72), (70, 131), (3, 129), (300, 257)])
 def test_alignment_and_leading_dimensions(M, N):
     """Rows anywhere: the tight aligned call's bits, nothing but O's elements written."""
     G = make(M, N, "bf16", 7)
     want = run("bf16", G, 5)
-    for off, ldg, ldo in ((1, N, N), (0, N + 3, N + 8), (0, N + 8, N + 5), (8, N + 64, N + 1), (3, N + 1, N + 1)):
+    up = (N + 7) // 8 * 8
+    for off, ldg, ldo in ((0, up, up), (0, N, up + 8), (1, N, N), (0, N + 3, N + 8), (0, N + 8, N + 5), (8, N + 64, N + 1), (3, N + 1, N + 1)):
         assert torch.equal(run("bf16", G, 5, off, ldg, ldo), want), (off, ldg, ldo)
     assert torch.equal(run("bf16", G, 5, in_place=True), want)
+    row = G[:1].cuda().contiguous()
+    one, far = torch.empty(N, dtype=torch.bfloat16, device="cuda"), torch.empty(N, dtype=torch.bfloat16, device="cuda")
+    g.gemm_orthogonalize("bf16", row.reshape(-1), N, one, N, 5, 1, N)
+    g.gemm_orthogonalize("bf16", row.reshape(-1), 1 << 45, far, 1 << 50, 5, 1, N)  # a single row: never stepped by
+    g.gemm_synchronize()
+    assert torch.equal(one, far)
     assert torch.equal(run("bf16", G, 5, 1, N + 3, in_place=True), want)
 
 
