@@ -401,8 +401,8 @@ struct Layout {
 constexpr long long kPiece = 256LL << 20;  // bytes of a piece of dZ, or of a padded piece of W
 
 // How the logits' tiles are cut: few go in 128 columns, and where one wave of them takes
-// joined pairs, a half of K each, if they are done first (forward of 1 x 1000 x 4096 18.5 us
-// against 26.8, 4 x 5000 x 4096 22.9 against 27.0, 1500 x 1500 x 4000 24.7 against 28.7; 1 x
+// joined pairs, a half of K each, if they are done first (forward of 1 x 1000 x 4096 16.6 us
+// against 26.8, 4 x 5000 x 4096 22.6 against 27.0, 1500 x 1500 x 4000 24.6 against 28.7; 1 x
 // 12000 x 4096, three waves of joined pairs, 45.6 against 29.0).  Times in 1/100 us: a block
 // of 64 k of 256 x bn, a join.
 struct LogitPlan {
@@ -418,7 +418,7 @@ LogitPlan logit_plan(int M, int N, long long kb, int dev) {
         const int c = joined == 1 ? clusters_max<FORMAT, Epi<false>>(dev) : joined_max<FORMAT, Epi<true>>(dev);
         const long long tiles = ceil_div(M, 256) * ceil_div(N, bn);
         if (c <= 0 || tiles > 0x7FFFFFFFLL || (joined > 1 && (tiles > c || kb < 2))) continue;
-        const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * (bn == 256 ? 28 : 20) + (joined > 1 ? 150 : 0);
+        const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * (bn == 256 ? 28 : 20) + (joined > 1 ? 80 : 0);
         if (!best.bn || time < least) {
             best = {bn, joined, c, tiles};
             least = time;

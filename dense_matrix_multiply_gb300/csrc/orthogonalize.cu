@@ -328,8 +328,10 @@ orth_start_kernel(const uint16_t *G, long long ldg, int M, int N, const double *
 long long up64(long long n) { return (n + 63) / 64 * 64; }
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// A product's tiles: their width, and pairs joined on a tile, as are done first.  Times in
-// 1/100 us: a block of 64 k of 256 x bn, a tile's writing, a join.
+// A product's tiles: their width, and, where one wave of them takes it, pairs joined on a
+// tile, as are done first (five steps of 512 x 512 98 us with joined pairs, 115 without, 1024
+// x 1024 119 and 196, 1000 x 3001 165 and 221; three waves of joined pairs for X of 1000 x
+// 3001 220).  Times in 1/100 us: a block of 64 k of 256 x bn, a tile's writing and join.
 struct Plan {
     int bn, joined, clusters;
     long long tiles;
@@ -361,8 +363,8 @@ Plan plan(bool lower, int rows, int cols, int k, int dev) {
             const int c = !lower        ? mul_clusters(dev, joined)
                           : joined == 1 ? clusters_max<0, SymEpi>(dev)
                                         : joined_max<0, SymEpi>(dev);
-            if (c <= 0 || joined > kb) continue;
-            const long long block = bn == 256 ? 30 : 20, write = bn == 256 ? 250 : joined == 1 ? 150 : 250;
+            if (c <= 0 || (joined > 1 && (tiles > c || kb < 2))) continue;
+            const long long block = bn == 256 ? 30 : 20, write = bn == 256 ? 250 : joined == 1 ? 150 : 200;
             const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * block + write;
             if (!best.bn || time < least) {
                 best = {bn, joined, c, tiles};

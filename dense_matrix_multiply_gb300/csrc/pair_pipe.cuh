@@ -87,6 +87,13 @@ __device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool
            ((n >> 3) << 17) | ((256u >> 4) << 24);
 }
 
+// An accumulator's columns are in registers (tcgen05.wait::ld has returned) and may be
+// overwritten.  Nothing in memory is handed over, so the arrival is relaxed: one that
+// releases waits for the warp's output on its way to memory, 1700 cycles, and with it the
+// accumulator's next tile (dW of 8 x 32000 x 4096 54 us against 77).
+__device__ __forceinline__ void arrive_read(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // On the barrier at this offset in both CTAs of the pair whose leader is CTA `lead`.
 __device__ __forceinline__ void commit_to_pair(uint64_t *bar, uint32_t lead) {
     asm volatile(
@@ -127,8 +134,11 @@ inline long long lower_tiles(int n, int bn) {
 // of the warps that have no columns to write.
 constexpr int JOIN_QUAD = 128 * 16, JOIN_CHUNK = 8 * JOIN_QUAD, JOIN_AT = EPI_WARPS * STG_BOX;
 static_assert(JOIN_AT + 2 * JOIN_CHUNK <= 2 * EPI_WARPS * STG_BOX, "two boxes a warp");
-__device__ __forceinline__ void st_cluster_f4(uint32_t cluster_addr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+// Four sums to another CTA, counted on a barrier there: the barrier's phase ends when all
+// have arrived, without a fence at the sender.
+__device__ __forceinline__ void send4(uint32_t cluster_addr, const uint32_t *r, uint32_t cluster_bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(cluster_addr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(cluster_bar)
                  : "memory");
 }
 
@@ -260,11 +270,12 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             mbar_init(&bars->acc_full[b], 1);
             mbar_init(&bars->acc_empty[b], 2 * EPI_WARPS);
         }
-        mbar_init(&bars->joined, 4);
+        mbar_init(&bars->joined, 1);
         mbar_init(&bars->drain, 1);
         mbar_init(&bars->peer_done, 1);
         bars->abort = 0;
         mbar_init_fence();
+        if (joined) mbar_arrive_expect_tx(&bars->joined, 2 * JOIN_CHUNK);
         prefetch_desc(&tmA);
         prefetch_desc(&tmB);
     }
@@ -432,20 +443,15 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (joined) {
                 uint8_t *in = staging + JOIN_AT + (quarter * 32 + lane) * 16;
                 if (gives) {
-                    const uint32_t at = map_to_rank(in, cta ^ 2u);
+                    const uint32_t at = map_to_rank(in, cta ^ 2u), bar = map_to_rank(&bars->joined, cta ^ 2u);
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t r[32];
                         tmem_ld32(p.tmem + (uint32_t)(p.first + c * 32), r);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            st_cluster_f4(at + c * JOIN_CHUNK + j * JOIN_QUAD,
-                                          make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
-                                                      __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+                        for (int j = 0; j < 8; ++j) send4(at + c * JOIN_CHUNK + j * JOIN_QUAD, r + 4 * j, bar);
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->joined, cta ^ 2u));  // release: the sums are visible first
                 } else {
                     if (!__all_sync(0xffffffffu, mbar_wait(&bars->joined, 0, abort_flag, true))) {
                         ok = false;
@@ -457,7 +463,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (some && !gives) epi.run(p, pre);
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(&bars->acc_empty[buf], lead));
+            if (lane == 0) arrive_read(map_to_rank(&bars->acc_empty[buf], lead));
             u += nclusters;
             if (u < units) {
                 p.split = u / args.tiles;
@@ -468,6 +474,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (!ok && lane == 0) {
             atomicOr(args.status, ST_EPILOGUE);
             raise_abort_pair(abort_flag, cta);
+            if (joined && !gives) mbar_wait(&bars->joined, 0, abort_flag, false);  // sums that are on their way here
         }
     }
 
