@@ -418,9 +418,13 @@ struct BwdArgs {
 // bytes are under way at all times; loads to registers, waited for row by row, reached
 // half of the rate (8192 x 4096: 72 us against 39).  dw's sums stay in registers: a thread
 // has the same columns of every row.
-constexpr int ctas_per_sm(int wpr) { return wpr <= 4 ? 3 : wpr == 8 ? 2 : 1; }
+// After a wait that gave up: no copy is left in flight when the CTA ends.
+__device__ __noinline__ void drain_copies(uint64_t *full, int stages, int turns, volatile int *abort) {
+    for (int i = max(turns - stages, 0); i < turns; ++i) tc::mbar_wait(&full[i % stages], (uint32_t)((i / stages) & 1), abort, false);
+}
+constexpr int bulk_ctas(int wpr) { return wpr <= 8 ? 2 : 1; }  // an SM
 template <typename T, int WPR>
-__global__ void __launch_bounds__(row_warps(WPR) * 32, ctas_per_sm(WPR))
+__global__ void __launch_bounds__(row_warps(WPR) * 32, bulk_ctas(WPR))
 rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
 {
     constexpr int WARPS = row_warps(WPR), ROWS = WARPS / WPR, MAX_STAGES = 8;
@@ -431,7 +435,7 @@ rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, K = a.K, group = warp / WPR;
     const uint32_t plane = (uint32_t)(ROWS * K * 2), stage_bytes = 3 * plane;
     const bool has_dh = a.dH && a.dX;
-    const long long step = (long long)gridDim.x * ROWS, row00 = (long long)blockIdx.x * ROWS;
+    const uint32_t step = gridDim.x * ROWS, row00 = blockIdx.x * ROWS, M = (uint32_t)a.M;  // (M + 8 steps < 2^32)
     if (threadIdx.x == 0) {
         abort = 0;
         for (int i = 0; i < stages; ++i) tc::mbar_init(&full[i], 1);
@@ -439,16 +443,14 @@ rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
     }
     __syncthreads();
     pdl_wait();
-    long long fetched = 0;
-    auto fetch = [&](long long row0, int stage) {  // one thread
-        if (row0 >= a.M) return;
-        ++fetched;
-        const uint32_t bytes = (uint32_t)min((long long)ROWS, a.M - row0) * (uint32_t)(K * 2);
+    auto fetch = [&](uint32_t row0, int stage) {  // one thread
+        if (row0 >= M) return;
+        const uint32_t bytes = min((uint32_t)ROWS, M - row0) * (uint32_t)(K * 2);
         uint8_t *to = ring + stage * stage_bytes;
         tc::mbar_arrive_expect_tx(&full[stage], bytes * (has_dh ? 3u : 2u));
-        tc::bulk_load(to, a.H + row0 * K, bytes, &full[stage]);
-        tc::bulk_load(to + plane, a.dY + row0 * K, bytes, &full[stage]);
-        if (has_dh) tc::bulk_load(to + 2 * plane, a.dH + row0 * K, bytes, &full[stage]);
+        tc::bulk_load(to, a.H + (long long)row0 * K, bytes, &full[stage]);
+        tc::bulk_load(to + plane, a.dY + (long long)row0 * K, bytes, &full[stage]);
+        if (has_dh) tc::bulk_load(to + 2 * plane, a.dH + (long long)row0 * K, bytes, &full[stage]);
     };
     if (threadIdx.x == 0)
         for (int i = 0; i < stages; ++i) fetch(row00 + i * step, i);
@@ -464,9 +466,9 @@ rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
     float acc[NV][8] = {};
     int stage = 0, flip = 0;
     uint32_t phase = 0;
-    for (long long row0 = row00; row0 < a.M; row0 += step, flip ^= 1) {
-        const long long row = row0 + group;
-        const bool valid = row < a.M;
+    for (uint32_t row0 = row00; row0 < M; row0 += step, flip ^= 1) {
+        const uint32_t row = row0 + group;
+        const bool valid = row < M;
         const float r = valid ? a.rstd[row] : 0.0f;
         if (!tc::mbar_wait(&full[stage], phase, &abort, true)) {  // (the results are then undefined)
             abort = 1;
@@ -512,13 +514,12 @@ rms_norm_backward_bulk_kernel(const BwdArgs a, const int stages, int *status)
                 gains8<T>(a.w != nullptr, KEEP ? w[i] : gain(i), g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d[j] = fmaf(r, fmaf(-f[j] * r, mean, d[j] * g[j]), e[j]);
-                if (valid && k0 + i * STEP < K) *reinterpret_cast<uint4 *>(a.dX + row * K + k0 + i * STEP) = pack8<T>(d);
+                if (valid && k0 + i * STEP < K) *reinterpret_cast<uint4 *>(a.dX + (long long)row * K + k0 + i * STEP) = pack8<T>(d);
             }
         }
     }
-    if (abort && threadIdx.x == 0)  // given up: no copy is left in flight when the CTA ends
-        for (long long i = max(fetched - stages, 0LL); i < fetched; ++i)
-            tc::mbar_wait(&full[i % stages], (uint32_t)((i / stages) & 1), &abort, false);
+    if (abort && threadIdx.x == 0)
+        drain_copies(full, stages, (int)((a.M - blockIdx.x * ROWS + gridDim.x * ROWS - 1) / (gridDim.x * ROWS)), &abort);
     if (!a.part) return;
     float *part = a.part + (long long)blockIdx.x * K;
     if constexpr (ROWS == 1) {
@@ -805,7 +806,7 @@ cudaError_t backward(const NormBackward &p, int num_sms, int *status, cudaStream
     const int wpr = row_split(p.K, kind);
     const int rows = wpr ? row_warps(wpr) / wpr : 1;
     // as many CTAs as stay resident, and partial sums of dw
-    const int per_sm = ctas_per_sm(wpr ? wpr : MAX_WPR);
+    const int per_sm = kind == 0 ? bulk_ctas(wpr ? wpr : MAX_WPR) : wpr <= 4 ? 3 : wpr == 8 ? 2 : 1;
     const long long ctas = std::min<long long>(((long long)p.M + rows - 1) / rows, (long long)num_sms * per_sm);
     const int n = wpr ? (int)ctas : std::min(p.M, 256);
     void *ws = nullptr;

@@ -396,7 +396,7 @@ GEMM_API gemm_status_t gemm_rms_norm_e4m3(gemm_dtype_t dtype, const void *X, con
  *     dw = sum_i dY H rstd
  * dX [M,K] (dtype; may be dH itself), dw FP32 [K], each overwritten; a null one is left
  * out.  Sums in FP32, in a fixed order.  FP32 partials of dw (4 K bytes for each of up to
- * four CTAs an SM) lie in stream-ordered scratch for the duration of the call, from the
+ * three CTAs an SM) lie in stream-ordered scratch for the duration of the call, from the
  * library's pool (see gemm_gated).  M = 0 gives dw = 0.  GEMM_ERR_ALIAS as above. */
 GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H, const void *w, const float *rstd,
                                               const void *dY, const void *dH, void *dX, float *dw, int M, int K);
