@@ -2,7 +2,7 @@
 // gradients, without the logits in memory.
 //
 // Forward: tiles of Z stay in tensor memory; the epilogue takes the largest logit m and
-// s = sum exp(z - m) of each row's 128 columns (online, 32 at a time: s <- s e^(m - m')
+// s = sum exp(z - m) of each row's 64 or 128 columns (online, 32 at a time: s <- s e^(m - m')
 // + sum e^(z - m')), and the row's own target's logit.  A second kernel joins the pairs
 // of a row, in order: lse = m + log s.  All in FP32.
 //
@@ -38,7 +38,7 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 units of 2^-23 off; 0
 
 // Of the columns [c0, c0 + 32) within a row's [0, N), c0 < N: the rest count as -inf.
 struct LseArgs {
-    float2 *part;             // (m, s) of slot column / (bn / 2), [slot][M]
+    float2 *part;             // (m, s) of slot column / width, [slot][M]; width: a warp's columns of a tile
     float *zt;                // Z_i,t_i
     const long long *target;
     int M, N, v0, total;      // rows; columns of this piece, and its first; of Z
@@ -403,11 +403,14 @@ constexpr long long kPiece = 256LL << 20;  // bytes of a piece of dZ, or of a pa
 // How the logits' tiles are cut: few go in 128 columns, and where one wave of them takes
 // joined pairs, a half of K each, if they are done first (forward of 1 x 1000 x 4096 16.6 us
 // against 26.8, 4 x 5000 x 4096 22.6 against 27.0, 1500 x 1500 x 4000 24.6 against 28.7; 1 x
-// 12000 x 4096, three waves of joined pairs, 45.6 against 29.0).  Times in 1/100 us: a block
-// of 64 k of 256 x bn, a join.
+// 12000 x 4096, three waves of joined pairs, 45.6 against 29.0).  Up to 128 rows in tiles of
+// 128 x 256 (128 x 50257 x 1000: 28.7 us, backward 90, against 30.8 and 95; 64 x 32000 x 4096
+// 51.5 and 154 against 53.4 and 158).  Times in 1/100 us: a block of 64 k of rows x bn, a join.
 struct LogitPlan {
-    int bn, joined, clusters;
+    int bn, joined, clusters, rows;
     long long tiles;
+
+    int width() const { return rows == 128 ? bn / 4 : bn / 2; }  // columns of a tile to a warp
 };
 template <uint32_t FORMAT, template <bool> class Epi>
 LogitPlan logit_plan(int M, int N, long long kb, int dev) {
@@ -418,9 +421,10 @@ LogitPlan logit_plan(int M, int N, long long kb, int dev) {
         const int c = joined == 1 ? clusters_max<FORMAT, Epi<false>>(dev) : joined_max<FORMAT, Epi<true>>(dev);
         const long long tiles = ceil_div(M, 256) * ceil_div(N, bn);
         if (c <= 0 || tiles > 0x7FFFFFFFLL || (joined > 1 && (tiles > c || kb < 2))) continue;
-        const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * (bn == 256 ? 28 : 20) + (joined > 1 ? 80 : 0);
+        const int rows = joined > 1 || bn == 128 ? 256 : tile_rows(M);
+        const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * (bn == 128 ? 20 : rows == 128 ? 15 : 28) + (joined > 1 ? 80 : 0);
         if (!best.bn || time < least) {
-            best = {bn, joined, c, tiles};
+            best = {bn, joined, c, rows, tiles};
             least = time;
         }
     }
@@ -437,7 +441,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
     const long long vp = pad_w ? std::min<long long>(up(p.N, 256), std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256)) : p.N;
     const LogitPlan pl = logit_plan<FORMAT, LseEpi>(rows, (int)std::min<long long>(vp, p.N), ceil_div(kp, BK), dev);
     if (!pl.bn) return cudaErrorNotSupported;
-    const int bn = pl.bn, slots = (int)ceil_div(p.N, bn / 2);
+    const int bn = pl.bn, slots = (int)ceil_div(p.N, pl.width());
     Layout l;
     const size_t at_x = l.add(pad_x ? (size_t)rows * kp * 2 : 0), at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0),
                  at_part = l.add((size_t)slots * rows * 8), at_zt = l.add((size_t)rows * 4);
@@ -463,14 +467,14 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             }
             const long long tiles = ceil_div(m, 256) * ceil_div(n, bn);
             CUtensorMap ta, tb;
-            if (tiles > 0x7FFFFFFFLL || !map_operand(&ta, x, FORMAT, false, m, kp, kp, left_rows(m)) ||
+            if (tiles > 0x7FFFFFFFLL || !map_operand(&ta, x, FORMAT, false, m, kp, kp, left_rows(m, pl.rows)) ||
                 !map_operand(&tb, w, FORMAT, false, n, kp, kp, bn / 2)) {
                 e = cudaErrorInvalidValue;
                 break;
             }
             lse.N = n;
             lse.v0 = (int)v0;
-            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, pl.joined, left_rows(m), BK, status};
+            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, pl.joined, left_rows(m, pl.rows), BK, pl.rows, status};
             e = pl.joined > 1 ? launch<FORMAT>(ta, tb, LseEpi<true>{lse}, a, pl.clusters, s)
                               : launch<FORMAT>(ta, tb, LseEpi<false>{lse}, a, pl.clusters, s);
         }
@@ -554,7 +558,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
         CUtensorMap ta, tb;
         {
             DzArgs epi;
-            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, left_rows(p.M)) ||
+            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, left_rows(p.M, pl.rows)) ||
                 !map_operand(&tb, w, FORMAT, false, n, kp, kp, pl.bn / 2) ||
                 !map16(&epi.tm, z, FORMAT, p.M, n, vp, 32, 64)) {
                 e = cudaErrorInvalidValue;
@@ -569,7 +573,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.v0 = (int)v0;
             epi.total = p.N;
             epi.bf16 = bf16;
-            const Args a = {p.M, n, (int)ceil_div(kp, BK), pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, left_rows(p.M), BK, status};
+            const Args a = {p.M, n, (int)ceil_div(kp, BK), pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, left_rows(p.M, pl.rows), BK, pl.rows, status};
             e = pl.joined > 1 ? launch<FORMAT>(ta, tb, DzEpi<true>{epi}, a, pl.clusters, s)
                               : launch<FORMAT>(ta, tb, DzEpi<false>{epi}, a, pl.clusters, s);
         }
@@ -590,12 +594,12 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.M = n;
             epi.N = p.K;
             epi.bf16 = bf16;
-            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, status};
+            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, 256, status};
             e = launch<FORMAT>(ta, tb, epi, a, cw, s);
         }
         if (e == cudaSuccess && p.dX) {
             AccEpi epi;
-            if (!map_operand(&ta, z, FORMAT, false, p.M, n, vp, left_rows(p.M)) || !map_operand(&tb, w, FORMAT, true, kp, n, kp, 0) ||
+            if (!map_operand(&ta, z, FORMAT, false, p.M, n, vp, left_rows(p.M, tile_rows(p.M))) || !map_operand(&tb, w, FORMAT, true, kp, n, kp, 0) ||
                 !make_map3(&epi.tm, base + at_slab, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, ldx * 4,
                            p.M * ldx * 4, 32, 32, 1, 128)) {
                 e = cudaErrorInvalidValue;
@@ -605,7 +609,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.add = v0 > 0;
             // (a short last piece: fewer ranges, each of one block at least)
             const int kb = (int)ceil_div(n, BK);
-            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, left_rows(p.M), BK, status};
+            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, left_rows(p.M, tile_rows(p.M)), BK, tile_rows(p.M), status};
             e = launch<FORMAT>(ta, tb, epi, a, cx, s);
         }
     }

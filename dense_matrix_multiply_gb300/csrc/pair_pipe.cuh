@@ -2,9 +2,9 @@
 // orthogonalised update (orthogonalize.cu): D = A B of 16-bit operands, FP32 sums, whose
 // tiles are handed to an epilogue of the caller's.
 //
-// A 256 x bn tile (bn 64, 128 or 256; 64 only where B lies K-major) belongs to a cluster of two CTAs (tcgen05
-// cta_group::2), 128 rows of A and half of B's columns loaded by each, K in stages of
-// 64.  Either operand may lie K-major (rows of adjacent k) or MN-major (k by k, adjacent
+// A 256 x bn tile (bn 64, 128 or 256; 64 only where B lies K-major) belongs to a cluster of
+// two CTAs (tcgen05 cta_group::2), 128 rows of A and half of B's columns loaded by each, K in
+// stages of 64; up to 128 rows may go in 128 x 256 tiles, 64 of them to a CTA.  Either operand may lie K-major (rows of adjacent k) or MN-major (k by k, adjacent
 // rows or columns), as its tensor map and the flags say.  Warp 0 loads, warp 1 of the
 // leader issues the MMAs -- both converged, one elected lane for the instructions -- and
 // warps 2-9 write out, 32 rows and half of the columns to each.  Two accumulators, so
@@ -62,14 +62,18 @@ struct Args {
     int tiles;
     int splits;      // K ranges of a tile, each a unit of its own
     int joined;      // pairs on a tile: 1, or 2 (bn 128, splits 1, a cluster to each tile)
-    // Rows of A's boxes.  For M <= 128 those that there are, up to eights: the leader's, the
-    // peer loads none (zeros behind the matrix cost a load as much time as its elements: M =
-    // 1, N = 32000, K = 4096 84 us with boxes of 128 rows); what the rows behind them hold
-    // reaches no row of D but theirs.
+    // Rows of A's boxes.  For M up to half of a tile's rows those that there are, up to eights:
+    // the leader's, the peer loads none (zeros behind the matrix cost a load as much time as
+    // its elements: M = 1, N = 32000, K = 4096 84 us with boxes of 128 rows); what the rows
+    // behind them hold reaches no row of D but theirs.
     int a_rows;
     // k that a stage's boxes hold, 64, where both operands lie MN-major and K is less 16, 32
     // or 48 at least as many: the rest of the only block is neither loaded nor multiplied.
     int k_rows;
+    // Rows of a tile: 256, or 128 where M is no more (A K-major, pairs not joined): half the
+    // MMAs' time.  A CTA then has 64 rows, and its accumulator those of the first half of the
+    // columns in tensor-memory lanes 0-63, of the second half in lanes 64-127.
+    int rows;
     int *status;
 };
 
@@ -81,10 +85,10 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// FP32 accumulator, A and B of one 16-bit type (0 f16, 1 bf16), M = 256.
-__device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t n, bool a_mn, bool b_mn) {
+// FP32 accumulator, A and B of one 16-bit type (0 f16, 1 bf16).
+__device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
     return (1u << 4) | (format << 7) | (format << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((n >> 3) << 17) | ((256u >> 4) << 24);
+           ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 // An accumulator's columns are in registers (tcgen05.wait::ld has returned) and may be
@@ -258,7 +262,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     // bytes of a stage that this CTA loads, and its peer
     const uint32_t a_bytes = args.a_mn ? 2u * (uint32_t)args.k_rows * 128u : (uint32_t)args.a_rows * 128u;
     const uint32_t b_bytes = args.b_mn ? (uint32_t)(bn >> 7) * (uint32_t)args.k_rows * 128u : (uint32_t)(bn >> 1) * 128u;
-    const bool few = args.a_rows < 128;
+    const bool few = !args.a_mn && args.M <= args.rows / 2;  // none of the rows are the peer's
     const uint32_t peer_tx = b_bytes + (few ? 0u : a_bytes), stage_tx = a_bytes + b_bytes + peer_tx;
 
     if (threadIdx.x == 0) {
@@ -309,7 +313,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         Tile t = range(cluster, kb0, kb1);
         pdl_wait();
         for (int u = cluster; ok && u < units;) {
-            const int row0 = t.m * 256 + (int)rank * 128, col0 = t.n * bn + (int)rank * (bn >> 1);
+            const int row0 = t.m * 256 + (int)rank * (args.rows >> 1), col0 = t.n * bn + (int)rank * (bn >> 1);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
                 const uint32_t full = map_to_rank(&bars->full[stage], lead);
@@ -370,7 +374,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         // K-major: a K step of 16 is 32 bytes of a 128-byte row.  MN-major: 16 rows of
         // 128 bytes, 64-element boxes BOX64 bytes apart.
         const bool a_mn = args.a_mn != 0, b_mn = args.b_mn != 0;
-        const uint32_t idesc = make_idesc(FORMAT, (uint32_t)bn, a_mn, b_mn);
+        const uint32_t idesc = make_idesc(FORMAT, (uint32_t)args.rows, (uint32_t)bn, a_mn, b_mn);
         const uint64_t a_desc0 = desc_sw128(smem_u32(a_tiles), a_mn ? BOX64 : 16, 1024);
         const uint64_t b_desc0 = desc_sw128(smem_u32(b_tiles), b_mn ? BOX64 : 16, 1024);
         const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
@@ -417,8 +421,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         p.bn = bn;
         p.lane = lane;
         p.box = staging + (joined ? quarter : warp - 2) * Epi::BOXES * STG_BOX;
-        p.first = half * (bn >> 1);
-        p.width = bn >> 1;
+        const bool thin = args.rows == 128;
+        p.first = thin ? (quarter >> 1) * (bn >> 1) + half * (bn >> 2) : half * (bn >> 1);
+        p.width = bn >> (thin ? 2 : 1);
         p.joined = nullptr;
         p.turn = 0;
         int it = 0;
@@ -428,9 +433,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         pdl_wait();
         for (int u = cluster; u < units; ++it) {
             const int buf = it & 1;
-            p.row0 = t.m * 256 + (int)rank * 128 + quarter * 32;
+            p.row0 = t.m * 256 + (thin ? (int)rank * 64 + (quarter & 1) * 32 : (int)rank * 128 + quarter * 32);
             p.col0 = t.n * bn;
-            p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256);
+            p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256 - (thin ? (quarter >> 1) * (bn >> 1) : 0));
             const bool some = p.row0 < args.M;
             typename Epi::Pre pre;
             if (some && !gives) epi.prefetch(p, pre);
@@ -526,10 +531,12 @@ inline bool map16(CUtensorMap *m, const void *p, uint32_t format, long long rows
                   int box_cols) {
     return make_map3(m, p, map_type(format), cols, rows, 1, ld * 2, rows * ld * 2, box_cols, box_rows, 1, 128);
 }
-// left_rows: of the left operand's boxes, K-major.
+// Rows of the tiles, where the caller takes Args::rows of 128, and of the left operand's boxes
+// in tiles of `rows`, K-major.
+inline int tile_rows(long long m) { return m <= 128 ? 128 : 256; }
+inline int left_rows(long long m, int rows) { return m <= rows / 2 ? (int)(m + 7) / 8 * 8 : rows / 2; }
 // An operand of the product from its stored matrix: mn: [K, MN] in k_rows x 64 boxes, else
 // [MN, K] in boxes of `rows` x 64.
-inline int left_rows(long long m) { return m <= 120 ? (int)(m + 7) / 8 * 8 : 128; }
 inline bool map_operand(CUtensorMap *m, const void *p, uint32_t format, bool mn, long long mn_size, long long k, long long ld,
                         int rows, int k_rows = BK) {
     return mn ? map16(m, p, format, k, mn_size, ld, k_rows, 64) : map16(m, p, format, mn_size, k, ld, rows, BK);

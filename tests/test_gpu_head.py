@@ -93,6 +93,13 @@ def test_loss_and_gradients(M, N, K, dtype):
     check(run(dtype, data, M, N, K), data, dtype)
 
 
+@pytest.mark.parametrize("M", [31, 32, 64, 72, 96, 97, 127, 128, 129])
+@pytest.mark.parametrize("N,K", [(257, 520), (21001, 72), (5000, 131)])
+def test_rows_up_to_half_a_tile(M, N, K):
+    data = make(M, N, K, "bf16", M + N, left_out=0.1)
+    check(run("bf16", data, M, N, K), data, "bf16")
+
+
 @pytest.mark.parametrize("M,N,K,off", [(3, 72, 40, 1), (200, 1000, 264, 3)])
 def test_operands_off_16_bytes(M, N, K, off):
     """Every 16-bit operand off an aligned base: the aligned call's bits."""
