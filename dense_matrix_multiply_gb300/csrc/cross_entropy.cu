@@ -2,7 +2,7 @@
 // gradients, without the logits in memory.
 //
 // Forward: tiles of Z stay in tensor memory; the epilogue takes the largest logit m and
-// s = sum exp(z - m) of each row's 64 or 128 columns (online, 32 at a time: s <- s e^(m - m')
+// s = sum exp(z - m) of each row's 64 to 128 columns (online, 32 at a time: s <- s e^(m - m')
 // + sum e^(z - m')), and the row's own target's logit.  A second kernel joins the pairs
 // of a row, in order: lse = m + log s.  All in FP32.
 //
@@ -38,10 +38,11 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 units of 2^-23 off; 0
 
 // Of the columns [c0, c0 + 32) within a row's [0, N), c0 < N: the rest count as -inf.
 struct LseArgs {
-    float2 *part;             // (m, s) of slot column / width, [slot][M]; width: a warp's columns of a tile
+    float2 *part;             // (m, s) of a warp's columns of a tile, [slot][M], slots from slot0 on
     float *zt;                // Z_i,t_i
     const long long *target;
     int M, N, v0, total;      // rows; columns of this piece, and its first; of Z
+    int slot0;
 };
 template <bool JOINED>
 struct LseEpi : LseArgs {
@@ -51,16 +52,15 @@ struct LseEpi : LseArgs {
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
     __device__ __forceinline__ void run(Part &p, const Pre &) const {
-        const int row = p.row0 + p.lane, width = p.width, first = p.col0 + p.first;
-        if (first >= N) return;  // warp-uniform
+        const int row = p.row0 + p.lane, first = p.col0 + p.first, width = min(p.width, N - first);
         long long t = row < M ? target[row] : -1;
         t = t >= 0 && t < total ? t - v0 : -1;
         float m = -INFINITY, s = 0.0f;
 #pragma unroll 1
-        for (int c = 0; c < width && first + c < N; c += 32) {
+        for (int c = 0; c < width; c += 32) {
             uint32_t r[32];
             p.load<JOIN>(p.first + c, r);
-            const int left = N - first - c;
+            const int left = width - c;
             if (left < 32) {  // warp-uniform
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -89,7 +89,7 @@ struct LseEpi : LseArgs {
             s = (s0 + s1) + (s2 + s3);
             m = top;
         }
-        if (row < M) part[(long long)((v0 + first) / width) * M + row] = make_float2(m, s);
+        if (row < M) part[(long long)(slot0 + p.col0 / p.bn * p.ranges + p.range) * M + row] = make_float2(m, s);
     }
 };
 
@@ -405,26 +405,30 @@ constexpr long long kPiece = 256LL << 20;  // bytes of a piece of dZ, or of a pa
 // against 26.8, 4 x 5000 x 4096 22.6 against 27.0, 1500 x 1500 x 4000 24.6 against 28.7; 1 x
 // 12000 x 4096, three waves of joined pairs, 45.6 against 29.0).  Up to 128 rows in tiles of
 // 128 x 256 (128 x 50257 x 1000: 28.7 us, backward 90, against 30.8 and 95; 64 x 32000 x 4096
-// 51.5 and 154 against 53.4 and 158).  Times in 1/100 us: a block of 64 k of rows x bn, a join.
+// 51.5 and 154 against 53.4 and 158).  192 columns where that fills the waves (700 x 9000 x
+// 2000 23.8 us, against 26.9 in 256 and 29.8 in 128; 1000 x 32000 x 512 29.5 against 27.0 in
+// 256).  Times in 1/100 us: a block of 64 k of rows x bn, a join.
 struct LogitPlan {
     int bn, joined, clusters, rows;
     long long tiles;
 
-    int width() const { return rows == 128 ? bn / 4 : bn / 2; }  // columns of a tile to a warp
+    int ranges() const { return rows == 128 ? 4 : 2; }  // of a tile's columns, a warp each
 };
 template <uint32_t FORMAT, template <bool> class Epi>
 LogitPlan logit_plan(int M, int N, long long kb, int dev) {
     LogitPlan best = {};
     long long least = 0;
-    for (int way = 0; way < 3; ++way) {
-        const int bn = way == 0 ? 256 : 128, joined = way == 2 ? 2 : 1;
-        const int c = joined == 1 ? clusters_max<FORMAT, Epi<false>>(dev) : joined_max<FORMAT, Epi<true>>(dev);
-        const long long tiles = ceil_div(M, 256) * ceil_div(N, bn);
-        if (c <= 0 || tiles > 0x7FFFFFFFLL || (joined > 1 && (tiles > c || kb < 2))) continue;
-        const int rows = joined > 1 || bn == 128 ? 256 : tile_rows(M);
-        const long long time = ceil_div(tiles, c) * ceil_div(kb, joined) * (bn == 128 ? 20 : rows == 128 ? 15 : 28) + (joined > 1 ? 80 : 0);
+    constexpr struct {
+        int bn, joined, rows, block;
+    } ways[5] = {{256, 1, 256, 28}, {256, 1, 128, 15}, {192, 1, 256, 24}, {128, 1, 256, 20}, {128, 2, 256, 20}};
+    for (const auto &w : ways) {
+        if (w.rows < 256 && M > w.rows) continue;
+        const int c = w.joined == 1 ? clusters_max<FORMAT, Epi<false>>(dev) : joined_max<FORMAT, Epi<true>>(dev);
+        const long long tiles = ceil_div(M, 256) * ceil_div(N, w.bn);
+        if (c <= 0 || tiles > 0x7FFFFFFFLL || (w.joined > 1 && (tiles > c || kb < 2))) continue;
+        const long long time = ceil_div(tiles, c) * ceil_div(kb, w.joined) * w.block + (w.joined > 1 ? 80 : 0);
         if (!best.bn || time < least) {
-            best = {bn, joined, c, rows, tiles};
+            best = {w.bn, w.joined, c, w.rows, tiles};
             least = time;
         }
     }
@@ -441,7 +445,9 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
     const long long vp = pad_w ? std::min<long long>(up(p.N, 256), std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256)) : p.N;
     const LogitPlan pl = logit_plan<FORMAT, LseEpi>(rows, (int)std::min<long long>(vp, p.N), ceil_div(kp, BK), dev);
     if (!pl.bn) return cudaErrorNotSupported;
-    const int bn = pl.bn, slots = (int)ceil_div(p.N, pl.width());
+    const int bn = pl.bn, piece_slots = (int)ceil_div(std::min<long long>(vp, p.N), bn) * pl.ranges();
+    const long long last = (p.N - 1) / vp;  // piece
+    const int slots = (int)(last * piece_slots + ceil_div(p.N - last * vp, bn) * pl.ranges());
     Layout l;
     const size_t at_x = l.add(pad_x ? (size_t)rows * kp * 2 : 0), at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0),
                  at_part = l.add((size_t)slots * rows * 8), at_zt = l.add((size_t)rows * 4);
@@ -456,7 +462,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             e = copy(x, m, p.K, base + at_x, kp, nullptr, 1, s);
             x = reinterpret_cast<const uint16_t *>(base + at_x);
         }
-        LseArgs lse = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N};
+        LseArgs lse = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N, 0};
         for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
             const int n = (int)std::min<long long>(vp, p.N - v0);
             const uint16_t *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
@@ -474,6 +480,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             }
             lse.N = n;
             lse.v0 = (int)v0;
+            lse.slot0 = (int)(v0 / vp) * piece_slots;
             const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, pl.joined, left_rows(m, pl.rows), BK, pl.rows, status};
             e = pl.joined > 1 ? launch<FORMAT>(ta, tb, LseEpi<true>{lse}, a, pl.clusters, s)
                               : launch<FORMAT>(ta, tb, LseEpi<false>{lse}, a, pl.clusters, s);

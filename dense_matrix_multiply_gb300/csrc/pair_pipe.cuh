@@ -2,7 +2,7 @@
 // orthogonalised update (orthogonalize.cu): D = A B of 16-bit operands, FP32 sums, whose
 // tiles are handed to an epilogue of the caller's.
 //
-// A 256 x bn tile (bn 64, 128 or 256; 64 only where B lies K-major) belongs to a cluster of
+// A 256 x bn tile (bn 128, 192 or 256; 192 only where B lies K-major) belongs to a cluster of
 // two CTAs (tcgen05 cta_group::2), 128 rows of A and half of B's columns loaded by each, K in
 // stages of 64; up to 128 rows may go in 128 x 256 tiles, 64 of them to a CTA.  Either operand may lie K-major (rows of adjacent k) or MN-major (k by k, adjacent
 // rows or columns), as its tensor map and the flags say.  Warp 0 loads, warp 1 of the
@@ -147,11 +147,12 @@ __device__ __forceinline__ void send4(uint32_t cluster_addr, const uint32_t *r, 
 }
 
 // What an epilogue warp sees of a unit: 32 rows of D and columns [first, first + width) of
-// a tile, width a multiple of 32 (of 64 unless bn is 64).
+// a tile, multiples of 64.
 struct Part {
     uint32_t tmem;          // this warp's rows, the tile's first column
     int row0, col0;         // of D: the warp's first row, the tile's first column
     int first, width;
+    int range, ranges;      // these columns are the tile's range-th of so many
     int split;              // which K range
     int bn, lane;
     uint8_t *box;           // STG_BOX bytes of this warp's, once or twice
@@ -422,8 +423,11 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         p.lane = lane;
         p.box = staging + (joined ? quarter : warp - 2) * Epi::BOXES * STG_BOX;
         const bool thin = args.rows == 128;
-        p.first = thin ? (quarter >> 1) * (bn >> 1) + half * (bn >> 2) : half * (bn >> 1);
-        p.width = bn >> (thin ? 2 : 1);
+        const int all = thin ? bn >> 1 : bn, left = (all / 2 + 63) & ~63;
+        p.range = thin ? (quarter >> 1) * 2 + half : half;
+        p.ranges = thin ? 4 : 2;
+        p.first = (p.range >> 1) * all + half * left;
+        p.width = half ? all - left : left;
         p.joined = nullptr;
         p.turn = 0;
         int it = 0;
