@@ -229,59 +229,48 @@ struct MaxSum {
         if (lse) *lse = l;
     }
 };
-// Joins the slots of many rows: 32 rows to a CTA, slots dealt to its 32 warps.
+// Joins the slots.  ROWS to a CTA: 8 (of a slot 64 adjacent bytes, two whole sectors), slots
+// dealt to 128 lanes of each, or, of few rows, 1 -- a row's joins are a chain of latencies
+// (forward of 200 x 50257 x 64 12.5 us, against 14.9 with 256 threads to a row; 65 x 50257 x 64 11.0, against
+// 12.3 with 8).
+template <int ROWS>
 __global__ void __launch_bounds__(1024)
 head_join_kernel(const float2 *__restrict__ part, const float *__restrict__ zt, const long long *__restrict__ target,
                  float *__restrict__ loss, float *__restrict__ lse, int slots, int M, int N)
 {
-    __shared__ float2 mine[32][32];
+    __shared__ float2 mine[32][ROWS];
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long row = blockIdx.x * 32LL + lane;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane % ROWS;
+    const long long row = (long long)blockIdx.x * ROWS + r;
     MaxSum v;
     if (row < M) {
-#pragma unroll 8
-        for (int i = warp; i < slots; i += 32) {
+#pragma unroll 4
+        for (int i = threadIdx.x / ROWS; i < slots; i += 1024 / ROWS) {
             const float2 p = __ldcg(part + (long long)i * M + row);
             v.join(p.x, p.y);
         }
     }
-    mine[warp][lane] = make_float2(v.m, v.s);
+    auto fold = [&] {  // the lanes of a row
+#pragma unroll
+        for (int o = 16; o >= ROWS; o >>= 1) {
+            const float om = __shfl_down_sync(0xffffffffu, v.m, o), os = __shfl_down_sync(0xffffffffu, v.s, o);
+            v.join(om, os);
+        }
+    };
+    fold();
+    if (lane < ROWS) mine[warp][r] = make_float2(v.m, v.s);
     __syncthreads();
-    if (warp != 0 || row >= M) return;
-    for (int w = 1; w < 32; ++w) v.join(mine[w][lane].x, mine[w][lane].y);
-    v.store(zt[row], target[row], N, loss + row, lse ? lse + row : nullptr);
-}
-// The same of few rows, a CTA to a row: a row's joins are a chain of latencies (1 x 32000:
-// 250 slots), which 256 threads and five steps of shuffles keep short
-// (53.5 us against 55.3).
-constexpr int kJoinRows = 256;
-__global__ void __launch_bounds__(256)
-head_join_row_kernel(const float2 *__restrict__ part, const float *__restrict__ zt, const long long *__restrict__ target,
-                     float *__restrict__ loss, float *__restrict__ lse, int slots, int M, int N)
-{
-    __shared__ float2 mine[8];
-    pdl_wait();
-    const int row = blockIdx.x;
-    MaxSum v;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < slots; i += 256) {
-        const float2 p = __ldcg(part + (long long)i * M + row);
+    if (warp != 0) return;
+    const float z = lane < ROWS && row < M ? zt[row] : 0.0f;
+    const long long t = lane < ROWS && row < M ? target[row] : -1;
+    v = MaxSum{};
+#pragma unroll
+    for (int w = 0; w < ROWS; ++w) {
+        const float2 p = mine[lane / ROWS * ROWS + w][r];
         v.join(p.x, p.y);
     }
-    const float z = threadIdx.x == 0 ? zt[row] : 0.0f;
-    const long long t = threadIdx.x == 0 ? target[row] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float om = __shfl_down_sync(0xffffffffu, v.m, o), os = __shfl_down_sync(0xffffffffu, v.s, o);
-        v.join(om, os);
-    }
-    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = make_float2(v.m, v.s);
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-#pragma unroll
-    for (int w = 1; w < 8; ++w) v.join(mine[w].x, mine[w].y);
-    v.store(z, t, N, loss + row, lse ? lse + row : nullptr);
+    fold();
+    if (lane < ROWS && row < M) v.store(z, t, N, loss + row, lse ? lse + row : nullptr);
 }
 
 __global__ void __launch_bounds__(256)
@@ -487,9 +476,9 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
         }
         if (e != cudaSuccess) break;
         cudaLaunchAttribute attr[1];
-        const cudaLaunchConfig_t cfg = m <= kJoinRows ? pdl_config(dim3((unsigned)m), dim3(256), 0, s, attr)
-                                                      : pdl_config(dim3((unsigned)ceil_div(m, 32)), dim3(1024), 0, s, attr);
-        e = launch_counted(&cfg, m <= kJoinRows ? head_join_row_kernel : head_join_kernel, static_cast<const float2 *>(lse.part), static_cast<const float *>(lse.zt),
+        const bool few = m <= 128;  // (one to an SM)
+        const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)(few ? m : ceil_div(m, 8))), dim3(1024), 0, s, attr);
+        e = launch_counted(&cfg, few ? head_join_kernel<1> : head_join_kernel<8>, static_cast<const float2 *>(lse.part), static_cast<const float *>(lse.zt),
                            lse.target, p.loss + r0, p.lse ? p.lse + r0 : nullptr, slots, m, p.N);
     }
     const cudaError_t f = cudaFreeAsync(ws, s);
