@@ -285,15 +285,58 @@ head_flat_kernel(const long long *__restrict__ target, float *__restrict__ loss,
     if (lse) lse[row] = l;
 }
 
+// Half precision: the power of two that takes the largest |dloss| of a row with a target
+// to [2^14, 2^15), so that dZ, at most as large, keeps half's full precision down to
+// probabilities of 2^-28; and its inverse.  By a CTA.
+struct ScaleArgs {
+    const float *dloss;
+    const long long *target;
+    float2 *scale;
+    int M, N;
+};
+template <int THREADS>
+__device__ __forceinline__ void find_scale(const ScaleArgs &a) {
+    __shared__ float tops[THREADS / 32];
+    float top = 0.0f;
+#pragma unroll 4
+    for (long long i = threadIdx.x; i < a.M; i += THREADS) {
+        const long long t = a.target[i];
+        const float d = fabsf(a.dloss[i]);
+        if (t >= 0 && t < a.N) top = fmaxf(top, d);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < THREADS / 32; ++w) top = fmaxf(top, tops[w]);
+    int e = 0;
+    if (top > 0.0f && isfinite(top)) {
+        frexpf(top, &e);
+        e = max(min(15 - e, 126), -126);
+    }
+    *a.scale = make_float2(ldexpf(1.0f, e), ldexpf(1.0f, -e));
+}
+__global__ void __launch_bounds__(1024)
+head_scale_kernel(const ScaleArgs a)
+{
+    pdl_wait();
+    find_scale<1024>(a);
+}
+
 // dst [rows, dst_cols] (rows of whole 16 bytes) = src [rows, cols] (any 2 bytes), zeros
 // behind the row and, where targets are given, in rows whose target is no column of N: a
-// lane two 16-byte pieces (fp4.h).
+// lane two 16-byte pieces (fp4.h).  A scale to find is one more CTA's.
 constexpr int COPY_WARPS = 4;
 __global__ void __launch_bounds__(COPY_WARPS * 32)
 head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long cols, uint16_t *__restrict__ dst,
-                 long long dst_cols, const long long *__restrict__ target, int N)
+                 long long dst_cols, const long long *__restrict__ target, int N, const ScaleArgs a)
 {
     pdl_wait();
+    if (a.scale && blockIdx.x == gridDim.x - 1) {
+        if (blockIdx.y == 0) find_scale<COPY_WARPS * 32>(a);
+        return;
+    }
     const long long row = (long long)blockIdx.x * COPY_WARPS + (threadIdx.x >> 5);
     if (row >= rows) return;  // warp-uniform
     const int lane = threadIdx.x & 31;
@@ -310,39 +353,12 @@ head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long col
     }
 }
 cudaError_t copy(const void *src, long long rows, long long cols, void *dst, long long dst_cols, const long long *target,
-                 int N, cudaStream_t s) {
-    const long long gx = (rows + COPY_WARPS - 1) / COPY_WARPS, gy = std::min<long long>((dst_cols + 511) / 512, 65535);
+                 int N, const ScaleArgs &scale, cudaStream_t s) {
+    const long long gx = (rows + COPY_WARPS - 1) / COPY_WARPS + (scale.scale ? 1 : 0), gy = std::min<long long>((dst_cols + 511) / 512, 65535);
     cudaLaunchAttribute attr[1];
     const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)gx, (unsigned)gy), dim3(COPY_WARPS * 32), 0, s, attr);
     return launch_counted(&cfg, head_copy_kernel, static_cast<const uint16_t *>(src), rows, cols, static_cast<uint16_t *>(dst),
-                          dst_cols, target, N);
-}
-
-// Half precision: the power of two that takes the largest |dloss| of a row with a target
-// to [2^14, 2^15), so that dZ, at most as large, keeps half's full precision down to
-// probabilities of 2^-28; and its inverse.
-__global__ void __launch_bounds__(1024)
-head_scale_kernel(const float *__restrict__ dloss, const long long *__restrict__ target, float2 *scale, int M, int N)
-{
-    __shared__ float tops[32];
-    pdl_wait();
-    float top = 0.0f;
-    for (long long i = threadIdx.x; i < M; i += 1024) {
-        const long long t = target[i];
-        if (t >= 0 && t < N) top = fmaxf(top, fabsf(dloss[i]));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
-    __syncthreads();
-    if (threadIdx.x != 0) return;
-    for (int w = 1; w < 32; ++w) top = fmaxf(top, tops[w]);
-    int e = 0;
-    if (top > 0.0f && isfinite(top)) {
-        frexpf(top, &e);
-        e = max(min(15 - e, 126), -126);
-    }
-    *scale = make_float2(ldexpf(1.0f, e), ldexpf(1.0f, -e));
+                          dst_cols, target, N, scale);
 }
 
 // dX = (sum of the slabs, in order) scale->y, four elements to a thread.
@@ -448,7 +464,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
         const int m = (int)std::min<long long>(rows, p.M - r0);
         const uint16_t *x = static_cast<const uint16_t *>(p.X) + r0 * p.K;
         if (pad_x) {
-            e = copy(x, m, p.K, base + at_x, kp, nullptr, 1, s);
+            e = copy(x, m, p.K, base + at_x, kp, nullptr, 1, {}, s);
             x = reinterpret_cast<const uint16_t *>(base + at_x);
         }
         LseArgs lse = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N, 0};
@@ -456,7 +472,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             const int n = (int)std::min<long long>(vp, p.N - v0);
             const uint16_t *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
             if (pad_w) {
-                e = copy(w, n, p.K, base + at_w, kp, nullptr, 1, s);
+                e = copy(w, n, p.K, base + at_w, kp, nullptr, 1, {}, s);
                 if (e != cudaSuccess) break;
                 w = reinterpret_cast<const uint16_t *>(base + at_w);
             }
@@ -524,23 +540,26 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
     if (e != cudaSuccess) return e;
     uint8_t *base = static_cast<uint8_t *>(ws);
     cudaLaunchAttribute attr[1];
-    const float2 *scale = nullptr;
     const bool bf16 = FORMAT == 1;
-    if (!bf16) {
-        scale = reinterpret_cast<const float2 *>(base + at_scale);
+    ScaleArgs find = {};
+    if (!bf16) find = {p.dloss, p.target, reinterpret_cast<float2 *>(base + at_scale), p.M, p.N};
+    const float2 *scale = find.scale;
+    // X's copy finds the scale of few rows (a launch less: 1.3 us)
+    if (!bf16 && (!copy_x || p.M > 1024)) {
         const cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(1024), 0, s, attr);
-        e = launch_counted(&cfg, head_scale_kernel, p.dloss, p.target, reinterpret_cast<float2 *>(base + at_scale), p.M, p.N);
+        e = launch_counted(&cfg, head_scale_kernel, find);
+        find = {};
     }
     const void *x = p.X;
     if (e == cudaSuccess && copy_x) {
-        e = copy(p.X, p.M, p.K, base + at_x, kp, p.dW ? p.target : nullptr, p.dW ? p.N : 1, s);
+        e = copy(p.X, p.M, p.K, base + at_x, kp, p.dW ? p.target : nullptr, p.dW ? p.N : 1, find, s);
         x = base + at_x;
     }
     for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
         const int n = (int)std::min<long long>(vp, p.N - v0);
         const void *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
         if (pad_w) {
-            e = copy(w, n, p.K, base + at_w, kp, nullptr, 1, s);
+            e = copy(w, n, p.K, base + at_w, kp, nullptr, 1, {}, s);
             if (e != cudaSuccess) break;
             w = base + at_w;
         }
