@@ -118,7 +118,7 @@ struct ProblemEx {
     Elt elt;
 };
 
-// Stream-ordered scratch of the 4-bit and gated operators, from a pool of the
+// Stream-ordered scratch of the operators from the 4-bit ones on, from a pool of the
 // library's own on the current device (scratch.h).  Free with cudaFreeAsync on the
 // same stream.
 cudaError_t scratch_alloc(void **p, size_t bytes, cudaStream_t s);

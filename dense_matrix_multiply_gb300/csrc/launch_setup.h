@@ -1,4 +1,4 @@
-// What the launches of the 4-bit and gated kernels look up once and keep (host code):
+// What the launches of the 4-bit, gated, norm, head and update kernels look up once and keep (host code):
 // the driver's encoder of TMA descriptors, and how many clusters of a kernel fit the
 // device.  Only answers are kept: a look-up that failed is made again by the next call,
 // and leaves nothing in the runtime's last error.

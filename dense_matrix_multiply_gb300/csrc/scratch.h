@@ -1,4 +1,4 @@
-// Stream-ordered scratch of the 4-bit and gated operators (host code).
+// Stream-ordered scratch of the 4-bit, gated, norm, head and update operators (host code).
 #pragma once
 
 #include <cuda_runtime.h>

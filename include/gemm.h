@@ -29,8 +29,8 @@
  * leave a nearly empty last wave (at most a quarter of the clusters busy, K of
  * at least 48 blocks of 64) takes FP32 partial tiles for its stream-K tail from
  * the same pool (512 KiB per participating CTA pair, at most ~39 MB), freed on
- * the stream after the call; without it the call runs whole tiles.  The FP8, 4-bit
- * and gated entry points name their scratch below.  The allocation-free entry point
+ * the stream after the call; without it the call runs whole tiles.  The other entry
+ * points' scratch is named below, with them.  The allocation-free entry point
  * never allocates.
  *
  * Leading dimensions are tight:
@@ -51,11 +51,13 @@
  * of tiles is at most half full launches two grids; the second reads A and B
  * while the first still runs, and completes only after it; so do the two
  * products of gemm_gated_backward.)  A call launches one to five kernels, or
- * more for a general-form batch beyond 65535 matrices and for a gated block's
- * operands that are padded;
+ * more for a general-form batch beyond 65535 matrices, for a gated block's
+ * operands that are padded, for each piece of a head's vocabulary and each step of
+ * gemm_orthogonalize (three);
  * gemm_kernel_launches() counts them.  Calls may be captured into CUDA
  * graphs.  Results are deterministic: the same inputs give bit-identical C on
- * every run (no atomics, fixed summation order per element).
+ * every run (no atomics, fixed summation order per element; a head's dX grows by
+ * one addition to an element a launch, in stream order).
  *
  * Errors.  Every entry point returns a status; nothing is thrown across the ABI.
  *   GEMM_ERR_INVALID_VALUE      a dimension < 0, or a null pointer needed by the
@@ -372,8 +374,8 @@ GEMM_API gemm_status_t gemm_gated_backward(gemm_dtype_t dtype, gemm_act_t act, c
  * with R given: the sum is not stored.  H may be X or R itself (the residual stream
  * updated in place).  rstd (null: not stored): FP32 [M], for gemm_rms_norm_backward.
  * eps: a normal number below 2^30 (GEMM_ERR_INVALID_VALUE otherwise).  Any M and K: one
- * token to a long prompt; rows up to 16384 elements are read once.  Operands whose bases
- * lie alike to 16 bytes are fastest (any K).  Rows of bf16 whose squares overflow FP32
+ * token to a long prompt.  Where the operands' bases lie alike to 16 bytes (any K), rows
+ * of up to 16384 elements are read once, else twice.  Rows of bf16 whose squares overflow FP32
  * are summed again, scaled down; a NaN or an infinity in a row reaches that row alone.
  * M = 0 or K = 0: nothing is written.  GEMM_ERR_ALIAS if any other output overlaps an
  * input or another output. */
@@ -498,7 +500,8 @@ GEMM_API const char *gemm_last_error(void);
  * after loading one stage while the first has loaded further, so that the pair
  * ends with loads of only one CTA outstanding.  gemm_bf16_rm_noalloc
  * honours "umma_stall" (recording in its static status word) and ignores the
- * other families; the FP8, 4-bit and gated entry points ignore them all. */
+ * other families; the FP8, 4-bit, gated, norm, head and update entry points ignore
+ * them all. */
 GEMM_API gemm_status_t gemm_force_kernel(const char *family);
 
 #ifdef __cplusplus
