@@ -42,19 +42,25 @@ struct LseArgs {
     float *zt;                // Z_i,t_i
     const long long *target;
     int M, N, v0, total;      // rows; columns of this piece, and its first; of Z
-    int slot0;
+    int slot0, classes;
 };
-template <bool JOINED>
+template <bool JOINED, bool OF_CLASSES>
 struct LseEpi : LseArgs {
-    static constexpr bool LOWER = false, JOIN = JOINED;
+    static constexpr bool LOWER = false, JOIN = JOINED, CLASSES = OF_CLASSES;
     static constexpr int BOXES = JOINED ? 2 : 1;
 
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
     __device__ __forceinline__ void run(Part &p, const Pre &) const {
-        const int row = p.row0 + p.lane, first = p.col0 + p.first, width = min(p.width, N - first);
+        const int row = p.row0 + p.lane, first = p.col0 + p.first;
         long long t = row < M ? target[row] : -1;
         t = t >= 0 && t < total ? t - v0 : -1;
+        int cols = N;
+        if (CLASSES) {  // columns cls, cls + classes, ... of N
+            cols = (N - p.cls + classes - 1) / classes;
+            t = t >= 0 && (int)t % classes == p.cls ? (int)t / classes : -1;
+        }
+        const int width = min(p.width, cols - first);
         float m = -INFINITY, s = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < width; c += 32) {
@@ -89,7 +95,7 @@ struct LseEpi : LseArgs {
             s = (s0 + s1) + (s2 + s3);
             m = top;
         }
-        if (row < M) part[(long long)(slot0 + p.col0 / p.bn * p.ranges + p.range) * M + row] = make_float2(m, s);
+        if (row < M) part[(long long)(slot0 + p.tile_n * p.ranges + p.range) * M + row] = make_float2(m, s);
     }
 };
 
@@ -102,9 +108,9 @@ struct DzArgs {
     int M, N, v0, total;  // total: columns of Z
     bool bf16;
 };
-template <bool JOINED>
+template <bool JOINED, bool OF_CLASSES>
 struct DzEpi : DzArgs {
-    static constexpr bool LOWER = false, JOIN = JOINED;
+    static constexpr bool LOWER = false, JOIN = JOINED, CLASSES = false;
     static constexpr int BOXES = JOINED ? 2 : 1;
 
     struct Pre {};
@@ -149,7 +155,7 @@ struct DzEpi : DzArgs {
 
 // FP32 sums to slab `split`, or added to it.
 struct AccEpi {
-    static constexpr bool LOWER = false, JOIN = false;
+    static constexpr bool LOWER = false, JOIN = false, CLASSES = false;
     static constexpr int BOXES = 1;
     CUtensorMap tm;
     int N;
@@ -178,7 +184,7 @@ struct AccEpi {
 
 // 16-bit results times scale->y.
 struct OutEpi {
-    static constexpr bool LOWER = false, JOIN = false;
+    static constexpr bool LOWER = false, JOIN = false, CLASSES = false;
     static constexpr int BOXES = 2;
     CUtensorMap tm;
     const float2 *scale;  // null: 1
@@ -326,11 +332,12 @@ head_scale_kernel(const ScaleArgs a)
 
 // dst [rows, dst_cols] (rows of whole 16 bytes) = src [rows, cols] (any 2 bytes), zeros
 // behind the row and, where targets are given, in rows whose target is no column of N: a
-// lane two 16-byte pieces (fp4.h).  A scale to find is one more CTA's.
+// lane two 16-byte pieces (fp4.h).  A scale to find is one more CTA's.  Of classes: matrix z
+// of dst has its rows behind as many zeros as the z-th four bits of `shifts` say, 7 at most.
 constexpr int COPY_WARPS = 4;
 __global__ void __launch_bounds__(COPY_WARPS * 32)
 head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long cols, uint16_t *__restrict__ dst,
-                 long long dst_cols, const long long *__restrict__ target, int N, const ScaleArgs a)
+                 long long dst_cols, const long long *__restrict__ target, int N, uint32_t shifts, const ScaleArgs a)
 {
     pdl_wait();
     if (a.scale && blockIdx.x == gridDim.x - 1) {
@@ -343,22 +350,27 @@ head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long col
     const long long t = target ? target[row] : 0;
     const long long width = t >= 0 && t < N ? cols : -1024;
     const uint8_t *lo = reinterpret_cast<const uint8_t *>(src), *hi = reinterpret_cast<const uint8_t *>(src + rows * cols);
-    uint16_t *d = dst + row * dst_cols;
+    uint16_t *d = dst + (blockIdx.z * rows + row) * dst_cols;
+    const int front = shifts >> (4 * blockIdx.z) & 7;
     for (long long k0 = blockIdx.y * 512LL; k0 < dst_cols; k0 += gridDim.y * 512LL) {
         const long long k = k0 + lane * 16;
         uint32_t v[8];
-        fp4_load16_any(src + row * cols + k, (int)max(min(width - k, 512LL), -512LL), lo, hi, v);
+        fp4_load16_any(src + row * cols + k - front, (int)max(min(width + front - k, 512LL), -512LL), lo, hi, v);
+        if (k == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] &= (2 * j < front ? 0u : 0xFFFFu) | (2 * j + 1 < front ? 0u : 0xFFFF0000u);
+        }
         if (k < dst_cols) *reinterpret_cast<uint4 *>(d + k) = make_uint4(v[0], v[1], v[2], v[3]);
         if (k + 8 < dst_cols) *reinterpret_cast<uint4 *>(d + k + 8) = make_uint4(v[4], v[5], v[6], v[7]);
     }
 }
 cudaError_t copy(const void *src, long long rows, long long cols, void *dst, long long dst_cols, const long long *target,
-                 int N, const ScaleArgs &scale, cudaStream_t s) {
+                 int N, const ScaleArgs &scale, cudaStream_t s, int classes = 1, uint32_t shifts = 0) {
     const long long gx = (rows + COPY_WARPS - 1) / COPY_WARPS + (scale.scale ? 1 : 0), gy = std::min<long long>((dst_cols + 511) / 512, 65535);
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)gx, (unsigned)gy), dim3(COPY_WARPS * 32), 0, s, attr);
+    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)gx, (unsigned)gy, (unsigned)classes), dim3(COPY_WARPS * 32), 0, s, attr);
     return launch_counted(&cfg, head_copy_kernel, static_cast<const uint16_t *>(src), rows, cols, static_cast<uint16_t *>(dst),
-                          dst_cols, target, N, scale);
+                          dst_cols, target, N, shifts, scale);
 }
 
 // dX = (sum of the slabs, in order) scale->y, four elements to a thread.
@@ -419,8 +431,8 @@ struct LogitPlan {
 
     int ranges() const { return rows == 128 ? 4 : 2; }  // of a tile's columns, a warp each
 };
-template <uint32_t FORMAT, template <bool> class Epi>
-LogitPlan logit_plan(int M, int N, long long kb, int dev) {
+template <uint32_t FORMAT, template <bool, bool> class Epi, bool CLASSES>
+LogitPlan logit_plan(int M, int N, long long kb, int classes, int dev) {
     LogitPlan best = {};
     long long least = 0;
     constexpr struct {
@@ -428,8 +440,8 @@ LogitPlan logit_plan(int M, int N, long long kb, int dev) {
     } ways[5] = {{256, 1, 256, 28}, {256, 1, 128, 15}, {192, 1, 256, 24}, {128, 1, 256, 20}, {128, 2, 256, 20}};
     for (const auto &w : ways) {
         if (w.rows < 256 && M > w.rows) continue;
-        const int c = w.joined == 1 ? clusters_max<FORMAT, Epi<false>>(dev) : joined_max<FORMAT, Epi<true>>(dev);
-        const long long tiles = ceil_div(M, 256) * ceil_div(N, w.bn);
+        const int c = w.joined == 1 ? clusters_max<FORMAT, Epi<false, CLASSES>>(dev) : joined_max<FORMAT, Epi<true, CLASSES>>(dev);
+        const long long tiles = ceil_div(M, 256) * ceil_div(ceil_div(N, classes), w.bn) * classes;
         if (c <= 0 || tiles > 0x7FFFFFFFLL || (w.joined > 1 && (tiles > c || kb < 2))) continue;
         const long long time = ceil_div(tiles, c) * ceil_div(kb, w.joined) * w.block + (w.joined > 1 ? 80 : 0);
         if (!best.bn || time < least) {
@@ -440,22 +452,57 @@ LogitPlan logit_plan(int M, int N, long long kb, int dev) {
     return best;
 }
 
+// W read in place where its rows lie off 16 bytes (pair_pipe.cuh), of K elements from w on: its
+// classes and their shifts.
+struct Classes {
+    int n;
+    uint32_t shifts;
+
+    Classes(const void *w, int K) : n(1), shifts(0) {
+        while (n * (K % 8) % 8) n *= 2;
+        for (int r = 0; r < n; ++r) shifts |= (uint32_t)(((uintptr_t)w / 2 + (uintptr_t)r * (K % 8)) % 8) << (4 * r);
+    }
+    int shift(int r) const { return (int)(shifts >> (4 * r) & 7); }
+    // Class r of N rows, K-major.
+    bool map(CUtensorMap *m, const void *w, uint32_t format, int N, long long K, int r, int box_rows) const {
+        const int s = shift(r);
+        return map16(m, static_cast<const uint16_t *>(w) + r * K - s, format, (N - r + n - 1) / n, K + s, n * K, box_rows, BK);
+    }
+};
+
+template <uint32_t FORMAT, bool CLASSES>
+cudaError_t launch_lse(const CUtensorMap &ta, const BMaps<CLASSES> &tb, const LseArgs &lse, const Args &a, int clusters, cudaStream_t s) {
+    return a.joined > 1 ? launch<FORMAT>(ta, tb, LseEpi<true, CLASSES>{lse}, a, clusters, s)
+                        : launch<FORMAT>(ta, tb, LseEpi<false, CLASSES>{lse}, a, clusters, s);
+}
+
 template <uint32_t FORMAT>
 cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) {
     const bool aligned = p.K % 8 == 0;
-    const bool pad_x = !aligned || !on16(p.X), pad_w = !aligned || !on16(p.W);
-    const long long kp = aligned ? p.K : up(p.K, 64);
     const int rows_max = 16384;
     const int rows = std::min(p.M, rows_max);
+    const bool off_w = !aligned || !on16(p.W);
+    const Classes cl(p.W, p.K);
+    // W in place costs a copy of X for each class and a pause of the MMAs for the zeros in front
+    // of each tile, W's copy twice its reading and writing (22 x 60179 x 951 36 us against 71,
+    // 1000 x 50000 x 2001 148 against 188; 3000 x 60000 x 701 225 against 180, 1000 x 8000 x
+    // 2001 43 against 39)
+    const bool classes = cl.n > 1 && p.N <= 1 << 30 && 4LL * cl.n * rows <= p.N;
+    const bool pad_w = off_w && !classes, pad_x = classes || !aligned || !on16(p.X);
+    const long long kp = classes ? up(p.K + 7LL, 64) : aligned ? p.K : up(p.K, 64);
     const long long vp = pad_w ? std::min<long long>(up(p.N, 256), std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256)) : p.N;
-    const LogitPlan pl = logit_plan<FORMAT, LseEpi>(rows, (int)std::min<long long>(vp, p.N), ceil_div(kp, BK), dev);
+    const int vn = (int)std::min<long long>(vp, p.N), num_kb = (int)ceil_div(kp, BK);
+    const LogitPlan pl = classes ? logit_plan<FORMAT, LseEpi, true>(rows, vn, num_kb, cl.n, dev)
+                                 : logit_plan<FORMAT, LseEpi, false>(rows, vn, num_kb, 1, dev);
     if (!pl.bn) return cudaErrorNotSupported;
-    const int bn = pl.bn, piece_slots = (int)ceil_div(std::min<long long>(vp, p.N), bn) * pl.ranges();
+    const int bn = pl.bn, class_tiles = (int)ceil_div(ceil_div(vn, classes ? cl.n : 1), bn),
+              piece_slots = class_tiles * (classes ? cl.n : 1) * pl.ranges();
     const long long last = (p.N - 1) / vp;  // piece
-    const int slots = (int)(last * piece_slots + ceil_div(p.N - last * vp, bn) * pl.ranges());
+    const int slots = classes ? piece_slots : (int)(last * piece_slots + ceil_div(p.N - last * vp, bn) * pl.ranges());
     Layout l;
-    const size_t at_x = l.add(pad_x ? (size_t)rows * kp * 2 : 0), at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0),
-                 at_part = l.add((size_t)slots * rows * 8), at_zt = l.add((size_t)rows * 4);
+    const size_t at_x = l.add(pad_x ? (size_t)(classes ? cl.n : 1) * rows * kp * 2 : 0),
+                 at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0), at_part = l.add((size_t)slots * rows * 8),
+                 at_zt = l.add((size_t)rows * 4);
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(&ws, l.bytes, s);
     if (e != cudaSuccess) return e;
@@ -464,10 +511,11 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
         const int m = (int)std::min<long long>(rows, p.M - r0);
         const uint16_t *x = static_cast<const uint16_t *>(p.X) + r0 * p.K;
         if (pad_x) {
-            e = copy(x, m, p.K, base + at_x, kp, nullptr, 1, {}, s);
+            e = copy(x, m, p.K, base + at_x, kp, nullptr, 1, {}, s, classes ? cl.n : 1, classes ? cl.shifts : 0);
             x = reinterpret_cast<const uint16_t *>(base + at_x);
         }
-        LseArgs lse = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N, 0};
+        LseArgs lse = {reinterpret_cast<float2 *>(base + at_part), reinterpret_cast<float *>(base + at_zt), p.target + r0, m, 0, 0, p.N, 0, cl.n};
+        const int box = left_rows(m, pl.rows);
         for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
             const int n = (int)std::min<long long>(vp, p.N - v0);
             const uint16_t *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
@@ -476,19 +524,25 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
                 if (e != cudaSuccess) break;
                 w = reinterpret_cast<const uint16_t *>(base + at_w);
             }
-            const long long tiles = ceil_div(m, 256) * ceil_div(n, bn);
-            CUtensorMap ta, tb;
-            if (tiles > 0x7FFFFFFFLL || !map_operand(&ta, x, FORMAT, false, m, kp, kp, left_rows(m, pl.rows)) ||
-                !map_operand(&tb, w, FORMAT, false, n, kp, kp, bn / 2)) {
-                e = cudaErrorInvalidValue;
-                break;
-            }
             lse.N = n;
             lse.v0 = (int)v0;
             lse.slot0 = (int)(v0 / vp) * piece_slots;
-            const Args a = {m, n, (int)ceil_div(kp, BK), bn, 0, 0, (int)tiles, 1, pl.joined, left_rows(m, pl.rows), BK, pl.rows, status};
-            e = pl.joined > 1 ? launch<FORMAT>(ta, tb, LseEpi<true>{lse}, a, pl.clusters, s)
-                              : launch<FORMAT>(ta, tb, LseEpi<false>{lse}, a, pl.clusters, s);
+            const int n_tiles = classes ? class_tiles * cl.n : (int)ceil_div(n, bn);
+            const long long tiles = ceil_div(m, 256) * n_tiles;
+            const Args a = {m, classes ? n_tiles * bn : n, num_kb, bn, 0, 0, (int)tiles, 1, pl.joined, box, BK, pl.rows, cl.n, class_tiles,
+                            cl.shifts, status};
+            CUtensorMap ta;
+            bool ok = tiles <= 0x7FFFFFFFLL;
+            if (classes) {
+                BMaps<true> tb = {};
+                ok = ok && make_map3(&ta, x, map_type(FORMAT), kp, m, cl.n, kp * 2, m * kp * 2, BK, box, 1, 128);
+                for (int r = 0; r < cl.n; ++r) ok = ok && cl.map(&tb.m[r], w, FORMAT, n, p.K, r, bn / 2);
+                e = ok ? launch_lse<FORMAT, true>(ta, tb, lse, a, pl.clusters, s) : cudaErrorInvalidValue;
+            } else {
+                BMaps<false> tb;
+                ok = ok && map_operand(&ta, x, FORMAT, false, m, kp, kp, box) && map_operand(&tb.m[0], w, FORMAT, false, n, kp, kp, bn / 2);
+                e = ok ? launch_lse<FORMAT, false>(ta, tb, lse, a, pl.clusters, s) : cudaErrorInvalidValue;
+            }
         }
         if (e != cudaSuccess) break;
         cudaLaunchAttribute attr[1];
@@ -564,7 +618,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             w = base + at_w;
         }
         const void *z = base + at_z;
-        const LogitPlan pl = logit_plan<FORMAT, DzEpi>(p.M, n, ceil_div(kp, BK), dev);
+        const LogitPlan pl = logit_plan<FORMAT, DzEpi, false>(p.M, n, ceil_div(kp, BK), 1, dev);
         const long long w_tiles = ceil_div(n, 256) * ceil_div(p.K, 256);
         if (!pl.bn || w_tiles > 0x7FFFFFFFLL || x_tiles * splits > 0x7FFFFFFFLL) {
             e = cudaErrorInvalidValue;
@@ -588,9 +642,9 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.v0 = (int)v0;
             epi.total = p.N;
             epi.bf16 = bf16;
-            const Args a = {p.M, n, (int)ceil_div(kp, BK), pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, left_rows(p.M, pl.rows), BK, pl.rows, status};
-            e = pl.joined > 1 ? launch<FORMAT>(ta, tb, DzEpi<true>{epi}, a, pl.clusters, s)
-                              : launch<FORMAT>(ta, tb, DzEpi<false>{epi}, a, pl.clusters, s);
+            const Args a = {p.M, n, (int)ceil_div(kp, BK), pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, left_rows(p.M, pl.rows), BK, pl.rows, 1, 0, 0, status};
+            e = pl.joined > 1 ? launch<FORMAT>(ta, tb, DzEpi<true, false>{epi}, a, pl.clusters, s)
+                              : launch<FORMAT>(ta, tb, DzEpi<false, false>{epi}, a, pl.clusters, s);
         }
         if (e == cudaSuccess && p.dW) {
             OutEpi epi;
@@ -609,7 +663,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.M = n;
             epi.N = p.K;
             epi.bf16 = bf16;
-            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, 256, status};
+            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, 256, 1, 0, 0, status};
             e = launch<FORMAT>(ta, tb, epi, a, cw, s);
         }
         if (e == cudaSuccess && p.dX) {
@@ -624,7 +678,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.add = v0 > 0;
             // (a short last piece: fewer ranges, each of one block at least)
             const int kb = (int)ceil_div(n, BK);
-            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, left_rows(p.M, tile_rows(p.M)), BK, tile_rows(p.M), status};
+            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, left_rows(p.M, tile_rows(p.M)), BK, tile_rows(p.M), 1, 0, 0, status};
             e = launch<FORMAT>(ta, tb, epi, a, cx, s);
         }
     }

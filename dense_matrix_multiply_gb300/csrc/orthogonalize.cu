@@ -76,7 +76,7 @@ __device__ __forceinline__ void row_half(const uint8_t *box, int lane, int h, ui
 
 // A [m, m] = f X X^T, or B = b A + c A A^T: both triangles.
 struct SymEpi {
-    static constexpr bool LOWER = true, JOIN = true;
+    static constexpr bool LOWER = true, JOIN = true, CLASSES = false;
     static constexpr int BOXES = 2;
     CUtensorMap tm, tmT;    // the output, and in boxes of 64 rows x 32 columns
     const uint16_t *old;    // A, or null
@@ -154,7 +154,7 @@ struct MulArgs {
 };
 template <bool LO, bool LAST>
 struct MulEpi : MulArgs {
-    static constexpr bool LOWER = false, JOIN = true;
+    static constexpr bool LOWER = false, JOIN = true, CLASSES = false;
     static constexpr int BOXES = 2;
 
     struct Pre {
@@ -435,7 +435,7 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
     if (tma_out) ok = ok && map16(&res, p.O, bf16 ? 1 : 0, p.M, p.N, p.ldo, 32, 64);
     if (!ok && e == cudaSuccess) e = cudaErrorInvalidValue;
     auto args = [&](int rows, int cols, int k, const Plan &q, bool a_mn, bool b_mn) {
-        return Args{rows, cols, (int)ceil_div(k, BK), q.bn, a_mn, b_mn, (int)q.tiles, 1, q.joined, 128, BK, 256, status};
+        return Args{rows, cols, (int)ceil_div(k, BK), q.bn, a_mn, b_mn, (int)q.tiles, 1, q.joined, 128, BK, 256, 1, 0, 0, status};
     };
     for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
         const int in = i & 1, out = in ^ 1;

@@ -16,6 +16,15 @@
 // to the shared memory of its counterpart there and writes out its own 64.  (All of a
 // tile's sums through the cluster, among four pairs: 7 us a tile; this way about 1.)
 //
+// Classes (Epi::CLASSES): a B whose rows lie off 16 bytes, K-major, which TMA cannot describe,
+// is read in place.  Every eighth row (fourth, second: G = 8 / gcd(K, 8)) lies alike to 16
+// bytes, so that rows r, r + G, ... make a matrix of their own whose rows are a multiple of
+// 16 bytes apart.  It starts at the 16-byte piece that holds its first element, s_r elements
+// before it; A has s_r zeros in front of its rows, a copy for each class, and before their
+// first use the s_r elements in front of B's rows -- the ends of the rows before -- are
+// overwritten with zeros in shared memory (0 times an infinity is a NaN).  A tile's columns
+// are of one class.
+//
 // Every wait is bounded; on expiry a code goes to the status word, both CTAs give up,
 // their loads and MMAs are waited for, and the tensor memory is released.
 #pragma once
@@ -74,7 +83,15 @@ struct Args {
     // MMAs' time.  A CTA then has 64 rows, and its accumulator those of the first half of the
     // columns in tensor-memory lanes 0-63, of the second half in lanes 64-127.
     int rows;
+    // Classes: how many, tiles (columns of them) of each, and s_r, four bits each.
+    int classes, class_tiles;
+    uint32_t shifts;
     int *status;
+};
+// B's tensor maps, one of each class.
+template <bool CLASSES>
+struct BMaps {
+    CUtensorMap m[CLASSES ? 8 : 1];
 };
 
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -89,6 +106,16 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
 __device__ __forceinline__ uint32_t make_idesc(uint32_t format, uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
     return (1u << 4) | (format << 7) | (format << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+
+// The first s elements (s < 8) of the rows of a K-major operand, 128-byte swizzle, set to
+// zero: whole warp, in either CTA's shared memory.
+__device__ __forceinline__ void zero_front(uint32_t cluster_addr, int rows, uint32_t s, int lane) {
+    for (int r = lane; r < rows; r += 32) {
+        const uint32_t at = cluster_addr + (uint32_t)(r * 128 + ((r & 7) << 4));
+        for (uint32_t i = 0; i + 1 < s; i += 2) st_cluster_u32(at + 2 * i, 0u);
+        if (s & 1) asm volatile("st.shared::cluster.b16 [%0], %1;" ::"r"(at + 2 * (s - 1)), "h"((uint16_t)0) : "memory");
+    }
 }
 
 // An accumulator's columns are in registers (tcgen05.wait::ld has returned) and may be
@@ -150,7 +177,8 @@ __device__ __forceinline__ void send4(uint32_t cluster_addr, const uint32_t *r, 
 // a tile, multiples of 64.
 struct Part {
     uint32_t tmem;          // this warp's rows, the tile's first column
-    int row0, col0;         // of D: the warp's first row, the tile's first column
+    int row0, col0;         // of D: the warp's first row, the tile's first column (of its class)
+    int tile_n, cls;        // the tile's index in a row of them; its class
     int first, width;
     int range, ranges;      // these columns are the tile's range-th of so many
     int split;              // which K range
@@ -235,12 +263,12 @@ __device__ __forceinline__ void box_scatter(const uint8_t *box, int lane, uint16
     __syncwarp();
 }
 
-// Epi: static constexpr bool LOWER, and JOIN (whether pairs may be joined); int BOXES, 2
-// with JOIN; a type Pre and prefetch(Part, Pre), for what a unit's writing reads from memory,
+// Epi: static constexpr bool LOWER, JOIN (whether pairs may be joined) and CLASSES (whether B
+// is of classes); int BOXES, 2 with JOIN; a type Pre and prefetch(Part, Pre), for what a unit's writing reads from memory,
 // before its sums are waited for; run(Part, Pre); both called by whole warps with row0 < M.
 template <uint32_t FORMAT, typename Epi>
 __global__ void __launch_bounds__(THREADS, 1)
-pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps<Epi::CLASSES> mapsB,
             const __grid_constant__ Epi epi, const Args args)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -282,7 +310,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         mbar_init_fence();
         if (joined) mbar_arrive_expect_tx(&bars->joined, 2 * JOIN_CHUNK);
         prefetch_desc(&tmA);
-        prefetch_desc(&tmB);
+        prefetch_desc(&mapsB.m[0]);
     }
     if (warp == 1) tmem_alloc<2>(&bars->tmem_base, TMEM_COLS);
     fence_before();
@@ -314,7 +342,10 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         Tile t = range(cluster, kb0, kb1);
         pdl_wait();
         for (int u = cluster; ok && u < units;) {
-            const int row0 = t.m * 256 + (int)rank * (args.rows >> 1), col0 = t.n * bn + (int)rank * (bn >> 1);
+            const int cls = Epi::CLASSES ? t.n / args.class_tiles : 0;
+            const int row0 = t.m * 256 + (int)rank * (args.rows >> 1);
+            const int col0 = (t.n - cls * args.class_tiles) * bn + (int)rank * (bn >> 1);
+            const CUtensorMap *const tmB = &mapsB.m[cls];
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
                 const uint32_t full = map_to_rank(&bars->full[stage], lead);
@@ -325,13 +356,13 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         tma_load_3d_pair(a, &tmA, full, row0, kb * BK, 0);
                         tma_load_3d_pair(a + BOX64, &tmA, full, row0 + 64, kb * BK, 0);
                     } else if (leader || !few) {
-                        tma_load_3d_pair(a, &tmA, full, kb * BK, row0, 0);
+                        tma_load_3d_pair(a, &tmA, full, kb * BK, row0, cls);
                     }
                     if (args.b_mn) {
                         for (int c = 0; c < (bn >> 1); c += 64)
-                            tma_load_3d_pair(b + (c >> 6) * BOX64, &tmB, full, col0 + c, kb * BK, 0);
+                            tma_load_3d_pair(b + (c >> 6) * BOX64, tmB, full, col0 + c, kb * BK, 0);
                     } else {
-                        tma_load_3d_pair(b, &tmB, full, kb * BK, col0, 0);
+                        tma_load_3d_pair(b, tmB, full, kb * BK, col0, 0);
                     }
                 }
                 ++issued;
@@ -385,13 +416,20 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         bool ok = true;
         for (int u = cluster; ok && u < units; u += nclusters, ++it) {
             int kb0, kb1;
-            range(u, kb0, kb1);
+            const Tile t = range(u, kb0, kb1);
+            const uint32_t front = Epi::CLASSES ? args.shifts >> (4 * (t.n / args.class_tiles)) & 7u : 0u;
             const int buf = it & 1;
             if (!mbar_wait(&bars->acc_empty[buf], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, true)) { ok = false; break; }
             fence_after();
             const uint32_t d = tmem_base + (uint32_t)(buf * 256);
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait(&bars->full[stage], phase, abort_flag, true)) { ok = false; break; }
+                if (Epi::CLASSES && kb == 0 && front) {
+                    __syncwarp();
+                    for (uint32_t c = lead; c < lead + 2; ++c) zero_front(map_to_rank(b_tiles + stage * B_STAGE, c), bn >> 1, front, lane);
+                    asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async;" ::: "memory");
+                    __syncwarp();
+                }
                 fence_after();
                 const uint64_t ad = a_desc0 + (uint64_t)((stage * A_STAGE) >> 4);
                 const uint64_t bd = b_desc0 + (uint64_t)((stage * B_STAGE) >> 4);
@@ -438,7 +476,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int u = cluster; u < units; ++it) {
             const int buf = it & 1;
             p.row0 = t.m * 256 + (thin ? (int)rank * 64 + (quarter & 1) * 32 : (int)rank * 128 + quarter * 32);
-            p.col0 = t.n * bn;
+            p.tile_n = t.n;
+            p.cls = Epi::CLASSES ? t.n / args.class_tiles : 0;
+            p.col0 = (t.n - p.cls * args.class_tiles) * bn;
             p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256 - (thin ? (quarter >> 1) * (bn >> 1) : 0));
             const bool some = p.row0 < args.M;
             typename Epi::Pre pre;
@@ -509,7 +549,7 @@ int joined_max(int dev) {
 }
 
 template <uint32_t FORMAT, typename Epi>
-cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Epi &epi, const Args &args, int cmax, cudaStream_t s) {
+cudaError_t launch(const CUtensorMap &ta, const BMaps<Epi::CLASSES> &tb, const Epi &epi, const Args &args, int cmax, cudaStream_t s) {
     const long long units = (long long)args.tiles * args.splits;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(args.joined > 1 ? 4 * units : 2 * (units < cmax ? units : cmax)), 1, 1);
@@ -525,6 +565,11 @@ cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Epi &epi,
     cfg.attrs = attr;
     cfg.numAttrs = g_pdl ? 2 : 1;
     return launch_counted(&cfg, pair_kernel<FORMAT, Epi>, ta, tb, epi, args);
+}
+
+template <uint32_t FORMAT, typename Epi>
+cudaError_t launch(const CUtensorMap &ta, const CUtensorMap &tb, const Epi &epi, const Args &args, int cmax, cudaStream_t s) {
+    return launch<FORMAT>(ta, BMaps<false>{{tb}}, epi, args, cmax, s);
 }
 
 constexpr CUtensorMapDataType map_type(uint32_t format) {

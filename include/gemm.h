@@ -412,7 +412,9 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H,
  * outside 0 .. N - 1 leaves its row out: loss 0 (lse is stored all the same), and no part
  * in the gradients, whatever the row of X holds.  Logits, largest value, sum and
  * logarithm in FP32.  Any M, N, K; K and the bases multiples of 8 elements are fastest:
- * other operands are copied to padded rows in scratch, W a piece (up to 256 MiB) at a time.  Scratch:
+ * of other operands X is copied to padded rows in scratch (up to eight times), W read in
+ * place where K is no multiple of 8 and N large against M, else copied too, a piece (up to
+ * 256 MiB) at a time.  Scratch:
  * 8 bytes for each row and 64 to 128 entries, for up to 16384 rows at once, and the copies, in
  * stream-ordered memory for the duration of the call from the library's pool (see
  * gemm_gated).  K = 0: logits of 0; N = 0: lse is -inf.  GEMM_ERR_ALIAS if an output

@@ -109,6 +109,34 @@ def test_operands_off_16_bytes(M, N, K, off):
         assert torch.equal(a[k], b[k]), k
 
 
+@pytest.mark.parametrize("M,N", [(1, 1000), (3, 17), (40, 3001), (129, 5000), (7, 8)])
+@pytest.mark.parametrize("K,off", [(1, 0), (9, 1), (63, 0), (66, 3), (124, 0), (132, 5), (128, 1), (1001, 7)])
+def test_rows_of_the_vocabulary_off_16_bytes(M, N, K, off):
+    """Rows of one, two, four or eight alignments, whole tiles and parts of them."""
+    data = make(M, N, K, "bf16", M + 3 * N + 7 * K, left_out=0.1 if M > 1 else 0.0)
+    check(run("bf16", data, M, N, K, off), data, "bf16")
+
+
+@pytest.mark.parametrize("K", [57, 130, 1001])
+def test_an_infinity_reaches_its_own_row_alone(K):
+    """Rows of W that end, or begin, in infinities beside ones that do not: logits of -inf,
+    which weigh as much as very small ones -- nothing."""
+    M, N = 5, 1500
+    X, W, t, d = make(M, N, K, "bf16", K)
+    X[:, :8] = X[:, :8].abs() + 0.5
+    X[:, -8:] = X[:, -8:].abs() + 0.5
+    rows = torch.arange(3, N - 1, 7)
+    t[:] = 0
+    got = []
+    for v in (-np.inf, -30000.0):
+        W[rows, -7:] = v
+        W[rows[::2], :7] = v
+        got.append(run("bf16", (X, W, t, d), M, N, K, want=()))
+    for k in ("loss", "lse"):
+        assert torch.isfinite(got[0][k]).all()
+        assert torch.equal(got[0][k], got[1][k]), k
+
+
 @pytest.mark.parametrize("spread", [40.0, 300.0])
 def test_large_logits(spread):
     data = make(70, 1000, 256, "bf16", 6, spread=spread)
