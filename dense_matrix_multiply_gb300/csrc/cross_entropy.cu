@@ -106,11 +106,12 @@ struct DzArgs {
     const long long *target;
     const float2 *scale;  // null: 1
     int M, N, v0, total;  // total: columns of Z
+    int classes;          // of columns (N: of the largest class): a matrix of dZ each
     bool bf16;
 };
 template <bool JOINED, bool OF_CLASSES>
 struct DzEpi : DzArgs {
-    static constexpr bool LOWER = false, JOIN = JOINED, CLASSES = false;
+    static constexpr bool LOWER = false, JOIN = JOINED, CLASSES = OF_CLASSES;
     static constexpr int BOXES = JOINED ? 2 : 1;
 
     struct Pre {};
@@ -122,6 +123,11 @@ struct DzEpi : DzArgs {
         const float d = counts ? dloss[row] * (scale ? scale->x : 1.0f) : 0.0f;
         const float base = counts ? lse[row] * kLog2e : 0.0f;
         t = counts ? t - v0 : -1;
+        int cols = N;
+        if (CLASSES) {
+            cols = (total - p.cls + classes - 1) / classes;
+            t = t >= 0 && (int)t % classes == p.cls ? (int)t / classes : -1;
+        }
 #pragma unroll 1
         for (int g = p.first; g < p.first + p.width; g += 64) {
             const int c0 = p.col0 + g;
@@ -140,6 +146,11 @@ struct DzEpi : DzArgs {
                     for (int j = 0; j < 32; ++j)
                         if (j == at) v[j] -= 1.0f;
                 }
+                if (CLASSES && c0 + h * 32 + 32 > cols) {  // (a class may be one column short)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (c0 + h * 32 + j >= cols) v[j] = 0.0f;
+                }
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                     const float x = counts ? v[2 * j] * d : 0.0f, y = counts ? v[2 * j + 1] * d : 0.0f;
@@ -148,14 +159,15 @@ struct DzEpi : DzArgs {
             }
             uint8_t *box = box_next<BOXES>(p);
             box_put(box, p.lane, z);
-            box_store(&tm, box, p.lane, c0, p.row0, 0);
+            box_store(&tm, box, p.lane, c0, p.row0, p.cls);
         }
     }
 };
 
 // FP32 sums to slab `split`, or added to it.
+template <bool OF_CLASSES>
 struct AccEpi {
-    static constexpr bool LOWER = false, JOIN = false, CLASSES = false;
+    static constexpr bool LOWER = false, JOIN = false, CLASSES = OF_CLASSES;
     static constexpr int BOXES = 1;
     CUtensorMap tm;
     int N;
@@ -190,6 +202,7 @@ struct OutEpi {
     const float2 *scale;  // null: 1
     uint16_t *out;        // not null: by the element, rows ld apart
     long long ld;
+    int classes, class_rows;  // of out's rows, a class after the other in D, each class_rows (whole tiles)
     int M, N;
     bool bf16;
 
@@ -214,8 +227,16 @@ struct OutEpi {
             }
             uint8_t *box = box_next<BOXES>(p);
             box_put(box, p.lane, z);
-            if (out) box_scatter(box, p.lane, out, ld, p.row0, c0, M, N);
-            else box_store(&tm, box, p.lane, c0, p.row0, 0);
+            if (out) {
+                int cls = 0, rows = M;
+                if (classes > 1) {
+                    cls = p.row0 / class_rows;
+                    rows = (M - cls + classes - 1) / classes;
+                }
+                box_scatter(box, p.lane, out + cls * ld, ld * classes, p.row0 - cls * class_rows, c0, rows, N);
+            } else {
+                box_store(&tm, box, p.lane, c0, p.row0, 0);
+            }
         }
     }
 };
@@ -341,7 +362,7 @@ head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long col
 {
     pdl_wait();
     if (a.scale && blockIdx.x == gridDim.x - 1) {
-        if (blockIdx.y == 0) find_scale<COPY_WARPS * 32>(a);
+        if (blockIdx.y == 0 && blockIdx.z == 0) find_scale<COPY_WARPS * 32>(a);
         return;
     }
     const long long row = (long long)blockIdx.x * COPY_WARPS + (threadIdx.x >> 5);
@@ -373,23 +394,32 @@ cudaError_t copy(const void *src, long long rows, long long cols, void *dst, lon
                           dst_cols, target, N, shifts, scale);
 }
 
-// dX = (sum of the slabs, in order) scale->y, four elements to a thread.
+// dX = (sum of the slabs, in order) scale->y, four elements to a thread.  Of classes, `per`
+// slabs each, a slab's columns lie as far right as the class's four bits of `shifts` say.
 template <typename T>
 __global__ void __launch_bounds__(256)
-head_finish_kernel(const float *__restrict__ slab, int slabs, long long rows, int cols, long long ld, const float2 *scale,
-                   T *__restrict__ out)
+head_finish_kernel(const float *__restrict__ slab, int slabs, long long rows, int cols, long long ld, int per, uint32_t shifts,
+                   const float2 *scale, T *__restrict__ out)
 {
     pdl_wait();
-    const long long per = (cols + 3) / 4, i = blockIdx.x * 256LL + threadIdx.x;
-    if (i >= rows * per) return;
-    const long long row = i / per;
-    const int c = (int)(i - row * per) * 4;
+    const long long quads = (cols + 3) / 4, i = blockIdx.x * 256LL + threadIdx.x;
+    if (i >= rows * quads) return;
+    const long long row = i / quads;
+    const int c = (int)(i - row * quads) * 4;
     const float *p = slab + row * ld + c;
-    float4 v = __ldcg(reinterpret_cast<const float4 *>(p));
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (per) {
 #pragma unroll 4
-    for (int j = 1; j < slabs; ++j) {
-        const float4 w = __ldcg(reinterpret_cast<const float4 *>(p + j * rows * ld));
-        v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+        for (int j = 0; j < slabs; ++j) {
+            const float *q = p + j * rows * ld + (shifts >> (4 * (j / per)) & 7);
+            v.x += __ldcg(q); v.y += __ldcg(q + 1); v.z += __ldcg(q + 2); v.w += __ldcg(q + 3);
+        }
+    } else {
+#pragma unroll 4
+        for (int j = 0; j < slabs; ++j) {
+            const float4 w = __ldcg(reinterpret_cast<const float4 *>(p + j * rows * ld));
+            v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
+        }
     }
     const float f = scale ? scale->y : 1.0f;
     T *o = out + row * cols + c;
@@ -462,6 +492,11 @@ struct Classes {
         while (n * (K % 8) % 8) n *= 2;
         for (int r = 0; r < n; ++r) shifts |= (uint32_t)(((uintptr_t)w / 2 + (uintptr_t)r * (K % 8)) % 8) << (4 * r);
     }
+    // W in place costs a copy of X for each class and a pause of the MMAs for the zeros in front
+    // of each tile, W's copy twice its reading and writing (forward of 22 x 60179 x 951 36 us
+    // against 71, 1000 x 50000 x 2001 148 against 188; 3000 x 60000 x 701 225 against 180, 1000
+    // x 8000 x 2001 43 against 39).
+    bool pay(long long M, int N) const { return n > 1 && N <= 1 << 30 && 4LL * n * M <= N; }
     int shift(int r) const { return (int)(shifts >> (4 * r) & 7); }
     // Class r of N rows, K-major.
     bool map(CUtensorMap *m, const void *w, uint32_t format, int N, long long K, int r, int box_rows) const {
@@ -469,6 +504,9 @@ struct Classes {
         return map16(m, static_cast<const uint16_t *>(w) + r * K - s, format, (N - r + n - 1) / n, K + s, n * K, box_rows, BK);
     }
 };
+
+// Rows of a class of N, whole tiles of them.
+long long head_class_rows(long long N, int classes) { return up(ceil_div(N, classes), 256); }
 
 template <uint32_t FORMAT, bool CLASSES>
 cudaError_t launch_lse(const CUtensorMap &ta, const BMaps<CLASSES> &tb, const LseArgs &lse, const Args &a, int clusters, cudaStream_t s) {
@@ -483,11 +521,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
     const int rows = std::min(p.M, rows_max);
     const bool off_w = !aligned || !on16(p.W);
     const Classes cl(p.W, p.K);
-    // W in place costs a copy of X for each class and a pause of the MMAs for the zeros in front
-    // of each tile, W's copy twice its reading and writing (22 x 60179 x 951 36 us against 71,
-    // 1000 x 50000 x 2001 148 against 188; 3000 x 60000 x 701 225 against 180, 1000 x 8000 x
-    // 2001 43 against 39)
-    const bool classes = cl.n > 1 && p.N <= 1 << 30 && 4LL * cl.n * rows <= p.N;
+    const bool classes = cl.pay(rows, p.N);
     const bool pad_w = off_w && !classes, pad_x = classes || !aligned || !on16(p.X);
     const long long kp = classes ? up(p.K + 7LL, 64) : aligned ? p.K : up(p.K, 64);
     const long long vp = pad_w ? std::min<long long>(up(p.N, 256), std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256)) : p.N;
@@ -529,7 +563,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             lse.slot0 = (int)(v0 / vp) * piece_slots;
             const int n_tiles = classes ? class_tiles * cl.n : (int)ceil_div(n, bn);
             const long long tiles = ceil_div(m, 256) * n_tiles;
-            const Args a = {m, classes ? n_tiles * bn : n, num_kb, bn, 0, 0, (int)tiles, 1, pl.joined, box, BK, pl.rows, cl.n, class_tiles,
+            const Args a = {m, classes ? n_tiles * bn : n, num_kb, bn, 0, 0, (int)tiles, 1, pl.joined, box, BK, pl.rows, class_tiles, 0,
                             cl.shifts, status};
             CUtensorMap ta;
             bool ok = tiles <= 0x7FFFFFFFLL;
@@ -567,28 +601,51 @@ int dx_splits(long long tiles, long long num_kb, int cmax, double slab_us) {
     return best;
 }
 
-template <typename T, uint32_t FORMAT>
-cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s) {
-    const int cx = clusters_max<FORMAT, AccEpi>(dev), cw = clusters_max<FORMAT, OutEpi>(dev);
+template <uint32_t FORMAT, bool CLASSES>
+cudaError_t launch_dz(const CUtensorMap &ta, const BMaps<CLASSES> &tb, const DzArgs &dz, const Args &a, int clusters, cudaStream_t s) {
+    if (a.joined > 1) {
+        DzEpi<true, CLASSES> epi;
+        static_cast<DzArgs &>(epi) = dz;
+        return launch<FORMAT>(ta, tb, epi, a, clusters, s);
+    }
+    DzEpi<false, CLASSES> epi;
+    static_cast<DzArgs &>(epi) = dz;
+    return launch<FORMAT>(ta, tb, epi, a, clusters, s);
+}
+
+// CLASSES: of the vocabulary's rows (Classes), all in one piece; dZ a matrix [M, class_rows]
+// to a class, side by side.
+template <typename T, uint32_t FORMAT, bool CLASSES>
+cudaError_t backward(const HeadBackward &p, const Classes &cl, int dev, int *status, cudaStream_t s) {
+    const int cx = clusters_max<FORMAT, AccEpi<CLASSES>>(dev), cw = clusters_max<FORMAT, OutEpi>(dev);
     if (cx <= 0 || cw <= 0) return cudaErrorNotSupported;
+    const int G = CLASSES ? cl.n : 1, front = CLASSES ? 7 : 0;  // elements in front of a row, at most
     const bool aligned = p.K % 8 == 0;
-    const long long kp = aligned ? p.K : up(p.K, 64);
+    const long long kp = aligned ? p.K : up(p.K + front, 64);
     // X: rows without a target are zeros in dW's product, whatever they hold (0 times an
-    // infinity is a NaN)
-    const bool copy_x = p.dW || !aligned || !on16(p.X), pad_w = !aligned || !on16(p.W);
-    long long vp = std::max<long long>(kPiece / (2LL * p.M) / 256 * 256, 256);
-    if (pad_w) vp = std::min(vp, std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256));
-    const long long pieces = ceil_div(p.N, vp);
-    vp = up(ceil_div(p.N, pieces), 256);
+    // infinity is a NaN).  Of classes a copy with each front, one of them 0 (dW's operand)
+    const bool copy_x = p.dW || !aligned || !on16(p.X), pad_w = !CLASSES && (!aligned || !on16(p.W));
+    int x0 = 0;
+    while (CLASSES && x0 < G && cl.shift(x0)) ++x0;
+    const int copies = std::max(G, x0 + 1);
+    long long vp;
+    if (CLASSES) {
+        vp = head_class_rows(p.N, G) * G;
+    } else {
+        vp = std::max<long long>(kPiece / (2LL * p.M) / 256 * 256, 256);
+        if (pad_w) vp = std::min(vp, std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256));
+        const long long pieces = ceil_div(p.N, vp);
+        vp = up(ceil_div(p.N, pieces), 256);
+    }
     // dX
-    const long long x_tiles = ceil_div(p.M, 256) * ceil_div(p.K, 256), ldx = up(p.K, 64);
+    const long long x_cols = p.K + front, x_tiles = ceil_div(p.M, 256) * ceil_div(x_cols, 256), ldx = up(x_cols + (CLASSES ? 3 : 0), 64);
     const double slab_us = (double)p.M * ldx * 4 * 2 / 5e6;
-    int splits = dx_splits(x_tiles, vp / BK, cx, slab_us);
-    splits = (int)std::max<long long>(1, std::min<long long>(splits, kPiece / ((long long)p.M * ldx * 4)));
+    int splits = dx_splits(x_tiles * G, vp / G / BK, cx, G * slab_us);  // of a class
+    splits = (int)std::max<long long>(1, std::min<long long>(splits, kPiece / ((long long)p.M * ldx * 4 * G)));
     Layout l;
-    const size_t at_z = l.add((size_t)p.M * vp * 2), at_x = l.add(copy_x ? (size_t)p.M * kp * 2 : 0),
+    const size_t at_z = l.add((size_t)p.M * vp * 2), at_x = l.add(copy_x ? (size_t)copies * p.M * kp * 2 : 0),
                  at_w = l.add(pad_w ? (size_t)vp * kp * 2 : 0),
-                 at_slab = l.add(p.dX ? (size_t)splits * p.M * ldx * 4 : 0), at_scale = l.add(8);
+                 at_slab = l.add(p.dX ? (size_t)splits * G * p.M * ldx * 4 : 0), at_scale = l.add(8);
     void *ws = nullptr;
     cudaError_t e = scratch_alloc(&ws, l.bytes, s);
     if (e != cudaSuccess) return e;
@@ -604,32 +661,43 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
         e = launch_counted(&cfg, head_scale_kernel, find);
         find = {};
     }
-    const void *x = p.X;
+    const uint16_t *x = static_cast<const uint16_t *>(p.X);
     if (e == cudaSuccess && copy_x) {
-        e = copy(p.X, p.M, p.K, base + at_x, kp, p.dW ? p.target : nullptr, p.dW ? p.N : 1, find, s);
-        x = base + at_x;
+        e = copy(p.X, p.M, p.K, base + at_x, kp, p.dW ? p.target : nullptr, p.dW ? p.N : 1, find, s, copies, CLASSES ? cl.shifts : 0);
+        x = reinterpret_cast<const uint16_t *>(base + at_x);
     }
     for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
-        const int n = (int)std::min<long long>(vp, p.N - v0);
-        const void *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
+        const int n = (int)std::min<long long>(vp, p.N - v0), cn = (int)ceil_div(n, G);  // of the (largest) class
+        const uint16_t *w = static_cast<const uint16_t *>(p.W) + v0 * p.K;
         if (pad_w) {
             e = copy(w, n, p.K, base + at_w, kp, nullptr, 1, {}, s);
             if (e != cudaSuccess) break;
-            w = base + at_w;
+            w = reinterpret_cast<const uint16_t *>(base + at_w);
         }
-        const void *z = base + at_z;
-        const LogitPlan pl = logit_plan<FORMAT, DzEpi, false>(p.M, n, ceil_div(kp, BK), 1, dev);
-        const long long w_tiles = ceil_div(n, 256) * ceil_div(p.K, 256);
-        if (!pl.bn || w_tiles > 0x7FFFFFFFLL || x_tiles * splits > 0x7FFFFFFFLL) {
+        const uint8_t *z = base + at_z;
+        const int num_kb = (int)ceil_div(kp, BK);
+        const LogitPlan pl = logit_plan<FORMAT, DzEpi, CLASSES>(p.M, n, num_kb, G, dev);
+        // dZ's columns as rows of dW: all that there are, of classes the gaps behind them too
+        const int z_rows = CLASSES ? (int)vp : n;
+        const long long w_tiles = ceil_div(z_rows, 256) * ceil_div(p.K, 256);
+        if (!pl.bn || w_tiles > 0x7FFFFFFFLL || x_tiles * splits * G > 0x7FFFFFFFLL) {
             e = cudaErrorInvalidValue;
             break;
         }
-        CUtensorMap ta, tb;
+        CUtensorMap ta;
+        BMaps<CLASSES> tb = {};
+        // dZ in boxes of rows x 64
+        auto map_z = [&](CUtensorMap *m, int rows) {
+            return make_map3(m, z, map_type(FORMAT), cn, p.M, G, vp * 2, CLASSES ? vp / G * 2 : p.M * vp * 2, 64, rows, 1, 128);
+        };
         {
             DzArgs epi;
-            if (!map_operand(&ta, x, FORMAT, false, p.M, kp, kp, left_rows(p.M, pl.rows)) ||
-                !map_operand(&tb, w, FORMAT, false, n, kp, kp, pl.bn / 2) ||
-                !map16(&epi.tm, z, FORMAT, p.M, n, vp, 32, 64)) {
+            const int box = left_rows(p.M, pl.rows), class_tiles = (int)ceil_div(cn, pl.bn);
+            bool ok = make_map3(&ta, x, map_type(FORMAT), kp, p.M, G, kp * 2, p.M * kp * 2, BK, box, 1, 128) && map_z(&epi.tm, 32);
+            for (int r = 0; r < G && ok; ++r)
+                ok = CLASSES ? cl.map(&tb.m[r], w, FORMAT, n, p.K, r, pl.bn / 2)
+                             : map_operand(&tb.m[0], w, FORMAT, false, n, kp, kp, pl.bn / 2);
+            if (!ok) {
                 e = cudaErrorInvalidValue;
                 break;
             }
@@ -638,21 +706,23 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.target = p.target;
             epi.scale = scale;
             epi.M = p.M;
-            epi.N = n;
+            epi.N = cn;
             epi.v0 = (int)v0;
             epi.total = p.N;
+            epi.classes = G;
             epi.bf16 = bf16;
-            const Args a = {p.M, n, (int)ceil_div(kp, BK), pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, left_rows(p.M, pl.rows), BK, pl.rows, 1, 0, 0, status};
-            e = pl.joined > 1 ? launch<FORMAT>(ta, tb, DzEpi<true, false>{epi}, a, pl.clusters, s)
-                              : launch<FORMAT>(ta, tb, DzEpi<false, false>{epi}, a, pl.clusters, s);
+            const Args a = {p.M, CLASSES ? class_tiles * G * pl.bn : n, num_kb, pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, box, BK, pl.rows,
+                            class_tiles, 0, cl.shifts, status};
+            e = launch_dz<FORMAT, CLASSES>(ta, tb, epi, a, pl.clusters, s);
         }
         if (e == cudaSuccess && p.dW) {
             OutEpi epi;
+            CUtensorMap tx;
             uint16_t *out = static_cast<uint16_t *>(p.dW) + v0 * p.K;
             const bool tma = aligned && on16(p.dW);
             const int k_rows = p.M <= 48 ? (p.M + 15) / 16 * 16 : BK;
-            if (!map_operand(&ta, z, FORMAT, true, n, p.M, vp, 0, k_rows) ||
-                !map_operand(&tb, x, FORMAT, true, kp, p.M, kp, 0, k_rows) ||
+            if (!map_operand(&ta, z, FORMAT, true, z_rows, p.M, vp, 0, k_rows) ||
+                !map_operand(&tx, x + (long long)x0 * p.M * kp, FORMAT, true, kp, p.M, kp, 0, k_rows) ||
                 !map16(&epi.tm, tma ? (const void *)out : z, FORMAT, n, tma ? p.K : 64, tma ? p.K : 64, 32, 64)) {
                 e = cudaErrorInvalidValue;
                 break;
@@ -660,38 +730,56 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
             epi.scale = scale;
             epi.out = tma ? nullptr : out;
             epi.ld = p.K;
+            epi.classes = G;
+            epi.class_rows = (int)(vp / G);
             epi.M = n;
             epi.N = p.K;
             epi.bf16 = bf16;
-            const Args a = {n, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, 256, 1, 0, 0, status};
-            e = launch<FORMAT>(ta, tb, epi, a, cw, s);
+            const Args a = {z_rows, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, 256, 0, 0, 0, status};
+            e = launch<FORMAT>(ta, tx, epi, a, cw, s);
         }
         if (e == cudaSuccess && p.dX) {
-            AccEpi epi;
-            if (!map_operand(&ta, z, FORMAT, false, p.M, n, vp, left_rows(p.M, tile_rows(p.M))) || !map_operand(&tb, w, FORMAT, true, kp, n, kp, 0) ||
-                !make_map3(&epi.tm, base + at_slab, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.K, p.M, splits, ldx * 4,
-                           p.M * ldx * 4, 32, 32, 1, 128)) {
+            AccEpi<CLASSES> epi;
+            const int box = left_rows(p.M, tile_rows(p.M));
+            bool ok = map_z(&ta, box) && make_map3(&epi.tm, base + at_slab, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, x_cols, p.M, splits * G,
+                                                   ldx * 4, p.M * ldx * 4, 32, 32, 1, 128);
+            for (int r = 0; r < G && ok; ++r)
+                ok = CLASSES ? cl.map(&tb.m[r], w, FORMAT, n, p.K, r, BK) : map_operand(&tb.m[0], w, FORMAT, true, kp, n, kp, 0);
+            if (!ok) {
                 e = cudaErrorInvalidValue;
                 break;
             }
-            epi.N = p.K;
+            epi.N = (int)x_cols;
             epi.add = v0 > 0;
             // (a short last piece: fewer ranges, each of one block at least)
-            const int kb = (int)ceil_div(n, BK);
-            const Args a = {p.M, p.K, kb, 256, 0, 1, (int)x_tiles, std::min(splits, kb), 1, left_rows(p.M, tile_rows(p.M)), BK, tile_rows(p.M), 1, 0, 0, status};
+            const int kb = (int)ceil_div(cn, BK), ranges = std::min(splits, kb);
+            const Args a = {p.M, (int)x_cols, kb, 256, 0, 1, (int)x_tiles, ranges * G, 1, box, BK, tile_rows(p.M), 0, CLASSES ? ranges : 0,
+                            cl.shifts, status};
             e = launch<FORMAT>(ta, tb, epi, a, cx, s);
         }
     }
     if (e == cudaSuccess && p.dX) {
         const long long blocks = ceil_div((long long)p.M * ((p.K + 3) / 4), 256);
-        const int used = (int)std::min<long long>(splits, ceil_div(std::min<long long>(vp, p.N), BK));
+        const int used = (int)std::min<long long>(splits, ceil_div(ceil_div(std::min<long long>(vp, p.N), G), BK));
         const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)blocks), dim3(256), 0, s, attr);
         e = blocks > 0x7FFFFFFFLL ? cudaErrorInvalidValue
                                   : launch_counted(&cfg, head_finish_kernel<T>, reinterpret_cast<const float *>(base + at_slab),
-                                                   used, (long long)p.M, p.K, ldx, scale, static_cast<T *>(p.dX));
+                                                   used * G, (long long)p.M, p.K, ldx, CLASSES ? used : 0, cl.shifts, scale,
+                                                   static_cast<T *>(p.dX));
     }
     const cudaError_t f = cudaFreeAsync(ws, s);
     return e != cudaSuccess ? e : f;
+}
+template <typename T, uint32_t FORMAT>
+cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s) {
+    const Classes cl(p.W, p.K);
+    const long long z = 2LL * p.M * head_class_rows(p.N, cl.n) * cl.n, slabs = 4LL * cl.n * p.M * up(p.K + 10LL, 64);
+    // a slab of dX for each class: for fewer rows yet, and a W of 8 MB or more (22 x 60179 x 951
+    // 125 us against 151, 1 x 32000 x 4095 230 against 293; 300 x 40000 x 1501 197 against 189,
+    // 1 x 1000 x 130 24.7 against 22.6)
+    const bool classes = cl.pay(16LL * p.M, p.N) && (long long)p.N * p.K >= 4 << 20;
+    return classes && z <= kPiece && slabs <= kPiece ? backward<T, FORMAT, true>(p, cl, dev, status, s)
+                                                     : backward<T, FORMAT, false>(p, cl, dev, status, s);
 }
 
 cudaError_t device(int *dev) {

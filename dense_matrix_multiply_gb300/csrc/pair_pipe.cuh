@@ -23,7 +23,8 @@
 // before it; A has s_r zeros in front of its rows, a copy for each class, and before their
 // first use the s_r elements in front of B's rows -- the ends of the rows before -- are
 // overwritten with zeros in shared memory (0 times an infinity is a NaN).  A tile's columns
-// are of one class.
+// are of one class.  Or the rows are K and B lies MN-major: a K range is of one class, A has a
+// matrix for each, and D's columns are s_r too far right.
 //
 // Every wait is bounded; on expiry a code goes to the status word, both CTAs give up,
 // their loads and MMAs are waited for, and the tensor memory is released.
@@ -83,8 +84,9 @@ struct Args {
     // MMAs' time.  A CTA then has 64 rows, and its accumulator those of the first half of the
     // columns in tensor-memory lanes 0-63, of the second half in lanes 64-127.
     int rows;
-    // Classes: how many, tiles (columns of them) of each, and s_r, four bits each.
-    int classes, class_tiles;
+    // Classes: tiles (columns of them) of each, K ranges of each (0: the classes are of
+    // columns), and s_r, four bits each.
+    int class_tiles, class_splits;
     uint32_t shifts;
     int *status;
 };
@@ -264,8 +266,9 @@ __device__ __forceinline__ void box_scatter(const uint8_t *box, int lane, uint16
 }
 
 // Epi: static constexpr bool LOWER, JOIN (whether pairs may be joined) and CLASSES (whether B
-// is of classes); int BOXES, 2 with JOIN; a type Pre and prefetch(Part, Pre), for what a unit's writing reads from memory,
-// before its sums are waited for; run(Part, Pre); both called by whole warps with row0 < M.
+// is of classes); int BOXES, 2 with JOIN; a type Pre and prefetch(Part, Pre), for what a
+// unit's writing reads from memory, before its sums are waited for; run(Part, Pre); both
+// called by whole warps with row0 < M.
 template <uint32_t FORMAT, typename Epi>
 __global__ void __launch_bounds__(THREADS, 1)
 pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMaps<Epi::CLASSES> mapsB,
@@ -325,10 +328,19 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMa
     // unit u: K range u / tiles of tile u % tiles (clusters share a range's operands); joined
     // pairs: a half of K each
     auto range = [&](int u, int &kb0, int &kb1) {
-        const int j = u / args.tiles, at = joined ? (int)(cta >> 1) : j, n = joined ? 2 : args.splits;
+        const int j = u / args.tiles, own = Epi::CLASSES ? args.class_splits : 0;
+        const int at = joined ? (int)(cta >> 1) : own ? j % own : j, n = joined ? 2 : own ? own : args.splits;
         kb0 = args.num_kb * at / n;  // (num_kb < 2^26, n <= 16)
         kb1 = args.num_kb * (at + 1) / n;
         return tile_at<Epi::LOWER>(u - j * args.tiles, args);
+    };
+
+    // the class of a unit's tile, and the tile's first column of it
+    auto class_of = [&](int u, const Tile &t, int &col0) {
+        int cls = 0;
+        if (Epi::CLASSES) cls = args.class_splits ? u / args.tiles / args.class_splits : t.n / args.class_tiles;
+        col0 = (t.n - (Epi::CLASSES && !args.class_splits ? cls * args.class_tiles : 0)) * bn;
+        return cls;
     };
 
     if (warp == 0) {
@@ -342,9 +354,9 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMa
         Tile t = range(cluster, kb0, kb1);
         pdl_wait();
         for (int u = cluster; ok && u < units;) {
-            const int cls = Epi::CLASSES ? t.n / args.class_tiles : 0;
-            const int row0 = t.m * 256 + (int)rank * (args.rows >> 1);
-            const int col0 = (t.n - cls * args.class_tiles) * bn + (int)rank * (bn >> 1);
+            int col0;
+            const int cls = class_of(u, t, col0), row0 = t.m * 256 + (int)rank * (args.rows >> 1);
+            col0 += (int)rank * (bn >> 1);
             const CUtensorMap *const tmB = &mapsB.m[cls];
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
@@ -417,7 +429,8 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMa
         for (int u = cluster; ok && u < units; u += nclusters, ++it) {
             int kb0, kb1;
             const Tile t = range(u, kb0, kb1);
-            const uint32_t front = Epi::CLASSES ? args.shifts >> (4 * (t.n / args.class_tiles)) & 7u : 0u;
+            int col0;
+            const uint32_t front = Epi::CLASSES && !b_mn ? args.shifts >> (4 * class_of(u, t, col0)) & 7u : 0u;
             const int buf = it & 1;
             if (!mbar_wait(&bars->acc_empty[buf], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag, true)) { ok = false; break; }
             fence_after();
@@ -477,8 +490,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMa
             const int buf = it & 1;
             p.row0 = t.m * 256 + (thin ? (int)rank * 64 + (quarter & 1) * 32 : (int)rank * 128 + quarter * 32);
             p.tile_n = t.n;
-            p.cls = Epi::CLASSES ? t.n / args.class_tiles : 0;
-            p.col0 = (t.n - p.cls * args.class_tiles) * bn;
+            p.cls = class_of(u, t, p.col0);
             p.tmem = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(buf * 256 - (thin ? (quarter >> 1) * (bn >> 1) : 0));
             const bool some = p.row0 < args.M;
             typename Epi::Pre pre;

@@ -117,6 +117,19 @@ def test_rows_of_the_vocabulary_off_16_bytes(M, N, K, off):
     check(run("bf16", data, M, N, K, off), data, "bf16")
 
 
+LARGE_OFF = [(1, 20000, 257, 0), (5, 33001, 131, 1), (3, 8200, 516, 3), (2, 9001, 514, 1), (16, 70001, 67, 0), (70, 72000, 68, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K,off", LARGE_OFF)
+def test_gradients_of_large_vocabularies_off_16_bytes(M, N, K, off, dtype):
+    data = make(M, N, K, dtype, M + N + K, left_out=0.2 if M > 1 else 0.0)
+    both = run(dtype, data, M, N, K, off)
+    check(both, data, dtype)
+    for k in ("dX", "dW"):
+        assert torch.equal(run(dtype, data, M, N, K, off, want=(k,))[k], both[k]), k
+
+
 @pytest.mark.parametrize("K", [57, 130, 1001])
 def test_an_infinity_reaches_its_own_row_alone(K):
     """Rows of W that end, or begin, in infinities beside ones that do not: logits of -inf,
