@@ -194,6 +194,20 @@ struct AccEpi {
     }
 };
 
+// Columns g .. g + 63 of a tile times f, in 16 bits.
+__device__ __forceinline__ void scaled(const Part &p, int g, float f, bool bf16, uint32_t (&z)[32]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t r[32];
+        p.load<false>(g + h * 32, r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float x = __uint_as_float(r[2 * j]) * f, y = __uint_as_float(r[2 * j + 1]) * f;
+            z[h * 16 + j] = bf16 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
+        }
+    }
+}
+
 // 16-bit results times scale->y.
 struct OutEpi {
     static constexpr bool LOWER = false, JOIN = false, CLASSES = false;
@@ -202,7 +216,6 @@ struct OutEpi {
     const float2 *scale;  // null: 1
     uint16_t *out;        // not null: by the element, rows ld apart
     long long ld;
-    int classes, class_rows;  // of out's rows, a class after the other in D, each class_rows (whole tiles)
     int M, N;
     bool bf16;
 
@@ -215,27 +228,55 @@ struct OutEpi {
             const int c0 = p.col0 + g;
             if (c0 >= N) return;  // warp-uniform
             uint32_t z[32];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t r[32];
-                p.load<false>(g + h * 32, r);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float x = __uint_as_float(r[2 * j]) * f, y = __uint_as_float(r[2 * j + 1]) * f;
-                    z[h * 16 + j] = bf16 ? pack2(x, y, (__nv_bfloat16 *)nullptr) : pack2(x, y, (__half *)nullptr);
-                }
-            }
+            scaled(p, g, f, bf16, z);
             uint8_t *box = box_next<BOXES>(p);
             box_put(box, p.lane, z);
-            if (out) {
-                int cls = 0, rows = M;
-                if (classes > 1) {
-                    cls = p.row0 / class_rows;
-                    rows = (M - cls + classes - 1) / classes;
+            if (out) box_scatter(box, p.lane, out, ld, p.row0, c0, M, N);
+            else box_store(&tm, box, p.lane, c0, p.row0, 0);
+        }
+    }
+};
+
+// The same to rows off 16 bytes, of classes (pair_pipe.cuh): D has a class's rows after the
+// other's, class_rows (whole tiles) each, and its columns are turned, from the first whole 16
+// bytes of out's row, u_r elements behind its start, to its end and on from its start.  Whole
+// pieces go by TMA, a matrix of every classes-th row each, the up to seven elements at each
+// end of a row one by one (dW of 1 x 32000 x 4095 78 us, by
+// the element 126).
+struct TurnEpi {
+    static constexpr bool LOWER = false, JOIN = false, CLASSES = false;
+    static constexpr int BOXES = 2;
+    BMaps<true> tm;
+    const float2 *scale;  // null: 1
+    uint16_t *out;
+    int classes, class_rows;
+    uint32_t turns;  // u_r, four bits each
+    int M, N;        // of out
+    bool bf16;
+
+    struct Pre {};
+    __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
+    __device__ __forceinline__ void run(Part &p, const Pre &) const {
+        const float f = scale ? scale->y : 1.0f;
+        const int cls = p.row0 / class_rows, row0 = p.row0 - cls * class_rows, rows = (M - cls + classes - 1) / classes;
+        if (row0 >= rows) return;
+        const int u = turns >> (4 * cls) & 7, whole = (N - u) & ~7;
+        uint16_t *const row = out + ((long long)(row0 + p.lane) * classes + cls) * N;
+#pragma unroll 1
+        for (int g = p.first; g < p.first + p.width; g += 64) {
+            const int c0 = p.col0 + g;
+            if (c0 >= N) return;  // warp-uniform
+            uint32_t z[32];
+            scaled(p, g, f, bf16, z);
+            uint8_t *box = box_next<BOXES>(p);
+            box_put(box, p.lane, z);
+            if (c0 < whole) box_store(&tm.m[cls], box, p.lane, c0, row0, 0);
+            if (row0 + p.lane < rows) {
+                for (int c = max(c0, whole); c < min(c0 + 64, N); ++c) {
+                    const int e = c - c0;
+                    row[c + u < N ? c + u : c + u - N] =
+                        *reinterpret_cast<const uint16_t *>(box + p.lane * 128 + (((e >> 3) ^ (p.lane & 7)) << 4) + (e & 7) * 2);
                 }
-                box_scatter(box, p.lane, out + cls * ld, ld * classes, p.row0 - cls * class_rows, c0, rows, N);
-            } else {
-                box_store(&tm, box, p.lane, c0, p.row0, 0);
             }
         }
     }
@@ -354,11 +395,12 @@ head_scale_kernel(const ScaleArgs a)
 // dst [rows, dst_cols] (rows of whole 16 bytes) = src [rows, cols] (any 2 bytes), zeros
 // behind the row and, where targets are given, in rows whose target is no column of N: a
 // lane two 16-byte pieces (fp4.h).  A scale to find is one more CTA's.  Of classes: matrix z
-// of dst has its rows behind as many zeros as the z-th four bits of `shifts` say, 7 at most.
+// of dst has its rows behind as many zeros as the z-th four bits of `fronts` say, 7 at most,
+// or turned left by as many elements as those of `turns` do.
 constexpr int COPY_WARPS = 4;
 __global__ void __launch_bounds__(COPY_WARPS * 32)
 head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long cols, uint16_t *__restrict__ dst,
-                 long long dst_cols, const long long *__restrict__ target, int N, uint32_t shifts, const ScaleArgs a)
+                 long long dst_cols, const long long *__restrict__ target, int N, unsigned long long fronts, unsigned long long turns, const ScaleArgs a)
 {
     pdl_wait();
     if (a.scale && blockIdx.x == gridDim.x - 1) {
@@ -372,11 +414,18 @@ head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long col
     const long long width = t >= 0 && t < N ? cols : -1024;
     const uint8_t *lo = reinterpret_cast<const uint8_t *>(src), *hi = reinterpret_cast<const uint8_t *>(src + rows * cols);
     uint16_t *d = dst + (blockIdx.z * rows + row) * dst_cols;
-    const int front = shifts >> (4 * blockIdx.z) & 7;
+    const int front = (int)(fronts >> (4 * blockIdx.z) & 7), turn = (int)(turns >> (4 * blockIdx.z) & 7);
     for (long long k0 = blockIdx.y * 512LL; k0 < dst_cols; k0 += gridDim.y * 512LL) {
         const long long k = k0 + lane * 16;
         uint32_t v[8];
-        fp4_load16_any(src + row * cols + k - front, (int)max(min(width + front - k, 512LL), -512LL), lo, hi, v);
+        fp4_load16_any(src + row * cols + k - front + turn, (int)max(min(width + front - turn - k, 512LL), -512LL), lo, hi, v);
+        if (turn && width > 0) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const long long at = k + j - (cols - turn);
+                if (at >= 0 && at < turn) v[j >> 1] |= (uint32_t)src[row * cols + at] << (16 * (j & 1));
+            }
+        }
         if (k == 0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] &= (2 * j < front ? 0u : 0xFFFFu) | (2 * j + 1 < front ? 0u : 0xFFFF0000u);
@@ -386,12 +435,13 @@ head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long col
     }
 }
 cudaError_t copy(const void *src, long long rows, long long cols, void *dst, long long dst_cols, const long long *target,
-                 int N, const ScaleArgs &scale, cudaStream_t s, int classes = 1, uint32_t shifts = 0) {
+                 int N, const ScaleArgs &scale, cudaStream_t s, int matrices = 1, unsigned long long fronts = 0,
+                 unsigned long long turns = 0) {
     const long long gx = (rows + COPY_WARPS - 1) / COPY_WARPS + (scale.scale ? 1 : 0), gy = std::min<long long>((dst_cols + 511) / 512, 65535);
     cudaLaunchAttribute attr[1];
-    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)gx, (unsigned)gy, (unsigned)classes), dim3(COPY_WARPS * 32), 0, s, attr);
+    const cudaLaunchConfig_t cfg = pdl_config(dim3((unsigned)gx, (unsigned)gy, (unsigned)matrices), dim3(COPY_WARPS * 32), 0, s, attr);
     return launch_counted(&cfg, head_copy_kernel, static_cast<const uint16_t *>(src), rows, cols, static_cast<uint16_t *>(dst),
-                          dst_cols, target, N, shifts, scale);
+                          dst_cols, target, N, fronts, turns, scale);
 }
 
 // dX = (sum of the slabs, in order) scale->y, four elements to a thread.  Of classes, `per`
@@ -564,7 +614,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
             const int n_tiles = classes ? class_tiles * cl.n : (int)ceil_div(n, bn);
             const long long tiles = ceil_div(m, 256) * n_tiles;
             const Args a = {m, classes ? n_tiles * bn : n, num_kb, bn, 0, 0, (int)tiles, 1, pl.joined, box, BK, pl.rows, class_tiles, 0,
-                            cl.shifts, status};
+                            cl.shifts, 0, status};
             CUtensorMap ta;
             bool ok = tiles <= 0x7FFFFFFFLL;
             if (classes) {
@@ -617,17 +667,21 @@ cudaError_t launch_dz(const CUtensorMap &ta, const BMaps<CLASSES> &tb, const DzA
 // to a class, side by side.
 template <typename T, uint32_t FORMAT, bool CLASSES>
 cudaError_t backward(const HeadBackward &p, const Classes &cl, int dev, int *status, cudaStream_t s) {
-    const int cx = clusters_max<FORMAT, AccEpi<CLASSES>>(dev), cw = clusters_max<FORMAT, OutEpi>(dev);
+    const int cx = clusters_max<FORMAT, AccEpi<CLASSES>>(dev),
+              cw = CLASSES ? clusters_max<FORMAT, TurnEpi>(dev) : clusters_max<FORMAT, OutEpi>(dev);
     if (cx <= 0 || cw <= 0) return cudaErrorNotSupported;
     const int G = CLASSES ? cl.n : 1, front = CLASSES ? 7 : 0;  // elements in front of a row, at most
     const bool aligned = p.K % 8 == 0;
     const long long kp = aligned ? p.K : up(p.K + front, 64);
     // X: rows without a target are zeros in dW's product, whatever they hold (0 times an
-    // infinity is a NaN).  Of classes a copy with each front, one of them 0 (dW's operand)
+    // infinity is a NaN).  Of classes a copy with each front, and for dW one turned for each
     const bool copy_x = p.dW || !aligned || !on16(p.X), pad_w = !CLASSES && (!aligned || !on16(p.W));
-    int x0 = 0;
-    while (CLASSES && x0 < G && cl.shift(x0)) ++x0;
-    const int copies = std::max(G, x0 + 1);
+    const int copies = CLASSES && p.dW ? 2 * G : G;
+    unsigned long long turns = 0;
+    if (CLASSES) {
+        const Classes out(p.dW, p.K);
+        for (int r = 0; r < G; ++r) turns |= (unsigned long long)(-out.shift(r) & 7) << (4 * r);
+    }
     long long vp;
     if (CLASSES) {
         vp = head_class_rows(p.N, G) * G;
@@ -663,7 +717,7 @@ cudaError_t backward(const HeadBackward &p, const Classes &cl, int dev, int *sta
     }
     const uint16_t *x = static_cast<const uint16_t *>(p.X);
     if (e == cudaSuccess && copy_x) {
-        e = copy(p.X, p.M, p.K, base + at_x, kp, p.dW ? p.target : nullptr, p.dW ? p.N : 1, find, s, copies, CLASSES ? cl.shifts : 0);
+        e = copy(p.X, p.M, p.K, base + at_x, kp, p.dW ? p.target : nullptr, p.dW ? p.N : 1, find, s, copies, CLASSES ? cl.shifts : 0, p.dW ? turns << (4 * G) : 0);
         x = reinterpret_cast<const uint16_t *>(base + at_x);
     }
     for (long long v0 = 0; v0 < p.N && e == cudaSuccess; v0 += vp) {
@@ -712,31 +766,46 @@ cudaError_t backward(const HeadBackward &p, const Classes &cl, int dev, int *sta
             epi.classes = G;
             epi.bf16 = bf16;
             const Args a = {p.M, CLASSES ? class_tiles * G * pl.bn : n, num_kb, pl.bn, 0, 0, (int)pl.tiles, 1, pl.joined, box, BK, pl.rows,
-                            class_tiles, 0, cl.shifts, status};
+                            class_tiles, 0, cl.shifts, 0, status};
             e = launch_dz<FORMAT, CLASSES>(ta, tb, epi, a, pl.clusters, s);
         }
         if (e == cudaSuccess && p.dW) {
-            OutEpi epi;
             CUtensorMap tx;
             uint16_t *out = static_cast<uint16_t *>(p.dW) + v0 * p.K;
-            const bool tma = aligned && on16(p.dW);
-            const int k_rows = p.M <= 48 ? (p.M + 15) / 16 * 16 : BK;
-            if (!map_operand(&ta, z, FORMAT, true, z_rows, p.M, vp, 0, k_rows) ||
-                !map_operand(&tx, x + (long long)x0 * p.M * kp, FORMAT, true, kp, p.M, kp, 0, k_rows) ||
-                !map16(&epi.tm, tma ? (const void *)out : z, FORMAT, n, tma ? p.K : 64, tma ? p.K : 64, 32, 64)) {
-                e = cudaErrorInvalidValue;
-                break;
+            const int k_rows = p.M <= 48 ? (p.M + 15) / 16 * 16 : BK, class_rows = (int)(vp / G);
+            const Args a = {z_rows, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, 256, 0, 0, 0,
+                            CLASSES ? class_rows : 0, status};
+            bool ok = map_operand(&ta, z, FORMAT, true, z_rows, p.M, vp, 0, k_rows) &&
+                      make_map3(&tx, x + (CLASSES ? G * (long long)p.M * kp : 0), map_type(FORMAT), kp, p.M, G, kp * 2, p.M * kp * 2, 64,
+                                k_rows, 1, 128);
+            if constexpr (CLASSES) {
+                TurnEpi epi;
+                epi.tm = {};
+                for (int r = 0; r < G && ok; ++r) {
+                    const int u = (int)(turns >> (4 * r) & 7);
+                    ok = map16(&epi.tm.m[r], out + (long long)r * p.K + u, FORMAT, (n - r + G - 1) / G, (p.K - u) / 8 * 8, (long long)G * p.K, 32, 64);
+                }
+                epi.scale = scale;
+                epi.out = out;
+                epi.classes = G;
+                epi.class_rows = class_rows;
+                epi.turns = (uint32_t)turns;
+                epi.M = n;
+                epi.N = p.K;
+                epi.bf16 = bf16;
+                e = ok ? launch<FORMAT>(ta, tx, epi, a, cw, s) : cudaErrorInvalidValue;
+            } else {
+                OutEpi epi;
+                const bool tma = aligned && on16(p.dW);
+                ok = ok && map16(&epi.tm, tma ? (const void *)out : z, FORMAT, n, tma ? p.K : 64, tma ? p.K : 64, 32, 64);
+                epi.scale = scale;
+                epi.out = tma ? nullptr : out;
+                epi.ld = p.K;
+                epi.M = n;
+                epi.N = p.K;
+                epi.bf16 = bf16;
+                e = ok ? launch<FORMAT>(ta, tx, epi, a, cw, s) : cudaErrorInvalidValue;
             }
-            epi.scale = scale;
-            epi.out = tma ? nullptr : out;
-            epi.ld = p.K;
-            epi.classes = G;
-            epi.class_rows = (int)(vp / G);
-            epi.M = n;
-            epi.N = p.K;
-            epi.bf16 = bf16;
-            const Args a = {z_rows, p.K, (int)ceil_div(p.M, BK), 256, 1, 1, (int)w_tiles, 1, 1, 128, k_rows, 256, 0, 0, 0, status};
-            e = launch<FORMAT>(ta, tx, epi, a, cw, s);
         }
         if (e == cudaSuccess && p.dX) {
             AccEpi<CLASSES> epi;
@@ -754,7 +823,7 @@ cudaError_t backward(const HeadBackward &p, const Classes &cl, int dev, int *sta
             // (a short last piece: fewer ranges, each of one block at least)
             const int kb = (int)ceil_div(cn, BK), ranges = std::min(splits, kb);
             const Args a = {p.M, (int)x_cols, kb, 256, 0, 1, (int)x_tiles, ranges * G, 1, box, BK, tile_rows(p.M), 0, CLASSES ? ranges : 0,
-                            cl.shifts, status};
+                            cl.shifts, 0, status};
             e = launch<FORMAT>(ta, tb, epi, a, cx, s);
         }
     }
@@ -777,7 +846,7 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
     // a slab of dX for each class: for fewer rows yet, and a W of 8 MB or more (22 x 60179 x 951
     // 125 us against 151, 1 x 32000 x 4095 230 against 293; 300 x 40000 x 1501 197 against 189,
     // 1 x 1000 x 130 24.7 against 22.6)
-    const bool classes = cl.pay(16LL * p.M, p.N) && (long long)p.N * p.K >= 4 << 20;
+    const bool classes = cl.pay(16LL * p.M, p.N) && p.K >= 64 && (long long)p.N * p.K >= 4 << 20;
     return classes && z <= kPiece && slabs <= kPiece ? backward<T, FORMAT, true>(p, cl, dev, status, s)
                                                      : backward<T, FORMAT, false>(p, cl, dev, status, s);
 }

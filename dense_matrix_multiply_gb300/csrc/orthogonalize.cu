@@ -435,7 +435,7 @@ cudaError_t run(const OrthProblem &p, int dev, int num_sms, int *status, cudaStr
     if (tma_out) ok = ok && map16(&res, p.O, bf16 ? 1 : 0, p.M, p.N, p.ldo, 32, 64);
     if (!ok && e == cudaSuccess) e = cudaErrorInvalidValue;
     auto args = [&](int rows, int cols, int k, const Plan &q, bool a_mn, bool b_mn) {
-        return Args{rows, cols, (int)ceil_div(k, BK), q.bn, a_mn, b_mn, (int)q.tiles, 1, q.joined, 128, BK, 256, 0, 0, 0, status};
+        return Args{rows, cols, (int)ceil_div(k, BK), q.bn, a_mn, b_mn, (int)q.tiles, 1, q.joined, 128, BK, 256, 0, 0, 0, 0, status};
     };
     for (int i = 0; i < p.steps && e == cudaSuccess; ++i) {
         const int in = i & 1, out = in ^ 1;

@@ -88,6 +88,7 @@ struct Args {
     // columns), and s_r, four bits each.
     int class_tiles, class_splits;
     uint32_t shifts;
+    int b_rows;  // rows of D to a matrix of B, MN-major (0: one for all)
     int *status;
 };
 // B's tensor maps, one of each class.
@@ -358,6 +359,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMa
             const int cls = class_of(u, t, col0), row0 = t.m * 256 + (int)rank * (args.rows >> 1);
             col0 += (int)rank * (bn >> 1);
             const CUtensorMap *const tmB = &mapsB.m[cls];
+            const int b_at = args.b_rows ? t.m * 256 / args.b_rows : 0;
             for (int kb = kb0; kb < kb1; ++kb) {
                 if (!mbar_wait(&bars->empty[stage], phase ^ 1u, abort_flag, true)) { ok = false; break; }
                 const uint32_t full = map_to_rank(&bars->full[stage], lead);
@@ -372,7 +374,7 @@ pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BMa
                     }
                     if (args.b_mn) {
                         for (int c = 0; c < (bn >> 1); c += 64)
-                            tma_load_3d_pair(b + (c >> 6) * BOX64, tmB, full, col0 + c, kb * BK, 0);
+                            tma_load_3d_pair(b + (c >> 6) * BOX64, tmB, full, col0 + c, kb * BK, b_at);
                     } else {
                         tma_load_3d_pair(b, tmB, full, kb * BK, col0, 0);
                     }
