@@ -6,6 +6,9 @@
 // + sum e^(z - m')), and the row's own target's logit.  A second kernel joins the pairs
 // of a row, in order: lse = m + log s.  All in FP32.
 //
+// Rows of W off 16 bytes (K no multiple of 8) are read in place by classes of their alignment
+// where there are few rows of X against them (Classes; pair_pipe.cuh), else copied, padded.
+//
 // Backward, in pieces of the vocabulary: the piece's logits anew, dZ = (e^(z - lse) -
 // [j = t]) dloss rounded to 16 bits (the operand of the products to come) in scratch,
 // dW of the piece = dZ^T X, and dX += dZ W in FP32.  Where a piece of dX has few tiles
@@ -571,7 +574,7 @@ cudaError_t forward(const HeadProblem &p, int dev, int *status, cudaStream_t s) 
     const int rows = std::min(p.M, rows_max);
     const bool off_w = !aligned || !on16(p.W);
     const Classes cl(p.W, p.K);
-    const bool classes = cl.pay(rows, p.N);
+    const bool classes = cl.pay(rows, p.N) && 2LL * cl.n * rows * up(p.K + 7LL, 64) <= kPiece;
     const bool pad_w = off_w && !classes, pad_x = classes || !aligned || !on16(p.X);
     const long long kp = classes ? up(p.K + 7LL, 64) : aligned ? p.K : up(p.K, 64);
     const long long vp = pad_w ? std::min<long long>(up(p.N, 256), std::max<long long>(kPiece / (2 * kp) / 256 * 256, 256)) : p.N;
@@ -844,8 +847,8 @@ cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s
     const Classes cl(p.W, p.K);
     const long long z = 2LL * p.M * head_class_rows(p.N, cl.n) * cl.n, slabs = 4LL * cl.n * p.M * up(p.K + 10LL, 64);
     // a slab of dX for each class: for fewer rows yet, and a W of 8 MB or more (22 x 60179 x 951
-    // 125 us against 151, 1 x 32000 x 4095 230 against 293; 300 x 40000 x 1501 197 against 189,
-    // 1 x 1000 x 130 24.7 against 22.6)
+    // 101 us against 151, 1 x 32000 x 4095 180 against 293; dX of 300 x 40000 x 1501 130 against
+    // 128, 1 x 1000 x 130 18.2 against 16.9)
     const bool classes = cl.pay(16LL * p.M, p.N) && p.K >= 64 && (long long)p.N * p.K >= 4 << 20;
     return classes && z <= kPiece && slabs <= kPiece ? backward<T, FORMAT, true>(p, cl, dev, status, s)
                                                      : backward<T, FORMAT, false>(p, cl, dev, status, s);

@@ -414,10 +414,9 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H,
  * logarithm in FP32.  Any M, N, K; K and the bases multiples of 8 elements are fastest:
  * of other operands X is copied to padded rows in scratch (up to eight times), W read in
  * place where K is no multiple of 8 and N large against M, else copied too, a piece (up to
- * 256 MiB) at a time.  Scratch:
- * 8 bytes for each row and 64 to 128 entries, for up to 16384 rows at once, and the copies, in
- * stream-ordered memory for the duration of the call from the library's pool (see
- * gemm_gated).  K = 0: logits of 0; N = 0: lse is -inf.  GEMM_ERR_ALIAS if an output
+ * 256 MiB) at a time.  Scratch: 8 bytes for each row and 64 to 128 entries, for up to 16384
+ * rows at once, and the copies, in stream-ordered memory for the duration of the call from
+ * the library's pool (see gemm_gated).  K = 0: logits of 0; N = 0: lse is -inf.  GEMM_ERR_ALIAS if an output
  * overlaps an input or the other output. */
 GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
                                           float *loss, float *lse, int M, int N, int K);
@@ -432,8 +431,8 @@ GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, con
  * probabilities are not lost; loss scales up to FP32's range do no harm), the operand of
  * the products, whose sums are FP32, in a fixed order, rounded once.  Scratch as above:
  * a piece of dZ (256 MiB, or 256 entries of every row where that is more), FP32 sums of
- * dX (up to 256 MiB, or once 4 M K bytes where that is more) and a copy of X (for dW, with
- * zeros in the rows left out).  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as above. */
+ * dX (up to 256 MiB, or once 4 M K bytes where that is more) and copies of X (one for
+ * dW, with zeros in the rows left out; up to sixteen where W is read in place).  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as above. */
 GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
                                                    const float *lse, const float *dloss, void *dX, void *dW, int M, int N,
                                                    int K);
