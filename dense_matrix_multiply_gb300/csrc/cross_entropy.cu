@@ -102,12 +102,12 @@ struct LseEpi : LseArgs {
     }
 };
 
-// Scale factors of dZ: (up, down), powers of two whose product is 1.
+// Scale factors of dZ: (up, down), whose product is 1 but for rounding.
 struct DzArgs {
     CUtensorMap tm;  // dZ of the piece
     const float *lse, *dloss;
     const long long *target;
-    const float2 *scale;  // null: 1
+    const float2 *scale;
     int M, N, v0, total;  // total: columns of Z
     int classes;          // of columns (N: of the largest class): a matrix of dZ each
     bool bf16;
@@ -123,7 +123,7 @@ struct DzEpi : DzArgs {
         const int row = p.row0 + p.lane;
         long long t = row < M ? target[row] : -1;
         const bool counts = t >= 0 && t < total;
-        const float d = counts ? dloss[row] * (scale ? scale->x : 1.0f) : 0.0f;
+        const float d = counts ? dloss[row] * scale->x : 0.0f;
         const float base = counts ? lse[row] * kLog2e : 0.0f;
         t = counts ? t - v0 : -1;
         int cols = N;
@@ -216,7 +216,7 @@ struct OutEpi {
     static constexpr bool LOWER = false, JOIN = false, CLASSES = false;
     static constexpr int BOXES = 2;
     CUtensorMap tm;
-    const float2 *scale;  // null: 1
+    const float2 *scale;
     uint16_t *out;        // not null: by the element, rows ld apart
     long long ld;
     int M, N;
@@ -225,7 +225,7 @@ struct OutEpi {
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
     __device__ __forceinline__ void run(Part &p, const Pre &) const {
-        const float f = scale ? scale->y : 1.0f;
+        const float f = scale->y;
 #pragma unroll 1
         for (int g = p.first; g < p.first + p.width; g += 64) {
             const int c0 = p.col0 + g;
@@ -250,7 +250,7 @@ struct TurnEpi {
     static constexpr bool LOWER = false, JOIN = false, CLASSES = false;
     static constexpr int BOXES = 2;
     BMaps<true> tm;
-    const float2 *scale;  // null: 1
+    const float2 *scale;
     uint16_t *out;
     int classes, class_rows;
     uint32_t turns;  // u_r, four bits each
@@ -260,7 +260,7 @@ struct TurnEpi {
     struct Pre {};
     __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
     __device__ __forceinline__ void run(Part &p, const Pre &) const {
-        const float f = scale ? scale->y : 1.0f;
+        const float f = scale->y;
         const int cls = p.row0 / class_rows, row0 = p.row0 - cls * class_rows, rows = (M - cls + classes - 1) / classes;
         if (row0 >= rows) return;
         const int u = turns >> (4 * cls) & 7, whole = (N - u) & ~7;
@@ -356,13 +356,17 @@ head_flat_kernel(const long long *__restrict__ target, float *__restrict__ loss,
     if (lse) lse[row] = l;
 }
 
-// Half precision: the power of two that takes the largest |dloss| of a row with a target
-// to [2^14, 2^15), so that dZ, at most as large, keeps half's full precision down to
-// probabilities of 2^-28; and its inverse.  By a CTA.
+// The factor that takes the largest |dloss| of a row with a target to `peak`, and its inverse.
+// peak is a power of two, so that where all rows weigh alike a probable target's dZ, -peak
+// (1 - p), is nearly representable: a weight of 1 / 777 in 16 bits is off by a relative 2^-9
+// or less, but by the same in every row, and both gradients with it (bf16, 1100 x
+// 5000 x 512, weights of 1 / 848: 0.0034 off against 0.0017).  Half: 2^14, so that dZ keeps half's full precision
+// down to probabilities of 2^-28.  By a CTA.
 struct ScaleArgs {
     const float *dloss;
     const long long *target;
     float2 *scale;
+    float peak;
     int M, N;
 };
 template <int THREADS>
@@ -381,12 +385,9 @@ __device__ __forceinline__ void find_scale(const ScaleArgs &a) {
     __syncthreads();
     if (threadIdx.x != 0) return;
     for (int w = 1; w < THREADS / 32; ++w) top = fmaxf(top, tops[w]);
-    int e = 0;
-    if (top > 0.0f && isfinite(top)) {
-        frexpf(top, &e);
-        e = max(min(15 - e, 126), -126);
-    }
-    *a.scale = make_float2(ldexpf(1.0f, e), ldexpf(1.0f, -e));
+    // (no factor leaves the normal numbers)
+    top = top > 0.0f && isfinite(top) ? fminf(fmaxf(top, 0x1p-110f), 0x1p110f) : a.peak;
+    *a.scale = make_float2(a.peak / top, top / a.peak);
 }
 __global__ void __launch_bounds__(1024)
 head_scale_kernel(const ScaleArgs a)
@@ -474,7 +475,7 @@ head_finish_kernel(const float *__restrict__ slab, int slabs, long long rows, in
             v.x += w.x; v.y += w.y; v.z += w.z; v.w += w.w;
         }
     }
-    const float f = scale ? scale->y : 1.0f;
+    const float f = scale->y;
     T *o = out + row * cols + c;
     if (((uintptr_t)o & 7) == 0 && c + 4 <= cols) {
         *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(v.x * f, v.y * f, (T *)nullptr), pack2(v.z * f, v.w * f, (T *)nullptr));
@@ -709,11 +710,11 @@ cudaError_t backward(const HeadBackward &p, const Classes &cl, int dev, int *sta
     uint8_t *base = static_cast<uint8_t *>(ws);
     cudaLaunchAttribute attr[1];
     const bool bf16 = FORMAT == 1;
-    ScaleArgs find = {};
-    if (!bf16) find = {p.dloss, p.target, reinterpret_cast<float2 *>(base + at_scale), p.M, p.N};
-    const float2 *scale = find.scale;
-    // X's copy finds the scale of few rows (a launch less: 1.3 us)
-    if (!bf16 && (!copy_x || p.M > 1024)) {
+    ScaleArgs find = {p.dloss, p.target, reinterpret_cast<float2 *>(base + at_scale), bf16 ? 1.0f : 16384.0f, p.M, p.N};
+    const float2 *const scale = find.scale;
+    // X's copy finds the scale of few rows (1100 x 5000 x 512 39.2 us, in a launch of its own
+    // 41.0; 2000 x 5000 x 512 50.2 and 49.7)
+    if (!copy_x || p.M > 1536) {
         const cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(1024), 0, s, attr);
         e = launch_counted(&cfg, head_scale_kernel, find);
         find = {};

@@ -427,9 +427,9 @@ GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, con
  *     dX = dZ W,  dW = dZ^T X
  * dX [M,K], dW [N,K] (dtype), each overwritten; a null one is left out.  The logits are
  * computed anew, a piece of the vocabulary at a time; dZ is formed in FP32 and rounded to
- * dtype (half: scaled by a power of two from the largest |dloss|, so that small
- * probabilities are not lost; loss scales up to FP32's range do no harm), the operand of
- * the products, whose sums are FP32, in a fixed order, rounded once.  Scratch as above:
+ * dtype, scaled by the largest |dloss| (so that neither small probabilities nor a weight
+ * that dtype does not hold exactly are lost; any loss scale does), the operand of the
+ * products, whose sums are FP32, in a fixed order, rounded once.  Scratch as above:
  * a piece of dZ (256 MiB, or 256 entries of every row where that is more), FP32 sums of
  * dX (up to 256 MiB, or once 4 M K bytes where that is more) and copies of X (one for
  * dW, with zeros in the rows left out; up to sixteen where W is read in place).  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as above. */

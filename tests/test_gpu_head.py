@@ -156,6 +156,23 @@ def test_large_logits(spread):
     check(run("bf16", data, 70, 1000, 256), data, "bf16")
 
 
+@pytest.mark.parametrize("weight", [1.0 / 777, 1.0 / 848, 0.3])
+def test_a_common_weight_is_not_rounded(weight):
+    """bf16: all rows weigh alike, by what bf16 does not hold (0.0012 to 0.0028 off), and the
+    most of dZ is the targets' -weight (1 - p), p 1/4000 or so.  Scaled so that weight is a
+    power of two it rounds to -weight for p < 2^-9: the gradients' projections on the right
+    ones are 1 + p, 2.5e-4 and the rounding of many independent results, whose mean of 38400
+    and more, 2^-9 at most each, is below 1e-4."""
+    M, N, K = 300, 4000, 128
+    X, W, t, _ = make(M, N, K, "bf16", 11, spread=0.5, left_out=0.0)
+    d = torch.full((M,), weight, dtype=torch.float32)
+    got = run("bf16", (X, W, t, d), M, N, K)
+    dX, dW, _ = ref.backward(*(x.double().numpy() if x.is_floating_point() else x.numpy() for x in (X, W, t, d)))
+    for k, want in (("dX", dX), ("dW", dW)):
+        have = got[k].double().cpu().numpy()
+        assert abs((have * want).sum() / (want * want).sum() - 1) < 5e-4, k
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1e-6, 2.0 ** 14])
 def test_weights_of_the_losses_from_tiny_to_large(scale):
     """Half precision: dZ keeps its precision whatever dloss is (results below half's
