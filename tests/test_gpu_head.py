@@ -354,6 +354,86 @@ def test_captured_and_replayed_beside_another_stream():
             assert torch.equal(x.reshape(want[1][k].shape), want[1][k]), k
 
 
+def test_captured_and_replayed_off_16_bytes():
+    """Rows off 16 bytes, a large vocabulary, dW off another way than W: the same bits from a
+    graph and beside it."""
+    M, N, K = 5, 33001, 131
+    a, b = make(M, N, K, "bf16", 15), make(M, N, K, "bf16", 16)
+    want = [run("bf16", x, M, N, K) for x in (a, b)]
+    bufs = [x.cuda() for x in a]
+    loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    dX, (whole, dW) = torch.empty(M, K, dtype=torch.bfloat16, device="cuda"), guarded(N * K, torch.bfloat16, 5)
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            g.gemm_cross_entropy("bf16", bufs[0], bufs[1], bufs[2], loss, lse, M, N, K)
+            g.gemm_cross_entropy_backward("bf16", bufs[0], bufs[1], bufs[2], lse, bufs[3], dX, dW, M, N, K)
+    eb = [x.cuda() for x in b]
+    eo = [torch.empty(n, dtype=dt, device="cuda") for n, dt in ((M, torch.float32), (M, torch.float32), (M * K, torch.bfloat16), (N * K, torch.bfloat16))]
+    torch.cuda.synchronize()
+    for data, w in ((a, want[0]), (b, want[1])):
+        with torch.cuda.stream(s):
+            for x, v in zip(bufs, data):
+                x.copy_(v)
+            graph.replay()
+        with torch.cuda.stream(other):
+            g.gemm_cross_entropy("bf16", eb[0], eb[1], eb[2], eo[0], eo[1], M, N, K)
+            g.gemm_cross_entropy_backward("bf16", eb[0], eb[1], eb[2], eo[1], eb[3], eo[2], eo[3], M, N, K)
+        torch.cuda.synchronize()
+        for k, x, y in zip(("loss", "lse", "dX", "dW"), (loss, lse, dX, dW), eo):
+            assert torch.equal(x.reshape(w[k].shape), w[k]), k
+            assert torch.equal(y.reshape(w[k].shape), want[1][k]), k
+        h = whole.float()
+        assert (h[:5] == FILL).all() and (h[5 + N * K:] == FILL).all()
+
+
+def test_past_2_31_elements_off_16_bytes():
+    """The same of rows off 16 bytes: entries of zeros before the last 500."""
+    K, tail, M = 8191, 500, 3
+    N = (1 << 31) // K + tail
+    X, Wt, t, d = make(M, tail, K, "bf16", 17, left_out=0.0)
+    W = torch.zeros(N, K, dtype=torch.bfloat16, device="cuda")
+    W[-tail:].copy_(Wt)
+    loss, lse, dX = torch.empty(M, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    dW = torch.empty_like(W)
+    x, tt = X.cuda(), (t + N - tail).cuda()
+    g.gemm_cross_entropy("bf16", x, W, tt, loss, lse, M, N, K)
+    g.gemm_cross_entropy_backward("bf16", x, W, tt, lse, d.cuda(), dX, dW, M, N, K)
+    g.gemm_synchronize()
+    Xd, Wd, td, dd = X.double().numpy(), Wt.double().numpy(), t.numpy(), d.double().numpy()
+    Z = Xd @ Wd.T
+    want = np.log(np.exp(Z).sum(1) + (N - tail))
+    assert np.allclose(lse.cpu().numpy(), want, rtol=1e-5)
+    dZ = np.exp(Z - want[:, None])
+    dZ[np.arange(M), td] -= 1
+    dZ *= dd[:, None]
+    for got, ex in ((dX, dZ @ Wd), (dW[-tail:], dZ.T @ Xd)):
+        got = got.double().cpu().numpy()
+        assert np.linalg.norm(got - ex) <= 0.01 * np.linalg.norm(ex)
+    first = (np.exp(-want) * dd) @ Xd
+    got = dW[[0, N // 2, N - tail - 1]].double().cpu().numpy()
+    assert np.linalg.norm(got - first) <= 0.01 * np.linalg.norm(np.tile(first, (3, 1)))
+    del W, dW
+    torch.cuda.empty_cache()
+
+
+def test_pieces_of_rows_off_16_bytes():
+    """More than 16384 rows against a vocabulary that is read in place: rows of both pieces."""
+    M, N, K = 16400, 540001, 65
+    X, W, t, _ = make(M, N, K, "bf16", 18, left_out=0.0)
+    loss, lse = torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    g.gemm_cross_entropy("bf16", X.cuda(), W.cuda(), t.cuda(), loss, lse, M, N, K)
+    g.gemm_synchronize()
+    rows = torch.tensor([0, 1, 8000, 16383, 16384, 16399])
+    Xr, tr = X[rows], t[rows]
+    want, wlse, _ = ref.forward(Xr.double().numpy(), W.double().numpy(), tr.numpy())
+    tl, te = ref.forward_tolerance(Xr.double().numpy(), W.double().numpy(), tr.numpy())
+    close(loss[rows.cuda()], want, tl, "loss")
+    close(lse[rows.cuda()], wlse, te, "lse")
+
+
 def test_empty_sizes():
     """No hidden units: logits of 0; no vocabulary; no rows."""
     t, z = torch.tensor([3, -1, 9], device="cuda"), torch.empty(0, dtype=torch.bfloat16, device="cuda")
