@@ -847,10 +847,11 @@ template <typename T, uint32_t FORMAT>
 cudaError_t backward(const HeadBackward &p, int dev, int *status, cudaStream_t s) {
     const Classes cl(p.W, p.K);
     const long long z = 2LL * p.M * head_class_rows(p.N, cl.n) * cl.n, slabs = 4LL * cl.n * p.M * up(p.K + 10LL, 64);
-    // a slab of dX for each class: for fewer rows yet, and a W of 8 MB or more (22 x 60179 x 951
-    // 101 us against 151, 1 x 32000 x 4095 180 against 293; dX of 300 x 40000 x 1501 130 against
-    // 128, 1 x 1000 x 130 18.2 against 16.9)
-    const bool classes = cl.pay(16LL * p.M, p.N) && p.K >= 64 && (long long)p.N * p.K >= 4 << 20;
+    // a slab of dX for each class: for fewer rows yet, and a W of 4 MB or more (22 x 60179 x 951
+    // 101 us against 151, 1 x 32000 x 4095 180 against 293, 300 x 40000 x 1500 152 against 193;
+    // 300 x 12000 x 2001 98 both ways, 1000 x 50000 x 2001 480 against 447, 30 x 3000 x 701 32
+    // against 29)
+    const bool classes = cl.pay(8LL * p.M, p.N) && p.K >= 64 && (long long)p.N * p.K >= 2 << 20;
     return classes && z <= kPiece && slabs <= kPiece ? backward<T, FORMAT, true>(p, cl, dev, status, s)
                                                      : backward<T, FORMAT, false>(p, cl, dev, status, s);
 }
