@@ -543,6 +543,7 @@ struct Classes {
     uint32_t shifts;
 
     Classes(const void *w, int K) : n(1), shifts(0) {
+        if (K < 8) return;  // a class's rows, up to seven elements in front, would overlap
         while (n * (K % 8) % 8) n *= 2;
         for (int r = 0; r < n; ++r) shifts |= (uint32_t)(((uintptr_t)w / 2 + (uintptr_t)r * (K % 8)) % 8) << (4 * r);
     }

@@ -4,12 +4,13 @@
 //
 // A 256 x bn tile (bn 128, 192 or 256; 192 only where B lies K-major) belongs to a cluster of
 // two CTAs (tcgen05 cta_group::2), 128 rows of A and half of B's columns loaded by each, K in
-// stages of 64; up to 128 rows may go in 128 x 256 tiles, 64 of them to a CTA.  Either operand may lie K-major (rows of adjacent k) or MN-major (k by k, adjacent
-// rows or columns), as its tensor map and the flags say.  Warp 0 loads, warp 1 of the
-// leader issues the MMAs -- both converged, one elected lane for the instructions -- and
-// warps 2-9 write out, 32 rows and half of the columns to each.  Two accumulators, so
-// that a tile is written while the next is computed.  Clusters walk over the units (a
-// tile, or one of its K ranges) in the same order.
+// stages of 64; up to 128 rows may go in 128 x 256 tiles, 64 of them to a CTA.  Either
+// operand may lie K-major (rows of adjacent k) or MN-major (k by k, adjacent rows or
+// columns), as its tensor map and the flags say.  Warp 0 loads, warp 1 of the leader issues
+// the MMAs -- both converged, one elected lane for the instructions -- and warps 2-9 write
+// out, 32 rows and half of the columns to each.  Two accumulators, so that a tile is
+// written while the next is computed.  Clusters walk over the units (a tile, or one of its
+// K ranges) in the same order.
 //
 // Where there are few tiles of a long K, two pairs of one cluster are joined on a tile of
 // 256 x 128, half of K each: every CTA stores the FP32 sums of the other pair's 64 columns

@@ -117,6 +117,13 @@ def test_rows_of_the_vocabulary_off_16_bytes(M, N, K, off):
     check(run("bf16", data, M, N, K, off), data, "bf16")
 
 
+@pytest.mark.parametrize("K,off", [(1, 3), (2, 0), (2, 1), (2, 7), (4, 0), (4, 1), (4, 3), (6, 5), (7, 2), (12, 7)])
+def test_few_hidden_units_off_16_bytes(K, off):
+    """Rows shorter than the elements that may lie in front of them."""
+    data = make(3, 2000, K, "bf16", K + off)
+    check(run("bf16", data, 3, 2000, K, off), data, "bf16")
+
+
 LARGE_OFF = [(1, 20000, 257, 0), (5, 33001, 131, 1), (3, 8200, 516, 3), (2, 9001, 514, 1), (16, 70001, 67, 0), (70, 72000, 68, 0)]
 
 
