@@ -748,8 +748,11 @@ cudaError_t with_split(int wpr, F f) {
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_smem(void (*kern)(KArgs...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args... args) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // Above 48 KB, a kernel's own few hundred bytes included, a launch needs leave: for as much
+    // as any takes, so that no call takes back what another, on another thread, is about to use.
+    constexpr size_t kFree = 47 * 1024, kMost = 224 * 1024;
+    if (smem > kFree) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (e != cudaSuccess) {
             cudaGetLastError();
             return e;

@@ -1,6 +1,10 @@
 """The root-mean-square norm with residual on the GPU, through the C ABI, against 64-bit
 values within norm_ref's tolerances."""
 
+import subprocess
+import sys
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -297,3 +301,27 @@ def test_no_rows():
     g.gemm_rms_norm("bf16", z, None, z, EPS, None, z, None, 0, 8)
     g.gemm_synchronize()
     assert not dw.any()
+
+
+FIRST = """
+import sys
+import torch
+import dense_matrix_multiply_gb300 as g
+for K in map(int, sys.argv[1:]):
+    for name, dt in (("bf16", torch.bfloat16), ("f16", torch.float16)):
+        X, w, dY = (torch.randn(n, device="cuda").to(dt) for n in (8 * K, K, 8 * K))
+        Y, dX = torch.empty_like(X), torch.empty_like(X)
+        rstd, dw = torch.empty(8, device="cuda"), torch.empty(K, device="cuda")
+        g.gemm_rms_norm(name, X, None, w, 1e-5, None, Y, rstd, 8, K)
+        g.gemm_rms_norm_backward(name, X, w, rstd, dY, None, dX, dw, 8, K)
+g.gemm_synchronize()
+"""
+
+
+@pytest.mark.parametrize("sizes", [("256", "8121"), ("8105", "8167")])
+def test_first_calls_of_a_process(sizes):
+    """Sizes whose shared memory, with what the kernel itself declares, just passes the 48 KB
+    that need no leave, before any larger call has asked for it."""
+    root = Path(__file__).resolve().parents[1]
+    r = subprocess.run([sys.executable, "-c", FIRST, *sizes], cwd=root, capture_output=True, text=True, timeout=180)
+    assert r.returncode == 0, r.stderr[-2000:]
