@@ -274,6 +274,7 @@ struct TurnEpi {
             uint8_t *box = box_next<BOXES>(p);
             box_put(box, p.lane, z);
             if (c0 < whole) box_store(&tm.m[cls], box, p.lane, c0, row0, 0);
+            else box_unstored(p.lane);  // 64 columns of a row's tail alone: K of 64 i + 1 to 64 i + 14
             if (row0 + p.lane < rows) {
                 for (int c = max(c0, whole); c < min(c0 + 64, N); ++c) {
                     const int e = c - c0;

@@ -229,7 +229,9 @@ __device__ __forceinline__ void box_begin(int lane) {
     if (lane == 0) tma_stores_read_wait0();
     __syncwarp();
 }
-// One box, or two in turn: the next one, once the store that last read it has done so.
+// One box, or two in turn: the next one, once the store that last read it has done so.  Of two
+// all groups of stores but the youngest are waited for, so that every turn has to commit one
+// group: box_store, or box_unstored in a turn that stores nothing.
 template <int BOXES>
 __device__ __forceinline__ uint8_t *box_next(Part &p) {
     if (BOXES == 1) {
@@ -246,6 +248,9 @@ __device__ __forceinline__ void box_store(const CUtensorMap *map, const uint8_t 
     fence_async_shared();
     __syncwarp();
     if (lane == 0) tma_store_3d(map, box, x, y, z);
+}
+__device__ __forceinline__ void box_unstored(int lane) {
+    if (lane == 0) tma_store_none();
 }
 __device__ __forceinline__ void tma_add_3d(const CUtensorMap *map, const void *src, int x, int y, int z) {
     asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(

@@ -114,6 +114,8 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void 
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+// A group of no stores, complete at once.
+__device__ __forceinline__ void tma_store_none() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // A tile to L2 ahead of its load: a hint, no shared memory and no barrier.
 __device__ __forceinline__ void tma_prefetch_l2_3d(const CUtensorMap *map, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
