@@ -186,8 +186,9 @@ struct FwdArgs {
 __host__ __device__ constexpr int row_warps(int wpr) { return wpr < 4 ? 4 : wpr; }
 
 // Squares of bf16 overflow from 2^64 on: a row whose sum does is summed again of values
-// taken down by 2^70 (half's squares stay within FP32).
-constexpr float kDown = 8.470329472543003e-22f;  // 2^-70
+// taken down by 2^80, whose squares are below 2^96, the sum of 2^31 of them below 2^127
+// (half's squares stay within FP32).
+constexpr float kDown = 0x1p-80f;
 template <typename T>
 constexpr bool kMayOverflow = std::is_same<T, __nv_bfloat16>::value;
 // 1 / sqrt(mean + eps) of values times `by`
