@@ -185,16 +185,65 @@ struct FwdArgs {
 };
 __host__ __device__ constexpr int row_warps(int wpr) { return wpr < 4 ? 4 : wpr; }
 
-// Squares of bf16 overflow from 2^64 on: a row whose sum does is summed again of values
-// taken down by 2^80, whose squares are below 2^96, the sum of 2^31 of them below 2^127
-// (half's squares stay within FP32).
-constexpr float kDown = 0x1p-80f;
+// A row's scales, from its sum of squares and, for E4M3, the largest |w H|, top: |Y| rises with
+// it.  They come from one pass over the row; of bf16, at the ends of its range, from two or
+// three, each with H times another power of two:
+//   squares overflow from 2^64 on: a row whose sum does is taken down by 2^80, its squares
+//     below 2^96, the sum of 2^31 of them below 2^127;
+//   a top below 2^-100 (448 / amax overflows from 2^-119 on): up by 2^100, or by 2^60 where
+//     elements may be above 1 (below 2^64: the sum is finite);
+//   a top past FP32's largest, where Y need not be: by rstd's power of two, H rstd being
+//     below sqrt(K).
+// (Half's squares, and w H between 2^-48 and 2^32, stay within FP32.)
+constexpr float kDown = 0x1p-80f, kLeast = 0x1p-100f;
 template <typename T>
 constexpr bool kMayOverflow = std::is_same<T, __nv_bfloat16>::value;
-// 1 / sqrt(mean + eps) of values times `by`
-__device__ __forceinline__ float rstd_of(float sum, int K, float eps, float by) {
-    return 1.0f / sqrtf(sum / (float)K + eps * by * by);
-}
+template <typename T, bool E4M3>
+struct RowScales {
+    float by = 1.0f;     // what H is to be multiplied by, all passes' together, and the last one's
+    float last = 1.0f;
+    float r, rstd;       // 1 / sqrt(mean + eps) of the values summed; of H
+    float q, amax;       // E4M3: codes are of H by w q = Y / down, whose largest is amax
+    float down = 1.0f;
+    bool summed = false;
+
+    // A pass's sums; true: one more is needed.  (Again of a row that needed none: nothing changes.)
+    __device__ __forceinline__ bool take(float sum, float top, int K, float eps) {
+        last = 1.0f;
+        if (!summed) {
+            if (kMayOverflow<T> && __builtin_expect(sum == INFINITY && by == 1.0f, 0)) {
+                by = last = kDown;
+                return true;
+            }
+            summed = true;
+            r = 1.0f / sqrtf(sum / (float)K + eps * by * by);
+            rstd = r * by;
+            q = isfinite(sum) ? r : NAN;
+            if (E4M3 && kMayOverflow<T> && __builtin_expect(isfinite(sum) && !(top >= kLeast && top < INFINITY), 0)) {
+                if (top < kLeast) {
+                    last = sum < 1.0f ? 0x1p100f : 0x1p60f;
+                    down = sum < 1.0f ? 0x1p-100f : 0x1p-60f;
+                } else {
+                    last = __uint_as_float(__float_as_uint(r) & 0x7F800000u);
+                    q = __uint_as_float((__float_as_uint(r) & 0x007FFFFFu) | 0x3F800000u);
+                }
+                by *= last;
+                return true;
+            }
+        }
+        if (E4M3) {
+            if (down == 1.0f && top * q < kLeast) {
+                down = 0x1p-50f;
+                q *= 0x1p50f;
+            }
+            amax = top * q;
+            if (amax * 0x1p50f * down < kLeast) amax = 0.0f;  // Y below 2^-150: 0 in FP32
+        }
+        return false;
+    }
+    __device__ __forceinline__ float inverse() const { return amax == 0.0f ? 0.0f : 448.0f / amax; }
+    __device__ __forceinline__ float scale() const { return amax / 448.0f * down; }
+};
 
 // How a thread of a row's warps takes the row: pieces k0 + i STEP below `body` from element
 // `head` on, and, where they are not whole pieces, one element `one` of the head or the tail.
@@ -241,14 +290,16 @@ __device__ __forceinline__ uint16_t bits(float f) {
 }
 
 // Rows held in registers, WPR warps to a row, four warps at least to a CTA.  ODD: K is no
-// multiple of 8, or the bases lie off 16 bytes, all alike.
-__host__ __device__ constexpr int fwd_ctas(int wpr) { return wpr == 16 ? 2 : wpr == 8 ? 4 : 7; }
+// multiple of 8, or the bases lie off 16 bytes, all alike.  CTAs an SM: registers for eight of
+// 128 threads, but for odd rows' (E4M3 of 8192 x 4096 39.5 us against 39.8 with seven, of 10000
+// x 2047 29.6 against 30.5 with eight).
+__host__ __device__ constexpr int fwd_ctas(int wpr, bool odd) { return wpr == 16 ? 2 : wpr == 8 ? 4 : odd ? 7 : 8; }
 template <typename T, int WPR, bool ODD, bool E4M3>
-__global__ void __launch_bounds__(row_warps(WPR) * 32, fwd_ctas(WPR))
+__global__ void __launch_bounds__(row_warps(WPR) * 32, fwd_ctas(WPR, ODD))
 rms_norm_kernel(const FwdArgs a)
 {
     extern __shared__ __align__(16) uint16_t gains_s[];  // ODD
-    __shared__ float2 red[2][row_warps(WPR)];
+    __shared__ float2 red[3][row_warps(WPR)];
     pdl_wait();  // dependents launch as this grid's CTAs exit (several CTAs per SM: no early trigger)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, K = a.K;
     constexpr int ROWS = row_warps(WPR) / WPR, STEP = WPR * 256;
@@ -288,10 +339,9 @@ rms_norm_kernel(const FwdArgs a)
         else gains8<T>(a.w != nullptr, a.w && k < me.body ? ld16(a.w + k) : kZero, g);
     };
     const float one_gain = ODD && me.one >= 0 ? value<T>(gains_s + me.one) : 0.0f;
-    float by = 1.0f, sum, top;
-    auto sums = [&] {
+    auto sums = [&](float by, float &sum, float &top) {
         sum = ODD ? (one * by) * (one * by) : 0.0f;
-        top = ODD && E4M3 ? fabsf(one * by * one_gain) : 0.0f;
+        top = ODD && E4M3 ? fabsf(one * one_gain) : 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float f[8], g[8];
@@ -301,28 +351,39 @@ rms_norm_kernel(const FwdArgs a)
             for (int j = 0; j < 8; ++j) {
                 const float v = f[j] * by;
                 sum = fmaf(v, v, sum);
-                if (E4M3) top = fmaxf(top, fabsf(v * g[j]));
+                if (E4M3) top = fmaxf(top, fabsf(f[j] * g[j]));
             }
         }
     };
-    sums();
+    RowScales<T, E4M3> c;
+    float sum, top;
+    sums(1.0f, sum, top);
     reduce_row<WPR>(sum, top, red[0]);
+    bool more = c.take(sum, top, K, a.eps);
     if (kMayOverflow<T>) {
-        const bool over = sum == INFINITY;
-        if (over) by = kDown;
-        if (WPR > 1 ? __syncthreads_or(over) : over) {
-            sums();
-            reduce_row<WPR>(sum, top, red[1]);
+#pragma unroll 1
+        for (int t = 1; t < (E4M3 ? 3 : 2) && __builtin_expect(WPR > 1 ? __syncthreads_or(more) : more, 0); ++t) {
+            if (E4M3) {  // of codes H itself is multiplied (the ordinary row then needs no factor); elements
+                         // that leave bf16's range are nothing beside the largest
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    float f[8];
+                    unpack8<T>(h[i], f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] *= c.last;
+                    h[i] = pack8<T>(f);
+                }
+                one *= c.last;
+            }
+            sums(E4M3 ? 1.0f : c.by, sum, top);
+            reduce_row<WPR>(sum, top, red[t]);
+            more = c.take(sum, top, K, a.eps);
         }
     }
-    const float r = rstd_of(sum, K, a.eps, by);
-    if (first && a.rstd) a.rstd[row] = r * by;
-    float inv = 0.0f;
-    if (E4M3) {
-        const float amax = isfinite(sum) ? top * r : NAN;
-        inv = amax == 0.0f ? 0.0f : 448.0f / amax;
-        if (first) a.scale[row] = amax / 448.0f;
-    }
+    if (first && a.rstd) a.rstd[row] = c.rstd;
+    const float inv = E4M3 ? c.inverse() : 0.0f;
+    if (E4M3 && first) a.scale[row] = c.scale();
+    auto y = [&](float v, float w) { return E4M3 ? v * w * c.q : v * c.by * c.r * w; };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (me.k0 + i * STEP >= me.body) break;
@@ -330,14 +391,14 @@ rms_norm_kernel(const FwdArgs a)
         unpack8<T>(h[i], f);
         gains(i, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * by * r * g[j];
+        for (int j = 0; j < 8; ++j) f[j] = y(f[j], g[j]);
         if (E4M3) *reinterpret_cast<uint2 *>(a.Q + body + me.k0 + i * STEP) = codes8(f, inv);
         else *reinterpret_cast<uint4 *>(a.Y + body + me.k0 + i * STEP) = pack8<T>(f);
     }
     if (ODD && me.one >= 0) {
-        const float y = one * by * r * one_gain;
-        if (E4M3) a.Q[at + me.one] = (uint8_t)__nv_cvt_float_to_fp8(y * inv, __NV_SATFINITE, __NV_E4M3);
-        else a.Y[at + me.one] = bits<T>(y);
+        const float v = y(one, one_gain);
+        if (E4M3) a.Q[at + me.one] = (uint8_t)__nv_cvt_float_to_fp8(v * inv, __NV_SATFINITE, __NV_E4M3);
+        else a.Y[at + me.one] = bits<T>(v);
     }
 }
 
@@ -347,7 +408,7 @@ template <typename T, bool E4M3>
 __global__ void __launch_bounds__(MAX_WPR * 32)
 rms_norm_long_kernel(const FwdArgs a)
 {
-    __shared__ float2 red[2][MAX_WPR];
+    __shared__ float2 red[3][MAX_WPR];
     pdl_wait();
     const long long row = blockIdx.x;
     const int K = a.K;
@@ -361,8 +422,7 @@ rms_norm_long_kernel(const FwdArgs a)
         return a.R ? add8<T>(x, load8(a.R + at, k, K)) : x;
     };
     auto gain = [&](long long k, float(&g)[8]) { gains8<T>(a.w != nullptr, a.w ? load8(a.w, k, K) : kZero, g); };
-    float by = 1.0f, sum, top;
-    auto sums = [&] {
+    auto sums = [&](float by, float &sum, float &top) {
         sum = top = 0.0f;
         for (long long k = k0; k < K; k += STEP) {
             float f[8], g[8];
@@ -376,21 +436,22 @@ rms_norm_long_kernel(const FwdArgs a)
             }
         }
     };
-    sums();
+    RowScales<T, E4M3> c;
+    float sum, top;
+    sums(1.0f, sum, top);
     reduce_row<MAX_WPR>(sum, top, red[0]);
-    if (kMayOverflow<T> && sum == INFINITY) {  // the same in every thread
-        by = kDown;
-        sums();
-        reduce_row<MAX_WPR>(sum, top, red[1]);
+    bool more = c.take(sum, top, K, a.eps);  // the same in every thread
+    if (kMayOverflow<T>) {
+#pragma unroll 1
+        for (int t = 1; more; ++t) {  // (twice at most)
+            sums(c.by, sum, top);
+            reduce_row<MAX_WPR>(sum, top, red[t]);
+            more = c.take(sum, top, K, a.eps);
+        }
     }
-    const float r = rstd_of(sum, K, a.eps, by);
-    if (threadIdx.x == 0 && a.rstd) a.rstd[row] = r * by;
-    float inv = 0.0f;
-    if (E4M3) {
-        const float amax = isfinite(sum) ? top * r : NAN;
-        inv = amax == 0.0f ? 0.0f : 448.0f / amax;
-        if (threadIdx.x == 0) a.scale[row] = amax / 448.0f;
-    }
+    if (threadIdx.x == 0 && a.rstd) a.rstd[row] = c.rstd;
+    const float inv = E4M3 ? c.inverse() : 0.0f;
+    if (E4M3 && threadIdx.x == 0) a.scale[row] = c.scale();
     const bool wy = E4M3 ? on(a.Q + at - off, 8) : on(a.Y + at - off, 16);
     for (long long k = k0; k < K; k += STEP) {
         const uint4 h = value(k);
@@ -399,7 +460,7 @@ rms_norm_long_kernel(const FwdArgs a)
         unpack8<T>(h, f);
         gain(k, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * by * r * g[j];
+        for (int j = 0; j < 8; ++j) f[j] = E4M3 ? f[j] * c.by * g[j] * c.q : f[j] * c.by * c.r * g[j];
         if (E4M3) store8_codes(a.Q + at, k, K, wy, codes8(f, inv));
         else store8(a.Y + at, k, K, wy, pack8<T>(f));
     }

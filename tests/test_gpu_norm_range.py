@@ -71,3 +71,46 @@ def test_rows_of_the_largest_numbers(K):
     # rstd half a step of subnormals off: as much more of dw's terms, which it multiplies
     close(f64(dw, K), want_w, tol_w + np.abs(d * h).sum(0) * LEAST, "dw")
     close(f64(dX, 3, K), want_x, tol_x, "dX")
+
+
+def check_e4m3(x, w, eps):
+    """Codes within half a step of Y / scale, no NaN; FP32 operations as elsewhere, one product
+    more, and scales down to FP32's subnormals."""
+    X = torch.from_numpy(x.astype(np.float32)).bfloat16()
+    wt = None if w is None else torch.from_numpy(w.astype(np.float32)).bfloat16()
+    Q, scale = run_e4m3(X, wt, eps)
+    _, y = ref.forward(X.double().numpy(), 1.0 if w is None else wt.double().numpy(), eps)
+    _, ey = ref.forward_error(x.shape[1])
+    s = np.abs(y).max(1) / 448
+    s[s < 2.0 ** -150 / 448] = 0  # Y is 0 in FP32
+    close(scale, s, s * (ey + 4 * ref.U) + LEAST, "scale")
+    v = np.where(s[:, None] > 0, y / np.where(s > 0, s, 1)[:, None], 0)
+    close(Q, v, ref.e4m3_tolerance(v, ey + ref.U), "Q")
+
+
+LENGTHS = [(7, 64), (7, 512), (6, 1027), (5, 2040), (5, 2047), (3, 4096), (3, 8200), (6, 20000)]
+NEARLY_ZERO = np.array([1e-40, 9.2e-41, 0.0, 1e-39, 3.0, 1e-38, 2e-37])
+
+
+@pytest.mark.parametrize("eps", [EPS, 1.0, 2.0 ** 29])
+@pytest.mark.parametrize("M,K", LENGTHS)
+def test_codes_of_rows_that_are_nearly_zero(M, K, eps):
+    """bf16's least numbers, with zeros between them, beside rows of zeros and ordinary ones."""
+    rng = np.random.default_rng(K)
+    x = (1 + rng.random((M, K))) * NEARLY_ZERO[:M, None] * rng.choice([1.0, -1.0, 0.0], (M, K))
+    check_e4m3(x, None, eps)
+    check_e4m3(x, 1 + 0.3 * rng.standard_normal(K), eps)
+    # gains that take Y to FP32's subnormals, below them, or back among the normal numbers
+    for gain in (1e-5, 1e-12, 1e25):
+        check_e4m3(x, gain * (1 + rng.random(K)), eps)
+
+
+@pytest.mark.parametrize("M,K", LENGTHS)
+def test_codes_of_gains_that_take_h_out_of_fp32(M, K):
+    """w H above FP32's largest number, or below its least, where Y = w H rstd is neither."""
+    rng = np.random.default_rng(K)
+    x = rng.standard_normal((M, K)) * np.array([1e10, 1.0, 1e30, 0.0, 1e18, 1e-3, 1e9])[:M, None]
+    check_e4m3(x, 1e30 * (1 + 0.3 * rng.standard_normal(K)), EPS)
+    check_e4m3(x * 1e-8, 1e-30 * (1 + 0.3 * rng.standard_normal(K)), 1.2e-38)
+    w = 10.0 ** rng.uniform(-37, 37, K)
+    check_e4m3(x, w, EPS)
