@@ -31,13 +31,25 @@ namespace {
 
 using namespace pair;
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x, 2 units of 2^-23 off; 0 for -inf
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// A partial sum s of e^z with the largest logit m is kept as the sum of 2^(z log2 e - base_of(m)),
+// terms of one fused operation each.  base_of(m) is m log2 e rounded, everywhere: m log2 e left to
+// a fused operation differs from it, so that a maximum that stayed took up to 2^-24 m with it
+// from each sum to the next (loss of 131072 logits of 1000 3e-4 off), and from 2^31 on left no
+// sum at all.  Logits beyond kFar are 32 and more apart, and m log2 e may overflow: 2^(z - m),
+// which is 1 or as good as nothing; of infinite m 2^z.
+constexpr float kFar = 0x1p29f;
+__device__ __forceinline__ bool is_far(float m) { return !(fabsf(m) <= kFar); }
+__device__ __forceinline__ float base_of(float m) { return __fmul_rn(m, kLog2e); }
+// m log2 e - base_of(m)
+__device__ __forceinline__ float left_of(float m) { return is_far(m) ? 0.0f : fmaf(m, kLog2e, -base_of(m)); }
 
 // Of the columns [c0, c0 + 32) within a row's [0, N), c0 < N: the rest count as -inf.
 struct LseArgs {
@@ -85,15 +97,15 @@ struct LseEpi : LseArgs {
 #pragma unroll
             for (int j = 1; j < 32; ++j) top = fmaxf(top, __uint_as_float(r[j]));
             top = fmaxf(top, m);
-            // differences to a finite maximum: e^(-inf) = 0 and e^inf = inf come out of themselves
-            const float base = (isfinite(top) ? top : 0.0f) * kLog2e;
-            float s0 = s * ex2(m * kLog2e - base), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+            const bool far = is_far(top);
+            const float base = far ? (isinf(top) ? 0.0f : top) : base_of(top), by = far ? 1.0f : kLog2e;
+            float s0 = s * ex2(far ? (m == top ? 0.0f : -INFINITY) : base_of(m) - base), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-                s0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -base));
-                s1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -base));
-                s2 += ex2(fmaf(__uint_as_float(r[j + 2]), kLog2e, -base));
-                s3 += ex2(fmaf(__uint_as_float(r[j + 3]), kLog2e, -base));
+                s0 += ex2(fmaf(__uint_as_float(r[j]), by, -base));
+                s1 += ex2(fmaf(__uint_as_float(r[j + 1]), by, -base));
+                s2 += ex2(fmaf(__uint_as_float(r[j + 2]), by, -base));
+                s3 += ex2(fmaf(__uint_as_float(r[j + 3]), by, -base));
             }
             s = (s0 + s1) + (s2 + s3);
             m = top;
@@ -117,14 +129,26 @@ struct DzEpi : DzArgs {
     static constexpr bool LOWER = false, JOIN = JOINED, CLASSES = OF_CLASSES;
     static constexpr int BOXES = JOINED ? 2 : 1;
 
-    struct Pre {};
-    __device__ __forceinline__ void prefetch(const Part &, Pre &) const {}
-    __device__ __forceinline__ void run(Part &p, const Pre &) const {
+    struct Pre {  // a row's
+        long long t;
+        bool counts;
+        float base, by;  // p is 2^(z by - base) 2^-left, left the base's rounding: the latter goes with d
+        float d, one;
+    };
+    __device__ __forceinline__ void prefetch(const Part &p, Pre &pre) const {
         const int row = p.row0 + p.lane;
-        long long t = row < M ? target[row] : -1;
-        const bool counts = t >= 0 && t < total;
-        const float d = counts ? dloss[row] * scale->x : 0.0f;
-        const float base = counts ? lse[row] * kLog2e : 0.0f;
+        pre.t = row < M ? target[row] : -1;
+        pre.counts = pre.t >= 0 && pre.t < total;
+        const float l = pre.counts ? lse[row] : 0.0f, left = left_of(l);
+        pre.base = is_far(l) ? l : base_of(l);
+        pre.by = is_far(l) ? 1.0f : kLog2e;
+        pre.d = pre.counts ? dloss[row] * scale->x * ex2(-left) : 0.0f;
+        pre.one = ex2(left);
+    }
+    __device__ __forceinline__ void run(Part &p, const Pre &pre) const {
+        const bool counts = pre.counts;
+        const float d = pre.d, base = pre.base, by = pre.by, one = pre.one;
+        long long t = pre.t;
         t = counts ? t - v0 : -1;
         int cols = N;
         if (CLASSES) {
@@ -142,12 +166,12 @@ struct DzEpi : DzArgs {
                 p.load<JOIN>(g + h * 32, r);
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -base));
+                for (int j = 0; j < 32; ++j) v[j] = ex2(fmaf(__uint_as_float(r[j]), by, -base));
                 const long long at = t - (c0 + h * 32);
                 if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (j == at) v[j] -= 1.0f;
+                        if (j == at) v[j] -= one;
                 }
                 if (CLASSES && c0 + h * 32 + 32 > cols) {  // (a class may be one column short)
 #pragma unroll
@@ -291,14 +315,17 @@ struct MaxSum {
     float m = -INFINITY, s = 0.0f;
 
     __device__ __forceinline__ void join(float om, float os) {
-        const float top = fmaxf(m, om), base = (isfinite(top) ? top : 0.0f) * kLog2e;
-        s = s * ex2(m * kLog2e - base) + os * ex2(om * kLog2e - base);
+        const float top = fmaxf(m, om), b = base_of(m), ob = base_of(om);
+        float f = ex2(fminf(b, ob) - fmaxf(b, ob));
+        if (is_far(top)) f = m == om ? 1.0f : 0.0f;
+        s = m >= om ? fmaf(os, f, s) : fmaf(s, f, os);
         m = top;
     }
+    // The loss without lse's rounding, which is of m's size.
     __device__ __forceinline__ void store(float zt, long long t, int N, float *loss, float *lse) const {
-        const float l = (isfinite(m) ? m : 0.0f) + logf(s);
-        *loss = t >= 0 && t < N ? l - zt : 0.0f;
-        if (lse) *lse = l;
+        const float o = isfinite(m) ? m : 0.0f, l = logf(s) - left_of(o) * kLn2;
+        *loss = t >= 0 && t < N ? (o - zt) + l : 0.0f;
+        if (lse) *lse = o + l;
     }
 };
 // Joins the slots.  ROWS to a CTA: 8 (of a slot 64 adjacent bytes, two whole sectors), slots

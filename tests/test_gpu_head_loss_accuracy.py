@@ -91,3 +91,21 @@ def test_logits_next_to_fp32s_largest(N, sign):
     dw[N // 3, 0], dw[0, 0] = 0.5, -0.5
     assert torch.equal(dW.float().cpu(), dw)
     assert not dX[0].any() and abs(float(dX[1, 0]) / (0.5 * want[1]) - 1) <= 2.0 ** -8 + 4 * U
+
+
+@pytest.mark.parametrize("m", [12.0, 29952.0, 2.0 ** 20, -2.0 ** 27])
+def test_the_softmax_is_of_the_lse_given(m):
+    """p = e^(z - lse) with lse as it is, however large: dW of one row is dZ, rounded to bf16
+    twice; p's exponent by a rounding of at most 8 and 2^x by two units of 2^-23."""
+    N = 700
+    z = np.full(N, m)
+    _, lse, X, W, t = head(z, [5])
+    lse.add_(3.0)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    g.gemm_cross_entropy_backward("bf16", X, W, t, lse, torch.ones(1, device="cuda"), dX, dW, 1, N, 8)
+    g.gemm_synchronize()
+    want = np.exp(z - float(lse[0]))
+    want[5] -= 1
+    got = dW[:, 0].double().cpu().numpy()
+    tol = np.abs(want) * (2 * 2.0 ** -8 + 2.0 ** -16) + (8 + 8) * U * np.exp(m - float(lse[0]))
+    assert (np.abs(got - want) <= tol).all(), float((np.abs(got - want) / tol).max())
