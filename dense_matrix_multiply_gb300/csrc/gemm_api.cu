@@ -680,6 +680,17 @@ gemm_status_t run_rms_norm_backward(int dtype, const void *H, const void *w, con
     return finish(launch_rms_norm_backward(p, dev->num_sms, dev->status, t_stream), "rms_norm_backward");
 }
 
+// The tensor-core pipeline of the head and the update counts rows and columns up to the end of
+// a tile of 256 in 32 bits.
+bool tiles_countable(const char *who, std::initializer_list<int> sizes) {
+    for (const int n : sizes)
+        if (n > 0x7FFFFFFF - 255) {
+            snprintf(t_last_error, sizeof(t_last_error), "%s: sizes have to be at most 2^31 - 256", who);
+            return false;
+        }
+    return true;
+}
+
 // ------------------------------------------------------------ cross entropy of a linear head
 bool targets_aligned(const char *who, const int64_t *t) {
     if (((uintptr_t)t & 7) == 0) return true;
@@ -694,7 +705,7 @@ gemm_status_t run_cross_entropy(int dtype, const void *X, const void *W, const i
     if (!elements_aligned(who, {X, W}, {loss, lse}) || !targets_aligned(who, targets)) return GEMM_ERR_INVALID_VALUE;
     if (M == 0) { t_last_kernel = "noop"; return GEMM_OK; }
     const bool work = N > 0 && K > 0;
-    if (!loss || !targets || (work && (!X || !W))) return GEMM_ERR_INVALID_VALUE;
+    if (!loss || !targets || (work && (!X || !W || !tiles_countable(who, {M, N, K})))) return GEMM_ERR_INVALID_VALUE;
     const size_t m4 = (size_t)M * 4;
     const Span lo{loss, m4}, ls{lse, m4};
     if (any_overlap({lo, ls}, {{X, (size_t)M * K * 2}, {W, (size_t)N * K * 2}, {targets, (size_t)M * 8}})) return GEMM_ERR_ALIAS;
@@ -713,7 +724,7 @@ gemm_status_t run_cross_entropy_backward(int dtype, const void *X, const void *W
     if (!elements_aligned(who, {X, W, dX, dW}, {lse, dloss}) || !targets_aligned(who, targets)) return GEMM_ERR_INVALID_VALUE;
     if (K == 0 || (!dX && !dW)) { t_last_kernel = "noop"; return GEMM_OK; }
     const bool work = M > 0 && N > 0;
-    if (work && (!X || !W || !targets || !lse || !dloss)) return GEMM_ERR_INVALID_VALUE;
+    if (work && (!X || !W || !targets || !lse || !dloss || !tiles_countable(who, {M, N, K}))) return GEMM_ERR_INVALID_VALUE;
     const size_t x = (size_t)M * K * 2, w = (size_t)N * K * 2, m4 = (size_t)M * 4;
     const Span ox{dX, x}, ow{dW, w};
     if (any_overlap({ox, ow}, {{X, x}, {W, w}, {targets, (size_t)M * 8}, {lse, m4}, {dloss, m4}})) return GEMM_ERR_ALIAS;
@@ -738,7 +749,7 @@ gemm_status_t run_orthogonalize(int dtype, const void *G, int64_t ldg, void *O, 
         return GEMM_ERR_INVALID_VALUE;
     }
     if (M == 0 || N == 0) { t_last_kernel = "noop"; return GEMM_OK; }
-    if (!G || !O) return GEMM_ERR_INVALID_VALUE;
+    if (!G || !O || !tiles_countable(who, {M, N})) return GEMM_ERR_INVALID_VALUE;
     long long g = 0, o = 0;
     if (!span_elems(1, 0, M, ldg, N, &g) || !span_elems(1, 0, M, ldo, N, &o) || g > (1LL << 61) || o > (1LL << 61))
         return GEMM_ERR_INVALID_VALUE;

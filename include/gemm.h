@@ -411,7 +411,7 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H,
  * strides; targets int64 [M]; loss and lse FP32 [M] (lse null: not stored).  A target
  * outside 0 .. N - 1 leaves its row out: loss 0 (lse is stored all the same), and no part
  * in the gradients, whatever the row of X holds.  Logits, largest value, sum and
- * logarithm in FP32.  Any M, N, K; K and the bases multiples of 8 elements are fastest:
+ * logarithm in FP32.  M, N, K up to 2^31 - 256; K and the bases multiples of 8 elements are fastest:
  * of other operands X is copied to padded rows in scratch (up to eight times), W read in
  * place where K is no multiple of 8 and N large against M, else copied too, a piece (up to
  * 256 MiB) at a time.  Scratch: 8 bytes for each row and 64 to 128 entries, for up to 16384
@@ -447,8 +447,8 @@ GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const voi
  * a, b, c finite, and such that X and A stay within half's range: intermediate matrices
  * are half (X in two halves, 22 bits), sums and |G|_F^2 FP32 or more.  The relative error
  * of the usual five steps is 1e-3 to 2e-3 (2-norm) before O's own rounding.  A matrix of
- * zeros gives zeros; a NaN or an infinity in G makes O NaN.  Any M, N and alignment of
- * elements.  Scratch: 8 bytes for each element of G and 4 for each of A, in stream-ordered
+ * zeros gives zeros; a NaN or an infinity in G makes O NaN.  M, N up to 2^31 - 256, any
+ * alignment of elements.  Scratch: 8 bytes for each element of G and 4 for each of A, in stream-ordered
  * memory for the duration of the call from the library's pool (see gemm_gated).
  * GEMM_ERR_ALIAS if O overlaps G otherwise. */
 GEMM_API gemm_status_t gemm_orthogonalize(gemm_dtype_t dtype, const void *G, int64_t ldg, void *O, int64_t ldo, int steps,
