@@ -115,20 +115,23 @@ def _addr(x) -> int:
 _raw_stream = _raw_device = None
 
 
-def _current_stream(device: int) -> int:
-    """Handle of torch's current stream on a device."""
+def _point_at(lib, device: int) -> None:
+    """Points the library at torch's current stream of a device.  That has to be the current
+    device, where the library launches; a call refused for it leaves the stream as it was."""
     global _raw_stream, _raw_device
     if _raw_stream is None:
         import torch
         _raw_device = torch._C._cuda_getDevice
         _raw_stream = torch._C._cuda_getCurrentRawStream
-    return _raw_stream(device)
+    if device != _raw_device():
+        raise ValueError(f"tensors on cuda:{device}, the current device is cuda:{_raw_device()}")
+    lib.gemm_set_stream(_raw_stream(device))
 
 
 def _bind_torch_stream(*tensors) -> None:
     """Points the library at torch's current stream of the tensors' device.
-    Every tensor argument must live on one CUDA device: a kernel given another
-    device's address would read memory it cannot reach."""
+    Every tensor argument must live on the current CUDA device: a kernel given
+    another device's address would read memory it cannot reach."""
     dev = None
     for t in tensors:
         if t is None or type(t) is int or not hasattr(t, "get_device"):
@@ -141,7 +144,7 @@ def _bind_torch_stream(*tensors) -> None:
         elif d != dev:
             raise ValueError(f"tensors on two devices: cuda:{dev} and cuda:{d}")
     if dev is not None:
-        load().gemm_set_stream(_current_stream(dev))
+        _point_at(_lib or load(), dev)
 
 
 def _span(outer: int, inner: int, ld: int, stride: int = 0, batch: int = 1) -> int:
@@ -196,8 +199,8 @@ def _check_rows(name: str, t, ld: int, need: int) -> None:
 def _take(lib, name: str, *args):
     """Addresses of several tensor arguments (argument, tensor, element size,
     elements, tight), each checked as by _check -- a contiguous tensor with room
-    passes without a message being built -- and all on one CUDA device, to whose
-    current torch stream the library is pointed."""
+    passes without a message being built -- and all on the current CUDA device, to
+    whose current torch stream the library is pointed."""
     out, dev, mixed = [], None, False
     for arg, t, size, need, tight in args:
         if t is None:
@@ -218,9 +221,7 @@ def _take(lib, name: str, *args):
             raise ValueError("tensors must live on a CUDA device")
         if mixed:
             raise ValueError("tensors on two devices")
-        lib.gemm_set_stream(_current_stream(dev))
-        if dev != _raw_device():  # (known since _current_stream) the library launches on the current device
-            raise ValueError(f"tensors on cuda:{dev}, the current device is cuda:{_raw_device()}")
+        _point_at(lib, dev)
     return out
 
 
