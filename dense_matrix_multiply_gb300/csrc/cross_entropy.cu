@@ -330,8 +330,8 @@ struct MaxSum {
 };
 // Joins the slots.  ROWS to a CTA: 8 (of a slot 64 adjacent bytes, two whole sectors), slots
 // dealt to 128 lanes of each, or, of few rows, 1 -- a row's joins are a chain of latencies
-// (forward of 200 x 50257 x 64 12.5 us, against 14.9 with 256 threads to a row; 65 x 50257 x 64 11.0, against
-// 12.3 with 8).
+// (forward of 200 x 50257 x 64 12.5 us, against 14.9 with 256 threads to a row; 65 x 50257 x 64
+// 11.0, against 12.3 with 8).
 template <int ROWS>
 __global__ void __launch_bounds__(1024)
 head_join_kernel(const float2 *__restrict__ part, const float *__restrict__ zt, const long long *__restrict__ target,
@@ -387,9 +387,9 @@ head_flat_kernel(const long long *__restrict__ target, float *__restrict__ loss,
 // The factor that takes the largest |dloss| of a row with a target to `peak`, and its inverse.
 // peak is a power of two, so that where all rows weigh alike a probable target's dZ, -peak
 // (1 - p), is nearly representable: a weight of 1 / 777 in 16 bits is off by a relative 2^-9
-// or less, but by the same in every row, and both gradients with it (bf16, 1100 x
-// 5000 x 512, weights of 1 / 848: 0.0034 off against 0.0017).  Half: 2^14, so that dZ keeps half's full precision
-// down to probabilities of 2^-28.  By a CTA.
+// or less, but by the same in every row, and both gradients with it (bf16, 1100 x 5000 x 512,
+// weights of 1 / 848: 0.0034 off against 0.0017).  Half: 2^14, so that dZ keeps half's full
+// precision down to probabilities of 2^-28.  By a CTA.
 struct ScaleArgs {
     const float *dloss;
     const long long *target;
@@ -432,7 +432,8 @@ head_scale_kernel(const ScaleArgs a)
 constexpr int COPY_WARPS = 4;
 __global__ void __launch_bounds__(COPY_WARPS * 32)
 head_copy_kernel(const uint16_t *__restrict__ src, long long rows, long long cols, uint16_t *__restrict__ dst,
-                 long long dst_cols, const long long *__restrict__ target, int N, unsigned long long fronts, unsigned long long turns, const ScaleArgs a)
+                 long long dst_cols, const long long *__restrict__ target, int N, unsigned long long fronts,
+                 unsigned long long turns, const ScaleArgs a)
 {
     pdl_wait();
     if (a.scale && blockIdx.x == gridDim.x - 1) {

@@ -1,6 +1,7 @@
 // PTX wrappers of the tensor-core kernels for 4-bit products (fp4_gemm.cu,
 // fp4_skinny.cu), the gated feed-forward block (gated.cu), the head and the update
-// (pair_pipe.cuh), and of the norm's gradients (rms_norm.cu): mbarriers with bounded waits, TMA, tensor memory, tcgen05 in one- and two-CTA forms.
+// (pair_pipe.cuh), and of the norm's gradients (rms_norm.cu): mbarriers with bounded
+// waits, TMA, tensor memory, tcgen05 in one- and two-CTA forms.
 #pragma once
 
 #include <cuda.h>

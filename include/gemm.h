@@ -375,8 +375,8 @@ GEMM_API gemm_status_t gemm_gated_backward(gemm_dtype_t dtype, gemm_act_t act, c
  * updated in place).  rstd (null: not stored): FP32 [M], for gemm_rms_norm_backward.
  * eps: a normal number below 2^30 (GEMM_ERR_INVALID_VALUE otherwise).  Any M and K: one
  * token to a long prompt.  Where the operands' bases lie alike to 16 bytes (any K), rows
- * of up to 16384 elements are read once, else twice.  Rows of bf16 whose squares overflow FP32
- * are summed again, scaled down; a NaN or an infinity in a row reaches that row alone.
+ * of up to 16384 elements are read once, else twice.  Rows of bf16 whose squares overflow
+ * FP32 are summed again, scaled down; a NaN or an infinity in a row reaches that row alone.
  * M = 0 or K = 0: nothing is written.  GEMM_ERR_ALIAS if any other output overlaps an
  * input or another output. */
 GEMM_API gemm_status_t gemm_rms_norm(gemm_dtype_t dtype, const void *X, const void *R, const void *w, float eps, void *H,
@@ -387,7 +387,9 @@ GEMM_API gemm_status_t gemm_rms_norm(gemm_dtype_t dtype, const void *X, const vo
  *     scale_i = amax_k |Y[i,k]| / 448,  Q[i,k] = E4M3(Y[i,k] * (448 / amax_i))
  * nearest, ties to even, clamped to +-448 (as gemm_quantize_rows_e4m3).  Q [M,K] codes,
  * scale FP32 [M].  A row of zeros gives codes 0 and scale 0; a NaN or an infinity in a
- * row makes its scale NaN. */
+ * row makes its scale NaN.  bf16 rows and gains at the ends of their range are gone over
+ * twice or three times, so that no intermediate value leaves FP32; a scale below 2^-126 is
+ * an FP32 subnormal and has fewer bits, a row whose largest |Y| is below 2^-150 gives 0. */
 GEMM_API gemm_status_t gemm_rms_norm_e4m3(gemm_dtype_t dtype, const void *X, const void *R, const void *w, float eps,
                                           void *H, uint8_t *Q, float *scale, int M, int K);
 
@@ -411,12 +413,14 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H,
  * strides; targets int64 [M]; loss and lse FP32 [M] (lse null: not stored).  A target
  * outside 0 .. N - 1 leaves its row out: loss 0 (lse is stored all the same), and no part
  * in the gradients, whatever the row of X holds.  Logits, largest value, sum and
- * logarithm in FP32.  M, N, K up to 2^31 - 256; K and the bases multiples of 8 elements are fastest:
- * of other operands X is copied to padded rows in scratch (up to eight times), W read in
- * place where K is no multiple of 8 and N large against M, else copied too, a piece (up to
- * 256 MiB) at a time.  Scratch: 8 bytes for each row and 64 to 128 entries, for up to 16384
- * rows at once, and the copies, in stream-ordered memory for the duration of the call from
- * the library's pool (see gemm_gated).  K = 0: logits of 0; N = 0: lse is -inf.  GEMM_ERR_ALIAS if an output
+ * logarithm in FP32; the loss is formed without lse's rounding.  M, N, K up to 2^31 - 256
+ * (GEMM_ERR_INVALID_VALUE above); K and the bases multiples of 8 elements are fastest: of
+ * other operands X is copied in scratch (up to eight times), W read in place where K is no
+ * multiple of 8 and N large against M, else copied too, a piece at a time (up to 256 MiB, or
+ * 256 rows where that is more).  Rows of the copies are padded to a multiple of 64 elements.
+ * Scratch: 8 bytes for each row and 64 to 128 entries, for up to 16384 rows at once, and the
+ * copies, in stream-ordered memory for the duration of the call from the library's pool (see
+ * gemm_gated).  K = 0: logits of 0; N = 0: lse is -inf.  GEMM_ERR_ALIAS if an output
  * overlaps an input or the other output. */
 GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
                                           float *loss, float *lse, int M, int N, int K);
@@ -426,13 +430,15 @@ GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, con
  *     dZ[i,j] = (exp(Z[i,j] - lse_i) - [j = targets_i]) dloss_i  (0 in rows left out)
  *     dX = dZ W,  dW = dZ^T X
  * dX [M,K], dW [N,K] (dtype), each overwritten; a null one is left out.  The logits are
- * computed anew, a piece of the vocabulary at a time; dZ is formed in FP32 and rounded to
+ * computed anew, a piece of the vocabulary at a time; exp(Z - lse) has lse's rounding, up to
+ * 2^-24 |lse| of itself; dZ is formed in FP32 and rounded to
  * dtype, scaled by the largest |dloss| (so that neither small probabilities nor a weight
  * that dtype does not hold exactly are lost; any loss scale does), the operand of the
  * products, whose sums are FP32, in a fixed order, rounded once.  Scratch as above:
  * a piece of dZ (256 MiB, or 256 entries of every row where that is more), FP32 sums of
- * dX (up to 256 MiB, or once 4 M K bytes where that is more) and copies of X (one for
- * dW, with zeros in the rows left out; up to sixteen where W is read in place).  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as above. */
+ * dX (rows padded to a multiple of 64; up to 256 MiB, or a single set where that is more) and
+ * copies of X (one for dW, with zeros in the rows left out; up to sixteen where W is read in
+ * place).  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as above. */
 GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
                                                    const float *lse, const float *dloss, void *dX, void *dW, int M, int N,
                                                    int K);
@@ -447,9 +453,11 @@ GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const voi
  * a, b, c finite, and such that X and A stay within half's range: intermediate matrices
  * are half (X in two halves, 22 bits), sums and |G|_F^2 FP32 or more.  The relative error
  * of the usual five steps is 1e-3 to 2e-3 (2-norm) before O's own rounding.  A matrix of
- * zeros gives zeros; a NaN or an infinity in G makes O NaN.  M, N up to 2^31 - 256, any
- * alignment of elements.  Scratch: 8 bytes for each element of G and 4 for each of A, in stream-ordered
- * memory for the duration of the call from the library's pool (see gemm_gated).
+ * zeros gives zeros; a NaN or an infinity in G makes O NaN.  M, N up to 2^31 - 256
+ * (GEMM_ERR_INVALID_VALUE above), any alignment of elements.  Scratch: 8 bytes for each
+ * element of G and 4 for each of A, rows of both padded to a multiple of 64 elements (a column
+ * of M elements takes 512 M bytes), in stream-ordered memory for the duration of the call
+ * from the library's pool (see gemm_gated).
  * GEMM_ERR_ALIAS if O overlaps G otherwise. */
 GEMM_API gemm_status_t gemm_orthogonalize(gemm_dtype_t dtype, const void *G, int64_t ldg, void *O, int64_t ldo, int steps,
                                           float a, float b, float c, int M, int N);
