@@ -452,7 +452,9 @@ GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const voi
  * bring singular values from about 0.01 of |G|_F up to between 0.7 and 1.2.  steps >= 1;
  * a, b, c finite, and such that X and A stay within half's range: intermediate matrices
  * are half (X in two halves, 22 bits), sums and |G|_F^2 FP32 or more.  The relative error
- * of the usual five steps is 1e-3 to 2e-3 (2-norm) before O's own rounding.  A matrix of
+ * of the usual five steps is 1e-3 to 2e-3 (Frobenius norm) before O's own rounding, up to
+ * 1e-2 in matrices of a few rows or columns, whose few singular values it does not average
+ * over.  A matrix of
  * zeros gives zeros; a NaN or an infinity in G makes O NaN.  M, N up to 2^31 - 256
  * (GEMM_ERR_INVALID_VALUE above), any alignment of elements.  Scratch: 8 bytes for each
  * element of G and 4 for each of A, rows of both padded to a multiple of 64 elements (a column
