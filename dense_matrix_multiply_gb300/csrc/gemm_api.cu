@@ -705,7 +705,7 @@ gemm_status_t run_cross_entropy(int dtype, const void *X, const void *W, const i
     if (!elements_aligned(who, {X, W}, {loss, lse}) || !targets_aligned(who, targets)) return GEMM_ERR_INVALID_VALUE;
     if (M == 0) { t_last_kernel = "noop"; return GEMM_OK; }
     const bool work = N > 0 && K > 0;
-    if (!loss || !targets || (work && (!X || !W || !tiles_countable(who, {M, N, K})))) return GEMM_ERR_INVALID_VALUE;
+    if (!loss || !targets || (work && (!X || !W || !tiles_countable(who, {N, K})))) return GEMM_ERR_INVALID_VALUE;  // (rows go in pieces)
     const size_t m4 = (size_t)M * 4;
     const Span lo{loss, m4}, ls{lse, m4};
     if (any_overlap({lo, ls}, {{X, (size_t)M * K * 2}, {W, (size_t)N * K * 2}, {targets, (size_t)M * 8}})) return GEMM_ERR_ALIAS;

@@ -413,7 +413,7 @@ GEMM_API gemm_status_t gemm_rms_norm_backward(gemm_dtype_t dtype, const void *H,
  * strides; targets int64 [M]; loss and lse FP32 [M] (lse null: not stored).  A target
  * outside 0 .. N - 1 leaves its row out: loss 0 (lse is stored all the same), and no part
  * in the gradients, whatever the row of X holds.  Logits, largest value, sum and
- * logarithm in FP32; the loss is formed without lse's rounding.  M, N, K up to 2^31 - 256
+ * logarithm in FP32; the loss is formed without lse's rounding.  N and K up to 2^31 - 256
  * (GEMM_ERR_INVALID_VALUE above); K and the bases multiples of 8 elements are fastest: of
  * other operands X is copied in scratch (up to eight times), W read in place where K is no
  * multiple of 8 and N large against M, else copied too, a piece at a time (up to 256 MiB, or
@@ -438,7 +438,8 @@ GEMM_API gemm_status_t gemm_cross_entropy(gemm_dtype_t dtype, const void *X, con
  * a piece of dZ (256 MiB, or 256 entries of every row where that is more), FP32 sums of
  * dX (rows padded to a multiple of 64; up to 256 MiB, or a single set where that is more) and
  * copies of X (one for dW, with zeros in the rows left out; up to sixteen where W is read in
- * place).  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as above. */
+ * place).  M too is at most 2^31 - 256.  M = 0 or N = 0 gives zeros.  GEMM_ERR_ALIAS as
+ * above. */
 GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const void *X, const void *W, const int64_t *targets,
                                                    const float *lse, const float *dloss, void *dX, void *dW, int M, int N,
                                                    int K);
@@ -454,13 +455,12 @@ GEMM_API gemm_status_t gemm_cross_entropy_backward(gemm_dtype_t dtype, const voi
  * are half (X in two halves, 22 bits), sums and |G|_F^2 FP32 or more.  The relative error
  * of the usual five steps is 1e-3 to 2e-3 (Frobenius norm) before O's own rounding, up to
  * 1e-2 in matrices of a few rows or columns, whose few singular values it does not average
- * over.  A matrix of
- * zeros gives zeros; a NaN or an infinity in G makes O NaN.  M, N up to 2^31 - 256
- * (GEMM_ERR_INVALID_VALUE above), any alignment of elements.  Scratch: 8 bytes for each
- * element of G and 4 for each of A, rows of both padded to a multiple of 64 elements (a column
- * of M elements takes 512 M bytes), in stream-ordered memory for the duration of the call
- * from the library's pool (see gemm_gated).
- * GEMM_ERR_ALIAS if O overlaps G otherwise. */
+ * over.  A matrix of zeros gives zeros; a NaN or an infinity in G makes O NaN.  M, N up to
+ * 2^31 - 256 (GEMM_ERR_INVALID_VALUE above), any alignment of elements.  Scratch: 8 bytes
+ * for each element of G and 4 for each of A, rows of both padded to a multiple of 64
+ * elements (a column of M elements takes 512 M bytes), in stream-ordered memory for the
+ * duration of the call from the library's pool (see gemm_gated).  GEMM_ERR_ALIAS if O
+ * overlaps G otherwise. */
 GEMM_API gemm_status_t gemm_orthogonalize(gemm_dtype_t dtype, const void *G, int64_t ldg, void *O, int64_t ldo, int steps,
                                           float a, float b, float c, int M, int N);
 

@@ -23,7 +23,8 @@ def refused(fn, *args):
 
 @pytest.mark.parametrize("dims", [(1, TOP + 1, 8), (1, (1 << 31) - 1, 8), (1, 1, TOP + 1), (TOP + 1, 1, 8)])
 def test_head(dims):
-    refused(g.gemm_cross_entropy, "bf16", A, 2 * A, 3 * A, 4 * A, 5 * A, *dims)
+    if dims[0] == 1:  # the loss takes any rows: they go in pieces
+        refused(g.gemm_cross_entropy, "bf16", A, 2 * A, 3 * A, 4 * A, 5 * A, *dims)
     refused(g.gemm_cross_entropy_backward, "bf16", A, 2 * A, 3 * A, 4 * A, 5 * A, 6 * A, 7 * A, *dims)
 
 
